@@ -410,6 +410,116 @@ muon_status muon_update_static(muon_handle* handle, int n, const muon_matrix* gr
                                const muon_matrix* update_out, const muon_config* cfg);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The rest of a training step: the head's loss with its gradient, the global
+ * gradient norm with clipping, and AdamW for the parameters that Muon does
+ * not take (embeddings, head, one-dimensional ones).
+ *
+ * The conventions above hold, with these differences. The tensors of the list
+ * calls are any rows x cols with unit column stride, up to 2^42 elements (a
+ * vector is one row, whose ld is not looked at); none of the Newton-Schulz
+ * limits applies. Outputs share no element with any other buffer of the call
+ * unless said below (MUON_ERR_INVALID_ARG). norm, coef, loss, grad_out and
+ * grad_scale are device pointers to fp32 values. Lists travel in the kernel
+ * arguments, so these calls upload nothing; they can be captured in a graph
+ * once a first call of the same sizes has grown the handle's buffers.
+ */
+
+/*
+ * muon_grad_norm - norm = sqrt(sum over all elements of all tensors of g^2),
+ * the squares summed in 64 bits (no overflow for any fp32 gradient); with
+ * coef not NULL also coef = min(1, max_norm / (norm + 1e-6)), NaN where the
+ * norm is. An empty list has norm 0. max_norm > 0 is read only with coef.
+ */
+muon_status muon_grad_norm(muon_handle* handle, int n, const muon_matrix* grad, float max_norm,
+                           float* norm, float* coef);
+
+/*
+ * muon_clip_grad_norm - muon_grad_norm, then out_i = coef grad_i (out NULL:
+ * in place, and nothing is written when coef is 1). out_i may be grad_i
+ * itself; its type may differ from grad_i's. coef must not be NULL.
+ */
+muon_status muon_clip_grad_norm(muon_handle* handle, int n, const muon_matrix* grad, const muon_matrix* out,
+                                float max_norm, float* norm, float* coef);
+
+/* out_i = coef in_i with coef on the device (out NULL: in place, nothing written when it is 1). */
+muon_status muon_scale(muon_handle* handle, int n, const muon_matrix* in, const muon_matrix* out,
+                       const float* coef);
+
+/*
+ * adamw_update - AdamW with decoupled weight decay, in place, for each tensor:
+ *   g' = grad_scale g (grad_scale: device scalar, for example muon_grad_norm's
+ *   coef; NULL = 1), m = beta1 m + (1 - beta1) g', v = beta2 v +
+ *   (1 - beta2) g'^2, w = w (1 - lr weight_decay) - lr (m / (1 - beta1^step))
+ *   / (sqrt(v / (1 - beta2^step)) + eps).
+ *   grad, weight F32 or BF16 (each its own), exp_avg, exp_avg_sq F32; copy
+ *   (array may be NULL, entries may be empty) receives the new weight, for a
+ *   model that computes on 16-bit copies of 32-bit weights. All arithmetic is
+ *   fp32; a BF16 weight is rounded to nearest even once a step. step counts
+ *   from 1. Every tensor is read and written once.
+ * muon_adamw_config_default: lr 0.01, betas (0.8, 0.95), eps 1e-10,
+ * weight_decay 0 (the [Aurora page]'s AdamW beside Muon), step 1.
+ */
+typedef struct {
+  float lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+} muon_adamw_config;
+void muon_adamw_config_default(muon_adamw_config* cfg);
+muon_status adamw_update(muon_handle* handle, int n, const muon_matrix* grad, const muon_matrix* exp_avg,
+                         const muon_matrix* exp_avg_sq, const muon_matrix* weight, const muon_matrix* copy,
+                         const muon_adamw_config* cfg, const float* grad_scale);
+
+/*
+ * linear_cross_entropy(_grad) - softmax cross entropy of a language-model
+ * head: z = hidden weight^T (N x V, fp32 accumulation, never stored as a
+ * whole), with softcap c > 0: z <- c tanh(z / c); loss_i = log sum_v exp z_iv
+ * - z_i,target. The gradient is that of sum_i g_i loss_i, g_i = grad_out[i]
+ * (reduction none), grad_out[0] (sum) or grad_out[0] / valid tokens (mean);
+ * grad_out NULL = 1.
+ *   hidden   N x D; weight V x D, same type, F32 or BF16 (D <= 65536,
+ *            V <= 2^22, N <= 2^24; N may be 0)
+ *   targets  N integers of target_bytes 4 or 8 each. Tokens whose target is
+ *            ignore_index are left out: loss 0, gradient 0, and whatever
+ *            their hidden rows hold (NaN too) is never read. Any other target
+ *            outside [0, V) gives that token a NaN loss and no gradient.
+ *   loss     N values (reduction none) or one; mean is over the valid tokens,
+ *            0 if there is none
+ *   dhidden, dweight  gradients, of the types of hidden and weight; one of
+ *            them may be NULL (its product is left out)
+ * BF16 inputs are multiplied on the bf16 matrix cores (the logits' gradient
+ * is rounded to bf16 once), F32 ones in fp32 throughout; statistics and sums
+ * are fp32. The handle keeps up to about 1 GiB for the pieces of tokens (256
+ * at least), plus, when a call takes more than one piece, an fp32 V x D sum,
+ * and a padded copy of a weight whose width or alignment is not a multiple of
+ * 128 bytes or 16.
+ */
+typedef enum { MUON_REDUCE_NONE = 0, MUON_REDUCE_SUM = 1, MUON_REDUCE_MEAN = 2 } muon_reduction;
+typedef struct {
+  int32_t reduction;     /* muon_reduction */
+  float   softcap;       /* 0 = off */
+  int64_t ignore_index;
+} muon_loss_config;
+/* mean, no softcap, ignore_index -100 */
+void muon_loss_config_default(muon_loss_config* cfg);
+muon_status linear_cross_entropy(muon_handle* handle, const muon_matrix* hidden, const muon_matrix* weight,
+                                 const void* targets, int target_bytes, const muon_loss_config* cfg, float* loss);
+muon_status linear_cross_entropy_grad(muon_handle* handle, const muon_matrix* hidden, const muon_matrix* weight,
+                                      const void* targets, int target_bytes, const muon_loss_config* cfg,
+                                      const float* grad_out, float* loss, const muon_matrix* dhidden,
+                                      const muon_matrix* dweight);
+
+/* Host-only validation with the rules of the calls above; enqueue nothing, need no device. */
+muon_status muon_check_norm_args(int n, const muon_matrix* grad, const muon_matrix* out, float max_norm,
+                                 const float* norm, const float* coef, char* msg, int msg_len);
+muon_status muon_check_adamw_args(int n, const muon_matrix* grad, const muon_matrix* exp_avg,
+                                  const muon_matrix* exp_avg_sq, const muon_matrix* weight, const muon_matrix* copy,
+                                  const muon_adamw_config* cfg, const float* grad_scale, char* msg, int msg_len);
+muon_status muon_check_loss_args(const muon_matrix* hidden, const muon_matrix* weight, const void* targets,
+                                 int target_bytes, const muon_loss_config* cfg, const float* grad_out,
+                                 const float* loss, const muon_matrix* dhidden, const muon_matrix* dweight,
+                                 char* msg, int msg_len);
+
+/*
  * Profiling of the library's own launches (for roofline reporting): when
  * enabled, each kernel launch is bracketed by HIP events on the handle's
  * stream and its time, its algorithmic flops or bytes are added to totals.

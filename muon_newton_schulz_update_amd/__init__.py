@@ -28,6 +28,9 @@ __all__ = [
     "aurora_orthogonalize", "muon_update", "check_update_args",
     "check_polar_args", "get_handle", "STATUS", "muon_update_static", "MUON_FLAG_SGD_MOMENTUM", "MUON_FLAG_WIDE_ROWS",
     "MUON_FLAG_FP8_GRAM", "MUON_FLAG_CHECK_FINITE", "debug_check_plan",
+    # the rest of a training step (training.py)
+    "linear_cross_entropy", "linear_cross_entropy_grad", "grad_norm", "clip_grad_norm", "scale", "adamw_update",
+    "AdamWConfig", "LossConfig", "check_norm_args", "check_adamw_args", "check_loss_args",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -138,6 +141,23 @@ def load_library() -> ctypes.CDLL:
             "muon_profile_reset": (ctypes.c_int, [ctypes.c_void_p]),
             "muon_profile_read": (ctypes.c_int, [ctypes.c_void_p, P(MuonProfile)]),
         }
+        M, F, V, I = P(MuonMatrix), ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+        # the training-step entry points (training.py): device scalars and
+        # vectors travel as addresses, configurations by reference
+        text = [ctypes.c_char_p, I]
+        sig.update({
+            "muon_grad_norm": (I, [V, I, M, F, V, V]),
+            "muon_clip_grad_norm": (I, [V, I, M, M, F, V, V]),
+            "muon_scale": (I, [V, I, M, M, V]),
+            "muon_adamw_config_default": (None, [V]),
+            "adamw_update": (I, [V, I, M, M, M, M, M, V, V]),
+            "muon_loss_config_default": (None, [V]),
+            "linear_cross_entropy": (I, [V, M, M, V, I, V, V]),
+            "linear_cross_entropy_grad": (I, [V, M, M, V, I, V, V, V, M, M]),
+            "muon_check_norm_args": (I, [I, M, M, F, V, V] + text),
+            "muon_check_adamw_args": (I, [I, M, M, M, M, M, V, V] + text),
+            "muon_check_loss_args": (I, [M, M, V, I, V, V, V, M, M] + text),
+        })
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
             fn.restype = res
@@ -402,3 +422,8 @@ def check_polar_args(inputs, outputs, cfg=None) -> tuple[int, str]:
     rc = lib.muon_check_polar_args(len(inputs), _array(list(inputs)), _array(list(outputs)),
                                    ctypes.byref(cfg) if cfg is not None else None, buf, 256)
     return rc, buf.value.decode()
+
+
+from .training import (AdamWConfig, LossConfig, adamw_update, check_adamw_args, check_loss_args,  # noqa: E402
+                       check_norm_args, clip_grad_norm, grad_norm, linear_cross_entropy, linear_cross_entropy_grad,
+                       scale)

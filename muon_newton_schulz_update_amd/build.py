@@ -21,8 +21,9 @@ LIB = os.path.join(PKG, "libmuon.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-DEVICE_SOURCES = ["ns_gemm.hip", "stream_kernels.hip", "static_scratch.hip"]
-HOST_SOURCES = ["api.cpp", "validate.cpp"]
+DEVICE_SOURCES = ["ns_gemm.hip", "stream_kernels.hip", "static_scratch.hip", "train_kernels.hip",
+                  "head_kernels.hip"]
+HOST_SOURCES = ["api.cpp", "train_api.cpp", "validate.cpp"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",
           f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}"]

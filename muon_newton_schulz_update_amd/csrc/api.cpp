@@ -35,6 +35,7 @@
 #include <vector>
 
 #include "../../include/libmuon.h"
+#include "handle.hpp"
 #include "muon_device.hpp"
 #include "validate.hpp"
 
@@ -298,6 +299,7 @@ struct muon_handle {
   hipEvent_t static_done = nullptr;
   bool static_pending = false;
   bool in_static = false;    // inside muon_update_static: no profiling events
+  muon::TrainState train;    // buffers of the training-step entry points (train_api.cpp)
   std::string err;
   // profiling
   bool prof = false;
@@ -1448,6 +1450,8 @@ extern "C" muon_status muon_destroy(muon_handle* h) {
   for (auto& kv : h->plans)
     if (kv.second->meta_dev) (void)hipFree(kv.second->meta_dev);
   if (h->ws) (void)hipFree(h->ws);
+  if (h->train.head.ptr) (void)hipFree(h->train.head.ptr);
+  if (h->train.norm.ptr) (void)hipFree(h->train.norm.ptr);
   if (h->pinned) (void)hipHostFree(h->pinned);
   if (h->upload_done) (void)hipEventDestroy(h->upload_done);
   if (h->static_done) (void)hipEventDestroy(h->static_done);
@@ -1465,6 +1469,29 @@ extern "C" muon_status muon_destroy(muon_handle* h) {
   delete h;
   return MUON_OK;
 }
+
+namespace muon {
+TrainState& train_state(muon_handle* h) { return h->train; }
+hipStream_t handle_stream(const muon_handle* h) { return h->stream; }
+int handle_device(const muon_handle* h) { return h->device; }
+muon_status handle_error(muon_handle* h, muon_status code, const std::string& msg) { return set_err(h, code, msg); }
+void handle_clear_error(muon_handle* h) { h->err.clear(); }
+// Work already enqueued may still read the old buffer: the stream drains first.
+muon_status grow(muon_handle* h, GrowBuffer& b, size_t bytes, const char* what) {
+  if (bytes <= b.bytes && b.ptr) return MUON_OK;
+  HIP_TRY(h, hipStreamSynchronize(h->stream));
+  if (b.ptr) HIP_TRY(h, hipFree(b.ptr));
+  b.ptr = nullptr;
+  b.bytes = 0;
+  if (hipMalloc(&b.ptr, bytes) != hipSuccess) {
+    b.ptr = nullptr;
+    (void)hipGetLastError();
+    return set_err(h, MUON_ERR_ALLOC, std::string(what) + " workspace of " + std::to_string(bytes) + " bytes: allocation failed");
+  }
+  b.bytes = bytes;
+  return MUON_OK;
+}
+}  // namespace muon
 
 extern "C" muon_status muon_set_stream(muon_handle* h, void* stream) {
   if (!h) return MUON_ERR_INVALID_ARG;

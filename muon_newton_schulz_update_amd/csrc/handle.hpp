@@ -1,0 +1,32 @@
+// What the training-step entry points (train_api.cpp) use of a handle whose
+// definition is api.cpp's.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <string>
+
+#include "../../include/libmuon.h"
+
+namespace muon {
+
+// A device buffer that grows on demand and is freed with the handle. Each
+// user has its own: the Newton-Schulz workspace keeps zero padding that no
+// other kernel may write.
+struct GrowBuffer {
+  void* ptr = nullptr;
+  size_t bytes = 0;
+};
+struct TrainState {
+  GrowBuffer head;            // cross entropy pieces
+  GrowBuffer norm;            // NormState
+  bool norm_clean = false;    // the norm kernel's ticket is 0
+};
+
+TrainState& train_state(muon_handle* h);
+hipStream_t handle_stream(const muon_handle* h);
+int handle_device(const muon_handle* h);
+muon_status handle_error(muon_handle* h, muon_status code, const std::string& msg);
+void handle_clear_error(muon_handle* h);
+muon_status grow(muon_handle* h, GrowBuffer& b, size_t bytes, const char* what);
+
+}  // namespace muon

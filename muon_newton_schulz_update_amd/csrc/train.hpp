@@ -1,0 +1,153 @@
+// Descriptors shared by the training-step kernels (train_kernels.hip,
+// head_kernels.hip) and their host code (train_api.cpp).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/libmuon.h"
+
+namespace muon {
+
+// ---------------------------------------------------------------------------
+// Tensor lists (gradient norm, scaling, AdamW). A list travels in the kernel
+// arguments, up to kListMax tensors a launch, so a call uploads nothing and
+// can be captured in a graph; longer lists take more launches.
+// ---------------------------------------------------------------------------
+constexpr int kChunk = 8192;      // elements per work item of a list kernel
+constexpr int kNormMax = 88;      // tensors per norm or scale launch
+constexpr int kAdamMax = 32;      // tensors per AdamW launch
+constexpr int kNormBlocks = 2048; // blocks of a norm launch at most (one partial each)
+
+struct ListItem {      // one tensor: 40 bytes
+  const void* src;
+  int64_t ld;          // row stride, elements
+  int64_t cols;
+  int64_t n;           // rows * cols
+  int32_t dt;          // MUON_F32 / MUON_BF16
+  int32_t flat;        // 1: one contiguous run with 16-byte aligned start
+};
+struct NormList {
+  int32_t n;
+  int32_t chunk0[kNormMax + 1];   // first work item of each tensor
+  ListItem t[kNormMax];
+};
+static_assert(sizeof(NormList) <= 4000, "kernel arguments");
+
+// One destination beside one source (scaling).
+constexpr int kScaleMax = 56;
+struct ScaleItem {
+  const void* src;
+  void* dst;
+  int64_t ld_src, ld_dst, cols, n;
+  int32_t dt;          // bit 0: source bf16, bit 1: destination bf16, bit 2: flat
+};
+struct ScaleList {
+  int32_t n;
+  int32_t chunk0[kScaleMax + 1];
+  ScaleItem t[kScaleMax];
+};
+static_assert(sizeof(ScaleList) <= 4000, "kernel arguments");
+
+struct AdamItem {
+  const void* g;
+  float* m;
+  float* v;
+  void* w;
+  void* copy;          // or null
+  int64_t ld[5];       // of g, m, v, w, copy
+  int64_t cols, n;
+  int32_t dt;          // bit 0: g bf16, bit 1: w bf16, bit 2: copy bf16, bit 3: flat
+};
+struct AdamList {
+  int32_t n;
+  int32_t chunk0[kAdamMax + 1];
+  AdamItem t[kAdamMax];
+};
+static_assert(sizeof(AdamList) <= 4000, "kernel arguments");
+
+struct AdamConst {
+  float beta1, c1;      // 1 - beta1
+  float beta2, c2;
+  float keep;           // 1 - lr weight_decay
+  float lr1;            // lr / (1 - beta1^step)
+  float rs2;            // 1 / sqrt(1 - beta2^step)
+  float eps;
+};
+
+// The norm kernel's state in the handle's workspace.
+struct NormState {
+  uint32_t ticket;      // blocks done; the last one of a call sets it back to 0
+  uint32_t pad[3];
+  double part[1];       // one partial per block of every launch of the call
+};
+
+hipError_t launch_norm(const NormList& L, int blocks, int chunks, NormState* st, int part0, int total_blocks,
+                       float max_norm, float* norm, float* coef, hipStream_t s);
+hipError_t launch_norm_reset(NormState* st, hipStream_t s);
+hipError_t launch_norm_empty(float max_norm, float* norm, float* coef, hipStream_t s);
+hipError_t launch_scale(const ScaleList& L, int chunks, const float* coef, int in_place, hipStream_t s);
+hipError_t launch_adamw(const AdamList& L, int chunks, const AdamConst& c, const float* scale, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Head cross entropy. The valid tokens (target != ignore_index) are gathered
+// into a compact order and taken in pieces of at most `piece` tokens.
+//
+// Panel layout of the per-piece matrices (rows = tokens, contraction over
+// either index): blocks of 64 tokens; in a block, columns in 16-byte chunks,
+// chunk after chunk, each chunk for the block's 64 tokens in turn. A stage of
+// a product over tokens or over columns is then whole kilobytes either way.
+// ---------------------------------------------------------------------------
+constexpr int kPanelRows = 64;
+template <typename T>
+__host__ __device__ inline int64_t panel_at(int64_t row, int64_t col, int64_t ld) {
+  constexpr int ch = 16 / (int)sizeof(T);
+  return ((row / kPanelRows) * (ld / ch) + col / ch) * (kPanelRows * ch) + (row % kPanelRows) * ch + col % ch;
+}
+
+struct HeadArgs {
+  const void* h;   int64_t ld_h;
+  const void* w;   int64_t ld_w;      // the caller's weight, or its padded copy
+  void* dh;        int64_t ld_dh;
+  void* dw;        int64_t ld_dw;
+  int32_t n, v, d;                    // tokens, vocabulary, width
+  int32_t dp, vp;                     // padded width (64 or 32 elements), padded vocabulary (256)
+  int32_t vtile, n_vt;                // columns per logits tile, tiles
+  int32_t piece, row0;                // tokens per piece, first compact token of this piece
+  int32_t per_token;                  // reduction none
+  int32_t mean;
+  float softcap;
+  // workspace
+  int32_t* count;                     // [0] valid tokens
+  int32_t* idx;                       // compact -> token
+  int32_t* tgt;                       // compact -> target, -1: out of range
+  float* lossc;                       // compact losses
+  void* hp;                           // piece x dp panels of the gathered hidden states
+  void* e;                            // piece x vp panels: exponentials, then the logits' gradient
+  float* tmax;                        // n_vt x piece: integer power-of-two reference of each tile's row
+  float* tsum;                        // n_vt x piece: sum of the tile's exponentials without the target's
+  float* zt;                          // piece: the target's logit
+  float4* rs;                         // piece: {reference, factor, target's gradient, 0}
+  float* part;                        // dH partial sums: split x piece x dp
+  int32_t split;
+  float* dwacc;                       // v x dp fp32 sum over pieces, or null: one piece
+  int32_t first, last;                // this piece starts / ends the sum over pieces
+  float* loss;                        // caller's: one value, or n
+  const float* grad_out;              // device, or null (1)
+};
+
+// Per-token reference and factors written by the merge kernel.
+hipError_t launch_head_compact(const HeadArgs& a, const void* targets, int target_bytes, int64_t ignore,
+                               hipStream_t s);
+hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s);
+hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v, int d, int dp, int dt,
+                                   hipStream_t s);
+hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s);
+hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s);
+hipError_t launch_head_total(const HeadArgs& a, hipStream_t s);
+hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s);
+hipError_t launch_head_dhidden(const HeadArgs& a, int dt, hipStream_t s);
+hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, const void* targets, int target_bytes, int64_t ignore,
+                                   hipStream_t s);
+hipError_t launch_head_dweight(const HeadArgs& a, int dt, hipStream_t s);
+
+}  // namespace muon

@@ -231,7 +231,224 @@ int check_update(int n, const muon_matrix* g, const muon_matrix* m, const muon_m
   return check_overlaps(v, false, msg, len);
 }
 
+// ---------------------------------------------------------------------------
+// Training-step entry points. Their tensors are not tied to the matrix limits
+// of the Newton-Schulz engine: vectors of any length and tall embeddings.
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_tensor(const muon_matrix& m, const char* what, int i, char* msg, int len) {
+  if (m.dtype != MUON_F32 && m.dtype != MUON_BF16)
+    return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "%s[%d]: dtype %d is not MUON_F32 or MUON_BF16", what, i,
+                (int)m.dtype);
+  if (m.rows < 0 || m.cols < 0)
+    return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "%s[%d]: negative shape %lld x %lld", what, i,
+                (long long)m.rows, (long long)m.cols);
+  if (m.rows == 0 || m.cols == 0) return MUON_OK;
+  if (!m.ptr) return fail(msg, len, MUON_ERR_INVALID_ARG, "%s[%d]: NULL pointer for a non-empty tensor", what, i);
+  if (m.rows > kMaxListElems || m.cols > kMaxListElems || m.rows > kMaxListElems / m.cols)
+    return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "%s[%d]: %lld x %lld exceeds 2^42 elements", what, i,
+                (long long)m.rows, (long long)m.cols);
+  if (m.rows > 1 && m.ld < m.cols)
+    return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "%s[%d]: ld %lld < cols %lld", what, i, (long long)m.ld,
+                (long long)m.cols);
+  if (m.rows > 1 && m.ld > kMaxLd)
+    return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "%s[%d]: ld %lld exceeds 2^40", what, i, (long long)m.ld);
+  if (((uintptr_t)m.ptr) % (uintptr_t)elem_size(m.dtype) != 0)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "%s[%d]: pointer not aligned to its element size", what, i);
+  return MUON_OK;
+}
+
+// A single row has no stride of its own: the span takes its length.
+Span tensor_span(muon_matrix m, const char* what, int idx, bool writes) {
+  if (m.rows == 1) m.ld = m.cols;
+  return make_span(m, what, idx, writes);
+}
+
+bool same_buffer(const muon_matrix& a, const muon_matrix& b) {
+  return a.ptr == b.ptr && a.dtype == b.dtype && a.rows == b.rows && a.cols == b.cols &&
+         (a.rows <= 1 || a.ld == b.ld);
+}
+
+// Device scalars and vectors as one-row spans.
+Span flat_span(const void* p, int64_t bytes, const char* what, bool writes) {
+  Span s;
+  s.lo = (u128)(uintptr_t)p;
+  s.ldb = s.rowb = (u128)bytes;
+  s.hi = s.lo + (u128)bytes;
+  s.rows = 1;
+  s.what = what;
+  s.idx = 0;
+  s.writes = writes;
+  return s;
+}
+
+}  // namespace
+
+int check_norm(int n, const muon_matrix* g, const muon_matrix* out, float max_norm, const float* norm,
+               const float* coef, int writes, char* msg, int len) {
+  if (msg && len > 0) msg[0] = 0;
+  if (n < 0 || n > kMaxBatch) return fail(msg, len, MUON_ERR_INVALID_ARG, "list length %d outside [0, %d]", n, kMaxBatch);
+  if (n > 0 && !g) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL grad array");
+  if (!norm) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL norm or coefficient");
+  if (((uintptr_t)norm | (uintptr_t)coef) % 4 != 0)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "norm or coefficient not aligned to 4 bytes");
+  if (coef && !(max_norm > 0.0f)) return fail(msg, len, MUON_ERR_INVALID_ARG, "max_norm must be positive");
+  int rc;
+  for (int i = 0; i < n; ++i) {
+    if ((rc = check_tensor(g[i], "grad", i, msg, len))) return rc;
+    if (!out) continue;
+    if ((rc = check_tensor(out[i], "out", i, msg, len))) return rc;
+    if ((rc = same_shape(g[i], out[i], "grad", "out", i, msg, len))) return rc;
+  }
+  // the kernels read a tensor again after they wrote others: an output shares
+  // memory with nothing but the input it replaces, element for element
+  std::vector<Span> v;
+  for (int i = 0; i < n; ++i) {
+    if (!nonempty(g[i])) continue;
+    const bool own = !out || same_buffer(g[i], out[i]);
+    v.push_back(tensor_span(g[i], "grad", i, own && writes));
+    if (!own) v.push_back(tensor_span(out[i], "out", i, true));
+  }
+  if (norm != coef) v.push_back(flat_span(norm, 4, "norm", true));
+  if (coef) v.push_back(flat_span(coef, 4, "coefficient", norm != coef));
+  return check_overlaps(v, false, msg, len);
+}
+
+int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_matrix* v, const muon_matrix* w,
+                const muon_matrix* copy, const muon_adamw_config* c, const float* scale, char* msg, int len) {
+  if (msg && len > 0) msg[0] = 0;
+  if (n < 0 || n > kMaxBatch) return fail(msg, len, MUON_ERR_INVALID_ARG, "list length %d outside [0, %d]", n, kMaxBatch);
+  if (n > 0 && (!g || !m || !v || !w)) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL tensor array");
+  if (!c) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL configuration");
+  if (!finitef(c->lr)) return fail(msg, len, MUON_ERR_INVALID_ARG, "lr must be finite");
+  if (!(c->beta1 >= 0.0f && c->beta1 < 1.0f) || !(c->beta2 >= 0.0f && c->beta2 < 1.0f))
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "betas %g, %g outside [0, 1)", c->beta1, c->beta2);
+  if (!(c->eps >= 0.0f) || !finitef(c->eps)) return fail(msg, len, MUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!(c->weight_decay >= 0.0f) || !finitef(c->weight_decay))
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "weight_decay must be finite and >= 0");
+  if (c->step < 1) return fail(msg, len, MUON_ERR_INVALID_ARG, "step %lld: the first step is 1", (long long)c->step);
+  if ((uintptr_t)scale % 4 != 0) return fail(msg, len, MUON_ERR_INVALID_ARG, "grad_scale not aligned to 4 bytes");
+  int rc;
+  std::vector<Span> spans;
+  for (int i = 0; i < n; ++i) {
+    if ((rc = check_tensor(w[i], "weight", i, msg, len))) return rc;
+    const muon_matrix* xs[] = {&g[i], &m[i], &v[i]};
+    const char* names[] = {"grad", "exp_avg", "exp_avg_sq"};
+    for (int k = 0; k < 3; ++k) {
+      if ((rc = check_tensor(*xs[k], names[k], i, msg, len))) return rc;
+      if ((rc = same_shape(w[i], *xs[k], "weight", names[k], i, msg, len))) return rc;
+      if (k && xs[k]->dtype != MUON_F32)
+        return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "%s[%d] must be MUON_F32", names[k], i);
+    }
+    const bool cp = copy && nonempty(copy[i]);
+    if (cp) {
+      if ((rc = check_tensor(copy[i], "copy", i, msg, len))) return rc;
+      if ((rc = same_shape(w[i], copy[i], "weight", "copy", i, msg, len))) return rc;
+    }
+    if (!nonempty(w[i])) continue;
+    spans.push_back(tensor_span(g[i], "grad", i, false));
+    spans.push_back(tensor_span(m[i], "exp_avg", i, true));
+    spans.push_back(tensor_span(v[i], "exp_avg_sq", i, true));
+    spans.push_back(tensor_span(w[i], "weight", i, true));
+    if (cp) spans.push_back(tensor_span(copy[i], "copy", i, true));
+  }
+  if (scale) spans.push_back(flat_span(scale, 4, "grad_scale", false));
+  return check_overlaps(spans, false, msg, len);
+}
+
+int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
+               const muon_loss_config* c, const float* grad_out, const float* loss, const muon_matrix* dh,
+               const muon_matrix* dw, int grad, char* msg, int len) {
+  if (msg && len > 0) msg[0] = 0;
+  if (!hidden || !weight) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL hidden or weight");
+  if (grad && !dh && !dw) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL dhidden and dweight");
+  if (target_bytes != 4 && target_bytes != 8)
+    return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "targets of %d bytes: 4 or 8 are supported", target_bytes);
+  if (c->reduction != MUON_REDUCE_NONE && c->reduction != MUON_REDUCE_SUM && c->reduction != MUON_REDUCE_MEAN)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "unknown reduction %d", (int)c->reduction);
+  if (!(c->softcap >= 0.0f) || !finitef(c->softcap))
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  int rc;
+  if ((rc = check_tensor(*hidden, "hidden", 0, msg, len))) return rc;
+  if ((rc = check_tensor(*weight, "weight", 0, msg, len))) return rc;
+  if (weight->rows < 1 || weight->cols < 1)
+    return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "weight is %lld x %lld: at least one row and column are needed",
+                (long long)weight->rows, (long long)weight->cols);
+  if (hidden->cols != weight->cols)
+    return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "hidden has %lld columns, weight %lld", (long long)hidden->cols,
+                (long long)weight->cols);
+  if (hidden->dtype != weight->dtype)
+    return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "hidden and weight have different types");
+  if (hidden->rows > (1 << 24) || weight->rows > kMaxVocab || weight->cols > kMaxDim)
+    return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "%lld tokens, %lld x %lld weight: past 2^24, 2^22, %d",
+                (long long)hidden->rows, (long long)weight->rows, (long long)weight->cols, kMaxDim);
+  const int64_t n = hidden->rows;
+  if (n > 0 && !targets) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL targets");
+  if ((uintptr_t)targets % (uintptr_t)target_bytes != 0 || ((uintptr_t)loss | (uintptr_t)grad_out) % 4 != 0)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "targets, loss or grad_out not aligned to their element size");
+  const int64_t each = c->reduction == MUON_REDUCE_NONE ? n : 1;
+  if (each > 0 && !loss) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL loss");
+  std::vector<Span> v;
+  if (n > 0) v.push_back(tensor_span(*hidden, "hidden", 0, false));
+  v.push_back(tensor_span(*weight, "weight", 0, false));
+  if (n > 0) v.push_back(flat_span(targets, n * target_bytes, "targets", false));
+  if (each > 0) v.push_back(flat_span(loss, each * 4, "loss", true));
+  const muon_matrix* in[] = {hidden, weight};
+  const muon_matrix* out[] = {dh, dw};
+  const char* from[] = {"hidden", "weight"};
+  const char* to[] = {"dhidden", "dweight"};
+  for (int k = 0; grad && k < 2; ++k) {
+    if (!out[k]) continue;
+    if ((rc = check_tensor(*out[k], to[k], 0, msg, len))) return rc;
+    if ((rc = same_shape(*in[k], *out[k], from[k], to[k], 0, msg, len))) return rc;
+    if (out[k]->dtype != in[k]->dtype)
+      return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "%s has not the type of %s", to[k], from[k]);
+    if (nonempty(*out[k])) v.push_back(tensor_span(*out[k], to[k], 0, true));
+  }
+  if (grad && grad_out && each > 0) v.push_back(flat_span(grad_out, each * 4, "grad_out", false));
+  return check_overlaps(v, false, msg, len);
+}
+
 }  // namespace muon
+
+extern "C" muon_status muon_check_norm_args(int n, const muon_matrix* grad, const muon_matrix* out, float max_norm,
+                                            const float* norm, const float* coef, char* msg, int msg_len) {
+  return muon::check_norm(n, grad, out, max_norm, norm, coef, out != nullptr, msg, msg_len);
+}
+extern "C" muon_status muon_check_adamw_args(int n, const muon_matrix* grad, const muon_matrix* exp_avg,
+                                             const muon_matrix* exp_avg_sq, const muon_matrix* weight,
+                                             const muon_matrix* copy, const muon_adamw_config* cfg,
+                                             const float* grad_scale, char* msg, int msg_len) {
+  return muon::check_adamw(n, grad, exp_avg, exp_avg_sq, weight, copy, cfg, grad_scale, msg, msg_len);
+}
+extern "C" muon_status muon_check_loss_args(const muon_matrix* hidden, const muon_matrix* weight, const void* targets,
+                                            int target_bytes, const muon_loss_config* cfg, const float* grad_out,
+                                            const float* loss, const muon_matrix* dhidden, const muon_matrix* dweight,
+                                            char* msg, int msg_len) {
+  muon_loss_config c;
+  muon_loss_config_default(&c);
+  if (cfg) c = *cfg;
+  return muon::check_loss(hidden, weight, targets, target_bytes, &c, grad_out, loss, dhidden, dweight,
+                          dhidden || dweight ? 1 : 0, msg, msg_len);
+}
+
+extern "C" void muon_loss_config_default(muon_loss_config* c) {
+  if (!c) return;
+  c->reduction = MUON_REDUCE_MEAN;
+  c->softcap = 0.0f;
+  c->ignore_index = -100;
+}
+
+extern "C" void muon_adamw_config_default(muon_adamw_config* c) {
+  if (!c) return;
+  c->lr = 0.01f;
+  c->beta1 = 0.8f;
+  c->beta2 = 0.95f;
+  c->eps = 1e-10f;
+  c->weight_decay = 0.0f;
+  c->step = 1;
+}
 
 extern "C" muon_status muon_check_update_args(int n, const muon_matrix* grad, const muon_matrix* momentum,
                                               const muon_matrix* weight, const muon_matrix* update_out,

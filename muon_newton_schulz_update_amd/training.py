@@ -1,0 +1,348 @@
+"""The rest of a training step around the Muon update: the head's softmax
+cross entropy with its gradient, the global gradient norm with clipping, and
+AdamW for the parameters Muon does not take. Argument marshalling only, like
+the package's other entry points; the kernels are reached through libmuon's C
+ABI (include/libmuon.h).
+
+    loss = mu.linear_cross_entropy(hidden, head, targets)      # differentiable
+    loss, dhidden, dhead = mu.linear_cross_entropy_grad(hidden, head, targets)
+    norm, coef = mu.grad_norm(grads, max_norm=1.0)             # both stay on the device
+    mu.adamw_update(grads, exp_avgs, exp_avg_sqs, weights, step=1, lr=3e-3, grad_scale=coef)
+    norm = mu.clip_grad_norm(matrix_grads, 1.0)                # in place
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Sequence
+
+import torch
+
+from . import (MuonMatrix, MUON_BF16, MUON_F32, _DT, get_handle, load_library)
+
+REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+
+
+class AdamWConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
+                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("step", ctypes.c_int64)]
+
+
+class LossConfig(ctypes.Structure):
+    _fields_ = [("reduction", ctypes.c_int32), ("softcap", ctypes.c_float), ("ignore_index", ctypes.c_int64)]
+
+
+# ---------------------------------------------------------------------------
+# descriptors: a list is packed as five 64-bit words a tensor (MuonMatrix)
+# ---------------------------------------------------------------------------
+_WORDS = ctypes.sizeof(MuonMatrix) // 8
+_CODE = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
+
+
+def _words(t: torch.Tensor, what: str, device: int, out: list) -> None:
+    """Append a tensor's descriptor: a matrix with its row stride, anything
+    else (a vector, a contiguous tensor of more dimensions) as one row."""
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: dtype {t.dtype} is not float32 or bfloat16")
+    if t.dim() == 2:
+        rows, cols = t.shape
+        if t.stride(1) != 1 and cols > 1 and rows:
+            raise ValueError(f"{what}: columns must be contiguous (stride(1) == 1)")
+        ld = t.stride(0) if rows > 1 else cols
+    else:
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: a tensor that is not a matrix must be contiguous")
+        rows, cols = 1, t.numel()
+        ld = cols
+    if rows and cols and t.get_device() != device:
+        raise ValueError(f"{what}: expected a tensor on GPU {device}, got {t.device}")
+    out += (t.data_ptr(), rows, cols, ld, code)
+
+
+_EMPTY = (0, 0, 0, 0, MUON_F32)
+
+
+def _pack(words: list):
+    return ctypes.cast((ctypes.c_int64 * max(_WORDS, len(words)))(*words), ctypes.POINTER(MuonMatrix))
+
+
+def _list(tensors: Sequence[torch.Tensor], what: str, device: int):
+    words: list = []
+    for t in tensors:
+        _words(t, what, device, words)
+    return _pack(words)
+
+
+def _same_shapes(a, b, what_a, what_b):
+    if len(a) != len(b):
+        raise ValueError(f"{what_a} and {what_b} differ in length")
+    for i, (x, y) in enumerate(zip(a, b)):
+        if x.shape != y.shape:
+            raise ValueError(f"{what_b}[{i}] has shape {tuple(y.shape)}, {what_a}[{i}] {tuple(x.shape)}")
+
+
+def _handle_for(tensors, handle):
+    if handle is None:
+        device = next((t.get_device() for t in tensors if t.is_cuda), None)
+        handle = get_handle(device)
+    handle._bind_stream()
+    return handle
+
+
+def _scalar(t: torch.Tensor | None, what: str, device: int, n: int | None = None):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.get_device() != device:
+        raise ValueError(f"{what}: expected float32 on GPU {device}, got {t.dtype} on {t.device}")
+    if t.numel() != (1 if n is None else n) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {1 if n is None else n} contiguous values, got shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+# ---------------------------------------------------------------------------
+# gradient norm and clipping
+# ---------------------------------------------------------------------------
+def grad_norm(grads: Sequence[torch.Tensor], *, max_norm: float | None = None, handle=None):
+    """Global 2-norm of a list of gradients (libmuon `muon_grad_norm`), a
+    float32 scalar on the device. With max_norm also the clipping coefficient
+    min(1, max_norm / (norm + 1e-6)): (norm, coef), for `adamw_update`'s
+    grad_scale. Nothing waits for the GPU."""
+    grads = list(grads)
+    h = _handle_for(grads, handle)
+    out = torch.empty(2, device=f"cuda:{h.device}", dtype=torch.float32)
+    at = out.data_ptr()
+    h._check(h._lib.muon_grad_norm(h.ptr, len(grads), _list(grads, "grad", h.device),
+                                   0.0 if max_norm is None else float(max_norm), at,
+                                   None if max_norm is None else at + 4))
+    return out[0] if max_norm is None else (out[0], out[1])
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Sequence[torch.Tensor] | None = None,
+                   handle=None) -> torch.Tensor:
+    """Scale gradients so that their global norm is at most max_norm (libmuon
+    `muon_clip_grad_norm`), in place or into `out`, and return the norm before
+    clipping. In place, nothing is written when the norm is within the limit."""
+    grads = list(grads)
+    h = _handle_for(grads, handle)
+    outs = None
+    if out is not None:
+        out = list(out)
+        _same_shapes(grads, out, "grads", "out")
+        outs = _list(out, "out", h.device)
+    both = torch.empty(2, device=f"cuda:{h.device}", dtype=torch.float32)
+    at = both.data_ptr()
+    h._check(h._lib.muon_clip_grad_norm(h.ptr, len(grads), _list(grads, "grad", h.device), outs, float(max_norm), at,
+                                        at + 4))
+    return both[0]
+
+
+def scale(tensors: Sequence[torch.Tensor], coef: torch.Tensor, *, out: Sequence[torch.Tensor] | None = None,
+          handle=None) -> None:
+    """Multiply tensors by a scalar that lives on the device (libmuon
+    `muon_scale`), in place or into `out`."""
+    tensors = list(tensors)
+    h = _handle_for(tensors, handle)
+    outs = None
+    if out is not None:
+        out = list(out)
+        _same_shapes(tensors, out, "tensors", "out")
+        outs = _list(out, "out", h.device)
+    h._check(h._lib.muon_scale(h.ptr, len(tensors), _list(tensors, "tensor", h.device), outs,
+                               _scalar(coef, "coef", h.device)))
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+def adamw_update(grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
+                 exp_avg_sqs: Sequence[torch.Tensor], weights: Sequence[torch.Tensor], *, step: int,
+                 lr: float | None = None, beta1: float | None = None, beta2: float | None = None,
+                 eps: float | None = None, weight_decay: float | None = None,
+                 grad_scale: torch.Tensor | None = None,
+                 copies: Sequence[torch.Tensor | None] | None = None, handle=None) -> None:
+    """One AdamW step in place (libmuon `adamw_update`); what is not given has
+    the library's default. grad_scale: a float32 device scalar that multiplies
+    every gradient (`grad_norm`'s coefficient). copies[i], when given, receives
+    the new weight, for a model that computes on 16-bit copies of 32-bit ones."""
+    grads, exp_avgs, exp_avg_sqs, weights = list(grads), list(exp_avgs), list(exp_avg_sqs), list(weights)
+    _same_shapes(weights, grads, "weights", "grads")
+    _same_shapes(weights, exp_avgs, "weights", "exp_avgs")
+    _same_shapes(weights, exp_avg_sqs, "weights", "exp_avg_sqs")
+    h = _handle_for(weights, handle)
+    cp = None
+    if copies is not None:
+        if len(copies) != len(weights):
+            raise ValueError("weights and copies differ in length")
+        words: list = []
+        for i, (c, w) in enumerate(zip(copies, weights)):
+            if c is None:
+                words += _EMPTY
+                continue
+            if c.shape != w.shape:
+                raise ValueError(f"copies[{i}] has shape {tuple(c.shape)}, weights[{i}] {tuple(w.shape)}")
+            _words(c, "copy", h.device, words)
+        cp = _pack(words)
+    cfg = AdamWConfig()
+    h._lib.muon_adamw_config_default(ctypes.byref(cfg))
+    cfg.step = step
+    for name, value in (("lr", lr), ("beta1", beta1), ("beta2", beta2), ("eps", eps), ("weight_decay", weight_decay)):
+        if value is not None:
+            setattr(cfg, name, value)
+    d = h.device
+    h._check(h._lib.adamw_update(h.ptr, len(weights), _list(grads, "grad", d), _list(exp_avgs, "exp_avg", d),
+                                 _list(exp_avg_sqs, "exp_avg_sq", d), _list(weights, "weight", d), cp,
+                                 ctypes.byref(cfg), _scalar(grad_scale, "grad_scale", d)))
+
+
+# ---------------------------------------------------------------------------
+# head cross entropy
+# ---------------------------------------------------------------------------
+def _matrix(t: torch.Tensor, what: str, device: int):
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-D tensor, got shape {tuple(t.shape)}")
+    words: list = []
+    _words(t, what, device, words)
+    return _pack(words)
+
+
+def _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_out, dhidden, dweight, grad, handle):
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"unknown reduction {reduction!r}")
+    if hidden.dim() < 1 or tuple(targets.shape) != tuple(hidden.shape[:-1]):
+        raise ValueError(f"targets of shape {tuple(targets.shape)} for hidden states of {tuple(hidden.shape)}")
+    if targets.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"targets: dtype {targets.dtype} is not int64 or int32")
+    if not targets.is_contiguous():
+        raise ValueError("targets must be contiguous")
+    h = _handle_for((weight, hidden), handle)
+    d = h.device
+    if targets.numel() and targets.get_device() != d:
+        raise ValueError(f"targets: expected a tensor on GPU {d}, got {targets.device}")
+    hid = hidden if hidden.dim() == 2 else hidden.view(-1, hidden.shape[-1])
+    n = hid.shape[0]
+    loss = torch.empty(targets.shape if reduction == "none" else (), device=weight.device, dtype=torch.float32)
+    cfg = LossConfig(REDUCTIONS[reduction], float(softcap), int(ignore_index))
+    args = (h.ptr, _matrix(hid, "hidden", d), _matrix(weight, "weight", d), targets.data_ptr(),
+            targets.element_size(), ctypes.byref(cfg))
+    if not grad:
+        h._check(h._lib.linear_cross_entropy(*args, loss.data_ptr()))
+        return loss, None, None
+    go = _scalar(grad_out, "grad_out", d, n if reduction == "none" else None)
+    dh = dw = None
+    if dhidden is not False:
+        if dhidden is None:
+            dhidden = torch.empty(hidden.shape, device=weight.device, dtype=hidden.dtype)
+        if dhidden.shape != hidden.shape:
+            raise ValueError(f"dhidden of shape {tuple(dhidden.shape)} for hidden states of {tuple(hidden.shape)}")
+        dh = _matrix(dhidden if dhidden.dim() == 2 else dhidden.view(-1, dhidden.shape[-1]), "dhidden", d)
+    if dweight is not False:
+        if dweight is None:
+            dweight = torch.empty(weight.shape, device=weight.device, dtype=weight.dtype)
+        dw = _matrix(dweight, "dweight", d)
+    h._check(h._lib.linear_cross_entropy_grad(*args, go, loss.data_ptr(), dh, dw))
+    return loss, dhidden if dh is not None else None, dweight if dw is not None else None
+
+
+def linear_cross_entropy_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,
+                              ignore_index: int = -100, reduction: str = "mean", softcap: float = 0.0,
+                              grad_out: torch.Tensor | None = None, dhidden: torch.Tensor | None | bool = None,
+                              dweight: torch.Tensor | None | bool = None, handle=None):
+    """(loss, dhidden, dweight): softmax cross entropy of the logits hidden
+    weight^T against targets, and its gradient, in one call (libmuon
+    `linear_cross_entropy_grad`); the logits are never stored as a whole.
+
+    hidden: (..., D), targets: (...) int64 or int32, weight: (V, D). grad_out
+    (float32, on the device): one value that multiplies the gradient, or with
+    reduction "none" one a token. dhidden, dweight: tensors to write to; False
+    leaves that gradient out (and its product)."""
+    return _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_out, dhidden, dweight, True,
+                      handle)
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, ignore_index, reduction, softcap, handle):
+        need_h, need_w = ctx.needs_input_grad[:2]
+        ctx.opts = (ignore_index, reduction, softcap, need_h, need_w)
+        if reduction == "none":
+            # the gradient's weights come with backward: it takes the logits again
+            ctx.save_for_backward(hidden, weight, targets)
+            return _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, None, None, None, False,
+                              handle)[0]
+        loss, dh, dw = _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, None,
+                                  None if need_h else False, None if need_w else False, True, handle)
+        ctx.grads = (dh, dw)
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        ignore_index, reduction, softcap, need_h, need_w = ctx.opts
+        grad_out = grad_out.contiguous()
+        if reduction == "none":
+            hidden, weight, targets = ctx.saved_tensors
+            _, dh, dw = _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_out,
+                                   None if need_h else False, None if need_w else False, True, None)
+        else:
+            if ctx.grads is None:
+                raise RuntimeError("linear_cross_entropy: the gradient was taken before (it is scaled in place)")
+            dh, dw = ctx.grads
+            ctx.grads = None
+            scale([g for g in (dh, dw) if g is not None], grad_out)
+        return dh, dw, None, None, None, None, None
+
+
+def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,
+                         ignore_index: int = -100, reduction: str = "mean", softcap: float = 0.0,
+                         handle=None) -> torch.Tensor:
+    """Softmax cross entropy of the logits hidden weight^T against targets,
+    float32: one value ("mean" over the tokens whose target is not
+    ignore_index, "sum") or one a token ("none", 0 where ignored). The logits
+    are never stored as a whole.
+
+    Differentiable in hidden and weight. "mean" and "sum" compute the gradient
+    with the loss, so one backward per forward; "none" computes it in backward."""
+    if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
+        return _LinearCrossEntropy.apply(hidden, weight, targets, ignore_index, reduction, softcap, handle)
+    return _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, None, None, None, False, handle)[0]
+
+
+# ---------------------------------------------------------------------------
+# host-only validation (no device needed); descriptors may be MuonMatrix objects
+# ---------------------------------------------------------------------------
+def _descriptors(xs):
+    if xs is None:
+        return None
+    arr = (MuonMatrix * max(1, len(xs)))()
+    for i, x in enumerate(xs):
+        arr[i] = x
+    return arr
+
+
+def _checked(call, *args):
+    buf = ctypes.create_string_buffer(256)
+    rc = call(*args, buf, 256)
+    return rc, buf.value.decode()
+
+
+def check_norm_args(grads, out=None, max_norm: float = 1.0, norm=4096, coef=None) -> tuple[int, str]:
+    return _checked(load_library().muon_check_norm_args, len(grads), _descriptors(grads), _descriptors(out), max_norm,
+                    norm, coef)
+
+
+def check_adamw_args(grads, exp_avgs, exp_avg_sqs, weights, copies=None, cfg: AdamWConfig | None = None,
+                     grad_scale=None) -> tuple[int, str]:
+    lib = load_library()
+    if cfg is None:
+        cfg = AdamWConfig()
+        lib.muon_adamw_config_default(ctypes.byref(cfg))
+    return _checked(lib.muon_check_adamw_args, len(weights), _descriptors(grads), _descriptors(exp_avgs),
+                    _descriptors(exp_avg_sqs), _descriptors(weights), _descriptors(copies), ctypes.byref(cfg),
+                    grad_scale)
+
+
+def check_loss_args(hidden, weight, targets=4096, target_bytes=8, cfg: LossConfig | None = None, grad_out=None,
+                    loss=1 << 20, dhidden=None, dweight=None) -> tuple[int, str]:
+    ref = lambda m: ctypes.byref(m) if m is not None else None
+    return _checked(load_library().muon_check_loss_args, ref(hidden), ref(weight), targets, target_bytes, ref(cfg),
+                    grad_out, loss, ref(dhidden), ref(dweight))
