@@ -22,7 +22,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 DEVICE_SOURCES = ["ns_gemm.hip", "stream_kernels.hip", "static_scratch.hip", "train_kernels.hip",
-                  "head_kernels.hip"]
+                  "head_kernels.hip", "head_gemm.hip"]
 HOST_SOURCES = ["api.cpp", "train_api.cpp", "validate.cpp"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",
@@ -51,7 +51,7 @@ def _compile(src: str) -> str:
 def build(jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = DEVICE_SOURCES + HOST_SOURCES
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(4, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
         objs = list(ex.map(_compile, srcs))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]

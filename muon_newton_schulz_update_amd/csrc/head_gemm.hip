@@ -1,0 +1,561 @@
+// Matrix-core products of the head's cross entropy.
+//
+//   logits    z^T = W H^T       vocabulary x tokens, K = width
+//   dhidden   dH  = dz W        tokens x width,      K = vocabulary (split)
+//   dweight   dW  = dz^T H      vocabulary x width,  K = tokens
+//
+// One kernel shape for the three: a 256 x 256 tile per workgroup of 8 waves,
+// K in stages of 128 bytes (64 bf16, 32 fp32), both operands of a stage
+// brought to LDS by direct buffer loads into a ring of five 32 KB slots, so
+// that while one stage feeds the matrix cores the next and half of the one
+// after are on their way. bf16 runs v_mfma_f32_32x32x16_bf16, fp32
+// v_mfma_f32_32x32x2f32.
+//
+// Neither the weight nor the per-piece matrices are ever transposed in
+// memory: an operand whose tile rows are the contraction index is read from
+// LDS with the transposing 64-bit read (bf16: four rows of sixteen columns
+// per sixteen lanes, so two reads make one operand) or with 32-bit reads
+// (fp32). LDS layouts, in 16-byte chunks, and their bank swizzles:
+//   OP_ROW_K    row-major matrix, K along the row: [256 rows][8 chunks],
+//               chunk ^ (row / 2) % 8
+//   OP_ROW_T    row-major matrix, K down the rows: [K rows][columns],
+//               bf16: chunk ^ (row % 4) 4
+//   OP_PANEL_K  panels (train.hpp), K along the chunks: [4 token blocks]
+//               [8 chunks][64 tokens], no conflicts as it is
+//   OP_PANEL_T  panels, K down the tokens: [chunks][K tokens], token ^ (chunk
+//               % 4) 4 (bf16) or chunk % 8 (fp32)
+// Every address is clamped into its matrix: rows and columns past the edge
+// repeat the last ones and their results are not stored (K itself is padded
+// with zeros on one side at least).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "train.hpp"
+
+namespace muon {
+namespace {
+
+typedef unsigned short u16;
+typedef __bf16 bf16x8_t __attribute__((__vector_size__(8 * sizeof(__bf16))));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+
+#define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
+
+enum OpLayout { OP_ROW_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
+enum Product { P_LOGITS, P_DHIDDEN, P_DWEIGHT };
+
+constexpr int kSlot = 32768;      // one operand of one stage
+constexpr int kSlots = 5;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kRefFloor = -3.0e38f;
+
+template <int n>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(n >= 0 && n < 64, "vmcnt immediate");
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x0F70);
+}
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+// A barrier the compiler does not drain the direct loads for; every wait it
+// needs is written before it.
+__device__ __forceinline__ void ring_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+__device__ __forceinline__ u16 f2bf(float f) {
+  unsigned int u = __float_as_uint(f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u16)((u >> 16) | 0x40);
+  u += 0x7FFFu + ((u >> 16) & 1u);
+  return (u16)(u >> 16);
+}
+
+__device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
+
+// Transposing LDS read: sixteen lanes give the addresses of four rows, four
+// 16-bit columns each (lanes 0-3 the first row, ...), and lane l gets column l
+// of the four rows. The pointer is restrict so that the read carries alias
+// information: without any, the compiler waits for every direct load in flight
+// before each such read (plain reads carry a type's; the waits that are needed
+// are in the K loop).
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+__device__ __forceinline__ s16x4_t read_tr16(lds_s16x4_t* __restrict p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
+
+// One operand of a tile's product.
+struct Operand {
+  const uint8_t* base;   // tile start at the first stage
+  uint32_t pitch;        // bytes: row pitch (row layouts), token-block pitch (panels)
+  int lim;               // last valid row (row layouts), last valid chunk (OP_PANEL_T)
+  uint32_t lane;         // this lane's byte offset, the same in every stage
+};
+
+template <typename T, int L>
+struct Op {
+  static constexpr int KE = 128 / (int)sizeof(T);
+  // the lane's part of a load's address (row layouts: the column part)
+  __device__ static uint32_t lane_part(int lane, int wave, int last_chunk) {
+    if constexpr (L == OP_ROW_K) {
+      const int row = 8 * wave + (lane >> 3);
+      return ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+    } else if constexpr (L == OP_ROW_T) {
+      if constexpr (sizeof(T) == 2) {
+        const int row = 2 * wave + (lane >> 5);
+        return min((lane & 31) ^ ((row & 3) << 2), last_chunk) * 16;
+      } else {
+        return min(lane, last_chunk) * 16;
+      }
+    } else if constexpr (L == OP_PANEL_K) {
+      return lane * 16;
+    } else {
+      if constexpr (sizeof(T) == 2) return (lane ^ ((wave & 3) << 2)) * 16;
+      else return (lane >> 5) * 1024 + ((lane & 31) ^ ((2 * wave + (lane >> 5)) & 7)) * 16;
+    }
+  }
+  // direct load i of this wave for stage ks (of the whole K), into slot memory sm
+  __device__ static __forceinline__ void load(const Operand& o, uint8_t* sm, int lane, int wave, int ks, int i) {
+    const uint8_t* p = o.base;
+    uint32_t voff = o.lane, soff = 0;
+    if constexpr (L == OP_ROW_K) {
+      p += (int64_t)ks * 128;
+      voff += __umul24(min(8 * (8 * i + wave) + (lane >> 3), o.lim), o.pitch);
+    } else if constexpr (L == OP_ROW_T) {
+      p += (int64_t)ks * KE * o.pitch;
+      const int row = sizeof(T) == 2 ? 2 * (8 * i + wave) + (lane >> 5) : 8 * i + wave;
+      voff += __umul24(min(row, o.lim - ks * KE), o.pitch);
+    } else if constexpr (L == OP_PANEL_K) {
+      p += (int64_t)ks * 8192;
+      soff = i * o.pitch + wave * 1024;
+    } else {
+      if constexpr (sizeof(T) == 2) {
+        p += (int64_t)ks * o.pitch;
+        soff = min(8 * i + wave, o.lim) * 1024;
+      } else {
+        p += (int64_t)(ks >> 1) * o.pitch + (ks & 1) * 512;
+        soff = min(2 * (8 * i + wave), o.lim - 1) * 1024;
+      }
+    }
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, -1, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(sm + (8 * i + wave) * 1024), 16, voff, soff, 0, 0);
+  }
+  static constexpr int kReads = L == OP_ROW_K || L == OP_PANEL_K ? 1 : sizeof(T) == 2 ? 2 : 4;   // LDS reads a fragment
+  // fragment of rows (columns) at..at+31 for k-step s: lane l holds index
+  // at + l % 32 and the k of chunk 2 s + l / 32
+  template <typename F>
+  __device__ static __forceinline__ F frag(const uint8_t* sm, int lane, int at, int s) {
+    const int lr = lane & 31, hf = lane >> 5;
+    if constexpr (L == OP_ROW_K) {
+      return *(const F*)(sm + (at + lr) * 128 + (((2 * s + hf) ^ ((lr >> 1) & 7)) * 16));
+    } else if constexpr (L == OP_PANEL_K) {
+      return *(const F*)(sm + ((at >> 6) * 8 + 2 * s + hf) * 1024 + ((at & 63) + lr) * 16);
+    } else if constexpr (sizeof(T) == 2) {
+      // sixteen lanes give the addresses of four rows of K, sixteen columns
+      // each, and get a column's four rows back
+      const int i = lane & 15, k = 16 * s + 8 * hf + (i >> 2);
+      const int c = (at >> 3) + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+      s16x4_t q[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int kk = k + 4 * j;
+        const uint8_t* p = L == OP_ROW_T ? sm + kk * 512 + (c ^ ((kk & 3) << 2)) * 16 + (i & 1) * 8
+                                         : sm + c * 1024 + (kk ^ ((c & 3) << 2)) * 16 + (i & 1) * 8;
+        q[j] = read_tr16((lds_s16x4_t*)p);
+      }
+      const s16x8_t v = __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      return __builtin_bit_cast(F, v);
+    } else {
+      F v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 4 * (2 * s + hf) + e, m = at + lr, c = m >> 2;
+        v[e] = L == OP_ROW_T ? *(const float*)(sm + k * 1024 + m * 4)
+                             : *(const float*)(sm + c * 512 + (k ^ (c & 7)) * 16 + (m & 3) * 4);
+      }
+      return v;
+    }
+  }
+};
+
+template <typename T> struct FragOf { typedef bf16x8_t type; };
+template <> struct FragOf<float> { typedef f32x4_t type; };
+
+// The K loop: acc += A B over stages [k0, k1).
+template <typename T, int LA, int LB, int MI, int NI>
+__device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, const Operand& oa, const Operand& ob,
+                                       int lane, int wave, int am, int bn, int k0, int k1) {
+  typedef typename FragOf<T>::type Frag;
+  typedef Op<T, LA> A;
+  typedef Op<T, LB> B;
+  constexpr int LPO = 4;                                   // loads per wave per operand and stage
+  constexpr int kReadStep = MI * A::kReads + NI * B::kReads;
+  constexpr int S = kSlots;
+  Frag fa[2][MI], fb[2][NI];
+  // operand stage o: A (o even) or B (o odd) of stage k0 + o / 2, slot o % 5
+  auto issue = [&](int slot, int o, int i0, int i1) {
+    const int ks = min(k0 + (o >> 1), k1 - 1);
+#pragma unroll
+    for (int i = i0; i < i1; ++i) {
+      if (o & 1) B::load(ob, smem + slot * kSlot, lane, wave, ks, i);
+      else A::load(oa, smem + slot * kSlot, lane, wave, ks, i);
+    }
+  };
+  auto read = [&](int sa, int sb, int s, int buf) {
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) fa[buf][mi] = A::template frag<Frag>(smem + sa * kSlot, lane, am + mi * 32, s);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) fb[buf][ni] = B::template frag<Frag>(smem + sb * kSlot, lane, bn + ni * 32, s);
+  };
+  auto mfmas = [&](int buf) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[buf][mi], fb[buf][ni], acc[mi][ni], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni)
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[buf][mi][e], fb[buf][ni][e], acc[mi][ni], 0, 0, 0);
+    }
+  };
+  auto spread = [&](int loads) {
+    constexpr int nmf = MI * NI * (sizeof(T) == 4 ? 4 : 1);
+    const int nmem = kReadStep + loads;
+#pragma unroll
+    for (int q = 0; q < nmf; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+      for (int t = q * nmem / nmf; t < (q + 1) * nmem / nmf; ++t) {
+        if (t < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+    }
+  };
+  const int nk = k1 - k0;
+  issue(0, 0, 0, LPO);
+  issue(1, 1, 0, LPO);
+  wait_vm<0>();
+  issue(2, 2, 0, LPO);
+  issue(3, 3, 0, LPO / 2);
+  ring_barrier();
+  read(0, 1, 0, 0);
+  int sa = 0, sb = 1, na = 2, nb = 3;   // slots of this stage and the next
+  for (int k = 0; k < nk - 1; ++k) {
+    const int ds = na + 2 >= S ? na + 2 - S : na + 2;
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      if (s == 0) {
+        __builtin_amdgcn_s_setprio(1);
+        __builtin_amdgcn_sched_barrier(0);
+        issue(nb, 2 * k + 3, LPO / 2, LPO);
+      } else {
+        issue(ds, 2 * k + 4, (s - 1) * LPO / 2, s * LPO / 2);
+      }
+      read(sa, sb, s + 1, (s + 1) & 1);
+      mfmas(s & 1);
+      spread(LPO / 2);
+      if (s == 0) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // the next stage has landed (only the operand stage after it may be on
+    // its way); this stage's fragments have been read by every wave
+    wait_lgkm0();
+    wait_vm<LPO>();
+    ring_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(2);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(sa, 2 * k + 5, 0, LPO / 2);
+    read(na, nb, 0, 0);
+    mfmas(1);
+    spread(LPO / 2);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    sa = na;
+    sb = nb;
+    na = na + 2 >= S ? na + 2 - S : na + 2;
+    nb = nb + 2 >= S ? nb + 2 - S : nb + 2;
+  }
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    read(sa, sb, s + 1, (s + 1) & 1);
+    mfmas(s & 1);
+  }
+  mfmas(1);
+  wait_vm<0>();
+}
+
+// Tile order: blocks b, b + 8, ... run on one XCD; each XCD takes runs of 32
+// consecutive tiles, and tiles go down strips of SM rows, so a run shares SM
+// row panels and about 32 / SM column panels in that XCD's L2.
+__device__ __forceinline__ int xcd_index(int b) {
+  const int j = b >> 3;
+  return ((j >> 5) * 8 + (b & 7)) * 32 + (j & 31);
+}
+template <int SM>
+__device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, int& c) {
+  if (idx >= rows * cols) return false;
+  const int strip = idx / (SM * cols), h = min(SM, rows - strip * SM), pos = idx - strip * SM * cols;
+  c = pos / h;
+  r = strip * SM + pos % h;
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// Logits. The vocabulary is on the accumulators' rows and the tokens on their
+// columns, so a lane holds 64 logits of each of its two tokens: maximum and
+// sum need one exchange with the other half-wave. The statistics are per
+// wave's 128 vocabulary rows, so waves never wait for one another. The
+// exponentials go to the panels as whole chunks after a half-wave swap.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(512, 1) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
+  constexpr int MI = 4, NI = 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * kSlot];
+  int vi, ti;
+  const int rows = piece_rows(a), lane = threadIdx.x & 63;
+  if (!strip_tile<4>(xcd_index(blockIdx.x), vt, min(tt, (rows + 255) / 256), vi, ti)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
+  const int v0 = vi * 256, r0 = ti * 256;
+  typedef Op<T, OP_ROW_K> A;
+  typedef Op<T, OP_PANEL_K> B;
+  const Operand oa = {(const uint8_t*)a.w + (int64_t)v0 * a.ld_w * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)),
+                      a.v - 1 - v0, A::lane_part(lane, wave, 0)};
+  const uint32_t blk = (uint32_t)a.dp * sizeof(T) * kPanelRows;
+  const Operand ob = {(const uint8_t*)a.hp + (int64_t)ti * 4 * blk, blk, 0, B::lane_part(lane, wave, 0)};
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
+  k_loop<T, OP_ROW_K, OP_PANEL_K, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 128, wn * 64, 0, a.dp / A::KE);
+
+  const int lr = lane & 31, hf = lane >> 5;
+  const int vw = v0 + wm * 128;                      // the wave's first vocabulary row
+  if (vw >= a.v) return;                             // (the exponentials' padding is cleared with the gradient)
+  const int tile = vi * 2 + wm;
+  if (a.softcap > 0.f) {
+    const float s = 2.f * kLog2e / a.softcap;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          // c tanh(z / c) = c - 2 c / (exp(2 z / c) + 1)
+          const float e = __builtin_amdgcn_exp2f(acc[mi][ni][r] * s);
+          acc[mi][ni][r] = fmaf(-2.f * a.softcap, __builtin_amdgcn_rcpf(e + 1.f), a.softcap);
+        }
+  }
+  const float none = -__builtin_inff();
+  if (vw + 128 > a.v) {
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (vw + mi * 32 + 8 * (r >> 2) + 4 * hf + (r & 3) >= a.v)
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni) acc[mi][ni][r] = none;
+  }
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) {
+    const int r = r0 + wn * 64 + ni * 32 + lr;       // the lane's token in the piece
+    // the target's logit leaves the tile: it has its own place in the sums
+    const int tg = r < rows ? a.tgt[a.row0 + r] - vw : -1;
+    const bool mine = tg >= 0 && tg < 128 && ((tg >> 2) & 1) == hf;
+    if (__any(mine)) {
+      float z = 0.f;
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          if (mine && mi * 32 + 8 * (q >> 2) + 4 * hf + (q & 3) == tg) {
+            z = acc[mi][ni][q];
+            acc[mi][ni][q] = none;
+          }
+      if (mine) a.zt[r] = z;
+    }
+    float top = kRefFloor;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    top = ceilf(fmaxf(top * kLog2e, kRefFloor));
+    float sum = 0.f;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      float e[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        e[q] = __builtin_amdgcn_exp2f(fmaf(acc[mi][ni][q], kLog2e, -top));
+        sum += e[q];
+      }
+      if (!keep) continue;
+      const int64_t col = vw + mi * 32;
+      if constexpr (sizeof(T) == 2) {
+        unsigned int c[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int lo = max((int)((__float_as_uint(e[2 * q]) + 0x1000u) >> 13) - (int)kCodeBase, 0);
+          const int hi = max((int)((__float_as_uint(e[2 * q + 1]) + 0x1000u) >> 13) - (int)kCodeBase, 0);
+          c[q] = (unsigned int)min(lo, 0xFFFF) | (unsigned int)min(hi, 0xFFFF) << 16;
+        }
+        uint8_t* dst = (uint8_t*)a.e + (((int64_t)(r >> 6) * (a.vp >> 3) + (col >> 3)) << 10) + (r & 63) * 16;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          // groups 2 g and 2 g + 1 of four rows: the low half-wave ends up
+          // with the even group's eight rows, the high one with the odd's
+          const u32x2_t x = __builtin_amdgcn_permlane32_swap(c[4 * g], c[4 * g + 2], false, false);
+          const u32x2_t y = __builtin_amdgcn_permlane32_swap(c[4 * g + 1], c[4 * g + 3], false, false);
+          *(u32x4_t*)(dst + ((2 * g + hf) << 10)) = (u32x4_t){x[0], y[0], x[1], y[1]};
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *(f32x4_t*)((float*)a.e + panel_at<float>(r, col + 8 * g + 4 * hf, a.vp)) =
+              (f32x4_t){e[4 * g], e[4 * g + 1], e[4 * g + 2], e[4 * g + 3]};
+      }
+    }
+    sum += __shfl_xor(sum, 32);
+    if (hf == 0) {
+      a.tmax[(int64_t)tile * a.piece + r] = top;
+      a.tsum[(int64_t)tile * a.piece + r] = sum;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dH: partial sums over a range of the vocabulary, 32-bit, row-major.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(512, 1) void k_dhidden_mfma(HeadArgs a, int tt, int dt) {
+  constexpr int MI = 2, NI = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * kSlot];
+  const int rows = piece_rows(a), lane = threadIdx.x & 63;
+  const int nt = min(tt, (rows + 255) / 256), idx = xcd_index(blockIdx.x);
+  if (nt == 0 || idx >= nt * dt * a.split) return;
+  const int q = idx / (nt * dt), t = idx - q * nt * dt, ti = t / dt, di = t - ti * dt;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+  const int r0 = ti * 256, d0 = di * 256;
+  typedef Op<T, OP_PANEL_K> A;
+  typedef Op<T, OP_ROW_T> B;
+  const uint32_t blk = (uint32_t)a.vp * sizeof(T) * kPanelRows;
+  const Operand oa = {(const uint8_t*)a.e + (int64_t)ti * 4 * blk, blk, 0, A::lane_part(lane, wave, 0)};
+  const int chunks = (a.dp - d0) * (int)sizeof(T) / 16;
+  const Operand ob = {(const uint8_t*)a.w + (int64_t)d0 * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)), a.v - 1,
+                      B::lane_part(lane, wave, chunks - 1)};
+  const int nk = (a.v + A::KE - 1) / A::KE;
+  const int k0 = (int)((int64_t)nk * q / a.split), k1 = (int)((int64_t)nk * (q + 1) / a.split);
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
+  if (k1 > k0)
+    k_loop<T, OP_PANEL_K, OP_ROW_T, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * 128, k0, k1);
+  float* out = a.part + (int64_t)q * a.piece * a.dp;
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) {
+    const int d = d0 + wn * 128 + ni * 32 + (lane & 31);
+    if (d >= a.dp) continue;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = r0 + wm * 64 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        out[(int64_t)row * a.dp + d] = acc[mi][ni][r];
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dW: the piece's sum, added to the pieces before it; the last one is scaled
+// and rounded to the weight's type.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(512, 1) void k_dweight_mfma(HeadArgs a, int vt, int dt) {
+  constexpr int MI = 2, NI = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * kSlot];
+  const int rows = piece_rows(a), lane = threadIdx.x & 63;
+  int vi, di;
+  if (!strip_tile<8>(xcd_index(blockIdx.x), vt, dt, vi, di)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+  const int v0 = vi * 256, d0 = di * 256;
+  typedef Op<T, OP_PANEL_T> O;
+  constexpr int CH = 16 / (int)sizeof(T);
+  const uint32_t be = (uint32_t)a.vp * sizeof(T) * kPanelRows, bh = (uint32_t)a.dp * sizeof(T) * kPanelRows;
+  const Operand oa = {(const uint8_t*)a.e + (int64_t)(v0 / CH) * 1024, be, 256 / CH - 1, O::lane_part(lane, wave, 0)};
+  const Operand ob = {(const uint8_t*)a.hp + (int64_t)(d0 / CH) * 1024, bh, (a.dp - d0) / CH - 1,
+                      O::lane_part(lane, wave, 0)};
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
+  const int nk = (rows + O::KE - 1) / O::KE;
+  if (nk > 0)
+    k_loop<T, OP_PANEL_T, OP_PANEL_T, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * 128, 0, nk);
+  float g = 1.f;
+  if (!a.per_token) {
+    if (a.grad_out) g = a.grad_out[0];
+    if (a.mean) g /= (float)max(a.count[0], 1);
+  }
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) {
+    const int d = d0 + wn * 128 + ni * 32 + (lane & 31);
+    if (d >= a.d) continue;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int v = v0 + wm * 64 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        if (v >= a.v) continue;
+        float x = acc[mi][ni][r];
+        if (!a.first) x += a.dwacc[(int64_t)v * a.dp + d];
+        if (!a.last) a.dwacc[(int64_t)v * a.dp + d] = x;
+        else if constexpr (sizeof(T) == 2) ((u16*)a.dw)[(int64_t)v * a.ld_dw + d] = f2bf(x * g);
+        else ((float*)a.dw)[(int64_t)v * a.ld_dw + d] = x * g;
+      }
+  }
+}
+
+inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+// blocks for n tiles dealt to the XCDs in runs of 32 (xcd_index)
+inline int xcd_grid(int64_t n) { return cdiv(n, 256) * 256; }
+
+}  // namespace
+
+hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
+  const int vt = a.vp / 256, tt = a.piece / 256;
+  const dim3 g(xcd_grid((int64_t)vt * tt)), b(512);
+  if (dt == MUON_BF16) hipLaunchKernelGGL((k_logits_mfma<u16>), g, b, 0, s, a, keep, vt, tt);
+  else hipLaunchKernelGGL((k_logits_mfma<float>), g, b, 0, s, a, keep, vt, tt);
+  return hipGetLastError();
+}
+hipError_t launch_head_dhidden(const HeadArgs& a, int dt, hipStream_t s) {
+  const int tt = a.piece / 256, nd = cdiv(a.dp, 256);
+  const dim3 g(xcd_grid((int64_t)tt * nd * a.split)), b(512);
+  if (dt == MUON_BF16) hipLaunchKernelGGL((k_dhidden_mfma<u16>), g, b, 0, s, a, tt, nd);
+  else hipLaunchKernelGGL((k_dhidden_mfma<float>), g, b, 0, s, a, tt, nd);
+  return hipGetLastError();
+}
+hipError_t launch_head_dweight(const HeadArgs& a, int dt, hipStream_t s) {
+  const int vt = a.vp / 256, nd = cdiv(a.d, 256);
+  const dim3 g(xcd_grid((int64_t)vt * nd)), b(512);
+  if (dt == MUON_BF16) hipLaunchKernelGGL((k_dweight_mfma<u16>), g, b, 0, s, a, vt, nd);
+  else hipLaunchKernelGGL((k_dweight_mfma<float>), g, b, 0, s, a, vt, nd);
+  return hipGetLastError();
+}
+
+}  // namespace muon

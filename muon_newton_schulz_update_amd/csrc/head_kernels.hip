@@ -21,7 +21,7 @@
 //              sum of the splits written to the tokens' rows
 //   dweight    dz^T H, summed over pieces in 32 bits
 //
-// A 16-bit exponential carries an eighth of the rounding of the bf16 value it
+// The products are in head_gemm.hip. A 16-bit exponential carries an eighth of the rounding of the bf16 value it
 // becomes, so the gradient's one rounding is the one to bf16.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -32,6 +32,10 @@ namespace muon {
 namespace {
 
 typedef unsigned short u16;
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -46,27 +50,17 @@ __device__ __forceinline__ u16 f2bf(float f) {
   u += 0x7FFFu + ((u >> 16) & 1u);
   return (u16)(u >> 16);
 }
+// Two values rounded to nearest even (the hardware's packed conversion).
+__device__ __forceinline__ unsigned int pack_bf16(float lo, float hi) {
+  const bf16x2_t q = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(unsigned int, q);
+}
 template <typename T> __device__ __forceinline__ float ld(const T* p, int64_t i);
 template <> __device__ __forceinline__ float ld<float>(const float* p, int64_t i) { return p[i]; }
 template <> __device__ __forceinline__ float ld<u16>(const u16* p, int64_t i) { return bf2f(p[i]); }
 template <typename T> __device__ __forceinline__ T to(float x);
 template <> __device__ __forceinline__ float to<float>(float x) { return x; }
 template <> __device__ __forceinline__ u16 to<u16>(float x) { return f2bf(x); }
-
-// Exponentials in (0, 1]: 6 bits of exponent (2^-63 and less become 0), 10 of
-// mantissa, rounded half up; 32-bit pieces keep them as they are.
-constexpr unsigned int kCodeBase = 64u << 10;
-__device__ __forceinline__ u16 encode(float e) {
-  const int q = (int)((__float_as_uint(e) + 0x1000u) >> 13) - (int)kCodeBase;
-  return (u16)min(max(q, 0), 0xFFFF);
-}
-__device__ __forceinline__ float decode(u16 q) { return q ? __uint_as_float(((unsigned int)q + kCodeBase) << 13) : 0.f; }
-template <typename T> __device__ __forceinline__ T keep_exp(float e);
-template <> __device__ __forceinline__ u16 keep_exp<u16>(float e) { return encode(e); }
-template <> __device__ __forceinline__ float keep_exp<float>(float e) { return e; }
-template <typename T> __device__ __forceinline__ float kept_exp(T q);
-template <> __device__ __forceinline__ float kept_exp<u16>(u16 q) { return decode(q); }
-template <> __device__ __forceinline__ float kept_exp<float>(float q) { return q; }
 
 __device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
 
@@ -138,73 +132,13 @@ __global__ __launch_bounds__(256) void k_pack_weight(const T* __restrict__ src, 
   for (int c = threadIdx.x; c < dp; c += 256) dst[r * dp + c] = c < d ? src[r * ld + c] : T(0);
 }
 
-// ---------------------------------------------------------------------------
-// Products. One shape for the three of them: a 64 x 64 tile per block, 16 of
-// K at a time in LDS, 4 x 4 sums per thread.
-// ---------------------------------------------------------------------------
-template <typename FA, typename FB, typename FE>
-__device__ __forceinline__ void tile_product(int k0, int k1, FA fa, FB fb, FE done) {
-  __shared__ float sa[16][65], sb[16][65];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k = k0; k < k1; k += 16) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e = threadIdx.x + 256 * q, m = e >> 4, kk = e & 15;
-      sa[kk][m] = k + kk < k1 ? fa(m, k + kk) : 0.f;
-      sb[kk][m] = k + kk < k1 ? fb(m, k + kk) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[kk][ty * 4 + i], sb[kk][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) done(ty * 4 + i, tx * 4 + j, acc[i][j]);
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void k_logits(HeadArgs a, int keep) {
-  __shared__ float z[64][65];   // token, vocabulary
-  const int rows = piece_rows(a), r0 = blockIdx.y * 64, v0 = blockIdx.x * 64;
-  if (r0 >= rows) return;
-  const T* hp = (const T*)a.hp;
-  const T* w = (const T*)a.w;
-  tile_product(
-      0, a.d, [&](int m, int k) { return ld<T>(hp, panel_at<T>(r0 + m, k, a.dp)); },
-      [&](int m, int k) { return v0 + m < a.v ? ld<T>(w, (int64_t)(v0 + m) * a.ld_w + k) : 0.f; },
-      [&](int i, int j, float x) { z[i][j] = a.softcap > 0.f ? a.softcap * tanhf(x / a.softcap) : x; });
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const int i = threadIdx.x, r = r0 + i;
-    const int tg = r < rows ? a.tgt[a.row0 + r] : -1, nv = min(64, a.v - v0);
-    float top = kRefFloor;
-    for (int j = 0; j < nv; ++j) top = fmaxf(top, z[i][j] * kLog2e);
-    top = ceilf(top);
-    float sum = 0.f;
-    for (int j = 0; j < 64; ++j) {
-      const float e = j < nv ? exp2f(fmaf(z[i][j], kLog2e, -top)) : 0.f;
-      if (v0 + j == tg) a.zt[r] = z[i][j];
-      else sum += e;
-      if (keep) ((T*)a.e)[panel_at<T>(r, v0 + j, a.vp)] = keep_exp<T>(e);
-    }
-    a.tmax[(int64_t)blockIdx.x * a.piece + r] = top;
-    a.tsum[(int64_t)blockIdx.x * a.piece + r] = sum;
-  }
-}
-
 // One thread per token of the piece.
 __global__ __launch_bounds__(256) void k_merge(HeadArgs a, int grad) {
   const int rows = piece_rows(a), r = blockIdx.x * 256 + threadIdx.x;
   if (r >= rows) return;
   const int tg = a.tgt[a.row0 + r], token = a.idx[a.row0 + r];
   float top = kRefFloor;
+  if (tg >= 0) top = ceilf(fmaxf(a.zt[r] * kLog2e, kRefFloor));   // no tile's reference covers the target
   for (int t = 0; t < a.n_vt; ++t) top = fmaxf(top, a.tmax[(int64_t)t * a.piece + r]);
   float others = 0.f;
   for (int t = 0; t < a.n_vt; ++t)
@@ -248,45 +182,75 @@ __global__ __launch_bounds__(1024) void k_total(HeadArgs a) {
   }
 }
 
-// Exponentials to the logits' gradient, in place; rows past the valid ones
-// (up to a whole tile) and columns past the vocabulary are zero.
+// Exponentials to the logits' gradient, in place, in panel order: a thread
+// keeps its token and goes over chunks, so a wave's accesses are whole
+// kilobytes. Rows past the valid ones (up to a whole tile) and columns past
+// the vocabulary become zero. Bound by HBM: a read and a write of every
+// exponential.
+constexpr int kDzChunks = 64;   // chunks per block
 template <typename T>
 __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a) {
-  const int rows = piece_rows(a), r = blockIdx.x;
-  if (r >= (rows + 255) / 256 * 256) return;
-  const bool real = r < rows;
+  constexpr int CH = 16 / (int)sizeof(T);
+  const int rows = piece_rows(a), r0 = blockIdx.y * kPanelRows;
+  if (r0 >= (rows + 255) / 256 * 256) return;
+  const int r = r0 + (threadIdx.x & 63);
+  const int tg = r < rows ? a.tgt[a.row0 + r] : -1;
+  const bool real = tg >= 0;
   const float4 rs = real ? a.rs[r] : float4{0.f, 0.f, 0.f, 0.f};
-  const int tg = real ? a.tgt[a.row0 + r] : -1;
-  T* e = (T*)a.e;
-  for (int c = threadIdx.x; c < a.vp; c += 256) {
-    const int64_t at = panel_at<T>(r, c, a.vp);
-    float x = 0.f;
-    if (real && tg >= 0 && c < a.v) {
-      const float k = a.tmax[(int64_t)(c / a.vtile) * a.piece + r];
-      const float ex = kept_exp<T>(e[at]);
-      x = ex * (rs.y * exp2f(k - rs.x));
-      if (a.softcap > 0.f) {
-        const float q = (__log2f(ex) + k) * (kLn2 / a.softcap);
-        x = ex > 0.f ? x * (1.f - q * q) : 0.f;
+  const int last = a.vp / CH, c1 = min((int)(blockIdx.x + 1) * kDzChunks, last);
+  uint8_t* base = (uint8_t*)a.e + ((int64_t)blockIdx.y * last << 10) + (threadIdx.x & 63) * 16;
+  const float back = a.softcap > 0.f ? kLn2 / a.softcap : 0.f;
+#pragma unroll 4
+  for (int c = blockIdx.x * kDzChunks + (threadIdx.x >> 6); c < c1; c += 4) {
+    uint8_t* p = base + ((int64_t)c << 10);
+    const int v = c * CH;
+    float x[CH];
+    if (real && v < a.v) {
+      const float k = a.tmax[(int64_t)(v / a.vtile) * a.piece + r];
+      const float f = rs.y * exp2f(k - rs.x);
+      if constexpr (sizeof(T) == 2) {
+        const u32x4_t q = *(const u32x4_t*)p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = __uint_as_float(((q[e] & 0xFFFFu) + kCodeBase) << 13);
+          x[2 * e + 1] = __uint_as_float(((q[e] >> 16) + kCodeBase) << 13);
+        }
+      } else {
+        const f32x4_t q = *(const f32x4_t*)p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = q[e];
       }
-      if (c == tg) x = rs.z;
+#pragma unroll
+      for (int e = 0; e < CH; ++e) {
+        const float ex = x[e];
+        x[e] = ex * f;
+        if (back > 0.f) {
+          // d softcap(z) / dz = 1 - (z / c)^2, z from its exponential
+          const float q = (__log2f(ex) + k) * back;
+          x[e] = ex > 0.f ? x[e] * (1.f - q * q) : 0.f;
+        }
+      }
+      if (v + CH > a.v)
+#pragma unroll
+        for (int e = 0; e < CH; ++e)
+          if (v + e >= a.v) x[e] = 0.f;
+      if (tg >= v && tg < v + CH)
+#pragma unroll
+        for (int e = 0; e < CH; ++e)
+          if (v + e == tg) x[e] = rs.z;
+    } else {
+#pragma unroll
+      for (int e = 0; e < CH; ++e) x[e] = 0.f;
     }
-    e[at] = to<T>(x);
+    if constexpr (sizeof(T) == 2) {
+      u32x4_t q;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+      *(u32x4_t*)p = q;
+    } else {
+      *(f32x4_t*)p = (f32x4_t){x[0], x[1], x[2], x[3]};
+    }
   }
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void k_dhidden(HeadArgs a) {
-  const int rows = piece_rows(a), r0 = blockIdx.y * 64, d0 = blockIdx.x * 64;
-  if (r0 >= rows) return;
-  const T* s = (const T*)a.e;
-  const T* w = (const T*)a.w;
-  tile_product(
-      0, a.v, [&](int m, int k) { return ld<T>(s, panel_at<T>(r0 + m, k, a.vp)); },
-      [&](int m, int k) { return d0 + m < a.d ? ld<T>(w, (int64_t)k * a.ld_w + d0 + m) : 0.f; },
-      [&](int i, int j, float x) {
-        if (d0 + j < a.dp) a.part[(int64_t)(r0 + i) * a.dp + d0 + j] = x;
-      });
 }
 
 // Sums of the splits to the tokens' rows, and zeros to the ignored ones: one
@@ -304,29 +268,22 @@ __global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a, const I* __rest
   if (r >= rows) return;
   const int64_t token = a.idx[a.row0 + r];
   const float g = common_factor(a);
-  for (int c = threadIdx.x; c < a.d; c += 256) {
-    float x = 0.f;
-    for (int q = 0; q < a.split; ++q) x += a.part[((int64_t)q * a.piece + r) * a.dp + c];
-    dh[token * a.ld_dh + c] = to<T>(x * g);
+  const bool whole = a.ld_dh % 4 == 0 && (uintptr_t)a.dh % (4 * sizeof(T)) == 0;
+  for (int c = threadIdx.x * 4; c < a.d; c += 1024) {
+    f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < a.split; ++q) x += *(const f32x4_t*)(a.part + ((int64_t)q * a.piece + r) * a.dp + c);
+    T* dst = dh + token * a.ld_dh + c;
+    if (whole && c + 4 <= a.d) {
+      if constexpr (sizeof(T) == 2)
+        *(u32x2_t*)dst = (u32x2_t){pack_bf16(x[0] * g, x[1] * g), pack_bf16(x[2] * g, x[3] * g)};
+      else
+        *(f32x4_t*)dst = x * g;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.d) dst[e] = to<T>(x[e] * g);
+    }
   }
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void k_dweight(HeadArgs a) {
-  const int rows = piece_rows(a), v0 = blockIdx.y * 64, d0 = blockIdx.x * 64;
-  const T* s = (const T*)a.e;
-  const T* hp = (const T*)a.hp;
-  const float g = common_factor(a);
-  tile_product(
-      0, rows, [&](int m, int k) { return v0 + m < a.v ? ld<T>(s, panel_at<T>(k, v0 + m, a.vp)) : 0.f; },
-      [&](int m, int k) { return d0 + m < a.d ? ld<T>(hp, panel_at<T>(k, d0 + m, a.dp)) : 0.f; },
-      [&](int i, int j, float x) {
-        const int64_t v = v0 + i, d = d0 + j;
-        if (v >= a.v || d >= a.d) return;
-        if (!a.first) x += a.dwacc[v * a.dp + d];
-        if (a.last) ((T*)a.dw)[v * a.ld_dw + d] = to<T>(x * g);
-        else a.dwacc[v * a.dp + d] = x;
-      });
 }
 
 inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
@@ -359,9 +316,6 @@ hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v
     hipLaunchKernelGGL((k_pack_weight<float>), dim3(v), dim3(256), 0, s, (const float*)src, ld, (float*)dst, d, dp);
   return hipGetLastError();
 }
-hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
-  BY_TYPE(dt, k_logits, dim3(a.n_vt, a.piece / 64), dim3(256), 0, s, a, keep);
-}
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s) {
   hipLaunchKernelGGL(k_merge, dim3(cdiv(a.piece, 256)), dim3(256), 0, s, a, grad);
   return hipGetLastError();
@@ -371,10 +325,8 @@ hipError_t launch_head_total(const HeadArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s) {
-  BY_TYPE(dt, k_dlogits, dim3(a.piece), dim3(256), 0, s, a);
-}
-hipError_t launch_head_dhidden(const HeadArgs& a, int dt, hipStream_t s) {
-  BY_TYPE(dt, k_dhidden, dim3(cdiv(a.d, 64), a.piece / 64), dim3(256), 0, s, a);
+  const int chunks = a.vp / (dt == MUON_BF16 ? 8 : 4);
+  BY_TYPE(dt, k_dlogits, dim3(cdiv(chunks, kDzChunks), a.piece / kPanelRows), dim3(256), 0, s, a);
 }
 hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, const void* targets, int target_bytes, int64_t ignore,
                                    hipStream_t s) {
@@ -387,9 +339,6 @@ hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, const void* target
     else hipLaunchKernelGGL((k_dhidden_out<float, int32_t>), g, b, 0, s, a, (const int32_t*)targets, ignore);
   }
   return hipGetLastError();
-}
-hipError_t launch_head_dweight(const HeadArgs& a, int dt, hipStream_t s) {
-  BY_TYPE(dt, k_dweight, dim3(cdiv(a.d, 64), cdiv(a.v, 64)), dim3(256), 0, s, a);
 }
 
 }  // namespace muon

@@ -98,6 +98,11 @@ hipError_t launch_adamw(const AdamList& L, int chunks, const AdamConst& c, const
 // a product over tokens or over columns is then whole kilobytes either way.
 // ---------------------------------------------------------------------------
 constexpr int kPanelRows = 64;
+// Kept exponentials of 16-bit inputs, in [0, 1]: the fp32 pattern's 6 low bits
+// of exponent and 10 high bits of mantissa, rounded half up; kCodeBase is the
+// pattern of 2^-63 shifted down, and what is smaller is kept as that.
+constexpr uint32_t kCodeBase = 64u << 10;
+constexpr int kStatCols = 128;     // vocabulary columns per reference and partial sum of a token
 template <typename T>
 __host__ __device__ inline int64_t panel_at(int64_t row, int64_t col, int64_t ld) {
   constexpr int ch = 16 / (int)sizeof(T);

@@ -122,6 +122,25 @@ muon_status scale_run(muon_handle* h, int n, const muon_matrix* src, const muon_
 constexpr size_t kHeadBytes = size_t(1) << 30;
 constexpr int kPieceRows = 256;
 
+// Splits of the vocabulary in dH = dz W: its tiles alone (tokens x width) are
+// fewer than the CUs for one piece of a narrow model. Rounds of 256 workgroups
+// times stages each, the ring's start-up (about six stages) and the sum's
+// traffic (a stage takes about 2 us, as long as 9 MB of HBM) added.
+int split_of(int piece, int dp, int v, int unit) {
+  const int64_t tiles = (int64_t)(piece / 256) * cdiv(dp, 256), stages = cdiv(v, unit);
+  const double sum = (double)piece * dp * 8 / 9e6;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 128 && (s == 1 || stages / s >= 8); ++s) {
+    const double t = (double)cdiv(tiles * s, 256) * ((double)cdiv(stages, s) + 6) + s * sum;
+    if (s == 1 || t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
 muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& wgt, const void* targets,
                      int target_bytes, const muon_loss_config& cfg, const float* grad_out, float* loss,
                      const muon_matrix* dh, const muon_matrix* dw) {
@@ -136,7 +155,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const int unit = 128 / e;                       // a stage of a product: 128 bytes of the contraction
   a.dp = (int)(cdiv(a.d, unit) * unit);
   a.vp = (int)(cdiv(a.v, 256) * 256);
-  a.vtile = 64;
+  a.vtile = kStatCols;
   a.n_vt = (int)cdiv(a.v, a.vtile);
   a.per_token = cfg.reduction == MUON_REDUCE_NONE;
   a.mean = cfg.reduction == MUON_REDUCE_MEAN;
@@ -153,15 +172,15 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
     a.dw = dw->ptr;
     a.ld_dw = dw->ld;
   }
-  a.split = 1;
   // the weight as it is, where a product's stage can be loaded from it in
   // 16-byte pieces with no remainder; otherwise a padded copy
-  const bool direct = a.d % unit == 0 && (uintptr_t)wgt.ptr % 16 == 0 && (wgt.rows == 1 || wgt.ld * e % 16 == 0);
+  const bool direct = a.d % unit == 0 && (uintptr_t)wgt.ptr % 16 == 0 && (wgt.rows == 1 || (wgt.ld * e % 16 == 0 && wgt.ld * e < (1 << 23)));
   // pieces
-  const size_t row = (size_t)a.dp * e + (size_t)a.n_vt * 8 + 24 + (grad ? (size_t)a.vp * e + (size_t)a.dp * 4 * a.split : 0);
+  const size_t row = (size_t)a.dp * e + (size_t)a.n_vt * 8 + 24 + (grad ? (size_t)a.vp * e : 0);
   const int64_t most = std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows);
   const int64_t pieces = std::max<int64_t>(1, cdiv(a.n, most));
   a.piece = (int)(std::max<int64_t>(1, cdiv(cdiv(a.n, pieces), kPieceRows)) * kPieceRows);
+  a.split = dh ? split_of(a.piece, a.dp, a.v, unit) : 1;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
