@@ -64,12 +64,7 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F
 // needs is written before it.
 __device__ __forceinline__ void ring_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-__device__ __forceinline__ u16 f2bf(float f) {
-  unsigned int u = __float_as_uint(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u16)((u >> 16) | 0x40);
-  u += 0x7FFFu + ((u >> 16) & 1u);
-  return (u16)(u >> 16);
-}
+__device__ __forceinline__ u16 f2bf(float f) { return __builtin_bit_cast(u16, (__bf16)f); }
 
 __device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
 
@@ -371,15 +366,15 @@ __global__ __launch_bounds__(512, 1) void k_logits_mfma(HeadArgs a, int keep, in
   for (int ni = 0; ni < NI; ++ni) {
     const int r = r0 + wn * 64 + ni * 32 + lr;       // the lane's token in the piece
     // the target's logit leaves the tile: it has its own place in the sums
-    const int tg = r < rows ? a.tgt[a.row0 + r] - vw : -1;
-    const bool mine = tg >= 0 && tg < 128 && ((tg >> 2) & 1) == hf;
+    const int tg = (r < rows ? a.tgt[a.row0 + r] : -1) - vw - 4 * hf;
+    const bool mine = tg >= 0 && tg < 128 && (tg & 4) == 0;
     if (__any(mine)) {
       float z = 0.f;
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          if (mine && mi * 32 + 8 * (q >> 2) + 4 * hf + (q & 3) == tg) {
+          if (mi * 32 + 8 * (q >> 2) + (q & 3) == tg) {
             z = acc[mi][ni][q];
             acc[mi][ni][q] = none;
           }
@@ -398,19 +393,21 @@ __global__ __launch_bounds__(512, 1) void k_logits_mfma(HeadArgs a, int keep, in
       float e[16];
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
-        e[q] = __builtin_amdgcn_exp2f(fmaf(acc[mi][ni][q], kLog2e, -top));
+        // no smaller than a kept exponential can say (kCodeBase); a maximum
+        // that keeps NaN, so that one bad logit reaches the token's loss
+        e[q] = __builtin_amdgcn_exp2f(__builtin_elementwise_maximum(fmaf(acc[mi][ni][q], kLog2e, -top), -63.f));
         sum += e[q];
       }
       if (!keep) continue;
       const int64_t col = vw + mi * 32;
       if constexpr (sizeof(T) == 2) {
+        // in [2^-63, 1] the pattern's upper two exponent bits say nothing:
+        // shifted out, the code is the upper half, rounded half up
         unsigned int c[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int lo = max((int)((__float_as_uint(e[2 * q]) + 0x1000u) >> 13) - (int)kCodeBase, 0);
-          const int hi = max((int)((__float_as_uint(e[2 * q + 1]) + 0x1000u) >> 13) - (int)kCodeBase, 0);
-          c[q] = (unsigned int)min(lo, 0xFFFF) | (unsigned int)min(hi, 0xFFFF) << 16;
-        }
+        for (int q = 0; q < 8; ++q)
+          c[q] = __builtin_amdgcn_perm((__float_as_uint(e[2 * q + 1]) << 3) + 0x8000u,
+                                       (__float_as_uint(e[2 * q]) << 3) + 0x8000u, 0x07060302u);
         uint8_t* dst = (uint8_t*)a.e + (((int64_t)(r >> 6) * (a.vp >> 3) + (col >> 3)) << 10) + (r & 63) * 16;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -439,13 +436,9 @@ __global__ __launch_bounds__(512, 1) void k_logits_mfma(HeadArgs a, int keep, in
 // dH: partial sums over a range of the vocabulary, 32-bit, row-major.
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ __launch_bounds__(512, 1) void k_dhidden_mfma(HeadArgs a, int tt, int dt) {
+__device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, int ti, int di, int q) {
   constexpr int MI = 2, NI = 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * kSlot];
-  const int rows = piece_rows(a), lane = threadIdx.x & 63;
-  const int nt = min(tt, (rows + 255) / 256), idx = xcd_index(blockIdx.x);
-  if (nt == 0 || idx >= nt * dt * a.split) return;
-  const int q = idx / (nt * dt), t = idx - q * nt * dt, ti = t / dt, di = t - ti * dt;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
   const int r0 = ti * 256, d0 = di * 256;
   typedef Op<T, OP_PANEL_K> A;
@@ -484,12 +477,9 @@ __global__ __launch_bounds__(512, 1) void k_dhidden_mfma(HeadArgs a, int tt, int
 // and rounded to the weight's type.
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ __launch_bounds__(512, 1) void k_dweight_mfma(HeadArgs a, int vt, int dt) {
+__device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, int vi, int di, int rows) {
   constexpr int MI = 2, NI = 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * kSlot];
-  const int rows = piece_rows(a), lane = threadIdx.x & 63;
-  int vi, di;
-  if (!strip_tile<8>(xcd_index(blockIdx.x), vt, dt, vi, di)) return;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
   const int v0 = vi * 256, d0 = di * 256;
   typedef Op<T, OP_PANEL_T> O;
@@ -511,22 +501,53 @@ __global__ __launch_bounds__(512, 1) void k_dweight_mfma(HeadArgs a, int vt, int
     if (a.grad_out) g = a.grad_out[0];
     if (a.mean) g /= (float)max(a.count[0], 1);
   }
+  const int vl = v0 + wm * 64 + 4 * (lane >> 5), dl = d0 + wn * 128 + (lane & 31);
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
-    const int d = d0 + wn * 128 + ni * 32 + (lane & 31);
+    const int d = dl + ni * 32;
     if (d >= a.d) continue;
+    if (!a.first) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int v = min(vl + mi * 32 + 8 * (r >> 2) + (r & 3), a.v - 1);   // (a row past the end is not stored)
+          acc[mi][ni][r] += a.dwacc[(int64_t)v * a.dp + d];
+        }
+    }
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int v = v0 + wm * 64 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        const int v = vl + mi * 32 + 8 * (r >> 2) + (r & 3);
         if (v >= a.v) continue;
-        float x = acc[mi][ni][r];
-        if (!a.first) x += a.dwacc[(int64_t)v * a.dp + d];
+        const float x = acc[mi][ni][r];
         if (!a.last) a.dwacc[(int64_t)v * a.dp + d] = x;
         else if constexpr (sizeof(T) == 2) ((u16*)a.dw)[(int64_t)v * a.ld_dw + d] = f2bf(x * g);
         else ((float*)a.dw)[(int64_t)v * a.ld_dw + d] = x * g;
       }
+  }
+}
+
+// Both gradients in one launch: they need only dz, and the tiles of one fill
+// the CUs that the last round of the other's leaves idle (the 50304 x 768
+// weight's 591 tiles are 2.3 rounds of the 256 CUs).
+template <typename T>
+__global__ __launch_bounds__(512, 1) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd, int weight_first) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * kSlot];
+  const int rows = piece_rows(a);
+  const int nt = min(tt, (rows + 255) / 256), n_h = nt * nd * a.split, n_w = vt * nd;
+  int idx = xcd_index(blockIdx.x);
+  if (idx >= n_h + n_w) return;
+  const int first = weight_first ? n_w : n_h;
+  const bool in_first = idx < first;
+  if (!in_first) idx -= first;
+  if (in_first == (weight_first != 0)) {
+    int vi, di;
+    if (strip_tile<8>(idx, vt, nd, vi, di)) dweight_tile<T>(a, smem, vi, di, rows);
+  } else {
+    const int q = idx / (nt * nd), t = idx - q * nt * nd;
+    dhidden_tile<T>(a, smem, t / nd, t % nd, q);
   }
 }
 
@@ -543,18 +564,14 @@ hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s
   else hipLaunchKernelGGL((k_logits_mfma<float>), g, b, 0, s, a, keep, vt, tt);
   return hipGetLastError();
 }
-hipError_t launch_head_dhidden(const HeadArgs& a, int dt, hipStream_t s) {
-  const int tt = a.piece / 256, nd = cdiv(a.dp, 256);
-  const dim3 g(xcd_grid((int64_t)tt * nd * a.split)), b(512);
-  if (dt == MUON_BF16) hipLaunchKernelGGL((k_dhidden_mfma<u16>), g, b, 0, s, a, tt, nd);
-  else hipLaunchKernelGGL((k_dhidden_mfma<float>), g, b, 0, s, a, tt, nd);
-  return hipGetLastError();
-}
-hipError_t launch_head_dweight(const HeadArgs& a, int dt, hipStream_t s) {
-  const int vt = a.vp / 256, nd = cdiv(a.d, 256);
-  const dim3 g(xcd_grid((int64_t)vt * nd)), b(512);
-  if (dt == MUON_BF16) hipLaunchKernelGGL((k_dweight_mfma<u16>), g, b, 0, s, a, vt, nd);
-  else hipLaunchKernelGGL((k_dweight_mfma<float>), g, b, 0, s, a, vt, nd);
+hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
+  const int tt = a.dh ? a.piece / 256 : 0, vt = a.dw ? a.vp / 256 : 0, nd = cdiv(a.dp, 256);
+  const int unit = dt == MUON_BF16 ? 64 : 32;
+  // the longer tiles go first
+  const int weight_first = cdiv(a.piece, unit) > cdiv(a.v, unit) / a.split;
+  const dim3 g(xcd_grid(((int64_t)tt * a.split + vt) * nd)), b(512);
+  if (dt == MUON_BF16) hipLaunchKernelGGL((k_gradients_mfma<u16>), g, b, 0, s, a, vt, tt, nd, weight_first);
+  else hipLaunchKernelGGL((k_gradients_mfma<float>), g, b, 0, s, a, vt, tt, nd, weight_first);
   return hipGetLastError();
 }
 

@@ -98,9 +98,9 @@ hipError_t launch_adamw(const AdamList& L, int chunks, const AdamConst& c, const
 // a product over tokens or over columns is then whole kilobytes either way.
 // ---------------------------------------------------------------------------
 constexpr int kPanelRows = 64;
-// Kept exponentials of 16-bit inputs, in [0, 1]: the fp32 pattern's 6 low bits
-// of exponent and 10 high bits of mantissa, rounded half up; kCodeBase is the
-// pattern of 2^-63 shifted down, and what is smaller is kept as that.
+// Kept exponentials of 16-bit inputs, in [2^-63, 1]: the fp32 pattern's 6 low
+// bits of exponent and 10 high bits of mantissa, rounded half up; kCodeBase is
+// the pattern of 2^-63 shifted down.
 constexpr uint32_t kCodeBase = 64u << 10;
 constexpr int kStatCols = 128;     // vocabulary columns per reference and partial sum of a token
 template <typename T>
@@ -150,9 +150,8 @@ hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s);
 hipError_t launch_head_total(const HeadArgs& a, hipStream_t s);
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s);
-hipError_t launch_head_dhidden(const HeadArgs& a, int dt, hipStream_t s);
+hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s);   // dh and dw, each if not null
 hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, const void* targets, int target_bytes, int64_t ignore,
                                    hipStream_t s);
-hipError_t launch_head_dweight(const HeadArgs& a, int dt, hipStream_t s);
 
 }  // namespace muon

@@ -123,16 +123,19 @@ constexpr size_t kHeadBytes = size_t(1) << 30;
 constexpr int kPieceRows = 256;
 
 // Splits of the vocabulary in dH = dz W: its tiles alone (tokens x width) are
-// fewer than the CUs for one piece of a narrow model. Rounds of 256 workgroups
-// times stages each, the ring's start-up (about six stages) and the sum's
-// traffic (a stage takes about 2 us, as long as 9 MB of HBM) added.
-int split_of(int piece, int dp, int v, int unit) {
+// fewer than the CUs for one piece of a narrow model. The launch (both
+// gradients) lasts its stages over the 256 CUs, each tile with the ring's
+// start-up (about six stages), half a split of dH at its end, and the traffic
+// of the partial sums (a stage takes about 2 us, as long as 9 MB of HBM).
+int split_of(int piece, int dp, int v, int unit, bool weight) {
   const int64_t tiles = (int64_t)(piece / 256) * cdiv(dp, 256), stages = cdiv(v, unit);
+  const double other = weight ? (double)cdiv(v, 256) * cdiv(dp, 256) * (cdiv(piece, unit) + 6) : 0.0;
   const double sum = (double)piece * dp * 8 / 9e6;
   int best = 1;
   double least = 0;
   for (int s = 1; s <= 128 && (s == 1 || stages / s >= 8); ++s) {
-    const double t = (double)cdiv(tiles * s, 256) * ((double)cdiv(stages, s) + 6) + s * sum;
+    const double each = (double)cdiv(stages, s) + 6;
+    const double t = std::max((tiles * s * each + other) / 256 + each / 2, each) + s * sum;
     if (s == 1 || t < least) {
       least = t;
       best = s;
@@ -180,7 +183,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const int64_t most = std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows);
   const int64_t pieces = std::max<int64_t>(1, cdiv(a.n, most));
   a.piece = (int)(std::max<int64_t>(1, cdiv(cdiv(a.n, pieces), kPieceRows)) * kPieceRows);
-  a.split = dh ? split_of(a.piece, a.dp, a.v, unit) : 1;
+  a.split = dh ? split_of(a.piece, a.dp, a.v, unit, dw != nullptr) : 1;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -226,11 +229,10 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
     HIP_DO(h, launch_head_merge(a, grad ? 1 : 0, s));
     if (!grad) continue;
     HIP_DO(h, launch_head_dlogits(a, dt, s));
+    HIP_DO(h, launch_head_gradients(a, dt, s));
     if (dh) {
-      HIP_DO(h, launch_head_dhidden(a, dt, s));
       HIP_DO(h, launch_head_dhidden_out(a, dt, targets, target_bytes, cfg.ignore_index, s));
     }
-    if (dw) HIP_DO(h, launch_head_dweight(a, dt, s));
   }
   if (!a.per_token) HIP_DO(h, launch_head_total(a, s));
   return MUON_OK;
