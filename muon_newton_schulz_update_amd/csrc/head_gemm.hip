@@ -4,9 +4,10 @@
 //   dhidden   dH  = dz W        tokens x width,      K = vocabulary (split)
 //   dweight   dW  = dz^T H      vocabulary x width,  K = tokens
 //
-// One kernel shape for the three: a 256 x 256 tile per workgroup of 8 waves,
+// One kernel shape for the three: a 256 x 256 tile per workgroup of 8 waves
+// (or 128 x 128 of 4, two workgroups to a CU, where tiles are few),
 // K in stages of 128 bytes (64 bf16, 32 fp32), both operands of a stage
-// brought to LDS by direct buffer loads into a ring of five 32 KB slots, so
+// brought to LDS by direct buffer loads into a ring of five slots, so
 // that while one stage feeds the matrix cores the next and half of the one
 // after are on their way. bf16 runs v_mfma_f32_32x32x16_bf16, fp32
 // v_mfma_f32_32x32x2f32.
@@ -29,6 +30,7 @@
 // with zeros on one side at least).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "train.hpp"
 
@@ -49,7 +51,6 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 enum OpLayout { OP_ROW_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
 enum Product { P_LOGITS, P_DHIDDEN, P_DWEIGHT };
 
-constexpr int kSlot = 32768;      // one operand of one stage
 constexpr int kSlots = 5;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kRefFloor = -3.0e38f;
@@ -64,7 +65,19 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F
 // needs is written before it.
 __device__ __forceinline__ void ring_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-__device__ __forceinline__ u16 f2bf(float f) { return __builtin_bit_cast(u16, (__bf16)f); }
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+// Two values rounded to nearest even (the hardware's packed conversion).
+__device__ __forceinline__ unsigned int pack_bf16(float lo, float hi) {
+  const bf16x2_t q = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(unsigned int, q);
+}
+// Hand-off through LDS between the lanes of one wave: the LDS executes a
+// wave's accesses in order, so only the compiler has to keep them so.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 __device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
 
@@ -87,21 +100,22 @@ struct Operand {
   uint32_t lane;         // this lane's byte offset, the same in every stage
 };
 
-template <typename T, int L>
+// Tile edges: 256 (8 waves, one workgroup per CU) and 128 (4 waves, two). A
+// stage of an operand is TILE x 128 bytes, TILE / 8 loads of 1 KB, four a wave.
+template <typename T, int L, int TILE>
 struct Op {
   static constexpr int KE = 128 / (int)sizeof(T);
+  static constexpr int NW = TILE / 32;                        // waves
+  static constexpr int kRowT = TILE * (int)sizeof(T);         // LDS row of OP_ROW_T, bytes
+  static constexpr int kRowsPerLoad = 1024 / kRowT;           // its rows per load
   // the lane's part of a load's address (row layouts: the column part)
   __device__ static uint32_t lane_part(int lane, int wave, int last_chunk) {
     if constexpr (L == OP_ROW_K) {
       const int row = 8 * wave + (lane >> 3);
       return ((lane & 7) ^ ((row >> 1) & 7)) * 16;
     } else if constexpr (L == OP_ROW_T) {
-      if constexpr (sizeof(T) == 2) {
-        const int row = 2 * wave + (lane >> 5);
-        return min((lane & 31) ^ ((row & 3) << 2), last_chunk) * 16;
-      } else {
-        return min(lane, last_chunk) * 16;
-      }
+      const int per = 64 / kRowsPerLoad, row = kRowsPerLoad * wave + lane / per, c = lane % per;
+      return min(sizeof(T) == 2 ? c ^ ((row & 3) << 2) : c, last_chunk) * 16;
     } else if constexpr (L == OP_PANEL_K) {
       return lane * 16;
     } else {
@@ -113,27 +127,27 @@ struct Op {
   __device__ static __forceinline__ void load(const Operand& o, uint8_t* sm, int lane, int wave, int ks, int i) {
     const uint8_t* p = o.base;
     uint32_t voff = o.lane, soff = 0;
+    const int g = NW * i + wave;
     if constexpr (L == OP_ROW_K) {
       p += (int64_t)ks * 128;
-      voff += __umul24(min(8 * (8 * i + wave) + (lane >> 3), o.lim), o.pitch);
+      voff += __umul24(min(8 * g + (lane >> 3), o.lim), o.pitch);
     } else if constexpr (L == OP_ROW_T) {
       p += (int64_t)ks * KE * o.pitch;
-      const int row = sizeof(T) == 2 ? 2 * (8 * i + wave) + (lane >> 5) : 8 * i + wave;
-      voff += __umul24(min(row, o.lim - ks * KE), o.pitch);
+      voff += __umul24(min(kRowsPerLoad * g + lane / (64 / kRowsPerLoad), o.lim - ks * KE), o.pitch);
     } else if constexpr (L == OP_PANEL_K) {
       p += (int64_t)ks * 8192;
-      soff = i * o.pitch + wave * 1024;
+      soff = (g >> 3) * o.pitch + (g & 7) * 1024;
     } else {
       if constexpr (sizeof(T) == 2) {
         p += (int64_t)ks * o.pitch;
-        soff = min(8 * i + wave, o.lim) * 1024;
+        soff = min(g, o.lim) * 1024;
       } else {
         p += (int64_t)(ks >> 1) * o.pitch + (ks & 1) * 512;
-        soff = min(2 * (8 * i + wave), o.lim - 1) * 1024;
+        soff = min(2 * g, o.lim - 1) * 1024;
       }
     }
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, -1, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(sm + (8 * i + wave) * 1024), 16, voff, soff, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(sm + g * 1024), 16, voff, soff, 0, 0);
   }
   static constexpr int kReads = L == OP_ROW_K || L == OP_PANEL_K ? 1 : sizeof(T) == 2 ? 2 : 4;   // LDS reads a fragment
   // fragment of rows (columns) at..at+31 for k-step s: lane l holds index
@@ -154,7 +168,7 @@ struct Op {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int kk = k + 4 * j;
-        const uint8_t* p = L == OP_ROW_T ? sm + kk * 512 + (c ^ ((kk & 3) << 2)) * 16 + (i & 1) * 8
+        const uint8_t* p = L == OP_ROW_T ? sm + kk * kRowT + (c ^ ((kk & 3) << 2)) * 16 + (i & 1) * 8
                                          : sm + c * 1024 + (kk ^ ((c & 3) << 2)) * 16 + (i & 1) * 8;
         q[j] = read_tr16((lds_s16x4_t*)p);
       }
@@ -165,7 +179,7 @@ struct Op {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int k = 4 * (2 * s + hf) + e, m = at + lr, c = m >> 2;
-        v[e] = L == OP_ROW_T ? *(const float*)(sm + k * 1024 + m * 4)
+        v[e] = L == OP_ROW_T ? *(const float*)(sm + k * kRowT + m * 4)
                              : *(const float*)(sm + c * 512 + (k ^ (c & 7)) * 16 + (m & 3) * 4);
       }
       return v;
@@ -177,12 +191,13 @@ template <typename T> struct FragOf { typedef bf16x8_t type; };
 template <> struct FragOf<float> { typedef f32x4_t type; };
 
 // The K loop: acc += A B over stages [k0, k1).
-template <typename T, int LA, int LB, int MI, int NI>
+template <typename T, int LA, int LB, int TILE, int MI, int NI>
 __device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, const Operand& oa, const Operand& ob,
                                        int lane, int wave, int am, int bn, int k0, int k1) {
   typedef typename FragOf<T>::type Frag;
-  typedef Op<T, LA> A;
-  typedef Op<T, LB> B;
+  typedef Op<T, LA, TILE> A;
+  typedef Op<T, LB, TILE> B;
+  constexpr int kSlot = TILE * 128;                        // one operand of one stage
   constexpr int LPO = 4;                                   // loads per wave per operand and stage
   constexpr int kReadStep = MI * A::kReads + NI * B::kReads;
   constexpr int S = kSlots;
@@ -313,32 +328,33 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 // wave's 128 vocabulary rows, so waves never wait for one another. The
 // exponentials go to the panels as whole chunks after a half-wave swap.
 // ---------------------------------------------------------------------------
-template <typename T>
-__global__ __launch_bounds__(512, 1) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
-  constexpr int MI = 4, NI = 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * kSlot];
+template <typename T, int TILE>
+__global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
+  constexpr int MI = 4, NI = TILE / 128, WM = TILE / 128;   // a wave: 128 vocabulary rows
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * TILE * 128];
   int vi, ti;
   const int rows = piece_rows(a), lane = threadIdx.x & 63;
-  if (!strip_tile<4>(xcd_index(blockIdx.x), vt, min(tt, (rows + 255) / 256), vi, ti)) return;
+  if (!strip_tile<4>(xcd_index(blockIdx.x), vt, min(tt, (rows + TILE - 1) / TILE), vi, ti)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
-  const int v0 = vi * 256, r0 = ti * 256;
-  typedef Op<T, OP_ROW_K> A;
-  typedef Op<T, OP_PANEL_K> B;
+  const int v0 = vi * TILE, r0 = ti * TILE;
+  typedef Op<T, OP_ROW_K, TILE> A;
+  typedef Op<T, OP_PANEL_K, TILE> B;
   const Operand oa = {(const uint8_t*)a.w + (int64_t)v0 * a.ld_w * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)),
                       a.v - 1 - v0, A::lane_part(lane, wave, 0)};
   const uint32_t blk = (uint32_t)a.dp * sizeof(T) * kPanelRows;
-  const Operand ob = {(const uint8_t*)a.hp + (int64_t)ti * 4 * blk, blk, 0, B::lane_part(lane, wave, 0)};
+  const Operand ob = {(const uint8_t*)a.hp + (int64_t)ti * (TILE / 64) * blk, blk, 0, B::lane_part(lane, wave, 0)};
   f32x16_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
-  k_loop<T, OP_ROW_K, OP_PANEL_K, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 128, wn * 64, 0, a.dp / A::KE);
+  k_loop<T, OP_ROW_K, OP_PANEL_K, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 128, wn * NI * 32, 0,
+                                                a.dp / A::KE);
 
   const int lr = lane & 31, hf = lane >> 5;
   const int vw = v0 + wm * 128;                      // the wave's first vocabulary row
   if (vw >= a.v) return;                             // (the exponentials' padding is cleared with the gradient)
-  const int tile = vi * 2 + wm;
+  const int tile = vi * WM + wm;
   if (a.softcap > 0.f) {
     const float s = 2.f * kLog2e / a.softcap;
 #pragma unroll
@@ -364,7 +380,7 @@ __global__ __launch_bounds__(512, 1) void k_logits_mfma(HeadArgs a, int keep, in
   }
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
-    const int r = r0 + wn * 64 + ni * 32 + lr;       // the lane's token in the piece
+    const int r = r0 + (wn * NI + ni) * 32 + lr;       // the lane's token in the piece
     // the target's logit leaves the tile: it has its own place in the sums
     const int tg = (r < rows ? a.tgt[a.row0 + r] : -1) - vw - 4 * hf;
     const bool mine = tg >= 0 && tg < 128 && (tg & 4) == 0;
@@ -435,16 +451,16 @@ __global__ __launch_bounds__(512, 1) void k_logits_mfma(HeadArgs a, int keep, in
 // ---------------------------------------------------------------------------
 // dH: partial sums over a range of the vocabulary, 32-bit, row-major.
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, int TILE>
 __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, int ti, int di, int q) {
-  constexpr int MI = 2, NI = 4;
+  constexpr int MI = 2, NI = TILE / 64;                     // waves: TILE / 64 x 2
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
-  const int r0 = ti * 256, d0 = di * 256;
-  typedef Op<T, OP_PANEL_K> A;
-  typedef Op<T, OP_ROW_T> B;
+  const int r0 = ti * TILE, d0 = di * TILE;
+  typedef Op<T, OP_PANEL_K, TILE> A;
+  typedef Op<T, OP_ROW_T, TILE> B;
   const uint32_t blk = (uint32_t)a.vp * sizeof(T) * kPanelRows;
-  const Operand oa = {(const uint8_t*)a.e + (int64_t)ti * 4 * blk, blk, 0, A::lane_part(lane, wave, 0)};
+  const Operand oa = {(const uint8_t*)a.e + (int64_t)ti * (TILE / 64) * blk, blk, 0, A::lane_part(lane, wave, 0)};
   const int chunks = (a.dp - d0) * (int)sizeof(T) / 16;
   const Operand ob = {(const uint8_t*)a.w + (int64_t)d0 * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)), a.v - 1,
                       B::lane_part(lane, wave, chunks - 1)};
@@ -456,11 +472,11 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   if (k1 > k0)
-    k_loop<T, OP_PANEL_K, OP_ROW_T, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * 128, k0, k1);
+    k_loop<T, OP_PANEL_K, OP_ROW_T, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * NI * 32, k0, k1);
   float* out = a.part + (int64_t)q * a.piece * a.dp;
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
-    const int d = d0 + wn * 128 + ni * 32 + (lane & 31);
+    const int d = d0 + (wn * NI + ni) * 32 + (lane & 31);
     if (d >= a.dp) continue;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
@@ -474,20 +490,24 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 
 // ---------------------------------------------------------------------------
 // dW: the piece's sum, added to the pieces before it; the last one is scaled
-// and rounded to the weight's type.
+// and rounded to the weight's type. The width is on the accumulators' rows, so
+// a lane has four neighbouring columns of one weight row; 16-bit results are
+// put together to whole rows of the wave's part in the idle LDS (chunks
+// swizzled by row) and leave as 16-byte stores.
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, int TILE>
 __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, int vi, int di, int rows) {
-  constexpr int MI = 2, NI = 4;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
-  const int v0 = vi * 256, d0 = di * 256;
-  typedef Op<T, OP_PANEL_T> O;
+  constexpr int MI = TILE / 64, NI = 2;                     // waves: 2 x TILE / 64
+  const int lane = threadIdx.x & 63, lr = lane & 31, hf = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / (TILE / 64), wn = wave % (TILE / 64);
+  const int v0 = vi * TILE, d0 = di * TILE;
+  typedef Op<T, OP_PANEL_T, TILE> O;
   constexpr int CH = 16 / (int)sizeof(T);
   const uint32_t be = (uint32_t)a.vp * sizeof(T) * kPanelRows, bh = (uint32_t)a.dp * sizeof(T) * kPanelRows;
-  const Operand oa = {(const uint8_t*)a.e + (int64_t)(v0 / CH) * 1024, be, 256 / CH - 1, O::lane_part(lane, wave, 0)};
-  const Operand ob = {(const uint8_t*)a.hp + (int64_t)(d0 / CH) * 1024, bh, (a.dp - d0) / CH - 1,
+  const Operand oa = {(const uint8_t*)a.hp + (int64_t)(d0 / CH) * 1024, bh, (a.dp - d0) / CH - 1,
                       O::lane_part(lane, wave, 0)};
+  const Operand ob = {(const uint8_t*)a.e + (int64_t)(v0 / CH) * 1024, be, TILE / CH - 1, O::lane_part(lane, wave, 0)};
   f32x16_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
@@ -495,48 +515,101 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   const int nk = (rows + O::KE - 1) / O::KE;
   if (nk > 0)
-    k_loop<T, OP_PANEL_T, OP_PANEL_T, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * 128, 0, nk);
+    k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * 64, 0, nk);
   float g = 1.f;
-  if (!a.per_token) {
+  if (a.last && !a.per_token) {
     if (a.grad_out) g = a.grad_out[0];
     if (a.mean) g /= (float)max(a.count[0], 1);
   }
-  const int vl = v0 + wm * 64 + 4 * (lane >> 5), dl = d0 + wn * 128 + (lane & 31);
+  const int vw = v0 + wn * 64, dw = d0 + wm * MI * 32;      // the wave's part
+  if (a.dwacc) {
+    // sums over pieces: padded rows, whole 16-byte groups
+    float* acc_at = a.dwacc + (int64_t)(vw + lr) * a.dp + dw + 4 * hf;
 #pragma unroll
-  for (int ni = 0; ni < NI; ++ni) {
-    const int d = dl + ni * 32;
-    if (d >= a.d) continue;
-    if (!a.first) {
+    for (int ni = 0; ni < NI; ++ni) {
+      if (vw + ni * 32 + lr >= a.v) continue;
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        if (dw + mi * 32 >= a.dp) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4_t* p = (f32x4_t*)(acc_at + (int64_t)ni * 32 * a.dp + mi * 32 + 8 * q);
+          f32x4_t x = {acc[mi][ni][4 * q], acc[mi][ni][4 * q + 1], acc[mi][ni][4 * q + 2], acc[mi][ni][4 * q + 3]};
+          if (!a.first) x += *p;
+          if (!a.last) *p = x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[mi][ni][4 * q + e] = x[e];
+        }
+      }
+    }
+    if (!a.last) return;
+  }
+  T* out = (T*)a.dw;
+  const bool whole = a.ld_dw % CH == 0 && (uintptr_t)a.dw % 16 == 0;
+  if constexpr (sizeof(T) == 2) {
+    constexpr int NC = MI * 4;                              // chunks of the wave's row
+    if (nk > 0) ring_barrier();                             // every wave is done with the slots
+    uint8_t* slab = smem + wave * (64 * NC * 16);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int v = min(vl + mi * 32 + 8 * (r >> 2) + (r & 3), a.v - 1);   // (a row past the end is not stored)
-          acc[mi][ni][r] += a.dwacc[(int64_t)v * a.dp + d];
+        for (int q = 0; q < 4; ++q) {
+          const u32x2_t x = {pack_bf16(acc[mi][ni][4 * q] * g, acc[mi][ni][4 * q + 1] * g),
+                             pack_bf16(acc[mi][ni][4 * q + 2] * g, acc[mi][ni][4 * q + 3] * g)};
+          const int row = ni * 32 + lr;
+          *(u32x2_t*)(slab + row * NC * 16 + (((mi * 4 + q) ^ (row & (NC - 1))) * 16) + hf * 8) = x;
+        }
+    wave_lds_sync();
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int row = i * (64 / NC) + lane / NC, c = lane % NC;
+      const u32x4_t x = *(const u32x4_t*)(slab + row * NC * 16 + ((c ^ (row & (NC - 1))) * 16));
+      const int v = vw + row, d = dw + c * 8;
+      if (v >= a.v || d >= a.d) continue;
+      u16* p = (u16*)out + (int64_t)v * a.ld_dw + d;
+      if (whole && d + 8 <= a.d) {
+        *(u32x4_t*)p = x;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (d + e < a.d) p[e] = (u16)(x[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      const int v = vw + ni * 32 + lr;
+      if (v >= a.v) continue;
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int d = dw + mi * 32 + 8 * q + 4 * hf;
+          float* p = (float*)out + (int64_t)v * a.ld_dw + d;
+          if (whole && d + 4 <= a.d) {
+            *(f32x4_t*)p = (f32x4_t){acc[mi][ni][4 * q] * g, acc[mi][ni][4 * q + 1] * g, acc[mi][ni][4 * q + 2] * g,
+                                     acc[mi][ni][4 * q + 3] * g};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (d + e < a.d) p[e] = acc[mi][ni][4 * q + e] * g;
+          }
         }
     }
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int v = vl + mi * 32 + 8 * (r >> 2) + (r & 3);
-        if (v >= a.v) continue;
-        const float x = acc[mi][ni][r];
-        if (!a.last) a.dwacc[(int64_t)v * a.dp + d] = x;
-        else if constexpr (sizeof(T) == 2) ((u16*)a.dw)[(int64_t)v * a.ld_dw + d] = f2bf(x * g);
-        else ((float*)a.dw)[(int64_t)v * a.ld_dw + d] = x * g;
-      }
   }
 }
 
 // Both gradients in one launch: they need only dz, and the tiles of one fill
 // the CUs that the last round of the other's leaves idle (the 50304 x 768
 // weight's 591 tiles are 2.3 rounds of the 256 CUs).
-template <typename T>
-__global__ __launch_bounds__(512, 1) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd, int weight_first) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * kSlot];
+template <typename T, int TILE>
+__global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
+                                                                                  int weight_first) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * TILE * 128];
   const int rows = piece_rows(a);
-  const int nt = min(tt, (rows + 255) / 256), n_h = nt * nd * a.split, n_w = vt * nd;
+  const int nt = min(tt, (rows + TILE - 1) / TILE), n_h = nt * nd * a.split, n_w = vt * nd;
   int idx = xcd_index(blockIdx.x);
   if (idx >= n_h + n_w) return;
   const int first = weight_first ? n_w : n_h;
@@ -544,35 +617,85 @@ __global__ __launch_bounds__(512, 1) void k_gradients_mfma(HeadArgs a, int vt, i
   if (!in_first) idx -= first;
   if (in_first == (weight_first != 0)) {
     int vi, di;
-    if (strip_tile<8>(idx, vt, nd, vi, di)) dweight_tile<T>(a, smem, vi, di, rows);
+    if (strip_tile<8>(idx, vt, nd, vi, di)) dweight_tile<T, TILE>(a, smem, vi, di, rows);
   } else {
     const int q = idx / (nt * nd), t = idx - q * nt * nd;
-    dhidden_tile<T>(a, smem, t / nd, t % nd, q);
+    dhidden_tile<T, TILE>(a, smem, t / nd, t % nd, q);
   }
 }
 
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // blocks for n tiles dealt to the XCDs in runs of 32 (xcd_index)
-inline int xcd_grid(int64_t n) { return cdiv(n, 256) * 256; }
+inline int xcd_grid(int64_t n) { return n > 0 ? cdiv(n, 256) * 256 : 256; }
 
 }  // namespace
 
-hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
-  const int vt = a.vp / 256, tt = a.piece / 256;
-  const dim3 g(xcd_grid((int64_t)vt * tt)), b(512);
-  if (dt == MUON_BF16) hipLaunchKernelGGL((k_logits_mfma<u16>), g, b, 0, s, a, keep, vt, tt);
-  else hipLaunchKernelGGL((k_logits_mfma<float>), g, b, 0, s, a, keep, vt, tt);
-  return hipGetLastError();
+// Tile edge of a launch, from its number of 256-tiles: with few of them
+// 128-tiles, four times as many and two to a CU, cover the CUs better. fp32
+// always takes 128: its matrix instructions are slow enough to hide the extra
+// operand traffic, and 256-tiles of its gradients do not fit the registers.
+//   measured (bf16, loss alone, 128 / 256): 384 tiles 62.7 / 67.6 us, 591
+//   170.5 / 174.4, 768 113.6 / 103.6, 1182 142.8 / 136.8; gradients: 708
+//   249 / 253, 825 470 / 459, 1760 916 / 764 (whole calls)
+constexpr int kFewTiles = 768;
+// dW's K is the tokens: with few of them its tiles are all start-up and
+// epilogue, which two workgroups to a CU overlap (300 tokens x 50304 x 2048:
+// 338 us with 128-tiles, 384 with 256; 700 tokens 587 and 556).
+constexpr int kShortK = 512;
+static int tile_of(int dt, int64_t tiles) {
+  if (const char* v = getenv("HEAD_TILE")) if (dt == MUON_BF16) return atoi(v);
+  return dt != MUON_BF16 || tiles < kFewTiles ? 128 : 256;
 }
+
+#define LAUNCH_TILES(k, dt, tile, n, ...)                                                                       \
+  do {                                                                                                          \
+    const dim3 g(xcd_grid(n)), b((tile) * 2);                                                                   \
+    if ((dt) != MUON_BF16) hipLaunchKernelGGL((k<float, 128>), g, b, 0, s, __VA_ARGS__);                        \
+    else if ((tile) == 256) hipLaunchKernelGGL((k<u16, 256>), g, b, 0, s, __VA_ARGS__);                         \
+    else hipLaunchKernelGGL((k<u16, 128>), g, b, 0, s, __VA_ARGS__);                                            \
+    return hipGetLastError();                                                                                   \
+  } while (0)
+
+hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
+  const int rows = a.rows_max;
+  const int tile = tile_of(dt, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256));
+  const int vt = cdiv(a.v, tile), tt = cdiv(rows, tile);
+  LAUNCH_TILES(k_logits_mfma, dt, tile, (int64_t)vt * tt, a, keep, vt, tt);
+}
+
 hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
-  const int tt = a.dh ? a.piece / 256 : 0, vt = a.dw ? a.vp / 256 : 0, nd = cdiv(a.dp, 256);
-  const int unit = dt == MUON_BF16 ? 64 : 32;
+  const int rows = a.rows_max, unit = dt == MUON_BF16 ? 64 : 32, tile = a.grad_tile;
+  const int tt = a.dh ? cdiv(rows, tile) : 0, vt = a.dw ? cdiv(a.v, tile) : 0, nd = cdiv(a.dp, tile);
   // the longer tiles go first
-  const int weight_first = cdiv(a.piece, unit) > cdiv(a.v, unit) / a.split;
-  const dim3 g(xcd_grid(((int64_t)tt * a.split + vt) * nd)), b(512);
-  if (dt == MUON_BF16) hipLaunchKernelGGL((k_gradients_mfma<u16>), g, b, 0, s, a, vt, tt, nd, weight_first);
-  else hipLaunchKernelGGL((k_gradients_mfma<float>), g, b, 0, s, a, vt, tt, nd, weight_first);
-  return hipGetLastError();
+  const int weight_first = cdiv(rows, unit) > cdiv(a.v, unit) / a.split;
+  LAUNCH_TILES(k_gradients_mfma, dt, tile, ((int64_t)tt * a.split + vt) * nd, a, vt, tt, nd, weight_first);
+}
+
+// Tile edge and splits of the vocabulary of the gradients' launch. dH's tiles
+// alone (tokens x width) are fewer than the CUs for one piece of a narrow
+// model. A launch lasts its stages over the CUs, each tile with the ring's
+// start-up (about six stages), half of its shortest tile at the end, and the
+// traffic of the partial sums (a 256-tile's stage takes about 2 us, as long
+// as 9 MB of HBM; a 128-tile's a quarter on half a CU).
+void head_gradient_plan(HeadArgs& a, int dt) {
+  const int rows = a.n < a.piece ? a.n : a.piece, unit = dt == MUON_BF16 ? 64 : 32;
+  const int64_t wide = (int64_t)cdiv(a.v, 256) * cdiv(a.dp, 256) * (a.dw ? 1 : 0);
+  const int64_t stages = cdiv(a.v, unit);
+  a.grad_tile = rows < kShortK ? 128 : tile_of(dt, wide + (a.dh ? cdiv(rows, 256) * cdiv(a.dp, 256) * (stages / 64 + 1) : 0));
+  const int tile = a.grad_tile, slots = tile == 256 ? 256 : 512;
+  const int64_t tiles = (int64_t)cdiv(rows, tile) * cdiv(a.dp, tile);
+  const double other = a.dw ? (double)cdiv(a.v, tile) * cdiv(a.dp, tile) * (cdiv(rows, unit) + 6) : 0.0;
+  const double sum = (double)rows * a.dp * 8 / (tile == 256 ? 9e6 : 4.5e6);
+  double least = 0;
+  a.split = 1;
+  for (int n = 1; a.dh && n <= 256 && (n == 1 || stages / n >= 6); ++n) {
+    const double each = (double)cdiv(stages, n) + 6, t0 = (tiles * n * each + other) / slots + each / 2;
+    const double t = (t0 > each ? t0 : each) + n * sum;
+    if (n == 1 || t < least) {
+      least = t;
+      a.split = n;
+    }
+  }
 }
 
 }  // namespace muon

@@ -62,6 +62,12 @@ template <typename T> __device__ __forceinline__ T to(float x);
 template <> __device__ __forceinline__ float to<float>(float x) { return x; }
 template <> __device__ __forceinline__ u16 to<u16>(float x) { return f2bf(x); }
 
+// Whether the merge kernel's only block sums a reduced loss; otherwise a block
+// of the next kernel does. (A last-block ticket there cost 30 us for 8192
+// tokens: its release writes back every L2's share of the exponentials.)
+__host__ __device__ inline bool total_in_merge(const HeadArgs& a) {
+  return !a.per_token && a.last && a.n <= kPanelRows;
+}
 __device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
 
 // What every token's gradient is multiplied by. It is applied to the 32-bit
@@ -75,18 +81,30 @@ __device__ __forceinline__ float common_factor(const HeadArgs& a) {
 }
 
 // ---------------------------------------------------------------------------
-// Compaction: one block; each thread takes a run of tokens, counts, and
-// writes its valid ones after the threads before it. A per-token loss of an
-// ignored token is 0.
+// Compaction of the valid tokens. Up to kPackScan tokens every pack block
+// scans the targets itself (a kernel of its own costs about 5 us more; for
+// 8192 tokens the scans would take 27 us longer than the rows, that kernel 10);
+// longer lists are scanned by one block beforehand, 8192 tokens at a time. A thread takes eight
+// neighbouring tokens. A per-token loss of an ignored token is 0.
 // ---------------------------------------------------------------------------
-template <typename I>
-__global__ __launch_bounds__(1024) void k_compact(HeadArgs a, const I* __restrict__ targets, int64_t ignore) {
-  __shared__ int sums[16];
-  const int t = threadIdx.x;
-  const int run = (a.n + 1023) / 1024;
-  const int lo = (int)min((int64_t)t * run, (int64_t)a.n), hi = (int)min((int64_t)lo + run, (int64_t)a.n);
-  int c = 0;
-  for (int i = lo; i < hi; ++i) c += (int64_t)targets[i] != ignore;
+constexpr int kPackScan = 2048;
+
+__device__ __forceinline__ int64_t target_at(const void* targets, int bytes, int64_t i) {
+  return bytes == 8 ? ((const int64_t*)targets)[i] : (int64_t)((const int32_t*)targets)[i];
+}
+
+// Scans tokens [i0, i0 + 8 THREADS): this thread's eight targets, which of
+// them are valid (bits), the valid ones before them and of all.
+template <int THREADS>
+__device__ __forceinline__ void scan_targets(const void* targets, int bytes, int64_t ignore, int i0, int n,
+                                             int64_t (&g)[8], unsigned& valid, int& before, int& all, int* sums) {
+  const int t = threadIdx.x, i = i0 + t * 8;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) g[e] = i + e < n ? target_at(targets, bytes, i + e) : ignore;
+  valid = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) valid |= (unsigned)(g[e] != ignore) << e;
+  const int c = __popc(valid);
   int x = c;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -95,42 +113,88 @@ __global__ __launch_bounds__(1024) void k_compact(HeadArgs a, const I* __restric
   }
   if ((t & 63) == 63) sums[t >> 6] = x;
   __syncthreads();
-  int before = x - c, all = 0;
+  before = x - c;
+  all = 0;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) {
+  for (int w = 0; w < THREADS / 64; ++w) {
     if (w < (t >> 6)) before += sums[w];
     all += sums[w];
   }
-  for (int i = lo; i < hi; ++i) {
-    const int64_t g = (int64_t)targets[i];
-    if (g == ignore) {
-      if (a.per_token) a.loss[i] = 0.f;
-      continue;
+  __syncthreads();
+}
+
+__device__ __forceinline__ int checked_target(const HeadArgs& a, int64_t g) { return g >= 0 && g < a.v ? (int)g : -1; }
+
+__global__ __launch_bounds__(1024) void k_compact(HeadArgs a) {
+  __shared__ int sums[16];
+  int base = 0;
+  for (int i0 = 0; i0 < a.n; i0 += 8192) {
+    int64_t g[8];
+    unsigned valid;
+    int before, all;
+    scan_targets<1024>(a.targets, a.target_bytes, a.ignore, i0, a.n, g, valid, before, all, sums);
+    before += base;
+    base += all;
+    const int i = i0 + (int)threadIdx.x * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (valid >> e & 1) {
+        a.idx[before] = i + e;
+        a.tgt[before] = checked_target(a, g[e]);
+        ++before;
+      } else if (a.per_token && i + e < a.n) {
+        a.loss[i + e] = 0.f;
+      }
     }
-    a.idx[before] = i;
-    a.tgt[before] = g >= 0 && g < a.v ? (int)g : -1;
-    ++before;
   }
-  if (t == 0) a.count[0] = all;
+  if (threadIdx.x == 0) a.count[0] = base;
 }
 
 // Gathered rows to panels: a wave takes 8 rows x 8 chunks at a time, so that
 // it reads and writes whole 128-byte lines; rows past the valid ones, up to a
-// whole tile, become zero. One block per 64 rows and 8 chunks.
+// whole panel (a stage of dW), become zero. One block per 64 rows and 8 chunks.
 template <typename T>
-__global__ __launch_bounds__(256) void k_pack(HeadArgs a) {
+__global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan) {
   constexpr int CH = 16 / (int)sizeof(T);
-  const int rows = piece_rows(a), r0 = blockIdx.y * kPanelRows;
-  if (r0 >= (rows + 255) / 256 * 256) return;
+  __shared__ int list[kPanelRows], sums[4];
+  const int r0 = blockIdx.y * kPanelRows;
+  int rows;
+  if (scan) {
+    const bool lists = blockIdx.x == 0 && blockIdx.y == 0;   // this block writes them
+    int64_t g[8];
+    unsigned valid;
+    int before;
+    scan_targets<256>(a.targets, a.target_bytes, a.ignore, 0, a.n, g, valid, before, rows, sums);
+    const int i = (int)threadIdx.x * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (valid >> e & 1) {
+        if (before >= r0 && before < r0 + kPanelRows) list[before - r0] = i + e;
+        if (lists) {
+          a.idx[before] = i + e;
+          a.tgt[before] = checked_target(a, g[e]);
+        }
+        ++before;
+      } else if (lists && a.per_token && i + e < a.n) {
+        a.loss[i + e] = 0.f;
+      }
+    }
+    if (lists && threadIdx.x == 0) a.count[0] = rows;
+  } else {
+    rows = piece_rows(a);
+    if (threadIdx.x < kPanelRows && r0 + (int)threadIdx.x < rows) list[threadIdx.x] = a.idx[a.row0 + r0 + threadIdx.x];
+  }
+  if (r0 >= rows) return;
+  __syncthreads();
   const int lane = threadIdx.x & 63, ch = blockIdx.x * 8 + (lane & 7), c = ch * CH;
   const bool whole = a.ld_h * sizeof(T) % 16 == 0 && (uintptr_t)a.h % 16 == 0 && c + CH <= a.d;
   uint8_t* dst = (uint8_t*)a.hp + (((int64_t)blockIdx.y * (a.dp / CH) + ch) << 10);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int rr = i * 32 + (threadIdx.x >> 6) * 8 + (lane >> 3), r = r0 + rr;
+    const int rr = i * 32 + (threadIdx.x >> 6) * 8 + (lane >> 3);
     u32x4_t q = {0, 0, 0, 0};
-    if (r < rows) {
-      const T* src = (const T*)a.h + (int64_t)a.idx[a.row0 + r] * a.ld_h;
+    if (r0 + rr < rows) {
+      const T* src = (const T*)a.h + (int64_t)list[rr] * a.ld_h;
       if (whole) {
         q = *(const u32x4_t*)(src + c);
       } else {
@@ -156,40 +220,20 @@ __global__ __launch_bounds__(256) void k_pack_weight(const T* __restrict__ src, 
 // order. (One thread per token, two dependent loads a tile, took 190 us for
 // 393 tiles whatever the number of tokens.)
 constexpr int kMergeParts = 16;
-__global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
-  __shared__ float tops[kMergeParts][64], sums[kMergeParts][64];
-  const int rows = piece_rows(a), lane = threadIdx.x & 63, part = threadIdx.x >> 6, r = blockIdx.x * 64 + lane;
-  if ((int)blockIdx.x * 64 >= rows) return;
-  float top = kRefFloor, others = 0.f;
-  if (r < rows) {
-#pragma unroll 4
-    for (int t = part; t < a.n_vt; t += kMergeParts) {
-      const float k = a.tmax[(int64_t)t * a.piece + r], x = a.tsum[(int64_t)t * a.piece + r], m = fmaxf(top, k);
-      others = others * exp2f(top - m) + x * exp2f(k - m);
-      top = m;
-    }
-  }
-  tops[part][lane] = top;
-  sums[part][lane] = others;
-  __syncthreads();
-  if (part != 0 || r >= rows) return;
+__device__ __forceinline__ void merge_token(const HeadArgs& a, int grad, int r, float top, float others) {
   const int tg = a.tgt[a.row0 + r], token = a.idx[a.row0 + r];
-  if (tg >= 0) top = fmaxf(top, ceilf(a.zt[r] * kLog2e));   // no tile's reference covers the target
-#pragma unroll
-  for (int p = 1; p < kMergeParts; ++p) top = fmaxf(top, tops[p][lane]);
-  others = 0.f;
-#pragma unroll
-  for (int p = 0; p < kMergeParts; ++p) others += sums[p][lane] * exp2f(tops[p][lane] - top);
-  float loss, g = 0.f;
+  float loss;
   float4 rs = {top, 0.f, 0.f, 0.f};
   if (tg < 0) {
     loss = __uint_as_float(0x7FC00000u);   // a target outside the vocabulary
   } else {
-    const float z = a.zt[r], y = fmaf(z, kLog2e, -top), e = exp2f(y);
+    const float z = a.zt[r], t = fmaxf(top, ceilf(z * kLog2e));   // no tile's reference covers the target
+    others *= exp2f(top - t);
+    const float y = fmaf(z, kLog2e, -t), e = exp2f(y);
     loss = y > -60.f ? log1pf(others / e) : logf(others + e) - y * kLn2;
     if (grad) {
-      g = a.grad_out && a.per_token ? a.grad_out[token] : 1.f;
-      rs.y = g / (others + e);
+      rs.x = t;
+      rs.y = (a.grad_out && a.per_token ? a.grad_out[token] : 1.f) / (others + e);
       rs.z = -rs.y * others;
       if (a.softcap > 0.f) {
         const float q = z / a.softcap;
@@ -202,34 +246,73 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
   if (a.per_token) a.loss[token] = loss;
 }
 
-// The reduced loss: the tokens' losses in a fixed order, in 64 bits.
-__global__ __launch_bounds__(1024) void k_total(HeadArgs a) {
-  __shared__ double sh[16];
+// One block: the reduced loss, the tokens' losses added in a fixed order in 64
+// bits.
+template <int THREADS>
+__device__ __forceinline__ void total_loss(const HeadArgs& a, double* sh) {
   const int n = a.count[0];
   double x = 0;
-  for (int i = threadIdx.x; i < n; i += 1024) x += a.lossc[i];
+  for (int i = threadIdx.x; i < n; i += THREADS) x += a.lossc[i];
 #pragma unroll
   for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
   __syncthreads();
   if (threadIdx.x == 0) {
     double s = 0;
-    for (int i = 0; i < 16; ++i) s += sh[i];
+    for (int i = 0; i < THREADS / 64; ++i) s += sh[i];
     a.loss[0] = (float)(a.mean ? (n ? s / n : 0.0) : s);
   }
+}
+__global__ __launch_bounds__(256) void k_total(HeadArgs a) {
+  __shared__ double sh[4];
+  total_loss<256>(a, sh);
+}
+
+__global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
+  __shared__ float tops[kMergeParts][64], sums[kMergeParts][64];
+  __shared__ double sh[16];
+  const int rows = piece_rows(a), lane = threadIdx.x & 63, part = threadIdx.x >> 6, r = blockIdx.x * 64 + lane;
+  float top = kRefFloor, others = 0.f;
+  if (r < rows) {
+#pragma unroll 4
+    for (int t = part; t < a.n_vt; t += kMergeParts) {
+      const float k = a.tmax[(int64_t)t * a.piece + r], x = a.tsum[(int64_t)t * a.piece + r], m = fmaxf(top, k);
+      others = others * exp2f(top - m) + x * exp2f(k - m);
+      top = m;
+    }
+  }
+  tops[part][lane] = top;
+  sums[part][lane] = others;
+  __syncthreads();
+  if (part == 0 && r < rows) {
+#pragma unroll
+    for (int p = 1; p < kMergeParts; ++p) top = fmaxf(top, tops[p][lane]);
+    others = 0.f;
+#pragma unroll
+    for (int p = 0; p < kMergeParts; ++p) others += sums[p][lane] * exp2f(tops[p][lane] - top);
+    merge_token(a, grad, r, top, others);
+  }
+  if (!total_in_merge(a)) return;
+  __syncthreads();
+  total_loss<1024>(a, sh);
 }
 
 // Exponentials to the logits' gradient, in place, in panel order: a thread
 // keeps its token and goes over chunks, so a wave's accesses are whole
-// kilobytes. Rows past the valid ones (up to a whole tile) and columns past
-// the vocabulary become zero. Bound by HBM: a read and a write of every
+// kilobytes. Rows past the valid ones (up to a whole panel, a stage of dW) and
+// columns past the vocabulary (a stage of dH) become zero. Bound by HBM: a read and a write of every
 // exponential.
 constexpr int kDzChunks = 64;   // chunks per block
 template <typename T>
 __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a) {
   constexpr int CH = 16 / (int)sizeof(T);
+  __shared__ double sh[4];
+  if (blockIdx.y == gridDim.y - 1) {   // one more line of blocks: the reduced loss
+    if (blockIdx.x == 0 && !a.per_token && a.last && !total_in_merge(a)) total_loss<256>(a, sh);
+    return;
+  }
   const int rows = piece_rows(a), r0 = blockIdx.y * kPanelRows;
-  if (r0 >= (rows + 255) / 256 * 256) return;
+  if (r0 >= rows) return;
   const int r = r0 + (threadIdx.x & 63);
   const int tg = r < rows ? a.tgt[a.row0 + r] : -1;
   const bool real = tg >= 0;
@@ -290,14 +373,14 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a) {
   }
 }
 
-// Sums of the splits to the tokens' rows, and zeros to the ignored ones: one
-// block per row of the piece, then one per token.
-template <typename T, typename I>
-__global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a, const I* __restrict__ targets, int64_t ignore) {
+// Sums of the splits to the tokens' rows, and, with the first piece, zeros to
+// the ignored tokens' rows: one block per row of the piece, then one per token.
+template <typename T>
+__global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a) {
   T* dh = (T*)a.dh;
-  if ((int)blockIdx.x >= a.piece) {   // only with the first piece
-    const int64_t i = (int)blockIdx.x - a.piece;
-    if ((int64_t)targets[i] != ignore) return;
+  if ((int)blockIdx.x >= a.rows_max) {
+    const int64_t i = (int)blockIdx.x - a.rows_max;
+    if (target_at(a.targets, a.target_bytes, i) != a.ignore) return;
     for (int c = threadIdx.x; c < a.d; c += 256) dh[i * a.ld_dh + c] = T(0);
     return;
   }
@@ -324,6 +407,9 @@ __global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a, const I* __rest
 }
 
 inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
+// whether the rows' kernel scans the targets: few tokens, all in one piece
+inline bool pack_scans(const HeadArgs& a) { return a.n <= kPackScan && a.n <= a.piece; }
+inline unsigned panels(const HeadArgs& a) { return a.rows_max > 0 ? cdiv(a.rows_max, kPanelRows) : 1; }
 
 }  // namespace
 
@@ -334,16 +420,14 @@ inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b);
     return hipGetLastError();                                                                                 \
   } while (0)
 
-hipError_t launch_head_compact(const HeadArgs& a, const void* targets, int target_bytes, int64_t ignore,
-                               hipStream_t s) {
-  if (target_bytes == 8)
-    hipLaunchKernelGGL((k_compact<int64_t>), dim3(1), dim3(1024), 0, s, a, (const int64_t*)targets, ignore);
-  else
-    hipLaunchKernelGGL((k_compact<int32_t>), dim3(1), dim3(1024), 0, s, a, (const int32_t*)targets, ignore);
+hipError_t launch_head_compact(const HeadArgs& a, hipStream_t s) {
+  if (pack_scans(a)) return hipSuccess;
+  hipLaunchKernelGGL(k_compact, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s) {
-  BY_TYPE(dt, k_pack, dim3(a.dp / (dt == MUON_BF16 ? 64 : 32), a.piece / kPanelRows), dim3(256), 0, s, a);
+  const int scan = pack_scans(a);
+  BY_TYPE(dt, k_pack, dim3(a.dp / (dt == MUON_BF16 ? 64 : 32), panels(a)), dim3(256), 0, s, a, scan);
 }
 hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v, int d, int dp, int dt,
                                    hipStream_t s) {
@@ -354,28 +438,19 @@ hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v
   return hipGetLastError();
 }
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s) {
-  hipLaunchKernelGGL(k_merge, dim3(a.piece / 64), dim3(64 * kMergeParts), 0, s, a, grad);
-  return hipGetLastError();
-}
-hipError_t launch_head_total(const HeadArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(k_total, dim3(1), dim3(1024), 0, s, a);
+  hipLaunchKernelGGL(k_merge, dim3(panels(a)), dim3(64 * kMergeParts), 0, s, a, grad);
+  if (!grad && a.last && !a.per_token && !total_in_merge(a))
+    hipLaunchKernelGGL(k_total, dim3(1), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s) {
   const int chunks = a.vp / (dt == MUON_BF16 ? 8 : 4);
-  BY_TYPE(dt, k_dlogits, dim3(cdiv(chunks, kDzChunks), a.piece / kPanelRows), dim3(256), 0, s, a);
+  BY_TYPE(dt, k_dlogits, dim3(cdiv(chunks, kDzChunks), panels(a) + 1), dim3(256), 0, s, a);
 }
-hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, const void* targets, int target_bytes, int64_t ignore,
-                                   hipStream_t s) {
-  const dim3 g(a.piece + (a.row0 == 0 ? a.n : 0)), b(256);
-  if (dt == MUON_BF16) {
-    if (target_bytes == 8) hipLaunchKernelGGL((k_dhidden_out<u16, int64_t>), g, b, 0, s, a, (const int64_t*)targets, ignore);
-    else hipLaunchKernelGGL((k_dhidden_out<u16, int32_t>), g, b, 0, s, a, (const int32_t*)targets, ignore);
-  } else {
-    if (target_bytes == 8) hipLaunchKernelGGL((k_dhidden_out<float, int64_t>), g, b, 0, s, a, (const int64_t*)targets, ignore);
-    else hipLaunchKernelGGL((k_dhidden_out<float, int32_t>), g, b, 0, s, a, (const int32_t*)targets, ignore);
-  }
-  return hipGetLastError();
+hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, hipStream_t s) {
+  const int blocks = a.rows_max + (a.row0 == 0 ? a.n : 0);
+  if (blocks == 0) return hipSuccess;
+  BY_TYPE(dt, k_dhidden_out, dim3(blocks), dim3(256), 0, s, a);
 }
 
 }  // namespace muon

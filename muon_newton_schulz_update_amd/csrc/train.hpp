@@ -117,7 +117,11 @@ struct HeadArgs {
   int32_t n, v, d;                    // tokens, vocabulary, width
   int32_t dp, vp;                     // padded width (64 or 32 elements), padded vocabulary (256)
   int32_t vtile, n_vt;                // columns per logits tile, tiles
-  int32_t piece, row0;                // tokens per piece, first compact token of this piece
+  int32_t piece, row0;                // tokens per piece (buffers), first compact token of this piece
+  int32_t rows_max;                   // tokens of this piece if none is ignored
+  const void* targets;
+  int64_t ignore;
+  int32_t target_bytes;
   int32_t per_token;                  // reduction none
   int32_t mean;
   float softcap;
@@ -133,25 +137,24 @@ struct HeadArgs {
   float* zt;                          // piece: the target's logit
   float4* rs;                         // piece: {reference, factor, target's gradient, 0}
   float* part;                        // dH partial sums: split x piece x dp
-  int32_t split;
+  int32_t split;                      // parts of the vocabulary in dH
+  int32_t grad_tile;                  // tile edge of the gradients' products
   float* dwacc;                       // v x dp fp32 sum over pieces, or null: one piece
   int32_t first, last;                // this piece starts / ends the sum over pieces
   float* loss;                        // caller's: one value, or n
   const float* grad_out;              // device, or null (1)
 };
 
-// Per-token reference and factors written by the merge kernel.
-hipError_t launch_head_compact(const HeadArgs& a, const void* targets, int target_bytes, int64_t ignore,
-                               hipStream_t s);
+// Picks grad_tile and split (before the workspace is laid out).
+void head_gradient_plan(HeadArgs& a, int dt);
+hipError_t launch_head_compact(const HeadArgs& a, hipStream_t s);
 hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s);
 hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v, int d, int dp, int dt,
                                    hipStream_t s);
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s);
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s);
-hipError_t launch_head_total(const HeadArgs& a, hipStream_t s);
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s);
 hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s);   // dh and dw, each if not null
-hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, const void* targets, int target_bytes, int64_t ignore,
-                                   hipStream_t s);
+hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, hipStream_t s);
 
 }  // namespace muon

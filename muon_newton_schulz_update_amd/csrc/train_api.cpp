@@ -122,28 +122,6 @@ muon_status scale_run(muon_handle* h, int n, const muon_matrix* src, const muon_
 constexpr size_t kHeadBytes = size_t(1) << 30;
 constexpr int kPieceRows = 256;
 
-// Splits of the vocabulary in dH = dz W: its tiles alone (tokens x width) are
-// fewer than the CUs for one piece of a narrow model. The launch (both
-// gradients) lasts its stages over the 256 CUs, each tile with the ring's
-// start-up (about six stages), half a split of dH at its end, and the traffic
-// of the partial sums (a stage takes about 2 us, as long as 9 MB of HBM).
-int split_of(int piece, int dp, int v, int unit, bool weight) {
-  const int64_t tiles = (int64_t)(piece / 256) * cdiv(dp, 256), stages = cdiv(v, unit);
-  const double other = weight ? (double)cdiv(v, 256) * cdiv(dp, 256) * (cdiv(piece, unit) + 6) : 0.0;
-  const double sum = (double)piece * dp * 8 / 9e6;
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= 128 && (s == 1 || stages / s >= 8); ++s) {
-    const double each = (double)cdiv(stages, s) + 6;
-    const double t = std::max((tiles * s * each + other) / 256 + each / 2, each) + s * sum;
-    if (s == 1 || t < least) {
-      least = t;
-      best = s;
-    }
-  }
-  return best;
-}
-
 muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& wgt, const void* targets,
                      int target_bytes, const muon_loss_config& cfg, const float* grad_out, float* loss,
                      const muon_matrix* dh, const muon_matrix* dw) {
@@ -163,6 +141,9 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.per_token = cfg.reduction == MUON_REDUCE_NONE;
   a.mean = cfg.reduction == MUON_REDUCE_MEAN;
   a.softcap = cfg.softcap;
+  a.targets = targets;
+  a.target_bytes = target_bytes;
+  a.ignore = cfg.ignore_index;
   a.h = hid.ptr;
   a.ld_h = hid.ld;
   a.loss = loss;
@@ -183,7 +164,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const int64_t most = std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows);
   const int64_t pieces = std::max<int64_t>(1, cdiv(a.n, most));
   a.piece = (int)(std::max<int64_t>(1, cdiv(cdiv(a.n, pieces), kPieceRows)) * kPieceRows);
-  a.split = dh ? split_of(a.piece, a.dp, a.v, unit, dw != nullptr) : 1;
+  if (grad) head_gradient_plan(a, dt);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -214,7 +195,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.dwacc = acc ? (float*)(b + o_acc) : nullptr;
   a.w = wgt.ptr;
   a.ld_w = wgt.ld;
-  HIP_DO(h, launch_head_compact(a, targets, target_bytes, cfg.ignore_index, s));
+  HIP_DO(h, launch_head_compact(a, s));
   if (!direct) {
     HIP_DO(h, launch_head_pack_weight(wgt.ptr, wgt.ld, b + o_w, a.v, a.d, a.dp, dt, s));
     a.w = b + o_w;
@@ -222,6 +203,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   }
   for (int64_t k = 0; k < pieces; ++k) {
     a.row0 = (int)(k * a.piece);
+    a.rows_max = std::max(0, std::min(a.piece, a.n - a.row0));
     a.first = k == 0;
     a.last = k + 1 == pieces;
     HIP_DO(h, launch_head_pack(a, dt, s));
@@ -231,10 +213,9 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
     HIP_DO(h, launch_head_dlogits(a, dt, s));
     HIP_DO(h, launch_head_gradients(a, dt, s));
     if (dh) {
-      HIP_DO(h, launch_head_dhidden_out(a, dt, targets, target_bytes, cfg.ignore_index, s));
+      HIP_DO(h, launch_head_dhidden_out(a, dt, s));
     }
   }
-  if (!a.per_token) HIP_DO(h, launch_head_total(a, s));
   return MUON_OK;
 }
 
