@@ -141,7 +141,8 @@ def load_library() -> ctypes.CDLL:
             "muon_profile_reset": (ctypes.c_int, [ctypes.c_void_p]),
             "muon_profile_read": (ctypes.c_int, [ctypes.c_void_p, P(MuonProfile)]),
         }
-        M, F, V, I = P(MuonMatrix), ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+        F, V, I = ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+        M = V                            # descriptors: packed bytes or an array's address
         # the training-step entry points (training.py): device scalars and
         # vectors travel as addresses, configurations by reference
         text = [ctypes.c_char_p, I]

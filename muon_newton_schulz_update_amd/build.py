@@ -3,7 +3,8 @@
     python -m muon_newton_schulz_update_amd.build [--jobs N]
 
 Objects go to muon_newton_schulz_update_amd/_build/, the library to
-muon_newton_schulz_update_amd/libmuon.so.
+muon_newton_schulz_update_amd/libmuon.so, the Python extension that packs
+tensors into descriptors to muon_newton_schulz_update_amd/_describe.so.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
+DESCRIBE = os.path.join(PKG, "_describe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -51,8 +53,10 @@ def _compile(src: str) -> str:
 def build(jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = DEVICE_SOURCES + HOST_SOURCES
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs) + 1)) as ex:
+        ext = ex.submit(_build_describe)
         objs = list(ex.map(_compile, srcs))
+        ext.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -62,6 +66,26 @@ def build(jobs: int | None = None, verbose: bool = False) -> str:
     if verbose:
         print(f"built {LIB}")
     return LIB
+
+
+def _build_describe() -> None:
+    """The Python extension that packs tensors into descriptors (host only)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    libs = cpp_extension.library_paths()
+    tmp = DESCRIBE + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-fPIC", "-shared", "-std=c++17", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{sysconfig.get_paths()['include']}", *[f"-I{d}" for d in cpp_extension.include_paths()],
+           os.path.join(CSRC, "describe.cpp"), "-o", tmp, *[f"-L{d}" for d in libs],
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    os.replace(tmp, DESCRIBE)
 
 
 def main() -> None:

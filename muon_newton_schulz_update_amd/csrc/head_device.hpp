@@ -1,0 +1,41 @@
+// Device helpers shared by the head's kernels (head_kernels.hip, head_gemm.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "train.hpp"
+
+namespace muon {
+
+// Valid tokens of the piece.
+__device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
+
+// What every token's gradient is multiplied by. It is applied to the 32-bit
+// sums, not to the logits' gradient before its rounding: 1 / n has one and the
+// same rounding error for all tokens, which no sum would average out, while
+// p - 1 of a word the model did not expect is nearly exact.
+__device__ __forceinline__ float common_factor(const HeadArgs& a) {
+  if (a.per_token) return 1.f;
+  const float g = a.grad_out ? a.grad_out[0] : 1.f;
+  return a.mean ? g / (float)max(a.count[0], 1) : g;
+}
+
+// One block: the reduced loss, the tokens' losses added in a fixed order in 64
+// bits. sh: one value per wave.
+template <int THREADS>
+__device__ __forceinline__ void total_loss(const HeadArgs& a, double* sh) {
+  const int n = a.count[0];
+  double x = 0;
+  for (int i = threadIdx.x; i < n; i += THREADS) x += a.lossc[i];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = 0;
+    for (int i = 0; i < THREADS / 64; ++i) s += sh[i];
+    a.loss[0] = (float)(a.mean ? (n ? s / n : 0.0) : s);
+  }
+}
+
+}  // namespace muon

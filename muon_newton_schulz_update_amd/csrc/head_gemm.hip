@@ -32,6 +32,7 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include "head_device.hpp"
 #include "train.hpp"
 
 namespace muon {
@@ -79,7 +80,6 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
 
 // Transposing LDS read: sixteen lanes give the addresses of four rows, four
 // 16-bit columns each (lanes 0-3 the first row, ...), and lane l gets column l
@@ -452,7 +452,7 @@ __global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_logits_mfma(H
 // dH: partial sums over a range of the vocabulary, 32-bit, row-major.
 // ---------------------------------------------------------------------------
 template <typename T, int TILE>
-__device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, int ti, int di, int q) {
+__device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, int ti, int di, int q, int rows) {
   constexpr int MI = 2, NI = TILE / 64;                     // waves: TILE / 64 x 2
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
@@ -473,18 +473,60 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   if (k1 > k0)
     k_loop<T, OP_PANEL_K, OP_ROW_T, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * NI * 32, k0, k1);
-  float* out = a.part + (int64_t)q * a.piece * a.dp;
+  const int lr = lane & 31, hf = lane >> 5;
+  if (a.split > 1) {
+    float* out = a.part + (int64_t)q * a.piece * a.dp;
 #pragma unroll
-  for (int ni = 0; ni < NI; ++ni) {
-    const int d = d0 + (wn * NI + ni) * 32 + (lane & 31);
-    if (d >= a.dp) continue;
+    for (int ni = 0; ni < NI; ++ni) {
+      const int d = d0 + (wn * NI + ni) * 32 + lr;
+      if (d >= a.dp) continue;
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = r0 + wm * 64 + mi * 32 + 8 * (r >> 2) + 4 * hf + (r & 3);
+          out[(int64_t)row * a.dp + d] = acc[mi][ni][r];
+        }
+    }
+    return;
+  }
+  // one split: the tokens' rows themselves, put together in the idle LDS
+  const float g = common_factor(a);
+  const int rw = r0 + wm * 64, dw = d0 + wn * NI * 32;      // the wave's part
+  constexpr int NC = NI * 32 * (int)sizeof(T) / 16, CH = 16 / (int)sizeof(T);   // chunks of its row
+  ring_barrier();                                           // every wave is done with the slots
+  uint8_t* slab = smem + wave * (32 * NC * 16);
+  const bool whole = a.ld_dh % CH == 0 && (uintptr_t)a.dh % 16 == 0;
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int row = r0 + wm * 64 + mi * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        out[(int64_t)row * a.dp + d] = acc[mi][ni][r];
+        const int row = 8 * (r >> 2) + 4 * hf + (r & 3), c = (ni * 32 + lr) / CH;
+        T* p = (T*)(slab + row * NC * 16 + ((c ^ (row & (NC - 1))) * 16)) + lr % CH;
+        if constexpr (sizeof(T) == 2) *p = (u16)pack_bf16(acc[mi][ni][r] * g, 0.f);
+        else *p = acc[mi][ni][r] * g;
       }
+    wave_lds_sync();
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) {
+      const int row = i * (64 / NC) + lane / NC, c = lane % NC;
+      const u32x4_t x = *(const u32x4_t*)(slab + row * NC * 16 + ((c ^ (row & (NC - 1))) * 16));
+      const int t = rw + mi * 32 + row, d = dw + c * CH;
+      if (t >= rows || d >= a.d) continue;
+      T* p = (T*)a.dh + (int64_t)a.idx[a.row0 + t] * a.ld_dh + d;
+      if (whole && d + CH <= a.d) {
+        *(u32x4_t*)p = x;
+      } else {
+        T y[CH];
+        __builtin_memcpy(y, &x, 16);
+#pragma unroll
+        for (int e = 0; e < CH; ++e)
+          if (d + e < a.d) p[e] = y[e];
+      }
+    }
+    wave_lds_sync();
   }
 }
 
@@ -516,11 +558,7 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
   const int nk = (rows + O::KE - 1) / O::KE;
   if (nk > 0)
     k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * 64, 0, nk);
-  float g = 1.f;
-  if (a.last && !a.per_token) {
-    if (a.grad_out) g = a.grad_out[0];
-    if (a.mean) g /= (float)max(a.count[0], 1);
-  }
+  const float g = common_factor(a);
   const int vw = v0 + wn * 64, dw = d0 + wm * MI * 32;      // the wave's part
   if (a.dwacc) {
     // sums over pieces: padded rows, whole 16-byte groups
@@ -611,7 +649,10 @@ __global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_gradients_mfm
   const int rows = piece_rows(a);
   const int nt = min(tt, (rows + TILE - 1) / TILE), n_h = nt * nd * a.split, n_w = vt * nd;
   int idx = xcd_index(blockIdx.x);
-  if (idx >= n_h + n_w) return;
+  if (idx >= n_h + n_w) {
+    if (idx == n_h + n_w && a.last && !a.per_token) total_loss<TILE * 2>(a, (double*)smem);
+    return;
+  }
   const int first = weight_first ? n_w : n_h;
   const bool in_first = idx < first;
   if (!in_first) idx -= first;
@@ -620,7 +661,7 @@ __global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_gradients_mfm
     if (strip_tile<8>(idx, vt, nd, vi, di)) dweight_tile<T, TILE>(a, smem, vi, di, rows);
   } else {
     const int q = idx / (nt * nd), t = idx - q * nt * nd;
-    dhidden_tile<T, TILE>(a, smem, t / nd, t % nd, q);
+    dhidden_tile<T, TILE>(a, smem, t / nd, t % nd, q, rows);
   }
 }
 
@@ -668,7 +709,7 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
   const int tt = a.dh ? cdiv(rows, tile) : 0, vt = a.dw ? cdiv(a.v, tile) : 0, nd = cdiv(a.dp, tile);
   // the longer tiles go first
   const int weight_first = cdiv(rows, unit) > cdiv(a.v, unit) / a.split;
-  LAUNCH_TILES(k_gradients_mfma, dt, tile, ((int64_t)tt * a.split + vt) * nd, a, vt, tt, nd, weight_first);
+  LAUNCH_TILES(k_gradients_mfma, dt, tile, ((int64_t)tt * a.split + vt) * nd + 1, a, vt, tt, nd, weight_first);
 }
 
 // Tile edge and splits of the vocabulary of the gradients' launch. dH's tiles
@@ -688,9 +729,10 @@ void head_gradient_plan(HeadArgs& a, int dt) {
   const double sum = (double)rows * a.dp * 8 / (tile == 256 ? 9e6 : 4.5e6);
   double least = 0;
   a.split = 1;
-  for (int n = 1; a.dh && n <= 256 && (n == 1 || stages / n >= 6); ++n) {
+  for (int n = 1; a.dh && n <= 256 && (n == 1 || stages / n >= 4); ++n) {
     const double each = (double)cdiv(stages, n) + 6, t0 = (tiles * n * each + other) / slots + each / 2;
-    const double t = (t0 > each ? t0 : each) + n * sum;
+    // more than one split: the sum is a launch of its own, about 5 us
+    const double t = (t0 > each ? t0 : each) + (n > 1 ? n * sum + (tile == 256 ? 3 : 5) : 0);
     if (n == 1 || t < least) {
       least = t;
       a.split = n;

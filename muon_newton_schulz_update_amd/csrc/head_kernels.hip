@@ -26,6 +26,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "head_device.hpp"
 #include "train.hpp"
 
 namespace muon {
@@ -62,24 +63,13 @@ template <typename T> __device__ __forceinline__ T to(float x);
 template <> __device__ __forceinline__ float to<float>(float x) { return x; }
 template <> __device__ __forceinline__ u16 to<u16>(float x) { return f2bf(x); }
 
-// Whether the merge kernel's only block sums a reduced loss; otherwise a block
-// of the next kernel does. (A last-block ticket there cost 30 us for 8192
+// Without gradients: whether the merge kernel's only block sums a reduced
+// loss; a kernel of its own does otherwise. (With gradients a block of their
+// launch does. A last-block ticket in the merge kernel cost 30 us for 8192
 // tokens: its release writes back every L2's share of the exponentials.)
 __host__ __device__ inline bool total_in_merge(const HeadArgs& a) {
   return !a.per_token && a.last && a.n <= kPanelRows;
 }
-__device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
-
-// What every token's gradient is multiplied by. It is applied to the 32-bit
-// sums, not to the logits' gradient before its rounding: 1 / n has one and the
-// same rounding error for all tokens, which no sum would average out, while
-// p - 1 of a word the model did not expect is nearly exact.
-__device__ __forceinline__ float common_factor(const HeadArgs& a) {
-  if (a.per_token) return 1.f;
-  const float g = a.grad_out ? a.grad_out[0] : 1.f;
-  return a.mean ? g / (float)max(a.count[0], 1) : g;
-}
-
 // ---------------------------------------------------------------------------
 // Compaction of the valid tokens. Up to kPackScan tokens every pack block
 // scans the targets itself (a kernel of its own costs about 5 us more; for
@@ -220,49 +210,55 @@ __global__ __launch_bounds__(256) void k_pack_weight(const T* __restrict__ src, 
 // order. (One thread per token, two dependent loads a tile, took 190 us for
 // 393 tiles whatever the number of tokens.)
 constexpr int kMergeParts = 16;
-__device__ __forceinline__ void merge_token(const HeadArgs& a, int grad, int r, float top, float others) {
-  const int tg = a.tgt[a.row0 + r], token = a.idx[a.row0 + r];
-  float loss;
+__device__ __forceinline__ void merge_tiles(const HeadArgs& a, int r, int rows, int part, int parts, float& top,
+                                            float& others) {
+  top = kRefFloor;
+  others = 0.f;
+  if (r >= rows) return;
+#pragma unroll 4
+  for (int t = part; t < a.n_vt; t += parts) {
+    const float k = a.tmax[(int64_t)t * a.piece + r], x = a.tsum[(int64_t)t * a.piece + r], m = fmaxf(top, k);
+    others = others * exp2f(top - m) + x * exp2f(k - m);
+    top = m;
+  }
+}
+template <int PARTS>
+__device__ __forceinline__ void merge_parts(const float (*tops)[64], const float (*sums)[64], int lane, float& top,
+                                            float& others) {
+#pragma unroll
+  for (int p = 1; p < PARTS; ++p) top = fmaxf(top, tops[p][lane]);
+  others = 0.f;
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) others += sums[p][lane] * exp2f(tops[p][lane] - top);
+}
+__device__ __forceinline__ float4 merge_token(const HeadArgs& a, int grad, int r, float top, float others,
+                                              float& loss) {
+  const int tg = a.tgt[a.row0 + r];
   float4 rs = {top, 0.f, 0.f, 0.f};
   if (tg < 0) {
     loss = __uint_as_float(0x7FC00000u);   // a target outside the vocabulary
-  } else {
-    const float z = a.zt[r], t = fmaxf(top, ceilf(z * kLog2e));   // no tile's reference covers the target
-    others *= exp2f(top - t);
-    const float y = fmaf(z, kLog2e, -t), e = exp2f(y);
-    loss = y > -60.f ? log1pf(others / e) : logf(others + e) - y * kLn2;
-    if (grad) {
-      rs.x = t;
-      rs.y = (a.grad_out && a.per_token ? a.grad_out[token] : 1.f) / (others + e);
-      rs.z = -rs.y * others;
-      if (a.softcap > 0.f) {
-        const float q = z / a.softcap;
-        rs.z *= 1.f - q * q;
-      }
+    return rs;
+  }
+  const float z = a.zt[r], t = fmaxf(top, ceilf(z * kLog2e));   // no tile's reference covers the target
+  others *= exp2f(top - t);
+  const float y = fmaf(z, kLog2e, -t), e = exp2f(y);
+  loss = y > -60.f ? log1pf(others / e) : logf(others + e) - y * kLn2;
+  if (grad) {
+    rs.x = t;
+    rs.y = (a.grad_out && a.per_token ? a.grad_out[a.idx[a.row0 + r]] : 1.f) / (others + e);
+    rs.z = -rs.y * others;
+    if (a.softcap > 0.f) {
+      const float q = z / a.softcap;
+      rs.z *= 1.f - q * q;
     }
   }
-  a.rs[r] = rs;
-  a.lossc[a.row0 + r] = loss;
-  if (a.per_token) a.loss[token] = loss;
+  return rs;
+}
+__device__ __forceinline__ void store_loss(const HeadArgs& a, int r, float loss) {
+  if (a.per_token) a.loss[a.idx[a.row0 + r]] = loss;
+  else a.lossc[a.row0 + r] = loss;
 }
 
-// One block: the reduced loss, the tokens' losses added in a fixed order in 64
-// bits.
-template <int THREADS>
-__device__ __forceinline__ void total_loss(const HeadArgs& a, double* sh) {
-  const int n = a.count[0];
-  double x = 0;
-  for (int i = threadIdx.x; i < n; i += THREADS) x += a.lossc[i];
-#pragma unroll
-  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0;
-    for (int i = 0; i < THREADS / 64; ++i) s += sh[i];
-    a.loss[0] = (float)(a.mean ? (n ? s / n : 0.0) : s);
-  }
-}
 __global__ __launch_bounds__(256) void k_total(HeadArgs a) {
   __shared__ double sh[4];
   total_loss<256>(a, sh);
@@ -272,27 +268,19 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
   __shared__ float tops[kMergeParts][64], sums[kMergeParts][64];
   __shared__ double sh[16];
   const int rows = piece_rows(a), lane = threadIdx.x & 63, part = threadIdx.x >> 6, r = blockIdx.x * 64 + lane;
-  float top = kRefFloor, others = 0.f;
-  if (r < rows) {
-#pragma unroll 4
-    for (int t = part; t < a.n_vt; t += kMergeParts) {
-      const float k = a.tmax[(int64_t)t * a.piece + r], x = a.tsum[(int64_t)t * a.piece + r], m = fmaxf(top, k);
-      others = others * exp2f(top - m) + x * exp2f(k - m);
-      top = m;
-    }
-  }
+  float top, others;
+  merge_tiles(a, r, rows, part, kMergeParts, top, others);
   tops[part][lane] = top;
   sums[part][lane] = others;
   __syncthreads();
   if (part == 0 && r < rows) {
-#pragma unroll
-    for (int p = 1; p < kMergeParts; ++p) top = fmaxf(top, tops[p][lane]);
-    others = 0.f;
-#pragma unroll
-    for (int p = 0; p < kMergeParts; ++p) others += sums[p][lane] * exp2f(tops[p][lane] - top);
-    merge_token(a, grad, r, top, others);
+    merge_parts<kMergeParts>(tops, sums, lane, top, others);
+    float loss;
+    const float4 rs = merge_token(a, grad, r, top, others, loss);
+    if (grad) a.rs[r] = rs;
+    store_loss(a, r, loss);
   }
-  if (!total_in_merge(a)) return;
+  if (grad || !total_in_merge(a)) return;
   __syncthreads();
   total_loss<1024>(a, sh);
 }
@@ -300,23 +288,41 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
 // Exponentials to the logits' gradient, in place, in panel order: a thread
 // keeps its token and goes over chunks, so a wave's accesses are whole
 // kilobytes. Rows past the valid ones (up to a whole panel, a stage of dW) and
-// columns past the vocabulary (a stage of dH) become zero. Bound by HBM: a read and a write of every
-// exponential.
+// columns past the vocabulary (a stage of dH) become zero. Bound by HBM: a
+// read and a write of every exponential. With few tiles (merged = 0) every
+// block merges its tokens' statistics itself, which costs less than a kernel.
 constexpr int kDzChunks = 64;   // chunks per block
+constexpr int kFuseTiles = 32;
 template <typename T>
-__global__ __launch_bounds__(256) void k_dlogits(HeadArgs a) {
+__global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged) {
   constexpr int CH = 16 / (int)sizeof(T);
-  __shared__ double sh[4];
-  if (blockIdx.y == gridDim.y - 1) {   // one more line of blocks: the reduced loss
-    if (blockIdx.x == 0 && !a.per_token && a.last && !total_in_merge(a)) total_loss<256>(a, sh);
-    return;
-  }
+  __shared__ float tops[4][64], sums[4][64];
+  __shared__ float4 merged_rs[64];
   const int rows = piece_rows(a), r0 = blockIdx.y * kPanelRows;
   if (r0 >= rows) return;
-  const int r = r0 + (threadIdx.x & 63);
+  const int lane = threadIdx.x & 63, r = r0 + lane;
   const int tg = r < rows ? a.tgt[a.row0 + r] : -1;
   const bool real = tg >= 0;
-  const float4 rs = real ? a.rs[r] : float4{0.f, 0.f, 0.f, 0.f};
+  float4 rs = {0.f, 0.f, 0.f, 0.f};
+  if (merged) {
+    if (real) rs = a.rs[r];
+  } else {
+    const int part = threadIdx.x >> 6;
+    float top, others;
+    merge_tiles(a, r, rows, part, 4, top, others);
+    tops[part][lane] = top;
+    sums[part][lane] = others;
+    __syncthreads();
+    if (part == 0 && r < rows) {
+      merge_parts<4>(tops, sums, lane, top, others);
+      float loss;
+      rs = merge_token(a, 1, r, top, others, loss);
+      merged_rs[lane] = rs;
+      if (blockIdx.x == 0) store_loss(a, r, loss);
+    }
+    __syncthreads();
+    if (real) rs = merged_rs[lane];
+  }
   const int last = a.vp / CH, c1 = min((int)(blockIdx.x + 1) * kDzChunks, last);
   uint8_t* base = (uint8_t*)a.e + ((int64_t)blockIdx.y * last << 10) + (threadIdx.x & 63) * 16;
   const float back = a.softcap > 0.f ? kLn2 / a.softcap : 0.f;
@@ -378,8 +384,8 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a) {
   T* dh = (T*)a.dh;
-  if ((int)blockIdx.x >= a.rows_max) {
-    const int64_t i = (int)blockIdx.x - a.rows_max;
+  if ((int)blockIdx.x >= a.rows_max * (a.split > 1)) {
+    const int64_t i = (int)blockIdx.x - a.rows_max * (a.split > 1);
     if (target_at(a.targets, a.target_bytes, i) != a.ignore) return;
     for (int c = threadIdx.x; c < a.d; c += 256) dh[i * a.ld_dh + c] = T(0);
     return;
@@ -438,6 +444,7 @@ hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v
   return hipGetLastError();
 }
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s) {
+  if (grad && a.n_vt <= kFuseTiles) return hipSuccess;   // with the logits' gradient
   hipLaunchKernelGGL(k_merge, dim3(panels(a)), dim3(64 * kMergeParts), 0, s, a, grad);
   if (!grad && a.last && !a.per_token && !total_in_merge(a))
     hipLaunchKernelGGL(k_total, dim3(1), dim3(256), 0, s, a);
@@ -445,10 +452,10 @@ hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s) {
 }
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s) {
   const int chunks = a.vp / (dt == MUON_BF16 ? 8 : 4);
-  BY_TYPE(dt, k_dlogits, dim3(cdiv(chunks, kDzChunks), panels(a) + 1), dim3(256), 0, s, a);
+  BY_TYPE(dt, k_dlogits, dim3(cdiv(chunks, kDzChunks), panels(a)), dim3(256), 0, s, a, (int)(a.n_vt > kFuseTiles));
 }
 hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, hipStream_t s) {
-  const int blocks = a.rows_max + (a.row0 == 0 ? a.n : 0);
+  const int blocks = a.rows_max * (a.split > 1) + (a.row0 == 0 ? a.n : 0);
   if (blocks == 0) return hipSuccess;
   BY_TYPE(dt, k_dhidden_out, dim3(blocks), dim3(256), 0, s, a);
 }

@@ -17,7 +17,7 @@ from typing import Sequence
 
 import torch
 
-from . import (MuonMatrix, MUON_BF16, MUON_F32, _DT, get_handle, load_library)
+from . import MuonMatrix, get_handle, load_library
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 
@@ -32,61 +32,37 @@ class LossConfig(ctypes.Structure):
 
 
 # ---------------------------------------------------------------------------
-# descriptors: a list is packed as five 64-bit words a tensor (MuonMatrix)
+# descriptors: packed natively (csrc/describe.cpp) into bytes, whose address
+# the C ABI takes. A matrix keeps its row stride; anything else (a vector, a
+# contiguous tensor of more dimensions) is one row.
 # ---------------------------------------------------------------------------
-_WORDS = ctypes.sizeof(MuonMatrix) // 8
-_CODE = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
+_native = None
 
 
-def _words(t: torch.Tensor, what: str, device: int, out: list) -> None:
-    """Append a tensor's descriptor: a matrix with its row stride, anything
-    else (a vector, a contiguous tensor of more dimensions) as one row."""
-    code = _CODE.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{what}: dtype {t.dtype} is not float32 or bfloat16")
-    if t.dim() == 2:
-        rows, cols = t.shape
-        if t.stride(1) != 1 and cols > 1 and rows:
-            raise ValueError(f"{what}: columns must be contiguous (stride(1) == 1)")
-        ld = t.stride(0) if rows > 1 else cols
-    else:
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: a tensor that is not a matrix must be contiguous")
-        rows, cols = 1, t.numel()
-        ld = cols
-    if rows and cols and t.get_device() != device:
-        raise ValueError(f"{what}: expected a tensor on GPU {device}, got {t.device}")
-    out += (t.data_ptr(), rows, cols, ld, code)
-
-
-_EMPTY = (0, 0, 0, 0, MUON_F32)
-
-
-def _pack(words: list):
-    return ctypes.cast((ctypes.c_int64 * max(_WORDS, len(words)))(*words), ctypes.POINTER(MuonMatrix))
-
-
-def _list(tensors: Sequence[torch.Tensor], what: str, device: int):
-    words: list = []
-    for t in tensors:
-        _words(t, what, device, words)
-    return _pack(words)
-
-
-def _same_shapes(a, b, what_a, what_b):
-    if len(a) != len(b):
-        raise ValueError(f"{what_a} and {what_b} differ in length")
-    for i, (x, y) in enumerate(zip(a, b)):
-        if x.shape != y.shape:
-            raise ValueError(f"{what_b}[{i}] has shape {tuple(y.shape)}, {what_a}[{i}] {tuple(x.shape)}")
+def _describe():
+    global _native
+    if _native is None:
+        try:
+            from . import _describe as module
+        except ImportError as e:
+            raise RuntimeError("the _describe extension is missing or does not load: build it with "
+                               f"`python -m muon_newton_schulz_update_amd.build` ({e})") from e
+        _native = module
+    return _native
 
 
 def _handle_for(tensors, handle):
     if handle is None:
-        device = next((t.get_device() for t in tensors if t.is_cuda), None)
-        handle = get_handle(device)
-    handle._bind_stream()
+        device = _describe().device_of(tensors)
+        handle = get_handle(None if device < 0 else device)
+    stream = torch._C._cuda_getCurrentRawStream(handle.device)
+    if stream != handle._stream:
+        handle._bind_stream()
     return handle
+
+
+def _pair(device: int) -> torch.Tensor:
+    return torch.empty(2, device=torch.device("cuda", device), dtype=torch.float32)
 
 
 def _scalar(t: torch.Tensor | None, what: str, device: int, n: int | None = None):
@@ -109,9 +85,9 @@ def grad_norm(grads: Sequence[torch.Tensor], *, max_norm: float | None = None, h
     grad_scale. Nothing waits for the GPU."""
     grads = list(grads)
     h = _handle_for(grads, handle)
-    out = torch.empty(2, device=f"cuda:{h.device}", dtype=torch.float32)
+    out = _pair(h.device)
     at = out.data_ptr()
-    h._check(h._lib.muon_grad_norm(h.ptr, len(grads), _list(grads, "grad", h.device),
+    h._check(h._lib.muon_grad_norm(h.ptr, len(grads), _describe().pack(grads, "grads", h.device),
                                    0.0 if max_norm is None else float(max_norm), at,
                                    None if max_norm is None else at + 4))
     return out[0] if max_norm is None else (out[0], out[1])
@@ -124,15 +100,12 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Seque
     clipping. In place, nothing is written when the norm is within the limit."""
     grads = list(grads)
     h = _handle_for(grads, handle)
-    outs = None
-    if out is not None:
-        out = list(out)
-        _same_shapes(grads, out, "grads", "out")
-        outs = _list(out, "out", h.device)
-    both = torch.empty(2, device=f"cuda:{h.device}", dtype=torch.float32)
+    pack = _describe().pack
+    words = pack(grads, "grads", h.device)
+    outs = None if out is None else pack(out, "out", h.device, grads, "grads")
+    both = _pair(h.device)
     at = both.data_ptr()
-    h._check(h._lib.muon_clip_grad_norm(h.ptr, len(grads), _list(grads, "grad", h.device), outs, float(max_norm), at,
-                                        at + 4))
+    h._check(h._lib.muon_clip_grad_norm(h.ptr, len(grads), words, outs, float(max_norm), at, at + 4))
     return both[0]
 
 
@@ -142,13 +115,10 @@ def scale(tensors: Sequence[torch.Tensor], coef: torch.Tensor, *, out: Sequence[
     `muon_scale`), in place or into `out`."""
     tensors = list(tensors)
     h = _handle_for(tensors, handle)
-    outs = None
-    if out is not None:
-        out = list(out)
-        _same_shapes(tensors, out, "tensors", "out")
-        outs = _list(out, "out", h.device)
-    h._check(h._lib.muon_scale(h.ptr, len(tensors), _list(tensors, "tensor", h.device), outs,
-                               _scalar(coef, "coef", h.device)))
+    pack = _describe().pack
+    words = pack(tensors, "tensors", h.device)
+    outs = None if out is None else pack(out, "out", h.device, tensors, "tensors")
+    h._check(h._lib.muon_scale(h.ptr, len(tensors), words, outs, _scalar(coef, "coef", h.device)))
 
 
 # ---------------------------------------------------------------------------
@@ -164,34 +134,21 @@ def adamw_update(grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor]
     the library's default. grad_scale: a float32 device scalar that multiplies
     every gradient (`grad_norm`'s coefficient). copies[i], when given, receives
     the new weight, for a model that computes on 16-bit copies of 32-bit ones."""
-    grads, exp_avgs, exp_avg_sqs, weights = list(grads), list(exp_avgs), list(exp_avg_sqs), list(weights)
-    _same_shapes(weights, grads, "weights", "grads")
-    _same_shapes(weights, exp_avgs, "weights", "exp_avgs")
-    _same_shapes(weights, exp_avg_sqs, "weights", "exp_avg_sqs")
+    weights = list(weights)
     h = _handle_for(weights, handle)
-    cp = None
-    if copies is not None:
-        if len(copies) != len(weights):
-            raise ValueError("weights and copies differ in length")
-        words: list = []
-        for i, (c, w) in enumerate(zip(copies, weights)):
-            if c is None:
-                words += _EMPTY
-                continue
-            if c.shape != w.shape:
-                raise ValueError(f"copies[{i}] has shape {tuple(c.shape)}, weights[{i}] {tuple(w.shape)}")
-            _words(c, "copy", h.device, words)
-        cp = _pack(words)
+    d, pack = h.device, _describe().pack
+    w = pack(weights, "weights", d)
+    lists = [pack(x, what, d, weights, "weights") for x, what in
+             ((grads, "grads"), (exp_avgs, "exp_avgs"), (exp_avg_sqs, "exp_avg_sqs"))]
+    cp = None if copies is None else pack(copies, "copies", d, weights, "weights")
     cfg = AdamWConfig()
     h._lib.muon_adamw_config_default(ctypes.byref(cfg))
     cfg.step = step
     for name, value in (("lr", lr), ("beta1", beta1), ("beta2", beta2), ("eps", eps), ("weight_decay", weight_decay)):
         if value is not None:
             setattr(cfg, name, value)
-    d = h.device
-    h._check(h._lib.adamw_update(h.ptr, len(weights), _list(grads, "grad", d), _list(exp_avgs, "exp_avg", d),
-                                 _list(exp_avg_sqs, "exp_avg_sq", d), _list(weights, "weight", d), cp,
-                                 ctypes.byref(cfg), _scalar(grad_scale, "grad_scale", d)))
+    h._check(h._lib.adamw_update(h.ptr, len(weights), *lists, w, cp, ctypes.byref(cfg),
+                                 _scalar(grad_scale, "grad_scale", d)))
 
 
 # ---------------------------------------------------------------------------
@@ -200,15 +157,13 @@ def adamw_update(grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor]
 def _matrix(t: torch.Tensor, what: str, device: int):
     if t.dim() != 2:
         raise ValueError(f"{what}: expected a 2-D tensor, got shape {tuple(t.shape)}")
-    words: list = []
-    _words(t, what, device, words)
-    return _pack(words)
+    return _describe().pack((t,), what, device)
 
 
 def _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_out, dhidden, dweight, grad, handle):
     if reduction not in REDUCTIONS:
         raise ValueError(f"unknown reduction {reduction!r}")
-    if hidden.dim() < 1 or tuple(targets.shape) != tuple(hidden.shape[:-1]):
+    if hidden.dim() < 1 or targets.shape != hidden.shape[:-1]:
         raise ValueError(f"targets of shape {tuple(targets.shape)} for hidden states of {tuple(hidden.shape)}")
     if targets.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"targets: dtype {targets.dtype} is not int64 or int32")
@@ -231,13 +186,13 @@ def _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_o
     dh = dw = None
     if dhidden is not False:
         if dhidden is None:
-            dhidden = torch.empty(hidden.shape, device=weight.device, dtype=hidden.dtype)
-        if dhidden.shape != hidden.shape:
+            dhidden = torch.empty_like(hidden, memory_format=torch.contiguous_format)
+        elif dhidden.shape != hidden.shape:
             raise ValueError(f"dhidden of shape {tuple(dhidden.shape)} for hidden states of {tuple(hidden.shape)}")
         dh = _matrix(dhidden if dhidden.dim() == 2 else dhidden.view(-1, dhidden.shape[-1]), "dhidden", d)
     if dweight is not False:
         if dweight is None:
-            dweight = torch.empty(weight.shape, device=weight.device, dtype=weight.dtype)
+            dweight = torch.empty_like(weight, memory_format=torch.contiguous_format)
         dw = _matrix(dweight, "dweight", d)
     h._check(h._lib.linear_cross_entropy_grad(*args, go, loss.data_ptr(), dh, dw))
     return loss, dhidden if dh is not None else None, dweight if dw is not None else None
