@@ -83,59 +83,59 @@ __device__ __forceinline__ int64_t target_at(const void* targets, int bytes, int
   return bytes == 8 ? ((const int64_t*)targets)[i] : (int64_t)((const int32_t*)targets)[i];
 }
 
-// Scans tokens [i0, i0 + 8 THREADS): this thread's eight targets, which of
-// them are valid (bits), the valid ones before them and of all.
+// Scans tokens [i0, i0 + 8 THREADS): thread t has tokens i0 + e THREADS + t,
+// their targets g[e] and, where valid, their places at[e] among the valid ones
+// (-1 elsewhere); returns how many there are. Loads and, through the places,
+// stores are coalesced.
 template <int THREADS>
-__device__ __forceinline__ void scan_targets(const void* targets, int bytes, int64_t ignore, int i0, int n,
-                                             int64_t (&g)[8], unsigned& valid, int& before, int& all, int* sums) {
-  const int t = threadIdx.x, i = i0 + t * 8;
+__device__ __forceinline__ int scan_targets(const void* targets, int bytes, int64_t ignore, int i0, int n,
+                                            int64_t (&g)[8], int (&at)[8], int* counts) {
+  constexpr int W = THREADS / 64;
+  const int t = threadIdx.x, w = t >> 6, lane = t & 63;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) g[e] = i + e < n ? target_at(targets, bytes, i + e) : ignore;
-  valid = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) valid |= (unsigned)(g[e] != ignore) << e;
-  const int c = __popc(valid);
-  int x = c;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(x, o);
-    if ((t & 63) >= o) x += y;
+  for (int e = 0; e < 8; ++e) {
+    const int i = i0 + e * THREADS + t;
+    g[e] = i < n ? target_at(targets, bytes, i) : ignore;
   }
-  if ((t & 63) == 63) sums[t >> 6] = x;
-  __syncthreads();
-  before = x - c;
-  all = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) {
-    if (w < (t >> 6)) before += sums[w];
-    all += sums[w];
+  for (int e = 0; e < 8; ++e) {
+    const uint64_t m = __ballot(g[e] != ignore);
+    at[e] = g[e] != ignore ? __popcll(m & ((1ull << lane) - 1)) : -1;
+    if (lane == 0) counts[e * W + w] = __popcll(m);
   }
   __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      if (k == w && at[e] >= 0) at[e] += all;
+      all += counts[e * W + k];
+    }
+  __syncthreads();
+  return all;
 }
 
 __device__ __forceinline__ int checked_target(const HeadArgs& a, int64_t g) { return g >= 0 && g < a.v ? (int)g : -1; }
 
 __global__ __launch_bounds__(1024) void k_compact(HeadArgs a) {
-  __shared__ int sums[16];
+  __shared__ int counts[8 * 16];
   int base = 0;
   for (int i0 = 0; i0 < a.n; i0 += 8192) {
     int64_t g[8];
-    unsigned valid;
-    int before, all;
-    scan_targets<1024>(a.targets, a.target_bytes, a.ignore, i0, a.n, g, valid, before, all, sums);
-    before += base;
-    base += all;
-    const int i = i0 + (int)threadIdx.x * 8;
+    int at[8];
+    const int all = scan_targets<1024>(a.targets, a.target_bytes, a.ignore, i0, a.n, g, at, counts);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (valid >> e & 1) {
-        a.idx[before] = i + e;
-        a.tgt[before] = checked_target(a, g[e]);
-        ++before;
-      } else if (a.per_token && i + e < a.n) {
-        a.loss[i + e] = 0.f;
+      const int i = i0 + e * 1024 + (int)threadIdx.x;
+      if (at[e] >= 0) {
+        a.idx[base + at[e]] = i;
+        a.tgt[base + at[e]] = checked_target(a, g[e]);
+      } else if (a.per_token && i < a.n) {
+        a.loss[i] = 0.f;
       }
     }
+    base += all;
   }
   if (threadIdx.x == 0) a.count[0] = base;
 }
@@ -146,27 +146,25 @@ __global__ __launch_bounds__(1024) void k_compact(HeadArgs a) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan) {
   constexpr int CH = 16 / (int)sizeof(T);
-  __shared__ int list[kPanelRows], sums[4];
+  __shared__ int list[kPanelRows], counts[8 * 4];
   const int r0 = blockIdx.y * kPanelRows;
   int rows;
   if (scan) {
     const bool lists = blockIdx.x == 0 && blockIdx.y == 0;   // this block writes them
     int64_t g[8];
-    unsigned valid;
-    int before;
-    scan_targets<256>(a.targets, a.target_bytes, a.ignore, 0, a.n, g, valid, before, rows, sums);
-    const int i = (int)threadIdx.x * 8;
+    int at[8];
+    rows = scan_targets<256>(a.targets, a.target_bytes, a.ignore, 0, a.n, g, at, counts);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (valid >> e & 1) {
-        if (before >= r0 && before < r0 + kPanelRows) list[before - r0] = i + e;
+      const int i = e * 256 + (int)threadIdx.x;
+      if (at[e] >= 0) {
+        if (at[e] >= r0 && at[e] < r0 + kPanelRows) list[at[e] - r0] = i;
         if (lists) {
-          a.idx[before] = i + e;
-          a.tgt[before] = checked_target(a, g[e]);
+          a.idx[at[e]] = i;
+          a.tgt[at[e]] = checked_target(a, g[e]);
         }
-        ++before;
-      } else if (lists && a.per_token && i + e < a.n) {
-        a.loss[i + e] = 0.f;
+      } else if (lists && a.per_token && i < a.n) {
+        a.loss[i] = 0.f;
       }
     }
     if (lists && threadIdx.x == 0) a.count[0] = rows;
@@ -269,16 +267,33 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
   __shared__ double sh[16];
   const int rows = piece_rows(a), lane = threadIdx.x & 63, part = threadIdx.x >> 6, r = blockIdx.x * 64 + lane;
   float top, others;
-  merge_tiles(a, r, rows, part, kMergeParts, top, others);
-  tops[part][lane] = top;
-  sums[part][lane] = others;
-  __syncthreads();
-  if (part == 0 && r < rows) {
-    merge_parts<kMergeParts>(tops, sums, lane, top, others);
-    float loss;
-    const float4 rs = merge_token(a, grad, r, top, others, loss);
-    if (grad) a.rs[r] = rs;
-    store_loss(a, r, loss);
+  if (a.rows_max <= kMergeParts) {
+    // few tokens: a wave for each, its lanes over the tiles
+    merge_tiles(a, part, rows, lane, 64, top, others);
+    float all = top;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) all = fmaxf(all, __shfl_xor(all, o));
+    others *= exp2f(top - all);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) others += __shfl_xor(others, o);
+    if (lane == 0 && part < rows) {
+      float loss;
+      const float4 rs = merge_token(a, grad, part, all, others, loss);
+      if (grad) a.rs[part] = rs;
+      store_loss(a, part, loss);
+    }
+  } else {
+    merge_tiles(a, r, rows, part, kMergeParts, top, others);
+    tops[part][lane] = top;
+    sums[part][lane] = others;
+    __syncthreads();
+    if (part == 0 && r < rows) {
+      merge_parts<kMergeParts>(tops, sums, lane, top, others);
+      float loss;
+      const float4 rs = merge_token(a, grad, r, top, others, loss);
+      if (grad) a.rs[r] = rs;
+      store_loss(a, r, loss);
+    }
   }
   if (grad || !total_in_merge(a)) return;
   __syncthreads();

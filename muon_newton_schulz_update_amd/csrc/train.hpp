@@ -16,7 +16,8 @@ namespace muon {
 constexpr int kChunk = 8192;      // elements per work item of a list kernel
 constexpr int kNormMax = 88;      // tensors per norm or scale launch
 constexpr int kAdamMax = 32;      // tensors per AdamW launch
-constexpr int kNormBlocks = 2048; // blocks of a norm launch at most (one partial each)
+constexpr int kNormChunk = 32768; // the norm kernel's (1024 threads, four pieces of eight elements each)
+constexpr int kNormBlocks = 512;  // blocks of a norm launch at most (one partial each)
 
 struct ListItem {      // one tensor: 40 bytes
   const void* src;

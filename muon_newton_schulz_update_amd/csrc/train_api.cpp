@@ -54,7 +54,7 @@ muon_status norm_run(muon_handle* h, int n, const muon_matrix* g, float max_norm
     L.n = 0;
     for (; i < n && L.n < kNormMax; ++i) {
       if (empty(g[i])) continue;
-      const int64_t e = g[i].rows * g[i].cols, k = cdiv(e, kChunk);
+      const int64_t e = g[i].rows * g[i].cols, k = cdiv(e, kNormChunk);
       if (c + k > kMaxChunks && L.n) break;
       L.chunk0[L.n] = (int32_t)c;
       L.t[L.n++] = ListItem{g[i].ptr, g[i].ld, g[i].cols, e, g[i].dtype, is_flat(g[i]) ? 1 : 0};
