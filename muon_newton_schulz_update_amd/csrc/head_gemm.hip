@@ -5,7 +5,8 @@
 //   dweight   dW  = dz^T H      vocabulary x width,  K = tokens
 //
 // One kernel shape for the three: a 256 x 256 tile per workgroup of 8 waves
-// (or 128 x 128 of 4, two workgroups to a CU, where tiles are few),
+// (or 128 x 128 of 4 and 64 x 64 of 2, two and four workgroups to a CU, where
+// tiles are few),
 // K in stages of 128 bytes (64 bf16, 32 fp32), both operands of a stage
 // brought to LDS by direct buffer loads into a ring of five slots, so
 // that while one stage feeds the matrix cores the next and half of the one
@@ -20,7 +21,7 @@
 //   OP_ROW_K    row-major matrix, K along the row: [256 rows][8 chunks],
 //               chunk ^ (row / 2) % 8
 //   OP_ROW_T    row-major matrix, K down the rows: [K rows][columns],
-//               bf16: chunk ^ (row % 4) 4
+//               bf16: chunk ^ (row % 4) 4 (64-tiles: chunk ^ (row / 2 % 2) 4)
 //   OP_PANEL_K  panels (train.hpp), K along the chunks: [4 token blocks]
 //               [8 chunks][64 tokens], no conflicts as it is
 //   OP_PANEL_T  panels, K down the tokens: [chunks][K tokens], token ^ (chunk
@@ -30,7 +31,6 @@
 // with zeros on one side at least).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "head_device.hpp"
 #include "train.hpp"
@@ -100,14 +100,18 @@ struct Operand {
   uint32_t lane;         // this lane's byte offset, the same in every stage
 };
 
-// Tile edges: 256 (8 waves, one workgroup per CU) and 128 (4 waves, two). A
-// stage of an operand is TILE x 128 bytes, TILE / 8 loads of 1 KB, four a wave.
+// Tile edges: 256 (8 waves, one workgroup per CU), 128 (4 waves, two) and 64
+// (2 waves, four). A stage of an operand is TILE x 128 bytes, TILE / 8 loads of
+// 1 KB, four a wave.
 template <typename T, int L, int TILE>
 struct Op {
   static constexpr int KE = 128 / (int)sizeof(T);
   static constexpr int NW = TILE / 32;                        // waves
   static constexpr int kRowT = TILE * (int)sizeof(T);         // LDS row of OP_ROW_T, bytes
   static constexpr int kRowsPerLoad = 1024 / kRowT;           // its rows per load
+  // bank swizzle of an OP_ROW_T row (16-bit): a read takes four chunks of four
+  // rows at once, which the pitch puts on the same banks (or every second row)
+  __device__ static int row_t_swizzle(int row) { return kRowT == 128 ? (row & 2) << 1 : (row & 3) << 2; }
   // the lane's part of a load's address (row layouts: the column part)
   __device__ static uint32_t lane_part(int lane, int wave, int last_chunk) {
     if constexpr (L == OP_ROW_K) {
@@ -115,7 +119,7 @@ struct Op {
       return ((lane & 7) ^ ((row >> 1) & 7)) * 16;
     } else if constexpr (L == OP_ROW_T) {
       const int per = 64 / kRowsPerLoad, row = kRowsPerLoad * wave + lane / per, c = lane % per;
-      return min(sizeof(T) == 2 ? c ^ ((row & 3) << 2) : c, last_chunk) * 16;
+      return min(sizeof(T) == 2 ? c ^ row_t_swizzle(row) : c, last_chunk) * 16;
     } else if constexpr (L == OP_PANEL_K) {
       return lane * 16;
     } else {
@@ -138,6 +142,8 @@ struct Op {
       p += (int64_t)ks * 8192;
       soff = (g >> 3) * o.pitch + (g & 7) * 1024;
     } else {
+      // (two waves: a wave's loads alternate between two values of the swizzle)
+      if constexpr (NW == 2) voff ^= (i & 1) * (sizeof(T) == 2 ? 128 : 64);
       if constexpr (sizeof(T) == 2) {
         p += (int64_t)ks * o.pitch;
         soff = min(g, o.lim) * 1024;
@@ -168,7 +174,7 @@ struct Op {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int kk = k + 4 * j;
-        const uint8_t* p = L == OP_ROW_T ? sm + kk * kRowT + (c ^ ((kk & 3) << 2)) * 16 + (i & 1) * 8
+        const uint8_t* p = L == OP_ROW_T ? sm + kk * kRowT + (c ^ row_t_swizzle(kk)) * 16 + (i & 1) * 8
                                          : sm + c * 1024 + (kk ^ ((c & 3) << 2)) * 16 + (i & 1) * 8;
         q[j] = read_tr16((lds_s16x4_t*)p);
       }
@@ -323,19 +329,20 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 
 // ---------------------------------------------------------------------------
 // Logits. The vocabulary is on the accumulators' rows and the tokens on their
-// columns, so a lane holds 64 logits of each of its two tokens: maximum and
-// sum need one exchange with the other half-wave. The statistics are per
-// wave's 128 vocabulary rows, so waves never wait for one another. The
+// columns, so a lane holds 64 logits of each of its two tokens (32 of one in the
+// smallest tiles): maximum and sum need one exchange with the other half-wave.
+// The statistics are per wave's vocabulary rows, so waves never wait for one another. The
 // exponentials go to the panels as whole chunks after a half-wave swap.
 // ---------------------------------------------------------------------------
 template <typename T, int TILE>
-__global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
-  constexpr int MI = 4, NI = TILE / 128, WM = TILE / 128;   // a wave: 128 vocabulary rows
+__global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
+  // a wave: 128 vocabulary rows (64 of a 64-tile) x 64 tokens (256) or 32
+  constexpr int MI = TILE == 64 ? 2 : 4, NI = TILE == 256 ? 2 : 1, WM = TILE / (MI * 32), WN = TILE / (NI * 32);
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * TILE * 128];
   int vi, ti;
   const int rows = piece_rows(a), lane = threadIdx.x & 63;
   if (!strip_tile<4>(xcd_index(blockIdx.x), vt, min(tt, (rows + TILE - 1) / TILE), vi, ti)) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   const int v0 = vi * TILE, r0 = ti * TILE;
   typedef Op<T, OP_ROW_K, TILE> A;
   typedef Op<T, OP_PANEL_K, TILE> B;
@@ -348,11 +355,11 @@ __global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_logits_mfma(H
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
-  k_loop<T, OP_ROW_K, OP_PANEL_K, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 128, wn * NI * 32, 0,
+  k_loop<T, OP_ROW_K, OP_PANEL_K, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0,
                                                 a.dp / A::KE);
 
   const int lr = lane & 31, hf = lane >> 5;
-  const int vw = v0 + wm * 128;                      // the wave's first vocabulary row
+  const int vw = v0 + wm * MI * 32;                  // the wave's first vocabulary row
   if (vw >= a.v) return;                             // (the exponentials' padding is cleared with the gradient)
   const int tile = vi * WM + wm;
   if (a.softcap > 0.f) {
@@ -369,7 +376,7 @@ __global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_logits_mfma(H
         }
   }
   const float none = -__builtin_inff();
-  if (vw + 128 > a.v) {
+  if (vw + MI * 32 > a.v) {
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
@@ -383,7 +390,7 @@ __global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_logits_mfma(H
     const int r = r0 + (wn * NI + ni) * 32 + lr;       // the lane's token in the piece
     // the target's logit leaves the tile: it has its own place in the sums
     const int tg = (r < rows ? a.tgt[a.row0 + r] : -1) - vw - 4 * hf;
-    const bool mine = tg >= 0 && tg < 128 && (tg & 4) == 0;
+    const bool mine = tg >= 0 && tg < MI * 32 && (tg & 4) == 0;
     if (__any(mine)) {
       float z = 0.f;
 #pragma unroll
@@ -643,7 +650,7 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
 // the CUs that the last round of the other's leaves idle (the 50304 x 768
 // weight's 591 tiles are 2.3 rounds of the 256 CUs).
 template <typename T, int TILE>
-__global__ __launch_bounds__(TILE * 2, TILE == 256 ? 1 : 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
+__global__ __launch_bounds__(TILE * 2, 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
                                                                                   int weight_first) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * TILE * 128];
   const int rows = piece_rows(a);
@@ -672,64 +679,79 @@ inline int xcd_grid(int64_t n) { return n > 0 ? cdiv(n, 256) * 256 : 256; }
 }  // namespace
 
 // Tile edge of a launch, from its number of 256-tiles: with few of them
-// 128-tiles, four times as many and two to a CU, cover the CUs better. fp32
-// always takes 128: its matrix instructions are slow enough to hide the extra
-// operand traffic, and 256-tiles of its gradients do not fit the registers.
-//   measured (bf16, loss alone, 128 / 256): 384 tiles 62.7 / 67.6 us, 591
-//   170.5 / 174.4, 768 113.6 / 103.6, 1182 142.8 / 136.8; gradients: 708
-//   249 / 253, 825 470 / 459, 1760 916 / 764 (whole calls)
-constexpr int kFewTiles = 768;
-// dW's K is the tokens: with few of them its tiles are all start-up and
-// epilogue, which two workgroups to a CU overlap (300 tokens x 50304 x 2048:
-// 338 us with 128-tiles, 384 with 256; 700 tokens 587 and 556).
-constexpr int kShortK = 512;
-static int tile_of(int dt, int64_t tiles) {
-  if (const char* v = getenv("HEAD_TILE")) if (dt == MUON_BF16) return atoi(v);
-  return dt != MUON_BF16 || tiles < kFewTiles ? 128 : 256;
+// 128-tiles, four times as many and two to a CU, cover the CUs better, and
+// 64-tiles where those are few in turn. Measured:
+//   128 / 256, bf16, loss alone: 384 tiles 62.7 / 67.6 us, 591 170.5 / 174.4,
+//   768 113.6 / 103.6, 1182 142.8 / 136.8; whole calls with gradients: 708
+//   249 / 253, 825 470 / 459, 1760 916 / 764
+//   64 / 128, bf16, loss alone: 64 tiles 22.1 / 25.9 us, 200 18.0 / 18.7, 393
+//   39.2 / 34.0, 471 23.6 / 21.5; gradients without the loss: 350 32.7 / 33.7,
+//   410 60.5 / 57.8, 2358 65 / 55
+// fp32's matrix instructions are slow enough to hide the operand traffic of
+// 64-tiles (loss alone 64 / 128: 252 tiles 46.7 / 48.3, 628 67.0 / 64.4), and
+// its gradients always take those (634 tiles 440 / 465).
+constexpr int kFewTiles = 768, kFewSmallTiles = 384;
+static int tile_of(int dt, int64_t tiles256, int64_t tiles128) {
+  if (dt == MUON_BF16 && tiles256 >= kFewTiles) return 256;
+  return tiles128 >= kFewSmallTiles ? 128 : 64;
 }
 
-#define LAUNCH_TILES(k, dt, tile, n, ...)                                                                       \
-  do {                                                                                                          \
-    const dim3 g(xcd_grid(n)), b((tile) * 2);                                                                   \
-    if ((dt) != MUON_BF16) hipLaunchKernelGGL((k<float, 128>), g, b, 0, s, __VA_ARGS__);                        \
-    else if ((tile) == 256) hipLaunchKernelGGL((k<u16, 256>), g, b, 0, s, __VA_ARGS__);                         \
-    else hipLaunchKernelGGL((k<u16, 128>), g, b, 0, s, __VA_ARGS__);                                            \
-    return hipGetLastError();                                                                                   \
-  } while (0)
-
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
-  const int rows = a.rows_max;
-  const int tile = tile_of(dt, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256));
-  const int vt = cdiv(a.v, tile), tt = cdiv(rows, tile);
-  LAUNCH_TILES(k_logits_mfma, dt, tile, (int64_t)vt * tt, a, keep, vt, tt);
+  const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
+  const dim3 g(xcd_grid((int64_t)vt * tt)), b(tile * 2);
+  if (dt == MUON_BF16 && tile == 256) hipLaunchKernelGGL((k_logits_mfma<u16, 256>), g, b, 0, s, a, keep, vt, tt);
+  else if (dt == MUON_BF16 && tile == 128) hipLaunchKernelGGL((k_logits_mfma<u16, 128>), g, b, 0, s, a, keep, vt, tt);
+  else if (dt == MUON_BF16) hipLaunchKernelGGL((k_logits_mfma<u16, 64>), g, b, 0, s, a, keep, vt, tt);
+  else if (tile == 128) hipLaunchKernelGGL((k_logits_mfma<float, 128>), g, b, 0, s, a, keep, vt, tt);
+  else hipLaunchKernelGGL((k_logits_mfma<float, 64>), g, b, 0, s, a, keep, vt, tt);
+  return hipGetLastError();
 }
 
 hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
   const int rows = a.rows_max, unit = dt == MUON_BF16 ? 64 : 32, tile = a.grad_tile;
   const int tt = a.dh ? cdiv(rows, tile) : 0, vt = a.dw ? cdiv(a.v, tile) : 0, nd = cdiv(a.dp, tile);
   // the longer tiles go first
-  const int weight_first = cdiv(rows, unit) > cdiv(a.v, unit) / a.split;
-  LAUNCH_TILES(k_gradients_mfma, dt, tile, ((int64_t)tt * a.split + vt) * nd + 1, a, vt, tt, nd, weight_first);
+  const int wf = cdiv(rows, unit) > cdiv(a.v, unit) / a.split;
+  const dim3 g(xcd_grid(((int64_t)tt * a.split + vt) * nd + 1)), b(tile * 2);
+  if (dt != MUON_BF16) hipLaunchKernelGGL((k_gradients_mfma<float, 64>), g, b, 0, s, a, vt, tt, nd, wf);
+  else if (tile == 256) hipLaunchKernelGGL((k_gradients_mfma<u16, 256>), g, b, 0, s, a, vt, tt, nd, wf);
+  else if (tile == 128) hipLaunchKernelGGL((k_gradients_mfma<u16, 128>), g, b, 0, s, a, vt, tt, nd, wf);
+  else hipLaunchKernelGGL((k_gradients_mfma<u16, 64>), g, b, 0, s, a, vt, tt, nd, wf);
+  return hipGetLastError();
 }
 
-// Tile edge and splits of the vocabulary of the gradients' launch. dH's tiles
-// alone (tokens x width) are fewer than the CUs for one piece of a narrow
-// model. A launch lasts its stages over the CUs, each tile with the ring's
-// start-up (about six stages), half of its shortest tile at the end, and the
-// traffic of the partial sums (a 256-tile's stage takes about 2 us, as long
-// as 9 MB of HBM; a 128-tile's a quarter on half a CU).
-void head_gradient_plan(HeadArgs& a, int dt) {
+// dW's K is the tokens: with few of them its tiles are all start-up and
+// epilogue, which two workgroups to a CU overlap (300 tokens x 50304 x 2048:
+// 338 us with 128-tiles, 384 with 256; 700 tokens 587 and 556).
+constexpr int kShortK = 512;
+
+// Tile edges of the products, columns per statistic, and splits of the
+// vocabulary in dH, whose tiles alone (tokens x width) are fewer than the CUs
+// for one piece of a narrow model. The gradients' launch lasts its stages over
+// the CUs, each tile with the ring's start-up (about six stages), half of its
+// shortest tile at the end, and the traffic of the partial sums (a 256-tile's
+// stage takes about 2 us, as long as 9 MB of HBM; a smaller one's half, on a
+// part of a CU).
+void head_plan(HeadArgs& a, int dt) {
   const int rows = a.n < a.piece ? a.n : a.piece, unit = dt == MUON_BF16 ? 64 : 32;
-  const int64_t wide = (int64_t)cdiv(a.v, 256) * cdiv(a.dp, 256) * (a.dw ? 1 : 0);
+  a.logit_tile = tile_of(dt, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256), (int64_t)cdiv(a.v, 128) * cdiv(rows, 128));
+  a.vtile = a.logit_tile == 64 ? 64 : 128;
+  a.n_vt = cdiv(a.v, a.vtile);
+  a.split = 1;
+  if (!a.dh && !a.dw) return;
   const int64_t stages = cdiv(a.v, unit);
-  a.grad_tile = rows < kShortK ? 128 : tile_of(dt, wide + (a.dh ? cdiv(rows, 256) * cdiv(a.dp, 256) * (stages / 64 + 1) : 0));
-  const int tile = a.grad_tile, slots = tile == 256 ? 256 : 512;
+  auto tiles_of = [&](int edge) {
+    return (a.dw ? (int64_t)cdiv(a.v, edge) * cdiv(a.dp, edge) : 0) +
+           (a.dh ? (int64_t)cdiv(rows, edge) * cdiv(a.dp, edge) * (stages / 64 + 1) : 0);
+  };
+  a.grad_tile = dt == MUON_BF16 ? tile_of(dt, rows < kShortK ? 0 : tiles_of(256), tiles_of(128)) : 64;
+  if (!a.dh) return;
+  const int tile = a.grad_tile, slots = 256 * (256 / tile);
   const int64_t tiles = (int64_t)cdiv(rows, tile) * cdiv(a.dp, tile);
   const double other = a.dw ? (double)cdiv(a.v, tile) * cdiv(a.dp, tile) * (cdiv(rows, unit) + 6) : 0.0;
   const double sum = (double)rows * a.dp * 8 / (tile == 256 ? 9e6 : 4.5e6);
   double least = 0;
-  a.split = 1;
-  for (int n = 1; a.dh && n <= 256 && (n == 1 || stages / n >= 4); ++n) {
+  for (int n = 1; n <= 256 && (n == 1 || stages / n >= 4); ++n) {
     const double each = (double)cdiv(stages, n) + 6, t0 = (tiles * n * each + other) / slots + each / 2;
     // more than one split: the sum is a launch of its own, about 5 us
     const double t = (t0 > each ? t0 : each) + (n > 1 ? n * sum + (tile == 256 ? 3 : 5) : 0);

@@ -306,10 +306,9 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
 // columns past the vocabulary (a stage of dH) become zero. Bound by HBM: a
 // read and a write of every exponential. With few tiles (merged = 0) every
 // block merges its tokens' statistics itself, which costs less than a kernel.
-constexpr int kDzChunks = 64;   // chunks per block
 constexpr int kFuseTiles = 32;
 template <typename T>
-__global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged) {
+__global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int block_chunks) {
   constexpr int CH = 16 / (int)sizeof(T);
   __shared__ float tops[4][64], sums[4][64];
   __shared__ float4 merged_rs[64];
@@ -338,11 +337,11 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged) {
     __syncthreads();
     if (real) rs = merged_rs[lane];
   }
-  const int last = a.vp / CH, c1 = min((int)(blockIdx.x + 1) * kDzChunks, last);
+  const int last = a.vp / CH, c1 = min((int)(blockIdx.x + 1) * block_chunks, last);
   uint8_t* base = (uint8_t*)a.e + ((int64_t)blockIdx.y * last << 10) + (threadIdx.x & 63) * 16;
   const float back = a.softcap > 0.f ? kLn2 / a.softcap : 0.f;
 #pragma unroll 4
-  for (int c = blockIdx.x * kDzChunks + (threadIdx.x >> 6); c < c1; c += 4) {
+  for (int c = blockIdx.x * block_chunks + (threadIdx.x >> 6); c < c1; c += 4) {
     uint8_t* p = base + ((int64_t)c << 10);
     const int v = c * CH;
     float x[CH];
@@ -412,6 +411,7 @@ __global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a) {
   const bool whole = a.ld_dh % 4 == 0 && (uintptr_t)a.dh % (4 * sizeof(T)) == 0;
   for (int c = threadIdx.x * 4; c < a.d; c += 1024) {
     f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int q = 0; q < a.split; ++q) x += *(const f32x4_t*)(a.part + ((int64_t)q * a.piece + r) * a.dp + c);
     T* dst = dh + token * a.ld_dh + c;
     if (whole && c + 4 <= a.d) {
@@ -467,7 +467,9 @@ hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s) {
 }
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s) {
   const int chunks = a.vp / (dt == MUON_BF16 ? 8 : 4);
-  BY_TYPE(dt, k_dlogits, dim3(cdiv(chunks, kDzChunks), panels(a)), dim3(256), 0, s, a, (int)(a.n_vt > kFuseTiles));
+  // chunks per block: 64, or 16 where that leaves CUs without four blocks
+  const int per = (int64_t)cdiv(chunks, 64) * panels(a) < 1024 ? 16 : 64;
+  BY_TYPE(dt, k_dlogits, dim3(cdiv(chunks, per), panels(a)), dim3(256), 0, s, a, (int)(a.n_vt > kFuseTiles), per);
 }
 hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, hipStream_t s) {
   const int blocks = a.rows_max * (a.split > 1) + (a.row0 == 0 ? a.n : 0);

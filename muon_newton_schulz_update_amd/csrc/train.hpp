@@ -103,7 +103,6 @@ constexpr int kPanelRows = 64;
 // bits of exponent and 10 high bits of mantissa, rounded half up; kCodeBase is
 // the pattern of 2^-63 shifted down.
 constexpr uint32_t kCodeBase = 64u << 10;
-constexpr int kStatCols = 128;     // vocabulary columns per reference and partial sum of a token
 template <typename T>
 __host__ __device__ inline int64_t panel_at(int64_t row, int64_t col, int64_t ld) {
   constexpr int ch = 16 / (int)sizeof(T);
@@ -117,7 +116,7 @@ struct HeadArgs {
   void* dw;        int64_t ld_dw;
   int32_t n, v, d;                    // tokens, vocabulary, width
   int32_t dp, vp;                     // padded width (64 or 32 elements), padded vocabulary (256)
-  int32_t vtile, n_vt;                // columns per logits tile, tiles
+  int32_t vtile, n_vt;                // vocabulary columns per statistic of a token, statistics
   int32_t piece, row0;                // tokens per piece (buffers), first compact token of this piece
   int32_t rows_max;                   // tokens of this piece if none is ignored
   const void* targets;
@@ -139,15 +138,16 @@ struct HeadArgs {
   float4* rs;                         // piece: {reference, factor, target's gradient, 0}
   float* part;                        // dH partial sums: split x piece x dp
   int32_t split;                      // parts of the vocabulary in dH
-  int32_t grad_tile;                  // tile edge of the gradients' products
+  int32_t logit_tile, grad_tile;      // tile edges of the products
   float* dwacc;                       // v x dp fp32 sum over pieces, or null: one piece
   int32_t first, last;                // this piece starts / ends the sum over pieces
   float* loss;                        // caller's: one value, or n
   const float* grad_out;              // device, or null (1)
 };
 
-// Picks grad_tile and split (before the workspace is laid out).
-void head_gradient_plan(HeadArgs& a, int dt);
+// Picks the tile edges, the statistics' columns and the splits, from the sizes
+// and from which gradients are wanted (before the workspace is laid out).
+void head_plan(HeadArgs& a, int dt);
 hipError_t launch_head_compact(const HeadArgs& a, hipStream_t s);
 hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s);
 hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v, int d, int dp, int dt,

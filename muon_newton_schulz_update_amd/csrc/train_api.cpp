@@ -136,8 +136,6 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const int unit = 128 / e;                       // a stage of a product: 128 bytes of the contraction
   a.dp = (int)(cdiv(a.d, unit) * unit);
   a.vp = (int)(cdiv(a.v, 256) * 256);
-  a.vtile = kStatCols;
-  a.n_vt = (int)cdiv(a.v, a.vtile);
   a.per_token = cfg.reduction == MUON_REDUCE_NONE;
   a.mean = cfg.reduction == MUON_REDUCE_MEAN;
   a.softcap = cfg.softcap;
@@ -160,11 +158,11 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   // 16-byte pieces with no remainder; otherwise a padded copy
   const bool direct = a.d % unit == 0 && (uintptr_t)wgt.ptr % 16 == 0 && (wgt.rows == 1 || (wgt.ld * e % 16 == 0 && wgt.ld * e < (1 << 23)));
   // pieces
-  const size_t row = (size_t)a.dp * e + (size_t)a.n_vt * 8 + 24 + (grad ? (size_t)a.vp * e : 0);
+  const size_t row = (size_t)a.dp * e + (size_t)cdiv(a.v, 64) * 8 + 24 + (grad ? (size_t)a.vp * e : 0);
   const int64_t most = std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows);
   const int64_t pieces = std::max<int64_t>(1, cdiv(a.n, most));
   a.piece = (int)(std::max<int64_t>(1, cdiv(cdiv(a.n, pieces), kPieceRows)) * kPieceRows);
-  if (grad) head_gradient_plan(a, dt);
+  head_plan(a, dt);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
