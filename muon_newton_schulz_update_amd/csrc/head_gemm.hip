@@ -53,6 +53,7 @@ enum OpLayout { OP_ROW_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
 enum Product { P_LOGITS, P_DHIDDEN, P_DWEIGHT };
 
 constexpr int kSlots = 5;
+constexpr int kFewTokens = 64;    // whose dW takes the targets' remainders too
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kRefFloor = -3.0e38f;
 
@@ -72,6 +73,7 @@ __device__ __forceinline__ unsigned int pack_bf16(float lo, float hi) {
   const bf16x2_t q = {(__bf16)lo, (__bf16)hi};
   return __builtin_bit_cast(unsigned int, q);
 }
+__device__ __forceinline__ float bf2f(u16 h) { return __uint_as_float((unsigned int)h << 16); }
 // Hand-off through LDS between the lanes of one wave: the LDS executes a
 // wave's accesses in order, so only the compiler has to keep them so.
 __device__ __forceinline__ void wave_lds_sync() {
@@ -500,6 +502,23 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
   // one split: the tokens' rows themselves, put together in the idle LDS
   const float g = common_factor(a);
   const int rw = r0 + wm * 64, dw = d0 + wn * NI * 32;      // the wave's part
+  if constexpr (sizeof(T) == 2) {
+    // what the target's gradient lost in its rounding
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int t = rw + mi * 32 + 8 * (r >> 2) + 4 * hf + (r & 3);
+        const float rest = t < rows ? a.rs[t].w : 0.f;
+        if (rest == 0.f) continue;
+        const u16* w = (const u16*)a.w + (int64_t)a.tgt[a.row0 + t] * a.ld_w;
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) {
+          const int d = dw + ni * 32 + lr;
+          if (d < a.d) acc[mi][ni][r] = fmaf(rest, bf2f(w[d]), acc[mi][ni][r]);
+        }
+      }
+  }
   constexpr int NC = NI * 32 * (int)sizeof(T) / 16, CH = 16 / (int)sizeof(T);   // chunks of its row
   ring_barrier();                                           // every wave is done with the slots
   uint8_t* slab = smem + wave * (32 * NC * 16);
@@ -567,6 +586,34 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
     k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * 64, 0, nk);
   const float g = common_factor(a);
   const int vw = v0 + wn * 64, dw = d0 + wm * MI * 32;      // the wave's part
+  if constexpr (sizeof(T) == 2) {
+    // few tokens, one to a lane: what the targets' gradients lost in their
+    // rounding, for those with their target among the wave's rows (one piece:
+    // row0 is 0)
+    const bool few = a.n <= kFewTokens && lane < rows;
+    const int lane_at = few ? a.tgt[lane] - vw : -1;
+    const float lane_rest = few ? a.rs[lane].w : 0.f;
+    uint64_t todo = __ballot(lane_at >= 0 && lane_at < 64 && lane_rest != 0.f);
+    for (; todo; todo &= todo - 1) {
+      const int i = __builtin_ctzll(todo), at = __builtin_amdgcn_readlane(lane_at, i);
+      const float rest = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_rest), i));
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        if (at != ni * 32 + lr) continue;
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int d = dw + mi * 32 + 8 * q + 4 * hf;
+            if (d >= a.dp) continue;
+            const u32x2_t h = *(const u32x2_t*)((const u16*)a.hp + panel_at<u16>(i, d, a.dp));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[mi][ni][4 * q + e] = fmaf(rest, bf2f((u16)(h[e >> 1] >> (16 * (e & 1)))), acc[mi][ni][4 * q + e]);
+          }
+      }
+    }
+  }
   if (a.dwacc) {
     // sums over pieces: padded rows, whole 16-byte groups
     float* acc_at = a.dwacc + (int64_t)(vw + lr) * a.dp + dw + 4 * hf;
@@ -676,8 +723,6 @@ inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // blocks for n tiles dealt to the XCDs in runs of 32 (xcd_index)
 inline int xcd_grid(int64_t n) { return n > 0 ? cdiv(n, 256) * 256 : 256; }
 
-}  // namespace
-
 // Tile edge of a launch, from its number of 256-tiles: with few of them
 // 128-tiles, four times as many and two to a CU, cover the CUs better, and
 // 64-tiles where those are few in turn. Measured:
@@ -691,10 +736,25 @@ inline int xcd_grid(int64_t n) { return n > 0 ? cdiv(n, 256) * 256 : 256; }
 // 64-tiles (loss alone 64 / 128: 252 tiles 46.7 / 48.3, 628 67.0 / 64.4), and
 // its gradients always take those (634 tiles 440 / 465).
 constexpr int kFewTiles = 768, kFewSmallTiles = 384;
-static int tile_of(int dt, int64_t tiles256, int64_t tiles128) {
+int tile_of(int dt, int64_t tiles256, int64_t tiles128) {
   if (dt == MUON_BF16 && tiles256 >= kFewTiles) return 256;
   return tiles128 >= kFewSmallTiles ? 128 : 64;
 }
+// The gradients' tiles also go by their own shape (whole calls):
+//   few tokens: dW's K is short, its tiles all start-up and epilogue, which two
+//   workgroups to a CU overlap (128 / 256: 300 tokens x 50304 x 2048 338 / 384
+//   us, 700 tokens 587 / 556); from there on 128 also pays with fewer tiles
+//   (64 / 128, 1000 x 8000: width 256, 158 tiles, 55.0 / 52.0 us)
+//   narrow: a 256-tile would be mostly padding (4000 x 44000, 128 / 256: width
+//   64 430 / 457 us, 128 458 / 488, 192 528 / 506)
+constexpr int kShortK = 512, kNarrow = 128;
+int grad_tile_of(int dt, int rows, int dp, int64_t tiles256, int64_t tiles128) {
+  if (dt != MUON_BF16) return 64;
+  if (rows >= kShortK && dp > kNarrow && tiles256 >= kFewTiles) return 256;
+  return tiles128 >= (rows >= kShortK ? 128 : kFewSmallTiles) ? 128 : 64;
+}
+
+}  // namespace
 
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
   const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
@@ -720,11 +780,6 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
   return hipGetLastError();
 }
 
-// dW's K is the tokens: with few of them its tiles are all start-up and
-// epilogue, which two workgroups to a CU overlap (300 tokens x 50304 x 2048:
-// 338 us with 128-tiles, 384 with 256; 700 tokens 587 and 556).
-constexpr int kShortK = 512;
-
 // Tile edges of the products, columns per statistic, and splits of the
 // vocabulary in dH, whose tiles alone (tokens x width) are fewer than the CUs
 // for one piece of a narrow model. The gradients' launch lasts its stages over
@@ -744,7 +799,7 @@ void head_plan(HeadArgs& a, int dt) {
     return (a.dw ? (int64_t)cdiv(a.v, edge) * cdiv(a.dp, edge) : 0) +
            (a.dh ? (int64_t)cdiv(rows, edge) * cdiv(a.dp, edge) * (stages / 64 + 1) : 0);
   };
-  a.grad_tile = dt == MUON_BF16 ? tile_of(dt, rows < kShortK ? 0 : tiles_of(256), tiles_of(128)) : 64;
+  a.grad_tile = grad_tile_of(dt, rows, a.dp, tiles_of(256), tiles_of(128));
   if (!a.dh) return;
   const int tile = a.grad_tile, slots = 256 * (256 / tile);
   const int64_t tiles = (int64_t)cdiv(rows, tile) * cdiv(a.dp, tile);

@@ -18,8 +18,11 @@
 //              over the exponentials; a factor common to all tokens waits for
 //              the 32-bit sums
 //   dhidden    dz W, split over the vocabulary where tiles are few, then a
-//              sum of the splits written to the tokens' rows
-//   dweight    dz^T H, summed over pieces in 32 bits
+//              sum of the splits written to the tokens' rows, with what the
+//              target's own gradient lost in its rounding to 16 bits times the
+//              target's row: that one term is most of a token's gradient
+//   dweight    dz^T H, summed over pieces in 32 bits; with few tokens, whose
+//              roundings no sum averages, also those remainders
 //
 // The products are in head_gemm.hip. A 16-bit exponential carries an eighth of the rounding of the bf16 value it
 // becomes, so the gradient's one rounding is the one to bf16.
@@ -140,17 +143,41 @@ __global__ __launch_bounds__(1024) void k_compact(HeadArgs a) {
   if (threadIdx.x == 0) a.count[0] = base;
 }
 
+// Rows r0.. of a weight that the products cannot load as it is, to the padded
+// copy, in the same shape of block (blocks past the rows' in the same launch).
+template <typename T>
+__device__ __forceinline__ void pack_weight(const HeadArgs& a, int r0) {
+  constexpr int CH = 16 / (int)sizeof(T);
+  const int lane = threadIdx.x & 63, c = (blockIdx.y * 8 + (lane & 7)) * CH;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = r0 + i * 32 + (threadIdx.x >> 6) * 8 + (lane >> 3);
+    if (r >= a.v) continue;
+    const T* src = (const T*)a.w_src + r * a.ld_src;
+    T x[CH];
+#pragma unroll
+    for (int e = 0; e < CH; ++e) x[e] = c + e < a.d ? src[c + e] : T(0);
+    u32x4_t q;
+    __builtin_memcpy(&q, x, 16);
+    *(u32x4_t*)((T*)a.w + r * a.ld_w + c) = q;
+  }
+}
+
 // Gathered rows to panels: a wave takes 8 rows x 8 chunks at a time, so that
 // it reads and writes whole 128-byte lines; rows past the valid ones, up to a
 // whole panel (a stage of dW), become zero. One block per 64 rows and 8 chunks.
 template <typename T>
-__global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan) {
+__global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan, int row_blocks) {
   constexpr int CH = 16 / (int)sizeof(T);
   __shared__ int list[kPanelRows], counts[8 * 4];
-  const int r0 = blockIdx.y * kPanelRows;
+  if (blockIdx.x >= row_blocks) {
+    pack_weight<T>(a, ((int)blockIdx.x - row_blocks) * kPanelRows);
+    return;
+  }
+  const int r0 = blockIdx.x * kPanelRows;
   int rows;
   if (scan) {
-    const bool lists = blockIdx.x == 0 && blockIdx.y == 0;   // this block writes them
+    const bool lists = blockIdx.y == 0 && blockIdx.x == 0;   // this block writes them
     int64_t g[8];
     int at[8];
     rows = scan_targets<256>(a.targets, a.target_bytes, a.ignore, 0, a.n, g, at, counts);
@@ -174,9 +201,9 @@ __global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan) {
   }
   if (r0 >= rows) return;
   __syncthreads();
-  const int lane = threadIdx.x & 63, ch = blockIdx.x * 8 + (lane & 7), c = ch * CH;
+  const int lane = threadIdx.x & 63, ch = blockIdx.y * 8 + (lane & 7), c = ch * CH;
   const bool whole = a.ld_h * sizeof(T) % 16 == 0 && (uintptr_t)a.h % 16 == 0 && c + CH <= a.d;
-  uint8_t* dst = (uint8_t*)a.hp + (((int64_t)blockIdx.y * (a.dp / CH) + ch) << 10);
+  uint8_t* dst = (uint8_t*)a.hp + (((int64_t)blockIdx.x * (a.dp / CH) + ch) << 10);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int rr = i * 32 + (threadIdx.x >> 6) * 8 + (lane >> 3);
@@ -194,13 +221,6 @@ __global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan) {
     }
     *(u32x4_t*)(dst + rr * 16) = q;
   }
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void k_pack_weight(const T* __restrict__ src, int64_t ld, T* __restrict__ dst, int d,
-                                                     int dp) {
-  const int64_t r = blockIdx.x;
-  for (int c = threadIdx.x; c < dp; c += 256) dst[r * dp + c] = c < d ? src[r * ld + c] : T(0);
 }
 
 // 64 tokens per block, 16 threads per token: each goes over every sixteenth
@@ -249,6 +269,7 @@ __device__ __forceinline__ float4 merge_token(const HeadArgs& a, int grad, int r
       const float q = z / a.softcap;
       rs.z *= 1.f - q * q;
     }
+    if (a.half) rs.w = rs.z - bf2f(f2bf(rs.z));
   }
   return rs;
 }
@@ -312,7 +333,7 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int blo
   constexpr int CH = 16 / (int)sizeof(T);
   __shared__ float tops[4][64], sums[4][64];
   __shared__ float4 merged_rs[64];
-  const int rows = piece_rows(a), r0 = blockIdx.y * kPanelRows;
+  const int rows = piece_rows(a), r0 = blockIdx.x * kPanelRows;
   if (r0 >= rows) return;
   const int lane = threadIdx.x & 63, r = r0 + lane;
   const int tg = r < rows ? a.tgt[a.row0 + r] : -1;
@@ -332,16 +353,19 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int blo
       float loss;
       rs = merge_token(a, 1, r, top, others, loss);
       merged_rs[lane] = rs;
-      if (blockIdx.x == 0) store_loss(a, r, loss);
+      if (blockIdx.y == 0) {
+        store_loss(a, r, loss);
+        a.rs[r] = rs;
+      }
     }
     __syncthreads();
     if (real) rs = merged_rs[lane];
   }
-  const int last = a.vp / CH, c1 = min((int)(blockIdx.x + 1) * block_chunks, last);
-  uint8_t* base = (uint8_t*)a.e + ((int64_t)blockIdx.y * last << 10) + (threadIdx.x & 63) * 16;
+  const int last = a.vp / CH, c1 = min((int)(blockIdx.y + 1) * block_chunks, last);
+  uint8_t* base = (uint8_t*)a.e + ((int64_t)blockIdx.x * last << 10) + (threadIdx.x & 63) * 16;
   const float back = a.softcap > 0.f ? kLn2 / a.softcap : 0.f;
 #pragma unroll 4
-  for (int c = blockIdx.x * block_chunks + (threadIdx.x >> 6); c < c1; c += 4) {
+  for (int c = blockIdx.y * block_chunks + (threadIdx.x >> 6); c < c1; c += 4) {
     uint8_t* p = base + ((int64_t)c << 10);
     const int v = c * CH;
     float x[CH];
@@ -407,12 +431,32 @@ __global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a) {
   const int rows = piece_rows(a), r = blockIdx.x;
   if (r >= rows) return;
   const int64_t token = a.idx[a.row0 + r];
-  const float g = common_factor(a);
+  const float g = common_factor(a), rest = a.rs[r].w;
+  const T* target_row = (const T*)a.w + (int64_t)max(a.tgt[a.row0 + r], 0) * a.ld_w;   // (rest is 0 without a target)
   const bool whole = a.ld_dh % 4 == 0 && (uintptr_t)a.dh % (4 * sizeof(T)) == 0;
-  for (int c = threadIdx.x * 4; c < a.d; c += 1024) {
+  // a narrow row leaves threads to share the splits; the parts are added in order
+  const int groups = (a.d + 3) / 4, width = groups > 128 ? 256 : groups > 64 ? 128 : groups > 32 ? 64 : 32;
+  const int parts = 256 / width, part = threadIdx.x / width;
+  __shared__ f32x4_t sh[256];
+  for (int c0 = 0; c0 < a.d; c0 += 4 * width) {
+    const int c = c0 + ((int)threadIdx.x % width) * 4;
     f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+    if (c < a.d) {
 #pragma unroll 8
-    for (int q = 0; q < a.split; ++q) x += *(const f32x4_t*)(a.part + ((int64_t)q * a.piece + r) * a.dp + c);
+      for (int q = part; q < a.split; q += parts) x += *(const f32x4_t*)(a.part + ((int64_t)q * a.piece + r) * a.dp + c);
+    }
+    if (parts > 1) {
+      sh[threadIdx.x] = x;
+      __syncthreads();
+      if (part == 0)
+        for (int p = 1; p < parts; ++p) x += sh[p * width + threadIdx.x];
+      __syncthreads();
+    }
+    if (part != 0 || c >= a.d) continue;
+    if (rest != 0.f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.d) x[e] = fmaf(rest, ld<T>(target_row, c + e), x[e]);
     T* dst = dh + token * a.ld_dh + c;
     if (whole && c + 4 <= a.d) {
       if constexpr (sizeof(T) == 2)
@@ -447,16 +491,9 @@ hipError_t launch_head_compact(const HeadArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s) {
-  const int scan = pack_scans(a);
-  BY_TYPE(dt, k_pack, dim3(a.dp / (dt == MUON_BF16 ? 64 : 32), panels(a)), dim3(256), 0, s, a, scan);
-}
-hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v, int d, int dp, int dt,
-                                   hipStream_t s) {
-  if (dt == MUON_BF16)
-    hipLaunchKernelGGL((k_pack_weight<u16>), dim3(v), dim3(256), 0, s, (const u16*)src, ld, (u16*)dst, d, dp);
-  else
-    hipLaunchKernelGGL((k_pack_weight<float>), dim3(v), dim3(256), 0, s, (const float*)src, ld, (float*)dst, d, dp);
-  return hipGetLastError();
+  const int scan = pack_scans(a), rows = (int)panels(a);
+  const int weight = a.w_src && a.row0 == 0 ? (int)cdiv(a.v, kPanelRows) : 0;
+  BY_TYPE(dt, k_pack, dim3(rows + weight, a.dp / (dt == MUON_BF16 ? 64 : 32)), dim3(256), 0, s, a, scan, rows);
 }
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s) {
   if (grad && a.n_vt <= kFuseTiles) return hipSuccess;   // with the logits' gradient
@@ -469,7 +506,7 @@ hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s) {
   const int chunks = a.vp / (dt == MUON_BF16 ? 8 : 4);
   // chunks per block: 64, or 16 where that leaves CUs without four blocks
   const int per = (int64_t)cdiv(chunks, 64) * panels(a) < 1024 ? 16 : 64;
-  BY_TYPE(dt, k_dlogits, dim3(cdiv(chunks, per), panels(a)), dim3(256), 0, s, a, (int)(a.n_vt > kFuseTiles), per);
+  BY_TYPE(dt, k_dlogits, dim3(panels(a), cdiv(chunks, per)), dim3(256), 0, s, a, (int)(a.n_vt > kFuseTiles), per);
 }
 hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, hipStream_t s) {
   const int blocks = a.rows_max * (a.split > 1) + (a.row0 == 0 ? a.n : 0);

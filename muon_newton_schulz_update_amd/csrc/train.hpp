@@ -112,6 +112,7 @@ __host__ __device__ inline int64_t panel_at(int64_t row, int64_t col, int64_t ld
 struct HeadArgs {
   const void* h;   int64_t ld_h;
   const void* w;   int64_t ld_w;      // the caller's weight, or its padded copy
+  const void* w_src; int64_t ld_src;  // the weight to copy, or null
   void* dh;        int64_t ld_dh;
   void* dw;        int64_t ld_dw;
   int32_t n, v, d;                    // tokens, vocabulary, width
@@ -124,6 +125,7 @@ struct HeadArgs {
   int32_t target_bytes;
   int32_t per_token;                  // reduction none
   int32_t mean;
+  int32_t half;                       // 16-bit inputs
   float softcap;
   // workspace
   int32_t* count;                     // [0] valid tokens
@@ -135,7 +137,7 @@ struct HeadArgs {
   float* tmax;                        // n_vt x piece: integer power-of-two reference of each tile's row
   float* tsum;                        // n_vt x piece: sum of the tile's exponentials without the target's
   float* zt;                          // piece: the target's logit
-  float4* rs;                         // piece: {reference, factor, target's gradient, 0}
+  float4* rs;                         // piece: {reference, factor, target's gradient, what its rounding lost}
   float* part;                        // dH partial sums: split x piece x dp
   int32_t split;                      // parts of the vocabulary in dH
   int32_t logit_tile, grad_tile;      // tile edges of the products
@@ -150,8 +152,6 @@ struct HeadArgs {
 void head_plan(HeadArgs& a, int dt);
 hipError_t launch_head_compact(const HeadArgs& a, hipStream_t s);
 hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s);
-hipError_t launch_head_pack_weight(const void* src, int64_t ld, void* dst, int v, int d, int dp, int dt,
-                                   hipStream_t s);
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s);
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s);
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s);

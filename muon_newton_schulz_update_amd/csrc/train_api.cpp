@@ -138,6 +138,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.vp = (int)(cdiv(a.v, 256) * 256);
   a.per_token = cfg.reduction == MUON_REDUCE_NONE;
   a.mean = cfg.reduction == MUON_REDUCE_MEAN;
+  a.half = dt == MUON_BF16;
   a.softcap = cfg.softcap;
   a.targets = targets;
   a.target_bytes = target_bytes;
@@ -195,7 +196,8 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.ld_w = wgt.ld;
   HIP_DO(h, launch_head_compact(a, s));
   if (!direct) {
-    HIP_DO(h, launch_head_pack_weight(wgt.ptr, wgt.ld, b + o_w, a.v, a.d, a.dp, dt, s));
+    a.w_src = wgt.ptr;
+    a.ld_src = wgt.ld;
     a.w = b + o_w;
     a.ld_w = a.dp;
   }
