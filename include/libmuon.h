@@ -422,7 +422,9 @@ muon_status muon_update_static(muon_handle* handle, int n, const muon_matrix* gr
  * unless said below (MUON_ERR_INVALID_ARG). norm, coef, loss, grad_out and
  * grad_scale are device pointers to fp32 values. Lists travel in the kernel
  * arguments, so these calls upload nothing; they can be captured in a graph
- * once a first call of the same sizes has grown the handle's buffers.
+ * once a first call of the same sizes has grown the handle's buffers. A buffer
+ * that a later call outgrows is kept until muon_destroy, so a captured graph
+ * stays valid; like any call it must not run beside others of its handle.
  */
 
 /*
@@ -488,7 +490,7 @@ muon_status adamw_update(muon_handle* handle, int n, const muon_matrix* grad, co
  *            them may be NULL (its product is left out)
  * BF16 inputs are multiplied on the bf16 matrix cores (the logits' gradient
  * is rounded to bf16 once), F32 ones in fp32 throughout; statistics and sums
- * are fp32. The handle keeps up to about 1 GiB for the pieces of tokens (256
+ * are fp32. The handle keeps up to about 1.3 GiB for the pieces of tokens (256
  * at least), plus, when a call takes more than one piece, an fp32 V x D sum,
  * and a padded copy of a weight whose width or alignment is not a multiple of
  * 128 bytes or 16.

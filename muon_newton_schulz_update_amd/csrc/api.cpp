@@ -1450,8 +1450,8 @@ extern "C" muon_status muon_destroy(muon_handle* h) {
   for (auto& kv : h->plans)
     if (kv.second->meta_dev) (void)hipFree(kv.second->meta_dev);
   if (h->ws) (void)hipFree(h->ws);
-  if (h->train.head.ptr) (void)hipFree(h->train.head.ptr);
-  if (h->train.norm.ptr) (void)hipFree(h->train.norm.ptr);
+  h->train.head.release();
+  h->train.norm.release();
   if (h->pinned) (void)hipHostFree(h->pinned);
   if (h->upload_done) (void)hipEventDestroy(h->upload_done);
   if (h->static_done) (void)hipEventDestroy(h->static_done);
@@ -1476,18 +1476,20 @@ hipStream_t handle_stream(const muon_handle* h) { return h->stream; }
 int handle_device(const muon_handle* h) { return h->device; }
 muon_status handle_error(muon_handle* h, muon_status code, const std::string& msg) { return set_err(h, code, msg); }
 void handle_clear_error(muon_handle* h) { h->err.clear(); }
-// Work already enqueued may still read the old buffer: the stream drains first.
 muon_status grow(muon_handle* h, GrowBuffer& b, size_t bytes, const char* what) {
   if (bytes <= b.bytes && b.ptr) return MUON_OK;
-  HIP_TRY(h, hipStreamSynchronize(h->stream));
-  if (b.ptr) HIP_TRY(h, hipFree(b.ptr));
-  b.ptr = nullptr;
-  b.bytes = 0;
-  if (hipMalloc(&b.ptr, bytes) != hipSuccess) {
-    b.ptr = nullptr;
+  const size_t more = b.ptr ? std::max(bytes, b.bytes + b.bytes / 2) : bytes;
+  b.outgrown.reserve(b.outgrown.size() + 1);
+  void* p = nullptr;
+  if (hipMalloc(&p, more) == hipSuccess) {
+    bytes = more;
+  } else if ((void)hipGetLastError(), more == bytes || hipMalloc(&p, bytes) != hipSuccess) {
     (void)hipGetLastError();
-    return set_err(h, MUON_ERR_ALLOC, std::string(what) + " workspace of " + std::to_string(bytes) + " bytes: allocation failed");
+    return set_err(h, MUON_ERR_ALLOC,
+                   std::string(what) + " workspace of " + std::to_string(bytes) + " bytes: allocation failed");
   }
+  if (b.ptr) b.outgrown.push_back(b.ptr);
+  b.ptr = p;
   b.bytes = bytes;
   return MUON_OK;
 }

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <string>
+#include <vector>
 
 #include "../../include/libmuon.h"
 
@@ -11,10 +12,20 @@ namespace muon {
 
 // A device buffer that grows on demand and is freed with the handle. Each
 // user has its own: the Newton-Schulz workspace keeps zero padding that no
-// other kernel may write.
+// other kernel may write. What it outgrows is kept until then too: a captured
+// graph may still replay on it. It grows at least by half, so all that is kept
+// is at most twice its size.
 struct GrowBuffer {
   void* ptr = nullptr;
   size_t bytes = 0;
+  std::vector<void*> outgrown;
+  void release() {
+    if (ptr) (void)hipFree(ptr);
+    for (void* p : outgrown) (void)hipFree(p);
+    outgrown.clear();
+    ptr = nullptr;
+    bytes = 0;
+  }
 };
 struct TrainState {
   GrowBuffer head;            // cross entropy pieces

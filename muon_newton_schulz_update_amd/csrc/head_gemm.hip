@@ -806,7 +806,8 @@ void head_plan(HeadArgs& a, int dt) {
   const double other = a.dw ? (double)cdiv(a.v, tile) * cdiv(a.dp, tile) * (cdiv(rows, unit) + 6) : 0.0;
   const double sum = (double)rows * a.dp * 8 / (tile == 256 ? 9e6 : 4.5e6);
   double least = 0;
-  for (int n = 1; n <= 256 && (n == 1 || stages / n >= 4); ++n) {
+  // (the partial sums stay within 256 MB)
+  for (int n = 1; n <= 256 && (n == 1 || (stages / n >= 4 && (double)n * a.piece * a.dp * 4 <= 256e6)); ++n) {
     const double each = (double)cdiv(stages, n) + 6, t0 = (tiles * n * each + other) / slots + each / 2;
     // more than one split: the sum is a launch of its own, about 5 us
     const double t = (t0 > each ? t0 : each) + (n > 1 ? n * sum + (tile == 256 ? 3 : 5) : 0);

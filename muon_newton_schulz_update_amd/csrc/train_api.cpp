@@ -121,6 +121,7 @@ muon_status scale_run(muon_handle* h, int n, const muon_matrix* src, const muon_
 // kPieceRows tokens, whatever the vocabulary).
 constexpr size_t kHeadBytes = size_t(1) << 30;
 constexpr int kPieceRows = 256;
+constexpr int64_t kPieceMost = 65536;   // keeps a launch's tiles far from 2^31
 
 muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& wgt, const void* targets,
                      int target_bytes, const muon_loss_config& cfg, const float* grad_out, float* loss,
@@ -160,7 +161,8 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const bool direct = a.d % unit == 0 && (uintptr_t)wgt.ptr % 16 == 0 && (wgt.rows == 1 || (wgt.ld * e % 16 == 0 && wgt.ld * e < (1 << 23)));
   // pieces
   const size_t row = (size_t)a.dp * e + (size_t)cdiv(a.v, 64) * 8 + 24 + (grad ? (size_t)a.vp * e : 0);
-  const int64_t most = std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows);
+  const int64_t most =
+      std::min(kPieceMost, std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows));
   const int64_t pieces = std::max<int64_t>(1, cdiv(a.n, most));
   a.piece = (int)(std::max<int64_t>(1, cdiv(cdiv(a.n, pieces), kPieceRows)) * kPieceRows);
   head_plan(a, dt);
@@ -175,7 +177,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const size_t o_hp = take(p * a.dp * e), o_tmax = take(p * a.n_vt * 4), o_tsum = take(p * a.n_vt * 4);
   const size_t o_zt = take(p * 4), o_rs = take(p * 16);
   const size_t o_w = direct ? 0 : take((size_t)a.v * a.dp * e);
-  const size_t o_e = grad ? take(p * a.vp * e) : 0, o_part = dh ? take(p * a.dp * 4 * a.split) : 0;
+  const size_t o_e = grad ? take(p * a.vp * e) : 0, o_part = a.split > 1 ? take(p * a.dp * 4 * a.split) : 0;
   const bool acc = dw && pieces > 1;
   const size_t o_acc = acc ? take((size_t)a.v * a.dp * 4) : 0;
   if (muon_status st = grow(h, ts.head, at, "cross entropy")) return st;

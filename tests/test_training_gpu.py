@@ -540,3 +540,16 @@ def test_refusals():
             pytest.fail(f"call {i} was accepted")
     torch.cuda.synchronize()
     assert torch.equal(h, keep[0]) and torch.equal(w, keep[1])
+
+
+def test_example_trains():
+    """examples/train_small_lm.py: every operator in one program; the loss falls from log(vocabulary)."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_small_lm.py")
+    spec = importlib.util.spec_from_file_location("train_small_lm", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    losses = module.train(40, say=None)
+    assert abs(losses[0] - math.log(module.VOCAB)) < 1.0 and losses[-1] < losses[0] - 3.0, (losses[0], losses[-1])
