@@ -5,6 +5,7 @@
 // dozen tensors of an optimizer's list is several times the GPU's work.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <ATen/Functions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -129,7 +130,28 @@ PyObject* device_of(PyObject*, PyObject* arg) {
   return PyLong_FromLong(device);
 }
 
+// empty(device, shape_of=None, type_of=None) -> a contiguous tensor on the GPU:
+// the shape of one tensor (None: a scalar), the type of another (None: float32)
+PyObject* empty(PyObject*, PyObject* args) {
+  PyObject *shape_of = Py_None, *type_of = Py_None;
+  long device;
+  if (!PyArg_ParseTuple(args, "l|OO", &device, &shape_of, &type_of)) return nullptr;
+  const at::Tensor *shape = nullptr, *type = nullptr;
+  if (shape_of != Py_None && !(shape = tensor_of(shape_of, "shape_of"))) return nullptr;
+  if (type_of != Py_None && !(type = tensor_of(type_of, "type_of"))) return nullptr;
+  try {
+    const auto options = at::TensorOptions()
+                             .dtype(type ? type->scalar_type() : at::kFloat)
+                             .device(at::kCUDA, (c10::DeviceIndex)device);
+    return THPVariable_Wrap(at::empty(shape ? shape->sizes() : at::IntArrayRef(), options));
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
 PyMethodDef methods[] = {
+    {"empty", empty, METH_VARARGS, "A tensor on the GPU with the shape and type of others."},
     {"pack", pack, METH_VARARGS, "Descriptors of a list of tensors, as bytes."},
     {"device_of", device_of, METH_O, "Index of the first tensor on a GPU, or -1."},
     {nullptr, nullptr, 0, nullptr},

@@ -61,10 +61,6 @@ def _handle_for(tensors, handle):
     return handle
 
 
-def _pair(device: int) -> torch.Tensor:
-    return torch.empty(2, device=torch.device("cuda", device), dtype=torch.float32)
-
-
 def _scalar(t: torch.Tensor | None, what: str, device: int, n: int | None = None):
     if t is None:
         return None
@@ -85,12 +81,15 @@ def grad_norm(grads: Sequence[torch.Tensor], *, max_norm: float | None = None, h
     grad_scale. Nothing waits for the GPU."""
     grads = list(grads)
     h = _handle_for(grads, handle)
-    out = _pair(h.device)
-    at = out.data_ptr()
-    h._check(h._lib.muon_grad_norm(h.ptr, len(grads), _describe().pack(grads, "grads", h.device),
-                                   0.0 if max_norm is None else float(max_norm), at,
-                                   None if max_norm is None else at + 4))
-    return out[0] if max_norm is None else (out[0], out[1])
+    native = _describe()
+    words = native.pack(grads, "grads", h.device)
+    norm = native.empty(h.device)
+    if max_norm is None:
+        h._check(h._lib.muon_grad_norm(h.ptr, len(grads), words, 0.0, norm.data_ptr(), None))
+        return norm
+    coef = native.empty(h.device)
+    h._check(h._lib.muon_grad_norm(h.ptr, len(grads), words, max_norm, norm.data_ptr(), coef.data_ptr()))
+    return norm, coef
 
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Sequence[torch.Tensor] | None = None,
@@ -100,13 +99,12 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Seque
     clipping. In place, nothing is written when the norm is within the limit."""
     grads = list(grads)
     h = _handle_for(grads, handle)
-    pack = _describe().pack
-    words = pack(grads, "grads", h.device)
-    outs = None if out is None else pack(out, "out", h.device, grads, "grads")
-    both = _pair(h.device)
-    at = both.data_ptr()
-    h._check(h._lib.muon_clip_grad_norm(h.ptr, len(grads), words, outs, float(max_norm), at, at + 4))
-    return both[0]
+    native = _describe()
+    words = native.pack(grads, "grads", h.device)
+    outs = None if out is None else native.pack(out, "out", h.device, grads, "grads")
+    norm, coef = native.empty(h.device), native.empty(h.device)
+    h._check(h._lib.muon_clip_grad_norm(h.ptr, len(grads), words, outs, max_norm, norm.data_ptr(), coef.data_ptr()))
+    return norm
 
 
 def scale(tensors: Sequence[torch.Tensor], coef: torch.Tensor, *, out: Sequence[torch.Tensor] | None = None,
@@ -124,6 +122,18 @@ def scale(tensors: Sequence[torch.Tensor], coef: torch.Tensor, *, out: Sequence[
 # ---------------------------------------------------------------------------
 # AdamW
 # ---------------------------------------------------------------------------
+_adamw_default = None
+
+
+def _adamw_defaults() -> AdamWConfig:
+    global _adamw_default
+    if _adamw_default is None:
+        cfg = AdamWConfig()
+        load_library().muon_adamw_config_default(ctypes.byref(cfg))
+        _adamw_default = cfg
+    return _adamw_default
+
+
 def adamw_update(grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
                  exp_avg_sqs: Sequence[torch.Tensor], weights: Sequence[torch.Tensor], *, step: int,
                  lr: float | None = None, beta1: float | None = None, beta2: float | None = None,
@@ -141,12 +151,10 @@ def adamw_update(grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor]
     lists = [pack(x, what, d, weights, "weights") for x, what in
              ((grads, "grads"), (exp_avgs, "exp_avgs"), (exp_avg_sqs, "exp_avg_sqs"))]
     cp = None if copies is None else pack(copies, "copies", d, weights, "weights")
-    cfg = AdamWConfig()
-    h._lib.muon_adamw_config_default(ctypes.byref(cfg))
-    cfg.step = step
-    for name, value in (("lr", lr), ("beta1", beta1), ("beta2", beta2), ("eps", eps), ("weight_decay", weight_decay)):
-        if value is not None:
-            setattr(cfg, name, value)
+    z = _adamw_defaults()
+    cfg = AdamWConfig(z.lr if lr is None else lr, z.beta1 if beta1 is None else beta1,
+                      z.beta2 if beta2 is None else beta2, z.eps if eps is None else eps,
+                      z.weight_decay if weight_decay is None else weight_decay, step)
     h._check(h._lib.adamw_update(h.ptr, len(weights), *lists, w, cp, ctypes.byref(cfg),
                                  _scalar(grad_scale, "grad_scale", d)))
 
@@ -175,7 +183,8 @@ def _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_o
         raise ValueError(f"targets: expected a tensor on GPU {d}, got {targets.device}")
     hid = hidden if hidden.dim() == 2 else hidden.view(-1, hidden.shape[-1])
     n = hid.shape[0]
-    loss = torch.empty(targets.shape if reduction == "none" else (), device=weight.device, dtype=torch.float32)
+    native = _describe()
+    loss = native.empty(d, targets if reduction == "none" else None)
     cfg = LossConfig(REDUCTIONS[reduction], float(softcap), int(ignore_index))
     args = (h.ptr, _matrix(hid, "hidden", d), _matrix(weight, "weight", d), targets.data_ptr(),
             targets.element_size(), ctypes.byref(cfg))
@@ -186,13 +195,13 @@ def _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_o
     dh = dw = None
     if dhidden is not False:
         if dhidden is None:
-            dhidden = torch.empty_like(hidden, memory_format=torch.contiguous_format)
+            dhidden = native.empty(d, hidden, hidden)
         elif dhidden.shape != hidden.shape:
             raise ValueError(f"dhidden of shape {tuple(dhidden.shape)} for hidden states of {tuple(hidden.shape)}")
         dh = _matrix(dhidden if dhidden.dim() == 2 else dhidden.view(-1, dhidden.shape[-1]), "dhidden", d)
     if dweight is not False:
         if dweight is None:
-            dweight = torch.empty_like(weight, memory_format=torch.contiguous_format)
+            dweight = native.empty(d, weight, weight)
         dw = _matrix(dweight, "dweight", d)
     h._check(h._lib.linear_cross_entropy_grad(*args, go, loss.data_ptr(), dh, dw))
     return loss, dhidden if dh is not None else None, dweight if dw is not None else None
