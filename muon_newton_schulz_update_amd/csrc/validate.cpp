@@ -246,7 +246,7 @@ int check_tensor(const muon_matrix& m, const char* what, int i, char* msg, int l
                 (long long)m.rows, (long long)m.cols);
   if (m.rows == 0 || m.cols == 0) return MUON_OK;
   if (!m.ptr) return fail(msg, len, MUON_ERR_INVALID_ARG, "%s[%d]: NULL pointer for a non-empty tensor", what, i);
-  if (m.rows > kMaxListElems || m.cols > kMaxListElems || m.rows > kMaxListElems / m.cols)
+  if ((u128)m.rows * (u128)m.cols > (u128)kMaxListElems)
     return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "%s[%d]: %lld x %lld exceeds 2^42 elements", what, i,
                 (long long)m.rows, (long long)m.cols);
   if (m.rows > 1 && m.ld < m.cols)
@@ -268,6 +268,27 @@ Span tensor_span(muon_matrix m, const char* what, int idx, bool writes) {
 bool same_buffer(const muon_matrix& a, const muon_matrix& b) {
   return a.ptr == b.ptr && a.dtype == b.dtype && a.rows == b.rows && a.cols == b.cols &&
          (a.rows <= 1 || a.ld == b.ld);
+}
+
+// check_overlaps behind a quick look: buffers whose extents are all apart, the
+// ordinary case, need neither the spans' sort nor the rules for interleaved
+// rows (most of a short list's validation time otherwise).
+int check_apart(std::vector<Span>& v, char* msg, int len) {
+  struct Extent {
+    uint64_t lo, hi;
+  };
+  std::vector<Extent> e;
+  e.reserve(v.size());
+  bool apart = true;
+  for (const Span& s : v) {
+    apart = apart && s.hi <= (u128)UINT64_MAX;
+    e.push_back(Extent{(uint64_t)s.lo, (uint64_t)s.hi});
+  }
+  if (apart) {
+    std::sort(e.begin(), e.end(), [](const Extent& a, const Extent& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < e.size(); ++i) apart = apart && e[i - 1].hi <= e[i].lo;
+  }
+  return apart ? (int)MUON_OK : check_overlaps(v, false, msg, len);
 }
 
 // Device scalars and vectors as one-row spans.
@@ -304,6 +325,7 @@ int check_norm(int n, const muon_matrix* g, const muon_matrix* out, float max_no
   // the kernels read a tensor again after they wrote others: an output shares
   // memory with nothing but the input it replaces, element for element
   std::vector<Span> v;
+  v.reserve((size_t)n * 2 + 2);
   for (int i = 0; i < n; ++i) {
     if (!nonempty(g[i])) continue;
     const bool own = !out || same_buffer(g[i], out[i]);
@@ -312,7 +334,7 @@ int check_norm(int n, const muon_matrix* g, const muon_matrix* out, float max_no
   }
   if (norm != coef) v.push_back(flat_span(norm, 4, "norm", true));
   if (coef) v.push_back(flat_span(coef, 4, "coefficient", norm != coef));
-  return check_overlaps(v, false, msg, len);
+  return check_apart(v, msg, len);
 }
 
 int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_matrix* v, const muon_matrix* w,
@@ -331,6 +353,7 @@ int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_ma
   if ((uintptr_t)scale % 4 != 0) return fail(msg, len, MUON_ERR_INVALID_ARG, "grad_scale not aligned to 4 bytes");
   int rc;
   std::vector<Span> spans;
+  spans.reserve((size_t)n * 5 + 1);
   for (int i = 0; i < n; ++i) {
     if ((rc = check_tensor(w[i], "weight", i, msg, len))) return rc;
     const muon_matrix* xs[] = {&g[i], &m[i], &v[i]};
@@ -354,7 +377,7 @@ int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_ma
     if (cp) spans.push_back(tensor_span(copy[i], "copy", i, true));
   }
   if (scale) spans.push_back(flat_span(scale, 4, "grad_scale", false));
-  return check_overlaps(spans, false, msg, len);
+  return check_apart(spans, msg, len);
 }
 
 int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
@@ -407,7 +430,7 @@ int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void*
     if (nonempty(*out[k])) v.push_back(tensor_span(*out[k], to[k], 0, true));
   }
   if (grad && grad_out && each > 0) v.push_back(flat_span(grad_out, each * 4, "grad_out", false));
-  return check_overlaps(v, false, msg, len);
+  return check_apart(v, msg, len);
 }
 
 }  // namespace muon
