@@ -492,8 +492,8 @@ muon_status adamw_update(muon_handle* handle, int n, const muon_matrix* grad, co
  * is rounded to bf16 once), F32 ones in fp32 throughout; statistics and sums
  * are fp32. The handle keeps up to about 1.3 GiB for the pieces of tokens (256
  * at least), plus, when a call takes more than one piece, an fp32 V x D sum,
- * and a padded copy of a weight whose width or alignment is not a multiple of
- * 128 bytes or 16.
+ * and a padded copy of a weight whose rows are not whole 16-byte pieces that
+ * start on 16 bytes.
  */
 typedef enum { MUON_REDUCE_NONE = 0, MUON_REDUCE_SUM = 1, MUON_REDUCE_MEAN = 2 } muon_reduction;
 typedef struct {

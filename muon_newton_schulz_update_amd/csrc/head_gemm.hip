@@ -28,7 +28,8 @@
 //               % 4) 4 (bf16) or chunk % 8 (fp32)
 // Every address is clamped into its matrix: rows and columns past the edge
 // repeat the last ones and their results are not stored (K itself is padded
-// with zeros on one side at least).
+// with zeros: in the panels, and past the end of the weight's rows by the
+// buffer's range check).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -99,6 +100,7 @@ struct Operand {
   const uint8_t* base;   // tile start at the first stage
   uint32_t pitch;        // bytes: row pitch (row layouts), token-block pitch (panels)
   int lim;               // last valid row (row layouts), last valid chunk (OP_PANEL_T)
+  int row_bytes;         // OP_ROW_K: bytes of a row; what a stage has past them is zero
   uint32_t lane;         // this lane's byte offset, the same in every stage
 };
 
@@ -136,7 +138,11 @@ struct Op {
     const int g = NW * i + wave;
     if constexpr (L == OP_ROW_K) {
       p += (int64_t)ks * 128;
+      // past the row's end the offset is out of the buffer's range, and such
+      // lanes load zeros
+      const bool past = (int)o.lane >= o.row_bytes - ks * 128;
       voff += __umul24(min(8 * g + (lane >> 3), o.lim), o.pitch);
+      voff = past ? 0x80000000u : voff;
     } else if constexpr (L == OP_ROW_T) {
       p += (int64_t)ks * KE * o.pitch;
       voff += __umul24(min(kRowsPerLoad * g + lane / (64 / kRowsPerLoad), o.lim - ks * KE), o.pitch);
@@ -154,7 +160,7 @@ struct Op {
         soff = min(2 * g, o.lim - 1) * 1024;
       }
     }
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, -1, 0x00020000);
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, L == OP_ROW_K ? 0x7FFFFFF0 : -1, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(sm + g * 1024), 16, voff, soff, 0, 0);
   }
   static constexpr int kReads = L == OP_ROW_K || L == OP_PANEL_K ? 1 : sizeof(T) == 2 ? 2 : 4;   // LDS reads a fragment
@@ -336,10 +342,12 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 // The statistics are per wave's vocabulary rows, so waves never wait for one another. The
 // exponentials go to the panels as whole chunks after a half-wave swap.
 // ---------------------------------------------------------------------------
-template <typename T, int TILE>
+template <typename T, int TILE, bool FEW>
 __global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
   // a wave: 128 vocabulary rows (64 of a 64-tile) x 64 tokens (256) or 32
-  constexpr int MI = TILE == 64 ? 2 : 4, NI = TILE == 256 ? 2 : 1, WM = TILE / (MI * 32), WN = TILE / (NI * 32);
+  // (FEW: at most 32 tokens; both waves of a 64-tile take those, 32 rows each)
+  constexpr int MI = FEW ? 1 : TILE == 64 ? 2 : 4, NI = TILE == 256 ? 2 : 1;
+  constexpr int WM = TILE / (MI * 32), WN = FEW ? 1 : TILE / (NI * 32);
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * TILE * 128];
   int vi, ti;
   const int rows = piece_rows(a), lane = threadIdx.x & 63;
@@ -349,9 +357,9 @@ __global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int kee
   typedef Op<T, OP_ROW_K, TILE> A;
   typedef Op<T, OP_PANEL_K, TILE> B;
   const Operand oa = {(const uint8_t*)a.w + (int64_t)v0 * a.ld_w * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)),
-                      a.v - 1 - v0, A::lane_part(lane, wave, 0)};
+                      a.v - 1 - v0, a.w_cols * (int)sizeof(T), A::lane_part(lane, wave, 0)};
   const uint32_t blk = (uint32_t)a.dp * sizeof(T) * kPanelRows;
-  const Operand ob = {(const uint8_t*)a.hp + (int64_t)ti * (TILE / 64) * blk, blk, 0, B::lane_part(lane, wave, 0)};
+  const Operand ob = {(const uint8_t*)a.hp + (int64_t)ti * (TILE / 64) * blk, blk, 0, 0, B::lane_part(lane, wave, 0)};
   f32x16_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
@@ -362,8 +370,8 @@ __global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int kee
 
   const int lr = lane & 31, hf = lane >> 5;
   const int vw = v0 + wm * MI * 32;                  // the wave's first vocabulary row
-  if (vw >= a.v) return;                             // (the exponentials' padding is cleared with the gradient)
-  const int tile = vi * WM + wm;
+  if (!FEW && vw >= a.v) return;                     // (the exponentials' padding is cleared with the gradient)
+  const int tile = FEW ? vi : vi * WM + wm;
   if (a.softcap > 0.f) {
     const float s = 2.f * kLog2e / a.softcap;
 #pragma unroll
@@ -411,6 +419,15 @@ __global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int kee
 #pragma unroll
       for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
     top = fmaxf(top, __shfl_xor(top, 32));
+    // the two waves' halves of a few tokens' tile have one reference and sum
+    float* half_stat = (float*)smem + (FEW ? 32 : 0);
+    if constexpr (FEW) {
+      ring_barrier();                                // both are done with the slots
+      if (hf == 0) half_stat[(wm - 1) * 32 + lr] = top;
+      wait_lgkm0();
+      ring_barrier();
+      top = fmaxf(half_stat[lr - 32], half_stat[lr]);
+    }
     top = ceilf(fmaxf(top * kLog2e, kRefFloor));
     float sum = 0.f;
 #pragma unroll
@@ -450,6 +467,13 @@ __global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int kee
       }
     }
     sum += __shfl_xor(sum, 32);
+    if constexpr (FEW) {
+      if (wm == 1 && hf == 0) half_stat[32 + lr] = sum;
+      wait_lgkm0();
+      ring_barrier();
+      if (wm == 1) return;
+      sum += half_stat[32 + lr];
+    }
     if (hf == 0) {
       a.tmax[(int64_t)tile * a.piece + r] = top;
       a.tsum[(int64_t)tile * a.piece + r] = sum;
@@ -469,9 +493,9 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
   typedef Op<T, OP_PANEL_K, TILE> A;
   typedef Op<T, OP_ROW_T, TILE> B;
   const uint32_t blk = (uint32_t)a.vp * sizeof(T) * kPanelRows;
-  const Operand oa = {(const uint8_t*)a.e + (int64_t)ti * (TILE / 64) * blk, blk, 0, A::lane_part(lane, wave, 0)};
-  const int chunks = (a.dp - d0) * (int)sizeof(T) / 16;
-  const Operand ob = {(const uint8_t*)a.w + (int64_t)d0 * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)), a.v - 1,
+  const Operand oa = {(const uint8_t*)a.e + (int64_t)ti * (TILE / 64) * blk, blk, 0, 0, A::lane_part(lane, wave, 0)};
+  const int chunks = (a.w_cols - d0) * (int)sizeof(T) / 16;
+  const Operand ob = {(const uint8_t*)a.w + (int64_t)d0 * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)), a.v - 1, 0,
                       B::lane_part(lane, wave, chunks - 1)};
   const int nk = (a.v + A::KE - 1) / A::KE;
   const int k0 = (int)((int64_t)nk * q / a.split), k1 = (int)((int64_t)nk * (q + 1) / a.split);
@@ -522,7 +546,6 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
   constexpr int NC = NI * 32 * (int)sizeof(T) / 16, CH = 16 / (int)sizeof(T);   // chunks of its row
   ring_barrier();                                           // every wave is done with the slots
   uint8_t* slab = smem + wave * (32 * NC * 16);
-  const bool whole = a.ld_dh % CH == 0 && (uintptr_t)a.dh % 16 == 0;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
 #pragma unroll
@@ -542,8 +565,8 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
       const int t = rw + mi * 32 + row, d = dw + c * CH;
       if (t >= rows || d >= a.d) continue;
       T* p = (T*)a.dh + (int64_t)a.idx[a.row0 + t] * a.ld_dh + d;
-      if (whole && d + CH <= a.d) {
-        *(u32x4_t*)p = x;
+      if (d + CH <= a.d) {
+        __builtin_memcpy(p, &x, 16);      // (one store, aligned or not)
       } else {
         T y[CH];
         __builtin_memcpy(y, &x, 16);
@@ -559,9 +582,9 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 // ---------------------------------------------------------------------------
 // dW: the piece's sum, added to the pieces before it; the last one is scaled
 // and rounded to the weight's type. The width is on the accumulators' rows, so
-// a lane has four neighbouring columns of one weight row; 16-bit results are
-// put together to whole rows of the wave's part in the idle LDS (chunks
-// swizzled by row) and leave as 16-byte stores.
+// a lane has four neighbouring columns of one weight row; the results are put
+// together to whole rows of the wave's part in the idle LDS (chunks swizzled by
+// row) and leave as 16-byte stores.
 // ---------------------------------------------------------------------------
 template <typename T, int TILE>
 __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, int vi, int di, int rows) {
@@ -573,9 +596,10 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
   typedef Op<T, OP_PANEL_T, TILE> O;
   constexpr int CH = 16 / (int)sizeof(T);
   const uint32_t be = (uint32_t)a.vp * sizeof(T) * kPanelRows, bh = (uint32_t)a.dp * sizeof(T) * kPanelRows;
-  const Operand oa = {(const uint8_t*)a.hp + (int64_t)(d0 / CH) * 1024, bh, (a.dp - d0) / CH - 1,
+  const Operand oa = {(const uint8_t*)a.hp + (int64_t)(d0 / CH) * 1024, bh, (a.dp - d0) / CH - 1, 0,
                       O::lane_part(lane, wave, 0)};
-  const Operand ob = {(const uint8_t*)a.e + (int64_t)(v0 / CH) * 1024, be, TILE / CH - 1, O::lane_part(lane, wave, 0)};
+  const Operand ob = {(const uint8_t*)a.e + (int64_t)(v0 / CH) * 1024, be, TILE / CH - 1, 0,
+                      O::lane_part(lane, wave, 0)};
   f32x16_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
@@ -636,59 +660,40 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
     }
     if (!a.last) return;
   }
-  T* out = (T*)a.dw;
-  const bool whole = a.ld_dw % CH == 0 && (uintptr_t)a.dw % 16 == 0;
-  if constexpr (sizeof(T) == 2) {
-    constexpr int NC = MI * 4;                              // chunks of the wave's row
-    if (nk > 0) ring_barrier();                             // every wave is done with the slots
-    uint8_t* slab = smem + wave * (64 * NC * 16);
+  constexpr int NC = MI * 2 * (int)sizeof(T);               // chunks of the wave's row
+  if (nk > 0) ring_barrier();                               // every wave is done with the slots
+  uint8_t* slab = smem + wave * (64 * NC * 16);
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
+  for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
+    for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const u32x2_t x = {pack_bf16(acc[mi][ni][4 * q] * g, acc[mi][ni][4 * q + 1] * g),
-                             pack_bf16(acc[mi][ni][4 * q + 2] * g, acc[mi][ni][4 * q + 3] * g)};
-          const int row = ni * 32 + lr;
-          *(u32x2_t*)(slab + row * NC * 16 + (((mi * 4 + q) ^ (row & (NC - 1))) * 16) + hf * 8) = x;
-        }
-    wave_lds_sync();
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int row = i * (64 / NC) + lane / NC, c = lane % NC;
-      const u32x4_t x = *(const u32x4_t*)(slab + row * NC * 16 + ((c ^ (row & (NC - 1))) * 16));
-      const int v = vw + row, d = dw + c * 8;
-      if (v >= a.v || d >= a.d) continue;
-      u16* p = (u16*)out + (int64_t)v * a.ld_dw + d;
-      if (whole && d + 8 <= a.d) {
-        *(u32x4_t*)p = x;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (d + e < a.d) p[e] = (u16)(x[e >> 1] >> (16 * (e & 1)));
+      for (int q = 0; q < 4; ++q) {
+        const int row = ni * 32 + lr;
+        const f32x4_t x = {acc[mi][ni][4 * q] * g, acc[mi][ni][4 * q + 1] * g, acc[mi][ni][4 * q + 2] * g,
+                           acc[mi][ni][4 * q + 3] * g};
+        if constexpr (sizeof(T) == 2)
+          *(u32x2_t*)(slab + row * NC * 16 + (((mi * 4 + q) ^ (row & (NC - 1))) * 16) + hf * 8) =
+              (u32x2_t){pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+        else
+          *(f32x4_t*)(slab + row * NC * 16 + (((mi * 8 + 2 * q + hf) ^ (row & (NC - 1))) * 16)) = x;
       }
-    }
-  } else {
+  wave_lds_sync();
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      const int v = vw + ni * 32 + lr;
-      if (v >= a.v) continue;
+  for (int i = 0; i < NC; ++i) {
+    const int row = i * (64 / NC) + lane / NC, c = lane % NC;
+    const u32x4_t x = *(const u32x4_t*)(slab + row * NC * 16 + ((c ^ (row & (NC - 1))) * 16));
+    const int v = vw + row, d = dw + c * CH;
+    if (v >= a.v || d >= a.d) continue;
+    T* p = (T*)a.dw + (int64_t)v * a.ld_dw + d;
+    if (d + CH <= a.d) {
+      __builtin_memcpy(p, &x, 16);        // (one store, aligned or not)
+    } else {
+      T y[CH];
+      __builtin_memcpy(y, &x, 16);
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int d = dw + mi * 32 + 8 * q + 4 * hf;
-          float* p = (float*)out + (int64_t)v * a.ld_dw + d;
-          if (whole && d + 4 <= a.d) {
-            *(f32x4_t*)p = (f32x4_t){acc[mi][ni][4 * q] * g, acc[mi][ni][4 * q + 1] * g, acc[mi][ni][4 * q + 2] * g,
-                                     acc[mi][ni][4 * q + 3] * g};
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (d + e < a.d) p[e] = acc[mi][ni][4 * q + e] * g;
-          }
-        }
+      for (int e = 0; e < CH; ++e)
+        if (d + e < a.d) p[e] = y[e];
     }
   }
 }
@@ -759,11 +764,12 @@ int grad_tile_of(int dt, int rows, int dp, int64_t tiles256, int64_t tiles128) {
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
   const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
   const dim3 g(xcd_grid((int64_t)vt * tt)), b(tile * 2);
-  if (dt == MUON_BF16 && tile == 256) hipLaunchKernelGGL((k_logits_mfma<u16, 256>), g, b, 0, s, a, keep, vt, tt);
-  else if (dt == MUON_BF16 && tile == 128) hipLaunchKernelGGL((k_logits_mfma<u16, 128>), g, b, 0, s, a, keep, vt, tt);
-  else if (dt == MUON_BF16) hipLaunchKernelGGL((k_logits_mfma<u16, 64>), g, b, 0, s, a, keep, vt, tt);
-  else if (tile == 128) hipLaunchKernelGGL((k_logits_mfma<float, 128>), g, b, 0, s, a, keep, vt, tt);
-  else hipLaunchKernelGGL((k_logits_mfma<float, 64>), g, b, 0, s, a, keep, vt, tt);
+  if (dt == MUON_BF16 && tile == 256) hipLaunchKernelGGL((k_logits_mfma<u16, 256, false>), g, b, 0, s, a, keep, vt, tt);
+  else if (dt == MUON_BF16 && tile == 128) hipLaunchKernelGGL((k_logits_mfma<u16, 128, false>), g, b, 0, s, a, keep, vt, tt);
+  else if (dt == MUON_BF16) hipLaunchKernelGGL((k_logits_mfma<u16, 64, false>), g, b, 0, s, a, keep, vt, tt);
+  else if (tile == 128) hipLaunchKernelGGL((k_logits_mfma<float, 128, false>), g, b, 0, s, a, keep, vt, tt);
+  else if (a.n > 32) hipLaunchKernelGGL((k_logits_mfma<float, 64, false>), g, b, 0, s, a, keep, vt, tt);
+  else hipLaunchKernelGGL((k_logits_mfma<float, 64, true>), g, b, 0, s, a, keep, vt, tt);
   return hipGetLastError();
 }
 

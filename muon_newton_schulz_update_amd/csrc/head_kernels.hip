@@ -143,6 +143,23 @@ __global__ __launch_bounds__(1024) void k_compact(HeadArgs a) {
   if (threadIdx.x == 0) a.count[0] = base;
 }
 
+// 16 bytes of a row from column c, zero past its d columns (one load where
+// whole, aligned or not).
+template <typename T>
+__device__ __forceinline__ u32x4_t load_chunk(const T* row, int c, int d) {
+  constexpr int CH = 16 / (int)sizeof(T);
+  u32x4_t q;
+  if (c + CH <= d) {
+    __builtin_memcpy(&q, row + c, 16);
+  } else {
+    T x[CH];
+#pragma unroll
+    for (int e = 0; e < CH; ++e) x[e] = c + e < d ? row[c + e] : T(0);
+    __builtin_memcpy(&q, x, 16);
+  }
+  return q;
+}
+
 // Rows r0.. of a weight that the products cannot load as it is, to the padded
 // copy, in the same shape of block (blocks past the rows' in the same launch).
 template <typename T>
@@ -154,12 +171,7 @@ __device__ __forceinline__ void pack_weight(const HeadArgs& a, int r0) {
     const int64_t r = r0 + i * 32 + (threadIdx.x >> 6) * 8 + (lane >> 3);
     if (r >= a.v) continue;
     const T* src = (const T*)a.w_src + r * a.ld_src;
-    T x[CH];
-#pragma unroll
-    for (int e = 0; e < CH; ++e) x[e] = c + e < a.d ? src[c + e] : T(0);
-    u32x4_t q;
-    __builtin_memcpy(&q, x, 16);
-    *(u32x4_t*)((T*)a.w + r * a.ld_w + c) = q;
+    *(u32x4_t*)((T*)a.w + r * a.ld_w + c) = load_chunk(src, c, a.d);
   }
 }
 
@@ -202,23 +214,12 @@ __global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan, int row_bloc
   if (r0 >= rows) return;
   __syncthreads();
   const int lane = threadIdx.x & 63, ch = blockIdx.y * 8 + (lane & 7), c = ch * CH;
-  const bool whole = a.ld_h * sizeof(T) % 16 == 0 && (uintptr_t)a.h % 16 == 0 && c + CH <= a.d;
   uint8_t* dst = (uint8_t*)a.hp + (((int64_t)blockIdx.x * (a.dp / CH) + ch) << 10);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int rr = i * 32 + (threadIdx.x >> 6) * 8 + (lane >> 3);
     u32x4_t q = {0, 0, 0, 0};
-    if (r0 + rr < rows) {
-      const T* src = (const T*)a.h + (int64_t)list[rr] * a.ld_h;
-      if (whole) {
-        q = *(const u32x4_t*)(src + c);
-      } else {
-        T x[CH];
-#pragma unroll
-        for (int e = 0; e < CH; ++e) x[e] = c + e < a.d ? src[c + e] : T(0);
-        __builtin_memcpy(&q, x, 16);
-      }
-    }
+    if (r0 + rr < rows) q = load_chunk((const T*)a.h + (int64_t)list[rr] * a.ld_h, c, a.d);
     *(u32x4_t*)(dst + rr * 16) = q;
   }
 }
@@ -433,7 +434,6 @@ __global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a) {
   const int64_t token = a.idx[a.row0 + r];
   const float g = common_factor(a), rest = a.rs[r].w;
   const T* target_row = (const T*)a.w + (int64_t)max(a.tgt[a.row0 + r], 0) * a.ld_w;   // (rest is 0 without a target)
-  const bool whole = a.ld_dh % 4 == 0 && (uintptr_t)a.dh % (4 * sizeof(T)) == 0;
   // a narrow row leaves threads to share the splits; the parts are added in order
   const int groups = (a.d + 3) / 4, width = groups > 128 ? 256 : groups > 64 ? 128 : groups > 32 ? 64 : 32;
   const int parts = 256 / width, part = threadIdx.x / width;
@@ -458,11 +458,14 @@ __global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a) {
       for (int e = 0; e < 4; ++e)
         if (c + e < a.d) x[e] = fmaf(rest, ld<T>(target_row, c + e), x[e]);
     T* dst = dh + token * a.ld_dh + c;
-    if (whole && c + 4 <= a.d) {
-      if constexpr (sizeof(T) == 2)
-        *(u32x2_t*)dst = (u32x2_t){pack_bf16(x[0] * g, x[1] * g), pack_bf16(x[2] * g, x[3] * g)};
-      else
-        *(f32x4_t*)dst = x * g;
+    if (c + 4 <= a.d) {                    // (one store, aligned or not)
+      if constexpr (sizeof(T) == 2) {
+        const u32x2_t y = {pack_bf16(x[0] * g, x[1] * g), pack_bf16(x[2] * g, x[3] * g)};
+        __builtin_memcpy(dst, &y, 8);
+      } else {
+        const f32x4_t y = x * g;
+        __builtin_memcpy(dst, &y, 16);
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)

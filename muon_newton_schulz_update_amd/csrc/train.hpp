@@ -117,6 +117,7 @@ struct HeadArgs {
   void* dw;        int64_t ld_dw;
   int32_t n, v, d;                    // tokens, vocabulary, width
   int32_t dp, vp;                     // padded width (64 or 32 elements), padded vocabulary (256)
+  int32_t w_cols;                     // columns of w: d, or dp of a padded copy
   int32_t vtile, n_vt;                // vocabulary columns per statistic of a token, statistics
   int32_t piece, row0;                // tokens per piece (buffers), first compact token of this piece
   int32_t rows_max;                   // tokens of this piece if none is ignored

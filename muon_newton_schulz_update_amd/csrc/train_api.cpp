@@ -156,9 +156,11 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
     a.dw = dw->ptr;
     a.ld_dw = dw->ld;
   }
-  // the weight as it is, where a product's stage can be loaded from it in
-  // 16-byte pieces with no remainder; otherwise a padded copy
-  const bool direct = a.d % unit == 0 && (uintptr_t)wgt.ptr % 16 == 0 && (wgt.rows == 1 || (wgt.ld * e % 16 == 0 && wgt.ld * e < (1 << 23)));
+  // the weight as it is, where its rows are whole 16-byte pieces on 16 bytes;
+  // otherwise a padded copy (the pitch also fits the products' 24-bit multiply)
+  const bool direct = a.d * e % 16 == 0 && (uintptr_t)wgt.ptr % 16 == 0 &&
+                      (wgt.rows == 1 || (wgt.ld * e % 16 == 0 && wgt.ld * e < (1 << 23)));
+  a.w_cols = direct ? a.d : a.dp;
   // pieces
   const size_t row = (size_t)a.dp * e + (size_t)cdiv(a.v, 64) * 8 + 24 + (grad ? (size_t)a.vp * e : 0);
   const int64_t most =
@@ -195,7 +197,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.part = (float*)(b + o_part);
   a.dwacc = acc ? (float*)(b + o_acc) : nullptr;
   a.w = wgt.ptr;
-  a.ld_w = wgt.ld;
+  a.ld_w = wgt.rows == 1 ? a.d : wgt.ld;
   HIP_DO(h, launch_head_compact(a, s));
   if (!direct) {
     a.w_src = wgt.ptr;
