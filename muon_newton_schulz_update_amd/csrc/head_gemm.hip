@@ -8,9 +8,9 @@
 // (or 128 x 128 of 4 and 64 x 64 of 2, two and four workgroups to a CU, where
 // tiles are few),
 // K in stages of 128 bytes (64 bf16, 32 fp32), both operands of a stage
-// brought to LDS by direct buffer loads into a ring of five slots, so
-// that while one stage feeds the matrix cores the next and half of the one
-// after are on their way. bf16 runs v_mfma_f32_32x32x16_bf16, fp32
+// brought to LDS by direct buffer loads into a ring of five slots (nine in
+// small launches of 64-tiles), so that while one stage feeds the matrix cores
+// the next and half of the one after (three and a half) are on their way. bf16 runs v_mfma_f32_32x32x16_bf16, fp32
 // v_mfma_f32_32x32x2f32.
 //
 // Neither the weight nor the per-piece matrices are ever transposed in
@@ -53,7 +53,6 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 enum OpLayout { OP_ROW_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
 enum Product { P_LOGITS, P_DHIDDEN, P_DWEIGHT };
 
-constexpr int kSlots = 5;
 constexpr int kFewTokens = 64;    // whose dW takes the targets' remainders too
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kRefFloor = -3.0e38f;
@@ -205,7 +204,7 @@ template <typename T> struct FragOf { typedef bf16x8_t type; };
 template <> struct FragOf<float> { typedef f32x4_t type; };
 
 // The K loop: acc += A B over stages [k0, k1).
-template <typename T, int LA, int LB, int TILE, int MI, int NI>
+template <typename T, int LA, int LB, int TILE, int S, int MI, int NI>
 __device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, const Operand& oa, const Operand& ob,
                                        int lane, int wave, int am, int bn, int k0, int k1) {
   typedef typename FragOf<T>::type Frag;
@@ -214,7 +213,7 @@ __device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, c
   constexpr int kSlot = TILE * 128;                        // one operand of one stage
   constexpr int LPO = 4;                                   // loads per wave per operand and stage
   constexpr int kReadStep = MI * A::kReads + NI * B::kReads;
-  constexpr int S = kSlots;
+  static_assert(S >= 5 && S % 2 == 1 && (S - 4) * LPO < 64, "slots");
   Frag fa[2][MI], fb[2][NI];
   // operand stage o: A (o even) or B (o odd) of stage k0 + o / 2, slot o % 5
   auto issue = [&](int slot, int o, int i0, int i1) {
@@ -265,21 +264,22 @@ __device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, c
   issue(0, 0, 0, LPO);
   issue(1, 1, 0, LPO);
   wait_vm<0>();
-  issue(2, 2, 0, LPO);
-  issue(3, 3, 0, LPO / 2);
+#pragma unroll
+  for (int o = 2; o < S - 2; ++o) issue(o, o, 0, LPO);
+  issue(S - 2, S - 2, 0, LPO / 2);
   ring_barrier();
   read(0, 1, 0, 0);
   int sa = 0, sb = 1, na = 2, nb = 3;   // slots of this stage and the next
+  int ha = S - 2, ds = S - 1;           // of the operand stages 2 k + S - 2 and 2 k + S - 1
   for (int k = 0; k < nk - 1; ++k) {
-    const int ds = na + 2 >= S ? na + 2 - S : na + 2;
 #pragma unroll
     for (int s = 0; s < 3; ++s) {
       if (s == 0) {
         __builtin_amdgcn_s_setprio(1);
         __builtin_amdgcn_sched_barrier(0);
-        issue(nb, 2 * k + 3, LPO / 2, LPO);
+        issue(ha, 2 * k + S - 2, LPO / 2, LPO);
       } else {
-        issue(ds, 2 * k + 4, (s - 1) * LPO / 2, s * LPO / 2);
+        issue(ds, 2 * k + S - 1, (s - 1) * LPO / 2, s * LPO / 2);
       }
       read(sa, sb, s + 1, (s + 1) & 1);
       mfmas(s & 1);
@@ -290,21 +290,25 @@ __device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, c
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    // the next stage has landed (only the operand stage after it may be on
-    // its way); this stage's fragments have been read by every wave
+    // the next stage has landed (only the S - 4 operand stages after it may be
+    // on their way); this stage's fragments have been read by every wave
     wait_lgkm0();
-    wait_vm<LPO>();
+    wait_vm<(S - 4) * LPO>();
     ring_barrier();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(2);
     __builtin_amdgcn_sched_barrier(0);
-    issue(sa, 2 * k + 5, 0, LPO / 2);
+    issue(sa, 2 * k + S, 0, LPO / 2);
     read(na, nb, 0, 0);
     mfmas(1);
     spread(LPO / 2);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
+    // operand stage 2 k + S went to this stage's first slot, 2 k + S + 1 goes to
+    // its second
+    ha = sa;
+    ds = sb;
     sa = na;
     sb = nb;
     na = na + 2 >= S ? na + 2 - S : na + 2;
@@ -342,13 +346,13 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 // The statistics are per wave's vocabulary rows, so waves never wait for one another. The
 // exponentials go to the panels as whole chunks after a half-wave swap.
 // ---------------------------------------------------------------------------
-template <typename T, int TILE, bool FEW>
-__global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
+template <typename T, int TILE, int S, bool FEW>
+__global__ __launch_bounds__(TILE * 2, S > 5 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
   // a wave: 128 vocabulary rows (64 of a 64-tile) x 64 tokens (256) or 32
   // (FEW: at most 32 tokens; both waves of a 64-tile take those, 32 rows each)
   constexpr int MI = FEW ? 1 : TILE == 64 ? 2 : 4, NI = TILE == 256 ? 2 : 1;
   constexpr int WM = TILE / (MI * 32), WN = FEW ? 1 : TILE / (NI * 32);
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * TILE * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
   int vi, ti;
   const int rows = piece_rows(a), lane = threadIdx.x & 63;
   if (!strip_tile<4>(xcd_index(blockIdx.x), vt, min(tt, (rows + TILE - 1) / TILE), vi, ti)) return;
@@ -365,7 +369,7 @@ __global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int kee
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
-  k_loop<T, OP_ROW_K, OP_PANEL_K, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0,
+  k_loop<T, OP_ROW_K, OP_PANEL_K, TILE, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0,
                                                 a.dp / A::KE);
 
   const int lr = lane & 31, hf = lane >> 5;
@@ -484,7 +488,7 @@ __global__ __launch_bounds__(TILE * 2, 2) void k_logits_mfma(HeadArgs a, int kee
 // ---------------------------------------------------------------------------
 // dH: partial sums over a range of the vocabulary, 32-bit, row-major.
 // ---------------------------------------------------------------------------
-template <typename T, int TILE>
+template <typename T, int TILE, int S>
 __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, int ti, int di, int q, int rows) {
   constexpr int MI = 2, NI = TILE / 64;                     // waves: TILE / 64 x 2
   const int lane = threadIdx.x & 63;
@@ -505,7 +509,7 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   if (k1 > k0)
-    k_loop<T, OP_PANEL_K, OP_ROW_T, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * NI * 32, k0, k1);
+    k_loop<T, OP_PANEL_K, OP_ROW_T, TILE, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * NI * 32, k0, k1);
   const int lr = lane & 31, hf = lane >> 5;
   if (a.split > 1) {
     float* out = a.part + (int64_t)q * a.piece * a.dp;
@@ -586,7 +590,7 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 // together to whole rows of the wave's part in the idle LDS (chunks swizzled by
 // row) and leave as 16-byte stores.
 // ---------------------------------------------------------------------------
-template <typename T, int TILE>
+template <typename T, int TILE, int S>
 __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, int vi, int di, int rows) {
   constexpr int MI = TILE / 64, NI = 2;                     // waves: 2 x TILE / 64
   const int lane = threadIdx.x & 63, lr = lane & 31, hf = lane >> 5;
@@ -607,7 +611,7 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   const int nk = (rows + O::KE - 1) / O::KE;
   if (nk > 0)
-    k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * 64, 0, nk);
+    k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * 64, 0, nk);
   const float g = common_factor(a);
   const int vw = v0 + wn * 64, dw = d0 + wm * MI * 32;      // the wave's part
   if constexpr (sizeof(T) == 2) {
@@ -701,10 +705,10 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
 // Both gradients in one launch: they need only dz, and the tiles of one fill
 // the CUs that the last round of the other's leaves idle (the 50304 x 768
 // weight's 591 tiles are 2.3 rounds of the 256 CUs).
-template <typename T, int TILE>
-__global__ __launch_bounds__(TILE * 2, 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
+template <typename T, int TILE, int S>
+__global__ __launch_bounds__(TILE * 2, S > 5 ? 1 : 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
                                                                                   int weight_first) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * TILE * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
   const int rows = piece_rows(a);
   const int nt = min(tt, (rows + TILE - 1) / TILE), n_h = nt * nd * a.split, n_w = vt * nd;
   int idx = xcd_index(blockIdx.x);
@@ -717,10 +721,10 @@ __global__ __launch_bounds__(TILE * 2, 2) void k_gradients_mfma(HeadArgs a, int 
   if (!in_first) idx -= first;
   if (in_first == (weight_first != 0)) {
     int vi, di;
-    if (strip_tile<8>(idx, vt, nd, vi, di)) dweight_tile<T, TILE>(a, smem, vi, di, rows);
+    if (strip_tile<8>(idx, vt, nd, vi, di)) dweight_tile<T, TILE, S>(a, smem, vi, di, rows);
   } else {
     const int q = idx / (nt * nd), t = idx - q * nt * nd;
-    dhidden_tile<T, TILE>(a, smem, t / nd, t % nd, q, rows);
+    dhidden_tile<T, TILE, S>(a, smem, t / nd, t % nd, q, rows);
   }
 }
 
@@ -741,6 +745,10 @@ inline int xcd_grid(int64_t n) { return n > 0 ? cdiv(n, 256) * 256 : 256; }
 // 64-tiles (loss alone 64 / 128: 252 tiles 46.7 / 48.3, 628 67.0 / 64.4), and
 // its gradients always take those (634 tiles 440 / 465).
 constexpr int kFewTiles = 768, kFewSmallTiles = 384;
+// 64-tiles that all fit the chip two to a CU: a ring of nine slots, whose loads
+// are asked for three and a half stages ahead. Such a launch reads its operands
+// for the first time, and a stage waits for memory rather than for its products.
+constexpr int kDeepTiles = 512;
 int tile_of(int dt, int64_t tiles256, int64_t tiles128) {
   if (dt == MUON_BF16 && tiles256 >= kFewTiles) return 256;
   return tiles128 >= kFewSmallTiles ? 128 : 64;
@@ -764,12 +772,21 @@ int grad_tile_of(int dt, int rows, int dp, int64_t tiles256, int64_t tiles128) {
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
   const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
   const dim3 g(xcd_grid((int64_t)vt * tt)), b(tile * 2);
-  if (dt == MUON_BF16 && tile == 256) hipLaunchKernelGGL((k_logits_mfma<u16, 256, false>), g, b, 0, s, a, keep, vt, tt);
-  else if (dt == MUON_BF16 && tile == 128) hipLaunchKernelGGL((k_logits_mfma<u16, 128, false>), g, b, 0, s, a, keep, vt, tt);
-  else if (dt == MUON_BF16) hipLaunchKernelGGL((k_logits_mfma<u16, 64, false>), g, b, 0, s, a, keep, vt, tt);
-  else if (tile == 128) hipLaunchKernelGGL((k_logits_mfma<float, 128, false>), g, b, 0, s, a, keep, vt, tt);
-  else if (a.n > 32) hipLaunchKernelGGL((k_logits_mfma<float, 64, false>), g, b, 0, s, a, keep, vt, tt);
-  else hipLaunchKernelGGL((k_logits_mfma<float, 64, true>), g, b, 0, s, a, keep, vt, tt);
+  const bool deep = tile == 64 && (int64_t)vt * tt <= kDeepTiles, few = a.n <= 32;
+#define LOGITS(T, ...) hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__>), g, b, 0, s, a, keep, vt, tt)
+  if (dt == MUON_BF16) {
+    if (tile == 256) LOGITS(u16, 256, 5, false);
+    else if (tile == 128) LOGITS(u16, 128, 5, false);
+    else if (deep) LOGITS(u16, 64, 9, false);
+    else LOGITS(u16, 64, 5, false);
+  } else {
+    if (tile == 128) LOGITS(float, 128, 5, false);
+    else if (deep && few) LOGITS(float, 64, 9, true);
+    else if (deep) LOGITS(float, 64, 9, false);
+    else if (few) LOGITS(float, 64, 5, true);
+    else LOGITS(float, 64, 5, false);
+  }
+#undef LOGITS
   return hipGetLastError();
 }
 
@@ -778,11 +795,20 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
   const int tt = a.dh ? cdiv(rows, tile) : 0, vt = a.dw ? cdiv(a.v, tile) : 0, nd = cdiv(a.dp, tile);
   // the longer tiles go first
   const int wf = cdiv(rows, unit) > cdiv(a.v, unit) / a.split;
-  const dim3 g(xcd_grid(((int64_t)tt * a.split + vt) * nd + 1)), b(tile * 2);
-  if (dt != MUON_BF16) hipLaunchKernelGGL((k_gradients_mfma<float, 64>), g, b, 0, s, a, vt, tt, nd, wf);
-  else if (tile == 256) hipLaunchKernelGGL((k_gradients_mfma<u16, 256>), g, b, 0, s, a, vt, tt, nd, wf);
-  else if (tile == 128) hipLaunchKernelGGL((k_gradients_mfma<u16, 128>), g, b, 0, s, a, vt, tt, nd, wf);
-  else hipLaunchKernelGGL((k_gradients_mfma<u16, 64>), g, b, 0, s, a, vt, tt, nd, wf);
+  const int64_t tiles = ((int64_t)tt * a.split + vt) * nd;
+  const dim3 g(xcd_grid(tiles + 1)), b(tile * 2);
+  const bool deep = tile == 64 && tiles <= kDeepTiles;
+#define GRADIENTS(T, ...) hipLaunchKernelGGL((k_gradients_mfma<T, __VA_ARGS__>), g, b, 0, s, a, vt, tt, nd, wf)
+  if (dt == MUON_BF16) {
+    if (tile == 256) GRADIENTS(u16, 256, 5);
+    else if (tile == 128) GRADIENTS(u16, 128, 5);
+    else if (deep) GRADIENTS(u16, 64, 9);
+    else GRADIENTS(u16, 64, 5);
+  } else {
+    if (deep) GRADIENTS(float, 64, 9);
+    else GRADIENTS(float, 64, 5);
+  }
+#undef GRADIENTS
   return hipGetLastError();
 }
 
