@@ -104,12 +104,16 @@ struct Operand {
 };
 
 // Tile edges: 256 (8 waves, one workgroup per CU), 128 (4 waves, two) and 64
-// (2 waves, four). A stage of an operand is TILE x 128 bytes, TILE / 8 loads of
-// 1 KB, four a wave.
-template <typename T, int L, int TILE>
+// (2 waves, or 4 for fp32, whose products take sixteen times as long a stage;
+// four workgroups, or two with the long ring). A stage of an operand is
+// TILE x 128 bytes, TILE / 8 loads of 1 KB shared by the NW waves.
+template <typename T, int TILE>
+constexpr int waves_of() {
+  return TILE == 64 && sizeof(T) == 4 ? 4 : TILE / 32;
+}
+template <typename T, int L, int TILE, int NW = waves_of<T, TILE>()>
 struct Op {
   static constexpr int KE = 128 / (int)sizeof(T);
-  static constexpr int NW = TILE / 32;                        // waves
   static constexpr int kRowT = TILE * (int)sizeof(T);         // LDS row of OP_ROW_T, bytes
   static constexpr int kRowsPerLoad = 1024 / kRowT;           // its rows per load
   // bank swizzle of an OP_ROW_T row (16-bit): a read takes four chunks of four
@@ -204,14 +208,14 @@ template <typename T> struct FragOf { typedef bf16x8_t type; };
 template <> struct FragOf<float> { typedef f32x4_t type; };
 
 // The K loop: acc += A B over stages [k0, k1).
-template <typename T, int LA, int LB, int TILE, int S, int MI, int NI>
+template <typename T, int LA, int LB, int TILE, int NW, int S, int MI, int NI>
 __device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, const Operand& oa, const Operand& ob,
                                        int lane, int wave, int am, int bn, int k0, int k1) {
   typedef typename FragOf<T>::type Frag;
-  typedef Op<T, LA, TILE> A;
-  typedef Op<T, LB, TILE> B;
+  typedef Op<T, LA, TILE, NW> A;
+  typedef Op<T, LB, TILE, NW> B;
   constexpr int kSlot = TILE * 128;                        // one operand of one stage
-  constexpr int LPO = 4;                                   // loads per wave per operand and stage
+  constexpr int LPO = TILE / 8 / NW;                       // loads per wave per operand and stage
   constexpr int kReadStep = MI * A::kReads + NI * B::kReads;
   static_assert(S >= 5 && S % 2 == 1 && (S - 4) * LPO < 64, "slots");
   Frag fa[2][MI], fb[2][NI];
@@ -347,19 +351,22 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 // exponentials go to the panels as whole chunks after a half-wave swap.
 // ---------------------------------------------------------------------------
 template <typename T, int TILE, int S, bool FEW>
-__global__ __launch_bounds__(TILE * 2, S > 5 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
-  // a wave: 128 vocabulary rows (64 of a 64-tile) x 64 tokens (256) or 32
-  // (FEW: at most 32 tokens; both waves of a 64-tile take those, 32 rows each)
-  constexpr int MI = FEW ? 1 : TILE == 64 ? 2 : 4, NI = TILE == 256 ? 2 : 1;
-  constexpr int WM = TILE / (MI * 32), WN = FEW ? 1 : TILE / (NI * 32);
+__global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
+  // a wave: 128 vocabulary rows x 64 tokens (256-tiles) or 32, 64 x 32 of a
+  // 64-tile. PAIR: 32 x 32 of one, and two waves put their statistics together:
+  // fp32, four waves, or (FEW: at most 32 tokens) two on the first 32 tokens
+  constexpr int NW = FEW ? 2 : waves_of<T, TILE>();
+  constexpr bool PAIR = TILE == 64 && sizeof(T) == 4;
+  constexpr int MI = PAIR ? 1 : TILE == 64 ? 2 : 4, NI = TILE == 256 ? 2 : 1;
+  constexpr int WM = TILE / (MI * 32), WN = NW / WM;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
   int vi, ti;
   const int rows = piece_rows(a), lane = threadIdx.x & 63;
   if (!strip_tile<4>(xcd_index(blockIdx.x), vt, min(tt, (rows + TILE - 1) / TILE), vi, ti)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   const int v0 = vi * TILE, r0 = ti * TILE;
-  typedef Op<T, OP_ROW_K, TILE> A;
-  typedef Op<T, OP_PANEL_K, TILE> B;
+  typedef Op<T, OP_ROW_K, TILE, NW> A;
+  typedef Op<T, OP_PANEL_K, TILE, NW> B;
   const Operand oa = {(const uint8_t*)a.w + (int64_t)v0 * a.ld_w * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)),
                       a.v - 1 - v0, a.w_cols * (int)sizeof(T), A::lane_part(lane, wave, 0)};
   const uint32_t blk = (uint32_t)a.dp * sizeof(T) * kPanelRows;
@@ -369,13 +376,13 @@ __global__ __launch_bounds__(TILE * 2, S > 5 ? 1 : 2) void k_logits_mfma(HeadArg
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
-  k_loop<T, OP_ROW_K, OP_PANEL_K, TILE, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0,
+  k_loop<T, OP_ROW_K, OP_PANEL_K, TILE, NW, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0,
                                                 a.dp / A::KE);
 
   const int lr = lane & 31, hf = lane >> 5;
   const int vw = v0 + wm * MI * 32;                  // the wave's first vocabulary row
-  if (!FEW && vw >= a.v) return;                     // (the exponentials' padding is cleared with the gradient)
-  const int tile = FEW ? vi : vi * WM + wm;
+  if (!PAIR && vw >= a.v) return;                    // (the exponentials' padding is cleared with the gradient)
+  const int tile = PAIR ? vi : vi * WM + wm;
   if (a.softcap > 0.f) {
     const float s = 2.f * kLog2e / a.softcap;
 #pragma unroll
@@ -423,14 +430,14 @@ __global__ __launch_bounds__(TILE * 2, S > 5 ? 1 : 2) void k_logits_mfma(HeadArg
 #pragma unroll
       for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
     top = fmaxf(top, __shfl_xor(top, 32));
-    // the two waves' halves of a few tokens' tile have one reference and sum
-    float* half_stat = (float*)smem + (FEW ? 32 : 0);
-    if constexpr (FEW) {
-      ring_barrier();                                // both are done with the slots
-      if (hf == 0) half_stat[(wm - 1) * 32 + lr] = top;
+    // PAIR: the two waves' rows have one reference and one sum
+    float* stat = (float*)smem + wn * 32 + lr;       // [wave row][token], then the second row's sums
+    if constexpr (PAIR) {
+      ring_barrier();                                // every wave is done with the slots
+      if (hf == 0) stat[wm * 64] = top;
       wait_lgkm0();
       ring_barrier();
-      top = fmaxf(half_stat[lr - 32], half_stat[lr]);
+      top = fmaxf(stat[0], stat[64]);
     }
     top = ceilf(fmaxf(top * kLog2e, kRefFloor));
     float sum = 0.f;
@@ -471,12 +478,12 @@ __global__ __launch_bounds__(TILE * 2, S > 5 ? 1 : 2) void k_logits_mfma(HeadArg
       }
     }
     sum += __shfl_xor(sum, 32);
-    if constexpr (FEW) {
-      if (wm == 1 && hf == 0) half_stat[32 + lr] = sum;
+    if constexpr (PAIR) {
+      if (wm == 1 && hf == 0) stat[128] = sum;
       wait_lgkm0();
       ring_barrier();
       if (wm == 1) return;
-      sum += half_stat[32 + lr];
+      sum += stat[128];
     }
     if (hf == 0) {
       a.tmax[(int64_t)tile * a.piece + r] = top;
@@ -490,12 +497,12 @@ __global__ __launch_bounds__(TILE * 2, S > 5 ? 1 : 2) void k_logits_mfma(HeadArg
 // ---------------------------------------------------------------------------
 template <typename T, int TILE, int S>
 __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, int ti, int di, int q, int rows) {
-  constexpr int MI = 2, NI = TILE / 64;                     // waves: TILE / 64 x 2
+  constexpr int NW = waves_of<T, TILE>(), MI = NW * 32 > TILE ? 1 : 2, NI = TILE == 64 ? 1 : TILE / 64;   // waves: NW / 2 x 2
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
   const int r0 = ti * TILE, d0 = di * TILE;
-  typedef Op<T, OP_PANEL_K, TILE> A;
-  typedef Op<T, OP_ROW_T, TILE> B;
+  typedef Op<T, OP_PANEL_K, TILE, NW> A;
+  typedef Op<T, OP_ROW_T, TILE, NW> B;
   const uint32_t blk = (uint32_t)a.vp * sizeof(T) * kPanelRows;
   const Operand oa = {(const uint8_t*)a.e + (int64_t)ti * (TILE / 64) * blk, blk, 0, 0, A::lane_part(lane, wave, 0)};
   const int chunks = (a.w_cols - d0) * (int)sizeof(T) / 16;
@@ -509,7 +516,7 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   if (k1 > k0)
-    k_loop<T, OP_PANEL_K, OP_ROW_T, TILE, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * 64, wn * NI * 32, k0, k1);
+    k_loop<T, OP_PANEL_K, OP_ROW_T, TILE, NW, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, k0, k1);
   const int lr = lane & 31, hf = lane >> 5;
   if (a.split > 1) {
     float* out = a.part + (int64_t)q * a.piece * a.dp;
@@ -521,59 +528,56 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int row = r0 + wm * 64 + mi * 32 + 8 * (r >> 2) + 4 * hf + (r & 3);
+          const int row = r0 + (wm * MI + mi) * 32 + 8 * (r >> 2) + 4 * hf + (r & 3);
           out[(int64_t)row * a.dp + d] = acc[mi][ni][r];
         }
     }
     return;
   }
-  // one split: the tokens' rows themselves, put together in the idle LDS
+  // one split: the tokens' rows themselves, put together in the idle LDS as
+  // 32-bit sums, so that what the target's gradient lost in its rounding is
+  // added, and the weight's row read, by whole chunks
   const float g = common_factor(a);
-  const int rw = r0 + wm * 64, dw = d0 + wn * NI * 32;      // the wave's part
-  if constexpr (sizeof(T) == 2) {
-    // what the target's gradient lost in its rounding
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int t = rw + mi * 32 + 8 * (r >> 2) + 4 * hf + (r & 3);
-        const float rest = t < rows ? a.rs[t].w : 0.f;
-        if (rest == 0.f) continue;
-        const u16* w = (const u16*)a.w + (int64_t)a.tgt[a.row0 + t] * a.ld_w;
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-          const int d = dw + ni * 32 + lr;
-          if (d < a.d) acc[mi][ni][r] = fmaf(rest, bf2f(w[d]), acc[mi][ni][r]);
-        }
-      }
-  }
-  constexpr int NC = NI * 32 * (int)sizeof(T) / 16, CH = 16 / (int)sizeof(T);   // chunks of its row
+  const int rw = r0 + wm * MI * 32, dw = d0 + wn * NI * 32;      // the wave's part
+  constexpr int CH = 16 / (int)sizeof(T), NF = NI * 8, NC = NI * 32 / CH;   // 16-byte chunks of its row: sums, results
   ring_barrier();                                           // every wave is done with the slots
-  uint8_t* slab = smem + wave * (32 * NC * 16);
+  uint8_t* slab = smem + wave * (32 * NF * 16);
+  auto chunk_at = [&](int row, int c) { return slab + row * NF * 16 + ((c ^ (row & (NF - 1))) * 16); };
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = 8 * (r >> 2) + 4 * hf + (r & 3), c = (ni * 32 + lr) / CH;
-        T* p = (T*)(slab + row * NC * 16 + ((c ^ (row & (NC - 1))) * 16)) + lr % CH;
-        if constexpr (sizeof(T) == 2) *p = (u16)pack_bf16(acc[mi][ni][r] * g, 0.f);
-        else *p = acc[mi][ni][r] * g;
-      }
+      for (int r = 0; r < 16; ++r)
+        ((float*)chunk_at(8 * (r >> 2) + 4 * hf + (r & 3), ni * 8 + (lr >> 2)))[lr & 3] = acc[mi][ni][r];
     wave_lds_sync();
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < NC / 2; ++i) {
       const int row = i * (64 / NC) + lane / NC, c = lane % NC;
-      const u32x4_t x = *(const u32x4_t*)(slab + row * NC * 16 + ((c ^ (row & (NC - 1))) * 16));
       const int t = rw + mi * 32 + row, d = dw + c * CH;
       if (t >= rows || d >= a.d) continue;
+      T y[CH];
+      f32x4_t x[CH / 4];
+#pragma unroll
+      for (int j = 0; j < CH / 4; ++j) x[j] = *(const f32x4_t*)chunk_at(row, c * (CH / 4) + j);
+      if constexpr (sizeof(T) == 2) {
+        const float rest = a.rs[t].w;
+        if (rest != 0.f) {
+          const u32x4_t w = *(const u32x4_t*)((const u16*)a.w + (int64_t)a.tgt[a.row0 + t] * a.ld_w + d);
+#pragma unroll
+          for (int e = 0; e < CH; ++e) x[e >> 2][e & 3] = fmaf(rest, bf2f((u16)(w[e >> 1] >> (16 * (e & 1)))), x[e >> 2][e & 3]);
+        }
+        const u32x4_t q = {pack_bf16(x[0][0] * g, x[0][1] * g), pack_bf16(x[0][2] * g, x[0][3] * g),
+                           pack_bf16(x[1][0] * g, x[1][1] * g), pack_bf16(x[1][2] * g, x[1][3] * g)};
+        __builtin_memcpy(y, &q, 16);
+      } else {
+        const f32x4_t q = x[0] * g;
+        __builtin_memcpy(y, &q, 16);
+      }
       T* p = (T*)a.dh + (int64_t)a.idx[a.row0 + t] * a.ld_dh + d;
       if (d + CH <= a.d) {
-        __builtin_memcpy(p, &x, 16);      // (one store, aligned or not)
+        __builtin_memcpy(p, y, 16);       // (one store, aligned or not)
       } else {
-        T y[CH];
-        __builtin_memcpy(y, &x, 16);
 #pragma unroll
         for (int e = 0; e < CH; ++e)
           if (d + e < a.d) p[e] = y[e];
@@ -592,12 +596,12 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 // ---------------------------------------------------------------------------
 template <typename T, int TILE, int S>
 __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, int vi, int di, int rows) {
-  constexpr int MI = TILE / 64, NI = 2;                     // waves: 2 x TILE / 64
+  constexpr int NW = waves_of<T, TILE>(), MI = TILE / 64, NI = NW * 32 > TILE ? 1 : 2, WN = NW / 2;   // waves: 2 x WN
   const int lane = threadIdx.x & 63, lr = lane & 31, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / (TILE / 64), wn = wave % (TILE / 64);
+  const int wm = wave / WN, wn = wave % WN;
   const int v0 = vi * TILE, d0 = di * TILE;
-  typedef Op<T, OP_PANEL_T, TILE> O;
+  typedef Op<T, OP_PANEL_T, TILE, NW> O;
   constexpr int CH = 16 / (int)sizeof(T);
   const uint32_t be = (uint32_t)a.vp * sizeof(T) * kPanelRows, bh = (uint32_t)a.dp * sizeof(T) * kPanelRows;
   const Operand oa = {(const uint8_t*)a.hp + (int64_t)(d0 / CH) * 1024, bh, (a.dp - d0) / CH - 1, 0,
@@ -611,17 +615,17 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   const int nk = (rows + O::KE - 1) / O::KE;
   if (nk > 0)
-    k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * 64, 0, nk);
+    k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, NW, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0, nk);
   const float g = common_factor(a);
-  const int vw = v0 + wn * 64, dw = d0 + wm * MI * 32;      // the wave's part
-  if constexpr (sizeof(T) == 2) {
-    // few tokens, one to a lane: what the targets' gradients lost in their
-    // rounding, for those with their target among the wave's rows (one piece:
-    // row0 is 0)
+  const int vw = v0 + wn * NI * 32, dw = d0 + wm * MI * 32;      // the wave's part
+  if constexpr (sizeof(T) == 2 && TILE < 256) {
+    // few tokens (which never have 256-tiles: kFewTokens < kShortK), one to a
+    // lane: what the targets' gradients lost in their rounding, for those with
+    // their target among the wave's rows (one piece: row0 is 0)
     const bool few = a.n <= kFewTokens && lane < rows;
     const int lane_at = few ? a.tgt[lane] - vw : -1;
     const float lane_rest = few ? a.rs[lane].w : 0.f;
-    uint64_t todo = __ballot(lane_at >= 0 && lane_at < 64 && lane_rest != 0.f);
+    uint64_t todo = __ballot(lane_at >= 0 && lane_at < NI * 32 && lane_rest != 0.f);
     for (; todo; todo &= todo - 1) {
       const int i = __builtin_ctzll(todo), at = __builtin_amdgcn_readlane(lane_at, i);
       const float rest = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_rest), i));
@@ -666,7 +670,7 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
   }
   constexpr int NC = MI * 2 * (int)sizeof(T);               // chunks of the wave's row
   if (nk > 0) ring_barrier();                               // every wave is done with the slots
-  uint8_t* slab = smem + wave * (64 * NC * 16);
+  uint8_t* slab = smem + wave * (NI * 32 * NC * 16);
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
@@ -684,7 +688,7 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
       }
   wave_lds_sync();
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
+  for (int i = 0; i < NI * NC / 2; ++i) {
     const int row = i * (64 / NC) + lane / NC, c = lane % NC;
     const u32x4_t x = *(const u32x4_t*)(slab + row * NC * 16 + ((c ^ (row & (NC - 1))) * 16));
     const int v = vw + row, d = dw + c * CH;
@@ -706,14 +710,14 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
 // the CUs that the last round of the other's leaves idle (the 50304 x 768
 // weight's 591 tiles are 2.3 rounds of the 256 CUs).
 template <typename T, int TILE, int S>
-__global__ __launch_bounds__(TILE * 2, S > 5 ? 1 : 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
+__global__ __launch_bounds__((waves_of<T, TILE>() * 64), S > 5 ? 1 : 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
                                                                                   int weight_first) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
   const int rows = piece_rows(a);
   const int nt = min(tt, (rows + TILE - 1) / TILE), n_h = nt * nd * a.split, n_w = vt * nd;
   int idx = xcd_index(blockIdx.x);
   if (idx >= n_h + n_w) {
-    if (idx == n_h + n_w && a.last && !a.per_token) total_loss<TILE * 2>(a, (double*)smem);
+    if (idx == n_h + n_w && a.last && !a.per_token) total_loss<waves_of<T, TILE>() * 64>(a, (double*)smem);
     return;
   }
   const int first = weight_first ? n_w : n_h;
@@ -771,8 +775,8 @@ int grad_tile_of(int dt, int rows, int dp, int64_t tiles256, int64_t tiles128) {
 
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
   const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
-  const dim3 g(xcd_grid((int64_t)vt * tt)), b(tile * 2);
   const bool deep = tile == 64 && (int64_t)vt * tt <= kDeepTiles, few = a.n <= 32;
+  const dim3 g(xcd_grid((int64_t)vt * tt)), b(dt != MUON_BF16 && tile == 64 && !few ? 256 : tile * 2);
 #define LOGITS(T, ...) hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__>), g, b, 0, s, a, keep, vt, tt)
   if (dt == MUON_BF16) {
     if (tile == 256) LOGITS(u16, 256, 5, false);
@@ -796,7 +800,7 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
   // the longer tiles go first
   const int wf = cdiv(rows, unit) > cdiv(a.v, unit) / a.split;
   const int64_t tiles = ((int64_t)tt * a.split + vt) * nd;
-  const dim3 g(xcd_grid(tiles + 1)), b(tile * 2);
+  const dim3 g(xcd_grid(tiles + 1)), b(dt == MUON_BF16 ? tile * 2 : 256);
   const bool deep = tile == 64 && tiles <= kDeepTiles;
 #define GRADIENTS(T, ...) hipLaunchKernelGGL((k_gradients_mfma<T, __VA_ARGS__>), g, b, 0, s, a, vt, tt, nd, wf)
   if (dt == MUON_BF16) {

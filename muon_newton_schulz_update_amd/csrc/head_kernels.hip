@@ -328,7 +328,7 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
 // columns past the vocabulary (a stage of dH) become zero. Bound by HBM: a
 // read and a write of every exponential. With few tiles (merged = 0) every
 // block merges its tokens' statistics itself, which costs less than a kernel.
-constexpr int kFuseTiles = 32;
+constexpr int kFuseTiles = 64;
 template <typename T>
 __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int block_chunks) {
   constexpr int CH = 16 / (int)sizeof(T);
