@@ -327,12 +327,20 @@ __device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, c
   wait_vm<0>();
 }
 
-// Tile order: blocks b, b + 8, ... run on one XCD; each XCD takes runs of 32
-// consecutive tiles, and tiles go down strips of SM rows, so a run shares SM
-// row panels and about 32 / SM column panels in that XCD's L2.
-__device__ __forceinline__ int xcd_index(int b) {
-  const int j = b >> 3;
-  return ((j >> 5) * 8 + (b & 7)) * 32 + (j & 31);
+// Tile order: blocks b, b + 8, ... run on one XCD; each XCD takes runs of at
+// most 32 consecutive tiles, and tiles go down strips of SM rows, so a run
+// shares SM row panels and about 32 / SM column panels in that XCD's L2. The
+// runs are as long as gives every XCD as many where there are few: in runs of
+// 32, 300 tiles would be 64 for one XCD and 32 for another (one token x 50304 x
+// 768 27.9 / 25.7 us; fp32 777 x 8191 x 331 with gradients 161 / 155).
+constexpr int kEvenRounds = 6;
+__host__ __device__ inline int rounds_of(int n) { return n > 256 ? (n + 255) / 256 : 1; }
+__host__ __device__ inline int run_of(int n, int rounds) {
+  return rounds > kEvenRounds ? 32 : n > 0 ? (n + 8 * rounds - 1) / (8 * rounds) : 1;
+}
+__device__ __forceinline__ int xcd_index(int b, int n) {
+  const int run = run_of(n, rounds_of(n)), j = b >> 3;
+  return (j / run * 8 + (b & 7)) * run + j % run;
 }
 template <int SM>
 __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, int& c) {
@@ -362,7 +370,8 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
   int vi, ti;
   const int rows = piece_rows(a), lane = threadIdx.x & 63;
-  if (!strip_tile<4>(xcd_index(blockIdx.x), vt, min(tt, (rows + TILE - 1) / TILE), vi, ti)) return;
+  const int nt = min(tt, (rows + TILE - 1) / TILE);
+  if (!strip_tile<4>(xcd_index(blockIdx.x, vt * nt), vt, nt, vi, ti)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   const int v0 = vi * TILE, r0 = ti * TILE;
   typedef Op<T, OP_ROW_K, TILE, NW> A;
@@ -708,22 +717,32 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
 
 // Both gradients in one launch: they need only dz, and the tiles of one fill
 // the CUs that the last round of the other's leaves idle (the 50304 x 768
-// weight's 591 tiles are 2.3 rounds of the 256 CUs).
+// weight's 591 tiles are 2.3 rounds of the 256 CUs). The kind with the longer
+// tiles comes first. In few rounds each kind is dealt to the XCDs by itself,
+// the first to the blocks below `first`; in many (first = 0) one follows the
+// other, which leaves the runs whole (8192 x 50304 x 2048: 3.73 / 3.82 ms).
 template <typename T, int TILE, int S>
 __global__ __launch_bounds__((waves_of<T, TILE>() * 64), S > 5 ? 1 : 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
-                                                                                  int weight_first) {
+                                                                                  int weight_first, int first) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
   const int rows = piece_rows(a);
   const int nt = min(tt, (rows + TILE - 1) / TILE), n_h = nt * nd * a.split, n_w = vt * nd;
-  int idx = xcd_index(blockIdx.x);
-  if (idx >= n_h + n_w) {
-    if (idx == n_h + n_w && a.last && !a.per_token) total_loss<waves_of<T, TILE>() * 64>(a, (double*)smem);
-    return;
+  const int n_first = weight_first ? n_w : n_h, n_second = n_h + n_w - n_first;
+  int idx;
+  bool in_first = (int)blockIdx.x < first;
+  if (in_first) {
+    idx = xcd_index(blockIdx.x, n_first);
+    if (idx >= n_first) return;
+  } else {
+    const int before = first ? 0 : n_first, n = before + n_second;
+    idx = xcd_index(blockIdx.x - first, n + 1);     // (the last item is the sum of the losses)
+    if (idx == n && a.last && !a.per_token) total_loss<waves_of<T, TILE>() * 64>(a, (double*)smem);
+    if (idx >= n) return;
+    in_first = idx < before;
+    if (!in_first) idx -= before;
   }
-  const int first = weight_first ? n_w : n_h;
-  const bool in_first = idx < first;
-  if (!in_first) idx -= first;
-  if (in_first == (weight_first != 0)) {
+  const bool weight = in_first == (weight_first != 0);
+  if (weight) {
     int vi, di;
     if (strip_tile<8>(idx, vt, nd, vi, di)) dweight_tile<T, TILE, S>(a, smem, vi, di, rows);
   } else {
@@ -733,8 +752,9 @@ __global__ __launch_bounds__((waves_of<T, TILE>() * 64), S > 5 ? 1 : 2) void k_g
 }
 
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-// blocks for n tiles dealt to the XCDs in runs of 32 (xcd_index)
-inline int xcd_grid(int64_t n) { return n > 0 ? cdiv(n, 256) * 256 : 256; }
+// blocks for up to n tiles dealt to the XCDs (xcd_index; a launch with fewer
+// tiles never needs more)
+inline int xcd_grid(int n) { return 8 * rounds_of(n) * run_of(n, rounds_of(n)); }
 
 // Tile edge of a launch, from its number of 256-tiles: with few of them
 // 128-tiles, four times as many and two to a CU, cover the CUs better, and
@@ -776,7 +796,7 @@ int grad_tile_of(int dt, int rows, int dp, int64_t tiles256, int64_t tiles128) {
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
   const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
   const bool deep = tile == 64 && (int64_t)vt * tt <= kDeepTiles, few = a.n <= 32;
-  const dim3 g(xcd_grid((int64_t)vt * tt)), b(dt != MUON_BF16 && tile == 64 && !few ? 256 : tile * 2);
+  const dim3 g(xcd_grid(vt * tt)), b(dt != MUON_BF16 && tile == 64 && !few ? 256 : tile * 2);
 #define LOGITS(T, ...) hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__>), g, b, 0, s, a, keep, vt, tt)
   if (dt == MUON_BF16) {
     if (tile == 256) LOGITS(u16, 256, 5, false);
@@ -799,10 +819,11 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
   const int tt = a.dh ? cdiv(rows, tile) : 0, vt = a.dw ? cdiv(a.v, tile) : 0, nd = cdiv(a.dp, tile);
   // the longer tiles go first
   const int wf = cdiv(rows, unit) > cdiv(a.v, unit) / a.split;
-  const int64_t tiles = ((int64_t)tt * a.split + vt) * nd;
-  const dim3 g(xcd_grid(tiles + 1)), b(dt == MUON_BF16 ? tile * 2 : 256);
+  const int n_h = tt * nd * a.split, n_w = vt * nd, tiles = n_h + n_w, n_first = wf ? n_w : n_h;
+  const int first = rounds_of(tiles) > kEvenRounds || n_first == 0 ? 0 : xcd_grid(n_first);
+  const dim3 g(first + xcd_grid(tiles + 1 - (first ? n_first : 0))), b(dt == MUON_BF16 ? tile * 2 : 256);
   const bool deep = tile == 64 && tiles <= kDeepTiles;
-#define GRADIENTS(T, ...) hipLaunchKernelGGL((k_gradients_mfma<T, __VA_ARGS__>), g, b, 0, s, a, vt, tt, nd, wf)
+#define GRADIENTS(T, ...) hipLaunchKernelGGL((k_gradients_mfma<T, __VA_ARGS__>), g, b, 0, s, a, vt, tt, nd, wf, first)
   if (dt == MUON_BF16) {
     if (tile == 256) GRADIENTS(u16, 256, 5);
     else if (tile == 128) GRADIENTS(u16, 128, 5);
