@@ -34,6 +34,8 @@
 #include <stdint.h>
 
 #include "head_device.hpp"
+#include <algorithm>
+
 #include "train.hpp"
 
 namespace muon {
@@ -604,7 +606,7 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 // row) and leave as 16-byte stores.
 // ---------------------------------------------------------------------------
 template <typename T, int TILE, int S>
-__device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, int vi, int di, int rows) {
+__device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, int vi, int di, int part, int rows) {
   constexpr int NW = waves_of<T, TILE>(), MI = TILE / 64, NI = NW * 32 > TILE ? 1 : 2, WN = NW / 2;   // waves: 2 x WN
   const int lane = threadIdx.x & 63, lr = lane & 31, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -623,8 +625,9 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   const int nk = (rows + O::KE - 1) / O::KE;
-  if (nk > 0)
-    k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, NW, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0, nk);
+  const int k0 = (int)((int64_t)nk * part / a.wsplit), k1 = (int)((int64_t)nk * (part + 1) / a.wsplit);
+  if (k1 > k0)
+    k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, NW, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, k0, k1);
   const float g = common_factor(a);
   const int vw = v0 + wn * NI * 32, dw = d0 + wm * MI * 32;      // the wave's part
   if constexpr (sizeof(T) == 2 && TILE < 256) {
@@ -655,9 +658,10 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
       }
     }
   }
-  if (a.dwacc) {
-    // sums over pieces: padded rows, whole 16-byte groups
-    float* acc_at = a.dwacc + (int64_t)(vw + lr) * a.dp + dw + 4 * hf;
+  const bool split = a.wsplit > 1;
+  if (split || a.dwacc) {
+    // sums over parts or pieces: padded rows, whole 16-byte groups
+    float* acc_at = (split ? a.wpart + (int64_t)part * a.v * a.dp : a.dwacc) + (int64_t)(vw + lr) * a.dp + dw + 4 * hf;
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) {
       if (vw + ni * 32 + lr >= a.v) continue;
@@ -668,14 +672,14 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
         for (int q = 0; q < 4; ++q) {
           f32x4_t* p = (f32x4_t*)(acc_at + (int64_t)ni * 32 * a.dp + mi * 32 + 8 * q);
           f32x4_t x = {acc[mi][ni][4 * q], acc[mi][ni][4 * q + 1], acc[mi][ni][4 * q + 2], acc[mi][ni][4 * q + 3]};
-          if (!a.first) x += *p;
-          if (!a.last) *p = x;
+          if (!split && !a.first) x += *p;
+          if (split || !a.last) *p = x;
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[mi][ni][4 * q + e] = x[e];
         }
       }
     }
-    if (!a.last) return;
+    if (split || !a.last) return;
   }
   constexpr int NC = MI * 2 * (int)sizeof(T);               // chunks of the wave's row
   if (nk > 0) ring_barrier();                               // every wave is done with the slots
@@ -726,7 +730,7 @@ __global__ __launch_bounds__((waves_of<T, TILE>() * 64), S > 5 ? 1 : 2) void k_g
                                                                                   int weight_first, int first) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
   const int rows = piece_rows(a);
-  const int nt = min(tt, (rows + TILE - 1) / TILE), n_h = nt * nd * a.split, n_w = vt * nd;
+  const int nt = min(tt, (rows + TILE - 1) / TILE), n_h = nt * nd * a.split, n_w = vt * nd * a.wsplit;
   const int n_first = weight_first ? n_w : n_h, n_second = n_h + n_w - n_first;
   int idx;
   bool in_first = (int)blockIdx.x < first;
@@ -743,8 +747,9 @@ __global__ __launch_bounds__((waves_of<T, TILE>() * 64), S > 5 ? 1 : 2) void k_g
   }
   const bool weight = in_first == (weight_first != 0);
   if (weight) {
+    const int q = idx / (vt * nd);
     int vi, di;
-    if (strip_tile<8>(idx, vt, nd, vi, di)) dweight_tile<T, TILE, S>(a, smem, vi, di, rows);
+    if (strip_tile<8>(idx - q * vt * nd, vt, nd, vi, di)) dweight_tile<T, TILE, S>(a, smem, vi, di, q, rows);
   } else {
     const int q = idx / (nt * nd), t = idx - q * nt * nd;
     dhidden_tile<T, TILE, S>(a, smem, t / nd, t % nd, q, rows);
@@ -818,8 +823,8 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
   const int rows = a.rows_max, unit = dt == MUON_BF16 ? 64 : 32, tile = a.grad_tile;
   const int tt = a.dh ? cdiv(rows, tile) : 0, vt = a.dw ? cdiv(a.v, tile) : 0, nd = cdiv(a.dp, tile);
   // the longer tiles go first
-  const int wf = cdiv(rows, unit) > cdiv(a.v, unit) / a.split;
-  const int n_h = tt * nd * a.split, n_w = vt * nd, tiles = n_h + n_w, n_first = wf ? n_w : n_h;
+  const int wf = cdiv(rows, unit) / a.wsplit > cdiv(a.v, unit) / a.split;
+  const int n_h = tt * nd * a.split, n_w = vt * nd * a.wsplit, tiles = n_h + n_w, n_first = wf ? n_w : n_h;
   const int first = rounds_of(tiles) > kEvenRounds || n_first == 0 ? 0 : xcd_grid(n_first);
   const dim3 g(first + xcd_grid(tiles + 1 - (first ? n_first : 0))), b(dt == MUON_BF16 ? tile * 2 : 256);
   const bool deep = tile == 64 && tiles <= kDeepTiles;
@@ -837,41 +842,57 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tile edges of the products, columns per statistic, and splits of the
-// vocabulary in dH, whose tiles alone (tokens x width) are fewer than the CUs
-// for one piece of a narrow model. The gradients' launch lasts its stages over
-// the CUs, each tile with the ring's start-up (about six stages), half of its
-// shortest tile at the end, and the traffic of the partial sums (a 256-tile's
-// stage takes about 2 us, as long as 9 MB of HBM; a smaller one's half, on a
-// part of a CU).
+// Tile edges of the products, columns per statistic, and the parts in which dH
+// goes over the vocabulary and dW over the piece's tokens: the tiles alone
+// (tokens x width, vocabulary x width) can be fewer than the CUs. The
+// gradients' launch lasts its stages over the CUs, each tile with the ring's
+// start-up, half of its shorter kind at the end, and no less than its longest
+// tile; then the partial sums' traffic and the launch that adds them. Counted
+// in stages, whose length, as start-up and traffic, follows from the tile and
+// type (a least-squares choice over 300 shapes of 64 to 16384 tokens: calls
+// within 0.3 % (256), 1.1 % (128), 0.6 % (64) and 1.7 % (fp32) of the best
+// parts). dW's parts measured (1 / chosen): 16384 x 6000 x 256 350 / 324 us,
+// 65536 x 256 x 512 646 / 250, fp32 2000 x 300 x 128 78 / 37.
 void head_plan(HeadArgs& a, int dt) {
   const int rows = a.n < a.piece ? a.n : a.piece, unit = dt == MUON_BF16 ? 64 : 32;
   a.logit_tile = tile_of(dt, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256), (int64_t)cdiv(a.v, 128) * cdiv(rows, 128));
   a.vtile = a.logit_tile == 64 ? 64 : 128;
   a.n_vt = cdiv(a.v, a.vtile);
-  a.split = 1;
+  a.split = a.wsplit = 1;
   if (!a.dh && !a.dw) return;
-  const int64_t stages = cdiv(a.v, unit);
+  const int64_t stages = cdiv(a.v, unit), wstages = cdiv(rows, unit);
   auto tiles_of = [&](int edge) {
     return (a.dw ? (int64_t)cdiv(a.v, edge) * cdiv(a.dp, edge) : 0) +
            (a.dh ? (int64_t)cdiv(rows, edge) * cdiv(a.dp, edge) * (stages / 64 + 1) : 0);
   };
   a.grad_tile = grad_tile_of(dt, rows, a.dp, tiles_of(256), tiles_of(128));
-  if (!a.dh) return;
   const int tile = a.grad_tile, slots = 256 * (256 / tile);
-  const int64_t tiles = (int64_t)cdiv(rows, tile) * cdiv(a.dp, tile);
-  const double other = a.dw ? (double)cdiv(a.v, tile) * cdiv(a.dp, tile) * (cdiv(rows, unit) + 6) : 0.0;
-  const double sum = (double)rows * a.dp * 8 / (tile == 256 ? 9e6 : 4.5e6);
+  const int64_t h_tiles = a.dh ? (int64_t)cdiv(rows, tile) * cdiv(a.dp, tile) : 0;
+  const int64_t w_tiles = a.dw ? (int64_t)cdiv(a.v, tile) * cdiv(a.dp, tile) : 0;
+  // start-up, the sums' launch, and bytes of traffic in a stage's time (2 us of
+  // a 256-tile, 0.7, 1, and 1.8 of fp32)
+  const bool half = dt == MUON_BF16;
+  const double start = half && tile == 64 ? 10 : 6, launch = half ? (tile == 256 ? 3 : 4) : 2;
+  const double bytes = !half ? 8e6 : tile == 256 ? 9e6 : tile == 128 ? 1.6e6 : 4.5e6;
+  const double h_sum = (double)rows * a.dp * 8 / bytes, w_sum = (double)a.v * a.dp * 8 / bytes;
+  // (partial sums stay within 256 MB, and a part has four stages or more)
+  const int h_most = a.dh ? (int)std::min<double>(std::min<int64_t>(256, stages / 4), 256e6 / ((double)a.piece * a.dp * 4)) : 1;
+  const int w_most = a.dw && a.n > kFewTokens ? (int)std::min<double>(std::min<int64_t>(256, wstages / 4), 256e6 / ((double)a.v * a.dp * 4)) : 1;
   double least = 0;
-  // (the partial sums stay within 256 MB)
-  for (int n = 1; n <= 256 && (n == 1 || (stages / n >= 4 && (double)n * a.piece * a.dp * 4 <= 256e6)); ++n) {
-    const double each = (double)cdiv(stages, n) + 6, t0 = (tiles * n * each + other) / slots + each / 2;
-    // more than one split: the sum is a launch of its own, about 5 us
-    const double t = (t0 > each ? t0 : each) + (n > 1 ? n * sum + (tile == 256 ? 3 : 5) : 0);
-    if (n == 1 || t < least) {
-      least = t;
-      a.split = n;
+  for (int m = 1; m == 1 || m <= w_most; m *= 2) {
+    for (int n = 1; n == 1 || n <= h_most; n += (n + 7) / 8) {
+      const double h_each = a.dh ? cdiv(stages, n) + start : 0, w_each = a.dw ? cdiv(wstages, m) + start : 0;
+      const double shorter = !a.dh ? w_each : !a.dw ? h_each : std::min(h_each, w_each);
+      double t = std::max((h_tiles * n * h_each + w_tiles * m * w_each) / slots + shorter / 2, std::max(h_each, w_each));
+      t += (n > 1 ? n * h_sum : 0) + (m > 1 ? m * w_sum : 0) + (n > 1 || m > 1 ? launch : 0);
+      // (more parts of dW for a gain that the model can tell)
+      if ((n == 1 && m == 1) || t < (m > a.wsplit ? 0.95 : 1.0) * least) {
+        least = t;
+        a.split = n;
+        a.wsplit = m;
+      }
     }
+    if (2.0 * (cdiv(wstages, m) + start) < least) break;     // dW's tiles are not what it waits for
   }
 }
 

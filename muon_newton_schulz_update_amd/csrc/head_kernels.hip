@@ -76,9 +76,8 @@ __host__ __device__ inline bool total_in_merge(const HeadArgs& a) {
 // ---------------------------------------------------------------------------
 // Compaction of the valid tokens. Up to kPackScan tokens every pack block
 // scans the targets itself (a kernel of its own costs about 5 us more; for
-// 8192 tokens the scans would take 27 us longer than the rows, that kernel 10);
-// longer lists are scanned by one block beforehand, 8192 tokens at a time. A thread takes eight
-// neighbouring tokens. A per-token loss of an ignored token is 0.
+// 8192 tokens the scans would take 27 us longer than the rows, that kernel 5);
+// longer lists are scanned by one block beforehand, 8192 tokens at a time. A per-token loss of an ignored token is 0.
 // ---------------------------------------------------------------------------
 constexpr int kPackScan = 2048;
 
@@ -107,14 +106,31 @@ __device__ __forceinline__ int scan_targets(const void* targets, int bytes, int6
     if (lane == 0) counts[e * W + w] = __popcll(m);
   }
   __syncthreads();
-  int all = 0;
+  // every wave scans the 8 W counts by itself, PER neighbours to a lane (a
+  // serial sum of them took 4 us of 9.5 for 8192 tokens)
+  constexpr int PER = 8 * W > 64 ? 8 * W / 64 : 1;
+  int c[PER], own = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
+  for (int j = 0; j < PER; ++j) {
+    c[j] = lane * PER + j < 8 * W ? counts[lane * PER + j] : 0;
+    own += c[j];
+  }
+  int upto = own;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      if (k == w && at[e] >= 0) at[e] += all;
-      all += counts[e * W + k];
-    }
+  for (int o = 1; o < 64; o *= 2) {
+    const int x = __shfl_up(upto, o);
+    if (lane >= o) upto += x;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int k = __builtin_amdgcn_readfirstlane(e * W + w), from = k / PER;
+    int before = __builtin_amdgcn_readlane(upto - own, from);
+#pragma unroll
+    for (int j = 0; j + 1 < PER; ++j)
+      if (j < k % PER) before += __builtin_amdgcn_readlane(c[j], from);
+    if (at[e] >= 0) at[e] += before;
+  }
+  const int all = __builtin_amdgcn_readlane(upto, 63);
   __syncthreads();
   return all;
 }
@@ -418,60 +434,99 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int blo
   }
 }
 
-// Sums of the splits to the tokens' rows, and, with the first piece, zeros to
-// the ignored tokens' rows: one block per row of the piece, then one per token.
+// Four results, scaled and rounded: one store, aligned or not, or the `left`
+// columns of a row's end.
 template <typename T>
-__global__ __launch_bounds__(256) void k_dhidden_out(HeadArgs a) {
-  T* dh = (T*)a.dh;
-  if ((int)blockIdx.x >= a.rows_max * (a.split > 1)) {
-    const int64_t i = (int)blockIdx.x - a.rows_max * (a.split > 1);
-    if (target_at(a.targets, a.target_bytes, i) != a.ignore) return;
-    for (int c = threadIdx.x; c < a.d; c += 256) dh[i * a.ld_dh + c] = T(0);
-    return;
+__device__ __forceinline__ void store4(T* dst, f32x4_t x, float g, int left) {
+  if (left >= 4) {
+    if constexpr (sizeof(T) == 2) {
+      const u32x2_t y = {pack_bf16(x[0] * g, x[1] * g), pack_bf16(x[2] * g, x[3] * g)};
+      __builtin_memcpy(dst, &y, 8);
+    } else {
+      const f32x4_t y = x * g;
+      __builtin_memcpy(dst, &y, 16);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) dst[e] = to<T>(x[e] * g);
   }
-  const int rows = piece_rows(a), r = blockIdx.x;
-  if (r >= rows) return;
-  const int64_t token = a.idx[a.row0 + r];
-  const float g = common_factor(a), rest = a.rs[r].w;
-  const T* target_row = (const T*)a.w + (int64_t)max(a.tgt[a.row0 + r], 0) * a.ld_w;   // (rest is 0 without a target)
-  // a narrow row leaves threads to share the splits; the parts are added in order
-  const int groups = (a.d + 3) / 4, width = groups > 128 ? 256 : groups > 64 ? 128 : groups > 32 ? 64 : 32;
-  const int parts = 256 / width, part = threadIdx.x / width;
-  __shared__ f32x4_t sh[256];
-  for (int c0 = 0; c0 < a.d; c0 += 4 * width) {
-    const int c = c0 + ((int)threadIdx.x % width) * 4;
-    f32x4_t x = {0.f, 0.f, 0.f, 0.f};
-    if (c < a.d) {
+}
+// threads that share the parts of one sum
+__host__ __device__ inline int share_of(int parts) { return parts >= 32 ? 8 : parts >= 16 ? 4 : parts >= 8 ? 2 : 1; }
+
+// One group of four columns of a sum of `parts` partial sums, `all` groups
+// apart: this thread's share, then the shares of the block joined in order.
+// Only the first share's threads return true.
+__device__ __forceinline__ bool sum_parts(const float* part, int parts, int64_t at, int64_t all, int64_t stride, f32x4_t* sh,
+                                          f32x4_t& x) {
+  const int shares = share_of(parts), width = 256 / shares, share = threadIdx.x / width;
+  x = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  if (at < all) {
 #pragma unroll 8
-      for (int q = part; q < a.split; q += parts) x += *(const f32x4_t*)(a.part + ((int64_t)q * a.piece + r) * a.dp + c);
-    }
-    if (parts > 1) {
-      sh[threadIdx.x] = x;
-      __syncthreads();
-      if (part == 0)
-        for (int p = 1; p < parts; ++p) x += sh[p * width + threadIdx.x];
-      __syncthreads();
-    }
-    if (part != 0 || c >= a.d) continue;
-    if (rest != 0.f)
+    for (int q = share; q < parts; q += shares) x += *(const f32x4_t*)(part + (q * stride + at) * 4);
+  }
+  if (shares > 1) {
+    sh[threadIdx.x] = x;
+    __syncthreads();
+    if (share == 0)
+      for (int p = 1; p < shares; ++p) x += sh[p * width + threadIdx.x];
+  }
+  return share == 0 && at < all;
+}
+
+// The gradients' last steps, three kinds of blocks: sums of dH's parts to the
+// tokens' rows (a thread has four columns), zeros to the ignored tokens' rows
+// with the first piece (a wave has kZeroTokens tokens), sums of dW's parts and
+// of the pieces before.
+constexpr int kZeroTokens = 16;
+template <typename T>
+__global__ __launch_bounds__(256) void k_gradients_out(HeadArgs a, int sums, int zeros) {
+  __shared__ f32x4_t sh[256];
+  const int groups = a.dp / 4, lane = threadIdx.x & 63;
+  int block = blockIdx.x;
+  f32x4_t x;
+  if (block < sums) {
+    const int width = 256 / share_of(a.split);
+    const int64_t at = (int64_t)block * width + threadIdx.x % width;
+    if (!sum_parts(a.part, a.split, at, (int64_t)piece_rows(a) * groups, (int64_t)a.piece * groups, sh, x)) return;
+    const int r = (int)(at / groups), c = (int)(at - (int64_t)r * groups) * 4;
+    if (c >= a.d) return;
+    const float rest = a.rs[r].w;
+    if (rest != 0.f) {
+      const T* target_row = (const T*)a.w + (int64_t)a.tgt[a.row0 + r] * a.ld_w;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (c + e < a.d) x[e] = fmaf(rest, ld<T>(target_row, c + e), x[e]);
-    T* dst = dh + token * a.ld_dh + c;
-    if (c + 4 <= a.d) {                    // (one store, aligned or not)
-      if constexpr (sizeof(T) == 2) {
-        const u32x2_t y = {pack_bf16(x[0] * g, x[1] * g), pack_bf16(x[2] * g, x[3] * g)};
-        __builtin_memcpy(dst, &y, 8);
-      } else {
-        const f32x4_t y = x * g;
-        __builtin_memcpy(dst, &y, 16);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (c + e < a.d) dst[e] = to<T>(x[e] * g);
+    }
+    store4((T*)a.dh + (int64_t)a.idx[a.row0 + r] * a.ld_dh + c, x, common_factor(a), a.d - c);
+    return;
+  }
+  block -= sums;
+  if (block < zeros) {
+    const int64_t t0 = ((int64_t)block * 4 + (threadIdx.x >> 6)) * kZeroTokens;
+    const bool mine = lane < kZeroTokens && t0 + lane < a.n && target_at(a.targets, a.target_bytes, t0 + lane) == a.ignore;
+    for (uint64_t todo = __ballot(mine); todo; todo &= todo - 1) {
+      T* row = (T*)a.dh + (t0 + __builtin_ctzll(todo)) * a.ld_dh;
+      for (int c = lane; c < a.d; c += 64) row[c] = T(0);
+    }
+    return;
+  }
+  block -= zeros;
+  const int width = 256 / share_of(a.wsplit);
+  const int64_t at = (int64_t)block * width + threadIdx.x % width, all = (int64_t)a.v * groups;
+  if (!sum_parts(a.wpart, a.wsplit, at, all, all, sh, x)) return;
+  const int row = (int)(at / groups), c = (int)(at - (int64_t)row * groups) * 4;
+  if (c >= a.d) return;
+  if (a.dwacc) {
+    f32x4_t* p = (f32x4_t*)(a.dwacc + at * 4);
+    if (!a.first) x += *p;
+    if (!a.last) {
+      *p = x;
+      return;
     }
   }
+  store4((T*)a.dw + (int64_t)row * a.ld_dw + c, x, common_factor(a), a.d - c);
 }
 
 inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
@@ -511,10 +566,13 @@ hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s) {
   const int per = (int64_t)cdiv(chunks, 64) * panels(a) < 1024 ? 16 : 64;
   BY_TYPE(dt, k_dlogits, dim3(panels(a), cdiv(chunks, per)), dim3(256), 0, s, a, (int)(a.n_vt > kFuseTiles), per);
 }
-hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, hipStream_t s) {
-  const int blocks = a.rows_max * (a.split > 1) + (a.row0 == 0 ? a.n : 0);
-  if (blocks == 0) return hipSuccess;
-  BY_TYPE(dt, k_dhidden_out, dim3(blocks), dim3(256), 0, s, a);
+hipError_t launch_head_gradients_out(const HeadArgs& a, int dt, hipStream_t s) {
+  auto blocks = [&](int64_t rows, int parts) { return (int)cdiv(rows * (a.dp / 4), 256 / share_of(parts)); };
+  const int sums = a.dh && a.split > 1 ? blocks(a.rows_max, a.split) : 0;
+  const int zeros = a.dh && a.row0 == 0 ? (int)cdiv(a.n, 4 * kZeroTokens) : 0;
+  const int weight = a.wsplit > 1 ? blocks(a.v, a.wsplit) : 0;
+  if (sums + zeros + weight == 0) return hipSuccess;
+  BY_TYPE(dt, k_gradients_out, dim3(sums + zeros + weight), dim3(256), 0, s, a, sums, zeros);
 }
 
 }  // namespace muon

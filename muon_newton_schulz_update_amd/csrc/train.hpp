@@ -141,6 +141,8 @@ struct HeadArgs {
   float4* rs;                         // piece: {reference, factor, target's gradient, what its rounding lost}
   float* part;                        // dH partial sums: split x piece x dp
   int32_t split;                      // parts of the vocabulary in dH
+  float* wpart;                       // dW partial sums: wsplit x v x dp
+  int32_t wsplit;                     // parts of the piece's tokens in dW
   int32_t logit_tile, grad_tile;      // tile edges of the products
   float* dwacc;                       // v x dp fp32 sum over pieces, or null: one piece
   int32_t first, last;                // this piece starts / ends the sum over pieces
@@ -157,6 +159,6 @@ hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s);
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s);
 hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s);   // dh and dw, each if not null
-hipError_t launch_head_dhidden_out(const HeadArgs& a, int dt, hipStream_t s);
+hipError_t launch_head_gradients_out(const HeadArgs& a, int dt, hipStream_t s);
 
 }  // namespace muon

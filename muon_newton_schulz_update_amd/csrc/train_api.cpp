@@ -180,6 +180,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const size_t o_zt = take(p * 4), o_rs = take(p * 16);
   const size_t o_w = direct ? 0 : take((size_t)a.v * a.dp * e);
   const size_t o_e = grad ? take(p * a.vp * e) : 0, o_part = a.split > 1 ? take(p * a.dp * 4 * a.split) : 0;
+  const size_t o_wpart = a.wsplit > 1 ? take((size_t)a.v * a.dp * 4 * a.wsplit) : 0;
   const bool acc = dw && pieces > 1;
   const size_t o_acc = acc ? take((size_t)a.v * a.dp * 4) : 0;
   if (muon_status st = grow(h, ts.head, at, "cross entropy")) return st;
@@ -195,6 +196,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.rs = (float4*)(b + o_rs);
   a.e = b + o_e;
   a.part = (float*)(b + o_part);
+  a.wpart = (float*)(b + o_wpart);
   a.dwacc = acc ? (float*)(b + o_acc) : nullptr;
   a.w = wgt.ptr;
   a.ld_w = wgt.rows == 1 ? a.d : wgt.ld;
@@ -216,9 +218,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
     if (!grad) continue;
     HIP_DO(h, launch_head_dlogits(a, dt, s));
     HIP_DO(h, launch_head_gradients(a, dt, s));
-    if (dh) {
-      HIP_DO(h, launch_head_dhidden_out(a, dt, s));
-    }
+    HIP_DO(h, launch_head_gradients_out(a, dt, s));
   }
   return MUON_OK;
 }

@@ -237,6 +237,14 @@ def test_cross_entropy_in_pieces(n, v, d, dtype):
     check_loss(*make(n, v, d, dtype, seed=21, ignored=0.2), reduction="sum")
 
 
+@pytest.mark.parametrize("n,v,d,dtype", [
+    (1500, 300, 72, BF), (1500, 300, 72, F32), (2100, 257, 33, F32), (5000, 200, 64, BF), (70000, 200, 32, BF),
+    (66000, 210, 40, F32)])
+def test_cross_entropy_of_many_tokens_and_a_small_weight(n, v, d, dtype):
+    """The weight's gradient is summed over the tokens in parts (past 65536 tokens in pieces too)."""
+    check_loss(*make(n, v, d, dtype, seed=24, ignored=0.2))
+
+
 def test_cross_entropy_repeats_bit_for_bit_and_on_other_streams():
     h, w, t = make(700, 3001, 192, BF, seed=22, ignored=0.1)
     first = mu.linear_cross_entropy_grad(h, w, t)
