@@ -93,11 +93,12 @@ muon_status norm_run(muon_handle* h, int n, const muon_matrix* g, float max_norm
 
 muon_status scale_run(muon_handle* h, int n, const muon_matrix* src, const muon_matrix* dst, const float* coef) {
   const hipStream_t s = handle_stream(h);
-  for (int i = 0; i < n;) {
+  // from the last tensor's end to the first's start (k_scale says why)
+  for (int i = n - 1; i >= 0;) {
     ScaleList L;
     L.n = 0;
     int64_t c = 0;
-    for (; i < n && L.n < kScaleMax; ++i) {
+    for (; i >= 0 && L.n < kScaleMax; --i) {
       if (empty(src[i])) continue;
       const muon_matrix& d = dst ? dst[i] : src[i];
       const int64_t e = src[i].rows * src[i].cols, k = cdiv(e, kChunk);
