@@ -1,17 +1,16 @@
 // Matrix-core products of the head's cross entropy.
 //
 //   logits    z^T = W H^T       vocabulary x tokens, K = width
-//   dhidden   dH  = dz W        tokens x width,      K = vocabulary (split)
-//   dweight   dW  = dz^T H      vocabulary x width,  K = tokens
+//   dhidden   dH  = dz W        tokens x width,      K = vocabulary (in parts)
+//   dweight   dW  = dz^T H      vocabulary x width,  K = tokens (in parts)
 //
-// One kernel shape for the three: a 256 x 256 tile per workgroup of 8 waves
-// (or 128 x 128 of 4 and 64 x 64 of 2, two and four workgroups to a CU, where
-// tiles are few),
-// K in stages of 128 bytes (64 bf16, 32 fp32), both operands of a stage
-// brought to LDS by direct buffer loads into a ring of five slots (nine in
-// small launches of 64-tiles), so that while one stage feeds the matrix cores
-// the next and half of the one after (three and a half) are on their way. bf16 runs v_mfma_f32_32x32x16_bf16, fp32
-// v_mfma_f32_32x32x2f32.
+// One kernel shape for the three: a 256 x 256 tile per workgroup of 8 waves, or
+// 128 x 128 of 4 and 64 x 64 of 2, two and four workgroups to a CU, where tiles
+// are few (fp32: 64 x 64 of 4); K in stages of 128 bytes (64 bf16, 32 fp32),
+// both operands of a stage brought to LDS by direct buffer loads into a ring of
+// five slots (nine in small launches of 64-tiles), so that while one stage feeds
+// the matrix cores the next and half of the one after (three and a half) are on
+// their way. bf16 runs v_mfma_f32_32x32x16_bf16, fp32 v_mfma_f32_32x32x2f32.
 //
 // Neither the weight nor the per-piece matrices are ever transposed in
 // memory: an operand whose tile rows are the contraction index is read from
@@ -33,9 +32,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "head_device.hpp"
 #include <algorithm>
 
+#include "head_device.hpp"
 #include "train.hpp"
 
 namespace muon {
@@ -53,7 +52,6 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 
 enum OpLayout { OP_ROW_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
-enum Product { P_LOGITS, P_DHIDDEN, P_DWEIGHT };
 
 constexpr int kFewTokens = 64;    // whose dW takes the targets' remainders too
 constexpr float kLog2e = 1.44269504088896341f;
@@ -106,12 +104,12 @@ struct Operand {
 };
 
 // Tile edges: 256 (8 waves, one workgroup per CU), 128 (4 waves, two) and 64
-// (2 waves, or 4 for fp32, whose products take sixteen times as long a stage;
-// four workgroups, or two with the long ring). A stage of an operand is
+// (2 waves, or 4 for fp32, whose products take sixteen times as long; four
+// workgroups, or two with the long ring). A stage of an operand is
 // TILE x 128 bytes, TILE / 8 loads of 1 KB shared by the NW waves.
 template <typename T, int TILE>
 constexpr int waves_of() {
-  return TILE == 64 && sizeof(T) == 4 ? 4 : TILE / 32;
+  return sizeof(T) == 4 ? 4 : TILE / 32;
 }
 template <typename T, int L, int TILE, int NW = waves_of<T, TILE>()>
 struct Op {
@@ -221,7 +219,7 @@ __device__ __forceinline__ void k_loop(f32x16_t (&acc)[MI][NI], uint8_t* smem, c
   constexpr int kReadStep = MI * A::kReads + NI * B::kReads;
   static_assert(S >= 5 && S % 2 == 1 && (S - 4) * LPO < 64, "slots");
   Frag fa[2][MI], fb[2][NI];
-  // operand stage o: A (o even) or B (o odd) of stage k0 + o / 2, slot o % 5
+  // operand stage o: A (o even) or B (o odd) of stage k0 + o / 2, slot o % S
   auto issue = [&](int slot, int o, int i0, int i1) {
     const int ks = min(k0 + (o >> 1), k1 - 1);
 #pragma unroll
@@ -355,10 +353,21 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 
 // ---------------------------------------------------------------------------
 // Logits. The vocabulary is on the accumulators' rows and the tokens on their
-// columns, so a lane holds 64 logits of each of its two tokens (32 of one in the
-// smallest tiles): maximum and sum need one exchange with the other half-wave.
-// The statistics are per wave's vocabulary rows, so waves never wait for one another. The
-// exponentials go to the panels as whole chunks after a half-wave swap.
+// columns, so a lane holds 64 logits of each of its two tokens (32 or 16 of one
+// in the smallest tiles): maximum and sum need one exchange with the other
+// half-wave. The statistics are per wave's vocabulary rows, so bf16's waves
+// never wait for one another. The exponentials go to the panels as whole chunks
+// after a half-wave swap.
+//
+// Bound by the matrix cores in large calls, whose clock falls under the load
+// (busy 55 % of the time at 1.8 GHz, the rest the epilogue: as many
+// exponentials as results, and 2 bytes of each kept), by the weight's one read
+// for few tokens. Measured: 8192 x 50304 x 768 with the exponentials kept
+// 665 us (950 TFLOP/s and 1.2 TB/s), 6963 x 50304 x 2048 with a soft cap 1210
+// (1190), 1536 x 50304 x 768 without 133 (890); one token x 50304 x 768 16.5
+// (4.7 TB/s); fp32 1987 x 30961 x 704 680 (127).
+// Two workgroups of 256 x 128 to a CU, so that one's epilogue runs beside the
+// other's products, took 13 % longer (more operand traffic from LDS).
 // ---------------------------------------------------------------------------
 template <typename T, int TILE, int S, bool FEW>
 __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
@@ -366,7 +375,7 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
   // 64-tile. PAIR: 32 x 32 of one, and two waves put their statistics together:
   // fp32, four waves, or (FEW: at most 32 tokens) two on the first 32 tokens
   constexpr int NW = FEW ? 2 : waves_of<T, TILE>();
-  constexpr bool PAIR = TILE == 64 && sizeof(T) == 4;
+  constexpr bool PAIR = sizeof(T) == 4;
   constexpr int MI = PAIR ? 1 : TILE == 64 ? 2 : 4, NI = TILE == 256 ? 2 : 1;
   constexpr int WM = TILE / (MI * 32), WN = NW / WM;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
@@ -504,7 +513,8 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
 }
 
 // ---------------------------------------------------------------------------
-// dH: partial sums over a range of the vocabulary, 32-bit, row-major.
+// dH: partial sums over a range of the vocabulary, 32-bit, row-major; one
+// range alone writes the tokens' rows itself.
 // ---------------------------------------------------------------------------
 template <typename T, int TILE, int S>
 __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, int ti, int di, int q, int rows) {
@@ -599,8 +609,8 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 }
 
 // ---------------------------------------------------------------------------
-// dW: the piece's sum, added to the pieces before it; the last one is scaled
-// and rounded to the weight's type. The width is on the accumulators' rows, so
+// dW: the piece's sum, or a part of its tokens', added to the pieces before
+// it; the last one is scaled and rounded to the weight's type. The width is on the accumulators' rows, so
 // a lane has four neighbouring columns of one weight row; the results are put
 // together to whole rows of the wave's part in the idle LDS (chunks swizzled by
 // row) and leave as 16-byte stores.
@@ -725,6 +735,10 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
 // tiles comes first. In few rounds each kind is dealt to the XCDs by itself,
 // the first to the blocks below `first`; in many (first = 0) one follows the
 // other, which leaves the runs whole (8192 x 50304 x 2048: 3.73 / 3.82 ms).
+// Bound by the matrix cores at the clock that their power leaves (busy 85 % of
+// the time at 1.4 to 1.6 GHz). Measured: 8192 x 50304 x 768 1020 us (1240
+// TFLOP/s of both products), 6963 x 50304 x 2048 2220 (1290), 16 x 3200 x 256
+// 5.5; fp32 777 x 8191 x 331 92 (83).
 template <typename T, int TILE, int S>
 __global__ __launch_bounds__((waves_of<T, TILE>() * 64), S > 5 ? 1 : 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
                                                                                   int weight_first, int first) {
@@ -771,15 +785,17 @@ inline int xcd_grid(int n) { return 8 * rounds_of(n) * run_of(n, rounds_of(n)); 
 //   39.2 / 34.0, 471 23.6 / 21.5; gradients without the loss: 350 32.7 / 33.7,
 //   410 60.5 / 57.8, 2358 65 / 55
 // fp32's matrix instructions are slow enough to hide the operand traffic of
-// 64-tiles (loss alone 64 / 128: 252 tiles 46.7 / 48.3, 628 67.0 / 64.4), and
-// its gradients always take those (634 tiles 440 / 465).
+// 64-tiles, which it always takes (loss alone, 64 / 128: 777 x 8191 x 331 64 /
+// 66 us, 300 x 50304 x 768 211 / 247, 1987 x 30961 x 704 686 / 685, 4000 x 3000
+// x 1024 215 / 211; 256-tiles would not fit the registers).
 constexpr int kFewTiles = 768, kFewSmallTiles = 384;
 // 64-tiles that all fit the chip two to a CU: a ring of nine slots, whose loads
 // are asked for three and a half stages ahead. Such a launch reads its operands
 // for the first time, and a stage waits for memory rather than for its products.
 constexpr int kDeepTiles = 512;
 int tile_of(int dt, int64_t tiles256, int64_t tiles128) {
-  if (dt == MUON_BF16 && tiles256 >= kFewTiles) return 256;
+  if (dt != MUON_BF16) return 64;
+  if (tiles256 >= kFewTiles) return 256;
   return tiles128 >= kFewSmallTiles ? 128 : 64;
 }
 // The gradients' tiles also go by their own shape (whole calls):
@@ -801,7 +817,7 @@ int grad_tile_of(int dt, int rows, int dp, int64_t tiles256, int64_t tiles128) {
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
   const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
   const bool deep = tile == 64 && (int64_t)vt * tt <= kDeepTiles, few = a.n <= 32;
-  const dim3 g(xcd_grid(vt * tt)), b(dt != MUON_BF16 && tile == 64 && !few ? 256 : tile * 2);
+  const dim3 g(xcd_grid(vt * tt)), b(dt != MUON_BF16 && !few ? 256 : tile * 2);
 #define LOGITS(T, ...) hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__>), g, b, 0, s, a, keep, vt, tt)
   if (dt == MUON_BF16) {
     if (tile == 256) LOGITS(u16, 256, 5, false);
@@ -809,8 +825,7 @@ hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s
     else if (deep) LOGITS(u16, 64, 9, false);
     else LOGITS(u16, 64, 5, false);
   } else {
-    if (tile == 128) LOGITS(float, 128, 5, false);
-    else if (deep && few) LOGITS(float, 64, 9, true);
+    if (deep && few) LOGITS(float, 64, 9, true);
     else if (deep) LOGITS(float, 64, 9, false);
     else if (few) LOGITS(float, 64, 5, true);
     else LOGITS(float, 64, 5, false);

@@ -17,15 +17,17 @@
 //   dlogits    p - [v = t] (times the token's own factor) in the operands' type,
 //              over the exponentials; a factor common to all tokens waits for
 //              the 32-bit sums
-//   dhidden    dz W, split over the vocabulary where tiles are few, then a
-//              sum of the splits written to the tokens' rows, with what the
+//   dhidden    dz W, in parts of the vocabulary where tiles are few, then a
+//              sum of the parts written to the tokens' rows, with what the
 //              target's own gradient lost in its rounding to 16 bits times the
 //              target's row: that one term is most of a token's gradient
-//   dweight    dz^T H, summed over pieces in 32 bits; with few tokens, whose
-//              roundings no sum averages, also those remainders
+//   dweight    dz^T H, in parts of the tokens where tiles are few, summed over
+//              parts and pieces in 32 bits; with few tokens, whose roundings no
+//              sum averages, also those remainders
 //
-// The products are in head_gemm.hip. A 16-bit exponential carries an eighth of the rounding of the bf16 value it
-// becomes, so the gradient's one rounding is the one to bf16.
+// The products are in head_gemm.hip. A 16-bit exponential carries an eighth of
+// the rounding of the bf16 value it becomes, so the gradient's one rounding is
+// the one to bf16.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -77,7 +79,8 @@ __host__ __device__ inline bool total_in_merge(const HeadArgs& a) {
 // Compaction of the valid tokens. Up to kPackScan tokens every pack block
 // scans the targets itself (a kernel of its own costs about 5 us more; for
 // 8192 tokens the scans would take 27 us longer than the rows, that kernel 5);
-// longer lists are scanned by one block beforehand, 8192 tokens at a time. A per-token loss of an ignored token is 0.
+// longer lists are scanned by one block beforehand, 8192 tokens at a time (6 us,
+// 16384 tokens 11, bound by latency). A per-token loss of an ignored token is 0.
 // ---------------------------------------------------------------------------
 constexpr int kPackScan = 2048;
 
@@ -194,6 +197,7 @@ __device__ __forceinline__ void pack_weight(const HeadArgs& a, int r0) {
 // Gathered rows to panels: a wave takes 8 rows x 8 chunks at a time, so that
 // it reads and writes whole 128-byte lines; rows past the valid ones, up to a
 // whole panel (a stage of dW), become zero. One block per 64 rows and 8 chunks.
+// Bound by the two trips to memory (8192 x 768: 25 MB in 8 us).
 template <typename T>
 __global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan, int row_blocks) {
   constexpr int CH = 16 / (int)sizeof(T);
@@ -240,6 +244,7 @@ __global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan, int row_bloc
   }
 }
 
+// Bound by latency: 8192 tokens of 393 tiles (26 MB) 12 us.
 // 64 tokens per block, 16 threads per token: each goes over every sixteenth
 // tile with a running reference and sum, then the first adds the sixteen in
 // order. (One thread per token, two dependent loads a tile, took 190 us for
@@ -342,7 +347,8 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
 // keeps its token and goes over chunks, so a wave's accesses are whole
 // kilobytes. Rows past the valid ones (up to a whole panel, a stage of dW) and
 // columns past the vocabulary (a stage of dH) become zero. Bound by HBM: a
-// read and a write of every exponential. With few tiles (merged = 0) every
+// read and a write of every exponential (8192 x 50304 in 16 bits 318 us, 5.2
+// TB/s). With few tiles (merged = 0) every
 // block merges its tokens' statistics itself, which costs less than a kernel.
 constexpr int kFuseTiles = 64;
 template <typename T>
@@ -478,7 +484,7 @@ __device__ __forceinline__ bool sum_parts(const float* part, int parts, int64_t 
 // The gradients' last steps, three kinds of blocks: sums of dH's parts to the
 // tokens' rows (a thread has four columns), zeros to the ignored tokens' rows
 // with the first piece (a wave has kZeroTokens tokens), sums of dW's parts and
-// of the pieces before.
+// of the pieces before. Bound by HBM: 8192 x 768 with 50304 rows of weight 22 us.
 constexpr int kZeroTokens = 16;
 template <typename T>
 __global__ __launch_bounds__(256) void k_gradients_out(HeadArgs a, int sums, int zeros) {
