@@ -490,7 +490,7 @@ muon_status adamw_update(muon_handle* handle, int n, const muon_matrix* grad, co
  *            them may be NULL (its product is left out)
  * BF16 inputs are multiplied on the bf16 matrix cores (the logits' gradient
  * is rounded to bf16 once), F32 ones in fp32 throughout; statistics and sums
- * are fp32. The handle keeps up to about 1.3 GiB for the pieces of tokens (256
+ * are fp32. The handle keeps up to about 1.6 GiB for the pieces of tokens (256
  * at least), plus, when a call takes more than one piece, an fp32 V x D sum,
  * and a padded copy of a weight whose rows are not whole 16-byte pieces that
  * start on 16 bytes.
