@@ -7,6 +7,12 @@
 
 namespace muon {
 
+__device__ __forceinline__ int64_t target_at(const void* targets, int bytes, int64_t i) {
+  return bytes == 8 ? ((const int64_t*)targets)[i] : (int64_t)((const int32_t*)targets)[i];
+}
+// A target as the products take it, -1 outside the vocabulary.
+__device__ __forceinline__ int checked_target(const HeadArgs& a, int64_t g) { return g >= 0 && g < a.v ? (int)g : -1; }
+
 // Valid tokens of the piece.
 __device__ __forceinline__ int piece_rows(const HeadArgs& a) { return min(max(a.count[0] - a.row0, 0), a.piece); }
 

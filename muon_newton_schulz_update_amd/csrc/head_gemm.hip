@@ -19,6 +19,7 @@
 // (fp32). LDS layouts, in 16-byte chunks, and their bank swizzles:
 //   OP_ROW_K    row-major matrix, K along the row: [256 rows][8 chunks],
 //               chunk ^ (row / 2) % 8
+//   OP_GATHER_K the same of rows in any order
 //   OP_ROW_T    row-major matrix, K down the rows: [K rows][columns],
 //               bf16: chunk ^ (row % 4) 4 (64-tiles: chunk ^ (row / 2 % 2) 4)
 //   OP_PANEL_K  panels (train.hpp), K along the chunks: [4 token blocks]
@@ -51,7 +52,7 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 
-enum OpLayout { OP_ROW_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
+enum OpLayout { OP_ROW_K, OP_GATHER_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
 
 constexpr int kFewTokens = 64;    // whose dW takes the targets' remainders too
 constexpr float kLog2e = 1.44269504088896341f;
@@ -101,6 +102,7 @@ struct Operand {
   int lim;               // last valid row (row layouts), last valid chunk (OP_PANEL_T)
   int row_bytes;         // OP_ROW_K: bytes of a row; what a stage has past them is zero
   uint32_t lane;         // this lane's byte offset, the same in every stage
+  uint32_t row[4];       // OP_GATHER_K: the offset of this lane's row in each of its loads
 };
 
 // Tile edges: 256 (8 waves, one workgroup per CU), 128 (4 waves, two) and 64
@@ -121,7 +123,7 @@ struct Op {
   __device__ static int row_t_swizzle(int row) { return kRowT == 128 ? (row & 2) << 1 : (row & 3) << 2; }
   // the lane's part of a load's address (row layouts: the column part)
   __device__ static uint32_t lane_part(int lane, int wave, int last_chunk) {
-    if constexpr (L == OP_ROW_K) {
+    if constexpr (L == OP_ROW_K || L == OP_GATHER_K) {
       const int row = 8 * wave + (lane >> 3);
       return ((lane & 7) ^ ((row >> 1) & 7)) * 16;
     } else if constexpr (L == OP_ROW_T) {
@@ -139,12 +141,12 @@ struct Op {
     const uint8_t* p = o.base;
     uint32_t voff = o.lane, soff = 0;
     const int g = NW * i + wave;
-    if constexpr (L == OP_ROW_K) {
+    if constexpr (L == OP_ROW_K || L == OP_GATHER_K) {
       p += (int64_t)ks * 128;
       // past the row's end the offset is out of the buffer's range, and such
       // lanes load zeros
       const bool past = (int)o.lane >= o.row_bytes - ks * 128;
-      voff += __umul24(min(8 * g + (lane >> 3), o.lim), o.pitch);
+      voff += L == OP_ROW_K ? __umul24(min(8 * g + (lane >> 3), o.lim), o.pitch) : o.row[i];
       voff = past ? 0x80000000u : voff;
     } else if constexpr (L == OP_ROW_T) {
       p += (int64_t)ks * KE * o.pitch;
@@ -163,16 +165,16 @@ struct Op {
         soff = min(2 * g, o.lim - 1) * 1024;
       }
     }
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, L == OP_ROW_K ? 0x7FFFFFF0 : -1, 0x00020000);
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, L == OP_ROW_K || L == OP_GATHER_K ? 0x7FFFFFF0 : -1, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(sm + g * 1024), 16, voff, soff, 0, 0);
   }
-  static constexpr int kReads = L == OP_ROW_K || L == OP_PANEL_K ? 1 : sizeof(T) == 2 ? 2 : 4;   // LDS reads a fragment
+  static constexpr int kReads = L == OP_ROW_K || L == OP_GATHER_K || L == OP_PANEL_K ? 1 : sizeof(T) == 2 ? 2 : 4;   // LDS reads a fragment
   // fragment of rows (columns) at..at+31 for k-step s: lane l holds index
   // at + l % 32 and the k of chunk 2 s + l / 32
   template <typename F>
   __device__ static __forceinline__ F frag(const uint8_t* sm, int lane, int at, int s) {
     const int lr = lane & 31, hf = lane >> 5;
-    if constexpr (L == OP_ROW_K) {
+    if constexpr (L == OP_ROW_K || L == OP_GATHER_K) {
       return *(const F*)(sm + (at + lr) * 128 + (((2 * s + hf) ^ ((lr >> 1) & 7)) * 16));
     } else if constexpr (L == OP_PANEL_K) {
       return *(const F*)(sm + ((at >> 6) * 8 + 2 * s + hf) * 1024 + ((at & 63) + lr) * 16);
@@ -369,7 +371,7 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 // Two workgroups of 256 x 128 to a CU, so that one's epilogue runs beside the
 // other's products, took 13 % longer (more operand traffic from LDS).
 // ---------------------------------------------------------------------------
-template <typename T, int TILE, int S, bool FEW>
+template <typename T, int TILE, int S, bool FEW, bool GATHER>
 __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
   // a wave: 128 vocabulary rows x 64 tokens (256-tiles) or 32, 64 x 32 of a
   // 64-tile. PAIR: 32 x 32 of one, and two waves put their statistics together:
@@ -380,24 +382,57 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
   constexpr int WM = TILE / (MI * 32), WN = NW / WM;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * TILE * 128];
   int vi, ti;
-  const int rows = piece_rows(a), lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63;
+  int rows, token = 0, target = 0;
+  if constexpr (GATHER) {
+    // at most 64 tokens: every wave lists the valid ones itself, lane r the
+    // r-th; the first block writes the list for the statistics' merge (with
+    // rows packed by a launch before this one: one token x 50304 x 768 24.9 us
+    // a call instead of 21.2, 16 x 3200 x 256 14.2 instead of 10.4)
+    const int64_t g = lane < a.n ? target_at(a.targets, a.target_bytes, lane) : a.ignore;
+    const bool valid = g != a.ignore;
+    const uint64_t mask = __ballot(valid), below = (1ull << lane) - 1;
+    rows = __popcll(mask);
+    const int to = 4 * (valid ? __popcll(mask & below) : rows + __popcll(~mask & below));
+    token = __builtin_amdgcn_ds_permute(to, lane);
+    target = __builtin_amdgcn_ds_permute(to, checked_target(a, g));
+    if (blockIdx.x == 0 && threadIdx.x < 64) {
+      if (lane < rows) {
+        a.idx[lane] = token;
+        a.tgt[lane] = target;
+      }
+      if (a.per_token && !valid && lane < a.n) a.loss[lane] = 0.f;
+      if (lane == 0) a.count[0] = rows;
+    }
+  } else {
+    rows = piece_rows(a);
+  }
   const int nt = min(tt, (rows + TILE - 1) / TILE);
   if (!strip_tile<4>(xcd_index(blockIdx.x, vt * nt), vt, nt, vi, ti)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   const int v0 = vi * TILE, r0 = ti * TILE;
   typedef Op<T, OP_ROW_K, TILE, NW> A;
-  typedef Op<T, OP_PANEL_K, TILE, NW> B;
+  constexpr int LB = GATHER ? OP_GATHER_K : OP_PANEL_K;
+  typedef Op<T, LB, TILE, NW> B;
   const Operand oa = {(const uint8_t*)a.w + (int64_t)v0 * a.ld_w * sizeof(T), (uint32_t)(a.ld_w * sizeof(T)),
                       a.v - 1 - v0, a.w_cols * (int)sizeof(T), A::lane_part(lane, wave, 0)};
   const uint32_t blk = (uint32_t)a.dp * sizeof(T) * kPanelRows;
-  const Operand ob = {(const uint8_t*)a.hp + (int64_t)ti * (TILE / 64) * blk, blk, 0, 0, B::lane_part(lane, wave, 0)};
+  Operand ob = {(const uint8_t*)a.hp + (int64_t)ti * (TILE / 64) * blk, blk, 0, 0, B::lane_part(lane, wave, 0)};
+  if constexpr (GATHER) {
+    ob.base = (const uint8_t*)a.h;
+    ob.row_bytes = a.d * (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < TILE / 8 / NW; ++i) {
+      const int r = min(8 * (NW * i + wave) + (lane >> 3), rows - 1);   // (r0 is 0)
+      ob.row[i] = (uint32_t)__shfl(token, r) * (uint32_t)(a.ld_h * sizeof(T));
+    }
+  }
   f32x16_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
-  k_loop<T, OP_ROW_K, OP_PANEL_K, TILE, NW, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0,
-                                                a.dp / A::KE);
+  k_loop<T, OP_ROW_K, LB, TILE, NW, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, 0, a.dp / A::KE);
 
   const int lr = lane & 31, hf = lane >> 5;
   const int vw = v0 + wm * MI * 32;                  // the wave's first vocabulary row
@@ -429,8 +464,9 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
     const int r = r0 + (wn * NI + ni) * 32 + lr;       // the lane's token in the piece
+    const int listed = GATHER ? __shfl(target, r & 63) : 0;
     // the target's logit leaves the tile: it has its own place in the sums
-    const int tg = (r < rows ? a.tgt[a.row0 + r] : -1) - vw - 4 * hf;
+    const int tg = (r >= rows ? -1 : GATHER ? listed : a.tgt[a.row0 + r]) - vw - 4 * hf;
     const bool mine = tg >= 0 && tg < MI * 32 && (tg & 4) == 0;
     if (__any(mine)) {
       float z = 0.f;
@@ -818,9 +854,13 @@ hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s
   const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
   const bool deep = tile == 64 && (int64_t)vt * tt <= kDeepTiles, few = a.n <= 32;
   const dim3 g(xcd_grid(vt * tt)), b(dt != MUON_BF16 && !few ? 256 : tile * 2);
-#define LOGITS(T, ...) hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__>), g, b, 0, s, a, keep, vt, tt)
+#define LOGITS(T, ...)                                                                                   \
+  do {                                                                                                   \
+    if (a.gather) hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__, true>), g, b, 0, s, a, keep, vt, tt); \
+    else hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__, false>), g, b, 0, s, a, keep, vt, tt);        \
+  } while (0)
   if (dt == MUON_BF16) {
-    if (tile == 256) LOGITS(u16, 256, 5, false);
+    if (tile == 256) hipLaunchKernelGGL((k_logits_mfma<u16, 256, 5, false, false>), g, b, 0, s, a, keep, vt, tt);
     else if (tile == 128) LOGITS(u16, 128, 5, false);
     else if (deep) LOGITS(u16, 64, 9, false);
     else LOGITS(u16, 64, 5, false);

@@ -3,7 +3,9 @@
 //
 //   compact    the valid tokens (target != ignore_index) in order; ignored
 //              ones are never read, so what their rows hold does not matter
-//   pack       the piece's hidden rows, gathered, zero-padded, in panels
+//   pack       the piece's hidden rows, gathered, zero-padded, in panels (not
+//              for the loss alone of up to 64 tokens: the logits' launch lists
+//              them and reads their rows itself)
 //   logits     z by tiles; per token and tile an integer reference
 //              K >= log2(e) max z and the sum of 2^(log2(e) z - K) over the
 //              tile without the target's term; with gradients also the
@@ -84,10 +86,6 @@ __host__ __device__ inline bool total_in_merge(const HeadArgs& a) {
 // ---------------------------------------------------------------------------
 constexpr int kPackScan = 2048;
 
-__device__ __forceinline__ int64_t target_at(const void* targets, int bytes, int64_t i) {
-  return bytes == 8 ? ((const int64_t*)targets)[i] : (int64_t)((const int32_t*)targets)[i];
-}
-
 // Scans tokens [i0, i0 + 8 THREADS): thread t has tokens i0 + e THREADS + t,
 // their targets g[e] and, where valid, their places at[e] among the valid ones
 // (-1 elsewhere); returns how many there are. Loads and, through the places,
@@ -137,8 +135,6 @@ __device__ __forceinline__ int scan_targets(const void* targets, int bytes, int6
   __syncthreads();
   return all;
 }
-
-__device__ __forceinline__ int checked_target(const HeadArgs& a, int64_t g) { return g >= 0 && g < a.v ? (int)g : -1; }
 
 __global__ __launch_bounds__(1024) void k_compact(HeadArgs a) {
   __shared__ int counts[8 * 16];
@@ -557,6 +553,7 @@ hipError_t launch_head_compact(const HeadArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s) {
+  if (a.gather) return hipSuccess;
   const int scan = pack_scans(a), rows = (int)panels(a);
   const int weight = a.w_src && a.row0 == 0 ? (int)cdiv(a.v, kPanelRows) : 0;
   BY_TYPE(dt, k_pack, dim3(rows + weight, a.dp / (dt == MUON_BF16 ? 64 : 32)), dim3(256), 0, s, a, scan, rows);

@@ -144,6 +144,7 @@ struct HeadArgs {
   float* wpart;                       // dW partial sums: wsplit x v x dp
   int32_t wsplit;                     // parts of the piece's tokens in dW
   int32_t logit_tile, grad_tile;      // tile edges of the products
+  int32_t gather;                     // the logits read the hidden rows themselves
   float* dwacc;                       // v x dp fp32 sum over pieces, or null: one piece
   int32_t first, last;                // this piece starts / ends the sum over pieces
   float* loss;                        // caller's: one value, or n

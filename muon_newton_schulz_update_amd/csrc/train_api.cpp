@@ -122,6 +122,7 @@ muon_status scale_run(muon_handle* h, int n, const muon_matrix* src, const muon_
 // kPieceRows tokens, whatever the vocabulary).
 constexpr size_t kHeadBytes = size_t(1) << 30;
 constexpr int kPieceRows = 256;
+constexpr int kGatherTokens = 64;       // tokens that one wave can list
 constexpr int64_t kPieceMost = 65536;   // keeps a launch's tiles far from 2^31
 
 muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& wgt, const void* targets,
@@ -169,6 +170,10 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const int64_t pieces = std::max<int64_t>(1, cdiv(a.n, most));
   a.piece = (int)(std::max<int64_t>(1, cdiv(cdiv(a.n, pieces), kPieceRows)) * kPieceRows);
   head_plan(a, dt);
+  // few tokens without gradients, whose rows the products can load as they are:
+  // no panels
+  a.gather = !grad && direct && a.n > 0 && a.n <= kGatherTokens && a.logit_tile < 256 && (uintptr_t)hid.ptr % 16 == 0 &&
+             (a.n == 1 || (hid.ld * e % 16 == 0 && hid.ld * e < (1 << 23)));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;

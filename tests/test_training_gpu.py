@@ -245,6 +245,28 @@ def test_cross_entropy_of_many_tokens_and_a_small_weight(n, v, d, dtype):
     check_loss(*make(n, v, d, dtype, seed=24, ignored=0.2))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n,v,d,ignored", [(1, 700, 64, 0.0), (2, 257, 72, 0.5), (31, 5000, 768, 0.3), (33, 300, 200, 0.6),
+                                           (63, 30000, 128, 0.4), (64, 50304, 768, 0.2), (64, 1000, 40, 0.0),
+                                           (65, 1000, 40, 0.3)])
+def test_cross_entropy_of_few_tokens(n, v, d, ignored, dtype):
+    """The loss alone of up to 64 tokens reads their rows in place: those of a wider buffer too, never the ignored ones."""
+    h, w, t = make(n, v, d, dtype, seed=25, ignored=ignored)
+    check_loss(h, w, t, reduction="none")
+    wide = torch.full((n, d + 24), float("nan"), device="cuda", dtype=dtype)
+    wide[:, 8:8 + d] = h
+    wide[t == -100] = float("nan")
+    for reduction in ("none", "mean"):
+        want = mu.linear_cross_entropy(h, w, t, reduction=reduction)
+        assert torch.equal(mu.linear_cross_entropy(wide[:, 8:8 + d], w, t, reduction=reduction), want)
+        assert torch.equal(mu.linear_cross_entropy(h, w, t.int(), reduction=reduction), want)
+    none = torch.full_like(t, -100)
+    assert mu.linear_cross_entropy(wide[:, 8:8 + d], w, none).item() == 0.0
+    assert not mu.linear_cross_entropy(wide[:, 8:8 + d], w, none, reduction="none").any()
+    t[0] = v                       # outside the vocabulary
+    assert bool(mu.linear_cross_entropy(h, w, t, reduction="none")[0].isnan())
+
+
 def test_cross_entropy_repeats_bit_for_bit_and_on_other_streams():
     h, w, t = make(700, 3001, 192, BF, seed=22, ignored=0.1)
     first = mu.linear_cross_entropy_grad(h, w, t)
