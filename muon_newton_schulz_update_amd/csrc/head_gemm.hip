@@ -362,7 +362,7 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 // after a half-wave swap.
 //
 // Bound by the matrix cores in large calls, whose clock falls under the load
-// (busy 55 % of the time at 1.8 GHz, the rest the epilogue: as many
+// (busy 56 % of the time at 1.6 to 1.8 GHz, the rest the epilogue: as many
 // exponentials as results, and 2 bytes of each kept), by the weight's one read
 // for few tokens. Measured: 8192 x 50304 x 768 with the exponentials kept
 // 665 us (950 TFLOP/s and 1.2 TB/s), 6963 x 50304 x 2048 with a soft cap 1210
