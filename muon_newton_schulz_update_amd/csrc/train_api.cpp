@@ -130,7 +130,6 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
                      const muon_matrix* dh, const muon_matrix* dw) {
   TrainState& ts = train_state(h);
   const hipStream_t s = handle_stream(h);
-  const bool grad = dh || dw;
   const int dt = wgt.dtype, e = esz(dt);
   HeadArgs a{};
   a.n = (int)hid.rows;
@@ -150,14 +149,17 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.ld_h = hid.ld;
   a.loss = loss;
   a.grad_out = grad_out;
-  if (dh) {
+  // (a gradient without elements is none: with no tokens and no dweight only
+  // the loss is left)
+  if (dh && !empty(*dh)) {
     a.dh = dh->ptr;
     a.ld_dh = dh->ld;
   }
-  if (dw) {
+  if (dw && !empty(*dw)) {
     a.dw = dw->ptr;
     a.ld_dw = dw->ld;
   }
+  const bool grad = a.dh || a.dw;
   // the weight as it is, where its rows are whole 16-byte pieces on 16 bytes;
   // otherwise a padded copy (the pitch also fits the products' 24-bit multiply)
   const bool direct = a.d * e % 16 == 0 && (uintptr_t)wgt.ptr % 16 == 0 &&
@@ -187,7 +189,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const size_t o_w = direct ? 0 : take((size_t)a.v * a.dp * e);
   const size_t o_e = grad ? take(p * a.vp * e) : 0, o_part = a.split > 1 ? take(p * a.dp * 4 * a.split) : 0;
   const size_t o_wpart = a.wsplit > 1 ? take((size_t)a.v * a.dp * 4 * a.wsplit) : 0;
-  const bool acc = dw && pieces > 1;
+  const bool acc = a.dw && pieces > 1;
   const size_t o_acc = acc ? take((size_t)a.v * a.dp * 4) : 0;
   if (muon_status st = grow(h, ts.head, at, "cross entropy")) return st;
   uint8_t* b = (uint8_t*)ts.head.ptr;

@@ -174,6 +174,23 @@ def test_cross_entropy_no_tokens(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
+def test_cross_entropy_no_tokens_and_one_gradient(dtype, reduction):
+    """An empty batch whose only gradient has no elements (a frozen head), or only the weight's."""
+    h, w, t = torch.empty((0, 64), device="cuda", dtype=dtype), normal((300, 64), 1).to(dtype), torch.empty(
+        0, device="cuda", dtype=torch.int64)
+    shape = (0,) if reduction == "none" else ()
+    for got in (mu.linear_cross_entropy(h, w, t, reduction=reduction),
+                mu.linear_cross_entropy_grad(h, w, t, reduction=reduction, dweight=False)[0],
+                mu.linear_cross_entropy_grad(h, w, t, reduction=reduction, dhidden=False)[0]):
+        assert got.shape == shape and not bool(got.any())
+    assert not bool(mu.linear_cross_entropy_grad(h, w, t, reduction=reduction, dhidden=False)[2].any())
+    loss = mu.linear_cross_entropy(h.requires_grad_(), w, t, reduction=reduction)
+    loss.sum().backward()
+    assert loss.shape == shape and h.grad.shape == (0, 64)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("n,v,d,pad,shift", [(70, 333, 64, 8, 0), (70, 333, 64, 3, 0), (130, 257, 128, 5, 1), (9, 600, 40, 1, 3)])
 def test_cross_entropy_strides_and_alignment(dtype, n, v, d, pad, shift):
     """Rows inside wider buffers, starts off 16 bytes, NaN all around."""
