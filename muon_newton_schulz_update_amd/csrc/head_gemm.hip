@@ -95,6 +95,21 @@ __device__ __forceinline__ s16x4_t read_tr16(lds_s16x4_t* __restrict p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
 }
 
+// c tanh(z / c) to within about 10 units of 2^-24 of the result, whatever the
+// cap: with x = |z / c| below 0.75 tanh is Lambert's continued fraction x / (1 +
+// x^2 / (3 + x^2 / (5 + x^2 / (7 + x^2 / 9)))) put over one denominator (off by
+// 6e-9 there), from there on (1 - e) / (1 + e) with e = exp(-2 x), and below
+// 2^-13 tanh x is x to 32 bits (its next term is x^3 / 3). A form that takes a
+// small logit from the difference of two numbers near c, such as c - 2 c /
+// (exp(2 x) + 1), is off by c 2^-23 instead. One reciprocal serves both forms.
+__device__ __forceinline__ float capped(float z, float c, float inv) {
+  const float x = fabsf(z * inv), q = x * x, e = __builtin_amdgcn_exp2f(x * (-2.f * kLog2e));
+  const bool low = x < 0.75f;
+  const float num = low ? x * fmaf(q, q + 105.f, 945.f) : 1.f - e;
+  const float den = low ? fmaf(q, fmaf(q, 15.f, 420.f), 945.f) : 1.f + e;
+  return x < 0x1p-13f ? z : copysignf(c * (num * __builtin_amdgcn_rcpf(den)), z);
+}
+
 // One operand of a tile's product.
 struct Operand {
   const uint8_t* base;   // tile start at the first stage
@@ -439,17 +454,12 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
   if (!PAIR && vw >= a.v) return;                    // (the exponentials' padding is cleared with the gradient)
   const int tile = PAIR ? vi : vi * WM + wm;
   if (a.softcap > 0.f) {
-    const float s = 2.f * kLog2e / a.softcap;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          // c tanh(z / c) = c - 2 c / (exp(2 z / c) + 1)
-          const float e = __builtin_amdgcn_exp2f(acc[mi][ni][r] * s);
-          acc[mi][ni][r] = fmaf(-2.f * a.softcap, __builtin_amdgcn_rcpf(e + 1.f), a.softcap);
-        }
+        for (int r = 0; r < 16; ++r) acc[mi][ni][r] = capped(acc[mi][ni][r], a.softcap, a.cap_inv);
   }
   const float none = -__builtin_inff();
   if (vw + MI * 32 > a.v) {

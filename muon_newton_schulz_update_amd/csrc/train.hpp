@@ -127,7 +127,7 @@ struct HeadArgs {
   int32_t per_token;                  // reduction none
   int32_t mean;
   int32_t half;                       // 16-bit inputs
-  float softcap;
+  float softcap, cap_inv;             // soft cap (0: none) and 1 / cap
   // workspace
   int32_t* count;                     // [0] valid tokens
   int32_t* idx;                       // compact -> token

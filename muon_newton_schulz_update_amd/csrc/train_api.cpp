@@ -3,6 +3,7 @@
 // and the head's softmax cross entropy with its gradient. Arguments are
 // validated on the host (validate.cpp) before anything is enqueued; the
 // kernels are in train_kernels.hip and head_kernels.hip.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -142,6 +143,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.mean = cfg.reduction == MUON_REDUCE_MEAN;
   a.half = dt == MUON_BF16;
   a.softcap = cfg.softcap;
+  a.cap_inv = cfg.softcap > 0.f ? std::min(1.f / cfg.softcap, FLT_MAX) : 0.f;   // (of a denormal cap: 0 times it stays 0)
   a.targets = targets;
   a.target_bytes = target_bytes;
   a.ignore = cfg.ignore_index;

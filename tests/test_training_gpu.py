@@ -140,6 +140,26 @@ def test_cross_entropy_options(dtype, reduction, softcap):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("softcap", [1e-40, 0.02, 1.0, 5.0, 30.0, 1e3, 1e5, 1e6, 1e8, 1e30, 3e38])
+@pytest.mark.parametrize("n,v,d", [(1, 3000, 64), (150, 900, 64)])
+def test_cross_entropy_soft_cap_of_any_size(n, v, d, softcap, dtype):
+    """A capped logit is off by the raw one's error and a dozen roundings of itself, not of the cap: one for the
+    product with 1 / cap and for that value, at most four of a quotient's two sides, two of a reciprocal, one of each
+    product after it (and, where exp(-2 x) is taken, x below 1 in it for each rounding of its argument)."""
+    h, w, t = make(n, v, d, dtype, seed=17)
+    raw = mm(h.double(), w.double().t())
+    cap = float(torch.tensor(softcap, dtype=F32))
+    z = cap * torch.tanh(raw / cap)
+    zt = z.gather(1, t[:, None])[:, 0]
+    others = torch.logsumexp((z - zt[:, None]).scatter(1, t[:, None], float("-inf")), 1)
+    want = torch.logaddexp(others, torch.zeros_like(others))
+    dz = (d + 2) * U * mm(h.double().abs(), w.double().abs().t()).amax(1) + 12 * U * z.abs().amax(1)
+    err = 2 * dz + (512 + v / 64) * U + 4 * U * (torch.logsumexp(z, 1).abs() + zt.abs() + z.abs().amax(1))
+    within(mu.linear_cross_entropy(h, w, t, reduction="none", softcap=softcap), want, err, "loss alone")
+    within(mu.linear_cross_entropy_grad(h, w, t, reduction="none", softcap=softcap)[0], want, err, "loss")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("where", ["all", "all but last", "all but first", "blocks"])
 def test_cross_entropy_ignored_rows_are_never_read(dtype, where):
     h, w, t = make(520, 300, 64, dtype, seed=5)
