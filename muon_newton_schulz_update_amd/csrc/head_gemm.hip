@@ -95,19 +95,46 @@ __device__ __forceinline__ s16x4_t read_tr16(lds_s16x4_t* __restrict p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
 }
 
-// c tanh(z / c) to within about 10 units of 2^-24 of the result, whatever the
-// cap: with x = |z / c| below 0.75 tanh is Lambert's continued fraction x / (1 +
-// x^2 / (3 + x^2 / (5 + x^2 / (7 + x^2 / 9)))) put over one denominator (off by
-// 6e-9 there), from there on (1 - e) / (1 + e) with e = exp(-2 x), and below
-// 2^-13 tanh x is x to 32 bits (its next term is x^3 / 3). A form that takes a
-// small logit from the difference of two numbers near c, such as c - 2 c /
-// (exp(2 x) + 1), is off by c 2^-23 instead. One reciprocal serves both forms.
-__device__ __forceinline__ float capped(float z, float c, float inv) {
-  const float x = fabsf(z * inv), q = x * x, e = __builtin_amdgcn_exp2f(x * (-2.f * kLog2e));
-  const bool low = x < 0.75f;
-  const float num = low ? x * fmaf(q, q + 105.f, 945.f) : 1.f - e;
-  const float den = low ? fmaf(q, fmaf(q, 15.f, 420.f), 945.f) : 1.f + e;
-  return x < 0x1p-13f ? z : copysignf(c * (num * __builtin_amdgcn_rcpf(den)), z);
+// The soft cap z = c tanh(y / c) of a raw logit y, to within a dozen roundings of
+// itself whatever the cap, and its slope 1 - tanh^2, to the same of itself. With
+// x = |y / c|: below kCapPoly z = y (1 + q r(q)), q = x^2, where r interpolates
+// (tanh(x) / x - 1) / q at the five Chebyshev nodes of [0, kCapPoly^2] (2 units of
+// 2^-24 at most; exact where q vanishes); from there on tanh is (1 - e) / (1 + e)
+// and the slope 4 e / (1 + e)^2 with e = exp(-2 x). (A small logit taken from the
+// difference of two numbers near c would be off by c 2^-23, and a slope near 0
+// from 1 - tanh^2 by as much as itself: at x = 5 by 7 % from z of 11 bits.)
+constexpr float kCapPoly = 0.625f;
+__device__ __forceinline__ float cap_low(float y, float inv, float& slope) {
+  const float x = y * inv, q = x * x;
+  float p = fmaf(q, -6.09671418e-3f, 2.09971797e-2f);
+  p = fmaf(q, p, -5.38509078e-2f);
+  p = fmaf(q, p, 1.33327693e-1f);
+  p = fmaf(q, p, -3.33333284e-1f);
+  p = fmaf(q, p, 1.f);
+  slope = fmaf(-q * p, p, 1.f);
+  return y * p;
+}
+__device__ __forceinline__ float cap_any(float y, float c, float inv, float& slope) {
+  const float x = fabsf(y * inv), low = cap_low(y, inv, slope);
+  if (x < kCapPoly) return low;                              // (a NaN goes on to the end)
+  const float e = __builtin_amdgcn_exp2f(x * (-2.f * kLog2e)), r = __builtin_amdgcn_rcpf(1.f + e);
+  slope = 4.f * e * r * r;
+  return copysignf(c * ((1.f - e) * r), y);
+}
+// Sixteen of them. Where no lane of the wave has one past kCapPoly, the usual
+// case (18.75 of a cap of 30), there are no exponentials to take: 4096 x 50304 x
+// 768, the loss alone, 377 us, with logits of four times the cap 468.
+__device__ __forceinline__ void cap16(f32x16_t& y, float c, float inv, float (&slope)[16]) {
+  float most = 0.f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) most = fmaxf(most, fabsf(y[q]));
+  if (__any(most * inv >= kCapPoly)) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) y[q] = cap_any(y[q], c, inv, slope[q]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) y[q] = cap_low(y[q], inv, slope[q]);
+  }
 }
 
 // One operand of a tile's product.
@@ -453,23 +480,21 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
   const int vw = v0 + wm * MI * 32;                  // the wave's first vocabulary row
   if (!PAIR && vw >= a.v) return;                    // (the exponentials' padding is cleared with the gradient)
   const int tile = PAIR ? vi : vi * WM + wm;
-  if (a.softcap > 0.f) {
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[mi][ni][r] = capped(acc[mi][ni][r], a.softcap, a.cap_inv);
-  }
   const float none = -__builtin_inff();
-  if (vw + MI * 32 > a.v) {
+  // what takes no part in a token's sum: rows past the vocabulary, its target.
+  // (With a soft cap these are raw logits, capped below, where the slopes are
+  // needed; the cap rises with its logit, so the largest stays the largest.)
+  const bool cap = a.softcap > 0.f, edge = vw + MI * 32 > a.v;
+  auto drop_past = [&](f32x16_t& z, int mi) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (vw + mi * 32 + 8 * (r >> 2) + 4 * hf + (r & 3) >= a.v) z[r] = none;
+  };
+  if (edge) {
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (vw + mi * 32 + 8 * (r >> 2) + 4 * hf + (r & 3) >= a.v)
-#pragma unroll
-          for (int ni = 0; ni < NI; ++ni) acc[mi][ni][r] = none;
+      for (int ni = 0; ni < NI; ++ni) drop_past(acc[mi][ni], mi);
   }
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) {
@@ -478,8 +503,9 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
     // the target's logit leaves the tile: it has its own place in the sums
     const int tg = (r >= rows ? -1 : GATHER ? listed : a.tgt[a.row0 + r]) - vw - 4 * hf;
     const bool mine = tg >= 0 && tg < MI * 32 && (tg & 4) == 0;
-    if (__any(mine)) {
-      float z = 0.f;
+    const bool any_mine = __any(mine);
+    if (any_mine) {
+      float z = 0.f, slope = 1.f;
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
@@ -488,7 +514,9 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
             z = acc[mi][ni][q];
             acc[mi][ni][q] = none;
           }
+      if (cap) z = cap_any(z, a.softcap, a.cap_inv, slope);
       if (mine) a.zt[r] = z;
+      if (mine && cap) a.zf[r] = slope;
     }
     float top = kRefFloor;
 #pragma unroll
@@ -496,6 +524,10 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
 #pragma unroll
       for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
     top = fmaxf(top, __shfl_xor(top, 32));
+    if (cap) {
+      float slope;
+      top = cap_any(top, a.softcap, a.cap_inv, slope);
+    }
     // PAIR: the two waves' rows have one reference and one sum
     float* stat = (float*)smem + wn * 32 + lr;       // [wave row][token], then the second row's sums
     if constexpr (PAIR) {
@@ -509,15 +541,31 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
     float sum = 0.f;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-      float e[16];
+      float e[16], slope[16];
+      f32x16_t z = acc[mi][ni];
+      if (cap) {
+        cap16(z, a.softcap, a.cap_inv, slope);
+        if (edge) drop_past(z, mi);
+        if (any_mine) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            if (mi * 32 + 8 * (q >> 2) + (q & 3) == tg) z[q] = none;
+        }
+      }
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         // no smaller than a kept exponential can say (kCodeBase); a maximum
         // that keeps NaN, so that one bad logit reaches the token's loss
-        e[q] = __builtin_amdgcn_exp2f(__builtin_elementwise_maximum(fmaf(acc[mi][ni][q], kLog2e, -top), -63.f));
+        e[q] = __builtin_amdgcn_exp2f(__builtin_elementwise_maximum(fmaf(z[q], kLog2e, -top), -63.f));
         sum += e[q];
       }
       if (!keep) continue;
+      if (cap) {
+        // what the gradient takes of the logit: its exponential times the slope
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          e[q] = sizeof(T) == 2 ? __builtin_elementwise_maximum(e[q] * slope[q], 0x1p-63f) : e[q] * slope[q];
+      }
       const int64_t col = vw + mi * 32;
       if constexpr (sizeof(T) == 2) {
         // in [2^-63, 1] the pattern's upper two exponent bits say nothing:

@@ -9,8 +9,9 @@
 //   logits     z by tiles; per token and tile an integer reference
 //              K >= log2(e) max z and the sum of 2^(log2(e) z - K) over the
 //              tile without the target's term; with gradients also the
-//              exponentials themselves, in 16 bits (10 bits of mantissa, 6 of
-//              exponent, no sign) or 32
+//              exponentials themselves (times the soft cap's slope at their
+//              logit, where it is still in 32 bits), in 16 bits (10 bits of
+//              mantissa, 6 of exponent, no sign) or 32
 //   merge      per token, over tiles: K = max K_t (differences of integer
 //              references scale exactly), L = sum_t 2^(K_t - K) sum_t, the
 //              target's e = 2^(log2(e) z_t - K), loss = log1p(L / e); the
@@ -283,10 +284,7 @@ __device__ __forceinline__ float4 merge_token(const HeadArgs& a, int grad, int r
     rs.x = t;
     rs.y = (a.grad_out && a.per_token ? a.grad_out[a.idx[a.row0 + r]] : 1.f) / (others + e);
     rs.z = -rs.y * others;
-    if (a.softcap > 0.f) {
-      const float q = z / a.softcap;
-      rs.z *= 1.f - q * q;
-    }
+    if (a.softcap > 0.f) rs.z *= a.zf[r];
     if (a.half) rs.w = rs.z - bf2f(f2bf(rs.z));
   }
   return rs;
@@ -384,15 +382,13 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int blo
   }
   const int last = a.vp / CH, g = gridDim.y - 1 - blockIdx.y, c1 = min((g + 1) * block_chunks, last);
   uint8_t* base = (uint8_t*)a.e + ((int64_t)blockIdx.x * last << 10) + (threadIdx.x & 63) * 16;
-  const float back = a.softcap > 0.f ? kLn2 / a.softcap : 0.f;
 #pragma unroll 4
   for (int c = g * block_chunks + (threadIdx.x >> 6); c < c1; c += 4) {
     uint8_t* p = base + ((int64_t)c << 10);
     const int v = c * CH;
     float x[CH];
     if (real && v < a.v) {
-      const float k = a.tmax[(int64_t)(v / a.vtile) * a.piece + r];
-      const float f = rs.y * exp2f(k - rs.x);
+      const float f = rs.y * exp2f(a.tmax[(int64_t)(v / a.vtile) * a.piece + r] - rs.x);
       if constexpr (sizeof(T) == 2) {
         const u32x4_t q = *(const u32x4_t*)p;
 #pragma unroll
@@ -406,15 +402,7 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int blo
         for (int e = 0; e < 4; ++e) x[e] = q[e];
       }
 #pragma unroll
-      for (int e = 0; e < CH; ++e) {
-        const float ex = x[e];
-        x[e] = ex * f;
-        if (back > 0.f) {
-          // d softcap(z) / dz = 1 - (z / c)^2, z from its exponential
-          const float q = (__log2f(ex) + k) * back;
-          x[e] = ex > 0.f ? x[e] * (1.f - q * q) : 0.f;
-        }
-      }
+      for (int e = 0; e < CH; ++e) x[e] *= f;
       if (v + CH > a.v)
 #pragma unroll
         for (int e = 0; e < CH; ++e)

@@ -187,7 +187,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const size_t n = (size_t)a.n, p = (size_t)a.piece;
   const size_t o_count = take(16), o_idx = take(n * 4), o_tgt = take(n * 4), o_lossc = take(n * 4);
   const size_t o_hp = take(p * a.dp * e), o_tmax = take(p * a.n_vt * 4), o_tsum = take(p * a.n_vt * 4);
-  const size_t o_zt = take(p * 4), o_rs = take(p * 16);
+  const size_t o_zt = take(p * 4), o_zf = take(cfg.softcap > 0.f ? p * 4 : 0), o_rs = take(p * 16);
   const size_t o_w = direct ? 0 : take((size_t)a.v * a.dp * e);
   const size_t o_e = grad ? take(p * a.vp * e) : 0, o_part = a.split > 1 ? take(p * a.dp * 4 * a.split) : 0;
   const size_t o_wpart = a.wsplit > 1 ? take((size_t)a.v * a.dp * 4 * a.wsplit) : 0;
@@ -203,6 +203,7 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.tmax = (float*)(b + o_tmax);
   a.tsum = (float*)(b + o_tsum);
   a.zt = (float*)(b + o_zt);
+  a.zf = (float*)(b + o_zf);
   a.rs = (float4*)(b + o_rs);
   a.e = b + o_e;
   a.part = (float*)(b + o_part);

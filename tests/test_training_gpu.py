@@ -160,6 +160,33 @@ def test_cross_entropy_soft_cap_of_any_size(n, v, d, softcap, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("softcap", [1.0, 5.0, 30.0, 1000.0])
+@pytest.mark.parametrize("v", [96, 640])
+def test_cross_entropy_soft_cap_slope_of_saturated_logits(v, softcap, dtype):
+    """The weight is the identity, so dhidden is the logits' gradient itself, value by value, of raw logits (exact) up
+    to 6.5 caps. Its bound has no absolute part but that of a kept exponential of 2^-63 and less: the cap as above; the
+    slope 4 e / (1 + e)^2, e = exp(-2 x), with 4 roundings of x twice in its exponent and 8 of its own; the
+    probability as in the other tests; in bf16 the kept value's 2^-11 and a rounding, and the output's."""
+    n = 70
+    cap = softcap
+    h = (cap * 13 * (torch.rand((n, v), generator=gen(18), device="cuda") - 0.5)).to(dtype)
+    t = torch.randint(0, v, (n,), generator=gen(19), device="cuda")
+    w = torch.eye(v, device="cuda").to(dtype)
+    raw = h.double()
+    z = cap * torch.tanh(raw / cap)
+    lse = torch.logsumexp(z, 1)
+    zt = z.gather(1, t[:, None])[:, 0]
+    others = torch.logsumexp((z - zt[:, None]).scatter(1, t[:, None], float("-inf")), 1)
+    q = torch.exp(z - lse[:, None]).scatter(1, t[:, None], -torch.sigmoid(others)[:, None])
+    want = q / torch.cosh(raw / cap) ** 2
+    x = (raw / cap).abs()
+    each = 24 * U * z.abs().amax(1) + (512 + v / 64) * U + 4 * U * (lse.abs() + zt.abs() + z.abs().amax(1))
+    rel = 2 * each[:, None] + 16 * U + (8 * x + 8) * U + (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -8 if dtype == BF else 2 * U)
+    got = mu.linear_cross_entropy_grad(h, w, t, reduction="sum", softcap=softcap, dweight=False)[1]
+    within(got, want, want.abs() * rel * (1 + 2.0 ** -7) + 2.0 ** -62, "dhidden")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("where", ["all", "all but last", "all but first", "blocks"])
 def test_cross_entropy_ignored_rows_are_never_read(dtype, where):
     h, w, t = make(520, 300, 64, dtype, seed=5)
