@@ -1,11 +1,16 @@
 // Device helpers shared by the head's kernels (head_kernels.hip, head_gemm.hip).
 #pragma once
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "train.hpp"
 
 namespace muon {
+
+// Lowest reference of a tile's logits: finite, so that a tile of logits at
+// -infinity has exponentials of 0.
+constexpr float kRefFloor = -FLT_MAX;
 
 __device__ __forceinline__ int64_t target_at(const void* targets, int bytes, int64_t i) {
   return bytes == 8 ? ((const int64_t*)targets)[i] : (int64_t)((const int32_t*)targets)[i];

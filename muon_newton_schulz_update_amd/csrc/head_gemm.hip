@@ -56,7 +56,6 @@ enum OpLayout { OP_ROW_K, OP_GATHER_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
 
 constexpr int kFewTokens = 64;    // whose dW takes the targets' remainders too
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kRefFloor = -3.0e38f;
 
 template <int n>
 __device__ __forceinline__ void wait_vm() {
@@ -537,7 +536,6 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
       ring_barrier();
       top = fmaxf(stat[0], stat[64]);
     }
-    top = ceilf(fmaxf(top * kLog2e, kRefFloor));
     float sum = 0.f;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
@@ -554,9 +552,12 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
       }
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
-        // no smaller than a kept exponential can say (kCodeBase); a maximum
-        // that keeps NaN, so that one bad logit reaches the token's loss
-        e[q] = __builtin_amdgcn_exp2f(__builtin_elementwise_maximum(fmaf(z[q], kLog2e, -top), -63.f));
+        // from the difference, which is exact near the largest however large
+        // both are (z log2(e) less its rounded maximum, one instruction fewer,
+        // is off by more than 1 past 2^24); no smaller than a kept exponential
+        // can say (kCodeBase); a maximum that keeps NaN, so that one bad logit
+        // reaches the token's loss
+        e[q] = __builtin_amdgcn_exp2f(__builtin_elementwise_maximum((z[q] - top) * kLog2e, -63.f));
         sum += e[q];
       }
       if (!keep) continue;

@@ -6,15 +6,15 @@
 //   pack       the piece's hidden rows, gathered, zero-padded, in panels (not
 //              for the loss alone of up to 64 tokens: the logits' launch lists
 //              them and reads their rows itself)
-//   logits     z by tiles; per token and tile an integer reference
-//              K >= log2(e) max z and the sum of 2^(log2(e) z - K) over the
-//              tile without the target's term; with gradients also the
-//              exponentials themselves (times the soft cap's slope at their
-//              logit, where it is still in 32 bits), in 16 bits (10 bits of
-//              mantissa, 6 of exponent, no sign) or 32
-//   merge      per token, over tiles: K = max K_t (differences of integer
-//              references scale exactly), L = sum_t 2^(K_t - K) sum_t, the
-//              target's e = 2^(log2(e) z_t - K), loss = log1p(L / e); the
+//   logits     z by tiles; per token and tile the largest logit m and the sum
+//              of exp(z - m) over the tile without the target's term (of
+//              differences, which are as good as the logits however large these
+//              are); with gradients also the exponentials themselves (times the
+//              soft cap's slope at their logit, where it is still in 32 bits), in
+//              16 bits (10 bits of mantissa, 6 of exponent, no sign) or 32
+//   merge      per token, over tiles: t = the largest m, or the target's logit
+//              if that is larger, L = sum of exp(m - t) times the tile's sum,
+//              the target's e = exp(z - t), loss = log1p(L / e); the
 //              target's own gradient is -g L / (L + e), which loses nothing
 //              when the model is sure of the target
 //   dlogits    p - [v = t] (times the token's own factor) in the operands' type,
@@ -47,10 +47,6 @@ typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kLn2 = 0.69314718055994531f;
-// Lowest reference: far below any finite logit's, but finite, so that a tile
-// of logits at -infinity has exponentials of 0.
-constexpr float kRefFloor = -3.0e38f;
 
 __device__ __forceinline__ float bf2f(u16 h) { return __uint_as_float((unsigned int)h << 16); }
 __device__ __forceinline__ u16 f2bf(float f) {
@@ -241,6 +237,9 @@ __global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan, int row_bloc
   }
 }
 
+// exp(x - y): what an exponential of reference x counts in one of reference y.
+__device__ __forceinline__ float scaled(float x, float y) { return exp2f((x - y) * kLog2e); }
+
 // Bound by latency: 8192 tokens of 393 tiles (26 MB) 12 us.
 // 64 tokens per block, 16 threads per token: each goes over every sixteenth
 // tile with a running reference and sum, then the first adds the sixteen in
@@ -255,7 +254,7 @@ __device__ __forceinline__ void merge_tiles(const HeadArgs& a, int r, int rows, 
 #pragma unroll 4
   for (int t = part; t < a.n_vt; t += parts) {
     const float k = a.tmax[(int64_t)t * a.piece + r], x = a.tsum[(int64_t)t * a.piece + r], m = fmaxf(top, k);
-    others = others * exp2f(top - m) + x * exp2f(k - m);
+    others = others * scaled(top, m) + x * scaled(k, m);
     top = m;
   }
 }
@@ -266,7 +265,7 @@ __device__ __forceinline__ void merge_parts(const float (*tops)[64], const float
   for (int p = 1; p < PARTS; ++p) top = fmaxf(top, tops[p][lane]);
   others = 0.f;
 #pragma unroll
-  for (int p = 0; p < PARTS; ++p) others += sums[p][lane] * exp2f(tops[p][lane] - top);
+  for (int p = 0; p < PARTS; ++p) others += sums[p][lane] * scaled(tops[p][lane], top);
 }
 __device__ __forceinline__ float4 merge_token(const HeadArgs& a, int grad, int r, float top, float others,
                                               float& loss) {
@@ -276,10 +275,10 @@ __device__ __forceinline__ float4 merge_token(const HeadArgs& a, int grad, int r
     loss = __uint_as_float(0x7FC00000u);   // a target outside the vocabulary
     return rs;
   }
-  const float z = a.zt[r], t = fmaxf(top, ceilf(z * kLog2e));   // no tile's reference covers the target
-  others *= exp2f(top - t);
-  const float y = fmaf(z, kLog2e, -t), e = exp2f(y);
-  loss = y > -60.f ? log1pf(others / e) : logf(others + e) - y * kLn2;
+  const float z = a.zt[r], t = fmaxf(top, z);   // no tile's reference covers the target
+  others *= scaled(top, t);
+  const float e = scaled(z, t);
+  loss = z - t > -40.f ? log1pf(others / e) : logf(others + e) - (z - t);
   if (grad) {
     rs.x = t;
     rs.y = (a.grad_out && a.per_token ? a.grad_out[a.idx[a.row0 + r]] : 1.f) / (others + e);
@@ -310,7 +309,7 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
     float all = top;
 #pragma unroll
     for (int o = 32; o; o >>= 1) all = fmaxf(all, __shfl_xor(all, o));
-    others *= exp2f(top - all);
+    others *= scaled(top, all);
 #pragma unroll
     for (int o = 32; o; o >>= 1) others += __shfl_xor(others, o);
     if (lane == 0 && part < rows) {
@@ -388,7 +387,7 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int blo
     const int v = c * CH;
     float x[CH];
     if (real && v < a.v) {
-      const float f = rs.y * exp2f(a.tmax[(int64_t)(v / a.vtile) * a.piece + r] - rs.x);
+      const float f = rs.y * scaled(a.tmax[(int64_t)(v / a.vtile) * a.piece + r], rs.x);
       if constexpr (sizeof(T) == 2) {
         const u32x4_t q = *(const u32x4_t*)p;
 #pragma unroll

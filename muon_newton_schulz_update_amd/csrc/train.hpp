@@ -135,8 +135,8 @@ struct HeadArgs {
   float* lossc;                       // compact losses
   void* hp;                           // piece x dp panels of the gathered hidden states
   void* e;                            // piece x vp panels: exponentials (times the soft cap's slope), then the logits' gradient
-  float* tmax;                        // n_vt x piece: integer power-of-two reference of each tile's row
-  float* tsum;                        // n_vt x piece: sum of the tile's exponentials without the target's
+  float* tmax;                        // n_vt x piece: each tile's largest logit of the row, without the target's
+  float* tsum;                        // n_vt x piece: sum of its exponentials over that reference, without the target's
   float* zt;                          // piece: the target's logit
   float* zf;                          // piece: the soft cap's slope there (with a soft cap)
   float4* rs;                         // piece: {reference, factor, target's gradient, what its rounding lost}

@@ -269,6 +269,38 @@ def test_cross_entropy_logit_ranges(dtype, spread):
     check_loss(h, w, t, reduction="sum")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("log2", [20, 25, 30, 37, 60, 120])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n,v", [(1, 300), (70, 20000)])
+def test_cross_entropy_of_huge_logits(n, v, sign, log2, dtype):
+    """Logits that 32 bits hold exactly, up to three spacings apart and in every tile: each difference is exact, so
+    the loss and probabilities are as good as those of small logits."""
+    step = max(1.0, 2.0 ** (log2 - 23))
+    k = torch.randint(0, 4, (v,), generator=gen(28), device="cuda") * (torch.rand(v, generator=gen(29), device="cuda") < 0.02)
+    t = torch.randint(0, v, (n,), generator=gen(30), device="cuda")
+    half = log2 // 2
+    h = torch.zeros((n, 8), device="cuda")
+    h[:, 0], h[:, 5] = 2.0 ** (log2 - half), 1.0
+    w = torch.zeros((v, 8), device="cuda")
+    w[:, 0], w[:, 5] = sign * 2.0 ** half, k * step
+    h, w = h.to(dtype), w.to(dtype)
+    z = mm(h.double(), w.double().t())
+    assert torch.equal(z, z.float().double())
+    zt = z.gather(1, t[:, None])[:, 0]
+    others = torch.logsumexp((z - zt[:, None]).scatter(1, t[:, None], float("-inf")), 1)
+    each = torch.logaddexp(others, torch.zeros_like(others))
+    err = (512 + v / 64) * U + 8 * U * each
+    loss, _, dw = mu.linear_cross_entropy_grad(h, w, t, reduction="none", dhidden=None)
+    within(loss, each, err, "loss")
+    within(mu.linear_cross_entropy(h, w, t, reduction="none"), each, err, "loss alone")
+    p = torch.exp(z - zt[:, None] - each[:, None]).scatter(1, t[:, None], -torch.sigmoid(others)[:, None])
+    rel = 2 * err[:, None] + 16 * U + (2.0 ** -8 + 2.0 ** -11 if dtype == BF else 0)
+    want = p.sum(0)                                   # the gradient of the last column's weights
+    bound = (p.abs() * (rel + (n + 8) * U) + 2.0 ** -62).sum(0) + (2.0 ** -8 if dtype == BF else 2 * U) * want.abs()
+    within(dw[:, 5], want, bound, "dweight")
+
+
 def test_cross_entropy_target_out_of_range():
     h, w, t = make(100, 300, 64, BF, seed=15)
     good = mu.linear_cross_entropy_grad(h, w, t, reduction="none")
