@@ -134,6 +134,19 @@ def test_loss_rules():
     expect(check(loss=B - 8, cfg=mu.LossConfig(0, 0.0, 0)), INVALID, "share memory")
 
 
+def test_tensors_with_a_forward_tangent_are_refused():
+    """Describing one would drop its tangent without a word."""
+    import torch
+    import torch.autograd.forward_ad as fwd
+
+    pack = mu.training._describe().pack
+    with fwd.dual_level():
+        for shape in ((2, 3), (3,), (0, 3)):
+            with pytest.raises(ValueError, match="tangent"):
+                pack((fwd.make_dual(torch.ones(shape), torch.ones(shape)),), "hidden", 0)
+        pack((torch.ones(0, 3),), "hidden", 0)
+
+
 @pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
 def test_training_validation_under_asan_ubsan(tmp_path):
     exe = tmp_path / "train_validate_fuzz"

@@ -413,6 +413,20 @@ def test_cross_entropy_second_backward_is_refused():
         loss.backward()
 
 
+@pytest.mark.parametrize("needs_grad", [False, True])
+def test_cross_entropy_refuses_forward_mode(needs_grad):
+    import torch.autograd.forward_ad as fwd
+
+    h, w, t = make(20, 100, 64, F32, seed=32)
+    h.requires_grad_(needs_grad)
+    with fwd.dual_level():
+        for a, b in ((fwd.make_dual(h, torch.ones_like(h)), w), (h, fwd.make_dual(w, torch.ones_like(w)))):
+            with pytest.raises((ValueError, RuntimeError)):
+                mu.linear_cross_entropy(a, b, t)
+    with pytest.raises((ValueError, RuntimeError)):
+        torch.func.jvp(lambda x: mu.linear_cross_entropy(x, w, t), (h.detach(),), (torch.ones_like(h),))
+
+
 @pytest.mark.parametrize("softcap", [0.0, 6.0])
 def test_cross_entropy_gradient_against_differences(softcap):
     """Central differences of the 32-bit loss along random directions. With
