@@ -235,7 +235,11 @@ class _LinearCrossEntropy(torch.autograd.Function):
                               handle)[0]
         loss, dh, dw = _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, None,
                                   None if need_h else False, None if need_w else False, True, handle)
-        ctx.grads = (dh, dw)
+        # (saved as tensors are, so that hooks on saved tensors see them; the graph
+        # lets go of them before it hands on what backward returns, which is then
+        # taken as it is, without a copy)
+        ctx.taken = False
+        ctx.save_for_backward(dh, dw)
         return loss
 
     @staticmethod
@@ -248,10 +252,10 @@ class _LinearCrossEntropy(torch.autograd.Function):
             _, dh, dw = _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_out,
                                    None if need_h else False, None if need_w else False, True, None)
         else:
-            if ctx.grads is None:
+            if ctx.taken:
                 raise RuntimeError("linear_cross_entropy: the gradient was taken before (it is scaled in place)")
-            dh, dw = ctx.grads
-            ctx.grads = None
+            dh, dw = ctx.saved_tensors
+            ctx.taken = True
             scale([g for g in (dh, dw) if g is not None], grad_out)
         return dh, dw, None, None, None, None, None
 

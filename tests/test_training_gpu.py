@@ -413,6 +413,33 @@ def test_cross_entropy_second_backward_is_refused():
         loss.backward()
 
 
+@pytest.mark.parametrize("reduction", ["sum", "mean", "none"])
+def test_cross_entropy_saved_tensor_hooks(reduction):
+    """Hooks on saved tensors see all that a forward keeps, and backward uses what they give back."""
+    h, w, t = make(90, 300, 64, BF, seed=33)
+    h.requires_grad_(), w.requires_grad_()
+    mu.linear_cross_entropy(h, w, t, reduction=reduction).sum().mul(0.5).backward()
+    want, h.grad, w.grad = (h.grad, w.grad), None, None
+    kept = []
+
+    def pack(x):
+        kept.append(x.shape)
+        return x.cpu()
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda x: x.cuda()):
+        loss = mu.linear_cross_entropy(h, w, t, reduction=reduction)
+    assert h.shape in kept and w.shape in kept
+    loss.sum().mul(0.5).backward()
+    assert torch.equal(h.grad, want[0]) and torch.equal(w.grad, want[1])
+    # without hooks the gradients become the leaves' own, uncopied
+    if reduction != "none":
+        h.grad = w.grad = None
+        loss = mu.linear_cross_entropy(h, w, t, reduction=reduction)
+        own = [x.data_ptr() for x in loss.grad_fn.saved_tensors]
+        loss.backward()
+        assert [h.grad.data_ptr(), w.grad.data_ptr()] == own
+
+
 @pytest.mark.parametrize("needs_grad", [False, True])
 def test_cross_entropy_refuses_forward_mode(needs_grad):
     import torch.autograd.forward_ad as fwd
