@@ -227,7 +227,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, targets, ignore_index, reduction, softcap, handle):
         need_h, need_w = ctx.needs_input_grad[:2]
-        ctx.opts = (ignore_index, reduction, softcap, need_h, need_w)
+        ctx.opts = (ignore_index, reduction, softcap, need_h, need_w, handle)
         if reduction == "none":
             # the gradient's weights come with backward: it takes the logits again
             ctx.save_for_backward(hidden, weight, targets)
@@ -245,18 +245,20 @@ class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out):
-        ignore_index, reduction, softcap, need_h, need_w = ctx.opts
+        # (a handle that was given serves the backward too; without one, the
+        # thread that runs it has its own)
+        ignore_index, reduction, softcap, need_h, need_w, handle = ctx.opts
         grad_out = grad_out.contiguous()
         if reduction == "none":
             hidden, weight, targets = ctx.saved_tensors
             _, dh, dw = _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, grad_out,
-                                   None if need_h else False, None if need_w else False, True, None)
+                                   None if need_h else False, None if need_w else False, True, handle)
         else:
             if ctx.taken:
                 raise RuntimeError("linear_cross_entropy: the gradient was taken before (it is scaled in place)")
             dh, dw = ctx.saved_tensors
             ctx.taken = True
-            scale([g for g in (dh, dw) if g is not None], grad_out)
+            scale([g for g in (dh, dw) if g is not None], grad_out, handle=handle)
         return dh, dw, None, None, None, None, None
 
 
@@ -268,8 +270,13 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: to
     ignore_index, "sum") or one a token ("none", 0 where ignored). The logits
     are never stored as a whole.
 
-    Differentiable in hidden and weight. "mean" and "sum" compute the gradient
-    with the loss, so one backward per forward; "none" computes it in backward."""
+    Differentiable in hidden and weight, in reverse mode (a tensor with a
+    forward-mode tangent is refused). "mean" and "sum" compute the gradient with
+    the loss, so one backward per forward; backward multiplies it by grad_out in
+    place, which rounds a bfloat16 gradient once more unless that is a power of
+    two (`linear_cross_entropy_grad` takes grad_out before its one rounding).
+    "none" computes the gradient in backward, logits and all. A handle that is
+    given serves both; without one each uses its own thread's."""
     if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
         return _LinearCrossEntropy.apply(hidden, weight, targets, ignore_index, reduction, softcap, handle)
     return _loss_call(hidden, weight, targets, ignore_index, reduction, softcap, None, None, None, False, handle)[0]

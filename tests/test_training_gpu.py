@@ -440,6 +440,24 @@ def test_cross_entropy_saved_tensor_hooks(reduction):
         assert [h.grad.data_ptr(), w.grad.data_ptr()] == own
 
 
+@pytest.mark.parametrize("reduction", ["sum", "none"])
+def test_cross_entropy_backward_uses_the_given_handle(reduction, monkeypatch):
+    """(Its own thread's handle would have a second workspace.)"""
+    h, w, t = make(90, 300, 64, BF, seed=34)
+    want = mu.linear_cross_entropy_grad(h, w, t, reduction=reduction)
+    handle = mu.Handle()
+
+    def other(device=None):
+        raise AssertionError("another handle was asked for")
+
+    monkeypatch.setattr(mu.training, "get_handle", other)
+    loss = mu.linear_cross_entropy(h.requires_grad_(), w.requires_grad_(), t, reduction=reduction, handle=handle)
+    loss.sum().backward()
+    torch.cuda.synchronize()
+    assert torch.equal(h.grad, want[1]) and torch.equal(w.grad, want[2])
+    handle.close()
+
+
 @pytest.mark.parametrize("needs_grad", [False, True])
 def test_cross_entropy_refuses_forward_mode(needs_grad):
     import torch.autograd.forward_ad as fwd
