@@ -294,7 +294,7 @@ extern "C" muon_status muon_scale(muon_handle* h, int n, const muon_matrix* in, 
                                   const float* coef) {
   return guarded(h, [&]() -> muon_status {
   char msg[256];
-  const int rc = check_norm(n, in, out, 1.0f, coef, coef, 1, msg, sizeof(msg));
+  const int rc = check_scale(n, in, out, coef, msg, sizeof(msg));
   if (rc) return handle_error(h, rc, msg);
   handle_clear_error(h);
   return scale_run(h, n, in, out, coef);

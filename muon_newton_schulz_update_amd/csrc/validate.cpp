@@ -306,12 +306,15 @@ Span flat_span(const void* p, int64_t bytes, const char* what, bool writes) {
 
 }  // namespace
 
-int check_norm(int n, const muon_matrix* g, const muon_matrix* out, float max_norm, const float* norm,
-               const float* coef, int writes, char* msg, int len) {
+namespace {
+
+// A list with its outputs and device scalars: writes tells whether tensors
+// without an output of their own are written, `scalars` whether norm and coef are.
+int check_list(int n, const muon_matrix* g, const muon_matrix* out, float max_norm, const float* norm,
+               const float* coef, bool writes, bool scalars, char* msg, int len) {
   if (msg && len > 0) msg[0] = 0;
   if (n < 0 || n > kMaxBatch) return fail(msg, len, MUON_ERR_INVALID_ARG, "list length %d outside [0, %d]", n, kMaxBatch);
   if (n > 0 && !g) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL grad array");
-  if (!norm) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL norm or coefficient");
   if (((uintptr_t)norm | (uintptr_t)coef) % 4 != 0)
     return fail(msg, len, MUON_ERR_INVALID_ARG, "norm or coefficient not aligned to 4 bytes");
   if (coef && !(max_norm > 0.0f)) return fail(msg, len, MUON_ERR_INVALID_ARG, "max_norm must be positive");
@@ -332,9 +335,22 @@ int check_norm(int n, const muon_matrix* g, const muon_matrix* out, float max_no
     v.push_back(tensor_span(g[i], "grad", i, own && writes));
     if (!own) v.push_back(tensor_span(out[i], "out", i, true));
   }
-  if (norm != coef) v.push_back(flat_span(norm, 4, "norm", true));
-  if (coef) v.push_back(flat_span(coef, 4, "coefficient", norm != coef));
+  if (norm) v.push_back(flat_span(norm, 4, "norm", scalars));
+  if (coef) v.push_back(flat_span(coef, 4, "coefficient", scalars));
   return check_apart(v, msg, len);
+}
+
+}  // namespace
+
+int check_norm(int n, const muon_matrix* g, const muon_matrix* out, float max_norm, const float* norm,
+               const float* coef, int writes, char* msg, int len) {
+  if (!norm) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL norm");
+  return check_list(n, g, out, max_norm, norm, coef, writes != 0, true, msg, len);
+}
+
+int check_scale(int n, const muon_matrix* in, const muon_matrix* out, const float* coef, char* msg, int len) {
+  if (!coef) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL coefficient");
+  return check_list(n, in, out, 1.0f, nullptr, coef, true, false, msg, len);
 }
 
 int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_matrix* v, const muon_matrix* w,

@@ -22,6 +22,7 @@ constexpr int64_t kMaxListElems = int64_t(1) << 42;   // elements of one tensor 
 constexpr int kMaxVocab = 1 << 22;
 int check_norm(int n, const muon_matrix* g, const muon_matrix* out, float max_norm, const float* norm,
                const float* coef, int writes, char* msg, int len);
+int check_scale(int n, const muon_matrix* in, const muon_matrix* out, const float* coef, char* msg, int len);
 int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_matrix* v, const muon_matrix* w,
                 const muon_matrix* copy, const muon_adamw_config* cfg, const float* scale, char* msg, int len);
 int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,

@@ -68,6 +68,20 @@ def test_norm_rules():
     expect(check([M(A, 4, 4, 8)], [M(A + 16, 4, 4, 8)]), OK)
 
 
+def test_norm_scalars_are_outputs():
+    """Norm and coefficient at one address, or in a tensor's place: the second write would destroy the first, or a
+    gradient."""
+    check = mu.check_norm_args
+    for out in (None, [M(B)], [M()]):
+        expect(check([M()], out, norm=C, coef=C + 4), OK)
+        expect(check([M()], out, norm=C, coef=C), INVALID, "share memory")
+        expect(check([M()], out, norm=C, coef=C + 2), INVALID, "aligned")
+        expect(check([M()], out, norm=A, coef=A), INVALID, "share memory")
+        expect(check([M()], out, norm=A + 8, coef=C), INVALID, "share memory")
+        expect(check([M()], out, norm=C, coef=A + 8), INVALID, "share memory")
+    expect(check([], norm=C, coef=C), INVALID, "share memory")
+
+
 def test_adamw_rules():
     def check(g=None, m=None, v=None, w=None, copies=None, scale=None, **cfg):
         c = mu.AdamWConfig()
