@@ -510,7 +510,12 @@ muon_status linear_cross_entropy_grad(muon_handle* handle, const muon_matrix* hi
                                       const float* grad_out, float* loss, const muon_matrix* dhidden,
                                       const muon_matrix* dweight);
 
-/* Host-only validation with the rules of the calls above; enqueue nothing, need no device. */
+/*
+ * Host-only validation with the rules of the calls above; enqueue nothing, need no device.
+ * muon_check_norm_args has muon_grad_norm's rules with out NULL (the list is only read: a
+ * tensor may be in it twice) and muon_clip_grad_norm's with out, coef apart, which that call
+ * also needs; for a clip in place, which writes the list, give the list itself as out.
+ */
 muon_status muon_check_norm_args(int n, const muon_matrix* grad, const muon_matrix* out, float max_norm,
                                  const float* norm, const float* coef, char* msg, int msg_len);
 muon_status muon_check_adamw_args(int n, const muon_matrix* grad, const muon_matrix* exp_avg,

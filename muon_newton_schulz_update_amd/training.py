@@ -301,6 +301,8 @@ def _checked(call, *args):
 
 
 def check_norm_args(grads, out=None, max_norm: float = 1.0, norm=4096, coef=None) -> tuple[int, str]:
+    """Rules of grad_norm (out None: the list is only read) or of clip_grad_norm into `out`; in place, where the list
+    is written, `out` is the list itself."""
     return _checked(load_library().muon_check_norm_args, len(grads), _descriptors(grads), _descriptors(out), max_norm,
                     norm, coef)
 

@@ -82,6 +82,14 @@ def test_norm_scalars_are_outputs():
     expect(check([], norm=C, coef=C), INVALID, "share memory")
 
 
+def test_norm_rules_of_a_list_in_place():
+    check = mu.check_norm_args
+    for twice in ([M(), M()], [M(), M(A + 16)], [M(A, 4, 8, 16), M(A, 4, 9, 16)]):
+        expect(check(twice), OK)                                   # a norm reads
+        expect(check(twice, twice), INVALID, "share memory")       # a clip in place writes
+    expect(check([M(), M(B)], [M(), M(B)]), OK)
+
+
 def test_adamw_rules():
     def check(g=None, m=None, v=None, w=None, copies=None, scale=None, **cfg):
         c = mu.AdamWConfig()
