@@ -451,15 +451,34 @@ int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void*
 
 }  // namespace muon
 
+namespace {
+
+// A checker's body behind a C entry point: no exception (the lists' spans are
+// on the heap) leaves it.
+template <typename F>
+muon_status checked(char* msg, int len, F body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return muon::fail(msg, len, MUON_ERR_ALLOC, "out of host memory");
+  }
+}
+
+}  // namespace
+
 extern "C" muon_status muon_check_norm_args(int n, const muon_matrix* grad, const muon_matrix* out, float max_norm,
                                             const float* norm, const float* coef, char* msg, int msg_len) {
-  return muon::check_norm(n, grad, out, max_norm, norm, coef, out != nullptr, msg, msg_len);
+  return checked(msg, msg_len, [&] {
+    return muon::check_norm(n, grad, out, max_norm, norm, coef, out != nullptr, msg, msg_len);
+  });
 }
 extern "C" muon_status muon_check_adamw_args(int n, const muon_matrix* grad, const muon_matrix* exp_avg,
                                              const muon_matrix* exp_avg_sq, const muon_matrix* weight,
                                              const muon_matrix* copy, const muon_adamw_config* cfg,
                                              const float* grad_scale, char* msg, int msg_len) {
-  return muon::check_adamw(n, grad, exp_avg, exp_avg_sq, weight, copy, cfg, grad_scale, msg, msg_len);
+  return checked(msg, msg_len, [&] {
+    return muon::check_adamw(n, grad, exp_avg, exp_avg_sq, weight, copy, cfg, grad_scale, msg, msg_len);
+  });
 }
 extern "C" muon_status muon_check_loss_args(const muon_matrix* hidden, const muon_matrix* weight, const void* targets,
                                             int target_bytes, const muon_loss_config* cfg, const float* grad_out,
@@ -468,8 +487,10 @@ extern "C" muon_status muon_check_loss_args(const muon_matrix* hidden, const muo
   muon_loss_config c;
   muon_loss_config_default(&c);
   if (cfg) c = *cfg;
-  return muon::check_loss(hidden, weight, targets, target_bytes, &c, grad_out, loss, dhidden, dweight,
-                          dhidden || dweight ? 1 : 0, msg, msg_len);
+  return checked(msg, msg_len, [&] {
+    return muon::check_loss(hidden, weight, targets, target_bytes, &c, grad_out, loss, dhidden, dweight,
+                            dhidden || dweight ? 1 : 0, msg, msg_len);
+  });
 }
 
 extern "C" void muon_loss_config_default(muon_loss_config* c) {
@@ -492,12 +513,13 @@ extern "C" void muon_adamw_config_default(muon_adamw_config* c) {
 extern "C" muon_status muon_check_update_args(int n, const muon_matrix* grad, const muon_matrix* momentum,
                                               const muon_matrix* weight, const muon_matrix* update_out,
                                               const muon_config* cfg, char* msg, int msg_len) {
-  return muon::check_update(n, grad, momentum, weight, update_out, cfg, msg, msg_len);
+  return checked(msg, msg_len,
+                 [&] { return muon::check_update(n, grad, momentum, weight, update_out, cfg, msg, msg_len); });
 }
 
 extern "C" muon_status muon_check_polar_args(int n, const muon_matrix* in, const muon_matrix* out,
                                              const muon_config* cfg, char* msg, int msg_len) {
-  return muon::check_polar(n, in, out, cfg, msg, msg_len);
+  return checked(msg, msg_len, [&] { return muon::check_polar(n, in, out, cfg, msg, msg_len); });
 }
 
 extern "C" void muon_config_default(muon_config* c) {

@@ -183,3 +183,14 @@ def test_training_validation_under_asan_ubsan(tmp_path):
     run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, (run.stdout[-2000:], run.stderr[-4000:])
     assert run.stdout.splitlines()[-1].startswith("ok "), run.stdout
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_checkers_when_memory_runs_out(tmp_path):
+    exe = tmp_path / "check_alloc"
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-g", f"-I{ROOT}/include", f"-I{ROOT}/muon_newton_schulz_update_amd/csrc",
+                        f"{ROOT}/tests/native/check_alloc.cpp", f"{ROOT}/muon_newton_schulz_update_amd/csrc/validate.cpp",
+                        "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert run.returncode == 0 and run.stdout == "ok\n", (run.returncode, run.stdout[-500:], run.stderr[-500:])
