@@ -459,12 +459,18 @@ muon_status muon_scale(muon_handle* handle, int n, const muon_matrix* in, const 
  *   model that computes on 16-bit copies of 32-bit weights. All arithmetic is
  *   fp32; a BF16 weight is rounded to nearest even once a step. step counts
  *   from 1. Every tensor is read and written once.
+ *   lr and step are constants of the launch: a graph that captured the call
+ *   repeats them on every replay. step_at and lr_at (device pointers, each or
+ *   both, NULL = the value here) are read when the kernel runs instead, so a
+ *   graph can count its steps (a step below 1 gives weights that are not finite).
  * muon_adamw_config_default: lr 0.01, betas (0.8, 0.95), eps 1e-10,
- * weight_decay 0 (the [Aurora page]'s AdamW beside Muon), step 1.
+ * weight_decay 0 (the [Aurora page]'s AdamW beside Muon), step 1, no device values.
  */
 typedef struct {
   float lr, beta1, beta2, eps, weight_decay;
   int64_t step;
+  const int64_t* step_at;
+  const float* lr_at;
 } muon_adamw_config;
 void muon_adamw_config_default(muon_adamw_config* cfg);
 muon_status adamw_update(muon_handle* handle, int n, const muon_matrix* grad, const muon_matrix* exp_avg,

@@ -74,6 +74,15 @@ struct AdamConst {
   float rs2;            // 1 / sqrt(1 - beta2^step)
   float eps;
 };
+// Step and rate that are read from the device when the kernel runs, and what
+// AdamConst's dependent members are made of (both pointers null: not used).
+struct AdamClock {
+  const int64_t* step_at;
+  const float* lr_at;
+  int64_t step;
+  double lr, weight_decay;
+  double log2_b1, log2_b2;
+};
 
 // The norm kernel's state in the handle's workspace.
 struct NormState {
@@ -87,7 +96,8 @@ hipError_t launch_norm(const NormList& L, int blocks, int chunks, NormState* st,
 hipError_t launch_norm_reset(NormState* st, hipStream_t s);
 hipError_t launch_norm_empty(float max_norm, float* norm, float* coef, hipStream_t s);
 hipError_t launch_scale(const ScaleList& L, int chunks, const float* coef, int in_place, hipStream_t s);
-hipError_t launch_adamw(const AdamList& L, int chunks, const AdamConst& c, const float* scale, hipStream_t s);
+hipError_t launch_adamw(const AdamList& L, int chunks, const AdamConst& c, const AdamClock& clock, const float* scale,
+                        hipStream_t s);
 
 // ---------------------------------------------------------------------------
 // Head cross entropy. The valid tokens (target != ignore_index) are gathered

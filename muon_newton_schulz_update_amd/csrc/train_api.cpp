@@ -319,6 +319,7 @@ extern "C" muon_status adamw_update(muon_handle* h, int n, const muon_matrix* gr
   c.lr1 = (float)((double)cfg->lr / (1.0 - pow(b1, (double)cfg->step)));
   c.rs2 = (float)(1.0 / sqrt(1.0 - pow(b2, (double)cfg->step)));
   c.eps = cfg->eps;
+  const AdamClock clock{cfg->step_at, cfg->lr_at, cfg->step, cfg->lr, cfg->weight_decay, log2(b1), log2(b2)};
   const hipStream_t s = handle_stream(h);
   for (int i = 0; i < n;) {
     AdamList L;
@@ -350,7 +351,7 @@ extern "C" muon_status adamw_update(muon_handle* h, int n, const muon_matrix* gr
       k0 += k;
     }
     L.chunk0[L.n] = (int32_t)k0;
-    if (L.n) HIP_DO(h, launch_adamw(L, (int)k0, c, grad_scale, s));
+    if (L.n) HIP_DO(h, launch_adamw(L, (int)k0, c, clock, grad_scale, s));
   }
   return MUON_OK;
   });

@@ -359,17 +359,19 @@ int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_ma
   if (n < 0 || n > kMaxBatch) return fail(msg, len, MUON_ERR_INVALID_ARG, "list length %d outside [0, %d]", n, kMaxBatch);
   if (n > 0 && (!g || !m || !v || !w)) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL tensor array");
   if (!c) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL configuration");
-  if (!finitef(c->lr)) return fail(msg, len, MUON_ERR_INVALID_ARG, "lr must be finite");
+  if (!c->lr_at && !finitef(c->lr)) return fail(msg, len, MUON_ERR_INVALID_ARG, "lr must be finite");
   if (!(c->beta1 >= 0.0f && c->beta1 < 1.0f) || !(c->beta2 >= 0.0f && c->beta2 < 1.0f))
     return fail(msg, len, MUON_ERR_INVALID_ARG, "betas %g, %g outside [0, 1)", c->beta1, c->beta2);
   if (!(c->eps >= 0.0f) || !finitef(c->eps)) return fail(msg, len, MUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
   if (!(c->weight_decay >= 0.0f) || !finitef(c->weight_decay))
     return fail(msg, len, MUON_ERR_INVALID_ARG, "weight_decay must be finite and >= 0");
-  if (c->step < 1) return fail(msg, len, MUON_ERR_INVALID_ARG, "step %lld: the first step is 1", (long long)c->step);
+  if (!c->step_at && c->step < 1) return fail(msg, len, MUON_ERR_INVALID_ARG, "step %lld: the first step is 1", (long long)c->step);
   if ((uintptr_t)scale % 4 != 0) return fail(msg, len, MUON_ERR_INVALID_ARG, "grad_scale not aligned to 4 bytes");
+  if ((uintptr_t)c->step_at % 8 != 0 || (uintptr_t)c->lr_at % 4 != 0)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "step_at or lr_at not aligned to its value's size");
   int rc;
   std::vector<Span> spans;
-  spans.reserve((size_t)n * 5 + 1);
+  spans.reserve((size_t)n * 5 + 3);
   for (int i = 0; i < n; ++i) {
     if ((rc = check_tensor(w[i], "weight", i, msg, len))) return rc;
     const muon_matrix* xs[] = {&g[i], &m[i], &v[i]};
@@ -393,6 +395,8 @@ int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_ma
     if (cp) spans.push_back(tensor_span(copy[i], "copy", i, true));
   }
   if (scale) spans.push_back(flat_span(scale, 4, "grad_scale", false));
+  if (c->step_at) spans.push_back(flat_span(c->step_at, 8, "step_at", false));
+  if (c->lr_at) spans.push_back(flat_span(c->lr_at, 4, "lr_at", false));
   return check_apart(spans, msg, len);
 }
 
@@ -508,6 +512,8 @@ extern "C" void muon_adamw_config_default(muon_adamw_config* c) {
   c->eps = 1e-10f;
   c->weight_decay = 0.0f;
   c->step = 1;
+  c->step_at = nullptr;
+  c->lr_at = nullptr;
 }
 
 extern "C" muon_status muon_check_update_args(int n, const muon_matrix* grad, const muon_matrix* momentum,

@@ -24,7 +24,8 @@ REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 
 class AdamWConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
-                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("step", ctypes.c_int64)]
+                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("step", ctypes.c_int64),
+                ("step_at", ctypes.c_void_p), ("lr_at", ctypes.c_void_p)]
 
 
 class LossConfig(ctypes.Structure):
@@ -61,11 +62,11 @@ def _handle_for(tensors, handle):
     return handle
 
 
-def _scalar(t: torch.Tensor | None, what: str, device: int, n: int | None = None):
+def _scalar(t: torch.Tensor | None, what: str, device: int, n: int | None = None, dtype=torch.float32):
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.get_device() != device:
-        raise ValueError(f"{what}: expected float32 on GPU {device}, got {t.dtype} on {t.device}")
+    if t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{what}: expected {dtype} on GPU {device}, got {t.dtype} on {t.device}")
     if t.numel() != (1 if n is None else n) or not t.is_contiguous():
         raise ValueError(f"{what}: expected {1 if n is None else n} contiguous values, got shape {tuple(t.shape)}")
     return t.data_ptr()
@@ -135,14 +136,16 @@ def _adamw_defaults() -> AdamWConfig:
 
 
 def adamw_update(grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
-                 exp_avg_sqs: Sequence[torch.Tensor], weights: Sequence[torch.Tensor], *, step: int,
-                 lr: float | None = None, beta1: float | None = None, beta2: float | None = None,
+                 exp_avg_sqs: Sequence[torch.Tensor], weights: Sequence[torch.Tensor], *, step: int | torch.Tensor,
+                 lr: float | torch.Tensor | None = None, beta1: float | None = None, beta2: float | None = None,
                  eps: float | None = None, weight_decay: float | None = None,
                  grad_scale: torch.Tensor | None = None,
                  copies: Sequence[torch.Tensor | None] | None = None, handle=None) -> None:
     """One AdamW step in place (libmuon `adamw_update`); what is not given has
     the library's default. grad_scale: a float32 device scalar that multiplies
-    every gradient (`grad_norm`'s coefficient). copies[i], when given, receives
+    every gradient (`grad_norm`'s coefficient). step (int64) and lr (float32) may
+    be one-element tensors on the device, read when the kernel runs: a captured
+    graph repeats numbers, and counts its steps with tensors. copies[i], when given, receives
     the new weight, for a model that computes on 16-bit copies of 32-bit ones."""
     weights = list(weights)
     h = _handle_for(weights, handle)
@@ -152,9 +155,14 @@ def adamw_update(grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor]
              ((grads, "grads"), (exp_avgs, "exp_avgs"), (exp_avg_sqs, "exp_avg_sqs"))]
     cp = None if copies is None else pack(copies, "copies", d, weights, "weights")
     z = _adamw_defaults()
+    step_at = lr_at = None
+    if isinstance(step, torch.Tensor):
+        step, step_at = 1, _scalar(step, "step", d, dtype=torch.int64)
+    if isinstance(lr, torch.Tensor):
+        lr, lr_at = None, _scalar(lr, "lr", d)
     cfg = AdamWConfig(z.lr if lr is None else lr, z.beta1 if beta1 is None else beta1,
                       z.beta2 if beta2 is None else beta2, z.eps if eps is None else eps,
-                      z.weight_decay if weight_decay is None else weight_decay, step)
+                      z.weight_decay if weight_decay is None else weight_decay, step, step_at, lr_at)
     h._check(h._lib.adamw_update(h.ptr, len(weights), *lists, w, cp, ctypes.byref(cfg),
                                  _scalar(grad_scale, "grad_scale", d)))
 

@@ -121,6 +121,27 @@ def test_adamw_rules():
     expect(check(scale=4097), INVALID, "aligned")
 
 
+def test_adamw_rules_of_device_step_and_rate():
+    def check(**cfg):
+        c = mu.AdamWConfig()
+        mu.load_library().muon_adamw_config_default(ctypes.byref(c))
+        assert c.step_at is None and c.lr_at is None
+        for k, x in cfg.items():
+            setattr(c, k, x)
+        return mu.check_adamw_args([M(A)], [M(B)], [M(C)], [M(D)], None, c, None)
+
+    expect(check(step_at=E, lr_at=E + 8), OK)
+    expect(check(step_at=E, step=0), OK)                           # not read
+    expect(check(lr_at=E, lr=float("nan")), OK)
+    expect(check(lr_at=E, step=0), INVALID, "step")
+    expect(check(step_at=E, lr=float("nan")), INVALID, "lr")
+    expect(check(step_at=E + 4), INVALID, "aligned")
+    expect(check(lr_at=E + 2), INVALID, "aligned")
+    expect(check(step_at=B), INVALID, "share memory")
+    expect(check(lr_at=D + 4), INVALID, "share memory")
+    expect(check(lr_at=A + 4), OK)                                 # the gradient is only read
+
+
 def test_loss_rules():
     def check(h=None, w=None, **kw):
         return mu.check_loss_args(h or M(A, 10, 64, dtype=BF16), w or M(B, 50, 64, dtype=BF16), **kw)

@@ -670,6 +670,51 @@ def test_training_step_in_a_graph():
             torch.zeros(1 << 20, device="cuda").sum()
 
 
+@pytest.mark.parametrize("wt", [F32, BF])
+def test_adamw_in_a_graph_counts_its_steps(wt):
+    """Step and rate on the device, changed between the replays, against the call with their numbers. The moments do
+    not depend on them; the weight's three constants are each one rounding from those made on the host."""
+    shapes = [(130, 257), (8193,), (5,)]
+    g = [normal(s, 90 + i, 1e-2) for i, s in enumerate(shapes)]
+    w = [normal(s, 93 + i).to(wt) for i, s in enumerate(shapes)]
+    m, v = [torch.zeros(s, device="cuda") for s in shapes], [torch.zeros(s, device="cuda") for s in shapes]
+    step, lr = torch.zeros((), device="cuda", dtype=torch.int64), torch.full((1,), 0.01, device="cuda")
+    hp = dict(beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+    clone = lambda xs: [x.clone() for x in xs]
+
+    def run(m, v, w):
+        step.add_(1)
+        mu.adamw_update(g, m, v, w, step=step, lr=lr, **hp)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        run(clone(m), clone(v), clone(w))
+        step.zero_()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            run(m, v, w)
+        for k in (1, 2, 3, 40, 41, 100000):
+            step.fill_(k - 1)
+            rate = 0.01 / k
+            lr.fill_(rate)
+            m2, v2, w2, old = clone(m), clone(v), clone(w), clone(w)
+            mu.adamw_update(g, m2, v2, w2, step=k, lr=rate, **hp)
+            graph.replay()
+            s.synchronize()
+            assert int(step) == k
+            for i in range(len(shapes)):
+                assert torch.equal(m[i], m2[i]) and torch.equal(v[i], v2[i])
+                move = 4 * U * ((w2[i].double() - old[i].double()).abs() + old[i].double().abs())
+                within(w[i], w2[i].double(), move + (2.0 ** -7 * w2[i].double().abs() if wt == BF else 0) + 1e-44, f"weight, step {k}")
+                if wt == F32:                  # (a late step's rate is too small to move 16-bit weights)
+                    assert not torch.equal(w[i], old[i])
+    with pytest.raises(ValueError, match="step"):
+        mu.adamw_update(g, m, v, w, step=step.int(), lr=0.1)
+    with pytest.raises(ValueError, match="lr"):
+        mu.adamw_update(g, m, v, w, step=1, lr=lr.cpu())
+
+
 def test_lists_past_32_bit_offsets():
     n = (1 << 32) + 12345
     g = torch.zeros(n, device="cuda", dtype=BF)
