@@ -455,9 +455,11 @@ muon_status muon_scale(muon_handle* handle, int n, const muon_matrix* in, const 
  *   (1 - beta2) g'^2, w = w (1 - lr weight_decay) - lr (m / (1 - beta1^step))
  *   / (sqrt(v / (1 - beta2^step)) + eps).
  *   grad, weight F32 or BF16 (each its own), exp_avg, exp_avg_sq F32; copy
- *   (array may be NULL, entries may be empty) receives the new weight, for a
- *   model that computes on 16-bit copies of 32-bit weights. All arithmetic is
- *   fp32; a BF16 weight is rounded to nearest even once a step. step counts
+ *   (array may be NULL, entries may be empty) receives the same fp32 result as
+ *   the weight, rounded to the copy's own type, for a model that computes on
+ *   16-bit copies of 32-bit weights; an F32 copy of a BF16 weight is therefore
+ *   the value that the weight was rounded from, not the weight. All arithmetic
+ *   is fp32; a BF16 weight is rounded to nearest even once a step. step counts
  *   from 1. Every tensor is read and written once.
  *   lr and step are constants of the launch: a graph that captured the call
  *   repeats them on every replay. step_at and lr_at (device pointers, each or

@@ -145,8 +145,10 @@ def adamw_update(grads: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor]
     the library's default. grad_scale: a float32 device scalar that multiplies
     every gradient (`grad_norm`'s coefficient). step (int64) and lr (float32) may
     be one-element tensors on the device, read when the kernel runs: a captured
-    graph repeats numbers, and counts its steps with tensors. copies[i], when given, receives
-    the new weight, for a model that computes on 16-bit copies of 32-bit ones."""
+    graph repeats numbers, and counts its steps with tensors. copies[i], when
+    given, receives the new weight's 32-bit value rounded to its own type, for a
+    model that computes on 16-bit copies of 32-bit weights (a float32 copy of a
+    bfloat16 weight is the value that the weight was rounded from)."""
     weights = list(weights)
     h = _handle_for(weights, handle)
     d, pack = h.device, _describe().pack

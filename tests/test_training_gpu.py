@@ -625,6 +625,21 @@ def test_adamw_mixed_list_and_copies_left_out():
     assert torch.equal(c[1], w[1].to(BF))
 
 
+@pytest.mark.parametrize("wt", [F32, BF])
+@pytest.mark.parametrize("ct", [F32, BF])
+def test_adamw_weight_and_copy_are_roundings_of_one_value(wt, ct):
+    x = normal((257, 130), 1, 0.02).to(wt).float()
+    g = [normal((257, 130), 2, 1e-2)]
+    got = []
+    for wide in (True, False):
+        w, c = [x.clone() if wide else x.to(wt)], [torch.empty(257, 130, device="cuda", dtype=F32 if wide else ct)]
+        m, v = [torch.zeros(257, 130, device="cuda")], [torch.zeros(257, 130, device="cuda")]
+        mu.adamw_update(g, m, v, w, step=1, lr=1e-2, copies=c)
+        got.append((w[0], c[0]))
+    value = got[0][0]
+    assert torch.equal(got[0][1], value) and torch.equal(got[1][0], value.to(wt)) and torch.equal(got[1][1], value.to(ct))
+
+
 def test_adamw_non_finite_gradient_stays_with_its_element():
     w, g = [torch.ones(1000, device="cuda", dtype=BF)], [torch.ones(1000, device="cuda")]
     m, v = [torch.zeros(1000, device="cuda")], [torch.zeros(1000, device="cuda")]
