@@ -423,8 +423,9 @@ muon_status muon_update_static(muon_handle* handle, int n, const muon_matrix* gr
  * grad_scale are device pointers to fp32 values. Lists travel in the kernel
  * arguments, so these calls upload nothing; they can be captured in a graph
  * once a first call of the same sizes has grown the handle's buffers. A buffer
- * that a later call outgrows is kept until muon_destroy, so a captured graph
- * stays valid; like any call it must not run beside others of its handle.
+ * that a later call outgrows is freed (that call waits for the stream), unless a
+ * captured call used it: then it is kept until muon_destroy, so that the graph
+ * stays valid. Like any call a graph must not run beside others of its handle.
  */
 
 /*
@@ -481,9 +482,9 @@ muon_status adamw_update(muon_handle* handle, int n, const muon_matrix* grad, co
 
 /*
  * linear_cross_entropy(_grad) - softmax cross entropy of a language-model
- * head: z = hidden weight^T (N x V, fp32 accumulation, never stored as a
- * whole), with softcap c > 0: z <- c tanh(z / c); loss_i = log sum_v exp z_iv
- * - z_i,target. The gradient is that of sum_i g_i loss_i, g_i = grad_out[i]
+ * head: z = hidden weight^T (N x V, fp32 accumulation; the loss alone
+ * stores none of them), with softcap c > 0: z <- c tanh(z / c); loss_i = log sum_v
+ * exp z_iv - z_i,target. The gradient is that of sum_i g_i loss_i, g_i = grad_out[i]
  * (reduction none), grad_out[0] (sum) or grad_out[0] / valid tokens (mean);
  * grad_out NULL = 1.
  *   hidden   N x D; weight V x D, same type, F32 or BF16 (D <= 65536,
@@ -498,10 +499,15 @@ muon_status adamw_update(muon_handle* handle, int n, const muon_matrix* grad, co
  *            them may be NULL (its product is left out)
  * BF16 inputs are multiplied on the bf16 matrix cores (the logits' gradient
  * is rounded to bf16 once), F32 ones in fp32 throughout; statistics and sums
- * are fp32. The handle keeps up to about 1.6 GiB for the pieces of tokens (256
- * at least), plus, when a call takes more than one piece, an fp32 V x D sum,
- * and a padded copy of a weight whose rows are not whole 16-byte pieces that
- * start on 16 bytes.
+ * are fp32. The tokens are taken in pieces; with gradients a piece's V
+ * exponentials a token (2 bytes each, F32 4) are kept beside its rows, as much as
+ * the logits of these tokens would take.
+ * Memory of the handle (each handle has its own; the Python binding has one a
+ * thread): the pieces, up to 1 GiB, or 256 tokens' if these take more; partial
+ * sums of each gradient, up to 256 MB; 12 bytes a token of the call; when a call takes more than one piece, an
+ * fp32 V x D sum; a padded copy of a weight whose rows are not whole 16-byte
+ * pieces that start on 16 bytes. A buffer that grows takes up to half as much
+ * again, 256 MiB at most.
  */
 typedef enum { MUON_REDUCE_NONE = 0, MUON_REDUCE_SUM = 1, MUON_REDUCE_MEAN = 2 } muon_reduction;
 typedef struct {

@@ -1476,21 +1476,45 @@ hipStream_t handle_stream(const muon_handle* h) { return h->stream; }
 int handle_device(const muon_handle* h) { return h->device; }
 muon_status handle_error(muon_handle* h, muon_status code, const std::string& msg) { return set_err(h, code, msg); }
 void handle_clear_error(muon_handle* h) { h->err.clear(); }
-muon_status grow(muon_handle* h, GrowBuffer& b, size_t bytes, const char* what) {
-  if (bytes <= b.bytes && b.ptr) return MUON_OK;
-  const size_t more = b.ptr ? std::max(bytes, b.bytes + b.bytes / 2) : bytes;
-  b.outgrown.reserve(b.outgrown.size() + 1);
-  void* p = nullptr;
-  if (hipMalloc(&p, more) == hipSuccess) {
-    bytes = more;
-  } else if ((void)hipGetLastError(), more == bytes || hipMalloc(&p, bytes) != hipSuccess) {
-    (void)hipGetLastError();
-    return set_err(h, MUON_ERR_ALLOC,
-                   std::string(what) + " workspace of " + std::to_string(bytes) + " bytes: allocation failed");
+bool handle_capturing(const muon_handle* h) {
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(h->stream, &st) != hipSuccess) {
+    (void)hipGetLastError();       // (the default stream, while another one is captured)
+    return false;
   }
-  if (b.ptr) b.outgrown.push_back(b.ptr);
+  return st != hipStreamCaptureStatusNone;
+}
+muon_status grow(muon_handle* h, GrowBuffer& b, size_t bytes, const char* what) {
+  const bool capturing = handle_capturing(h);
+  if (bytes <= b.bytes && b.ptr) {
+    b.captured = b.captured || capturing;
+    return MUON_OK;
+  }
+  size_t more = b.ptr ? std::max(bytes, b.bytes + std::min(b.bytes / 2, kGrowMost)) : bytes;
+  if (b.ptr) {
+    b.outgrown.reserve(b.outgrown.size() + 1);
+    // the work before this call is on the handle's stream
+    if (b.captured || capturing || hipStreamSynchronize(h->stream) != hipSuccess || hipFree(b.ptr) != hipSuccess) {
+      (void)hipGetLastError();
+      b.outgrown.push_back(b.ptr);
+    }
+    b.ptr = nullptr;
+    b.bytes = 0;
+    b.captured = false;
+  }
+  void* p = nullptr;
+  if (hipMalloc(&p, more) != hipSuccess) {
+    (void)hipGetLastError();
+    if (more == bytes || hipMalloc(&p, more = bytes) != hipSuccess) {
+      (void)hipGetLastError();
+      return set_err(h, MUON_ERR_ALLOC,
+                     std::string(what) + " workspace of " + std::to_string(bytes) + " bytes: allocation failed" +
+                         (capturing ? " (a captured call needs one of its sizes before the capture)" : ""));
+    }
+  }
   b.ptr = p;
-  b.bytes = bytes;
+  b.bytes = more;
+  b.captured = capturing;
   return MUON_OK;
 }
 }  // namespace muon

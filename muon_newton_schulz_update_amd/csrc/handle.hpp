@@ -12,12 +12,15 @@ namespace muon {
 
 // A device buffer that grows on demand and is freed with the handle. Each
 // user has its own: the Newton-Schulz workspace keeps zero padding that no
-// other kernel may write. What it outgrows is kept until then too: a captured
-// graph may still replay on it. It grows at least by half, so all that is kept
-// is at most twice its size.
+// other kernel may write. What it outgrows is freed, unless a call on it was
+// captured: then a graph may still replay on it, and it is kept until the
+// handle goes. It grows at least by half, but by no more than kGrowMost past
+// what is asked for.
+constexpr size_t kGrowMost = size_t(256) << 20;
 struct GrowBuffer {
   void* ptr = nullptr;
   size_t bytes = 0;
+  bool captured = false;         // a captured call uses it
   std::vector<void*> outgrown;
   void release() {
     if (ptr) (void)hipFree(ptr);
@@ -25,6 +28,7 @@ struct GrowBuffer {
     outgrown.clear();
     ptr = nullptr;
     bytes = 0;
+    captured = false;
   }
 };
 struct TrainState {
@@ -38,6 +42,9 @@ hipStream_t handle_stream(const muon_handle* h);
 int handle_device(const muon_handle* h);
 muon_status handle_error(muon_handle* h, muon_status code, const std::string& msg);
 void handle_clear_error(muon_handle* h);
+bool handle_capturing(const muon_handle* h);     // whether the handle's stream is being captured
+// At least `bytes` of b for a call that is about to be enqueued (to be called
+// for every use: it notes the captured ones).
 muon_status grow(muon_handle* h, GrowBuffer& b, size_t bytes, const char* what);
 
 }  // namespace muon

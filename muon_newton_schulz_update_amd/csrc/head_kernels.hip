@@ -1,5 +1,6 @@
 // Softmax cross entropy of a language-model head, z = H W^T, with its
-// gradient, without the n x V logits: tokens are taken in pieces.
+// gradient. The loss alone stores no logits; with gradients a piece of tokens
+// keeps one exponential a logit, in the operands' size.
 //
 //   compact    the valid tokens (target != ignore_index) in order; ignored
 //              ones are never read, so what their rows hold does not matter

@@ -71,11 +71,10 @@ muon_status norm_run(muon_handle* h, int n, const muon_matrix* g, float max_norm
     total += std::min(chunks, kNormBlocks);
   }
   const size_t need = sizeof(NormState) + (size_t)total * sizeof(double);
-  if (need > ts.norm.bytes) {
-    if (muon_status e = grow(h, ts.norm, std::max(need, size_t(64) << 10), "gradient norm")) return e;
-    ts.norm_clean = false;
-  }
-  if (!ts.norm_clean) {
+  const void* before = ts.norm.ptr;
+  if (muon_status e = grow(h, ts.norm, std::max(need, size_t(64) << 10), "gradient norm")) return e;
+  const bool clean = ts.norm_clean && ts.norm.ptr == before;
+  if (!clean) {
     // a new buffer, or a call that ended between its launches
     HIP_DO(h, launch_norm_reset((NormState*)ts.norm.ptr, s));
   }
@@ -88,7 +87,7 @@ muon_status norm_run(muon_handle* h, int n, const muon_matrix* g, float max_norm
     HIP_DO(h, launch_norm(L, blocks, chunks, (NormState*)ts.norm.ptr, part0, total, max_norm, norm, coef, s));
     part0 += blocks;
   }
-  ts.norm_clean = true;
+  ts.norm_clean = clean || !handle_capturing(h);   // (a captured reset has not run yet)
   return MUON_OK;
 }
 

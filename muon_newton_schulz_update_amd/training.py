@@ -223,7 +223,8 @@ def linear_cross_entropy_grad(hidden: torch.Tensor, weight: torch.Tensor, target
                               dweight: torch.Tensor | None | bool = None, handle=None):
     """(loss, dhidden, dweight): softmax cross entropy of the logits hidden
     weight^T against targets, and its gradient, in one call (libmuon
-    `linear_cross_entropy_grad`); the logits are never stored as a whole.
+    `linear_cross_entropy_grad`). Pieces of tokens at a time: what is kept of a
+    piece's logits (2 bytes each, float32 4) takes up to 1 GiB of the handle.
 
     hidden: (..., D), targets: (...) int64 or int32, weight: (V, D). grad_out
     (float32, on the device): one value that multiplies the gradient, or with
@@ -277,8 +278,9 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: to
                          handle=None) -> torch.Tensor:
     """Softmax cross entropy of the logits hidden weight^T against targets,
     float32: one value ("mean" over the tokens whose target is not
-    ignore_index, "sum") or one a token ("none", 0 where ignored). The logits
-    are never stored as a whole.
+    ignore_index, "sum") or one a token ("none", 0 where ignored). The loss
+    alone stores no logits; a call that computes the gradient keeps a piece's, as
+    `linear_cross_entropy_grad` says.
 
     Differentiable in hidden and weight, in reverse mode (a tensor with a
     forward-mode tangent is refused). "mean" and "sum" compute the gradient with

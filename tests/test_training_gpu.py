@@ -685,6 +685,49 @@ def test_training_step_in_a_graph():
             torch.zeros(1 << 20, device="cuda").sum()
 
 
+def test_outgrown_workspace_is_freed():
+    """Calls of growing size on one handle hold one workspace at the end, not all that they outgrew."""
+    v, d = 50304, 64
+    h, w, t = make(8192, v, d, BF, seed=72)
+    handle = mu.Handle()
+    torch.cuda.synchronize()
+    held = lambda: torch.cuda.mem_get_info()[1] - torch.cuda.mem_get_info()[0] - torch.cuda.memory_reserved()
+    before = held()
+    for n in (256, 512, 1024, 2048, 4096, 8192):
+        got = mu.linear_cross_entropy_grad(h[:n], w, t[:n], handle=handle)
+    torch.cuda.synchronize()
+    # the exponentials, and at most as much again of the rest as they may grow by
+    assert held() - before <= 8192 * 50432 * 2 + (320 << 20)
+    handle.close()
+    want = mu.linear_cross_entropy_grad(h, w, t)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_graph_replays_on_a_workspace_that_was_outgrown():
+    h, w, t = make(300, 1000, 128, BF, seed=73, ignored=0.1)
+    big = make(3000, 1500, 128, BF, seed=74)
+    many = [normal((33,), i) for i in range(3000)]
+    handle, s = mu.Handle(), torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        call = lambda: (*mu.linear_cross_entropy_grad(h, w, t, handle=handle), mu.grad_norm([h, w], handle=handle))
+        want = call()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = call()
+        for k in range(3):
+            for x in out:
+                x.fill_(float("nan"))
+            graph.replay()
+            s.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want)), k
+            mu.linear_cross_entropy_grad(*big, handle=handle)          # outgrows the captured workspace
+            mu.grad_norm(many * (k + 1), handle=handle)
+            torch.full((1 << 22,), float("nan"), device="cuda")
+        s.synchronize()
+    handle.close()
+
+
 @pytest.mark.parametrize("wt", [F32, BF])
 def test_adamw_in_a_graph_counts_its_steps(wt):
     """Step and rate on the device, changed between the replays, against the call with their numbers. The moments do
