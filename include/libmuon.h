@@ -497,9 +497,11 @@ muon_status adamw_update(muon_handle* handle, int n, const muon_matrix* grad, co
  *            0 if there is none
  *   dhidden, dweight  gradients, of the types of hidden and weight; one of
  *            them may be NULL (its product is left out)
- * BF16 inputs are multiplied on the bf16 matrix cores (the logits' gradient
- * is rounded to bf16 once), F32 ones in fp32 throughout; statistics and sums
- * are fp32. The tokens are taken in pieces; with gradients a piece's V
+ * BF16 inputs are multiplied on the bf16 matrix cores: a logit's gradient is
+ * rounded to 10 bits of mantissa (its kept exponential) and then to bf16, but
+ * the target's, most of a token's, counts with 16 bits; grad_out and 1 / valid
+ * tokens multiply the fp32 sums. F32 inputs are fp32 throughout; statistics and
+ * sums are fp32. The tokens are taken in pieces; with gradients a piece's V
  * exponentials a token (2 bytes each, F32 4) are kept beside its rows, as much as
  * the logits of these tokens would take.
  * Memory of the handle (each handle has its own; the Python binding has one a

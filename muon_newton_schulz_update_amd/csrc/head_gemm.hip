@@ -48,13 +48,13 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 
 enum OpLayout { OP_ROW_K, OP_GATHER_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
 
-constexpr int kFewTokens = 64;    // whose dW takes the targets' remainders too
 constexpr float kLog2e = 1.44269504088896341f;
 
 template <int n>
@@ -704,6 +704,147 @@ __device__ __forceinline__ void dhidden_tile(const HeadArgs& a, uint8_t* smem, i
 }
 
 // ---------------------------------------------------------------------------
+// What the targets' own gradients lost in their rounding to 16 bits, times the
+// tokens' rows, to dW's accumulators. That one term is most of a word's gradient
+// where few tokens have it as their target: without it dW of 65 x 8000 x 256 is
+// 1.99e-3 off and of 8192 x 50304 x 768 1.90e-3, with it 1.66e-3, which is the
+// output's own rounding. (The other words' terms are small, and their roundings
+// add nothing that shows.)
+// A tile lists the tokens t0 to t1 of the piece whose target is among its rows
+// and takes them 64 at a time through one more stage of its product: their
+// hidden rows gathered to LDS (from the caller's matrix, a row's chunks side by
+// side, where these are whole 16-byte pieces; from the panels otherwise), and
+// beside them a matrix that holds each remainder (in 16 bits again: sixteen of
+// the target's gradient in all) in its token's and word's place and is zero
+// elsewhere. The lists keep the tokens' order, so the sums repeat.
+// Measured, without / with: 8192 x 50304 x 768 1999 / 2016 us, 1000 x 8000 x 256
+// 55.5 / 58.5, 300 x 50304 x 2048 365 / 382; most where many tokens share few
+// words, whose tiles have the longest lists: 8192 x 2000 x 512 111 / 134.
+// ---------------------------------------------------------------------------
+// A wave's targets of a window of tokens, as they are in memory.
+template <int TILE, int NW>
+struct TargetWindow {
+  static constexpr int kTokens = 16 * TILE;                     // (their lists fit the ring)
+  static constexpr int kShare = kTokens / NW, kLoads = kShare / 256;
+  i32x4_t at[kLoads];
+  __device__ __forceinline__ static int token(int w0, int wave, int lane, int l) {
+    return w0 + wave * kShare + (l * 64 + lane) * 4;
+  }
+  // whole pieces of four (the list of targets is padded), the last one again past the end
+  __device__ __forceinline__ void load(const HeadArgs& a, int lane, int wave, int w0, int t1) {
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l)
+      at[l] = *(const i32x4_t*)(a.tgt + a.row0 + min(token(w0, wave, lane, l), (t1 - 1) & ~3));
+  }
+};
+template <int TILE, int NW, int MI, int NI>
+__device__ __forceinline__ void add_target_rests(f32x16_t (&acc)[MI][NI], const HeadArgs& a, uint8_t* smem,
+                                                 const Operand& rows, TargetWindow<TILE, NW>& window, int lane, int wave,
+                                                 int am, int bn, int v0, int d0, int t0, int t1) {
+  typedef Op<u16, OP_ROW_T, TILE, NW> R;                        // the gathered rows
+  typedef Op<u16, OP_PANEL_T, TILE, NW> O;                      // the remainders
+  typedef TargetWindow<TILE, NW> Window;
+  constexpr int kShare = Window::kShare, LPO = TILE / 8 / NW;
+  uint8_t* sb = smem + 2 * TILE * 128;                          // after two slots for the gathered rows
+  uint32_t* list = (uint32_t*)(sb + TILE * 128);                // token | word << 16, each wave's share
+  uint2* places = (uint2*)(list + Window::kTokens);             // row's offset, remainder | word << 16
+  int* counts = (int*)(places + Window::kTokens);
+  const uint64_t below = (1ull << lane) - 1;
+  const uint8_t* base = a.rows_direct ? (const uint8_t*)a.h + d0 * 2 : rows.base;
+  auto all_waves = [&]() {
+    wait_lgkm0();
+    ring_barrier();
+  };
+  bool cleared = false;
+  for (int w0 = t0; w0 < t1; w0 += Window::kTokens) {
+    if (w0 != t0) window.load(a, lane, wave, w0, t1);           // (the first one's came beside the product)
+    all_waves();                                                // the slots, and the list before, have been read
+    int found = 0;
+#pragma unroll
+    for (int l = 0; l < Window::kLoads; ++l) {
+      const int token = Window::token(w0, wave, lane, l);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int word = window.at[l][c] - v0;
+        const bool hit = token + c < t1 && word >= 0 && word < TILE;
+        const uint64_t m = __ballot(hit);
+        if (hit) list[wave * kShare + found + __popcll(m & below)] = (uint32_t)(token + c) | (uint32_t)word << 16;
+        found += __popcll(m);
+      }
+    }
+    if (lane == 0) counts[wave] = found;
+    all_waves();
+    int upto[NW], all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) upto[w] = all += counts[w];
+    all = __builtin_amdgcn_readfirstlane(all);
+    if (all == 0) continue;
+    // the shares put together, and what the stages need of each token
+    for (int h = wave * 64 + lane; h < all; h += NW * 64) {
+      int at = h;
+#pragma unroll
+      for (int w = 0; w < NW - 1; ++w)
+        if (h >= upto[w]) at = (w + 1) * kShare + h - upto[w];
+      const uint32_t entry = list[at], token = entry & 0xFFFF;
+      const uint32_t off = a.rows_direct ? (uint32_t)a.idx[a.row0 + token] * (uint32_t)(a.ld_h * 2)
+                                         : (token >> 6) * rows.pitch + (token & 63) * 16;
+      places[h] = make_uint2(off, pack_bf16(a.rs[token].w, 0.f) | (entry & 0xFFFF0000u));
+    }
+    if (!cleared)
+      for (int b = (wave * 64 + lane) * 16; b < TILE * 128; b += NW * 1024) *(u32x4_t*)(sb + b) = (u32x4_t){0, 0, 0, 0};
+    cleared = true;
+    all_waves();
+    // tokens h0.. h0 + 63 of the list, one to a lane (past the last, that one
+    // again: its second place in the sum is 0): their rows on their way to a slot
+    auto fetch = [&](int h0, int slot) {
+      const uint2 p = places[min(h0 + lane, all - 1)];
+      const int step = a.rows_direct ? 16 : 1024;               // from chunk to chunk of a token's row
+#pragma unroll
+      for (int i = 0; i < LPO; ++i) {
+        const int g = NW * i + wave, row = R::kRowsPerLoad * g + lane / (64 / R::kRowsPerLoad);
+        const int c = min((lane % (64 / R::kRowsPerLoad)) ^ R::row_t_swizzle(row), rows.lim);
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, -1, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(smem + slot * TILE * 128 + g * 1024), 16,
+                                                 __shfl(p.x, row) + c * step, 0, 0, 0);
+      }
+      return p.y;
+    };
+    uint32_t mark = fetch(0, 0), next_mark = 0;
+    for (int h0 = 0, slot = 0; h0 < all; h0 += 64, slot ^= 1) {
+      const int word = mark >> 16;
+      u16* place = (u16*)(sb + (word >> 3) * 1024 + ((lane ^ ((word >> 3 & 3) << 2)) * 16) + (word & 7) * 2);
+      const bool mine = wave == 0 && h0 + lane < all;
+      if (mine) *place = (u16)mark;
+      if (h0 + 64 < all) {
+        next_mark = fetch(h0 + 64, slot ^ 1);
+        wait_vm<LPO>();                                         // no more than the next ones' rows on their way
+      } else {
+        wait_vm<0>();
+      }
+      all_waves();
+      const uint8_t* sa = smem + slot * TILE * 128;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        bf16x8_t fa[MI], fb[NI];
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) fa[mi] = R::template frag<bf16x8_t>(sa, lane, am + mi * 32, s);
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) fb[ni] = O::template frag<bf16x8_t>(sb, lane, bn + ni * 32, s);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni)
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[mi], fb[ni], acc[mi][ni], 0, 0, 0);
+      }
+      all_waves();                                              // the slot and the places have been read
+      if (mine) *place = 0;
+      mark = next_mark;
+    }
+  }
+  if (cleared) wait_lgkm0();                                    // (the last places, before others write the slots)
+}
+
+// ---------------------------------------------------------------------------
 // dW: the piece's sum, or a part of its tokens', added to the pieces before
 // it; the last one is scaled and rounded to the weight's type. The width is on the accumulators' rows, so
 // a lane has four neighbouring columns of one weight row; the results are put
@@ -731,38 +872,16 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = (f32x16_t){};
   const int nk = (rows + O::KE - 1) / O::KE;
   const int k0 = (int)((int64_t)nk * part / a.wsplit), k1 = (int)((int64_t)nk * (part + 1) / a.wsplit);
+  TargetWindow<TILE, NW> window;
+  if constexpr (sizeof(T) == 2)
+    if (k1 > k0) window.load(a, lane, wave, k0 * O::KE, min(k1 * O::KE, rows));
   if (k1 > k0)
     k_loop<T, OP_PANEL_T, OP_PANEL_T, TILE, NW, S, MI, NI>(acc, smem, oa, ob, lane, wave, wm * MI * 32, wn * NI * 32, k0, k1);
+  if constexpr (sizeof(T) == 2)
+    add_target_rests<TILE, NW, MI, NI>(acc, a, smem, oa, window, lane, wave, wm * MI * 32, wn * NI * 32, v0, d0, k0 * O::KE,
+                                       min(k1 * O::KE, rows));
   const float g = common_factor(a);
   const int vw = v0 + wn * NI * 32, dw = d0 + wm * MI * 32;      // the wave's part
-  if constexpr (sizeof(T) == 2 && TILE < 256) {
-    // few tokens (which never have 256-tiles: kFewTokens < kShortK), one to a
-    // lane: what the targets' gradients lost in their rounding, for those with
-    // their target among the wave's rows (one piece: row0 is 0)
-    const bool few = a.n <= kFewTokens && lane < rows;
-    const int lane_at = few ? a.tgt[lane] - vw : -1;
-    const float lane_rest = few ? a.rs[lane].w : 0.f;
-    uint64_t todo = __ballot(lane_at >= 0 && lane_at < NI * 32 && lane_rest != 0.f);
-    for (; todo; todo &= todo - 1) {
-      const int i = __builtin_ctzll(todo), at = __builtin_amdgcn_readlane(lane_at, i);
-      const float rest = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_rest), i));
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        if (at != ni * 32 + lr) continue;
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int d = dw + mi * 32 + 8 * q + 4 * hf;
-            if (d >= a.dp) continue;
-            const u32x2_t h = *(const u32x2_t*)((const u16*)a.hp + panel_at<u16>(i, d, a.dp));
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc[mi][ni][4 * q + e] = fmaf(rest, bf2f((u16)(h[e >> 1] >> (16 * (e & 1)))), acc[mi][ni][4 * q + e]);
-          }
-      }
-    }
-  }
   const bool split = a.wsplit > 1;
   if (split || a.dwacc) {
     // sums over parts or pieces: padded rows, whole 16-byte groups
@@ -991,7 +1110,7 @@ void head_plan(HeadArgs& a, int dt) {
   const double h_sum = (double)rows * a.dp * 8 / bytes, w_sum = (double)a.v * a.dp * 8 / bytes;
   // (partial sums stay within 256 MB, and a part has four stages or more)
   const int h_most = a.dh ? (int)std::min<double>(std::min<int64_t>(256, stages / 4), 256e6 / ((double)a.piece * a.dp * 4)) : 1;
-  const int w_most = a.dw && a.n > kFewTokens ? (int)std::min<double>(std::min<int64_t>(256, wstages / 4), 256e6 / ((double)a.v * a.dp * 4)) : 1;
+  const int w_most = a.dw ? (int)std::min<double>(std::min<int64_t>(256, wstages / 4), 256e6 / ((double)a.v * a.dp * 4)) : 1;
   double least = 0;
   for (int m = 1; m == 1 || m <= w_most; m *= 2) {
     for (int n = 1; n == 1 || n <= h_most; n += (n + 7) / 8) {

@@ -25,13 +25,14 @@
 //              sum of the parts written to the tokens' rows, with what the
 //              target's own gradient lost in its rounding to 16 bits times the
 //              target's row: that one term is most of a token's gradient
-//   dweight    dz^T H, in parts of the tokens where tiles are few, summed over
-//              parts and pieces in 32 bits; with few tokens, whose roundings no
-//              sum averages, also those remainders
+//   dweight    dz^T H, in parts of the tokens where tiles are few, with the same
+//              remainders, summed over parts and pieces in 32 bits
 //
-// The products are in head_gemm.hip. A 16-bit exponential carries an eighth of
-// the rounding of the bf16 value it becomes, so the gradient's one rounding is
-// the one to bf16.
+// The products are in head_gemm.hip. A logit's gradient of 16-bit inputs is
+// rounded twice: as its kept exponential (an eighth of bf16's rounding, chosen so
+// that a logit takes 2 bytes) and as an operand of the 16-bit matrix cores. The
+// target's loses neither: its 32-bit value is in the product's operand and the
+// remainder.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -156,6 +156,7 @@ struct HeadArgs {
   int32_t wsplit;                     // parts of the piece's tokens in dW
   int32_t logit_tile, grad_tile;      // tile edges of the products
   int32_t gather;                     // the logits read the hidden rows themselves
+  int32_t rows_direct;                // hidden rows are whole 16-byte pieces within 2 GiB
   float* dwacc;                       // v x dp fp32 sum over pieces, or null: one piece
   int32_t first, last;                // this piece starts / ends the sum over pieces
   float* loss;                        // caller's: one value, or n

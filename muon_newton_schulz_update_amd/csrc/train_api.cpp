@@ -177,6 +177,8 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   // no panels
   a.gather = !grad && direct && a.n > 0 && a.n <= kGatherTokens && a.logit_tile < 256 && (uintptr_t)hid.ptr % 16 == 0 &&
              (a.n == 1 || (hid.ld * e % 16 == 0 && hid.ld * e < (1 << 23)));
+  a.rows_direct = a.d * e % 16 == 0 && (uintptr_t)hid.ptr % 16 == 0 &&
+                  (a.n == 1 || (hid.ld * e % 16 == 0 && hid.ld < (int64_t(1) << 31) / e / std::max(a.n, 1)));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;

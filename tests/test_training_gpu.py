@@ -363,6 +363,45 @@ def test_cross_entropy_of_few_tokens(n, v, d, ignored, dtype):
     assert bool(mu.linear_cross_entropy(h, w, t, reduction="none")[0].isnan())
 
 
+@pytest.mark.parametrize("n,v,d,pad,words,softcap", [
+    (65, 3000, 64, 0, 3000, 0.0), (64, 3000, 64, 0, 3000, 0.0), (300, 5003, 136, 0, 40, 0.0), (300, 5003, 129, 3, 5003, 20.0),
+    (1000, 200, 72, 0, 200, 0.0), (5000, 300, 64, 0, 1, 0.0), (5000, 300, 40, 5, 300, 0.0), (9000, 40000, 256, 0, 40000, 0.0),
+    (9000, 40000, 256, 1, 300, 0.0), (20000, 700, 128, 0, 700, 0.0), (13000, 50000, 40, 0, 50000, 0.0)])
+def test_cross_entropy_targets_gradient_keeps_sixteen_bits(n, v, d, pad, words, softcap):
+    """A token's gradient is mostly its target's: in 16-bit calls too that term has 2^-17 of itself (its rounding's
+    remainder is added, in 16 bits again) and the softmax's 32-bit error, for any number of tokens, also of one word,
+    in rows of whole 16-byte pieces or not. The other words' terms have the 2^-8 and 2^-11 of their roundings."""
+    h, w, t = make(n, v, d, BF, seed=35, ignored=0.1)
+    t = torch.where(t == -100, t, t % words)
+    buf = torch.zeros((n, d + pad), device="cuda", dtype=BF)
+    buf[:, :d] = h
+    _, dh, dw = mu.linear_cross_entropy_grad(buf[:, :d], w, t, reduction="sum", softcap=softcap)
+    w64 = w.double()
+    want_w, err_w = torch.zeros_like(w64), torch.zeros_like(w64)
+    for i in range(0, n, 4096):
+        hi, ti = h[i:i + 4096].double(), t[i:i + 4096]
+        keep = (ti != -100)[:, None]
+        raw = mm(hi, w64.t())
+        z = softcap * torch.tanh(raw / softcap) if softcap else raw
+        at = torch.where(ti == -100, 0, ti)[:, None]
+        zt = z.gather(1, at)
+        lse = torch.logsumexp(z, 1, keepdim=True)
+        others = torch.logsumexp((z - zt).scatter(1, at, float("-inf")), 1, keepdim=True)
+        dz = (d + 2) * U * mm(hi.abs(), w64.abs().t()).amax(1, keepdim=True) + (12 * U * z.abs().amax(1, keepdim=True) if softcap else 0)
+        each = 2 * dz + (512 + v / 64) * U + 4 * U * (lse.abs() + zt.abs() + z.abs().amax(1, keepdim=True))
+        f = 1 - (z / softcap) ** 2 if softcap else 1.0
+        q = torch.exp(z - lse).scatter(1, at, -torch.sigmoid(others)) * f * keep
+        rel = (2 * each + 16 * U + (4 * dz / softcap / f if softcap else 0) + 2.0 ** -8 + 2.0 ** -11).expand_as(q)
+        rel = rel.scatter(1, at, (rel - 2.0 ** -8 - 2.0 ** -11 + 2.0 ** -17).gather(1, at))
+        q_err = q.abs() * rel + 2.0 ** -62 * keep
+        want_h = mm(q, w64)
+        within(dh[i:i + 4096], want_h, mm(q_err + (v + 8) * U * q.abs(), w64.abs()) + 2.0 ** -8 * want_h.abs() + 1e-38, "dhidden")
+        want_w += mm(q.t(), hi)
+        err_w += mm((q_err + (n + 8) * U * q.abs()).t(), hi.abs())
+        del raw, z, f, q, rel, q_err
+    within(dw, want_w, err_w + 2.0 ** -8 * want_w.abs() + 1e-38, "dweight")
+
+
 def test_cross_entropy_repeats_bit_for_bit_and_on_other_streams():
     h, w, t = make(700, 3001, 192, BF, seed=22, ignored=0.1)
     first = mu.linear_cross_entropy_grad(h, w, t)
