@@ -25,6 +25,10 @@ bool describe(const at::Tensor& t, const char* what, long device, muon_matrix* m
     PyErr_Format(PyExc_ValueError, "%s: expected a dense tensor", what);
     return false;
   }
+  if (t.is_neg()) {
+    PyErr_Format(PyExc_ValueError, "%s: a negated view holds its values with the other sign", what);
+    return false;
+  }
   if (t._fw_grad(0).defined()) {
     // (the kernels see the values alone: the result would have no tangent)
     PyErr_Format(PyExc_ValueError, "%s: a forward-mode tangent cannot be carried through", what);

@@ -177,6 +177,18 @@ def test_loss_rules():
     expect(check(loss=B - 8, cfg=mu.LossConfig(0, 0.0, 0)), INVALID, "share memory")
 
 
+def test_negated_views_are_refused():
+    """Their memory holds the other sign."""
+    import torch
+
+    pack = mu.training._describe().pack
+    z = torch.ones(4, 1, dtype=torch.complex64)
+    for view in (torch.imag(z.conj()), torch._neg_view(torch.ones(2, 3)), torch._neg_view(torch.ones(0, 3))):
+        assert view.is_neg()
+        with pytest.raises(ValueError, match="negated"):
+            pack((view,), "hidden", 0)
+
+
 def test_tensors_with_a_forward_tangent_are_refused():
     """Describing one would drop its tangent without a word."""
     import torch
