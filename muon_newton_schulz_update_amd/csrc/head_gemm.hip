@@ -1003,13 +1003,18 @@ inline int xcd_grid(int n) { return 8 * rounds_of(n) * run_of(n, rounds_of(n)); 
 // 66 us, 300 x 50304 x 768 211 / 247, 1987 x 30961 x 704 686 / 685, 4000 x 3000
 // x 1024 215 / 211; 256-tiles would not fit the registers).
 constexpr int kFewTiles = 768, kFewSmallTiles = 384;
+// Tokens that fill at most half of a 256-tile: 128-tiles however large the
+// vocabulary (128 / 256, 200000 x 768: 1 token 78.9 / 103.4 us, 64 96.1 / 118.1,
+// 128 108.1 / 126.0, 129 139.3 / 129.1; 262144 x 2048: 128 279.8 / 307.4, 129
+// 350.4 / 310.4).
+constexpr int kHalfTile = 128;
 // 64-tiles that all fit the chip two to a CU: a ring of nine slots, whose loads
 // are asked for three and a half stages ahead. Such a launch reads its operands
 // for the first time, and a stage waits for memory rather than for its products.
 constexpr int kDeepTiles = 512;
-int tile_of(int dt, int64_t tiles256, int64_t tiles128) {
+int tile_of(int dt, int rows, int64_t tiles256, int64_t tiles128) {
   if (dt != MUON_BF16) return 64;
-  if (tiles256 >= kFewTiles) return 256;
+  if (tiles256 >= kFewTiles && rows > kHalfTile) return 256;
   return tiles128 >= kFewSmallTiles ? 128 : 64;
 }
 // The gradients' tiles also go by their own shape (whole calls):
@@ -1088,7 +1093,7 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
 // 65536 x 256 x 512 646 / 250, fp32 2000 x 300 x 128 78 / 37.
 void head_plan(HeadArgs& a, int dt) {
   const int rows = a.n < a.piece ? a.n : a.piece, unit = dt == MUON_BF16 ? 64 : 32;
-  a.logit_tile = tile_of(dt, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256), (int64_t)cdiv(a.v, 128) * cdiv(rows, 128));
+  a.logit_tile = tile_of(dt, rows, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256), (int64_t)cdiv(a.v, 128) * cdiv(rows, 128));
   a.vtile = a.logit_tile == 64 ? 64 : 128;
   a.n_vt = cdiv(a.v, a.vtile);
   a.split = a.wsplit = 1;

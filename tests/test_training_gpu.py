@@ -363,6 +363,13 @@ def test_cross_entropy_of_few_tokens(n, v, d, ignored, dtype):
     assert bool(mu.linear_cross_entropy(h, w, t, reduction="none")[0].isnan())
 
 
+@pytest.mark.parametrize("n", [1, 64, 128, 129])
+def test_cross_entropy_of_few_tokens_and_a_large_vocabulary(n):
+    """Either side of the tokens from which the widest tiles are taken, at a vocabulary that has many of them."""
+    h, w, t = make(n, 250001, 64, BF, seed=36)
+    check_loss(h, w, t, reduction="none")
+
+
 @pytest.mark.parametrize("n,v,d,pad,words,softcap", [
     (65, 3000, 64, 0, 3000, 0.0), (64, 3000, 64, 0, 3000, 0.0), (300, 5003, 136, 0, 40, 0.0), (300, 5003, 129, 3, 5003, 20.0),
     (1000, 200, 72, 0, 200, 0.0), (5000, 300, 64, 0, 1, 0.0), (5000, 300, 40, 5, 300, 0.0), (9000, 40000, 256, 0, 40000, 0.0),
