@@ -8,6 +8,18 @@
 
 namespace muon {
 
+typedef unsigned short u16;
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+constexpr float kLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ float bf2f(u16 h) { return __uint_as_float((unsigned int)h << 16); }
+// Two values rounded to nearest even (the hardware's packed conversion).
+__device__ __forceinline__ unsigned int pack_bf16(float lo, float hi) {
+  const bf16x2_t q = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(unsigned int, q);
+}
+__device__ __forceinline__ u16 f2bf(float f) { return (u16)pack_bf16(f, 0.f); }
+
 // Lowest reference of a tile's logits: finite, so that a tile of logits at
 // -infinity has exponentials of 0.
 constexpr float kRefFloor = -FLT_MAX;

@@ -41,7 +41,6 @@
 namespace muon {
 namespace {
 
-typedef unsigned short u16;
 typedef __bf16 bf16x8_t __attribute__((__vector_size__(8 * sizeof(__bf16))));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
@@ -55,8 +54,6 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 
 enum OpLayout { OP_ROW_K, OP_GATHER_K, OP_ROW_T, OP_PANEL_K, OP_PANEL_T };
 
-constexpr float kLog2e = 1.44269504088896341f;
-
 template <int n>
 __device__ __forceinline__ void wait_vm() {
   static_assert(n >= 0 && n < 64, "vmcnt immediate");
@@ -67,13 +64,6 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F
 // needs is written before it.
 __device__ __forceinline__ void ring_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-// Two values rounded to nearest even (the hardware's packed conversion).
-__device__ __forceinline__ unsigned int pack_bf16(float lo, float hi) {
-  const bf16x2_t q = {(__bf16)lo, (__bf16)hi};
-  return __builtin_bit_cast(unsigned int, q);
-}
-__device__ __forceinline__ float bf2f(u16 h) { return __uint_as_float((unsigned int)h << 16); }
 // Hand-off through LDS between the lanes of one wave: the LDS executes a
 // wave's accesses in order, so only the compiler has to keep them so.
 __device__ __forceinline__ void wave_lds_sync() {
@@ -81,7 +71,6 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
-
 
 // Transposing LDS read: sixteen lanes give the addresses of four rows, four
 // 16-bit columns each (lanes 0-3 the first row, ...), and lane l gets column l

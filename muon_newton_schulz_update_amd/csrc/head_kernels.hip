@@ -42,26 +42,10 @@
 namespace muon {
 namespace {
 
-typedef unsigned short u16;
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
-constexpr float kLog2e = 1.44269504088896341f;
-
-__device__ __forceinline__ float bf2f(u16 h) { return __uint_as_float((unsigned int)h << 16); }
-__device__ __forceinline__ u16 f2bf(float f) {
-  unsigned int u = __float_as_uint(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u16)((u >> 16) | 0x40);
-  u += 0x7FFFu + ((u >> 16) & 1u);
-  return (u16)(u >> 16);
-}
-// Two values rounded to nearest even (the hardware's packed conversion).
-__device__ __forceinline__ unsigned int pack_bf16(float lo, float hi) {
-  const bf16x2_t q = {(__bf16)lo, (__bf16)hi};
-  return __builtin_bit_cast(unsigned int, q);
-}
 template <typename T> __device__ __forceinline__ float ld(const T* p, int64_t i);
 template <> __device__ __forceinline__ float ld<float>(const float* p, int64_t i) { return p[i]; }
 template <> __device__ __forceinline__ float ld<u16>(const u16* p, int64_t i) { return bf2f(p[i]); }
