@@ -391,12 +391,12 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 // never wait for one another. The exponentials go to the panels as whole chunks
 // after a half-wave swap.
 //
-// Bound by the matrix cores in large calls, whose clock falls under the load
-// (busy 56 % of the time at 1.6 to 1.8 GHz, the rest the epilogue: as many
-// exponentials as results, and 2 bytes of each kept), by the weight's one read
-// for few tokens. Measured: 8192 x 50304 x 768 with the exponentials kept
-// 665 us (950 TFLOP/s and 1.2 TB/s), 6963 x 50304 x 2048 with a soft cap 1210
-// (1190), 1536 x 50304 x 768 without 133 (890); one token x 50304 x 768 16.5
+// In large calls the matrix cores are busy 56 % of the time (at 1.3 to 1.45 GHz;
+// 62 % at 1.8 in a launch of 130 us), the rest is the epilogue: as many
+// exponentials as results, and 2 bytes of each kept; few tokens are bound by the
+// weight's one read. Measured: 8192 x 50304 x 768 with the exponentials kept
+// 672 us (940 TFLOP/s and 1.2 TB/s), 6963 x 50304 x 2048 with a soft cap 1259
+// (1140), 1536 x 50304 x 768 without 131 (905); one token x 50304 x 768 16.6
 // (4.7 TB/s); fp32 1987 x 30961 x 704 680 (127).
 // Two workgroups of 256 x 128 to a CU, so that one's epilogue runs beside the
 // other's products, took 13 % longer (more operand traffic from LDS).
@@ -938,10 +938,10 @@ __device__ __forceinline__ void dweight_tile(const HeadArgs& a, uint8_t* smem, i
 // tiles comes first. In few rounds each kind is dealt to the XCDs by itself,
 // the first to the blocks below `first`; in many (first = 0) one follows the
 // other, which leaves the runs whole (8192 x 50304 x 2048: 3.73 / 3.82 ms).
-// Bound by the matrix cores at the clock that their power leaves (busy 85 % of
-// the time at 1.4 to 1.6 GHz). Measured: 8192 x 50304 x 768 1020 us (1240
-// TFLOP/s of both products), 6963 x 50304 x 2048 2220 (1290), 16 x 3200 x 256
-// 5.5; fp32 777 x 8191 x 331 92 (83).
+// Bound by the matrix cores at their clock under this load (busy 86 % of the time
+// at 1.6 GHz; memory kernels run at 2.2). Measured: 8192 x 50304 x 768 1003 us
+// (1260 TFLOP/s of both products), 6963 x 50304 x 2048 2256 (1270), 16 x 3200 x
+// 256 6; fp32 777 x 8191 x 331 91 (83).
 template <typename T, int TILE, int S>
 __global__ __launch_bounds__((waves_of<T, TILE>() * 64), S > 5 ? 1 : 2) void k_gradients_mfma(HeadArgs a, int vt, int tt, int nd,
                                                                                   int weight_first, int first) {

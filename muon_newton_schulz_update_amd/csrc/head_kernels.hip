@@ -326,7 +326,7 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
 // keeps its token and goes over chunks, so a wave's accesses are whole
 // kilobytes. Rows past the valid ones (up to a whole panel, a stage of dW) and
 // columns past the vocabulary (a stage of dH) become zero. Bound by HBM: a
-// read and a write of every exponential (8192 x 50304 in 16 bits 298 us, 5.5
+// read and a write of every exponential (8192 x 50304 in 16 bits 300 us, 5.5
 // TB/s). The vocabulary is taken from its end, which the logits' launch wrote
 // last and the last-level cache still has, to its start, where the weight's
 // gradient begins (from the start 320 us). With few tiles (merged = 0) every

@@ -235,10 +235,12 @@ __global__ __launch_bounds__(kThreads) void k_scale(ScaleList L, const float* __
 // AdamW with decoupled decay: g' = s g, m = b1 m + (1 - b1) g',
 // v = b2 v + (1 - b2) g'^2, w = w (1 - lr wd) - lr (m / c1) / (sqrt(v / c2) +
 // eps), c = 1 - beta^step; all in fp32, 16-bit weights rounded to nearest
-// even once; a copy takes the same fp32 value, rounded to its own type. Bound by HBM: four reads and three writes of an element, 22 bytes
-// with 16-bit gradients and weights, 28 with 32-bit ones. Measured: 77.3 M
-// elements of bf16 weights 324 us (5.2 TB/s), 12.7 M of fp32 in odd rows with
-// 16-bit copies 76.6 us (4.7), 24 x 768 elements 4.5 us.
+// even once; a copy takes the same fp32 value, rounded to its own type. Bound by
+// HBM: four reads and three writes of an element, 22 bytes with 16-bit gradients
+// and weights, 28 with 32-bit ones. Measured: 77.3 M elements of bf16 weights
+// 324 us (5.2 TB/s); 12.7 M of fp32 in odd rows with 16-bit copies 76 us (4.7)
+// over two lists in turn, 55 (6.5) over one again and again, which the last-level
+// cache keeps; 24 x 768 elements 4.5 us.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void adam(const AdamConst& c, float s, float g, float& m, float& v, float& w) {
   g *= s;
