@@ -740,6 +740,9 @@ __device__ __forceinline__ void add_target_rests(f32x16_t (&acc)[MI][NI], const 
   int* counts = (int*)(places + Window::kTokens);
   const uint64_t below = (1ull << lane) - 1;
   const uint8_t* base = a.rows_direct ? (const uint8_t*)a.h + d0 * 2 : rows.base;
+  // last chunk of the tile's columns: the caller's rows end with their width,
+  // the panels are padded
+  const int last_chunk = a.rows_direct ? (a.d - d0) / 8 - 1 : rows.lim;
   auto all_waves = [&]() {
     wait_lgkm0();
     ring_barrier();
@@ -791,7 +794,7 @@ __device__ __forceinline__ void add_target_rests(f32x16_t (&acc)[MI][NI], const 
 #pragma unroll
       for (int i = 0; i < LPO; ++i) {
         const int g = NW * i + wave, row = R::kRowsPerLoad * g + lane / (64 / R::kRowsPerLoad);
-        const int c = min((lane % (64 / R::kRowsPerLoad)) ^ R::row_t_swizzle(row), rows.lim);
+        const int c = min((lane % (64 / R::kRowsPerLoad)) ^ R::row_t_swizzle(row), last_chunk);
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, -1, 0x00020000);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(smem + slot * TILE * 128 + g * 1024), 16,
                                                  __shfl(p.x, row) + c * step, 0, 0, 0);

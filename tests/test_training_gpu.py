@@ -409,6 +409,25 @@ def test_cross_entropy_targets_gradient_keeps_sixteen_bits(n, v, d, pad, words, 
     within(dw, want_w, err_w + 2.0 ** -8 * want_w.abs() + 1e-38, "dweight")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n,v,d", [(70, 300, 136), (700, 900, 72), (1, 77, 8), (1500, 5000, 328)])
+def test_cross_entropy_rows_that_end_with_their_allocation(n, v, d, dtype):
+    """Rows of whole 16-byte pieces, whose width is no multiple of a stage, as the last bytes of a buffer: no kernel
+    reads a row past its width."""
+    h, w, t = make(n, v, d, dtype, seed=37)
+
+    def last(x):
+        buf = torch.empty(32 << 20, device="cuda", dtype=torch.uint8).view(dtype)
+        y = buf[buf.numel() - x.numel():].view_as(x)
+        assert y.data_ptr() % 16 == 0
+        return y.copy_(x)
+
+    want = mu.linear_cross_entropy_grad(h, w, t)
+    got = mu.linear_cross_entropy_grad(last(h), last(w), t, dhidden=last(h), dweight=last(w))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(mu.linear_cross_entropy(last(h), last(w), t), mu.linear_cross_entropy(h, w, t))
+
+
 def test_cross_entropy_repeats_bit_for_bit_and_on_other_streams():
     h, w, t = make(700, 3001, 192, BF, seed=22, ignored=0.1)
     first = mu.linear_cross_entropy_grad(h, w, t)
