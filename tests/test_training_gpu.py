@@ -160,6 +160,40 @@ def test_cross_entropy_soft_cap_of_any_size(n, v, d, softcap, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("cap", [1e8, 1e16, 1e30])
+@pytest.mark.parametrize("spread", [0.025, 1e-6])
+def test_cross_entropy_huge_logits_under_a_huge_soft_cap(cap, spread, dtype):
+    """Around the place where the cap's two forms meet, which may differ by more than a logit's spacing there: results
+    stay finite, and every token's gradients sum to nothing (their roundings: 2^-8 and 2^-11 of each in bf16)."""
+    n, v = 40, 700
+    h = (cap * (0.625 + spread * (2 * torch.rand((n, v), generator=gen(38), device="cuda") - 1))).to(dtype)
+    t = torch.randint(0, v, (n,), generator=gen(39), device="cuda")
+    w = torch.eye(v, device="cuda").to(dtype)
+    loss, dz, _ = mu.linear_cross_entropy_grad(h, w, t, reduction="none", softcap=cap)
+    only = mu.linear_cross_entropy(h, w, t, reduction="none", softcap=cap)
+    assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(dz).all()) and bool((only >= 0).all())
+    # every probability is in [0, 1] and a slope in [0.66, 0.71] (tanh^2 of 0.6 to 0.65)
+    x = dz.double() / (1 - torch.tanh(h.double() / cap) ** 2)
+    assert bool((x.abs() <= 1.02).all())
+    assert bool((x.sum(1).abs() <= x.abs().sum(1) * (2.0 ** -7 + 16 * U) + 1e-6).all())
+
+
+@pytest.mark.parametrize("first,cap", [(547008118784.0, 1e12), (273504059392.0, 5e11), (8962170817609728.0, 1e16)])
+def test_cross_entropy_huge_logits_whose_caps_fall(first, cap):
+    """Neighbouring 32-bit logits, whose capped values, a rounding each, need not rise with them and are thousands
+    apart: the largest logit's exponential still bounds the others'."""
+    n, v = 400, 200
+    low = torch.full((n,), first, device="cuda").view(torch.int32) + torch.arange(n, device="cuda", dtype=torch.int32)
+    h = low.view(F32)[:, None].repeat(1, v)
+    h[:, 5::16] = (low + 1).view(F32)[:, None]        # some in every wave's rows
+    t = torch.full((n,), 7, device="cuda")
+    w = torch.eye(v, device="cuda")
+    loss, dz, _ = mu.linear_cross_entropy_grad(h, w, t, reduction="none", softcap=cap)
+    assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(dz).all()) and bool((dz.abs() <= 1.0).all())
+    assert bool(torch.isfinite(mu.linear_cross_entropy(h, w, t, reduction="none", softcap=cap)).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("softcap", [1.0, 5.0, 30.0, 1000.0])
 @pytest.mark.parametrize("v", [96, 640])
 def test_cross_entropy_soft_cap_slope_of_saturated_logits(v, softcap, dtype):
