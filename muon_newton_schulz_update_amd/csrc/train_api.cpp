@@ -71,9 +71,9 @@ muon_status norm_run(muon_handle* h, int n, const muon_matrix* g, float max_norm
     total += std::min(chunks, kNormBlocks);
   }
   const size_t need = sizeof(NormState) + (size_t)total * sizeof(double);
-  const void* before = ts.norm.ptr;
+  const size_t before = ts.norm.bytes;    // (a larger buffer can have the freed one's address)
   if (muon_status e = grow(h, ts.norm, std::max(need, size_t(64) << 10), "gradient norm")) return e;
-  const bool clean = ts.norm_clean && ts.norm.ptr == before;
+  const bool clean = ts.norm_clean && ts.norm.bytes == before;
   if (!clean) {
     // a new buffer, or a call that ended between its launches
     HIP_DO(h, launch_norm_reset((NormState*)ts.norm.ptr, s));

@@ -630,6 +630,16 @@ def test_clip_list_longer_than_a_launch():
     assert float(mu.grad_norm([normal((5 + i % 300,), i) for i in range(400)])) == float(n)
 
 
+def test_norm_workspace_grows_between_calls():
+    """Each growth is a new buffer, wherever it lies, whose count of finished blocks has to start at 0."""
+    handle, one = mu.Handle(), torch.full((3,), 2.0, device="cuda")
+    for n in (1, 9000, 1, 14000, 22000, 33000, 2):
+        for _ in range(2):
+            torch.full((1 << 20,), float("nan"), device="cuda")
+            assert float(mu.grad_norm([one] * n, handle=handle)) == float(torch.tensor(math.sqrt(12.0 * n), dtype=F32))
+    handle.close()
+
+
 def test_norm_of_strided_and_unaligned_tensors():
     base = normal((300, 1000), 41)
     views = [base[:, 1:998], base[3:200:2, 8:16], base.view(-1)[1:777], base[:, 5:6], base.to(BF)[:, 3:900]]
