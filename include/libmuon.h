@@ -466,8 +466,9 @@ muon_status muon_scale(muon_handle* handle, int n, const muon_matrix* in, const 
  *   repeats them on every replay. step_at and lr_at (device pointers, each or
  *   both, NULL = the value here) are read when the kernel runs instead, so a
  *   graph can count its steps (a step below 1 gives weights that are not finite).
- * muon_adamw_config_default: lr 0.01, betas (0.8, 0.95), eps 1e-10,
- * weight_decay 0 (the [Aurora page]'s AdamW beside Muon), step 1, no device values.
+ * muon_adamw_config_default (start from it: fields may be added at the end): lr 0.01,
+ * betas (0.8, 0.95), eps 1e-10, weight_decay 0 (the [Aurora page]'s AdamW beside
+ * Muon), step 1, no device values.
  */
 typedef struct {
   float lr, beta1, beta2, eps, weight_decay;

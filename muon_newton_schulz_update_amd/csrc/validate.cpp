@@ -457,7 +457,7 @@ int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void*
 
 namespace {
 
-// A checker's body behind a C entry point: no exception (the lists' spans are
+// A validation's body behind a C entry point: no exception (the lists' spans are
 // on the heap) leaves it.
 template <typename F>
 muon_status checked(char* msg, int len, F body) noexcept {

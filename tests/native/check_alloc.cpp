@@ -1,4 +1,4 @@
-// The host-only checkers when memory runs out, built by
+// The host-only validation when memory runs out, built by
 // tests/test_training_abi.py (CPU only): each allocation of each call fails in
 // turn, and every call returns MUON_ERR_ALLOC with a terminated message; no
 // exception leaves a C entry point.

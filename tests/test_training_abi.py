@@ -219,7 +219,7 @@ def test_training_validation_under_asan_ubsan(tmp_path):
 
 
 @pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
-def test_checkers_when_memory_runs_out(tmp_path):
+def test_validation_when_memory_runs_out(tmp_path):
     exe = tmp_path / "check_alloc"
     r = subprocess.run(["g++", "-std=c++17", "-O1", "-g", f"-I{ROOT}/include", f"-I{ROOT}/muon_newton_schulz_update_amd/csrc",
                         f"{ROOT}/tests/native/check_alloc.cpp", f"{ROOT}/muon_newton_schulz_update_amd/csrc/validate.cpp",
