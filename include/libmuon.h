@@ -528,6 +528,45 @@ muon_status linear_cross_entropy_grad(muon_handle* handle, const muon_matrix* hi
                                       const muon_matrix* dweight);
 
 /*
+ * residual_norm(_grad) - the end of one block and the start of the next, for
+ * each row (token) of the residual stream x and of the block's result y:
+ *   n      = y / sqrt(mean(y^2) + eps) * post_gain      (post_norm 0: n = y)
+ *   out    = scale * x + gate * n
+ *   hidden = out / sqrt(mean(out^2) + eps) * pre_gain   (pre_norm 0: none)
+ * x alone (y NULL): out = scale * x, which need not be stored (out NULL) - the
+ * norm before the first block. Arithmetic is fp32; out and hidden are each
+ * rounded once, from the same fp32 sums. Squares are fp32, too: rows of values
+ * past 2^56 can overflow them.
+ *   x, out     N x D, D <= 16384, F32 or BF16, both of one type
+ *   y, hidden  N x D, both of one type: x's, or BF16 beside an F32 x
+ *   post_gain, pre_gain  D values (NULL: 1)
+ *   gate       one value, D values, or N x D of y's type (NULL: 1)
+ *   scale      one value or D values (NULL: 1)
+ * Parameters are F32 or BF16, each its own; vectors are one row. eps > 0.
+ * residual_norm_grad takes the gradients of out (dout) and hidden (dhidden; each
+ * may be NULL: zero, not both), of the types of out and hidden, and gives those of
+ * the inputs (grads; a NULL one is left out), each of its input's type and
+ * shape. It makes out again from x and y; nothing else of the forward call is
+ * needed. Outputs share no element with any other buffer of the call.
+ * Workspace: fp32 sums of up to 3 D + 4 values for each of up to 1024 blocks.
+ */
+typedef struct {
+  const muon_matrix *post_gain, *pre_gain, *gate, *scale;
+  int32_t post_norm, pre_norm;
+  float eps;
+} muon_norm_params;
+/* no parameters, both norms, eps 1e-6 */
+void muon_norm_params_default(muon_norm_params* p);
+typedef struct {
+  const muon_matrix *x, *y, *post_gain, *gate, *scale, *pre_gain;
+} muon_norm_grads;
+muon_status residual_norm(muon_handle* handle, const muon_matrix* x, const muon_matrix* y,
+                          const muon_norm_params* params, const muon_matrix* out, const muon_matrix* hidden);
+muon_status residual_norm_grad(muon_handle* handle, const muon_matrix* x, const muon_matrix* y,
+                               const muon_norm_params* params, const muon_matrix* dout, const muon_matrix* dhidden,
+                               const muon_norm_grads* grads);
+
+/*
  * Host-only validation with the rules of the calls above; enqueue nothing, need no device.
  * muon_check_norm_args has muon_grad_norm's rules with out NULL (the list is only read: a
  * tensor may be in it twice) and muon_clip_grad_norm's with out, coef apart, which that call
@@ -542,6 +581,12 @@ muon_status muon_check_loss_args(const muon_matrix* hidden, const muon_matrix* w
                                  int target_bytes, const muon_loss_config* cfg, const float* grad_out,
                                  const float* loss, const muon_matrix* dhidden, const muon_matrix* dweight,
                                  char* msg, int msg_len);
+muon_status muon_check_residual_norm_args(const muon_matrix* x, const muon_matrix* y, const muon_norm_params* params,
+                                          const muon_matrix* out, const muon_matrix* hidden, char* msg, int msg_len);
+muon_status muon_check_residual_norm_grad_args(const muon_matrix* x, const muon_matrix* y,
+                                               const muon_norm_params* params, const muon_matrix* dout,
+                                               const muon_matrix* dhidden, const muon_norm_grads* grads, char* msg,
+                                               int msg_len);
 
 /*
  * Profiling of the library's own launches (for roofline reporting): when

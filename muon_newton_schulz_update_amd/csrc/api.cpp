@@ -1452,6 +1452,7 @@ extern "C" muon_status muon_destroy(muon_handle* h) {
   if (h->ws) (void)hipFree(h->ws);
   h->train.head.release();
   h->train.norm.release();
+  h->train.rows.release();
   if (h->pinned) (void)hipHostFree(h->pinned);
   if (h->upload_done) (void)hipEventDestroy(h->upload_done);
   if (h->static_done) (void)hipEventDestroy(h->static_done);

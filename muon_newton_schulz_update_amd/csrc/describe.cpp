@@ -126,6 +126,44 @@ PyObject* pack(PyObject*, PyObject* args) {
   return out;
 }
 
+// pack_rows(tensors, names, device) -> (bytes, their address): one muon_matrix a
+// tensor, whose columns are its last dimension and whose rows all the others
+// together; None is an empty descriptor. The address holds while the bytes do.
+PyObject* pack_rows(PyObject*, PyObject* args) {
+  PyObject *tensors, *names;
+  long device;
+  if (!PyArg_ParseTuple(args, "O!O!l", &PyTuple_Type, &tensors, &PyTuple_Type, &names, &device)) return nullptr;
+  const Py_ssize_t n = PyTuple_GET_SIZE(tensors);
+  if (PyTuple_GET_SIZE(names) != n) {
+    PyErr_SetString(PyExc_ValueError, "tensors and names differ in length");
+    return nullptr;
+  }
+  PyObject* out = PyBytes_FromStringAndSize(nullptr, (n ? n : 1) * (Py_ssize_t)sizeof(muon_matrix));
+  if (!out) return nullptr;
+  muon_matrix* m = (muon_matrix*)PyBytes_AS_STRING(out);
+  memset(m, 0, (size_t)(n ? n : 1) * sizeof(muon_matrix));
+  bool ok = true;
+  try {
+    for (Py_ssize_t i = 0; ok && i < n; ++i) {
+      PyObject* o = PyTuple_GET_ITEM(tensors, i);
+      if (o == Py_None) continue;
+      const char* what = PyUnicode_AsUTF8(PyTuple_GET_ITEM(names, i));
+      const at::Tensor* t = what ? tensor_of(o, what) : nullptr;
+      ok = t && describe(*t, what, device, m + i);
+      if (!ok || t->dim() <= 2) continue;
+      const int64_t cols = t->size(-1);
+      m[i].rows = cols ? t->numel() / cols : 0;
+      m[i].cols = m[i].ld = cols;
+    }
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    ok = false;
+  }
+  PyObject* both = ok ? Py_BuildValue("(Nn)", out, (Py_ssize_t)m) : nullptr;
+  if (!both && !ok) Py_DECREF(out);
+  return both;
+}
+
 // device_of(tensors) -> index of the first tensor on a GPU, or -1
 PyObject* device_of(PyObject*, PyObject* arg) {
   PyObject* list = PySequence_Fast(arg, "expected a sequence of tensors");
@@ -162,6 +200,7 @@ PyObject* empty(PyObject*, PyObject* args) {
 PyMethodDef methods[] = {
     {"empty", empty, METH_VARARGS, "A tensor on the GPU with the shape and type of others."},
     {"pack", pack, METH_VARARGS, "Descriptors of a list of tensors, as bytes."},
+    {"pack_rows", pack_rows, METH_VARARGS, "Descriptors of tensors as rows, as bytes, and their address."},
     {"device_of", device_of, METH_O, "Index of the first tensor on a GPU, or -1."},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -11,7 +11,6 @@
 #include <string.h>
 
 #include <algorithm>
-#include <new>
 #include <string>
 
 #include "../../include/libmuon.h"
@@ -21,13 +20,6 @@
 
 namespace muon {
 namespace {
-
-#define HIP_DO(h, expr)                                                                                     \
-  do {                                                                                                      \
-    hipError_t e_ = (expr);                                                                                 \
-    if (e_ != hipSuccess)                                                                                   \
-      return handle_error((h), MUON_ERR_HIP, std::string(#expr) + ": " + hipGetErrorString(e_));            \
-  } while (0)
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
@@ -233,30 +225,6 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
     HIP_DO(h, launch_head_gradients_out(a, dt, s));
   }
   return MUON_OK;
-}
-
-// Runs an entry point's body with the handle's device current and keeps
-// exceptions (allocation failure in the host-side checks) from the caller.
-template <typename F>
-muon_status guarded(muon_handle* h, F body) noexcept {
-  if (!h) return MUON_ERR_INVALID_ARG;
-  int before = -1;
-  const int want = handle_device(h);
-  if (hipGetDevice(&before) != hipSuccess) before = want;
-  if (before != want && hipSetDevice(want) != hipSuccess) {
-    (void)hipGetLastError();
-    return MUON_ERR_HIP;
-  }
-  muon_status r;
-  try {
-    r = body();
-  } catch (const std::bad_alloc&) {
-    r = MUON_ERR_ALLOC;
-  } catch (...) {
-    r = MUON_ERR_INVALID_ARG;
-  }
-  if (before != want) (void)hipSetDevice(before);
-  return r;
 }
 
 }  // namespace

@@ -453,6 +453,111 @@ int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void*
   return check_apart(v, msg, len);
 }
 
+namespace {
+
+// x, y and the parameters, with the spans of what is read.
+int check_norm_inputs(const muon_matrix* x, const muon_matrix* y, const muon_norm_params* p, std::vector<Span>& v,
+                      char* msg, int len) {
+  if (!x) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL x");
+  if (!(p->eps > 0.0f) || !finitef(p->eps)) return fail(msg, len, MUON_ERR_INVALID_ARG, "eps must be finite and > 0");
+  int rc;
+  if ((rc = check_tensor(*x, "x", 0, msg, len))) return rc;
+  if (x->cols < 1 || x->cols > kNormMostD || x->rows >= kNormMostRows)
+    return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "x is %lld x %lld: 1 to %d columns and fewer than 2^31 rows are supported",
+                (long long)x->rows, (long long)x->cols, kNormMostD);
+  if (y) {
+    if ((rc = check_tensor(*y, "y", 0, msg, len))) return rc;
+    if ((rc = same_shape(*x, *y, "x", "y", 0, msg, len))) return rc;
+    if (y->dtype == MUON_F32 && x->dtype != MUON_F32)
+      return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "y is MUON_F32 beside a MUON_BF16 x");
+  }
+  if (p->post_gain && (!y || !p->post_norm)) return fail(msg, len, MUON_ERR_INVALID_ARG, "post_gain without a norm of y");
+  if (p->gate && !y) return fail(msg, len, MUON_ERR_INVALID_ARG, "gate without y");
+  if (p->pre_gain && !p->pre_norm) return fail(msg, len, MUON_ERR_INVALID_ARG, "pre_gain without a norm of out");
+  if (nonempty(*x)) v.push_back(tensor_span(*x, "x", 0, false));
+  if (y && nonempty(*y)) v.push_back(tensor_span(*y, "y", 0, false));
+  const muon_matrix* params[] = {p->post_gain, p->pre_gain, p->gate, p->scale};
+  const char* names[] = {"post_gain", "pre_gain", "gate", "scale"};
+  for (int k = 0; k < 4; ++k) {
+    if (!params[k]) continue;
+    const muon_matrix& m = *params[k];
+    if ((rc = check_tensor(m, names[k], 0, msg, len))) return rc;
+    const int kind = norm_kind(m, x->rows, x->cols);
+    // (one channel: its one value is the vector)
+    const bool fits = k < 2 ? m.rows == 1 && m.cols == x->cols
+                            : kind == NORM_ONE || kind == NORM_CHANNELS || (kind == NORM_FULL && k == 2);
+    if (!fits)
+      return fail(msg, len, MUON_ERR_SHAPE_MISMATCH, "%s is %lld x %lld for %lld x %lld", names[k], (long long)m.rows,
+                  (long long)m.cols, (long long)x->rows, (long long)x->cols);
+    if (kind == NORM_FULL && k == 2 && m.dtype != y->dtype)
+      return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "a gate of y's shape has not y's type");
+    if (nonempty(m)) v.push_back(tensor_span(m, names[k], 0, false));
+  }
+  return MUON_OK;
+}
+
+// A tensor with the shape of another and a given type, or null.
+int check_like(const muon_matrix* m, const char* what, const muon_matrix& like, const char* like_what, int dtype,
+               bool writes, std::vector<Span>& v, char* msg, int len) {
+  if (!m) return MUON_OK;
+  int rc;
+  if ((rc = check_tensor(*m, what, 0, msg, len))) return rc;
+  if ((rc = same_shape(like, *m, like_what, what, 0, msg, len))) return rc;
+  if (m->dtype != dtype) return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "%s has not the type of %s", what, like_what);
+  if (nonempty(*m)) v.push_back(tensor_span(*m, what, 0, writes));
+  return MUON_OK;
+}
+
+// The type of hidden and its gradient: y's, or without y x's or a 16-bit one.
+int hidden_dtype(const muon_matrix& x, const muon_matrix* y, const muon_matrix* hidden) {
+  if (y) return y->dtype;
+  return hidden && hidden->dtype == MUON_BF16 ? (int)MUON_BF16 : x.dtype;
+}
+
+}  // namespace
+
+int check_residual_norm(const muon_matrix* x, const muon_matrix* y, const muon_norm_params* p, const muon_matrix* out,
+                        const muon_matrix* hidden, char* msg, int len) {
+  if (msg && len > 0) msg[0] = 0;
+  std::vector<Span> v;
+  int rc;
+  if ((rc = check_norm_inputs(x, y, p, v, msg, len))) return rc;
+  if (y && !out) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL out beside y");
+  if (!out && !hidden) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL out and hidden");
+  if ((hidden != nullptr) != (p->pre_norm != 0))
+    return fail(msg, len, MUON_ERR_INVALID_ARG, hidden ? "hidden without a norm of out" : "NULL hidden");
+  if ((rc = check_like(out, "out", *x, "x", x->dtype, true, v, msg, len))) return rc;
+  if ((rc = check_like(hidden, "hidden", *x, y ? "y" : "x", hidden_dtype(*x, y, hidden), true, v, msg, len))) return rc;
+  return check_apart(v, msg, len);
+}
+
+int check_residual_norm_grad(const muon_matrix* x, const muon_matrix* y, const muon_norm_params* p,
+                             const muon_matrix* dout, const muon_matrix* dhidden, const muon_norm_grads* g, char* msg,
+                             int len) {
+  if (msg && len > 0) msg[0] = 0;
+  std::vector<Span> v;
+  int rc;
+  if ((rc = check_norm_inputs(x, y, p, v, msg, len))) return rc;
+  if (!dout && !dhidden) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL dout and dhidden");
+  if (dhidden && !p->pre_norm) return fail(msg, len, MUON_ERR_INVALID_ARG, "dhidden without a norm of out");
+  if ((rc = check_like(dout, "dout", *x, "x", x->dtype, false, v, msg, len))) return rc;
+  if ((rc = check_like(dhidden, "dhidden", *x, y ? "y" : "x", hidden_dtype(*x, y, dhidden), false, v, msg, len))) return rc;
+  if (!g) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL gradients");
+  const muon_matrix* of[] = {x, y, p->post_gain, p->gate, p->scale, p->pre_gain};
+  const muon_matrix* to[] = {g->x, g->y, g->post_gain, g->gate, g->scale, g->pre_gain};
+  const char* names[] = {"x", "y", "post_gain", "gate", "scale", "pre_gain"};
+  const char* grads[] = {"dx", "dy", "dpost_gain", "dgate", "dscale", "dpre_gain"};
+  bool any = false;
+  for (int k = 0; k < 6; ++k) {
+    if (!to[k]) continue;
+    any = true;
+    if (!of[k]) return fail(msg, len, MUON_ERR_INVALID_ARG, "%s without %s", grads[k], names[k]);
+    if ((rc = check_like(to[k], grads[k], *of[k], names[k], of[k]->dtype, true, v, msg, len))) return rc;
+  }
+  if (!any) return fail(msg, len, MUON_ERR_INVALID_ARG, "no gradient is asked for");
+  return check_apart(v, msg, len);
+}
+
 }  // namespace muon
 
 namespace {
@@ -495,6 +600,36 @@ extern "C" muon_status muon_check_loss_args(const muon_matrix* hidden, const muo
     return muon::check_loss(hidden, weight, targets, target_bytes, &c, grad_out, loss, dhidden, dweight,
                             dhidden || dweight ? 1 : 0, msg, msg_len);
   });
+}
+
+namespace {
+
+muon_norm_params params_or_default(const muon_norm_params* p) {
+  muon_norm_params q;
+  muon_norm_params_default(&q);
+  return p ? *p : q;
+}
+
+}  // namespace
+
+extern "C" muon_status muon_check_residual_norm_args(const muon_matrix* x, const muon_matrix* y,
+                                                     const muon_norm_params* params, const muon_matrix* out,
+                                                     const muon_matrix* hidden, char* msg, int msg_len) {
+  const muon_norm_params p = params_or_default(params);
+  return checked(msg, msg_len, [&] { return muon::check_residual_norm(x, y, &p, out, hidden, msg, msg_len); });
+}
+extern "C" muon_status muon_check_residual_norm_grad_args(const muon_matrix* x, const muon_matrix* y,
+                                                          const muon_norm_params* params, const muon_matrix* dout,
+                                                          const muon_matrix* dhidden, const muon_norm_grads* grads,
+                                                          char* msg, int msg_len) {
+  const muon_norm_params p = params_or_default(params);
+  return checked(msg, msg_len,
+                 [&] { return muon::check_residual_norm_grad(x, y, &p, dout, dhidden, grads, msg, msg_len); });
+}
+
+extern "C" void muon_norm_params_default(muon_norm_params* p) {
+  if (!p) return;
+  *p = muon_norm_params{nullptr, nullptr, nullptr, nullptr, 1, 1, 1e-6f};
 }
 
 extern "C" void muon_loss_config_default(muon_loss_config* c) {

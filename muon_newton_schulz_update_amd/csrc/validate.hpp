@@ -29,4 +29,20 @@ int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void*
                const muon_loss_config* cfg, const float* grad_out, const float* loss, const muon_matrix* dhidden,
                const muon_matrix* dweight, int grad, char* msg, int len);
 
+// Norms around a block (norm_api.cpp).
+constexpr int kNormMostD = 16384;                     // channels
+constexpr int64_t kNormMostRows = int64_t(1) << 31;
+// What a parameter of the norms is, by its shape.
+enum NormKind { NORM_NONE = 0, NORM_ONE = 1, NORM_CHANNELS = 2, NORM_FULL = 3 };
+inline int norm_kind(const muon_matrix& m, int64_t n, int64_t d) {
+  if (m.rows == 1 && m.cols == 1) return NORM_ONE;
+  if (m.rows == 1 && m.cols == d) return NORM_CHANNELS;
+  return m.rows == n && m.cols == d ? NORM_FULL : NORM_NONE;
+}
+int check_residual_norm(const muon_matrix* x, const muon_matrix* y, const muon_norm_params* p, const muon_matrix* out,
+                        const muon_matrix* hidden, char* msg, int len);
+int check_residual_norm_grad(const muon_matrix* x, const muon_matrix* y, const muon_norm_params* p,
+                             const muon_matrix* dout, const muon_matrix* dhidden, const muon_norm_grads* g, char* msg,
+                             int len);
+
 }  // namespace muon
