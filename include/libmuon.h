@@ -528,6 +528,54 @@ muon_status linear_cross_entropy_grad(muon_handle* handle, const muon_matrix* hi
                                       const muon_matrix* dweight);
 
 /*
+ * linear_logprobs(_grad) - log probabilities of given tokens under a language-model
+ * head, with the distribution's entropy and its likeliest tokens: z = hidden
+ * weight^T as above (soft cap included), lse_i = log sum_v exp z_iv,
+ *   logprobs_i = z_i,target - lse_i
+ *   entropy_i  = - sum_v p_iv log p_iv, p_iv = exp(z_iv - lse_i)
+ *   top_tokens_i, top_logprobs_i: the `top` largest logits in falling order,
+ *   equal ones by rising token
+ * No logits are stored. The gradient is that of sum_i grad_logprobs[i]
+ * logprobs_i + grad_entropy[i] entropy_i; the alternatives have none.
+ *   hidden, weight, targets   as for linear_cross_entropy. Tokens whose target
+ *            is ignore_index have log probability, entropy and top_logprobs 0,
+ *            top_tokens -1 and gradient 0, and their hidden rows are never read.
+ *            Any other target outside [0, V) gives that token's log probability
+ *            as NaN and no gradient; its entropy and alternatives do not depend on it.
+ *   cfg      NULL = defaults; top in [0, MUON_TOP_MOST], at most V
+ *   logprobs N values; entropy N values or NULL
+ *   stats    N x 4 values or NULL, on 16 bytes: what linear_logprobs_grad
+ *            needs of the call (each token's largest logit, log sum exp over it,
+ *            entropy and log probability)
+ *   top_logprobs, top_tokens  N x top each, row by row; not looked at with top 0
+ *   grad_logprobs, grad_entropy  N values each; one may be NULL (zero)
+ *   dhidden, dweight  as for linear_cross_entropy_grad
+ * The alternatives are ranked by the raw logits (a soft cap keeps their order): the
+ * top + 8 largest of the fp32 sums are summed again in 64 bits, so neighbours
+ * nearer than an fp32 sum's error are in order too. Where fewer than `top`
+ * logits are above minus infinity the rest are token -1 with log probability
+ * minus infinity; a NaN logit makes a token's values NaN and its alternatives -1.
+ * The gradient takes the logits again, as its own product, and with the same
+ * workspace as linear_cross_entropy_grad; a logit's gradient is rounded once, as
+ * the products' operand, and the target's counts with 16 bits of a BF16's 8.
+ */
+#define MUON_TOP_MOST 32
+typedef struct {
+  int32_t top;           /* alternatives a token */
+  float   softcap;       /* 0 = off */
+  int64_t ignore_index;
+} muon_logprob_config;
+/* no alternatives, no softcap, ignore_index -100 */
+void muon_logprob_config_default(muon_logprob_config* cfg);
+muon_status linear_logprobs(muon_handle* handle, const muon_matrix* hidden, const muon_matrix* weight,
+                            const void* targets, int target_bytes, const muon_logprob_config* cfg, float* logprobs,
+                            float* entropy, float* stats, float* top_logprobs, int64_t* top_tokens);
+muon_status linear_logprobs_grad(muon_handle* handle, const muon_matrix* hidden, const muon_matrix* weight,
+                                 const void* targets, int target_bytes, const muon_logprob_config* cfg,
+                                 const float* stats, const float* grad_logprobs, const float* grad_entropy,
+                                 const muon_matrix* dhidden, const muon_matrix* dweight);
+
+/*
  * residual_norm(_grad) - the end of one block and the start of the next, for
  * each row (token) of the residual stream x and of the block's result y:
  *   n      = y / sqrt(mean(y^2) + eps) * post_gain      (post_norm 0: n = y)
@@ -581,6 +629,15 @@ muon_status muon_check_loss_args(const muon_matrix* hidden, const muon_matrix* w
                                  int target_bytes, const muon_loss_config* cfg, const float* grad_out,
                                  const float* loss, const muon_matrix* dhidden, const muon_matrix* dweight,
                                  char* msg, int msg_len);
+muon_status muon_check_logprob_args(const muon_matrix* hidden, const muon_matrix* weight, const void* targets,
+                                    int target_bytes, const muon_logprob_config* cfg, const float* logprobs,
+                                    const float* entropy, const float* stats, const float* top_logprobs,
+                                    const int64_t* top_tokens, char* msg, int msg_len);
+muon_status muon_check_logprob_grad_args(const muon_matrix* hidden, const muon_matrix* weight, const void* targets,
+                                         int target_bytes, const muon_logprob_config* cfg, const float* stats,
+                                         const float* grad_logprobs, const float* grad_entropy,
+                                         const muon_matrix* dhidden, const muon_matrix* dweight, char* msg,
+                                         int msg_len);
 muon_status muon_check_residual_norm_args(const muon_matrix* x, const muon_matrix* y, const muon_norm_params* params,
                                           const muon_matrix* out, const muon_matrix* hidden, char* msg, int msg_len);
 muon_status muon_check_residual_norm_grad_args(const muon_matrix* x, const muon_matrix* y,

@@ -158,6 +158,11 @@ def load_library() -> ctypes.CDLL:
             "muon_check_norm_args": (I, [I, M, M, F, V, V] + text),
             "muon_check_adamw_args": (I, [I, M, M, M, M, M, V, V] + text),
             "muon_check_loss_args": (I, [M, M, V, I, V, V, V, M, M] + text),
+            "muon_logprob_config_default": (None, [V]),
+            "linear_logprobs": (I, [V, M, M, V, I, V, V, V, V, V, V]),
+            "linear_logprobs_grad": (I, [V, M, M, V, I, V, V, V, V, M, M]),
+            "muon_check_logprob_args": (I, [M, M, V, I, V, V, V, V, V, V] + text),
+            "muon_check_logprob_grad_args": (I, [M, M, V, I, V, V, V, V, M, M] + text),
             "muon_norm_params_default": (None, [V]),
             "residual_norm": (I, [V, M, M, V, M, M]),
             "residual_norm_grad": (I, [V, M, M, V, M, M, V]),
@@ -433,5 +438,7 @@ def check_polar_args(inputs, outputs, cfg=None) -> tuple[int, str]:
 from .training import (AdamWConfig, LossConfig, adamw_update, check_adamw_args, check_loss_args,  # noqa: E402
                        check_norm_args, clip_grad_norm, grad_norm, linear_cross_entropy, linear_cross_entropy_grad,
                        scale)
+from .logprobs import (LogProbConfig, LogProbs, check_logprob_args, check_logprob_grad_args,  # noqa: E402
+                       linear_logprobs, linear_logprobs_grad)
 from .norms import (NormGrads, NormParams, check_residual_norm_args, check_residual_norm_grad_args,  # noqa: E402
                     residual_norm, residual_norm_grad, rms_norm, rms_norm_grad)

@@ -24,7 +24,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 DEVICE_SOURCES = ["ns_gemm.hip", "stream_kernels.hip", "static_scratch.hip", "train_kernels.hip",
-                  "head_kernels.hip", "head_gemm.hip", "norm_kernels.hip"]
+                  "head_kernels.hip", "head_gemm.hip", "head_logprobs.hip", "norm_kernels.hip"]
 HOST_SOURCES = ["api.cpp", "train_api.cpp", "norm_api.cpp", "validate.cpp"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",

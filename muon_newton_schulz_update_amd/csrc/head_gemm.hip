@@ -383,6 +383,91 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
   return true;
 }
 
+// A lane's MI x 16 raw logits of one token (z[mi * step]): the largest, its first
+// place (6 bits) and the second largest, whose last 6 bits the place takes. Only
+// that a lane holds another candidate, and no larger a one, is read from the second.
+template <int MI>
+__device__ __forceinline__ float store_best(const HeadArgs& a, const f32x16_t* z, int step, int tile, int set, int r) {
+  float first = -__builtin_inff(), second = first;
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      second = __builtin_amdgcn_fmed3f(first, second, z[mi * step][q]);
+      first = fmaxf(first, z[mi * step][q]);
+    }
+  uint32_t place = 0;
+#pragma unroll
+  for (int i = MI * 16 - 1; i >= 0; --i) place = z[i / 16 * step][i % 16] == first ? i : place;
+  a.best[((int64_t)tile * a.piece + r) * a.sets + set] =
+      make_uint2(__float_as_uint(first), (__float_as_uint(second) & ~63u) | place);
+  return first;
+}
+
+// The logits' gradient dz = -p (b + g log p) and the target's (train.hpp: ts), to
+// the panels in the operands' type; z are a lane's raw logits of token r. Rows past
+// the piece's and columns past the vocabulary become zero (stages of dW and dH).
+template <typename T, int MI>
+__device__ __forceinline__ void store_logits_grad(const HeadArgs& a, f32x16_t (&z)[MI], int r, int rows, int vw, int hf,
+                                                  int tg, bool any_mine, bool edge) {
+  const bool real = r < rows, cap = a.softcap > 0.f;
+  float4 ts = {0.f, 0.f, 0.f, 0.f};
+  if (real) ts = a.ts[r];
+  float own = 0.f;
+  if (tg >= 0) own = a.rs[r].z;
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    float e[16], slope[16];
+    if (cap) cap16(z[mi], a.softcap, a.cap_inv, slope);
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      // log p from differences, as good as the logits however large these are
+      // (below 2^-126 p counts as 0: what it is multiplied by is no infinity)
+      const float lp = __builtin_elementwise_maximum((z[mi][q] - ts.x) - ts.y, -126.f / kLog2e);
+      const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
+      e[q] = -p * fmaf(ts.w, lp, ts.z);
+      if (cap) e[q] *= slope[q];
+      if (!real) e[q] = 0.f;
+    }
+    if (any_mine) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (mi * 32 + 8 * (q >> 2) + (q & 3) == tg) {
+          // most of a token's gradient: what its rounding loses is added to both products
+          const float x = cap ? own * slope[q] : own;
+          float4 rs = {0.f, 0.f, x, 0.f};
+          if (sizeof(T) == 2) rs.w = x - bf2f(f2bf(x));
+          a.rs[r] = rs;
+          e[q] = x;
+        }
+    }
+    if (edge) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (vw + mi * 32 + 8 * (q >> 2) + 4 * hf + (q & 3) >= a.v) e[q] = 0.f;
+    }
+    const int64_t col = vw + mi * 32;
+    if constexpr (sizeof(T) == 2) {
+      unsigned int c[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) c[q] = pack_bf16(e[2 * q], e[2 * q + 1]);
+      uint8_t* dst = (uint8_t*)a.e + (((int64_t)(r >> 6) * (a.vp >> 3) + (col >> 3)) << 10) + (r & 63) * 16;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        // (as the exponentials below: whole chunks after a half-wave swap)
+        const u32x2_t x = __builtin_amdgcn_permlane32_swap(c[4 * g], c[4 * g + 2], false, false);
+        const u32x2_t y = __builtin_amdgcn_permlane32_swap(c[4 * g + 1], c[4 * g + 3], false, false);
+        *(u32x4_t*)(dst + ((2 * g + hf) << 10)) = (u32x4_t){x[0], y[0], x[1], y[1]};
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *(f32x4_t*)((float*)a.e + panel_at<float>(r, col + 8 * g + 4 * hf, a.vp)) =
+            (f32x4_t){e[4 * g], e[4 * g + 1], e[4 * g + 2], e[4 * g + 3]};
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Logits. The vocabulary is on the accumulators' rows and the tokens on their
 // columns, so a lane holds 64 logits of each of its two tokens (32 or 16 of one
@@ -401,7 +486,7 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
 // Two workgroups of 256 x 128 to a CU, so that one's epilogue runs beside the
 // other's products, took 13 % longer (more operand traffic from LDS).
 // ---------------------------------------------------------------------------
-template <typename T, int TILE, int S, bool FEW, bool GATHER>
+template <typename T, int TILE, int S, bool FEW, bool GATHER, LogitsMode MODE = LOGITS_LOSS>
 __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {
   // a wave: 128 vocabulary rows x 64 tokens (256-tiles) or 32, 64 x 32 of a
   // 64-tile. PAIR: 32 x 32 of one, and two waves put their statistics together:
@@ -492,6 +577,13 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
     const int tg = (r >= rows ? -1 : GATHER ? listed : a.tgt[a.row0 + r]) - vw - 4 * hf;
     const bool mine = tg >= 0 && tg < MI * 32 && (tg & 4) == 0;
     const bool any_mine = __any(mine);
+    if constexpr (MODE == LOGITS_GRAD) {
+      f32x16_t z[MI];
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) z[mi] = acc[mi][ni];
+      store_logits_grad<T, MI>(a, z, r, rows, vw, hf, mine ? tg : -1, any_mine, edge);
+      continue;
+    }
     if (any_mine) {
       float z = 0.f, slope = 1.f;
 #pragma unroll
@@ -507,10 +599,21 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
       if (mine && cap) a.zf[r] = slope;
     }
     float top = kRefFloor;
+    if constexpr (MODE == LOGITS_STATS) {
+      if (a.top) {
+        top = fmaxf(top, store_best<MI>(a, &acc[0][ni], NI, tile, PAIR ? 2 * wm + hf : hf, r));
+      } else {
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
+        for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
+          for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
+      }
+    } else {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
+    }
     top = fmaxf(top, __shfl_xor(top, 32));
     if (cap) {
       float slope;
@@ -525,7 +628,7 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
       ring_barrier();
       top = fmaxf(stat[0], stat[64]);
     }
-    float sum = 0.f;
+    float sum = 0.f, ent = 0.f;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       float e[16], slope[16];
@@ -550,10 +653,12 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
         // is off by more than 1 past 2^24); no smaller than a kept exponential
         // can say (kCodeBase); a maximum that keeps NaN, so that one bad logit
         // reaches the token's loss
-        e[q] = __builtin_amdgcn_exp2f(__builtin_elementwise_maximum((z[q] - top) * kLog2e, -63.f));
+        const float y = __builtin_elementwise_maximum((z[q] - top) * kLog2e, -63.f);
+        e[q] = __builtin_amdgcn_exp2f(y);
         sum += e[q];
+        if constexpr (MODE == LOGITS_STATS) ent = fmaf(e[q], y, ent);
       }
-      if (!keep) continue;
+      if (MODE == LOGITS_STATS || !keep) continue;
       if (cap) {
         // what the gradient takes of the logit: its exponential times the slope
 #pragma unroll
@@ -586,16 +691,22 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
       }
     }
     sum += __shfl_xor(sum, 32);
+    if constexpr (MODE == LOGITS_STATS) ent += __shfl_xor(ent, 32);
     if constexpr (PAIR) {
-      if (wm == 1 && hf == 0) stat[128] = sum;
+      if (wm == 1 && hf == 0) {
+        stat[128] = sum;
+        if constexpr (MODE == LOGITS_STATS) stat[192] = ent;
+      }
       wait_lgkm0();
       ring_barrier();
       if (wm == 1) return;
       sum += stat[128];
+      if constexpr (MODE == LOGITS_STATS) ent += stat[192];
     }
     if (hf == 0) {
       a.tmax[(int64_t)tile * a.piece + r] = top;
       a.tsum[(int64_t)tile * a.piece + r] = sum;
+      if constexpr (MODE == LOGITS_STATS) a.tent[(int64_t)tile * a.piece + r] = ent;
     }
   }
 }
@@ -1029,17 +1140,21 @@ int grad_tile_of(int dt, int rows, int dp, int64_t tiles256, int64_t tiles128) {
 
 }  // namespace
 
-hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
+template <LogitsMode MODE>
+static hipError_t launch_logits(const HeadArgs& a, int dt, int keep, hipStream_t s) {
   const int tile = a.logit_tile, vt = cdiv(a.v, tile), tt = cdiv(a.rows_max, tile);
   const bool deep = tile == 64 && (int64_t)vt * tt <= kDeepTiles, few = a.n <= 32;
   const dim3 g(xcd_grid(vt * tt)), b(dt != MUON_BF16 && !few ? 256 : tile * 2);
-#define LOGITS(T, ...)                                                                                   \
-  do {                                                                                                   \
-    if (a.gather) hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__, true>), g, b, 0, s, a, keep, vt, tt); \
-    else hipLaunchKernelGGL((k_logits_mfma<T, __VA_ARGS__, false>), g, b, 0, s, a, keep, vt, tt);        \
+#define LOGITS_OF(T, TILE, S, FEW, GATHER) \
+  hipLaunchKernelGGL((k_logits_mfma<T, TILE, S, FEW, GATHER, MODE>), g, b, 0, s, a, keep, vt, tt)
+  // (the gradient reads its rows from panels, which dW needs)
+#define LOGITS(T, TILE, S, FEW)                                                      \
+  do {                                                                               \
+    if (MODE != LOGITS_GRAD && a.gather) LOGITS_OF(T, TILE, S, FEW, MODE != LOGITS_GRAD); \
+    else LOGITS_OF(T, TILE, S, FEW, false);                                          \
   } while (0)
   if (dt == MUON_BF16) {
-    if (tile == 256) hipLaunchKernelGGL((k_logits_mfma<u16, 256, 5, false, false>), g, b, 0, s, a, keep, vt, tt);
+    if (tile == 256) LOGITS_OF(u16, 256, 5, false, false);
     else if (tile == 128) LOGITS(u16, 128, 5, false);
     else if (deep) LOGITS(u16, 64, 9, false);
     else LOGITS(u16, 64, 5, false);
@@ -1050,7 +1165,13 @@ hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s
     else LOGITS(float, 64, 5, false);
   }
 #undef LOGITS
+#undef LOGITS_OF
   return hipGetLastError();
+}
+hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, LogitsMode mode, hipStream_t s) {
+  if (mode == LOGITS_STATS) return launch_logits<LOGITS_STATS>(a, dt, 0, s);
+  if (mode == LOGITS_GRAD) return launch_logits<LOGITS_GRAD>(a, dt, 0, s);
+  return launch_logits<LOGITS_LOSS>(a, dt, keep, s);
 }
 
 hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
@@ -1092,6 +1213,7 @@ void head_plan(HeadArgs& a, int dt) {
   a.logit_tile = tile_of(dt, rows, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256), (int64_t)cdiv(a.v, 128) * cdiv(rows, 128));
   a.vtile = a.logit_tile == 64 ? 64 : 128;
   a.n_vt = cdiv(a.v, a.vtile);
+  a.sets = dt == MUON_BF16 ? 2 : 4;
   a.split = a.wsplit = 1;
   if (!a.dh && !a.dw) return;
   const int64_t stages = cdiv(a.v, unit), wstages = cdiv(rows, unit);

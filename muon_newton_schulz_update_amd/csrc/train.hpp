@@ -161,17 +161,43 @@ struct HeadArgs {
   int32_t first, last;                // this piece starts / ends the sum over pieces
   float* loss;                        // caller's: one value, or n
   const float* grad_out;              // device, or null (1)
+  // log probabilities (head_logprobs.hip); loss holds them
+  int32_t top;                        // alternatives a token
+  int32_t sets;                       // lanes that share a statistic's vocabulary columns
+  float* tent;                        // n_vt x piece: sum of exponential times its logarithm (base 2)
+  uint2* best;                        // n_vt x piece x sets: each lane's largest logit, its place and the second largest
+  float* entropy;                     // caller's, n each, or null
+  float4* stats;
+  float* top_logprobs;                // caller's, n x top
+  int64_t* top_tokens;
+  const float4* stats_in;             // the gradient's: what the forward call left,
+  const float* grad_logprobs;         // and the results' gradients, or null
+  const float* grad_entropy;
+  float4* ts;                         // piece: {reference, log of the sum over it, grad_logprob + grad_entropy entropy, grad_entropy}
 };
+
+// What the logits' launch leaves: statistics and, where kept, exponentials for
+// the loss; statistics with entropy and largest logits; the logits' gradient.
+enum LogitsMode { LOGITS_LOSS, LOGITS_STATS, LOGITS_GRAD };
+
+// The place of a lane's value q among a statistic's vocabulary columns (`set`
+// of `sets` lanes): accumulators of 32 x 32 blocks, 4 rows of 8 to each half-wave.
+__host__ __device__ inline int set_column(int set, int sets, int q) {
+  return (sets == 4 ? (set >> 1) * 32 : 0) + (q >> 4) * 32 + 8 * ((q >> 2) & 3) + 4 * (set & 1) + (q & 3);
+}
 
 // Picks the tile edges, the statistics' columns and the splits, from the sizes
 // and from which gradients are wanted (before the workspace is laid out).
 void head_plan(HeadArgs& a, int dt);
 hipError_t launch_head_compact(const HeadArgs& a, hipStream_t s);
 hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s);
-hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, hipStream_t s);
+hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, LogitsMode mode, hipStream_t s);
 hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s);
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s);
 hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s);   // dh and dw, each if not null
 hipError_t launch_head_gradients_out(const HeadArgs& a, int dt, hipStream_t s);
+// head_logprobs.hip: after the logits' statistics, and before the logits' gradient
+hipError_t launch_logprobs(const HeadArgs& a, int dt, hipStream_t s);
+hipError_t launch_logprob_factors(const HeadArgs& a, hipStream_t s);
 
 }  // namespace muon

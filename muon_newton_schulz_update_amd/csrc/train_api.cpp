@@ -117,11 +117,30 @@ constexpr int kPieceRows = 256;
 constexpr int kGatherTokens = 64;       // tokens that one wave can list
 constexpr int64_t kPieceMost = 65536;   // keeps a launch's tiles far from 2^31
 
-muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& wgt, const void* targets,
-                     int target_bytes, const muon_loss_config& cfg, const float* grad_out, float* loss,
-                     const muon_matrix* dh, const muon_matrix* dw) {
+// A call on a head: the loss or log probabilities, alone or with gradients.
+struct HeadCall {
+  const muon_matrix *hidden, *weight;
+  const void* targets;
+  int target_bytes;
+  int64_t ignore;
+  float softcap;
+  const muon_matrix *dh = nullptr, *dw = nullptr;
+  LogitsMode mode = LOGITS_LOSS;
+  // the loss
+  int reduction = MUON_REDUCE_NONE;
+  const float* grad_out = nullptr;
+  float* loss = nullptr;                     // log probabilities: the values
+  // log probabilities, and what their gradient takes
+  int top = 0;
+  float *entropy = nullptr, *stats = nullptr, *top_logprobs = nullptr;
+  int64_t* top_tokens = nullptr;
+  const float *stats_in = nullptr, *grad_logprobs = nullptr, *grad_entropy = nullptr;
+};
+
+muon_status head_run(muon_handle* h, const HeadCall& c) {
   TrainState& ts = train_state(h);
   const hipStream_t s = handle_stream(h);
+  const muon_matrix &hid = *c.hidden, &wgt = *c.weight;
   const int dt = wgt.dtype, e = esz(dt);
   HeadArgs a{};
   a.n = (int)hid.rows;
@@ -130,36 +149,48 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const int unit = 128 / e;                       // a stage of a product: 128 bytes of the contraction
   a.dp = (int)(cdiv(a.d, unit) * unit);
   a.vp = (int)(cdiv(a.v, 256) * 256);
-  a.per_token = cfg.reduction == MUON_REDUCE_NONE;
-  a.mean = cfg.reduction == MUON_REDUCE_MEAN;
+  a.per_token = c.reduction == MUON_REDUCE_NONE;
+  a.mean = c.reduction == MUON_REDUCE_MEAN;
   a.half = dt == MUON_BF16;
-  a.softcap = cfg.softcap;
-  a.cap_inv = cfg.softcap > 0.f ? std::min(1.f / cfg.softcap, FLT_MAX) : 0.f;   // (of a denormal cap: 0 times it stays 0)
-  a.targets = targets;
-  a.target_bytes = target_bytes;
-  a.ignore = cfg.ignore_index;
+  a.softcap = c.softcap;
+  a.cap_inv = c.softcap > 0.f ? std::min(1.f / c.softcap, FLT_MAX) : 0.f;   // (of a denormal cap: 0 times it stays 0)
+  a.targets = c.targets;
+  a.target_bytes = c.target_bytes;
+  a.ignore = c.ignore;
   a.h = hid.ptr;
   a.ld_h = hid.ld;
-  a.loss = loss;
-  a.grad_out = grad_out;
+  a.loss = c.loss;
+  a.grad_out = c.grad_out;
+  a.top = c.top;
+  a.entropy = c.entropy;
+  a.stats = (float4*)c.stats;
+  a.top_logprobs = c.top_logprobs;
+  a.top_tokens = c.top_tokens;
+  a.stats_in = (const float4*)c.stats_in;
+  a.grad_logprobs = c.grad_logprobs;
+  a.grad_entropy = c.grad_entropy;
   // (a gradient without elements is none: with no tokens and no dweight only
   // the loss is left)
-  if (dh && !empty(*dh)) {
-    a.dh = dh->ptr;
-    a.ld_dh = dh->ld;
+  if (c.dh && !empty(*c.dh)) {
+    a.dh = c.dh->ptr;
+    a.ld_dh = c.dh->ld;
   }
-  if (dw && !empty(*dw)) {
-    a.dw = dw->ptr;
-    a.ld_dw = dw->ld;
+  if (c.dw && !empty(*c.dw)) {
+    a.dw = c.dw->ptr;
+    a.ld_dw = c.dw->ld;
   }
   const bool grad = a.dh || a.dw;
+  if (c.mode == LOGITS_GRAD && !grad) return MUON_OK;
   // the weight as it is, where its rows are whole 16-byte pieces on 16 bytes;
   // otherwise a padded copy (the pitch also fits the products' 24-bit multiply)
   const bool direct = a.d * e % 16 == 0 && (uintptr_t)wgt.ptr % 16 == 0 &&
                       (wgt.rows == 1 || (wgt.ld * e % 16 == 0 && wgt.ld * e < (1 << 23)));
   a.w_cols = direct ? a.d : a.dp;
   // pieces
-  const size_t row = (size_t)a.dp * e + (size_t)cdiv(a.v, 64) * 8 + 24 + (grad ? (size_t)a.vp * e : 0);
+  // (a row's statistics: at most 8 bytes for 64 words of the vocabulary, with entropy
+  // and candidates 12 and 8 for each lane that shares them)
+  const size_t each = c.mode == LOGITS_STATS ? 12 + (c.top ? (a.half ? 16 : 32) : 0) : 8;
+  const size_t row = (size_t)a.dp * e + (size_t)cdiv(a.v, 64) * each + 24 + (grad ? (size_t)a.vp * e : 0);
   const int64_t most =
       std::min(kPieceMost, std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows));
   const int64_t pieces = std::max<int64_t>(1, cdiv(a.n, most));
@@ -180,7 +211,10 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   const size_t n = (size_t)a.n, p = (size_t)a.piece;
   const size_t o_count = take(16), o_idx = take(n * 4), o_tgt = take(n * 4), o_lossc = take(n * 4);
   const size_t o_hp = take(p * a.dp * e), o_tmax = take(p * a.n_vt * 4), o_tsum = take(p * a.n_vt * 4);
-  const size_t o_zt = take(p * 4), o_zf = take(cfg.softcap > 0.f ? p * 4 : 0), o_rs = take(p * 16);
+  const size_t o_zt = take(p * 4), o_zf = take(c.softcap > 0.f ? p * 4 : 0), o_rs = take(p * 16);
+  const bool stats = c.mode == LOGITS_STATS;
+  const size_t o_tent = take(stats ? p * a.n_vt * 4 : 0), o_best = take(stats && c.top ? p * a.n_vt * a.sets * 8 : 0);
+  const size_t o_ts = take(c.mode == LOGITS_GRAD ? p * 16 : 0);
   const size_t o_w = direct ? 0 : take((size_t)a.v * a.dp * e);
   const size_t o_e = grad ? take(p * a.vp * e) : 0, o_part = a.split > 1 ? take(p * a.dp * 4 * a.split) : 0;
   const size_t o_wpart = a.wsplit > 1 ? take((size_t)a.v * a.dp * 4 * a.wsplit) : 0;
@@ -198,6 +232,10 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
   a.zt = (float*)(b + o_zt);
   a.zf = (float*)(b + o_zf);
   a.rs = (float4*)(b + o_rs);
+  a.tent = (float*)(b + o_tent);
+  a.best = (uint2*)(b + o_best);
+  a.ts = (float4*)(b + o_ts);
+  if (c.mode == LOGITS_GRAD) a.loss = a.lossc;    // (zeros of the ignored tokens go there)
   a.e = b + o_e;
   a.part = (float*)(b + o_part);
   a.wpart = (float*)(b + o_wpart);
@@ -217,10 +255,17 @@ muon_status head_run(muon_handle* h, const muon_matrix& hid, const muon_matrix& 
     a.first = k == 0;
     a.last = k + 1 == pieces;
     HIP_DO(h, launch_head_pack(a, dt, s));
-    HIP_DO(h, launch_head_logits(a, dt, grad ? 1 : 0, s));
-    HIP_DO(h, launch_head_merge(a, grad ? 1 : 0, s));
-    if (!grad) continue;
-    HIP_DO(h, launch_head_dlogits(a, dt, s));
+    if (c.mode == LOGITS_GRAD) HIP_DO(h, launch_logprob_factors(a, s));
+    HIP_DO(h, launch_head_logits(a, dt, grad ? 1 : 0, c.mode, s));
+    if (c.mode == LOGITS_STATS) {
+      HIP_DO(h, launch_logprobs(a, dt, s));
+      continue;
+    }
+    if (c.mode == LOGITS_LOSS) {
+      HIP_DO(h, launch_head_merge(a, grad ? 1 : 0, s));
+      if (!grad) continue;
+      HIP_DO(h, launch_head_dlogits(a, dt, s));
+    }
     HIP_DO(h, launch_head_gradients(a, dt, s));
     HIP_DO(h, launch_head_gradients_out(a, dt, s));
   }
@@ -338,7 +383,10 @@ extern "C" muon_status linear_cross_entropy(muon_handle* h, const muon_matrix* h
                             sizeof(msg));
   if (rc) return handle_error(h, rc, msg);
   handle_clear_error(h);
-  return head_run(h, *hidden, *weight, targets, target_bytes, c, nullptr, loss, nullptr, nullptr);
+  HeadCall call{hidden, weight, targets, target_bytes, c.ignore_index, c.softcap};
+  call.reduction = c.reduction;
+  call.loss = loss;
+  return head_run(h, call);
   });
 }
 
@@ -355,6 +403,58 @@ extern "C" muon_status linear_cross_entropy_grad(muon_handle* h, const muon_matr
                             sizeof(msg));
   if (rc) return handle_error(h, rc, msg);
   handle_clear_error(h);
-  return head_run(h, *hidden, *weight, targets, target_bytes, c, grad_out, loss, dhidden, dweight);
+  HeadCall call{hidden, weight, targets, target_bytes, c.ignore_index, c.softcap, dhidden, dweight};
+  call.reduction = c.reduction;
+  call.grad_out = grad_out;
+  call.loss = loss;
+  return head_run(h, call);
+  });
+}
+
+extern "C" muon_status linear_logprobs(muon_handle* h, const muon_matrix* hidden, const muon_matrix* weight,
+                                       const void* targets, int target_bytes, const muon_logprob_config* cfg,
+                                       float* logprobs, float* entropy, float* stats, float* top_logprobs,
+                                       int64_t* top_tokens) {
+  return guarded(h, [&]() -> muon_status {
+  char msg[256];
+  muon_logprob_config c;
+  muon_logprob_config_default(&c);
+  if (cfg) c = *cfg;
+  const int rc = check_logprobs(hidden, weight, targets, target_bytes, &c, logprobs, entropy, stats, top_logprobs,
+                                top_tokens, msg, sizeof(msg));
+  if (rc) return handle_error(h, rc, msg);
+  handle_clear_error(h);
+  if (hidden->rows == 0) return MUON_OK;
+  HeadCall call{hidden, weight, targets, target_bytes, c.ignore_index, c.softcap};
+  call.mode = LOGITS_STATS;
+  call.loss = logprobs;
+  call.top = c.top;
+  call.entropy = entropy;
+  call.stats = stats;
+  call.top_logprobs = top_logprobs;
+  call.top_tokens = top_tokens;
+  return head_run(h, call);
+  });
+}
+
+extern "C" muon_status linear_logprobs_grad(muon_handle* h, const muon_matrix* hidden, const muon_matrix* weight,
+                                            const void* targets, int target_bytes, const muon_logprob_config* cfg,
+                                            const float* stats, const float* grad_logprobs, const float* grad_entropy,
+                                            const muon_matrix* dhidden, const muon_matrix* dweight) {
+  return guarded(h, [&]() -> muon_status {
+  char msg[256];
+  muon_logprob_config c;
+  muon_logprob_config_default(&c);
+  if (cfg) c = *cfg;
+  const int rc = check_logprobs_grad(hidden, weight, targets, target_bytes, &c, stats, grad_logprobs, grad_entropy,
+                                     dhidden, dweight, msg, sizeof(msg));
+  if (rc) return handle_error(h, rc, msg);
+  handle_clear_error(h);
+  HeadCall call{hidden, weight, targets, target_bytes, c.ignore_index, c.softcap, dhidden, dweight};
+  call.mode = LOGITS_GRAD;
+  call.stats_in = stats;
+  call.grad_logprobs = grad_logprobs;
+  call.grad_entropy = grad_entropy;
+  return head_run(h, call);
   });
 }

@@ -400,17 +400,15 @@ int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_ma
   return check_apart(spans, msg, len);
 }
 
-int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
-               const muon_loss_config* c, const float* grad_out, const float* loss, const muon_matrix* dh,
-               const muon_matrix* dw, int grad, char* msg, int len) {
-  if (msg && len > 0) msg[0] = 0;
+namespace {
+
+// A head's hidden states, weight, targets and soft cap, with the spans of what is read.
+int check_head(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes, float softcap,
+               std::vector<Span>& v, char* msg, int len) {
   if (!hidden || !weight) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL hidden or weight");
-  if (grad && !dh && !dw) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL dhidden and dweight");
   if (target_bytes != 4 && target_bytes != 8)
     return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "targets of %d bytes: 4 or 8 are supported", target_bytes);
-  if (c->reduction != MUON_REDUCE_NONE && c->reduction != MUON_REDUCE_SUM && c->reduction != MUON_REDUCE_MEAN)
-    return fail(msg, len, MUON_ERR_INVALID_ARG, "unknown reduction %d", (int)c->reduction);
-  if (!(c->softcap >= 0.0f) || !finitef(c->softcap))
+  if (!(softcap >= 0.0f) || !finitef(softcap))
     return fail(msg, len, MUON_ERR_INVALID_ARG, "softcap must be finite and >= 0");
   int rc;
   if ((rc = check_tensor(*hidden, "hidden", 0, msg, len))) return rc;
@@ -428,20 +426,21 @@ int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void*
                 (long long)hidden->rows, (long long)weight->rows, (long long)weight->cols, kMaxDim);
   const int64_t n = hidden->rows;
   if (n > 0 && !targets) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL targets");
-  if ((uintptr_t)targets % (uintptr_t)target_bytes != 0 || ((uintptr_t)loss | (uintptr_t)grad_out) % 4 != 0)
-    return fail(msg, len, MUON_ERR_INVALID_ARG, "targets, loss or grad_out not aligned to their element size");
-  const int64_t each = c->reduction == MUON_REDUCE_NONE ? n : 1;
-  if (each > 0 && !loss) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL loss");
-  std::vector<Span> v;
+  if ((uintptr_t)targets % (uintptr_t)target_bytes != 0)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "targets not aligned to their element size");
   if (n > 0) v.push_back(tensor_span(*hidden, "hidden", 0, false));
   v.push_back(tensor_span(*weight, "weight", 0, false));
   if (n > 0) v.push_back(flat_span(targets, n * target_bytes, "targets", false));
-  if (each > 0) v.push_back(flat_span(loss, each * 4, "loss", true));
+  return MUON_OK;
+}
+int check_head_gradients(const muon_matrix* hidden, const muon_matrix* weight, const muon_matrix* dh,
+                         const muon_matrix* dw, std::vector<Span>& v, char* msg, int len) {
   const muon_matrix* in[] = {hidden, weight};
   const muon_matrix* out[] = {dh, dw};
   const char* from[] = {"hidden", "weight"};
   const char* to[] = {"dhidden", "dweight"};
-  for (int k = 0; grad && k < 2; ++k) {
+  int rc;
+  for (int k = 0; k < 2; ++k) {
     if (!out[k]) continue;
     if ((rc = check_tensor(*out[k], to[k], 0, msg, len))) return rc;
     if ((rc = same_shape(*in[k], *out[k], from[k], to[k], 0, msg, len))) return rc;
@@ -449,9 +448,82 @@ int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void*
       return fail(msg, len, MUON_ERR_UNSUPPORTED_DTYPE, "%s has not the type of %s", to[k], from[k]);
     if (nonempty(*out[k])) v.push_back(tensor_span(*out[k], to[k], 0, true));
   }
+  return MUON_OK;
+}
+
+}  // namespace
+
+int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
+               const muon_loss_config* c, const float* grad_out, const float* loss, const muon_matrix* dh,
+               const muon_matrix* dw, int grad, char* msg, int len) {
+  if (msg && len > 0) msg[0] = 0;
+  std::vector<Span> v;
+  int rc;
+  if ((rc = check_head(hidden, weight, targets, target_bytes, c->softcap, v, msg, len))) return rc;
+  if (grad && !dh && !dw) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL dhidden and dweight");
+  if (c->reduction != MUON_REDUCE_NONE && c->reduction != MUON_REDUCE_SUM && c->reduction != MUON_REDUCE_MEAN)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "unknown reduction %d", (int)c->reduction);
+  if (((uintptr_t)loss | (uintptr_t)grad_out) % 4 != 0)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "loss or grad_out not aligned to its element size");
+  const int64_t each = c->reduction == MUON_REDUCE_NONE ? hidden->rows : 1;
+  if (each > 0 && !loss) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL loss");
+  if (each > 0) v.push_back(flat_span(loss, each * 4, "loss", true));
+  if (grad && (rc = check_head_gradients(hidden, weight, dh, dw, v, msg, len))) return rc;
   if (grad && grad_out && each > 0) v.push_back(flat_span(grad_out, each * 4, "grad_out", false));
   return check_apart(v, msg, len);
 }
+
+int check_logprobs(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
+                   const muon_logprob_config* c, const float* logprobs, const float* entropy, const float* stats,
+                   const float* top_logprobs, const int64_t* top_tokens, char* msg, int len) {
+  if (msg && len > 0) msg[0] = 0;
+  std::vector<Span> v;
+  int rc;
+  if ((rc = check_head(hidden, weight, targets, target_bytes, c->softcap, v, msg, len))) return rc;
+  if (c->top < 0 || c->top > MUON_TOP_MOST || c->top > weight->rows)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "%d alternatives: 0 to %d, and no more than the vocabulary's %lld, are supported",
+                (int)c->top, MUON_TOP_MOST, (long long)weight->rows);
+  const int64_t n = hidden->rows;
+  if (n == 0) return MUON_OK;
+  if (!logprobs) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL logprobs");
+  if (c->top && (!top_logprobs || !top_tokens))
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL top_logprobs or top_tokens");
+  if (((uintptr_t)logprobs | (uintptr_t)entropy) % 4 != 0 || (uintptr_t)stats % 16 != 0 ||
+      (c->top && ((uintptr_t)top_logprobs % 4 != 0 || (uintptr_t)top_tokens % 8 != 0)))
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "an output is not aligned to its element size (stats: 16 bytes)");
+  v.push_back(flat_span(logprobs, n * 4, "logprobs", true));
+  if (entropy) v.push_back(flat_span(entropy, n * 4, "entropy", true));
+  if (stats) v.push_back(flat_span(stats, n * 16, "stats", true));
+  if (c->top) {
+    v.push_back(flat_span(top_logprobs, n * c->top * 4, "top_logprobs", true));
+    v.push_back(flat_span(top_tokens, n * c->top * 8, "top_tokens", true));
+  }
+  return check_apart(v, msg, len);
+}
+
+int check_logprobs_grad(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
+                        const muon_logprob_config* c, const float* stats, const float* grad_logprobs,
+                        const float* grad_entropy, const muon_matrix* dh, const muon_matrix* dw, char* msg, int len) {
+  if (msg && len > 0) msg[0] = 0;
+  std::vector<Span> v;
+  int rc;
+  if ((rc = check_head(hidden, weight, targets, target_bytes, c->softcap, v, msg, len))) return rc;
+  if (!dh && !dw) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL dhidden and dweight");
+  const int64_t n = hidden->rows;
+  if (n > 0 && !stats) return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL stats");
+  if (n > 0 && !grad_logprobs && !grad_entropy)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "NULL grad_logprobs and grad_entropy");
+  if ((uintptr_t)stats % 16 != 0 || ((uintptr_t)grad_logprobs | (uintptr_t)grad_entropy) % 4 != 0)
+    return fail(msg, len, MUON_ERR_INVALID_ARG, "stats or a gradient is not aligned to its element size (stats: 16 bytes)");
+  if (n > 0) {
+    v.push_back(flat_span(stats, n * 16, "stats", false));
+    if (grad_logprobs) v.push_back(flat_span(grad_logprobs, n * 4, "grad_logprobs", false));
+    if (grad_entropy) v.push_back(flat_span(grad_entropy, n * 4, "grad_entropy", false));
+  }
+  if ((rc = check_head_gradients(hidden, weight, dh, dw, v, msg, len))) return rc;
+  return check_apart(v, msg, len);
+}
+
 
 namespace {
 
@@ -600,6 +672,39 @@ extern "C" muon_status muon_check_loss_args(const muon_matrix* hidden, const muo
     return muon::check_loss(hidden, weight, targets, target_bytes, &c, grad_out, loss, dhidden, dweight,
                             dhidden || dweight ? 1 : 0, msg, msg_len);
   });
+}
+
+extern "C" muon_status muon_check_logprob_args(const muon_matrix* hidden, const muon_matrix* weight,
+                                               const void* targets, int target_bytes, const muon_logprob_config* cfg,
+                                               const float* logprobs, const float* entropy, const float* stats,
+                                               const float* top_logprobs, const int64_t* top_tokens, char* msg,
+                                               int msg_len) {
+  muon_logprob_config c;
+  muon_logprob_config_default(&c);
+  if (cfg) c = *cfg;
+  return checked(msg, msg_len, [&] {
+    return muon::check_logprobs(hidden, weight, targets, target_bytes, &c, logprobs, entropy, stats, top_logprobs,
+                                top_tokens, msg, msg_len);
+  });
+}
+extern "C" muon_status muon_check_logprob_grad_args(const muon_matrix* hidden, const muon_matrix* weight,
+                                                    const void* targets, int target_bytes,
+                                                    const muon_logprob_config* cfg, const float* stats,
+                                                    const float* grad_logprobs, const float* grad_entropy,
+                                                    const muon_matrix* dhidden, const muon_matrix* dweight, char* msg,
+                                                    int msg_len) {
+  muon_logprob_config c;
+  muon_logprob_config_default(&c);
+  if (cfg) c = *cfg;
+  return checked(msg, msg_len, [&] {
+    return muon::check_logprobs_grad(hidden, weight, targets, target_bytes, &c, stats, grad_logprobs, grad_entropy,
+                                     dhidden, dweight, msg, msg_len);
+  });
+}
+
+extern "C" void muon_logprob_config_default(muon_logprob_config* c) {
+  if (!c) return;
+  *c = muon_logprob_config{0, 0.0f, -100};
 }
 
 namespace {

@@ -28,6 +28,12 @@ int check_adamw(int n, const muon_matrix* g, const muon_matrix* m, const muon_ma
 int check_loss(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
                const muon_loss_config* cfg, const float* grad_out, const float* loss, const muon_matrix* dhidden,
                const muon_matrix* dweight, int grad, char* msg, int len);
+int check_logprobs(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
+                   const muon_logprob_config* c, const float* logprobs, const float* entropy, const float* stats,
+                   const float* top_logprobs, const int64_t* top_tokens, char* msg, int len);
+int check_logprobs_grad(const muon_matrix* hidden, const muon_matrix* weight, const void* targets, int target_bytes,
+                        const muon_logprob_config* c, const float* stats, const float* grad_logprobs,
+                        const float* grad_entropy, const muon_matrix* dh, const muon_matrix* dw, char* msg, int len);
 
 // Norms around a block (norm_api.cpp).
 constexpr int kNormMostD = 16384;                     // channels
