@@ -60,8 +60,9 @@ inline int64_t norm_part_floats(int want, int dp) {
 
 // x_half, y_half: types of x (out, dout, dx) and of y (hidden, dhidden, dy, a full gate).
 hipError_t launch_residual_norm(const NormArgs& a, int x_half, int y_half, hipStream_t s);
-// Blocks of the backward launch, which leaves as many partials.
-int norm_grad_blocks(int64_t n, int d);
+// Blocks of the backward launch (n > 0), which leaves as many partials.
+constexpr int kNormMostBlocks = 1024;
+int norm_grad_blocks(const NormArgs& a, int x_half, int y_half);
 hipError_t launch_residual_norm_grad(const NormArgs& a, int x_half, int y_half, hipStream_t s);
 hipError_t launch_norm_sums(const NormSums& a, hipStream_t s);
 

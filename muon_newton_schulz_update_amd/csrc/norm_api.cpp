@@ -93,14 +93,15 @@ extern "C" muon_status residual_norm_grad(muon_handle* h, const muon_matrix* x, 
   if (g.scale) a.want |= a.scale.kind == NORM_ONE ? kWantScaleOne : kWantScale;
   if (g.pre_gain) a.want |= kWantPre;
   const hipStream_t s = handle_stream(h);
-  if (a.n > 0) a.blocks = norm_grad_blocks(a.n, a.d);
+  const int x_half = half(x, *x), y_half = half(y ? y : dhidden, *x);
+  if (a.n > 0) a.blocks = norm_grad_blocks(a, x_half, y_half);
   if (a.want) {
     a.part_floats = norm_part_floats(a.want, a.dp);
     GrowBuffer& b = train_state(h).rows;
     if (muon_status st = grow(h, b, (size_t)a.part_floats * 4 * (a.blocks ? a.blocks : 1), "norm gradient")) return st;
     a.part = (float*)b.ptr;
   }
-  if (a.n > 0) HIP_DO(h, launch_residual_norm_grad(a, half(x, *x), half(y ? y : dhidden, *x), s));
+  if (a.n > 0) HIP_DO(h, launch_residual_norm_grad(a, x_half, y_half, s));
   if (!a.want) return MUON_OK;
   NormSums t{};
   t.part = a.part;

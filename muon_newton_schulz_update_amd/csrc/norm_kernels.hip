@@ -26,54 +26,50 @@ namespace {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
-// Eight channels from c of a row of d as they are in memory, zero past its end;
-// one or two loads where whole, aligned or not.
-template <typename T>
+// A thread's chunk of CH (4 or 8) channels from c of a row of d as they are in
+// memory, zero past its end; one or two loads where whole, aligned or not.
+template <typename T, int CH>
 struct Raw {
-  u32x4_t q[sizeof(T) / 2];
+  uint32_t w[CH * sizeof(T) / 4];
 };
-template <typename T>
-__device__ __forceinline__ void load_raw(const T* row, int c, int d, Raw<T>& v) {
-  if (c + 8 <= d) {
-    __builtin_memcpy(&v, row + c, 8 * sizeof(T));
+template <typename T, int CH>
+__device__ __forceinline__ void load_raw(const T* row, int c, int d, Raw<T, CH>& v) {
+  if (c + CH <= d) {
+    __builtin_memcpy(&v, row + c, sizeof(v));
   } else {
-    T x[8];
+    T x[CH];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = c + e < d ? row[c + e] : T(0);
-    __builtin_memcpy(&v, x, 8 * sizeof(T));
+    for (int e = 0; e < CH; ++e) x[e] = c + e < d ? row[c + e] : T(0);
+    __builtin_memcpy(&v, x, sizeof(v));
   }
 }
-template <typename T>
-__device__ __forceinline__ void unpack(const Raw<T>& r, float (&v)[8]) {
-  if constexpr (sizeof(T) == 2) {
+template <typename T, int CH>
+__device__ __forceinline__ void unpack(const Raw<T, CH>& r, float (&v)[CH]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(r.q[0][e] << 16);
-      v[2 * e + 1] = __uint_as_float(r.q[0][e] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r.q[e >> 2][e & 3]);
+  for (int e = 0; e < CH; ++e) {
+    if constexpr (sizeof(T) == 2) v[e] = __uint_as_float(e & 1 ? r.w[e / 2] & 0xFFFF0000u : r.w[e / 2] << 16);
+    else v[e] = __uint_as_float(r.w[e]);
   }
 }
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int d, float (&v)[8]) {
-  Raw<T> r;
+template <int CH, typename T>
+__device__ __forceinline__ void load_chunk(const T* row, int c, int d, float (&v)[CH]) {
+  Raw<T, CH> r;
   load_raw(row, c, d, r);
   unpack(r, v);
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* row, int c, int d, const float (&v)[8]) {
-  if (c + 8 <= d) {
-    if constexpr (sizeof(T) == 2) {
-      const u32x4_t q = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-      __builtin_memcpy(row + c, &q, 16);
-    } else {
-      __builtin_memcpy(row + c, v, 32);
+template <int CH, typename T>
+__device__ __forceinline__ void store_chunk(T* row, int c, int d, const float (&v)[CH]) {
+  if (c + CH <= d) {
+    Raw<T, CH> r;
+#pragma unroll
+    for (int e = 0; e < CH; ++e) {
+      if constexpr (sizeof(T) == 2) r.w[e / 2] = e & 1 ? pack_bf16(v[e & ~1], v[e]) : 0u;
+      else r.w[e] = __float_as_uint(v[e]);
     }
+    __builtin_memcpy(row + c, &r, sizeof(r));
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < CH; ++e)
       if (c + e < d) {
         if constexpr (sizeof(T) == 2) row[c + e] = f2bf(v[e]);
         else row[c + e] = v[e];
@@ -84,15 +80,16 @@ __device__ __forceinline__ void store8(T* row, int c, int d, const float (&v)[8]
 __device__ __forceinline__ float one_value(const NormParam& p, int64_t i) {
   return p.half ? bf2f(((const u16*)p.ptr)[i]) : ((const float*)p.ptr)[i];
 }
-// A parameter's eight channels (1 where it is not there; NORM_FULL is the rows').
-__device__ __forceinline__ void load_param(const NormParam& p, int c, int d, float (&v)[8]) {
+// A parameter's chunk (1 where it is not there; NORM_FULL is the rows').
+template <int CH>
+__device__ __forceinline__ void load_param(const NormParam& p, int c, int d, float (&v)[CH]) {
   if (p.kind == NORM_CHANNELS) {
-    if (p.half) load8((const u16*)p.ptr, c, d, v);
-    else load8((const float*)p.ptr, c, d, v);
+    if (p.half) load_chunk((const u16*)p.ptr, c, d, v);
+    else load_chunk((const float*)p.ptr, c, d, v);
   } else {
     const float x = p.kind == NORM_ONE ? one_value(p, 0) : 1.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = x;
+    for (int e = 0; e < CH; ++e) v[e] = x;
   }
 }
 
@@ -119,235 +116,219 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float* sh) {
   }
 }
 
-// A row's operands, loaded together and one row ahead of their use.
-template <typename TX, typename TY, int NC>
-struct ForwardRow {
-  Raw<TX> x[NC];
-  Raw<TY> y[NC], g[NC];
-  template <int TPR>
+// A row's operands, loaded together and, where the registers hold two, one row
+// ahead of their use. GENERAL, here and below: with a gate for each element, or a
+// scale for each channel.
+template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL, bool BACKWARD>
+struct Row {
+  Raw<TX, CH> x[NC], dout[BACKWARD ? NC : 1];
+  Raw<TY, CH> y[NC], g[GENERAL ? NC : 1], dhidden[BACKWARD ? NC : 1];
   __device__ __forceinline__ void load(const NormArgs& a, int64_t r, int t) {
+    auto rows = [&](auto& to, const void* p, int64_t ld, auto type) {
+      typedef decltype(type) T;
 #pragma unroll
-    for (int k = 0; k < NC; ++k) load_raw((const TX*)a.x.ptr + r * a.x.ld, 8 * (k * TPR + t), a.d, x[k]);
-    if (a.y.ptr)
-#pragma unroll
-      for (int k = 0; k < NC; ++k) load_raw((const TY*)a.y.ptr + r * a.y.ld, 8 * (k * TPR + t), a.d, y[k]);
-    if (a.gate.kind == NORM_FULL)
-#pragma unroll
-      for (int k = 0; k < NC; ++k) load_raw((const TY*)a.gate.ptr + r * a.gate.ld, 8 * (k * TPR + t), a.d, g[k]);
+      for (int k = 0; k < NC; ++k) load_raw((const T*)p + r * ld, CH * (k * TPR + t), a.d, to[k]);
+    };
+    rows(x, a.x.ptr, a.x.ld, TX());
+    if (a.y.ptr) rows(y, a.y.ptr, a.y.ld, TY());
+    if constexpr (BACKWARD) {
+      if (a.dhidden.ptr) rows(dhidden, a.dhidden.ptr, a.dhidden.ld, TY());
+      if (a.dout.ptr) rows(dout, a.dout.ptr, a.dout.ld, TX());
+    }
+    if constexpr (GENERAL)
+      if (a.gate.kind == NORM_FULL) rows(g, a.gate.ptr, a.gate.ld, TY());
   }
 };
 
-// TPR threads to a row, NC chunks of eight channels to a thread; the threads past
-// TPR of a block have other rows.
-template <typename TX, typename TY, int TPR, int NC, int BLOCK>
+// TPR threads to a row, NC chunks of CH channels to a thread; the threads past TPR
+// of a block have other rows.
+template <typename TX, typename TY, int TPR, int NC, int CH, int BLOCK, bool GENERAL>
 __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
   constexpr int ROWS = BLOCK / TPR;
-  constexpr bool AHEAD = NC == 1 || TPR <= 64;      // (the registers hold no second row otherwise)
+  constexpr bool AHEAD = NC * CH <= 12 || TPR <= 64;
   __shared__ float sh[2][BLOCK / 64];
   const int t = threadIdx.x % TPR, d = a.d;
   const int64_t step = (int64_t)gridDim.x * ROWS;
   // (every thread of a block goes round as often; rows past the last one are
   // the last one again and are not stored)
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-  ForwardRow<TX, TY, NC> next;
-  if (AHEAD) next.template load<TPR>(a, min(row, a.n - 1), t);
+  Row<TX, TY, TPR, NC, CH, GENERAL, false> now, next;
+  if (AHEAD) next.load(a, min(row, a.n - 1), t);
   const bool there = a.y.ptr != nullptr;
-  float gate[NC][8], pre[NC][8], scale[NC][8];
+  float gate[NC][CH], pre[NC][CH], scale[GENERAL ? NC : 1][CH];
+  const float scale1 = a.scale.kind == NORM_ONE ? one_value(a.scale, 0) : 1.f;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    const int c = 8 * (k * TPR + t);
-    float post[8];
-    load_param(a.scale, c, d, scale[k]);
+    const int c = CH * (k * TPR + t);
+    float post[CH];
+    if (GENERAL) load_param(a.scale, c, d, scale[GENERAL ? k : 0]);
     load_param(a.pre_gain, c, d, pre[k]);
     load_param(a.post_gain, c, d, post);
     load_param(a.gate, c, d, gate[k]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gate[k][e] *= post[e];
+    for (int e = 0; e < CH; ++e) gate[k][e] *= post[e];
   }
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.n; r0 += step, row += step) {
     const bool real = row < a.n;
-    ForwardRow<TX, TY, NC> now;
     if (AHEAD) {
       now = next;
-      if (r0 + step < a.n) next.template load<TPR>(a, min(row + step, a.n - 1), t);
+      if (r0 + step < a.n) next.load(a, min(row + step, a.n - 1), t);
     } else {
-      now.template load<TPR>(a, min(row, a.n - 1), t);
+      now.load(a, min(row, a.n - 1), t);
     }
-    float x[NC][8], s[1] = {0.f};
+    float x[NC][CH], s[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       unpack(now.x[k], x[k]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] *= scale[k][e];
+      for (int e = 0; e < CH; ++e) x[k][e] *= GENERAL ? scale[GENERAL ? k : 0][e] : scale1;
     }
     if (there) {
-      float y[NC][8], r1 = 1.f;
+      float y[NC][CH], r1 = 1.f;
 #pragma unroll
       for (int k = 0; k < NC; ++k) unpack(now.y[k], y[k]);
       if (a.post) {
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[0] = fmaf(y[k][e], y[k][e], s[0]);
+          for (int e = 0; e < CH; ++e) s[0] = fmaf(y[k][e], y[k][e], s[0]);
         row_sums<TPR>(s, sh[0]);
         r1 = 1.f / sqrtf(s[0] / d + a.eps);
       }
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
-        if (a.gate.kind == NORM_FULL) {
-          float g[8];
-          unpack(now.g[k], g);
+        if (GENERAL && a.gate.kind == NORM_FULL) {
+          float g[CH];
+          unpack(now.g[GENERAL ? k : 0], g);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[k][e] *= g[e];
+          for (int e = 0; e < CH; ++e) y[k][e] *= g[e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = fmaf(y[k][e] * r1, gate[k][e], x[k][e]);
+        for (int e = 0; e < CH; ++e) x[k][e] = fmaf(y[k][e] * r1, gate[k][e], x[k][e]);
       }
     }
     if (a.out.ptr && real)
 #pragma unroll
-      for (int k = 0; k < NC; ++k) store8((TX*)a.out.ptr + row * a.out.ld, 8 * (k * TPR + t), d, x[k]);
+      for (int k = 0; k < NC; ++k) store_chunk((TX*)a.out.ptr + row * a.out.ld, CH * (k * TPR + t), d, x[k]);
     if (a.pre) {
       s[0] = 0.f;
 #pragma unroll
       for (int k = 0; k < NC; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] = fmaf(x[k][e], x[k][e], s[0]);
+        for (int e = 0; e < CH; ++e) s[0] = fmaf(x[k][e], x[k][e], s[0]);
       row_sums<TPR>(s, sh[1]);
       const float r2 = 1.f / sqrtf(s[0] / d + a.eps);
       if (real)
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[k][e] *= r2 * pre[k][e];
-          store8((TY*)a.hidden.ptr + row * a.hidden.ld, 8 * (k * TPR + t), d, x[k]);
+          for (int e = 0; e < CH; ++e) x[k][e] *= r2 * pre[k][e];
+          store_chunk((TY*)a.hidden.ptr + row * a.hidden.ld, CH * (k * TPR + t), d, x[k]);
         }
     }
     if (TPR > 64 && r0 + step < a.n) __syncthreads();   // the sums are read before the next row's are written
   }
 }
 
-template <typename TX, typename TY, int NC, bool GENERAL>
-struct BackwardRow {
-  Raw<TX> x[NC], dout[NC];
-  Raw<TY> y[NC], g[GENERAL ? NC : 1], dhidden[NC];
-  template <int TPR>
-  __device__ __forceinline__ void load(const NormArgs& a, int64_t r, int t) {
-#pragma unroll
-    for (int k = 0; k < NC; ++k) load_raw((const TX*)a.x.ptr + r * a.x.ld, 8 * (k * TPR + t), a.d, x[k]);
-    if (a.y.ptr)
-#pragma unroll
-      for (int k = 0; k < NC; ++k) load_raw((const TY*)a.y.ptr + r * a.y.ld, 8 * (k * TPR + t), a.d, y[k]);
-    if (a.dhidden.ptr)
-#pragma unroll
-      for (int k = 0; k < NC; ++k) load_raw((const TY*)a.dhidden.ptr + r * a.dhidden.ld, 8 * (k * TPR + t), a.d, dhidden[k]);
-    if (a.dout.ptr)
-#pragma unroll
-      for (int k = 0; k < NC; ++k) load_raw((const TX*)a.dout.ptr + r * a.dout.ld, 8 * (k * TPR + t), a.d, dout[k]);
-    if (GENERAL && a.gate.kind == NORM_FULL)
-#pragma unroll
-      for (int k = 0; k < NC; ++k) load_raw((const TY*)a.gate.ptr + r * a.gate.ld, 8 * (k * TPR + t), a.d, g[k]);
-  }
-};
-
-// GENERAL: with a gate for each element, or a scale for each channel.
-template <typename TX, typename TY, int TPR, int NC, int BLOCK, bool GENERAL>
+template <typename TX, typename TY, int TPR, int NC, int CH, int BLOCK, bool GENERAL>
 __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
   constexpr int ROWS = BLOCK / TPR;
   // what the registers hold: a second row, and the parameters (read again for
   // each row otherwise)
-  constexpr bool WIDE = TPR == 1024, AHEAD = !WIDE && !(GENERAL && NC > 1);
+  constexpr bool WIDE = TPR == 1024, AHEAD = !WIDE && !(GENERAL && NC * CH > 12);
   __shared__ float sh[4][2 * (BLOCK / 64)];
-  __shared__ __attribute__((aligned(16))) float joined[ROWS > 1 ? BLOCK * 8 : 8];
+  __shared__ float joined[ROWS > 1 ? BLOCK * CH : 1];
   const int t = threadIdx.x % TPR, d = a.d;
   const bool there = a.y.ptr != nullptr, full = GENERAL && a.gate.kind == NORM_FULL, normed = a.dhidden.ptr != nullptr;
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-  BackwardRow<TX, TY, NC, GENERAL> next;
-  if (AHEAD) next.template load<TPR>(a, min(row, a.n - 1), t);
+  Row<TX, TY, TPR, NC, CH, GENERAL, true> now, next;
+  if (AHEAD) next.load(a, min(row, a.n - 1), t);
   // gate and post_gain multiplied (post_gain alone where the gate is full)
-  auto load_gated = [&](int k, float (&v)[8]) {
-    const int c = 8 * (k * TPR + t);
-    float post[8];
+  auto load_gated = [&](int k, float (&v)[CH]) {
+    const int c = CH * (k * TPR + t);
+    float post[CH];
     load_param(a.post_gain, c, d, post);
     load_param(a.gate, c, d, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= post[e];
+    for (int e = 0; e < CH; ++e) v[e] *= post[e];
   };
-  float scale[GENERAL ? NC : 1][8], gated[WIDE ? 1 : NC][8], pre[WIDE ? 1 : NC][8];
+  float scale[GENERAL ? NC : 1][CH], gated[WIDE ? 1 : NC][CH], pre[WIDE ? 1 : NC][CH];
   const float scale1 = a.scale.kind == NORM_ONE ? one_value(a.scale, 0) : 1.f;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    if (GENERAL) load_param(a.scale, 8 * (k * TPR + t), d, scale[GENERAL ? k : 0]);
+    if (GENERAL) load_param(a.scale, CH * (k * TPR + t), d, scale[GENERAL ? k : 0]);
     if (!WIDE) {
-      load_param(a.pre_gain, 8 * (k * TPR + t), d, pre[WIDE ? 0 : k]);
+      load_param(a.pre_gain, CH * (k * TPR + t), d, pre[WIDE ? 0 : k]);
       load_gated(k, gated[WIDE ? 0 : k]);
     }
   }
-  // (row by row in wide rows)
-  auto gated_of = [&](int k) -> float (&)[8] {
+  auto gated_of = [&](int k) -> float (&)[CH] {
     if (WIDE) load_gated(k, gated[0]);
     return gated[WIDE ? 0 : k];
   };
-  auto pre_of = [&](int k) -> float (&)[8] {
-    if (WIDE) load_param(a.pre_gain, 8 * (k * TPR + t), d, pre[0]);
+  auto pre_of = [&](int k) -> float (&)[CH] {
+    if (WIDE) load_param(a.pre_gain, CH * (k * TPR + t), d, pre[0]);
     return pre[WIDE ? 0 : k];
   };
   auto scale_of = [&](int k, int e) { return GENERAL ? scale[GENERAL ? k : 0][e] : scale1; };
-  float sum_block[NC][8], sum_scale[GENERAL ? NC : 1][8], sum_pre[NC][8], gate_one = 0.f, scale_one = 0.f;
+  // a single gate's gradient is that of the channels, weighted by post_gain in the end
+  const bool vector = (a.want & kWantBlock) || ((a.want & kWantGateOne) && a.post_gain.ptr);
+  float sum_block[NC][CH], sum_scale[GENERAL ? NC : 1][CH], sum_pre[NC][CH], gate_one = 0.f, scale_one = 0.f;
 #pragma unroll
   for (int k = 0; k < NC; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum_block[k][e] = sum_scale[GENERAL ? k : 0][e] = sum_pre[k][e] = 0.f;
+    for (int e = 0; e < CH; ++e) sum_block[k][e] = sum_scale[GENERAL ? k : 0][e] = sum_pre[k][e] = 0.f;
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.n; r0 += step, row += step) {
     const bool real = row < a.n;
-    BackwardRow<TX, TY, NC, GENERAL> now;
     if (AHEAD) {
       now = next;
-      if (r0 + step < a.n) next.template load<TPR>(a, min(row + step, a.n - 1), t);
+      if (r0 + step < a.n) next.load(a, min(row + step, a.n - 1), t);
     } else {
-      now.template load<TPR>(a, min(row, a.n - 1), t);
+      now.load(a, min(row, a.n - 1), t);
     }
     // y becomes yhat, o the row's out
-    float y[NC][8], o[NC][8], r1 = 1.f, s[2] = {0.f, 0.f};
+    float y[NC][CH], o[NC][CH], r1 = 1.f;
     if (there) {
-      float q[1] = {0.f};
 #pragma unroll
-      for (int k = 0; k < NC; ++k) {
-        unpack(now.y[k], y[k]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[0] = fmaf(y[k][e], y[k][e], q[0]);
-      }
+      for (int k = 0; k < NC; ++k) unpack(now.y[k], y[k]);
       if (a.post) {
+        float q[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+          for (int e = 0; e < CH; ++e) q[0] = fmaf(y[k][e], y[k][e], q[0]);
         row_sums<TPR>(q, sh[0]);
         r1 = 1.f / sqrtf(q[0] / d + a.eps);
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+          for (int e = 0; e < CH; ++e) y[k][e] *= r1;
       }
     }
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       unpack(now.x[k], o[k]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[k][e] *= scale_of(k, e);
+      for (int e = 0; e < CH; ++e) o[k][e] *= scale_of(k, e);
       if (there) {
-        float g[8];
+        float g[CH];
         if (full) unpack(now.g[GENERAL ? k : 0], g);
-        const float (&w)[8] = gated_of(k);
+        const float (&w)[CH] = gated_of(k);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[k][e] *= r1;
-          o[k][e] = fmaf(full ? w[e] * g[e] : w[e], y[k][e], o[k][e]);
-        }
+        for (int e = 0; e < CH; ++e) o[k][e] = fmaf(full ? w[e] * g[e] : w[e], y[k][e], o[k][e]);
       }
     }
     float r2 = 0.f, m = 0.f;
     if (normed) {
+      float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
-        float u[8];
+        float u[CH];
         unpack(now.dhidden[k], u);
-        const float (&w)[8] = pre_of(k);
+        const float (&w)[CH] = pre_of(k);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < CH; ++e) {
           s[0] = fmaf(o[k][e], o[k][e], s[0]);
           s[1] = fmaf(o[k][e], u[e] * w[e], s[1]);
         }
@@ -360,78 +341,76 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
     float v[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-      const int c = 8 * (k * TPR + t);
-      float dt[8], x[8];
+      const int c = CH * (k * TPR + t);
+      float dt[CH], x[CH];
       if (a.dout.ptr) {
         unpack(now.dout[k], dt);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dt[e] = 0.f;
+        for (int e = 0; e < CH; ++e) dt[e] = 0.f;
       }
       if (normed) {
-        float u[8];
+        float u[CH];
         unpack(now.dhidden[k], u);
-        const float (&w)[8] = pre_of(k);
+        const float (&w)[CH] = pre_of(k);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < CH; ++e) {
           const float xh = o[k][e] * r2;
           dt[e] += r2 * (u[e] * w[e] - xh * m);
           if (real) sum_pre[k][e] = fmaf(u[e], xh, sum_pre[k][e]);
         }
       }
       if (a.dx.ptr && real) {
-        float q[8];
+        float q[CH];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = dt[e] * scale_of(k, e);
-        store8((TX*)a.dx.ptr + row * a.dx.ld, c, d, q);
+        for (int e = 0; e < CH; ++e) q[e] = dt[e] * scale_of(k, e);
+        store_chunk((TX*)a.dx.ptr + row * a.dx.ld, c, d, q);
       }
       if ((a.want & (kWantScale | kWantScaleOne)) && real) {
         unpack(now.x[k], x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < CH; ++e) {
           if (GENERAL && (a.want & kWantScale)) sum_scale[GENERAL ? k : 0][e] = fmaf(dt[e], x[e], sum_scale[GENERAL ? k : 0][e]);
           else scale_one = fmaf(dt[e], x[e], scale_one);
         }
       }
       if (there) {
-        float g[8];
+        float g[CH];
         if (full) unpack(now.g[GENERAL ? k : 0], g);
-        const float (&w)[8] = gated_of(k);
+        const float (&w)[CH] = gated_of(k);
         if (full && a.dfull.ptr && real) {
-          float q[8];
+          float q[CH];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q[e] = dt[e] * w[e] * y[k][e];
-          store8((TY*)a.dfull.ptr + row * a.dfull.ld, c, d, q);
+          for (int e = 0; e < CH; ++e) q[e] = dt[e] * w[e] * y[k][e];
+          store_chunk((TY*)a.dfull.ptr + row * a.dfull.ld, c, d, q);
         }
-        if ((a.want & kWantBlock) && real)
+        if (vector && real) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum_block[k][e] = fmaf(full ? dt[e] * g[e] : dt[e], y[k][e], sum_block[k][e]);
-        if ((a.want & kWantGateOne) && real) {
-          float post[8];
-          load_param(a.post_gain, c, d, post);
+          for (int e = 0; e < CH; ++e) sum_block[k][e] = fmaf(full ? dt[e] * g[e] : dt[e], y[k][e], sum_block[k][e]);
+        } else if ((a.want & kWantGateOne) && real) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) gate_one = fmaf(dt[e] * post[e], y[k][e], gate_one);
+          for (int e = 0; e < CH; ++e) gate_one = fmaf(dt[e], y[k][e], gate_one);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          o[k][e] = dt[e] * (full ? w[e] * g[e] : w[e]);
-          v[0] = fmaf(o[k][e], y[k][e], v[0]);
-        }
+        for (int e = 0; e < CH; ++e) o[k][e] = dt[e] * (full ? w[e] * g[e] : w[e]);
       }
     }
     if (there && a.dy.ptr) {
-      float back = 0.f;
       if (a.post) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+          for (int e = 0; e < CH; ++e) v[0] = fmaf(o[k][e], y[k][e], v[0]);
         row_sums<TPR>(v, sh[2]);
-        back = v[0] / d;
+        const float back = v[0] / d;
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+          for (int e = 0; e < CH; ++e) o[k][e] = r1 * (o[k][e] - y[k][e] * back);
       }
       if (real)
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[k][e] = r1 * (o[k][e] - y[k][e] * back);
-          store8((TY*)a.dy.ptr + row * a.dy.ld, 8 * (k * TPR + t), d, o[k]);
-        }
+        for (int k = 0; k < NC; ++k) store_chunk((TY*)a.dy.ptr + row * a.dy.ld, CH * (k * TPR + t), d, o[k]);
     }
     if (TPR > 64) __syncthreads();   // the sums are read before the next row's are written
   }
@@ -439,24 +418,26 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
   float* part = a.part + blockIdx.x * a.part_floats;
   auto leave = [&](auto& sum) {
 #pragma unroll
-    for (int k = 0; k < (int)(sizeof(sum) / 32); ++k) {
-      const int c = 8 * (k * TPR + t);
+    for (int k = 0; k < (int)(sizeof(sum) / sizeof(sum[0])); ++k) {
       if constexpr (ROWS > 1) {
-        // (threads of neighbouring channels next to one another: no bank is asked twice)
+        // (threads of neighbouring chunks next to one another: no bank is asked twice)
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) joined[e * BLOCK + threadIdx.x] = sum[k][e];
+        for (int e = 0; e < CH; ++e) joined[e * BLOCK + threadIdx.x] = sum[k][e];
         __syncthreads();
-        for (int i = threadIdx.x; i < TPR * 8; i += BLOCK) {
+        for (int i = threadIdx.x; i < TPR * CH; i += BLOCK) {
+          // (neighbouring threads write neighbouring channels)
+          const int of = i / CH, e = i % CH, at = CH * (k * TPR) + i;
           float x = 0.f;
 #pragma unroll
-          for (int q = 0; q < ROWS; ++q) x += joined[i / TPR * BLOCK + q * TPR + i % TPR];
-          const int at = 8 * (k * TPR + i % TPR) + i / TPR;
+          for (int q = 0; q < ROWS; ++q) x += joined[e * BLOCK + q * TPR + of];
           if (at < a.dp) part[at] = x;
         }
-      } else if (c < a.dp) {
-        *(f32x4_t*)(part + c) = (f32x4_t){sum[k][0], sum[k][1], sum[k][2], sum[k][3]};
-        *(f32x4_t*)(part + c + 4) = (f32x4_t){sum[k][4], sum[k][5], sum[k][6], sum[k][7]};
+      } else {
+        const int c = CH * (k * TPR + t);
+#pragma unroll
+        for (int e = 0; e < CH; e += 4)
+          if (c + e < a.dp) *(f32x4_t*)(part + c + e) = (f32x4_t){sum[k][e], sum[k][e + 1], sum[k][e + 2], sum[k][e + 3]};
       }
     }
     part += a.dp;
@@ -465,6 +446,15 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
   if (GENERAL && (a.want & kWantScale)) leave(sum_scale);
   if (a.want & kWantPre) leave(sum_pre);
   if (a.want & (kWantGateOne | kWantScaleOne)) {
+    if (vector) {
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        float post[CH];
+        load_param(a.post_gain, CH * (k * TPR + t), d, post);
+#pragma unroll
+        for (int e = 0; e < CH; ++e) gate_one = fmaf(post[e], sum_block[k][e], gate_one);
+      }
+    }
     gate_one = lanes_sum<64>(gate_one);
     scale_one = lanes_sum<64>(scale_one);
     if ((threadIdx.x & 63) == 0) {
@@ -535,60 +525,105 @@ __global__ __launch_bounds__(1024) void k_norm_sums(NormSums a) {
 
 }  // namespace
 
-// By the width: chunks of eight channels to a thread, sixteen threads to a row up
-// to 128 channels, a wave up to 1024, then as many threads as there are chunks.
+// By the width, RUN(threads to a row, chunks to a thread, channels of a chunk):
+// sixteen threads up to 128 channels, a wave up to 1024, then as many threads as
+// there are chunks. (Up to 768: three chunks of 4 rather than two of 8, a
+// quarter of whose lanes would have nothing.)
 #define BY_WIDTH(d, RUN)                                  \
   do {                                                    \
-    if ((d) <= 128) RUN(16, 1);                           \
-    else if ((d) <= 512) RUN(64, 1);                      \
-    else if ((d) <= 1024) RUN(64, 2);                     \
-    else if ((d) <= 2048) RUN(256, 1);                    \
-    else if ((d) <= 4096) RUN(512, 1);                    \
-    else if ((d) <= 8192) RUN(512, 2);                    \
-    else RUN(1024, 2);                                    \
-  } while (0)
-#define BY_TYPES(g, K, TPR, NC, BLOCK, ...)                                                                          \
-  do {                                                                                                               \
-    if (x_half) hipLaunchKernelGGL((K<u16, u16, TPR, NC, BLOCK, ##__VA_ARGS__>), g, dim3(BLOCK), 0, s, a);           \
-    else if (y_half) hipLaunchKernelGGL((K<float, u16, TPR, NC, BLOCK, ##__VA_ARGS__>), g, dim3(BLOCK), 0, s, a);    \
-    else hipLaunchKernelGGL((K<float, float, TPR, NC, BLOCK, ##__VA_ARGS__>), g, dim3(BLOCK), 0, s, a);              \
+    if ((d) <= 128) RUN(16, 1, 8);                        \
+    else if ((d) <= 512) RUN(64, 1, 8);                   \
+    else if ((d) <= 768) RUN(64, 3, 4);                   \
+    else if ((d) <= 1024) RUN(64, 2, 8);                  \
+    else if ((d) <= 2048) RUN(256, 1, 8);                 \
+    else if ((d) <= 4096) RUN(512, 1, 8);                 \
+    else if ((d) <= 8192) RUN(512, 2, 8);                 \
+    else RUN(1024, 2, 8);                                 \
   } while (0)
 
-static int threads_of(int d) {
-  int tpr = 0;
-#define THREADS(TPR, NC) tpr = TPR
-  BY_WIDTH(d, THREADS);
-#undef THREADS
-  return tpr;
-}
+namespace {
+
 constexpr int at_least(int a, int b) { return a > b ? a : b; }
-// Threads of a block: several rows where they are short.
-constexpr int kForwardBlock = 256, kBackwardBlock = 512;
-constexpr int kForwardMost = 2048;           // blocks of a launch
+// Threads of a block: one row where that has a wave or more; several rows in the
+// backward pass, whose blocks leave a partial each.
+constexpr int kForwardBlock = 64, kBackwardBlock = 256;
+
+// Blocks of a kernel that the device holds at once.
+template <typename K>
+int resident(K kernel, int block) {
+  int device = 0, cus = 256, each = 1;
+  if (hipGetDevice(&device) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess ||
+      hipOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, block, 0) != hipSuccess)
+    (void)hipGetLastError();
+  return cus * (each > 0 ? each : 1);
+}
+// As many blocks as go through the rows in the fewest rounds of resident ones,
+// all of them as often: a block keeps its parameters and loads a row ahead.
+int blocks_of(int64_t n, int rows, int resident) {
+  const int64_t blocks = (n + rows - 1) / rows, rounds = (blocks + resident - 1) / resident;
+  return (int)((blocks + rounds - 1) / rounds);
+}
+bool general(const NormArgs& a) { return a.gate.kind == NORM_FULL || a.scale.kind == NORM_CHANNELS; }
+
+template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL>
+void forward(const NormArgs& a, hipStream_t s) {
+  constexpr int BLOCK = at_least(TPR, kForwardBlock);
+  static const int most = resident(k_residual_norm<TX, TY, TPR, NC, CH, BLOCK, GENERAL>, BLOCK);
+  const dim3 g((unsigned)blocks_of(a.n, BLOCK / TPR, most));
+  hipLaunchKernelGGL((k_residual_norm<TX, TY, TPR, NC, CH, BLOCK, GENERAL>), g, dim3(BLOCK), 0, s, a);
+}
+// blocks alone, or the launch
+template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL>
+int backward(const NormArgs& a, bool launch, hipStream_t s) {
+  constexpr int BLOCK = at_least(TPR, kBackwardBlock);
+  static const int most = resident(k_residual_norm_grad<TX, TY, TPR, NC, CH, BLOCK, GENERAL>, BLOCK);
+  const int blocks = blocks_of(a.n, BLOCK / TPR, most < kNormMostBlocks ? most : kNormMostBlocks);
+  if (launch) hipLaunchKernelGGL((k_residual_norm_grad<TX, TY, TPR, NC, CH, BLOCK, GENERAL>), dim3(blocks), dim3(BLOCK), 0, s, a);
+  return blocks;
+}
+
+#define BY_TYPES(f, TPR, NC, CH, ...)                                                    \
+  do {                                                                                   \
+    const bool g = general(a);                                                           \
+    if (x_half) f##_of<u16, u16, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);                    \
+    else if (y_half) f##_of<float, u16, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);             \
+    else f##_of<float, float, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);                       \
+  } while (0)
+
+template <typename TX, typename TY, int TPR, int NC, int CH>
+void forward_of(bool g, const NormArgs& a, hipStream_t s) {
+  if (g) forward<TX, TY, TPR, NC, CH, true>(a, s);
+  else forward<TX, TY, TPR, NC, CH, false>(a, s);
+}
+template <typename TX, typename TY, int TPR, int NC, int CH>
+void backward_of(bool g, const NormArgs& a, int* blocks, hipStream_t s) {
+  if (g) *blocks = backward<TX, TY, TPR, NC, CH, true>(a, !blocks[1], s);
+  else *blocks = backward<TX, TY, TPR, NC, CH, false>(a, !blocks[1], s);
+}
+
+}  // namespace
 
 hipError_t launch_residual_norm(const NormArgs& a, int x_half, int y_half, hipStream_t s) {
-  const int64_t rows = at_least(1, kForwardBlock / threads_of(a.d)), blocks = (a.n + rows - 1) / rows;
-  const dim3 g((unsigned)(blocks < kForwardMost ? blocks : kForwardMost));
-#define FORWARD(TPR, NC) BY_TYPES(g, k_residual_norm, TPR, NC, at_least(TPR, kForwardBlock))
+#define FORWARD(TPR, NC, CH) BY_TYPES(forward, TPR, NC, CH)
   BY_WIDTH(a.d, FORWARD);
 #undef FORWARD
   return hipGetLastError();
 }
 
-int norm_grad_blocks(int64_t n, int d) {
-  const int64_t rows = at_least(1, kBackwardBlock / threads_of(d)), blocks = (n + rows - 1) / rows;
-  const int most = d > 4096 || (d > 512 && d <= 1024) ? 256 : 512;     // what the CUs hold at once
-  return (int)(blocks < most ? blocks : most);
+int norm_grad_blocks(const NormArgs& a, int x_half, int y_half) {
+  int blocks[2] = {0, 1};      // (1: no launch)
+  hipStream_t s = nullptr;
+#define BLOCKS(TPR, NC, CH) BY_TYPES(backward, TPR, NC, CH, blocks)
+  BY_WIDTH(a.d, BLOCKS);
+#undef BLOCKS
+  return blocks[0];
 }
 
 hipError_t launch_residual_norm_grad(const NormArgs& a, int x_half, int y_half, hipStream_t s) {
-  const dim3 g((unsigned)a.blocks);
-#define BACKWARD(TPR, NC) BY_TYPES(g, k_residual_norm_grad, TPR, NC, at_least(TPR, kBackwardBlock), false)
-#define BACKWARD_GENERAL(TPR, NC) BY_TYPES(g, k_residual_norm_grad, TPR, NC, at_least(TPR, kBackwardBlock), true)
-  if (a.gate.kind == NORM_FULL || a.scale.kind == NORM_CHANNELS) BY_WIDTH(a.d, BACKWARD_GENERAL);
-  else BY_WIDTH(a.d, BACKWARD);
+  int blocks[2] = {0, 0};
+#define BACKWARD(TPR, NC, CH) BY_TYPES(backward, TPR, NC, CH, blocks)
+  BY_WIDTH(a.d, BACKWARD);
 #undef BACKWARD
-#undef BACKWARD_GENERAL
   return hipGetLastError();
 }
 
