@@ -704,9 +704,12 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
       if constexpr (MODE == LOGITS_STATS) ent += stat[192];
     }
     if (hf == 0) {
-      a.tmax[(int64_t)tile * a.piece + r] = top;
-      a.tsum[(int64_t)tile * a.piece + r] = sum;
-      if constexpr (MODE == LOGITS_STATS) a.tent[(int64_t)tile * a.piece + r] = ent;
+      if constexpr (MODE == LOGITS_STATS) {
+        a.tstat[(int64_t)tile * a.piece + r] = float4{top, sum, ent, 0.f};
+      } else {
+        a.tmax[(int64_t)tile * a.piece + r] = top;
+        a.tsum[(int64_t)tile * a.piece + r] = sum;
+      }
     }
   }
 }

@@ -24,6 +24,7 @@
 
 #include "head_device.hpp"
 #include "train.hpp"
+#include "wave.hpp"
 
 namespace muon {
 namespace {
@@ -41,17 +42,22 @@ __device__ __forceinline__ float scaled_log2(float x, float y) { return __builti
 struct Stat {
   float top, sum, ent;
 };
+// The same over another, larger or equal, reference.
+__device__ __forceinline__ Stat over(const Stat& s, float t) {
+  const float x = scaled_log2(s.top, t), f = exp2f(x);
+  return {t, s.sum * f, f * (s.ent + s.sum * x)};
+}
 __device__ __forceinline__ Stat joined(const Stat& a, const Stat& b) {
-  const float t = fmaxf(a.top, b.top), x = scaled_log2(a.top, t), y = scaled_log2(b.top, t);
-  const float ex = exp2f(x), ey = exp2f(y);
-  return Stat{t, a.sum * ex + b.sum * ey, ex * (a.ent + a.sum * x) + ey * (b.ent + b.sum * y)};
+  const float t = fmaxf(a.top, b.top);
+  const Stat x = over(a, t), y = over(b, t);
+  return {t, x.sum + y.sum, x.ent + y.ent};
 }
 __device__ __forceinline__ Stat tiles_stat(const HeadArgs& a, int r, int part, int parts) {
   Stat s = {kRefFloor, 0.f, 0.f};
 #pragma unroll 4
   for (int t = part; t < a.n_vt; t += parts) {
-    const int64_t at = (int64_t)t * a.piece + r;
-    s = joined(s, Stat{a.tmax[at], a.tsum[at], a.tent[at]});
+    const float4 x = a.tstat[(int64_t)t * a.piece + r];
+    s = joined(s, Stat{x.x, x.y, x.z});
   }
   return s;
 }
@@ -80,6 +86,14 @@ __device__ __forceinline__ void put_stat(const HeadArgs& a, int r, const float4&
   a.loss[i] = s.w;
   if (a.entropy) a.entropy[i] = s.z;
   if (a.stats) a.stats[i] = s;
+}
+
+// Hand-off through LDS between the lanes of one wave: the LDS executes a wave's
+// accesses in order, so only the compiler has to keep them so.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Sorting over a wave, lane 0 first: larger values, then smaller tokens.
@@ -118,122 +132,220 @@ __device__ __forceinline__ void merge_wave(Ranked<F>& x, const Ranked<F>& sorted
   for (int mask = 32; mask; mask /= 2) keep_order(x, lane, mask, true);
 }
 
-// The logit of a token and a word in 64 bits, the wave's lanes over the width.
+// Logits of a token and G words in 64 bits, the wave's lanes over the width.
+constexpr int kGroup = 4;
 template <typename T>
-__device__ __forceinline__ double fine_logit(const T* h, const T* w, int d, int lane) {
+__device__ __forceinline__ void fine_logits(const T* h, const T* w, int64_t ld, int d, const int (&words)[kGroup], int lane,
+                                            double (&z)[kGroup]) {
   constexpr int CH = 16 / (int)sizeof(T);
-  double s = 0;
+  auto value = [](T x) -> double {
+    if constexpr (sizeof(T) == 2) return (double)bf2f(x);
+    else return (double)x;
+  };
+#pragma unroll
+  for (int g = 0; g < kGroup; ++g) z[g] = 0;
   for (int c = lane * CH; c < d; c += 64 * CH) {
+    T x[CH], y[kGroup][CH];
     if (c + CH <= d) {
-      T x[CH], y[CH];
       __builtin_memcpy(x, h + c, 16);
-      __builtin_memcpy(y, w + c, 16);
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) __builtin_memcpy(y[g], w + words[g] * ld + c, 16);
+    } else {
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
-        if constexpr (sizeof(T) == 2) s = fma((double)bf2f(x[e]), (double)bf2f(y[e]), s);
-        else s = fma((double)x[e], (double)y[e], s);
+        x[e] = c + e < d ? h[c + e] : T(0);
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) y[g][e] = c + e < d ? w[words[g] * ld + c + e] : T(0);
       }
-    } else {
-      for (int e = c; e < d; ++e) {
-        if constexpr (sizeof(T) == 2) s = fma((double)bf2f(h[e]), (double)bf2f(w[e]), s);
-        else s = fma((double)h[e], (double)w[e], s);
-      }
+    }
+#pragma unroll
+    for (int e = 0; e < CH; ++e) {
+      const double v = value(x[e]);
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) z[g] = fma(v, value(y[g][e]), z[g]);
     }
   }
 #pragma unroll
-  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
-  return s;
+  for (int g = 0; g < kGroup; ++g) z[g] = lanes_sum<64>(z[g]);
 }
 
 constexpr int kNoToken = 0x7FFFFFFF;
+constexpr float kNone = -__builtin_inff();
 // A set's second largest logit, or a little more (its last bits are a place).
 __device__ __forceinline__ float second_of(uint2 b) {
   const uint32_t up = b.y >> 31 ? b.y & ~63u : b.y | 63u;
   return __uint_as_float(up > 0x7F800000u && up < 0x80000000u ? 0x7F800000u : up);
 }
+// Whole numbers in the order of their floats (which are no NaN).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+// The largest number that at least `count` of the lanes' keys reach, 0 if there are not as many keys.
+template <int K>
+__device__ __forceinline__ uint32_t reached_by(const uint32_t (&key)[K], int count) {
+  uint32_t least = 0;
+#pragma unroll 4
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t trial = least | 1u << bit;
+    int found = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) found += __popcll(__ballot(key[k] >= trial));
+    if (found >= count) least = trial;
+  }
+  return least;
+}
 
-// One token's alternatives, by one wave.
-template <typename T>
-__device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const float4& stat, int lane) {
+// A wave's candidates.
+struct Candidates {
+  double z[64];
+  int word[64];
+  float bound[64];
+};
+
+// The sets that the alternatives are in, in no order (word, bound of the set's
+// others), at most 63; returns how many.
+__device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int lane, Candidates& sh) {
+  const int count = a.top + kSpare, sets = a.sets;
+  auto best_of = [&](int tile, int set) { return a.best[((int64_t)tile * a.piece + r) * sets + set]; };
+  // each lane's largest logit of two halves of its sets: what `count` of these
+  // reach is reached by as many sets, and by few more
+  float most[2] = {kNone, kNone};
+#pragma unroll 4
+  for (int t = lane; t < a.n_vt; t += 64)
+    for (int k = 0; k < sets; ++k) most[k & 1] = fmaxf(most[k & 1], __uint_as_float(best_of(t, k).x));
+  const uint32_t keys[2] = {most[0] > kNone ? ordered(most[0]) : 0u, most[1] > kNone ? ordered(most[1]) : 0u};
+  const uint32_t least = reached_by(keys, count);
+  int found = 0;
+  for (int t0 = 0; t0 < a.n_vt; t0 += 64)
+    for (int k = 0; k < sets; ++k) {
+      const int t = t0 + lane;
+      uint2 b = {0xFF800000u, 0u};
+      if (t < a.n_vt) b = best_of(t, k);
+      const float z = __uint_as_float(b.x);
+      const bool in = z > kNone && ordered(z) >= least;
+      const uint64_t mask = __ballot(in);
+      const int at = found + __popcll(mask & ((1ull << lane) - 1));
+      if (in && at < 63) {
+        sh.word[at] = t * a.vtile + set_column(k, sets, b.y & 63);
+        sh.z[at] = z;
+        sh.bound[at] = second_of(b);
+      }
+      found += __popcll(mask);
+    }
+  if (found <= 63) return found;
+  // more of them (equal logits, or neighbours in one lane's sets): the first
+  // `count` by (logit, word), by sorting them 64 at a time
+  Ranked<float> best = {kNone, kNoToken};
+  const int all = a.n_vt * sets;
+  for (int s0 = 0; s0 < all; s0 += 64) {
+    const int s = s0 + lane;
+    Ranked<float> x = {kNone, kNoToken};
+    if (s < all) {
+      const uint2 b = best_of(s / sets, s % sets);
+      if (__uint_as_float(b.x) > kNone) x = {__uint_as_float(b.x), s / sets * a.vtile + set_column(s % sets, sets, b.y & 63)};
+    }
+    // (most have nothing for a list that is full)
+    if (s0 && !__any(before(x, Ranked<float>{__shfl(best.z, 63), __shfl(best.token, 63)}))) continue;
+    sort_wave(x, lane);
+    if (s0 == 0) best = x;
+    else merge_wave(best, x, lane);
+  }
+  if (lane < count) {
+    const int col = best.token % a.vtile;
+    sh.word[lane] = best.token;
+    sh.z[lane] = best.z;
+    sh.bound[lane] = second_of(best_of(best.token / a.vtile, column_set(col, sets)));
+  }
+  return count;
+}
+
+// One token's alternatives, by WAVES waves: each finds the candidates, with LDS
+// of its own (`own`); their 64-bit sums are shared out (and meet in sh).
+template <typename T, int WAVES>
+__device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const float4& stat, int wave, int lane,
+                                             Candidates& own, Candidates& sh) {
   const int i = a.idx[a.row0 + r], target = a.tgt[a.row0 + r], top = a.top;
   float* logps = a.top_logprobs + (int64_t)i * top;
   int64_t* tokens = a.top_tokens + (int64_t)i * top;
   if (stat.y != stat.y) {
-    if (lane < top) {
+    if (wave == 0 && lane < top) {
       logps[lane] = kNan;
       tokens[lane] = -1;
     }
     return;
   }
-  const int per = a.vtile / a.sets, all = a.n_vt * a.sets;
-  const float none = -__builtin_inff();
-  auto entry = [&](int s, Ranked<float>& x, float& bound) {
-    // (sets past the last, and of no logit, rank behind every other)
-    x = {none, kNoToken};
-    bound = none;
-    if (s >= all) return;
-    const int tile = s / a.sets, set = s % a.sets;
-    const uint2 b = a.best[((int64_t)tile * a.piece + r) * a.sets + set];
-    const float z = __uint_as_float(b.x);
-    if (!(z > none)) return;
-    x = {z, tile * a.vtile + set_column(set, a.sets, b.y & 63)};
-    bound = second_of(b);
-  };
-  // the 64 best sets
-  Ranked<float> best = {none, kNoToken};
-  float bounds_of = none;
-  for (int s0 = 0; s0 < all; s0 += 64) {
-    Ranked<float> x;
-    float bound;
-    entry(s0 + lane, x, bound);
-    sort_wave(x, lane);
-    if (s0 == 0) best = x;
-    else merge_wave(best, x, lane);
+  int count = candidate_sets(a, r, lane, own);
+  wave_sync();
+  const bool mine = lane < count;
+  const float z32 = mine ? (float)own.z[lane] : kNone, bound = mine ? own.bound[lane] : kNone;
+  // sets that may have two of the alternatives
+  const uint32_t key[1] = {mine ? ordered(z32) : 0u};
+  const uint32_t kth = reached_by(key, top);
+  const float least = kth ? __uint_as_float(kth >> 31 ? kth & 0x7FFFFFFFu : ~kth) : kNone;
+  const uint64_t whole = __ballot(bound > kNone && bound >= least - fabsf(least) * 0x1p-18f);
+  int word = mine ? own.word[lane] : kNoToken;
+  if (target >= 0 && a.zt[r] > kNone) {          // (its set leaves it out)
+    if (lane == count) word = target;
+    ++count;
   }
-  // the second largest of each, and which sets have two among the best
-  const float kth = __shfl(best.z, top - 1);
-  if (best.token != kNoToken) {
-    const int tile = best.token / a.vtile, col = best.token % a.vtile;
-    const int set = (a.sets == 4 ? (col >> 5) * 2 : 0) + ((col >> 2) & 1);
-    const uint2 b = a.best[((int64_t)tile * a.piece + r) * a.sets + set];
-    bounds_of = second_of(b);
-  }
-  const int count = top + kSpare;
-  const uint64_t whole = __ballot(lane < count && bounds_of > none && bounds_of >= kth - fabsf(kth) * 0x1p-18f);
-  if (lane >= count) best.token = kNoToken;
-  if (lane == 63 && target >= 0 && a.zt[r] > none) best.token = target;       // (its set leaves it out)
   const T* h = (const T*)a.h + (int64_t)i * a.ld_h;
   const T* w = (const T*)(a.w_src ? a.w_src : a.w);
   const int64_t ld = a.w_src ? a.ld_src : a.ld_w;
-  auto fine = [&](int token) {
-    Ranked<double> x = {-__builtin_inf(), kNoToken};
-    for (uint64_t todo = __ballot(token != kNoToken); todo; todo &= todo - 1) {
-      const int from = __builtin_ctzll(todo), word = __shfl(token, from);
-      const double z = fine_logit(h, w + (int64_t)word * ld, a.d, lane);
-      if (lane == from) x = {z, word};
+  // 64-bit logits of the lanes' words, from lane `from` in steps of whole groups
+  auto fine = [&](int words, int n, int from, int step) {
+    for (int g0 = from; g0 < n; g0 += step) {
+      int of[kGroup];
+      double z[kGroup];
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) of[g] = __builtin_amdgcn_readlane(words, min(g0 + g, n - 1));
+      fine_logits(h, w, ld, a.d, of, lane, z);
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g)
+        if (lane == g && g0 + g < n) sh.z[g0 + g] = z[g];
     }
-    sort_wave(x, lane);
-    return x;
   };
-  const int firsts = best.token;
-  Ranked<double> found = fine(firsts);
+  if (WAVES > 1) __syncthreads();                // (every wave has read its candidates)
+  else wave_sync();
+  fine(word, count, wave * kGroup, WAVES * kGroup);
+  if (WAVES > 1) __syncthreads();
+  else wave_sync();
+  if (wave != 0) return;
+  Ranked<double> found = {lane < count ? sh.z[lane] : -__builtin_inf(), lane < count ? word : kNoToken};
+  // ranks by counting who is in front
+  int rank = 0;
+  for (int k = 0; k < count; ++k)
+    rank += before(Ranked<double>{sh.z[k], __builtin_amdgcn_readlane(word, k)}, found) ? 1 : 0;
+  wave_sync();
+  if (lane < count) {
+    sh.z[rank] = found.z;
+    sh.word[rank] = found.token;
+  }
+  wave_sync();
+  found = {lane < count ? sh.z[lane] : -__builtin_inf(), lane < count ? sh.word[lane] : kNoToken};
+  const int per = a.vtile / a.sets;
   for (uint64_t todo = whole; todo; todo &= todo - 1) {
-    const int word = __shfl(firsts, __builtin_ctzll(todo));
-    const int tile = word / a.vtile, col = word % a.vtile;
-    const int set = (a.sets == 4 ? (col >> 5) * 2 : 0) + ((col >> 2) & 1);
-    int token = kNoToken;
-    if (lane < per) token = tile * a.vtile + set_column(set, a.sets, lane);
-    if (token >= a.v || token == word || token == target) token = kNoToken;
-    merge_wave(found, fine(token), lane);
+    const int first = __builtin_amdgcn_readlane(word, __builtin_ctzll(todo));
+    const int tile = first / a.vtile, set = column_set(first % a.vtile, a.sets);
+    int member = tile * a.vtile + set_column(set, a.sets, lane);
+    const bool in = lane < per && member < a.v && member != first && member != target;
+    // the members side by side in the first lanes
+    const uint64_t mask = __ballot(in);
+    const int n = __popcll(mask);
+    wave_sync();
+    if (in) sh.word[__popcll(mask & ((1ull << lane) - 1))] = member;
+    wave_sync();
+    member = lane < n ? sh.word[lane] : kNoToken;
+    fine(member, n, 0, kGroup);
+    wave_sync();
+    Ranked<double> x = {lane < n ? sh.z[lane] : -__builtin_inf(), member};
+    sort_wave(x, lane);
+    merge_wave(found, x, lane);
   }
   if (lane >= top) return;
   const bool there = found.token != kNoToken && found.z > -__builtin_inf();
-  double logp = (found.z - stat.x) - stat.y;
-  if (a.softcap > 0.f) {
-    const double c = a.softcap, x = tanh(found.z / c) * c;
-    logp = (x - stat.x) - stat.y;
-  }
-  logps[lane] = !there ? none : found.token == target ? stat.w : (float)logp;
+  const double c = a.softcap, z = c > 0 ? tanh(found.z / c) * c : found.z;
+  logps[lane] = !there ? kNone : found.token == target ? stat.w : (float)((z - stat.x) - stat.y);
   tokens[lane] = there ? found.token : -1;
 }
 
@@ -250,7 +362,8 @@ __device__ __forceinline__ void clear_ignored(const HeadArgs& a, int64_t from) {
   }
 }
 
-// 64 tokens a block, a token's tiles over 16 threads.
+// Many tokens without alternatives: 64 tokens a block, a token's tiles over 16
+// threads.
 constexpr int kParts = 16;
 __global__ __launch_bounds__(1024) void k_logprob_stats(HeadArgs a, int blocks) {
   __shared__ Stat sh[kParts][64];
@@ -268,13 +381,26 @@ __global__ __launch_bounds__(1024) void k_logprob_stats(HeadArgs a, int blocks) 
   put_stat(a, r, token_stat(a, r, s));
 }
 
-// A wave a token; neighbouring tokens, whose statistics share lines, on one XCD.
-template <typename T>
-__global__ __launch_bounds__(256) void k_alternatives(HeadArgs a) {
-  const int rows = piece_rows(a), per = (gridDim.x + 7) / 8;
-  const int block = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  const int r = block * 4 + (threadIdx.x >> 6);
-  if (r < rows) alternatives<T>(a, r, a.rs[r], threadIdx.x & 63);
+// A wave a token, or (few tokens) the block's four for one; neighbouring tokens,
+// whose statistics share lines, on one XCD.
+template <typename T, int WAVES>
+__global__ __launch_bounds__(256) void k_logprobs(HeadArgs a, int blocks) {
+  __shared__ Candidates sh[4];
+  if ((int)blockIdx.x >= blocks) {
+    clear_ignored(a, ((int64_t)blockIdx.x - blocks) * 1024);
+    return;
+  }
+  const int rows = piece_rows(a), lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int block = (blockIdx.x & 7) * (blocks / 8) + (blockIdx.x >> 3), r = WAVES == 1 ? block * 4 + wave : block;
+  if (r >= rows) return;
+  Stat s = tiles_stat(a, r, lane, 64);
+  s = over(s, over_lanes<64>(s.top, [](float x, float y) { return fmaxf(x, y); }));
+  s.sum = lanes_sum<64>(s.sum);
+  s.ent = lanes_sum<64>(s.ent);
+  const float4 stat = token_stat(a, r, s);
+  const int part = WAVES == 1 ? 0 : wave;
+  if (part == 0 && lane == 0) put_stat(a, r, stat);
+  if (a.top) alternatives<T, WAVES>(a, r, stat, part, lane, sh[wave], sh[WAVES == 1 ? wave : 0]);
 }
 
 __global__ __launch_bounds__(256) void k_logprob_factors(HeadArgs a) {
@@ -289,17 +415,29 @@ __global__ __launch_bounds__(256) void k_logprob_factors(HeadArgs a) {
   a.rs[r] = float4{0.f, 0.f, tg >= 0 ? -gp * expm1f(lp) - ge * expf(lp) * (lp + s.z) : 0.f, 0.f};
 }
 
+// Tokens that a block each still has room for at once.
+constexpr int kFewTokens = 512;
 inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
 
 }  // namespace
 
 hipError_t launch_logprobs(const HeadArgs& a, int dt, hipStream_t s) {
-  const int blocks = (int)cdiv(a.rows_max, 64), clear = a.row0 == 0 ? (int)cdiv(a.n, 1024) : 0;
-  hipLaunchKernelGGL(k_logprob_stats, dim3(blocks + clear), dim3(1024), 0, s, a, blocks);
-  if (a.top == 0) return hipGetLastError();
-  const dim3 g(cdiv(cdiv(a.rows_max, 4), 8) * 8);
-  if (dt == MUON_BF16) hipLaunchKernelGGL(k_alternatives<u16>, g, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_alternatives<float>, g, dim3(256), 0, s, a);
+  const int clear = a.row0 == 0 ? (int)cdiv(a.n, 1024) : 0;
+  if (a.top == 0 && a.rows_max > kFewTokens) {
+    const int blocks = (int)cdiv(a.rows_max, 64);
+    hipLaunchKernelGGL(k_logprob_stats, dim3(blocks + clear), dim3(1024), 0, s, a, blocks);
+    return hipGetLastError();
+  }
+  const bool few = a.rows_max <= kFewTokens;
+  const int blocks = (int)cdiv(few ? a.rows_max : cdiv(a.rows_max, 4), 8) * 8;
+  const dim3 g(blocks + clear), b(256);
+  if (dt == MUON_BF16) {
+    if (few) hipLaunchKernelGGL((k_logprobs<u16, 4>), g, b, 0, s, a, blocks);
+    else hipLaunchKernelGGL((k_logprobs<u16, 1>), g, b, 0, s, a, blocks);
+  } else {
+    if (few) hipLaunchKernelGGL((k_logprobs<float, 4>), g, b, 0, s, a, blocks);
+    else hipLaunchKernelGGL((k_logprobs<float, 1>), g, b, 0, s, a, blocks);
+  }
   return hipGetLastError();
 }
 

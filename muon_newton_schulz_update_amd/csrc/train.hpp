@@ -164,7 +164,8 @@ struct HeadArgs {
   // log probabilities (head_logprobs.hip); loss holds them
   int32_t top;                        // alternatives a token
   int32_t sets;                       // lanes that share a statistic's vocabulary columns
-  float* tent;                        // n_vt x piece: sum of exponential times its logarithm (base 2)
+  float4* tstat;                      // n_vt x piece: largest logit, sum of exponentials over it, sum of exponential
+                                      // times its logarithm (base 2), all without the target's
   uint2* best;                        // n_vt x piece x sets: each lane's largest logit, its place and the second largest
   float* entropy;                     // caller's, n each, or null
   float4* stats;
@@ -185,6 +186,8 @@ enum LogitsMode { LOGITS_LOSS, LOGITS_STATS, LOGITS_GRAD };
 __host__ __device__ inline int set_column(int set, int sets, int q) {
   return (sets == 4 ? (set >> 1) * 32 : 0) + (q >> 4) * 32 + 8 * ((q >> 2) & 3) + 4 * (set & 1) + (q & 3);
 }
+// The set of a column.
+__host__ __device__ inline int column_set(int col, int sets) { return (sets == 4 ? (col >> 5) * 2 : 0) + ((col >> 2) & 1); }
 
 // Picks the tile edges, the statistics' columns and the splits, from the sizes
 // and from which gradients are wanted (before the workspace is laid out).

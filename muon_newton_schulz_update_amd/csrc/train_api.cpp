@@ -188,8 +188,8 @@ muon_status head_run(muon_handle* h, const HeadCall& c) {
   a.w_cols = direct ? a.d : a.dp;
   // pieces
   // (a row's statistics: at most 8 bytes for 64 words of the vocabulary, with entropy
-  // and candidates 12 and 8 for each lane that shares them)
-  const size_t each = c.mode == LOGITS_STATS ? 12 + (c.top ? (a.half ? 16 : 32) : 0) : 8;
+  // 16, and 8 more for each lane that shares them with the candidates)
+  const size_t each = c.mode == LOGITS_STATS ? 16 + (c.top ? (a.half ? 16 : 32) : 0) : 8;
   const size_t row = (size_t)a.dp * e + (size_t)cdiv(a.v, 64) * each + 24 + (grad ? (size_t)a.vp * e : 0);
   const int64_t most =
       std::min(kPieceMost, std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows));
@@ -210,10 +210,10 @@ muon_status head_run(muon_handle* h, const HeadCall& c) {
   };
   const size_t n = (size_t)a.n, p = (size_t)a.piece;
   const size_t o_count = take(16), o_idx = take(n * 4), o_tgt = take(n * 4), o_lossc = take(n * 4);
-  const size_t o_hp = take(p * a.dp * e), o_tmax = take(p * a.n_vt * 4), o_tsum = take(p * a.n_vt * 4);
+  const bool stats = c.mode == LOGITS_STATS, loss = c.mode == LOGITS_LOSS;
+  const size_t o_hp = take(p * a.dp * e), o_tmax = take(loss ? p * a.n_vt * 4 : 0), o_tsum = take(loss ? p * a.n_vt * 4 : 0);
   const size_t o_zt = take(p * 4), o_zf = take(c.softcap > 0.f ? p * 4 : 0), o_rs = take(p * 16);
-  const bool stats = c.mode == LOGITS_STATS;
-  const size_t o_tent = take(stats ? p * a.n_vt * 4 : 0), o_best = take(stats && c.top ? p * a.n_vt * a.sets * 8 : 0);
+  const size_t o_tstat = take(stats ? p * a.n_vt * 16 : 0), o_best = take(stats && c.top ? p * a.n_vt * a.sets * 8 : 0);
   const size_t o_ts = take(c.mode == LOGITS_GRAD ? p * 16 : 0);
   const size_t o_w = direct ? 0 : take((size_t)a.v * a.dp * e);
   const size_t o_e = grad ? take(p * a.vp * e) : 0, o_part = a.split > 1 ? take(p * a.dp * 4 * a.split) : 0;
@@ -232,7 +232,7 @@ muon_status head_run(muon_handle* h, const HeadCall& c) {
   a.zt = (float*)(b + o_zt);
   a.zf = (float*)(b + o_zf);
   a.rs = (float4*)(b + o_rs);
-  a.tent = (float*)(b + o_tent);
+  a.tstat = (float4*)(b + o_tstat);
   a.best = (uint2*)(b + o_best);
   a.ts = (float4*)(b + o_ts);
   if (c.mode == LOGITS_GRAD) a.loss = a.lossc;    // (zeros of the ignored tokens go there)
