@@ -8,7 +8,6 @@
 
 namespace muon {
 
-typedef unsigned short u16;
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.44269504088896341f;
 

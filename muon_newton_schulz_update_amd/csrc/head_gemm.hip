@@ -383,25 +383,32 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
   return true;
 }
 
-// A lane's MI x 16 raw logits of one token (z[mi * step]): the largest, its first
-// place (6 bits) and the second largest, whose last 6 bits the place takes. Only
-// that a lane holds another candidate, and no larger a one, is read from the second.
-template <int MI>
+// The sets of a lane's MI x 16 raw logits of one token (z[mi * step]), from `set`
+// in steps of 2: the largest, its first place (6 bits) and the second largest,
+// whose last 6 bits the place takes: only that a set holds another candidate, and
+// no larger a one, is read from the second. Returns the largest of all.
+template <typename T, int MI>
 __device__ __forceinline__ float store_best(const HeadArgs& a, const f32x16_t* z, int step, int tile, int set, int r) {
-  float first = -__builtin_inff(), second = first;
+  constexpr int EACH = kSetRows<T> / 32 < MI ? kSetRows<T> / 32 : MI;
+  float top = -__builtin_inff();
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
+  for (int m0 = 0; m0 < MI; m0 += EACH) {
+    float first = -__builtin_inff(), second = first;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      second = __builtin_amdgcn_fmed3f(first, second, z[mi * step][q]);
-      first = fmaxf(first, z[mi * step][q]);
-    }
-  uint32_t place = 0;
+    for (int mi = m0; mi < m0 + EACH; ++mi)
 #pragma unroll
-  for (int i = MI * 16 - 1; i >= 0; --i) place = z[i / 16 * step][i % 16] == first ? i : place;
-  a.best[((int64_t)tile * a.piece + r) * a.sets + set] =
-      make_uint2(__float_as_uint(first), (__float_as_uint(second) & ~63u) | place);
-  return first;
+      for (int q = 0; q < 16; ++q) {
+        second = __builtin_amdgcn_fmed3f(first, second, z[mi * step][q]);
+        first = fmaxf(first, z[mi * step][q]);
+      }
+    uint32_t place = 0;
+#pragma unroll
+    for (int i = EACH * 16 - 1; i >= 0; --i) place = z[(m0 + i / 16) * step][i % 16] == first ? i : place;
+    a.best[((int64_t)tile * a.piece + r) * a.sets + set + m0 / EACH * 2] =
+        make_uint2(__float_as_uint(first), (__float_as_uint(second) & ~63u) | place);
+    top = fmaxf(top, first);
+  }
+  return top;
 }
 
 // The logits' gradient dz = -p (b + g log p) and the target's (train.hpp: ts), to
@@ -601,7 +608,7 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
     float top = kRefFloor;
     if constexpr (MODE == LOGITS_STATS) {
       if (a.top) {
-        top = fmaxf(top, store_best<MI>(a, &acc[0][ni], NI, tile, PAIR ? 2 * wm + hf : hf, r));
+        top = fmaxf(top, store_best<T, MI>(a, &acc[0][ni], NI, tile, PAIR ? 2 * wm + hf : hf, r));
       } else {
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi)
@@ -1216,7 +1223,7 @@ void head_plan(HeadArgs& a, int dt) {
   a.logit_tile = tile_of(dt, rows, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256), (int64_t)cdiv(a.v, 128) * cdiv(rows, 128));
   a.vtile = a.logit_tile == 64 ? 64 : 128;
   a.n_vt = cdiv(a.v, a.vtile);
-  a.sets = dt == MUON_BF16 ? 2 : 4;
+  a.sets = a.vtile / (dt == MUON_BF16 ? kSetRows<u16> : kSetRows<float>) * 2;
   a.split = a.wsplit = 1;
   if (!a.dh && !a.dw) return;
   const int64_t stages = cdiv(a.v, unit), wstages = cdiv(rows, unit);

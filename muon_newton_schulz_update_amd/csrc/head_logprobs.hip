@@ -44,7 +44,7 @@ struct Stat {
 };
 // The same over another, larger or equal, reference.
 __device__ __forceinline__ Stat over(const Stat& s, float t) {
-  const float x = scaled_log2(s.top, t), f = exp2f(x);
+  const float x = scaled_log2(s.top, t), f = __builtin_amdgcn_exp2f(x);
   return {t, s.sum * f, f * (s.ent + s.sum * x)};
 }
 __device__ __forceinline__ Stat joined(const Stat& a, const Stat& b) {
@@ -52,12 +52,26 @@ __device__ __forceinline__ Stat joined(const Stat& a, const Stat& b) {
   const Stat x = over(a, t), y = over(b, t);
   return {t, x.sum + y.sum, x.ent + y.ent};
 }
+// Every parts-th tile's, eight at a time over their common reference.
 __device__ __forceinline__ Stat tiles_stat(const HeadArgs& a, int r, int part, int parts) {
   Stat s = {kRefFloor, 0.f, 0.f};
-#pragma unroll 4
-  for (int t = part; t < a.n_vt; t += parts) {
-    const float4 x = a.tstat[(int64_t)t * a.piece + r];
-    s = joined(s, Stat{x.x, x.y, x.z});
+  for (int t0 = part; t0 < a.n_vt; t0 += 8 * parts) {
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[k] = float4{kRefFloor, 0.f, 0.f, 0.f};
+      if (t0 + k * parts < a.n_vt) x[k] = a.tstat[(int64_t)(t0 + k * parts) * a.piece + r];
+    }
+    float top = s.top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
+    s = over(s, top);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const Stat y = over(Stat{x[k].x, x[k].y, x[k].z}, top);
+      s.sum += y.sum;
+      s.ent += y.ent;
+    }
   }
   return s;
 }
@@ -133,7 +147,7 @@ __device__ __forceinline__ void merge_wave(Ranked<F>& x, const Ranked<F>& sorted
 }
 
 // Logits of a token and G words in 64 bits, the wave's lanes over the width.
-constexpr int kGroup = 4;
+constexpr int kGroup = 8;
 template <typename T>
 __device__ __forceinline__ void fine_logits(const T* h, const T* w, int64_t ld, int d, const int (&words)[kGroup], int lane,
                                             double (&z)[kGroup]) {
@@ -205,45 +219,66 @@ struct Candidates {
 
 // The sets that the alternatives are in, in no order (word, bound of the set's
 // others), at most 63; returns how many.
+template <typename T, int SETS>
 __device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int lane, Candidates& sh) {
-  const int count = a.top + kSpare, sets = a.sets;
-  auto best_of = [&](int tile, int set) { return a.best[((int64_t)tile * a.piece + r) * sets + set]; };
+  const int count = a.top + kSpare;
+  auto best_of = [&](int tile, int set) { return a.best[((int64_t)tile * a.piece + r) * SETS + set]; };
+  // 512 statistics at a time, which stay in registers where these are all (65536
+  // words; fp32 and few tokens 32768)
+  constexpr int TILES = 8, SPAN = 64 * TILES;
+  uint2 e[TILES][SETS];
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+#pragma unroll
+      for (int k = 0; k < SETS; ++k) e[j][k] = make_uint2(0xFF800000u, 0u);
+      const int t = t0 + j * 64 + lane;
+      if (t < a.n_vt) __builtin_memcpy(e[j], a.best + ((int64_t)t * a.piece + r) * SETS, sizeof(e[j]));
+    }
+  };
   // each lane's largest logit of two halves of its sets: what `count` of these
   // reach is reached by as many sets, and by few more
   float most[2] = {kNone, kNone};
-#pragma unroll 4
-  for (int t = lane; t < a.n_vt; t += 64)
-    for (int k = 0; k < sets; ++k) most[k & 1] = fmaxf(most[k & 1], __uint_as_float(best_of(t, k).x));
+  for (int t0 = 0; t0 < a.n_vt; t0 += SPAN) {
+    load(t0);
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int k = 0; k < SETS; ++k) most[k & 1] = fmaxf(most[k & 1], __uint_as_float(e[j][k].x));
+  }
   const uint32_t keys[2] = {most[0] > kNone ? ordered(most[0]) : 0u, most[1] > kNone ? ordered(most[1]) : 0u};
   const uint32_t least = reached_by(keys, count);
   int found = 0;
-  for (int t0 = 0; t0 < a.n_vt; t0 += 64)
-    for (int k = 0; k < sets; ++k) {
-      const int t = t0 + lane;
-      uint2 b = {0xFF800000u, 0u};
-      if (t < a.n_vt) b = best_of(t, k);
-      const float z = __uint_as_float(b.x);
-      const bool in = z > kNone && ordered(z) >= least;
-      const uint64_t mask = __ballot(in);
-      const int at = found + __popcll(mask & ((1ull << lane) - 1));
-      if (in && at < 63) {
-        sh.word[at] = t * a.vtile + set_column(k, sets, b.y & 63);
-        sh.z[at] = z;
-        sh.bound[at] = second_of(b);
+  for (int t0 = 0; t0 < a.n_vt; t0 += SPAN) {
+    if (a.n_vt > SPAN) load(t0);
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int k = 0; k < SETS; ++k) {
+        const float z = __uint_as_float(e[j][k].x);
+        const bool in = z > kNone && ordered(z) >= least;
+        const uint64_t mask = __ballot(in);
+        if (mask == 0) continue;
+        const int at = found + __popcll(mask & ((1ull << lane) - 1));
+        if (in && at < 63) {
+          sh.word[at] = (t0 + j * 64 + lane) * a.vtile + set_column<T>(k, e[j][k].y & 63);
+          sh.z[at] = z;
+          sh.bound[at] = second_of(e[j][k]);
+        }
+        found += __popcll(mask);
       }
-      found += __popcll(mask);
-    }
+  }
   if (found <= 63) return found;
   // more of them (equal logits, or neighbours in one lane's sets): the first
   // `count` by (logit, word), by sorting them 64 at a time
   Ranked<float> best = {kNone, kNoToken};
-  const int all = a.n_vt * sets;
+  const int all = a.n_vt * SETS;
   for (int s0 = 0; s0 < all; s0 += 64) {
     const int s = s0 + lane;
     Ranked<float> x = {kNone, kNoToken};
     if (s < all) {
-      const uint2 b = best_of(s / sets, s % sets);
-      if (__uint_as_float(b.x) > kNone) x = {__uint_as_float(b.x), s / sets * a.vtile + set_column(s % sets, sets, b.y & 63)};
+      const uint2 b = best_of(s / SETS, s % SETS);
+      if (__uint_as_float(b.x) > kNone) x = {__uint_as_float(b.x), s / SETS * a.vtile + set_column<T>(s % SETS, b.y & 63)};
     }
     // (most have nothing for a list that is full)
     if (s0 && !__any(before(x, Ranked<float>{__shfl(best.z, 63), __shfl(best.token, 63)}))) continue;
@@ -255,14 +290,14 @@ __device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int lane
     const int col = best.token % a.vtile;
     sh.word[lane] = best.token;
     sh.z[lane] = best.z;
-    sh.bound[lane] = second_of(best_of(best.token / a.vtile, column_set(col, sets)));
+    sh.bound[lane] = second_of(best_of(best.token / a.vtile, column_set<T>(col)));
   }
   return count;
 }
 
 // One token's alternatives, by WAVES waves: each finds the candidates, with LDS
 // of its own (`own`); their 64-bit sums are shared out (and meet in sh).
-template <typename T, int WAVES>
+template <typename T, int SETS, int WAVES>
 __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const float4& stat, int wave, int lane,
                                              Candidates& own, Candidates& sh) {
   const int i = a.idx[a.row0 + r], target = a.tgt[a.row0 + r], top = a.top;
@@ -275,15 +310,10 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const flo
     }
     return;
   }
-  int count = candidate_sets(a, r, lane, own);
+  int count = candidate_sets<T, SETS>(a, r, lane, own);
   wave_sync();
   const bool mine = lane < count;
-  const float z32 = mine ? (float)own.z[lane] : kNone, bound = mine ? own.bound[lane] : kNone;
-  // sets that may have two of the alternatives
-  const uint32_t key[1] = {mine ? ordered(z32) : 0u};
-  const uint32_t kth = reached_by(key, top);
-  const float least = kth ? __uint_as_float(kth >> 31 ? kth & 0x7FFFFFFFu : ~kth) : kNone;
-  const uint64_t whole = __ballot(bound > kNone && bound >= least - fabsf(least) * 0x1p-18f);
+  const float bound = mine ? own.bound[lane] : kNone;
   int word = mine ? own.word[lane] : kNoToken;
   if (target >= 0 && a.zt[r] > kNone) {          // (its set leaves it out)
     if (lane == count) word = target;
@@ -323,12 +353,14 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const flo
   }
   wave_sync();
   found = {lane < count ? sh.z[lane] : -__builtin_inf(), lane < count ? sh.word[lane] : kNoToken};
-  const int per = a.vtile / a.sets;
+  // sets that may have two of the alternatives: all of them
+  const float least = (float)__shfl(found.z, top - 1);
+  const uint64_t whole = __ballot(bound > kNone && bound >= least - fabsf(least) * 0x1p-18f);
   for (uint64_t todo = whole; todo; todo &= todo - 1) {
     const int first = __builtin_amdgcn_readlane(word, __builtin_ctzll(todo));
-    const int tile = first / a.vtile, set = column_set(first % a.vtile, a.sets);
-    int member = tile * a.vtile + set_column(set, a.sets, lane);
-    const bool in = lane < per && member < a.v && member != first && member != target;
+    const int tile = first / a.vtile, set = column_set<T>(first % a.vtile);
+    int member = tile * a.vtile + set_column<T>(set, lane);
+    const bool in = lane < kSetRows<T> / 2 && member < a.v && member != first && member != target;
     // the members side by side in the first lanes
     const uint64_t mask = __ballot(in);
     const int n = __popcll(mask);
@@ -383,7 +415,7 @@ __global__ __launch_bounds__(1024) void k_logprob_stats(HeadArgs a, int blocks) 
 
 // A wave a token, or (few tokens) the block's four for one; neighbouring tokens,
 // whose statistics share lines, on one XCD.
-template <typename T, int WAVES>
+template <typename T, int SETS, int WAVES>
 __global__ __launch_bounds__(256) void k_logprobs(HeadArgs a, int blocks) {
   __shared__ Candidates sh[4];
   if ((int)blockIdx.x >= blocks) {
@@ -400,7 +432,7 @@ __global__ __launch_bounds__(256) void k_logprobs(HeadArgs a, int blocks) {
   const float4 stat = token_stat(a, r, s);
   const int part = WAVES == 1 ? 0 : wave;
   if (part == 0 && lane == 0) put_stat(a, r, stat);
-  if (a.top) alternatives<T, WAVES>(a, r, stat, part, lane, sh[wave], sh[WAVES == 1 ? wave : 0]);
+  if (a.top) alternatives<T, SETS, WAVES>(a, r, stat, part, lane, sh[wave], sh[WAVES == 1 ? wave : 0]);
 }
 
 __global__ __launch_bounds__(256) void k_logprob_factors(HeadArgs a) {
@@ -431,13 +463,15 @@ hipError_t launch_logprobs(const HeadArgs& a, int dt, hipStream_t s) {
   const bool few = a.rows_max <= kFewTokens;
   const int blocks = (int)cdiv(few ? a.rows_max : cdiv(a.rows_max, 4), 8) * 8;
   const dim3 g(blocks + clear), b(256);
-  if (dt == MUON_BF16) {
-    if (few) hipLaunchKernelGGL((k_logprobs<u16, 4>), g, b, 0, s, a, blocks);
-    else hipLaunchKernelGGL((k_logprobs<u16, 1>), g, b, 0, s, a, blocks);
-  } else {
-    if (few) hipLaunchKernelGGL((k_logprobs<float, 4>), g, b, 0, s, a, blocks);
-    else hipLaunchKernelGGL((k_logprobs<float, 1>), g, b, 0, s, a, blocks);
-  }
+#define LOGPROBS(T, SETS)                                                                         \
+  do {                                                                                            \
+    if (few) hipLaunchKernelGGL((k_logprobs<T, SETS, 4>), g, b, 0, s, a, blocks);                 \
+    else hipLaunchKernelGGL((k_logprobs<T, SETS, 1>), g, b, 0, s, a, blocks);                     \
+  } while (0)
+  if (dt != MUON_BF16) LOGPROBS(float, 4);       // (head_plan: fp32 has 64-tiles alone)
+  else if (a.sets == 4) LOGPROBS(u16, 4);
+  else LOGPROBS(u16, 2);
+#undef LOGPROBS
   return hipGetLastError();
 }
 

@@ -108,6 +108,7 @@ hipError_t launch_adamw(const AdamList& L, int chunks, const AdamConst& c, const
 // chunk after chunk, each chunk for the block's 64 tokens in turn. A stage of
 // a product over tokens or over columns is then whole kilobytes either way.
 // ---------------------------------------------------------------------------
+typedef unsigned short u16;
 constexpr int kPanelRows = 64;
 // Kept exponentials of 16-bit inputs, in [2^-63, 1]: the fp32 pattern's 6 low
 // bits of exponent and 10 high bits of mantissa, rounded half up; kCodeBase is
@@ -163,10 +164,10 @@ struct HeadArgs {
   const float* grad_out;              // device, or null (1)
   // log probabilities (head_logprobs.hip); loss holds them
   int32_t top;                        // alternatives a token
-  int32_t sets;                       // lanes that share a statistic's vocabulary columns
+  int32_t sets;                       // sets of a statistic's vocabulary columns
   float4* tstat;                      // n_vt x piece: largest logit, sum of exponentials over it, sum of exponential
                                       // times its logarithm (base 2), all without the target's
-  uint2* best;                        // n_vt x piece x sets: each lane's largest logit, its place and the second largest
+  uint2* best;                        // n_vt x piece x sets: each one's largest logit, its place and the second largest
   float* entropy;                     // caller's, n each, or null
   float4* stats;
   float* top_logprobs;                // caller's, n x top
@@ -181,13 +182,17 @@ struct HeadArgs {
 // the loss; statistics with entropy and largest logits; the logits' gradient.
 enum LogitsMode { LOGITS_LOSS, LOGITS_STATS, LOGITS_GRAD };
 
-// The place of a lane's value q among a statistic's vocabulary columns (`set`
-// of `sets` lanes): accumulators of 32 x 32 blocks, 4 rows of 8 to each half-wave.
-__host__ __device__ inline int set_column(int set, int sets, int q) {
-  return (sets == 4 ? (set >> 1) * 32 : 0) + (q >> 4) * 32 + 8 * ((q >> 2) & 3) + 4 * (set & 1) + (q & 3);
+// Sets of logits that the alternatives are looked for in: 32 of a lane's (fp32:
+// 16), from kSetRows<T> of a statistic's columns, each half-wave's its own. The
+// column of a set's value q: accumulators of 32 x 32 blocks, 4 rows of 8 to each half.
+template <typename T>
+constexpr int kSetRows = sizeof(T) == 2 ? 64 : 32;
+template <typename T>
+__host__ __device__ inline int set_column(int set, int q) {
+  return (set >> 1) * kSetRows<T> + (q >> 4) * 32 + 8 * ((q >> 2) & 3) + 4 * (set & 1) + (q & 3);
 }
-// The set of a column.
-__host__ __device__ inline int column_set(int col, int sets) { return (sets == 4 ? (col >> 5) * 2 : 0) + ((col >> 2) & 1); }
+template <typename T>
+__host__ __device__ inline int column_set(int col) { return col / kSetRows<T> * 2 + ((col >> 2) & 1); }
 
 // Picks the tile edges, the statistics' columns and the splits, from the sizes
 // and from which gradients are wanted (before the workspace is laid out).

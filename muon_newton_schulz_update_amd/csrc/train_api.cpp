@@ -189,7 +189,7 @@ muon_status head_run(muon_handle* h, const HeadCall& c) {
   // pieces
   // (a row's statistics: at most 8 bytes for 64 words of the vocabulary, with entropy
   // 16, and 8 more for each lane that shares them with the candidates)
-  const size_t each = c.mode == LOGITS_STATS ? 16 + (c.top ? (a.half ? 16 : 32) : 0) : 8;
+  const size_t each = c.mode == LOGITS_STATS ? 16 + (c.top ? (a.half ? 16 : 32) : 0) : 8;   // (sets of 32 and 16)
   const size_t row = (size_t)a.dp * e + (size_t)cdiv(a.v, 64) * each + 24 + (grad ? (size_t)a.vp * e : 0);
   const int64_t most =
       std::min(kPieceMost, std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows));
