@@ -383,14 +383,15 @@ __device__ __forceinline__ bool strip_tile(int idx, int rows, int cols, int& r, 
   return true;
 }
 
-// The sets of a lane's MI x 16 raw logits of one token (z[mi * step]), from `set`
-// in steps of 2: the largest, its first place (6 bits) and the second largest,
-// whose last 6 bits the place takes: only that a set holds another candidate, and
-// no larger a one, is read from the second. Returns the largest of all.
+// The sets of a lane's MI x 16 raw logits of one token (z[mi * step]), to `to`: the
+// largest, its first place (6 bits) and the second largest, whose last 6 bits the
+// place takes: only that a set holds another candidate, and no larger a one, is
+// read from the second. Returns the largest of all.
 template <typename T, int MI>
-__device__ __forceinline__ float store_best(const HeadArgs& a, const f32x16_t* z, int step, int tile, int set, int r) {
+__device__ __forceinline__ float store_best(const f32x16_t* z, int step, uint2* to) {
   constexpr int EACH = kSetRows<T> / 32 < MI ? kSetRows<T> / 32 : MI;
   float top = -__builtin_inff();
+  uint2 b[MI / EACH];
 #pragma unroll
   for (int m0 = 0; m0 < MI; m0 += EACH) {
     float first = -__builtin_inff(), second = first;
@@ -404,10 +405,10 @@ __device__ __forceinline__ float store_best(const HeadArgs& a, const f32x16_t* z
     uint32_t place = 0;
 #pragma unroll
     for (int i = EACH * 16 - 1; i >= 0; --i) place = z[(m0 + i / 16) * step][i % 16] == first ? i : place;
-    a.best[((int64_t)tile * a.piece + r) * a.sets + set + m0 / EACH * 2] =
-        make_uint2(__float_as_uint(first), (__float_as_uint(second) & ~63u) | place);
+    b[m0 / EACH] = make_uint2(__float_as_uint(first), (__float_as_uint(second) & ~63u) | place);
     top = fmaxf(top, first);
   }
+  __builtin_memcpy(to, b, sizeof(b));
   return top;
 }
 
@@ -608,7 +609,11 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
     float top = kRefFloor;
     if constexpr (MODE == LOGITS_STATS) {
       if (a.top) {
-        top = fmaxf(top, store_best<T, MI>(a, &acc[0][ni], NI, tile, PAIR ? 2 * wm + hf : hf, r));
+        // (a token's statistics lie side by side: the four vocabulary tiles that run
+        // next to one another fill its lines)
+        constexpr int LANE_SETS = MI * 32 / kSetRows<T> > 0 ? MI * 32 / kSetRows<T> : 1;
+        uint2* to = a.best + ((int64_t)r * a.n_vt + tile) * a.sets + (PAIR ? 2 * wm + hf : hf * LANE_SETS);
+        top = fmaxf(top, store_best<T, MI>(&acc[0][ni], NI, to));
       } else {
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi)
@@ -712,7 +717,7 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
     }
     if (hf == 0) {
       if constexpr (MODE == LOGITS_STATS) {
-        a.tstat[(int64_t)tile * a.piece + r] = float4{top, sum, ent, 0.f};
+        a.tstat[(int64_t)r * a.n_vt + tile] = float4{top, sum, ent, 0.f};
       } else {
         a.tmax[(int64_t)tile * a.piece + r] = top;
         a.tsum[(int64_t)tile * a.piece + r] = sum;

@@ -60,7 +60,7 @@ __device__ __forceinline__ Stat tiles_stat(const HeadArgs& a, int r, int part, i
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       x[k] = float4{kRefFloor, 0.f, 0.f, 0.f};
-      if (t0 + k * parts < a.n_vt) x[k] = a.tstat[(int64_t)(t0 + k * parts) * a.piece + r];
+      if (t0 + k * parts < a.n_vt) x[k] = a.tstat[(int64_t)r * a.n_vt + t0 + k * parts];
     }
     float top = s.top;
 #pragma unroll
@@ -100,14 +100,6 @@ __device__ __forceinline__ void put_stat(const HeadArgs& a, int r, const float4&
   a.loss[i] = s.w;
   if (a.entropy) a.entropy[i] = s.z;
   if (a.stats) a.stats[i] = s;
-}
-
-// Hand-off through LDS between the lanes of one wave: the LDS executes a wave's
-// accesses in order, so only the compiler has to keep them so.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Sorting over a wave, lane 0 first: larger values, then smaller tokens.
@@ -195,12 +187,13 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x);
   return u >> 31 ? ~u : u | 0x80000000u;
 }
-// The largest number that at least `count` of the lanes' keys reach, 0 if there are not as many keys.
+// The largest number, to 20 bits (a float's 11 of mantissa), that at least `count`
+// of the lanes' keys reach; 0 if there are not as many keys.
 template <int K>
 __device__ __forceinline__ uint32_t reached_by(const uint32_t (&key)[K], int count) {
   uint32_t least = 0;
 #pragma unroll 4
-  for (int bit = 31; bit >= 0; --bit) {
+  for (int bit = 31; bit >= 12; --bit) {
     const uint32_t trial = least | 1u << bit;
     int found = 0;
 #pragma unroll
@@ -210,34 +203,44 @@ __device__ __forceinline__ uint32_t reached_by(const uint32_t (&key)[K], int cou
   return least;
 }
 
-// A wave's candidates.
-struct Candidates {
+// Four waves work on a token.
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kMostSets = 63;      // with the target one for each lane
+struct Found {
+  float z, bound;                  // a set's largest logit, and what its others do not pass
+  int word;
+};
+struct TokenShare {
+  Stat stat[kWaves];
+  Found of[kWaves][64];            // each wave's sets
+  int count[kWaves], total;
+  Found sets[64];
   double z[64];
   int word[64];
-  float bound[64];
 };
 
-// The sets that the alternatives are in, in no order (word, bound of the set's
-// others), at most 63; returns how many.
+// The sets that the alternatives are in, in no order, to sh.sets, at most
+// kMostSets; returns how many (the same in all threads).
 template <typename T, int SETS>
-__device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int lane, Candidates& sh) {
+__device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int wave, int lane, TokenShare& sh) {
   const int count = a.top + kSpare;
-  auto best_of = [&](int tile, int set) { return a.best[((int64_t)tile * a.piece + r) * SETS + set]; };
-  // 512 statistics at a time, which stay in registers where these are all (65536
-  // words; fp32 and few tokens 32768)
-  constexpr int TILES = 8, SPAN = 64 * TILES;
+  const uint64_t below = (1ull << lane) - 1;
+  const uint2* best = a.best + (int64_t)r * a.n_vt * SETS;
+  // 1024 statistics at a time, which stay in registers where these are all
+  // (131072 words; fp32 and few tokens 65536)
+  constexpr int TILES = 4, SPAN = kThreads * TILES;
   uint2 e[TILES][SETS];
+  auto tile = [&](int t0, int j) { return t0 + j * kThreads + wave * 64 + lane; };
   auto load = [&](int t0) {
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
 #pragma unroll
       for (int k = 0; k < SETS; ++k) e[j][k] = make_uint2(0xFF800000u, 0u);
-      const int t = t0 + j * 64 + lane;
-      if (t < a.n_vt) __builtin_memcpy(e[j], a.best + ((int64_t)t * a.piece + r) * SETS, sizeof(e[j]));
+      if (tile(t0, j) < a.n_vt) __builtin_memcpy(e[j], best + tile(t0, j) * SETS, sizeof(e[j]));
     }
   };
-  // each lane's largest logit of two halves of its sets: what `count` of these
-  // reach is reached by as many sets, and by few more
+  // each lane's largest logit of two halves of its sets: what `count` of a wave's
+  // reach is reached by as many of its sets, and by few more
   float most[2] = {kNone, kNone};
   for (int t0 = 0; t0 < a.n_vt; t0 += SPAN) {
     load(t0);
@@ -246,8 +249,8 @@ __device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int lane
 #pragma unroll
       for (int k = 0; k < SETS; ++k) most[k & 1] = fmaxf(most[k & 1], __uint_as_float(e[j][k].x));
   }
-  const uint32_t keys[2] = {most[0] > kNone ? ordered(most[0]) : 0u, most[1] > kNone ? ordered(most[1]) : 0u};
-  const uint32_t least = reached_by(keys, count);
+  const uint32_t halves[2] = {most[0] > kNone ? ordered(most[0]) : 0u, most[1] > kNone ? ordered(most[1]) : 0u};
+  const uint32_t least = reached_by(halves, count);
   int found = 0;
   for (int t0 = 0; t0 < a.n_vt; t0 += SPAN) {
     if (a.n_vt > SPAN) load(t0);
@@ -259,47 +262,62 @@ __device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int lane
         const bool in = z > kNone && ordered(z) >= least;
         const uint64_t mask = __ballot(in);
         if (mask == 0) continue;
-        const int at = found + __popcll(mask & ((1ull << lane) - 1));
-        if (in && at < 63) {
-          sh.word[at] = (t0 + j * 64 + lane) * a.vtile + set_column<T>(k, e[j][k].y & 63);
-          sh.z[at] = z;
-          sh.bound[at] = second_of(e[j][k]);
-        }
+        const int at = found + __popcll(mask & below);
+        if (in && at < 64) sh.of[wave][at] = Found{z, second_of(e[j][k]), tile(t0, j) * a.vtile + set_column<T, SETS>(k, e[j][k].y & 63)};
         found += __popcll(mask);
       }
   }
-  if (found <= 63) return found;
-  // more of them (equal logits, or neighbours in one lane's sets): the first
-  // `count` by (logit, word), by sorting them 64 at a time
-  Ranked<float> best = {kNone, kNoToken};
-  const int all = a.n_vt * SETS;
-  for (int s0 = 0; s0 < all; s0 += 64) {
-    const int s = s0 + lane;
-    Ranked<float> x = {kNone, kNoToken};
-    if (s < all) {
-      const uint2 b = best_of(s / SETS, s % SETS);
-      if (__uint_as_float(b.x) > kNone) x = {__uint_as_float(b.x), s / SETS * a.vtile + set_column<T>(s % SETS, b.y & 63)};
+  if (lane == 0) sh.count[wave] = found;
+  __syncthreads();
+  // of all waves' sets, those that `count` reach
+  if (wave == 0) {
+    uint32_t keys[kWaves];
+    bool over = false;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      over |= sh.count[w] > 64;
+      keys[w] = lane < sh.count[w] ? ordered(sh.of[w][lane].z) : 0u;
     }
-    // (most have nothing for a list that is full)
-    if (s0 && !__any(before(x, Ranked<float>{__shfl(best.z, 63), __shfl(best.token, 63)}))) continue;
-    sort_wave(x, lane);
-    if (s0 == 0) best = x;
-    else merge_wave(best, x, lane);
+    const uint32_t all_least = reached_by(keys, count);
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const bool in = keys[w] != 0 && keys[w] >= all_least;
+      const uint64_t mask = __ballot(in);
+      const int at = total + __popcll(mask & below);
+      if (in && at < 64) sh.sets[at] = sh.of[w][lane];
+      total += __popcll(mask);
+    }
+    if (over || total > kMostSets) {
+      // more of them (equal logits, or neighbours in one lane's sets): the first
+      // `count` by (logit, word), by sorting all sets 64 at a time
+      auto word_of = [&](int s, uint2 b) { return s / SETS * a.vtile + set_column<T, SETS>(s % SETS, b.y & 63); };
+      Ranked<float> list = {kNone, kNoToken};
+      for (int s0 = 0; s0 < a.n_vt * SETS; s0 += 64) {
+        Ranked<float> x = {kNone, kNoToken};
+        if (s0 + lane < a.n_vt * SETS) {
+          const uint2 b = best[s0 + lane];
+          if (__uint_as_float(b.x) > kNone) x = {__uint_as_float(b.x), word_of(s0 + lane, b)};
+        }
+        // (most have nothing for a list that is full)
+        if (s0 && !__any(before(x, Ranked<float>{__shfl(list.z, 63), __shfl(list.token, 63)}))) continue;
+        sort_wave(x, lane);
+        if (s0 == 0) list = x;
+        else merge_wave(list, x, lane);
+      }
+      total = count;         // (there are 64 and more)
+      if (lane < count)
+        sh.sets[lane] = Found{list.z, second_of(best[list.token / a.vtile * SETS + column_set<T, SETS>(list.token % a.vtile)]), list.token};
+    }
+    if (lane == 0) sh.total = total;
   }
-  if (lane < count) {
-    const int col = best.token % a.vtile;
-    sh.word[lane] = best.token;
-    sh.z[lane] = best.z;
-    sh.bound[lane] = second_of(best_of(best.token / a.vtile, column_set<T>(col)));
-  }
-  return count;
+  __syncthreads();
+  return sh.total;
 }
 
-// One token's alternatives, by WAVES waves: each finds the candidates, with LDS
-// of its own (`own`); their 64-bit sums are shared out (and meet in sh).
-template <typename T, int SETS, int WAVES>
-__device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const float4& stat, int wave, int lane,
-                                             Candidates& own, Candidates& sh) {
+// One token's alternatives.
+template <typename T, int SETS>
+__device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const float4& stat, int wave, int lane, TokenShare& sh) {
   const int i = a.idx[a.row0 + r], target = a.tgt[a.row0 + r], top = a.top;
   float* logps = a.top_logprobs + (int64_t)i * top;
   int64_t* tokens = a.top_tokens + (int64_t)i * top;
@@ -310,11 +328,9 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const flo
     }
     return;
   }
-  int count = candidate_sets<T, SETS>(a, r, lane, own);
-  wave_sync();
-  const bool mine = lane < count;
-  const float bound = mine ? own.bound[lane] : kNone;
-  int word = mine ? own.word[lane] : kNoToken;
+  int count = candidate_sets<T, SETS>(a, r, wave, lane, sh);
+  const float bound = lane < count ? sh.sets[lane].bound : kNone;
+  int word = lane < count ? sh.sets[lane].word : kNoToken;
   if (target >= 0 && a.zt[r] > kNone) {          // (its set leaves it out)
     if (lane == count) word = target;
     ++count;
@@ -322,9 +338,10 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const flo
   const T* h = (const T*)a.h + (int64_t)i * a.ld_h;
   const T* w = (const T*)(a.w_src ? a.w_src : a.w);
   const int64_t ld = a.w_src ? a.ld_src : a.ld_w;
-  // 64-bit logits of the lanes' words, from lane `from` in steps of whole groups
-  auto fine = [&](int words, int n, int from, int step) {
-    for (int g0 = from; g0 < n; g0 += step) {
+  // the first n lanes' words with their 64-bit logits, to which every wave sums a
+  // group at a time
+  auto fine = [&](int words, int n) {
+    for (int g0 = wave * kGroup; g0 < n; g0 += kWaves * kGroup) {
       int of[kGroup];
       double z[kGroup];
 #pragma unroll
@@ -334,47 +351,38 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const flo
       for (int g = 0; g < kGroup; ++g)
         if (lane == g && g0 + g < n) sh.z[g0 + g] = z[g];
     }
+    __syncthreads();
+    return Ranked<double>{lane < n ? sh.z[lane] : -__builtin_inf(), lane < n ? words : kNoToken};
   };
-  if (WAVES > 1) __syncthreads();                // (every wave has read its candidates)
-  else wave_sync();
-  fine(word, count, wave * kGroup, WAVES * kGroup);
-  if (WAVES > 1) __syncthreads();
-  else wave_sync();
-  if (wave != 0) return;
-  Ranked<double> found = {lane < count ? sh.z[lane] : -__builtin_inf(), lane < count ? word : kNoToken};
+  Ranked<double> found = fine(word, count);
   // ranks by counting who is in front
   int rank = 0;
   for (int k = 0; k < count; ++k)
     rank += before(Ranked<double>{sh.z[k], __builtin_amdgcn_readlane(word, k)}, found) ? 1 : 0;
-  wave_sync();
-  if (lane < count) {
+  __syncthreads();
+  if (wave == 0 && lane < count) {
     sh.z[rank] = found.z;
     sh.word[rank] = found.token;
   }
-  wave_sync();
+  __syncthreads();
   found = {lane < count ? sh.z[lane] : -__builtin_inf(), lane < count ? sh.word[lane] : kNoToken};
   // sets that may have two of the alternatives: all of them
   const float least = (float)__shfl(found.z, top - 1);
-  const uint64_t whole = __ballot(bound > kNone && bound >= least - fabsf(least) * 0x1p-18f);
-  for (uint64_t todo = whole; todo; todo &= todo - 1) {
+  for (uint64_t todo = __ballot(bound > kNone && bound >= least - fabsf(least) * 0x1p-18f); todo; todo &= todo - 1) {
     const int first = __builtin_amdgcn_readlane(word, __builtin_ctzll(todo));
-    const int tile = first / a.vtile, set = column_set<T>(first % a.vtile);
-    int member = tile * a.vtile + set_column<T>(set, lane);
+    const int member = first / a.vtile * a.vtile + set_column<T, SETS>(column_set<T, SETS>(first % a.vtile), lane);
     const bool in = lane < kSetRows<T> / 2 && member < a.v && member != first && member != target;
     // the members side by side in the first lanes
     const uint64_t mask = __ballot(in);
+    __syncthreads();
+    if (wave == 0 && in) sh.word[__popcll(mask & ((1ull << lane) - 1))] = member;
+    __syncthreads();
     const int n = __popcll(mask);
-    wave_sync();
-    if (in) sh.word[__popcll(mask & ((1ull << lane) - 1))] = member;
-    wave_sync();
-    member = lane < n ? sh.word[lane] : kNoToken;
-    fine(member, n, 0, kGroup);
-    wave_sync();
-    Ranked<double> x = {lane < n ? sh.z[lane] : -__builtin_inf(), member};
+    Ranked<double> x = fine(lane < n ? sh.word[lane] : kNoToken, n);
     sort_wave(x, lane);
     merge_wave(found, x, lane);
   }
-  if (lane >= top) return;
+  if (wave != 0 || lane >= top) return;
   const bool there = found.token != kNoToken && found.z > -__builtin_inf();
   const double c = a.softcap, z = c > 0 ? tanh(found.z / c) * c : found.z;
   logps[lane] = !there ? kNone : found.token == target ? stat.w : (float)((z - stat.x) - stat.y);
@@ -394,45 +402,46 @@ __device__ __forceinline__ void clear_ignored(const HeadArgs& a, int64_t from) {
   }
 }
 
-// Many tokens without alternatives: 64 tokens a block, a token's tiles over 16
-// threads.
-constexpr int kParts = 16;
-__global__ __launch_bounds__(1024) void k_logprob_stats(HeadArgs a, int blocks) {
-  __shared__ Stat sh[kParts][64];
+// All of a wave's statistics joined, the same in every lane.
+__device__ __forceinline__ Stat wave_stat(Stat s) {
+  s = over(s, over_lanes<64>(s.top, [](float x, float y) { return fmaxf(x, y); }));
+  s.sum = lanes_sum<64>(s.sum);
+  s.ent = lanes_sum<64>(s.ent);
+  return s;
+}
+
+// Many tokens without alternatives: a wave a token.
+__global__ __launch_bounds__(256) void k_logprob_stats(HeadArgs a, int blocks) {
   if ((int)blockIdx.x >= blocks) {
     clear_ignored(a, ((int64_t)blockIdx.x - blocks) * 1024);
     return;
   }
-  const int rows = piece_rows(a), lane = threadIdx.x & 63, part = threadIdx.x >> 6, r = blockIdx.x * 64 + lane;
-  if (r < rows) sh[part][lane] = tiles_stat(a, r, part, kParts);
-  __syncthreads();
-  if (part != 0 || r >= rows) return;
-  Stat s = sh[0][lane];
-#pragma unroll
-  for (int p = 1; p < kParts; ++p) s = joined(s, sh[p][lane]);
-  put_stat(a, r, token_stat(a, r, s));
+  const int lane = threadIdx.x & 63, r = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= piece_rows(a)) return;
+  const float4 stat = token_stat(a, r, wave_stat(tiles_stat(a, r, lane, 64)));
+  if (lane == 0) put_stat(a, r, stat);
 }
 
-// A wave a token, or (few tokens) the block's four for one; neighbouring tokens,
-// whose statistics share lines, on one XCD.
-template <typename T, int SETS, int WAVES>
-__global__ __launch_bounds__(256) void k_logprobs(HeadArgs a, int blocks) {
-  __shared__ Candidates sh[4];
+// A block a token.
+template <typename T, int SETS>
+__global__ __launch_bounds__(kThreads) void k_logprobs(HeadArgs a, int blocks) {
+  __shared__ TokenShare sh;
   if ((int)blockIdx.x >= blocks) {
     clear_ignored(a, ((int64_t)blockIdx.x - blocks) * 1024);
     return;
   }
   const int rows = piece_rows(a), lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int block = (blockIdx.x & 7) * (blocks / 8) + (blockIdx.x >> 3), r = WAVES == 1 ? block * 4 + wave : block;
+  const int r = blockIdx.x;
   if (r >= rows) return;
-  Stat s = tiles_stat(a, r, lane, 64);
-  s = over(s, over_lanes<64>(s.top, [](float x, float y) { return fmaxf(x, y); }));
-  s.sum = lanes_sum<64>(s.sum);
-  s.ent = lanes_sum<64>(s.ent);
+  Stat s = wave_stat(tiles_stat(a, r, threadIdx.x, kThreads));
+  if (lane == 0) sh.stat[wave] = s;
+  __syncthreads();
+  s = sh.stat[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) s = joined(s, sh.stat[w]);
   const float4 stat = token_stat(a, r, s);
-  const int part = WAVES == 1 ? 0 : wave;
-  if (part == 0 && lane == 0) put_stat(a, r, stat);
-  if (a.top) alternatives<T, SETS, WAVES>(a, r, stat, part, lane, sh[wave], sh[WAVES == 1 ? wave : 0]);
+  if (threadIdx.x == 0) put_stat(a, r, stat);
+  if (a.top) alternatives<T, SETS>(a, r, stat, wave, lane, sh);
 }
 
 __global__ __launch_bounds__(256) void k_logprob_factors(HeadArgs a) {
@@ -447,7 +456,7 @@ __global__ __launch_bounds__(256) void k_logprob_factors(HeadArgs a) {
   a.rs[r] = float4{0.f, 0.f, tg >= 0 ? -gp * expm1f(lp) - ge * expf(lp) * (lp + s.z) : 0.f, 0.f};
 }
 
-// Tokens that a block each still has room for at once.
+// Statistics alone: tokens of which a block each goes faster than a wave each.
 constexpr int kFewTokens = 512;
 inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
 
@@ -456,22 +465,16 @@ inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b);
 hipError_t launch_logprobs(const HeadArgs& a, int dt, hipStream_t s) {
   const int clear = a.row0 == 0 ? (int)cdiv(a.n, 1024) : 0;
   if (a.top == 0 && a.rows_max > kFewTokens) {
-    const int blocks = (int)cdiv(a.rows_max, 64);
-    hipLaunchKernelGGL(k_logprob_stats, dim3(blocks + clear), dim3(1024), 0, s, a, blocks);
+    const int blocks = (int)cdiv(a.rows_max, 4);
+    hipLaunchKernelGGL(k_logprob_stats, dim3(blocks + clear), dim3(256), 0, s, a, blocks);
     return hipGetLastError();
   }
-  const bool few = a.rows_max <= kFewTokens;
-  const int blocks = (int)cdiv(few ? a.rows_max : cdiv(a.rows_max, 4), 8) * 8;
-  const dim3 g(blocks + clear), b(256);
-#define LOGPROBS(T, SETS)                                                                         \
-  do {                                                                                            \
-    if (few) hipLaunchKernelGGL((k_logprobs<T, SETS, 4>), g, b, 0, s, a, blocks);                 \
-    else hipLaunchKernelGGL((k_logprobs<T, SETS, 1>), g, b, 0, s, a, blocks);                     \
-  } while (0)
-  if (dt != MUON_BF16) LOGPROBS(float, 4);       // (head_plan: fp32 has 64-tiles alone)
-  else if (a.sets == 4) LOGPROBS(u16, 4);
-  else LOGPROBS(u16, 2);
-#undef LOGPROBS
+  const int blocks = a.rows_max;
+  const dim3 g(blocks + clear), b(kThreads);
+  // (head_plan: fp32 has 64-tiles alone)
+  if (dt != MUON_BF16) hipLaunchKernelGGL((k_logprobs<float, 4>), g, b, 0, s, a, blocks);
+  else if (a.sets == 4) hipLaunchKernelGGL((k_logprobs<u16, 4>), g, b, 0, s, a, blocks);
+  else hipLaunchKernelGGL((k_logprobs<u16, 2>), g, b, 0, s, a, blocks);
   return hipGetLastError();
 }
 

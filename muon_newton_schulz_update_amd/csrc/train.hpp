@@ -165,9 +165,9 @@ struct HeadArgs {
   // log probabilities (head_logprobs.hip); loss holds them
   int32_t top;                        // alternatives a token
   int32_t sets;                       // sets of a statistic's vocabulary columns
-  float4* tstat;                      // n_vt x piece: largest logit, sum of exponentials over it, sum of exponential
+  float4* tstat;                      // piece x n_vt: largest logit, sum of exponentials over it, sum of exponential
                                       // times its logarithm (base 2), all without the target's
-  uint2* best;                        // n_vt x piece x sets: each one's largest logit, its place and the second largest
+  uint2* best;                        // piece x n_vt x sets: each one's largest logit, its place and the second largest
   float* entropy;                     // caller's, n each, or null
   float4* stats;
   float* top_logprobs;                // caller's, n x top
@@ -182,17 +182,23 @@ struct HeadArgs {
 // the loss; statistics with entropy and largest logits; the logits' gradient.
 enum LogitsMode { LOGITS_LOSS, LOGITS_STATS, LOGITS_GRAD };
 
-// Sets of logits that the alternatives are looked for in: 32 of a lane's (fp32:
-// 16), from kSetRows<T> of a statistic's columns, each half-wave's its own. The
-// column of a set's value q: accumulators of 32 x 32 blocks, 4 rows of 8 to each half.
+// Sets of logits that the alternatives are looked for in: 32 of a lane's (fp32: 16)
+// among a statistic's columns. The accumulators are 32 x 32 blocks with 4 rows of
+// 8 to each half-wave; a set has kSetRows<T> / 32 blocks of one half. 16-bit: a
+// half-wave's sets are neighbours; fp32: a wave's two.
 template <typename T>
 constexpr int kSetRows = sizeof(T) == 2 ? 64 : 32;
-template <typename T>
+// The column of a set's value q, and the set of a column.
+template <typename T, int SETS>
 __host__ __device__ inline int set_column(int set, int q) {
-  return (set >> 1) * kSetRows<T> + (q >> 4) * 32 + 8 * ((q >> 2) & 3) + 4 * (set & 1) + (q & 3);
+  const int half = sizeof(T) == 2 ? set / (SETS / 2) : set & 1, part = sizeof(T) == 2 ? set % (SETS / 2) : set >> 1;
+  return part * kSetRows<T> + (q >> 4) * 32 + 8 * ((q >> 2) & 3) + 4 * half + (q & 3);
 }
-template <typename T>
-__host__ __device__ inline int column_set(int col) { return col / kSetRows<T> * 2 + ((col >> 2) & 1); }
+template <typename T, int SETS>
+__host__ __device__ inline int column_set(int col) {
+  const int half = (col >> 2) & 1, part = col / kSetRows<T>;
+  return sizeof(T) == 2 ? half * (SETS / 2) + part : part * 2 + half;
+}
 
 // Picks the tile edges, the statistics' columns and the splits, from the sizes
 // and from which gradients are wanted (before the workspace is laid out).
