@@ -412,13 +412,13 @@ __device__ __forceinline__ float store_best(const f32x16_t* z, int step, uint2* 
   return top;
 }
 
-// The logits' gradient dz = -p (b + g log p) and the target's (train.hpp: ts), to
+// The logits' gradient dz = p (b + g log2 p) and the target's (train.hpp: ts), to
 // the panels in the operands' type; z are a lane's raw logits of token r. Rows past
 // the piece's and columns past the vocabulary become zero (stages of dW and dH).
 template <typename T, int MI>
 __device__ __forceinline__ void store_logits_grad(const HeadArgs& a, f32x16_t (&z)[MI], int r, int rows, int vw, int hf,
                                                   int tg, bool any_mine, bool edge) {
-  const bool real = r < rows, cap = a.softcap > 0.f;
+  const bool real = r < rows, cap = a.softcap > 0.f, some_past = !__all(real);
   float4 ts = {0.f, 0.f, 0.f, 0.f};
   if (real) ts = a.ts[r];
   float own = 0.f;
@@ -429,13 +429,18 @@ __device__ __forceinline__ void store_logits_grad(const HeadArgs& a, f32x16_t (&
     if (cap) cap16(z[mi], a.softcap, a.cap_inv, slope);
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
-      // log p from differences, as good as the logits however large these are
-      // (below 2^-126 p counts as 0: what it is multiplied by is no infinity)
-      const float lp = __builtin_elementwise_maximum((z[mi][q] - ts.x) - ts.y, -126.f / kLog2e);
-      const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
-      e[q] = -p * fmaf(ts.w, lp, ts.z);
-      if (cap) e[q] *= slope[q];
-      if (!real) e[q] = 0.f;
+      // log p, base 2, from a difference, which is as good as the logits however large
+      // these are (below 2^-126 p counts as 0: what it is multiplied by is no infinity)
+      const float y = __builtin_elementwise_maximum(fmaf(z[mi][q] - ts.x, kLog2e, ts.y), -126.f);
+      e[q] = __builtin_amdgcn_exp2f(y) * fmaf(ts.w, y, ts.z);
+    }
+    if (cap) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) e[q] *= slope[q];
+    }
+    if (some_past) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) e[q] = real ? e[q] : 0.f;
     }
     if (any_mine) {
 #pragma unroll

@@ -16,9 +16,9 @@
 //                 16-bit inputs every product is exact) and sorted. What is
 //                 outside the spare sets could only be in front by an error
 //                 of the 32-bit sums that passes over kSpare others.
-//   factors       for the gradient, dz = -p (b + g log p) with g the entropy's
-//                 gradient and b = g_logprob + g H; the target's is
-//                 g_logprob (1 - p) - g p (log p + H)
+//   factors       for the gradient, dz = p (b + g log2 p) with g the entropy's
+//                 gradient times -log(2) and b = -(g_logprob + g_entropy H); the
+//                 target's is g_logprob (1 - p) - g_entropy p (log p + H)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -450,7 +450,7 @@ __global__ __launch_bounds__(256) void k_logprob_factors(HeadArgs a) {
   const int i = a.idx[a.row0 + r], tg = a.tgt[a.row0 + r];
   const float4 s = a.stats_in[i];
   const float gp = tg >= 0 && a.grad_logprobs ? a.grad_logprobs[i] : 0.f, ge = a.grad_entropy ? a.grad_entropy[i] : 0.f;
-  a.ts[r] = float4{s.x, s.y, fmaf(ge, s.z, gp), ge};
+  a.ts[r] = float4{s.x, -s.y * kLog2e, -fmaf(ge, s.z, gp), -ge * kLn2};
   // (1 - p from log p, which keeps what a token that is nearly sure still has to learn)
   const float lp = __builtin_elementwise_maximum(s.w, -126.f / kLog2e);   // (as the other words': no infinity times 0)
   a.rs[r] = float4{0.f, 0.f, tg >= 0 ? -gp * expm1f(lp) - ge * expf(lp) * (lp + s.z) : 0.f, 0.f};

@@ -175,7 +175,7 @@ struct HeadArgs {
   const float4* stats_in;             // the gradient's: what the forward call left,
   const float* grad_logprobs;         // and the results' gradients, or null
   const float* grad_entropy;
-  float4* ts;                         // piece: {reference, log of the sum over it, grad_logprob + grad_entropy entropy, grad_entropy}
+  float4* ts;                         // piece: {reference, minus log2 of the sum over it, and dz's b and g (head_logprobs.hip)}
 };
 
 // What the logits' launch leaves: statistics and, where kept, exponentials for
