@@ -1,12 +1,14 @@
-"""Train a small language model with every step of libmuon: the head's cross
-entropy with its gradient, the global gradient norm, Muon on the matrices of
-the blocks and AdamW on the embedding, the head and the gains.
+"""Train a small language model with every step of libmuon: the norms between
+its blocks, the head's cross entropy with its gradient, the global gradient
+norm, Muon on the matrices of the blocks and AdamW on the embedding, the head
+and the gains; then look at what it has learnt: how likely it finds the words
+of a held-out text, how sure it is and what else it expects.
 
     python examples/train_small_lm.py [--steps 60]
 
-The text is synthetic: every word has a few likely successors. The body of the
-model (two residual blocks over the last two words) is plain torch; weights
-that AdamW owns are 32-bit with the 16-bit copies that the model computes with.
+The text is synthetic: every word has a few likely successors. The inside of
+the model's two blocks (over the last two words) is plain torch; weights that
+AdamW owns are 32-bit with the 16-bit copies that the model computes with.
 """
 from __future__ import annotations
 
@@ -43,14 +45,19 @@ class Model:
 
     def hidden(self, words: torch.Tensor) -> torch.Tensor:
         embedding, gains = self.copies[0], self.copies[2:]
-        norm = lambda x, g: x * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6).to(BF) * g
         x = embedding[words]
+        h = mu.rms_norm(x, gains[0])
         for b in range(BLOCKS):
-            y = norm(x, gains[b])
-            y = torch.cat((y, torch.roll(y, 1, 0)), 1)
+            y = torch.cat((h, torch.roll(h, 1, 0)), 1)
             y = torch.relu(y @ self.matrices[2 * b].t()).square()
-            x = x + y @ self.matrices[2 * b + 1].t()
-        return norm(x, gains[-1])
+            # the block's end and the next one's start (or the head's)
+            x, h = mu.residual_norm(x, y @ self.matrices[2 * b + 1].t(), post_norm=False, pre_gain=gains[b + 1])
+        return h
+
+    def score(self, words: torch.Tensor, targets: torch.Tensor, top: int = 4) -> mu.LogProbs:
+        """Log probabilities of the targets, the distributions' entropies and their likeliest words."""
+        with torch.no_grad():
+            return mu.linear_logprobs(self.hidden(words), self.copies[1], targets, top=top)
 
     def step(self, words: torch.Tensor, targets: torch.Tensor, number: int) -> tuple[torch.Tensor, torch.Tensor]:
         """One training step; (loss, gradient norm), both still on the device."""
@@ -80,11 +87,15 @@ def text(seed: int, likely: torch.Tensor) -> torch.Tensor:
     return torch.tensor(words, device="cuda")
 
 
-def train(steps: int, say=print) -> list[float]:
+def language() -> torch.Tensor:
+    """Each word's four likely successors; an eighth of the words occur."""
     g = torch.Generator()
     g.manual_seed(1)
-    likely = torch.randint(0, VOCAB // 8, (VOCAB, 4), generator=g)   # an eighth of the words occur
-    model, losses = Model(), []
+    return torch.randint(0, VOCAB // 8, (VOCAB, 4), generator=g)
+
+
+def train(steps: int, say=print, model: Model | None = None) -> list[float]:
+    model, likely, losses = model or Model(), language(), []
     for k in range(1, steps + 1):
         words = text(k, likely)
         targets = words[1:].clone()
@@ -95,7 +106,20 @@ def train(steps: int, say=print) -> list[float]:
     return [float(x) for x, _ in losses]
 
 
+def look(model: Model, say=print) -> dict[str, float]:
+    """A held-out text: mean log probability and entropy, and how often the next word is among the four likeliest."""
+    words = text(0, language())
+    out = model.score(words[:-1], words[1:])
+    among = (out.top_tokens == words[1:, None]).any(1).float().mean()
+    found = dict(logprob=float(out.logprobs.mean()), entropy=float(out.entropy.mean()), among_four=float(among))
+    if say:
+        say("held out  " + "  ".join(f"{k} {v:.3f}" for k, v in found.items()), flush=True)
+    return found
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
-    train(ap.parse_args().steps)
+    trained = Model()
+    train(ap.parse_args().steps, model=trained)
+    look(trained)
