@@ -22,6 +22,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "head_device.hpp"
 #include "train.hpp"
 #include "wave.hpp"
@@ -76,10 +78,18 @@ __device__ __forceinline__ Stat tiles_stat(const HeadArgs& a, int r, int part, i
   return s;
 }
 
+// A token's place in the call, its target and the target's logit (nothing that
+// means anything where the target is outside the vocabulary).
+struct Token {
+  int at, target;
+  float z;
+};
+__device__ __forceinline__ Token token_of(const HeadArgs& a, int r) { return {a.idx[a.row0 + r], a.tgt[a.row0 + r], a.zt[r]}; }
+
 // {reference, log of the sum over it, entropy, log probability}
-__device__ __forceinline__ float4 token_stat(const HeadArgs& a, int r, Stat s) {
-  const int tg = a.tgt[a.row0 + r];
-  const float z = tg >= 0 ? a.zt[r] : kRefFloor;
+__device__ __forceinline__ float4 token_stat(const Token& token, Stat s) {
+  const int tg = token.target;
+  const float z = tg >= 0 ? token.z : kRefFloor;
   const float t = fmaxf(s.top, z), x = scaled_log2(s.top, t);
   const float f = exp2f(x), others = s.sum * f;
   float all = others, ent = f * (s.ent + s.sum * x), log_sum = logf(others), logp = kNan;
@@ -94,9 +104,7 @@ __device__ __forceinline__ float4 token_stat(const HeadArgs& a, int r, Stat s) {
   if (log_sum != log_sum) logp = kNan;
   return {t, log_sum, log_sum - kLn2 * ent / all, logp};
 }
-__device__ __forceinline__ void put_stat(const HeadArgs& a, int r, const float4& s) {
-  const int i = a.idx[a.row0 + r];
-  a.rs[r] = s;
+__device__ __forceinline__ void put_stat(const HeadArgs& a, int i, const float4& s) {
   a.loss[i] = s.w;
   if (a.entropy) a.entropy[i] = s.z;
   if (a.stats) a.stats[i] = s;
@@ -139,40 +147,39 @@ __device__ __forceinline__ void merge_wave(Ranked<F>& x, const Ranked<F>& sorted
 }
 
 // Logits of a token and G words in 64 bits, the wave's lanes over the width.
-constexpr int kGroup = 8;
-template <typename T>
-__device__ __forceinline__ void fine_logits(const T* h, const T* w, int64_t ld, int d, const int (&words)[kGroup], int lane,
-                                            double (&z)[kGroup]) {
+template <int G, typename T>
+__device__ __forceinline__ void fine_logits(const T* h, const T* w, int64_t ld, int d, const int (&words)[G], int lane,
+                                            double (&z)[G]) {
   constexpr int CH = 16 / (int)sizeof(T);
   auto value = [](T x) -> double {
     if constexpr (sizeof(T) == 2) return (double)bf2f(x);
     else return (double)x;
   };
 #pragma unroll
-  for (int g = 0; g < kGroup; ++g) z[g] = 0;
+  for (int g = 0; g < G; ++g) z[g] = 0;
   for (int c = lane * CH; c < d; c += 64 * CH) {
-    T x[CH], y[kGroup][CH];
+    T x[CH], y[G][CH];
     if (c + CH <= d) {
       __builtin_memcpy(x, h + c, 16);
 #pragma unroll
-      for (int g = 0; g < kGroup; ++g) __builtin_memcpy(y[g], w + words[g] * ld + c, 16);
+      for (int g = 0; g < G; ++g) __builtin_memcpy(y[g], w + words[g] * ld + c, 16);
     } else {
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         x[e] = c + e < d ? h[c + e] : T(0);
 #pragma unroll
-        for (int g = 0; g < kGroup; ++g) y[g][e] = c + e < d ? w[words[g] * ld + c + e] : T(0);
+        for (int g = 0; g < G; ++g) y[g][e] = c + e < d ? w[words[g] * ld + c + e] : T(0);
       }
     }
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
       const double v = value(x[e]);
 #pragma unroll
-      for (int g = 0; g < kGroup; ++g) z[g] = fma(v, value(y[g][e]), z[g]);
+      for (int g = 0; g < G; ++g) z[g] = fma(v, value(y[g][e]), z[g]);
     }
   }
 #pragma unroll
-  for (int g = 0; g < kGroup; ++g) z[g] = lanes_sum<64>(z[g]);
+  for (int g = 0; g < G; ++g) z[g] = lanes_sum<64>(z[g]);
 }
 
 constexpr int kNoToken = 0x7FFFFFFF;
@@ -219,51 +226,55 @@ struct TokenShare {
   int word[64];
 };
 
+// A thread's statistics of a token's sets, 1024 at a time: they stay in registers
+// where these are all (131072 words; fp32 and few tokens 65536).
+template <int SETS>
+struct Sets {
+  static constexpr int kTiles = 4, kSpan = kThreads * kTiles;
+  uint2 of[kTiles][SETS];
+  __device__ __forceinline__ static int tile(int t0, int j) { return t0 + j * kThreads + (int)threadIdx.x; }
+  __device__ __forceinline__ void load(const uint2* best, int n_vt, int t0) {
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+#pragma unroll
+      for (int k = 0; k < SETS; ++k) of[j][k] = make_uint2(0xFF800000u, 0u);
+      if (tile(t0, j) < n_vt) __builtin_memcpy(of[j], best + tile(t0, j) * SETS, sizeof(of[j]));
+    }
+  }
+};
+
 // The sets that the alternatives are in, in no order, to sh.sets, at most
-// kMostSets; returns how many (the same in all threads).
+// kMostSets; returns how many (the same in all threads). e: the first statistics.
 template <typename T, int SETS>
-__device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int wave, int lane, TokenShare& sh) {
+__device__ __forceinline__ int candidate_sets(const HeadArgs& a, const uint2* best, Sets<SETS>& e, int wave, int lane, TokenShare& sh) {
   const int count = a.top + kSpare;
   const uint64_t below = (1ull << lane) - 1;
-  const uint2* best = a.best + (int64_t)r * a.n_vt * SETS;
-  // 1024 statistics at a time, which stay in registers where these are all
-  // (131072 words; fp32 and few tokens 65536)
-  constexpr int TILES = 4, SPAN = kThreads * TILES;
-  uint2 e[TILES][SETS];
-  auto tile = [&](int t0, int j) { return t0 + j * kThreads + wave * 64 + lane; };
-  auto load = [&](int t0) {
-#pragma unroll
-    for (int j = 0; j < TILES; ++j) {
-#pragma unroll
-      for (int k = 0; k < SETS; ++k) e[j][k] = make_uint2(0xFF800000u, 0u);
-      if (tile(t0, j) < a.n_vt) __builtin_memcpy(e[j], best + tile(t0, j) * SETS, sizeof(e[j]));
-    }
-  };
+  constexpr int TILES = Sets<SETS>::kTiles, SPAN = Sets<SETS>::kSpan;
   // each lane's largest logit of two halves of its sets: what `count` of a wave's
   // reach is reached by as many of its sets, and by few more
   float most[2] = {kNone, kNone};
   for (int t0 = 0; t0 < a.n_vt; t0 += SPAN) {
-    load(t0);
+    if (t0) e.load(best, a.n_vt, t0);
 #pragma unroll
     for (int j = 0; j < TILES; ++j)
 #pragma unroll
-      for (int k = 0; k < SETS; ++k) most[k & 1] = fmaxf(most[k & 1], __uint_as_float(e[j][k].x));
+      for (int k = 0; k < SETS; ++k) most[k & 1] = fmaxf(most[k & 1], __uint_as_float(e.of[j][k].x));
   }
   const uint32_t halves[2] = {most[0] > kNone ? ordered(most[0]) : 0u, most[1] > kNone ? ordered(most[1]) : 0u};
   const uint32_t least = reached_by(halves, count);
   int found = 0;
   for (int t0 = 0; t0 < a.n_vt; t0 += SPAN) {
-    if (a.n_vt > SPAN) load(t0);
+    if (a.n_vt > SPAN) e.load(best, a.n_vt, t0);
 #pragma unroll
     for (int j = 0; j < TILES; ++j)
 #pragma unroll
       for (int k = 0; k < SETS; ++k) {
-        const float z = __uint_as_float(e[j][k].x);
+        const float z = __uint_as_float(e.of[j][k].x);
         const bool in = z > kNone && ordered(z) >= least;
         const uint64_t mask = __ballot(in);
         if (mask == 0) continue;
         const int at = found + __popcll(mask & below);
-        if (in && at < 64) sh.of[wave][at] = Found{z, second_of(e[j][k]), tile(t0, j) * a.vtile + set_column<T, SETS>(k, e[j][k].y & 63)};
+        if (in && at < 64) sh.of[wave][at] = Found{z, second_of(e.of[j][k]), e.tile(t0, j) * a.vtile + set_column<T, SETS>(k, e.of[j][k].y & 63)};
         found += __popcll(mask);
       }
   }
@@ -317,8 +328,9 @@ __device__ __forceinline__ int candidate_sets(const HeadArgs& a, int r, int wave
 
 // One token's alternatives.
 template <typename T, int SETS>
-__device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const float4& stat, int wave, int lane, TokenShare& sh) {
-  const int i = a.idx[a.row0 + r], target = a.tgt[a.row0 + r], top = a.top;
+__device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& token, const uint2* best, Sets<SETS>& e,
+                                             const float4& stat, int wave, int lane, TokenShare& sh) {
+  const int i = token.at, target = token.target, top = a.top;
   float* logps = a.top_logprobs + (int64_t)i * top;
   int64_t* tokens = a.top_tokens + (int64_t)i * top;
   if (stat.y != stat.y) {
@@ -328,10 +340,10 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const flo
     }
     return;
   }
-  int count = candidate_sets<T, SETS>(a, r, wave, lane, sh);
+  int count = candidate_sets<T, SETS>(a, best, e, wave, lane, sh);
   const float bound = lane < count ? sh.sets[lane].bound : kNone;
   int word = lane < count ? sh.sets[lane].word : kNoToken;
-  if (target >= 0 && a.zt[r] > kNone) {          // (its set leaves it out)
+  if (target >= 0 && token.z > kNone) {          // (its set leaves it out)
     if (lane == count) word = target;
     ++count;
   }
@@ -340,17 +352,22 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const flo
   const int64_t ld = a.w_src ? a.ld_src : a.ld_w;
   // the first n lanes' words with their 64-bit logits, to which every wave sums a
   // group at a time
-  auto fine = [&](int words, int n) {
-    for (int g0 = wave * kGroup; g0 < n; g0 += kWaves * kGroup) {
-      int of[kGroup];
-      double z[kGroup];
+  auto groups = [&](int words, int n, auto size) {
+    constexpr int G = decltype(size)::value;
+    for (int g0 = wave * G; g0 < n; g0 += kWaves * G) {
+      int of[G];
+      double z[G];
 #pragma unroll
-      for (int g = 0; g < kGroup; ++g) of[g] = __builtin_amdgcn_readlane(words, min(g0 + g, n - 1));
-      fine_logits(h, w, ld, a.d, of, lane, z);
+      for (int g = 0; g < G; ++g) of[g] = __builtin_amdgcn_readlane(words, min(g0 + g, n - 1));
+      fine_logits<G>(h, w, ld, a.d, of, lane, z);
 #pragma unroll
-      for (int g = 0; g < kGroup; ++g)
+      for (int g = 0; g < G; ++g)
         if (lane == g && g0 + g < n) sh.z[g0 + g] = z[g];
     }
+  };
+  auto fine = [&](int words, int n) {
+    if (n <= kWaves * 4) groups(words, n, std::integral_constant<int, 4>());
+    else groups(words, n, std::integral_constant<int, 8>());
     __syncthreads();
     return Ranked<double>{lane < n ? sh.z[lane] : -__builtin_inf(), lane < n ? words : kNoToken};
   };
@@ -366,9 +383,10 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, int r, const flo
   }
   __syncthreads();
   found = {lane < count ? sh.z[lane] : -__builtin_inf(), lane < count ? sh.word[lane] : kNoToken};
-  // sets that may have two of the alternatives: all of them
-  const float least = (float)__shfl(found.z, top - 1);
-  for (uint64_t todo = __ballot(bound > kNone && bound >= least - fabsf(least) * 0x1p-18f); todo; todo &= todo - 1) {
+  // sets that may have two of the alternatives: all of them (the last one's logit
+  // less a 32-bit sum's error; of an infinite one that is no number, and none is out)
+  const float last = (float)__shfl(found.z, top - 1), least = last - fabsf(last) * 0x1p-18f;
+  for (uint64_t todo = __ballot(bound > kNone && !(bound < least)); todo; todo &= todo - 1) {
     const int first = __builtin_amdgcn_readlane(word, __builtin_ctzll(todo));
     const int member = first / a.vtile * a.vtile + set_column<T, SETS>(column_set<T, SETS>(first % a.vtile), lane);
     const bool in = lane < kSetRows<T> / 2 && member < a.v && member != first && member != target;
@@ -418,8 +436,9 @@ __global__ __launch_bounds__(256) void k_logprob_stats(HeadArgs a, int blocks) {
   }
   const int lane = threadIdx.x & 63, r = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= piece_rows(a)) return;
-  const float4 stat = token_stat(a, r, wave_stat(tiles_stat(a, r, lane, 64)));
-  if (lane == 0) put_stat(a, r, stat);
+  const Token token = token_of(a, r);
+  const float4 stat = token_stat(token, wave_stat(tiles_stat(a, r, lane, 64)));
+  if (lane == 0) put_stat(a, token.at, stat);
 }
 
 // A block a token.
@@ -433,15 +452,20 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(HeadArgs a, int blocks) {
   const int rows = piece_rows(a), lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = blockIdx.x;
   if (r >= rows) return;
+  // (all that the token's first steps read is asked for together)
+  const Token token = token_of(a, r);
+  const uint2* best = a.best + (int64_t)r * a.n_vt * SETS;
+  Sets<SETS> e;
+  if (a.top) e.load(best, a.n_vt, 0);
   Stat s = wave_stat(tiles_stat(a, r, threadIdx.x, kThreads));
   if (lane == 0) sh.stat[wave] = s;
   __syncthreads();
   s = sh.stat[0];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) s = joined(s, sh.stat[w]);
-  const float4 stat = token_stat(a, r, s);
-  if (threadIdx.x == 0) put_stat(a, r, stat);
-  if (a.top) alternatives<T, SETS>(a, r, stat, wave, lane, sh);
+  const float4 stat = token_stat(token, s);
+  if (threadIdx.x == 0) put_stat(a, token.at, stat);
+  if (a.top) alternatives<T, SETS>(a, token, best, e, stat, wave, lane, sh);
 }
 
 __global__ __launch_bounds__(256) void k_logprob_factors(HeadArgs a) {

@@ -349,6 +349,26 @@ def test_masked_words(n, low):
     assert bool((mu.linear_logprobs(h, w2, masked_target).logprobs <= -2e38).all())
 
 
+@pytest.mark.parametrize("n", [2, 90])
+def test_infinite_logits_under_a_soft_cap(n):
+    """They count as the cap, and come first, by rising token: several of them in one lane's set, and one given."""
+    v, d, cap = 900, 16, 5.0
+    h, w, t = make(n, v, d, F32, seed=47)
+    h[:, 0] = 1.0
+    words = torch.tensor([256, 257, 264, 290, 400, 777], device="cuda")
+    raw = mm(h.double(), w.double().t())
+    w[words, 0] = float("inf")
+    raw[:, words] = float("inf")
+    t[0] = 264
+    out = mu.linear_logprobs(h, w, t, top=9, softcap=cap)
+    assert torch.equal(out.top_tokens, raw.sort(dim=1, descending=True, stable=True).indices[:, :9])
+    z = cap * torch.tanh(raw / cap)
+    lp = torch.log_softmax(z, 1)
+    err = (512 + v / 64 + 40) * U + 12 * U * cap + 2 * (d + 2) * U * mm(h.abs().double(), w.nan_to_num(0, 0, 0).abs().double().t()).amax(1)
+    within(out.logprobs, lp.gather(1, t[:, None])[:, 0], err + 12 * U * cap, "logprobs")
+    within(out.top_logprobs, lp.gather(1, out.top_tokens), (err + 12 * U * cap)[:, None], "top_logprobs")
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_bad_hidden_row(value):
     h, w, t = make(100, 800, 64, BF, seed=24)

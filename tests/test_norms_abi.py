@@ -1,6 +1,9 @@
-"""Host-side rules of the norms around a block (no GPU): what is refused and with which status."""
+"""Host-side rules of the norms around a block (no GPU): what is refused and with which status, and the validation of
+these and of the log probabilities under sanitizers."""
 import ctypes
 import os
+import shutil
+import subprocess
 
 import pytest
 
@@ -139,3 +142,20 @@ def test_rows_of_tensors_on_the_host_are_refused():
         pack((3,), ("x",), 0)
     with pytest.raises(TypeError, match="dtype"):
         pack((torch.ones(3, dtype=torch.float16),), ("x",), 0)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_validation_under_asan_ubsan(tmp_path):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = tmp_path / "model_validate_fuzz"
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+           f"-I{root}/include", f"-I{root}/muon_newton_schulz_update_amd/csrc",
+           f"{root}/tests/native/model_validate_fuzz.cpp", f"{root}/muon_newton_schulz_update_amd/csrc/validate.cpp",
+           "-o", str(exe)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0 and "sanitizer" in (r.stderr or "").lower() and "cannot find" in r.stderr:
+        pytest.skip("sanitizer runtime not installed")
+    assert r.returncode == 0, r.stderr[-2000:]
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, (run.stdout[-2000:], run.stderr[-4000:])
+    assert run.stdout.splitlines()[-1].startswith("ok "), run.stdout

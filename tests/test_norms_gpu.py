@@ -332,6 +332,19 @@ def test_gradient_of_autograd_and_by_differences():
         assert not mu.rms_norm(x, kw["pre_gain"]).requires_grad
 
 
+def test_first_norm_of_a_32_bit_residual_for_16_bit_blocks():
+    x, gain = (3 * normal((70, 300), 41)).requires_grad_(), (1 + 0.3 * normal((300,), 42)).to(BF).requires_grad_()
+    h = mu.rms_norm(x, gain, dtype=BF)
+    dh = normal((70, 300), 43).to(BF)
+    dx, dgain = torch.autograd.grad(h, [x, gain], dh)
+    want = oracle(x.detach(), None, None, None, None, gain.detach(), False, True, 1e-6, dhidden=dh, like=BF)
+    assert h.dtype == BF and dx.dtype == F32 and dgain.dtype == BF
+    for name, t in (("hidden", h), ("dx", dx), ("dpre_gain", dgain)):
+        within(t, *want[name], name)
+    explicit = mu.rms_norm_grad(x.detach(), dh, gain.detach())
+    assert torch.equal(explicit[0], dx) and torch.equal(explicit[1], dgain)
+
+
 def test_repeats_bit_for_bit_and_on_another_stream():
     x, y, kw = tensors(3000, 768, BF, BF, seed=25)
     first = (*mu.residual_norm(x, y, **kw), *mu.residual_norm_grad(x, y, x, y, **kw))
