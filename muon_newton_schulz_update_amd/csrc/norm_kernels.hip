@@ -27,15 +27,18 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 // A thread's chunk of CH (4 or 8) channels from c of a row of d as they are in
-// memory, zero past its end; one or two loads where whole, aligned or not.
+// memory, zero past its end; one or two loads where whole, aligned or not. TAIL:
+// whether a row can end inside a chunk.
 template <typename T, int CH>
 struct Raw {
   uint32_t w[CH * sizeof(T) / 4];
 };
-template <typename T, int CH>
+template <bool TAIL, typename T, int CH>
 __device__ __forceinline__ void load_raw(const T* row, int c, int d, Raw<T, CH>& v) {
   if (c + CH <= d) {
     __builtin_memcpy(&v, row + c, sizeof(v));
+  } else if (!TAIL) {
+    v = {};
   } else {
     T x[CH];
 #pragma unroll
@@ -51,13 +54,13 @@ __device__ __forceinline__ void unpack(const Raw<T, CH>& r, float (&v)[CH]) {
     else v[e] = __uint_as_float(r.w[e]);
   }
 }
-template <int CH, typename T>
+template <bool TAIL, int CH, typename T>
 __device__ __forceinline__ void load_chunk(const T* row, int c, int d, float (&v)[CH]) {
   Raw<T, CH> r;
-  load_raw(row, c, d, r);
+  load_raw<TAIL>(row, c, d, r);
   unpack(r, v);
 }
-template <int CH, typename T>
+template <bool TAIL, int CH, typename T>
 __device__ __forceinline__ void store_chunk(T* row, int c, int d, const float (&v)[CH]) {
   if (c + CH <= d) {
     Raw<T, CH> r;
@@ -67,7 +70,7 @@ __device__ __forceinline__ void store_chunk(T* row, int c, int d, const float (&
       else r.w[e] = __float_as_uint(v[e]);
     }
     __builtin_memcpy(row + c, &r, sizeof(r));
-  } else {
+  } else if (TAIL) {
 #pragma unroll
     for (int e = 0; e < CH; ++e)
       if (c + e < d) {
@@ -81,11 +84,11 @@ __device__ __forceinline__ float one_value(const NormParam& p, int64_t i) {
   return p.half ? bf2f(((const u16*)p.ptr)[i]) : ((const float*)p.ptr)[i];
 }
 // A parameter's chunk (1 where it is not there; NORM_FULL is the rows').
-template <int CH>
+template <bool TAIL, int CH>
 __device__ __forceinline__ void load_param(const NormParam& p, int c, int d, float (&v)[CH]) {
   if (p.kind == NORM_CHANNELS) {
-    if (p.half) load_chunk((const u16*)p.ptr, c, d, v);
-    else load_chunk((const float*)p.ptr, c, d, v);
+    if (p.half) load_chunk<TAIL>((const u16*)p.ptr, c, d, v);
+    else load_chunk<TAIL>((const float*)p.ptr, c, d, v);
   } else {
     const float x = p.kind == NORM_ONE ? one_value(p, 0) : 1.f;
 #pragma unroll
@@ -117,8 +120,9 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float* sh) {
 }
 
 // A row's operands, loaded together and, where the registers hold two, one row
-// ahead of their use. GENERAL, here and below: with a gate for each element, or a
-// scale for each channel.
+// ahead of their use. GENERAL, here and below: with a gate for each element, a scale
+// for each channel, or a row that ends inside a chunk (kept apart for the
+// registers that these take).
 template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL, bool BACKWARD>
 struct Row {
   Raw<TX, CH> x[NC], dout[BACKWARD ? NC : 1];
@@ -127,11 +131,11 @@ struct Row {
     auto rows = [&](auto& to, const void* p, int64_t ld, auto type) {
       typedef decltype(type) T;
 #pragma unroll
-      for (int k = 0; k < NC; ++k) load_raw((const T*)p + r * ld, CH * (k * TPR + t), a.d, to[k]);
+      for (int k = 0; k < NC; ++k) load_raw<GENERAL>((const T*)p + r * ld, CH * (k * TPR + t), a.d, to[k]);
     };
     rows(x, a.x.ptr, a.x.ld, TX());
     if (a.y.ptr) rows(y, a.y.ptr, a.y.ld, TY());
-    if constexpr (BACKWARD) {
+    if constexpr (BACKWARD && !(TPR == 1024 && (NC > 1 || GENERAL))) {
       if (a.dhidden.ptr) rows(dhidden, a.dhidden.ptr, a.dhidden.ld, TY());
       if (a.dout.ptr) rows(dout, a.dout.ptr, a.dout.ld, TX());
     }
@@ -148,6 +152,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
   constexpr bool AHEAD = NC * CH <= 12 || TPR <= 64;
   __shared__ float sh[2][BLOCK / 64];
   const int t = threadIdx.x % TPR, d = a.d;
+  const float inv_d = 1.f / d;
   const int64_t step = (int64_t)gridDim.x * ROWS;
   // (every thread of a block goes round as often; rows past the last one are
   // the last one again and are not stored)
@@ -161,10 +166,10 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
   for (int k = 0; k < NC; ++k) {
     const int c = CH * (k * TPR + t);
     float post[CH];
-    if (GENERAL) load_param(a.scale, c, d, scale[GENERAL ? k : 0]);
-    load_param(a.pre_gain, c, d, pre[k]);
-    load_param(a.post_gain, c, d, post);
-    load_param(a.gate, c, d, gate[k]);
+    if (GENERAL) load_param<GENERAL>(a.scale, c, d, scale[GENERAL ? k : 0]);
+    load_param<GENERAL>(a.pre_gain, c, d, pre[k]);
+    load_param<GENERAL>(a.post_gain, c, d, post);
+    load_param<GENERAL>(a.gate, c, d, gate[k]);
 #pragma unroll
     for (int e = 0; e < CH; ++e) gate[k][e] *= post[e];
   }
@@ -180,8 +185,9 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       unpack(now.x[k], x[k]);
+      if (a.scale.ptr)
 #pragma unroll
-      for (int e = 0; e < CH; ++e) x[k][e] *= GENERAL ? scale[GENERAL ? k : 0][e] : scale1;
+        for (int e = 0; e < CH; ++e) x[k][e] *= GENERAL ? scale[GENERAL ? k : 0][e] : scale1;
     }
     if (there) {
       float y[NC][CH], r1 = 1.f;
@@ -193,7 +199,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
 #pragma unroll
           for (int e = 0; e < CH; ++e) s[0] = fmaf(y[k][e], y[k][e], s[0]);
         row_sums<TPR>(s, sh[0]);
-        r1 = 1.f / sqrtf(s[0] / d + a.eps);
+        r1 = rsqrtf(fmaf(s[0], inv_d, a.eps));
       }
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
@@ -209,7 +215,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
     }
     if (a.out.ptr && real)
 #pragma unroll
-      for (int k = 0; k < NC; ++k) store_chunk((TX*)a.out.ptr + row * a.out.ld, CH * (k * TPR + t), d, x[k]);
+      for (int k = 0; k < NC; ++k) store_chunk<GENERAL>((TX*)a.out.ptr + row * a.out.ld, CH * (k * TPR + t), d, x[k]);
     if (a.pre) {
       s[0] = 0.f;
 #pragma unroll
@@ -217,28 +223,35 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < CH; ++e) s[0] = fmaf(x[k][e], x[k][e], s[0]);
       row_sums<TPR>(s, sh[1]);
-      const float r2 = 1.f / sqrtf(s[0] / d + a.eps);
+      const float r2 = rsqrtf(fmaf(s[0], inv_d, a.eps));
       if (real)
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
 #pragma unroll
           for (int e = 0; e < CH; ++e) x[k][e] *= r2 * pre[k][e];
-          store_chunk((TY*)a.hidden.ptr + row * a.hidden.ld, CH * (k * TPR + t), d, x[k]);
+          store_chunk<GENERAL>((TY*)a.hidden.ptr + row * a.hidden.ld, CH * (k * TPR + t), d, x[k]);
         }
     }
     if (TPR > 64 && r0 + step < a.n) __syncthreads();   // the sums are read before the next row's are written
   }
 }
 
+// Waves to a SIMD that the backward pass is compiled for, where rows have several
+// waves: as many as the registers hold (a second raw row of 32-bit operands takes
+// twice as many), and four where a block alone has eight.
+constexpr int waves_wanted(int tpr, int nc, bool general, int bytes) {
+  return tpr <= 64 || nc > 1 || general ? 1 : bytes == 2 || tpr > 256 ? 4 : 3;
+}
 template <typename TX, typename TY, int TPR, int NC, int CH, int BLOCK, bool GENERAL>
-__global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
+__global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) void k_residual_norm_grad(NormArgs a) {
   constexpr int ROWS = BLOCK / TPR;
-  // what the registers hold: a second row, and the parameters (read again for
-  // each row otherwise)
-  constexpr bool WIDE = TPR == 1024, AHEAD = !WIDE && !(GENERAL && NC * CH > 12);
+  // what the registers hold: a second row, and the parameters (wide rows read these
+  // and the results' gradients again where they are needed)
+  constexpr bool WIDE = TPR == 1024 && (NC > 1 || GENERAL), AHEAD = !WIDE;
   __shared__ float sh[4][2 * (BLOCK / 64)];
   __shared__ float joined[ROWS > 1 ? BLOCK * CH : 1];
   const int t = threadIdx.x % TPR, d = a.d;
+  const float inv_d = 1.f / d;
   const bool there = a.y.ptr != nullptr, full = GENERAL && a.gate.kind == NORM_FULL, normed = a.dhidden.ptr != nullptr;
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
@@ -248,8 +261,8 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
   auto load_gated = [&](int k, float (&v)[CH]) {
     const int c = CH * (k * TPR + t);
     float post[CH];
-    load_param(a.post_gain, c, d, post);
-    load_param(a.gate, c, d, v);
+    load_param<GENERAL>(a.post_gain, c, d, post);
+    load_param<GENERAL>(a.gate, c, d, v);
 #pragma unroll
     for (int e = 0; e < CH; ++e) v[e] *= post[e];
   };
@@ -257,9 +270,9 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
   const float scale1 = a.scale.kind == NORM_ONE ? one_value(a.scale, 0) : 1.f;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    if (GENERAL) load_param(a.scale, CH * (k * TPR + t), d, scale[GENERAL ? k : 0]);
+    if (GENERAL) load_param<GENERAL>(a.scale, CH * (k * TPR + t), d, scale[GENERAL ? k : 0]);
     if (!WIDE) {
-      load_param(a.pre_gain, CH * (k * TPR + t), d, pre[WIDE ? 0 : k]);
+      load_param<GENERAL>(a.pre_gain, CH * (k * TPR + t), d, pre[WIDE ? 0 : k]);
       load_gated(k, gated[WIDE ? 0 : k]);
     }
   }
@@ -268,7 +281,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
     return gated[WIDE ? 0 : k];
   };
   auto pre_of = [&](int k) -> float (&)[CH] {
-    if (WIDE) load_param(a.pre_gain, CH * (k * TPR + t), d, pre[0]);
+    if (WIDE) load_param<GENERAL>(a.pre_gain, CH * (k * TPR + t), d, pre[0]);
     return pre[WIDE ? 0 : k];
   };
   auto scale_of = [&](int k, int e) { return GENERAL ? scale[GENERAL ? k : 0][e] : scale1; };
@@ -287,6 +300,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
     } else {
       now.load(a, min(row, a.n - 1), t);
     }
+    const int64_t at = min(row, a.n - 1);
     // y becomes yhat, o the row's out
     float y[NC][CH], o[NC][CH], r1 = 1.f;
     if (there) {
@@ -299,7 +313,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
 #pragma unroll
           for (int e = 0; e < CH; ++e) q[0] = fmaf(y[k][e], y[k][e], q[0]);
         row_sums<TPR>(q, sh[0]);
-        r1 = 1.f / sqrtf(q[0] / d + a.eps);
+        r1 = rsqrtf(fmaf(q[0], inv_d, a.eps));
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
@@ -309,8 +323,9 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       unpack(now.x[k], o[k]);
+      if (a.scale.ptr)
 #pragma unroll
-      for (int e = 0; e < CH; ++e) o[k][e] *= scale_of(k, e);
+        for (int e = 0; e < CH; ++e) o[k][e] *= scale_of(k, e);
       if (there) {
         float g[CH];
         if (full) unpack(now.g[GENERAL ? k : 0], g);
@@ -325,7 +340,8 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         float u[CH];
-        unpack(now.dhidden[k], u);
+        if (WIDE) load_raw<GENERAL>((const TY*)a.dhidden.ptr + at * a.dhidden.ld, CH * (k * TPR + t), d, now.dhidden[0]);
+        unpack(now.dhidden[WIDE ? 0 : k], u);
         const float (&w)[CH] = pre_of(k);
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
@@ -334,8 +350,8 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
         }
       }
       row_sums<TPR>(s, sh[1]);
-      r2 = 1.f / sqrtf(s[0] / d + a.eps);
-      m = s[1] * r2 / d;
+      r2 = rsqrtf(fmaf(s[0], inv_d, a.eps));
+      m = s[1] * r2 * inv_d;
     }
     // o becomes dT, then what comes to yhat
     float v[1] = {0.f};
@@ -344,14 +360,16 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
       const int c = CH * (k * TPR + t);
       float dt[CH], x[CH];
       if (a.dout.ptr) {
-        unpack(now.dout[k], dt);
+        if (WIDE) load_raw<GENERAL>((const TX*)a.dout.ptr + at * a.dout.ld, c, d, now.dout[0]);
+        unpack(now.dout[WIDE ? 0 : k], dt);
       } else {
 #pragma unroll
         for (int e = 0; e < CH; ++e) dt[e] = 0.f;
       }
       if (normed) {
         float u[CH];
-        unpack(now.dhidden[k], u);
+        if (WIDE) load_raw<GENERAL>((const TY*)a.dhidden.ptr + at * a.dhidden.ld, CH * (k * TPR + t), d, now.dhidden[0]);
+        unpack(now.dhidden[WIDE ? 0 : k], u);
         const float (&w)[CH] = pre_of(k);
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
@@ -363,8 +381,8 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
       if (a.dx.ptr && real) {
         float q[CH];
 #pragma unroll
-        for (int e = 0; e < CH; ++e) q[e] = dt[e] * scale_of(k, e);
-        store_chunk((TX*)a.dx.ptr + row * a.dx.ld, c, d, q);
+        for (int e = 0; e < CH; ++e) q[e] = a.scale.ptr ? dt[e] * scale_of(k, e) : dt[e];
+        store_chunk<GENERAL>((TX*)a.dx.ptr + row * a.dx.ld, c, d, q);
       }
       if ((a.want & (kWantScale | kWantScaleOne)) && real) {
         unpack(now.x[k], x);
@@ -382,7 +400,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
           float q[CH];
 #pragma unroll
           for (int e = 0; e < CH; ++e) q[e] = dt[e] * w[e] * y[k][e];
-          store_chunk((TY*)a.dfull.ptr + row * a.dfull.ld, c, d, q);
+          store_chunk<GENERAL>((TY*)a.dfull.ptr + row * a.dfull.ld, c, d, q);
         }
         if (vector && real) {
 #pragma unroll
@@ -402,7 +420,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
 #pragma unroll
           for (int e = 0; e < CH; ++e) v[0] = fmaf(o[k][e], y[k][e], v[0]);
         row_sums<TPR>(v, sh[2]);
-        const float back = v[0] / d;
+        const float back = v[0] * inv_d;
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
@@ -410,7 +428,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
       }
       if (real)
 #pragma unroll
-        for (int k = 0; k < NC; ++k) store_chunk((TY*)a.dy.ptr + row * a.dy.ld, CH * (k * TPR + t), d, o[k]);
+        for (int k = 0; k < NC; ++k) store_chunk<GENERAL>((TY*)a.dy.ptr + row * a.dy.ld, CH * (k * TPR + t), d, o[k]);
     }
     if (TPR > 64) __syncthreads();   // the sums are read before the next row's are written
   }
@@ -450,7 +468,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm_grad(NormArgs a) {
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         float post[CH];
-        load_param(a.post_gain, CH * (k * TPR + t), d, post);
+        load_param<GENERAL>(a.post_gain, CH * (k * TPR + t), d, post);
 #pragma unroll
         for (int e = 0; e < CH; ++e) gate_one = fmaf(post[e], sum_block[k][e], gate_one);
       }
@@ -489,9 +507,15 @@ __global__ __launch_bounds__(1024) void k_norm_sums(NormSums a) {
   if (bit <= kWantPre) {
     float x = 0.f;
     if (c < a.d) {
+      // (loads past the last partial left out one by one: a loop for the rest would wait for each)
       const float* p = a.part + (int64_t)blockIdx.y * a.dp + c;
-#pragma unroll 8
-      for (int b = share; b < a.blocks; b += 32) x += p[b * a.part_floats];
+      for (int b0 = share; b0 < a.blocks; b0 += 32 * 12) {
+        float v[12];
+#pragma unroll
+        for (int k = 0; k < 12; ++k) v[k] = b0 + 32 * k < a.blocks ? p[(b0 + 32 * k) * a.part_floats] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 12; ++k) x += v[k];
+      }
     }
     sh[share][lane] = x;
     __syncthreads();
@@ -526,27 +550,32 @@ __global__ __launch_bounds__(1024) void k_norm_sums(NormSums a) {
 }  // namespace
 
 // By the width, RUN(threads to a row, chunks to a thread, channels of a chunk):
-// sixteen threads up to 128 channels, a wave up to 1024, then as many threads as
-// there are chunks. (Up to 768: three chunks of 4 rather than two of 8, a
-// quarter of whose lanes would have nothing.)
-#define BY_WIDTH(d, RUN)                                  \
+// sixteen threads up to 128 channels, a wave up to 512, then as many threads as
+// there are chunks. Up to 768 a wave takes three chunks of 4 (two of 8 would leave
+// a quarter of its lanes nothing), but for the forward pass of 16-bit rows two
+// waves are faster, most for few rows (one row of 768: 3.2 / 4.0 us, 8192: 11.1 /
+// 12.2; of 32 bits 17.2 / 15.7; backward 8192 x 768 the same within 2 %, of 32 bits
+// 42 / 30).
+#define BY_WIDTH(d, RUN, RUN_768)                         \
   do {                                                    \
     if ((d) <= 128) RUN(16, 1, 8);                        \
     else if ((d) <= 512) RUN(64, 1, 8);                   \
-    else if ((d) <= 768) RUN(64, 3, 4);                   \
-    else if ((d) <= 1024) RUN(64, 2, 8);                  \
+    else if ((d) <= 768) RUN_768;                         \
+    else if ((d) <= 1024) RUN(128, 1, 8);                 \
+    else if ((d) <= 1536) RUN(192, 1, 8);                 \
     else if ((d) <= 2048) RUN(256, 1, 8);                 \
     else if ((d) <= 4096) RUN(512, 1, 8);                 \
-    else if ((d) <= 8192) RUN(512, 2, 8);                 \
+    else if ((d) <= 8192) RUN(1024, 1, 8);                \
     else RUN(1024, 2, 8);                                 \
   } while (0)
 
 namespace {
 
-constexpr int at_least(int a, int b) { return a > b ? a : b; }
+// A block of whole rows, of about so many threads.
+constexpr int whole_rows(int threads, int about) { return about > threads ? about / threads * threads : threads; }
 // Threads of a block: one row where that has a wave or more; several rows in the
 // backward pass, whose blocks leave a partial each.
-constexpr int kForwardBlock = 64, kBackwardBlock = 256;
+constexpr int kForwardBlock = 64, kBackwardBlock = 512;
 
 // Blocks of a kernel that the device holds at once.
 template <typename K>
@@ -563,11 +592,13 @@ int blocks_of(int64_t n, int rows, int resident) {
   const int64_t blocks = (n + rows - 1) / rows, rounds = (blocks + resident - 1) / resident;
   return (int)((blocks + rounds - 1) / rounds);
 }
-bool general(const NormArgs& a) { return a.gate.kind == NORM_FULL || a.scale.kind == NORM_CHANNELS; }
+bool general(const NormArgs& a, int chunk) {
+  return a.gate.kind == NORM_FULL || a.scale.kind == NORM_CHANNELS || a.d % chunk != 0;
+}
 
 template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL>
 void forward(const NormArgs& a, hipStream_t s) {
-  constexpr int BLOCK = at_least(TPR, kForwardBlock);
+  constexpr int BLOCK = whole_rows(TPR, kForwardBlock);
   static const int most = resident(k_residual_norm<TX, TY, TPR, NC, CH, BLOCK, GENERAL>, BLOCK);
   const dim3 g((unsigned)blocks_of(a.n, BLOCK / TPR, most));
   hipLaunchKernelGGL((k_residual_norm<TX, TY, TPR, NC, CH, BLOCK, GENERAL>), g, dim3(BLOCK), 0, s, a);
@@ -575,7 +606,7 @@ void forward(const NormArgs& a, hipStream_t s) {
 // blocks alone, or the launch
 template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL>
 int backward(const NormArgs& a, bool launch, hipStream_t s) {
-  constexpr int BLOCK = at_least(TPR, kBackwardBlock);
+  constexpr int BLOCK = whole_rows(TPR, kBackwardBlock);
   static const int most = resident(k_residual_norm_grad<TX, TY, TPR, NC, CH, BLOCK, GENERAL>, BLOCK);
   const int blocks = blocks_of(a.n, BLOCK / TPR, most < kNormMostBlocks ? most : kNormMostBlocks);
   if (launch) hipLaunchKernelGGL((k_residual_norm_grad<TX, TY, TPR, NC, CH, BLOCK, GENERAL>), dim3(blocks), dim3(BLOCK), 0, s, a);
@@ -584,7 +615,7 @@ int backward(const NormArgs& a, bool launch, hipStream_t s) {
 
 #define BY_TYPES(f, TPR, NC, CH, ...)                                                    \
   do {                                                                                   \
-    const bool g = general(a);                                                           \
+    const bool g = general(a, CH);                                                          \
     if (x_half) f##_of<u16, u16, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);                    \
     else if (y_half) f##_of<float, u16, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);             \
     else f##_of<float, float, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);                       \
@@ -605,7 +636,13 @@ void backward_of(bool g, const NormArgs& a, int* blocks, hipStream_t s) {
 
 hipError_t launch_residual_norm(const NormArgs& a, int x_half, int y_half, hipStream_t s) {
 #define FORWARD(TPR, NC, CH) BY_TYPES(forward, TPR, NC, CH)
-  BY_WIDTH(a.d, FORWARD);
+#define FORWARD_768                   \
+  do {                                \
+    if (x_half) FORWARD(128, 1, 8);   \
+    else FORWARD(64, 3, 4);           \
+  } while (0)
+  BY_WIDTH(a.d, FORWARD, FORWARD_768);
+#undef FORWARD_768
 #undef FORWARD
   return hipGetLastError();
 }
@@ -614,7 +651,7 @@ int norm_grad_blocks(const NormArgs& a, int x_half, int y_half) {
   int blocks[2] = {0, 1};      // (1: no launch)
   hipStream_t s = nullptr;
 #define BLOCKS(TPR, NC, CH) BY_TYPES(backward, TPR, NC, CH, blocks)
-  BY_WIDTH(a.d, BLOCKS);
+  BY_WIDTH(a.d, BLOCKS, BLOCKS(64, 3, 4));
 #undef BLOCKS
   return blocks[0];
 }
@@ -622,7 +659,7 @@ int norm_grad_blocks(const NormArgs& a, int x_half, int y_half) {
 hipError_t launch_residual_norm_grad(const NormArgs& a, int x_half, int y_half, hipStream_t s) {
   int blocks[2] = {0, 0};
 #define BACKWARD(TPR, NC, CH) BY_TYPES(backward, TPR, NC, CH, blocks)
-  BY_WIDTH(a.d, BACKWARD);
+  BY_WIDTH(a.d, BACKWARD, BACKWARD(64, 3, 4));
 #undef BACKWARD
   return hipGetLastError();
 }
