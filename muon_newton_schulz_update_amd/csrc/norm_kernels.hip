@@ -245,9 +245,10 @@ constexpr int waves_wanted(int tpr, int nc, bool general, int bytes) {
 template <typename TX, typename TY, int TPR, int NC, int CH, int BLOCK, bool GENERAL>
 __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) void k_residual_norm_grad(NormArgs a) {
   constexpr int ROWS = BLOCK / TPR;
-  // what the registers hold: a second row, and the parameters (wide rows read these
-  // and the results' gradients again where they are needed)
-  constexpr bool WIDE = TPR == 1024 && (NC > 1 || GENERAL), AHEAD = !WIDE;
+  // what the registers hold: the parameters (wide rows read these and the results'
+  // gradients again where they are needed), and a second row (4096 x 4096 of 32
+  // bits, with / without 117 / 88 us: it does not fit beside eight waves)
+  constexpr bool WIDE = TPR == 1024 && (NC > 1 || GENERAL), AHEAD = !WIDE && !(TPR >= 512 && sizeof(TX) == 4);
   __shared__ float sh[4][2 * (BLOCK / 64)];
   __shared__ float joined[ROWS > 1 ? BLOCK * CH : 1];
   const int t = threadIdx.x % TPR, d = a.d;
@@ -555,8 +556,10 @@ __global__ __launch_bounds__(1024) void k_norm_sums(NormSums a) {
 // a quarter of its lanes nothing), but for the forward pass of 16-bit rows two
 // waves are faster, most for few rows (one row of 768: 3.2 / 4.0 us, 8192: 11.1 /
 // 12.2; of 32 bits 17.2 / 15.7; backward 8192 x 768 the same within 2 %, of 32 bits
-// 42 / 30).
-#define BY_WIDTH(d, RUN, RUN_768)                         \
+// 42 / 30). Up to 8192 the backward pass has the registers of eight waves for two
+// chunks a thread, the forward one of sixteen for one (2048 x 8192: backward 43 / 56
+// us, forward 23.5 / 22.5).
+#define BY_WIDTH(d, RUN, RUN_768, RUN_8192)               \
   do {                                                    \
     if ((d) <= 128) RUN(16, 1, 8);                        \
     else if ((d) <= 512) RUN(64, 1, 8);                   \
@@ -565,7 +568,7 @@ __global__ __launch_bounds__(1024) void k_norm_sums(NormSums a) {
     else if ((d) <= 1536) RUN(192, 1, 8);                 \
     else if ((d) <= 2048) RUN(256, 1, 8);                 \
     else if ((d) <= 4096) RUN(512, 1, 8);                 \
-    else if ((d) <= 8192) RUN(1024, 1, 8);                \
+    else if ((d) <= 8192) RUN_8192;                       \
     else RUN(1024, 2, 8);                                 \
   } while (0)
 
@@ -641,7 +644,7 @@ hipError_t launch_residual_norm(const NormArgs& a, int x_half, int y_half, hipSt
     if (x_half) FORWARD(128, 1, 8);   \
     else FORWARD(64, 3, 4);           \
   } while (0)
-  BY_WIDTH(a.d, FORWARD, FORWARD_768);
+  BY_WIDTH(a.d, FORWARD, FORWARD_768, FORWARD(1024, 1, 8));
 #undef FORWARD_768
 #undef FORWARD
   return hipGetLastError();
@@ -651,7 +654,7 @@ int norm_grad_blocks(const NormArgs& a, int x_half, int y_half) {
   int blocks[2] = {0, 1};      // (1: no launch)
   hipStream_t s = nullptr;
 #define BLOCKS(TPR, NC, CH) BY_TYPES(backward, TPR, NC, CH, blocks)
-  BY_WIDTH(a.d, BLOCKS, BLOCKS(64, 3, 4));
+  BY_WIDTH(a.d, BLOCKS, BLOCKS(64, 3, 4), BLOCKS(512, 2, 8));
 #undef BLOCKS
   return blocks[0];
 }
@@ -659,7 +662,7 @@ int norm_grad_blocks(const NormArgs& a, int x_half, int y_half) {
 hipError_t launch_residual_norm_grad(const NormArgs& a, int x_half, int y_half, hipStream_t s) {
   int blocks[2] = {0, 0};
 #define BACKWARD(TPR, NC, CH) BY_TYPES(backward, TPR, NC, CH, blocks)
-  BY_WIDTH(a.d, BACKWARD, BACKWARD(64, 3, 4));
+  BY_WIDTH(a.d, BACKWARD, BACKWARD(64, 3, 4), BACKWARD(512, 2, 8));
 #undef BACKWARD
   return hipGetLastError();
 }
