@@ -173,6 +173,19 @@ __device__ __forceinline__ void pack_weight(const HeadArgs& a, int r0) {
   }
 }
 
+// What the gradient of a token's log probability and entropy takes of it: dz =
+// p (b + g log2 p) with g the entropy's gradient times -log(2) and b = -(g_logprob +
+// g_entropy H); the target's is g_logprob (1 - p) - g_entropy p (log p + H), with
+// 1 - p from log p, which keeps what a token that is nearly sure still has to learn.
+__device__ __forceinline__ void logprob_factors(const HeadArgs& a, int r, int token) {
+  const int tg = checked_target(a, target_at(a.targets, a.target_bytes, token));
+  const float4 s = a.stats_in[token];
+  const float gp = tg >= 0 && a.grad_logprobs ? a.grad_logprobs[token] : 0.f, ge = a.grad_entropy ? a.grad_entropy[token] : 0.f;
+  const float lp = __builtin_elementwise_maximum(s.w, -126.f / kLog2e);   // (as the other words': no infinity times 0)
+  a.ts[r] = float4{s.x, -s.y * kLog2e, -fmaf(ge, s.z, gp), -ge * kLn2};
+  a.rs[r] = float4{0.f, 0.f, tg >= 0 ? -gp * expm1f(lp) - ge * expf(lp) * (lp + s.z) : 0.f, 0.f};
+}
+
 // Gathered rows to panels: a wave takes 8 rows x 8 chunks at a time, so that
 // it reads and writes whole 128-byte lines; rows past the valid ones, up to a
 // whole panel (a stage of dW), become zero. One block per 64 rows and 8 chunks.
@@ -212,6 +225,8 @@ __global__ __launch_bounds__(256) void k_pack(HeadArgs a, int scan, int row_bloc
   }
   if (r0 >= rows) return;
   __syncthreads();
+  if (a.ts && blockIdx.y == 0 && threadIdx.x < kPanelRows && r0 + (int)threadIdx.x < rows)
+    logprob_factors(a, r0 + threadIdx.x, list[threadIdx.x]);
   const int lane = threadIdx.x & 63, ch = blockIdx.y * 8 + (lane & 7), c = ch * CH;
   uint8_t* dst = (uint8_t*)a.hp + (((int64_t)blockIdx.x * (a.dp / CH) + ch) << 10);
 #pragma unroll

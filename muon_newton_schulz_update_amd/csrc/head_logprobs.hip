@@ -16,13 +16,8 @@
 //                 16-bit inputs every product is exact) and sorted. What is
 //                 outside the spare sets could only be in front by an error
 //                 of the 32-bit sums that passes over kSpare others.
-//   factors       for the gradient, dz = p (b + g log2 p) with g the entropy's
-//                 gradient times -log(2) and b = -(g_logprob + g_entropy H); the
-//                 target's is g_logprob (1 - p) - g_entropy p (log p + H)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-
-#include <type_traits>
 
 #include "head_device.hpp"
 #include "train.hpp"
@@ -34,7 +29,6 @@ namespace {
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kSpare = 8;          // candidates beyond the asked-for alternatives
-constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNan = __builtin_nanf("");
 
 // exp(x - y) with its exponent, base 2; no smaller than what a product with it
@@ -146,40 +140,43 @@ __device__ __forceinline__ void merge_wave(Ranked<F>& x, const Ranked<F>& sorted
   for (int mask = 32; mask; mask /= 2) keep_order(x, lane, mask, true);
 }
 
-// Logits of a token and G words in 64 bits, the wave's lanes over the width.
-template <int G, typename T>
-__device__ __forceinline__ void fine_logits(const T* h, const T* w, int64_t ld, int d, const int (&words)[G], int lane,
-                                            double (&z)[G]) {
+// Logits of a token and kGroup words in 64 bits, the wave's lanes over the width.
+// (Groups of 8 hold twice as many loads in flight, but fewer tokens fit a CU:
+// 3000 x top 20 x 2048 114 us, with 4 111; 1536 x top 5 38, 35.)
+constexpr int kGroup = 4;
+template <typename T>
+__device__ __forceinline__ void fine_logits(const T* h, const T* w, int64_t ld, int d, const int (&words)[kGroup], int lane,
+                                            double (&z)[kGroup]) {
   constexpr int CH = 16 / (int)sizeof(T);
   auto value = [](T x) -> double {
     if constexpr (sizeof(T) == 2) return (double)bf2f(x);
     else return (double)x;
   };
 #pragma unroll
-  for (int g = 0; g < G; ++g) z[g] = 0;
+  for (int g = 0; g < kGroup; ++g) z[g] = 0;
   for (int c = lane * CH; c < d; c += 64 * CH) {
-    T x[CH], y[G][CH];
+    T x[CH], y[kGroup][CH];
     if (c + CH <= d) {
       __builtin_memcpy(x, h + c, 16);
 #pragma unroll
-      for (int g = 0; g < G; ++g) __builtin_memcpy(y[g], w + words[g] * ld + c, 16);
+      for (int g = 0; g < kGroup; ++g) __builtin_memcpy(y[g], w + words[g] * ld + c, 16);
     } else {
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         x[e] = c + e < d ? h[c + e] : T(0);
 #pragma unroll
-        for (int g = 0; g < G; ++g) y[g][e] = c + e < d ? w[words[g] * ld + c + e] : T(0);
+        for (int g = 0; g < kGroup; ++g) y[g][e] = c + e < d ? w[words[g] * ld + c + e] : T(0);
       }
     }
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
       const double v = value(x[e]);
 #pragma unroll
-      for (int g = 0; g < G; ++g) z[g] = fma(v, value(y[g][e]), z[g]);
+      for (int g = 0; g < kGroup; ++g) z[g] = fma(v, value(y[g][e]), z[g]);
     }
   }
 #pragma unroll
-  for (int g = 0; g < G; ++g) z[g] = lanes_sum<64>(z[g]);
+  for (int g = 0; g < kGroup; ++g) z[g] = lanes_sum<64>(z[g]);
 }
 
 constexpr int kNoToken = 0x7FFFFFFF;
@@ -352,22 +349,17 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
   const int64_t ld = a.w_src ? a.ld_src : a.ld_w;
   // the first n lanes' words with their 64-bit logits, to which every wave sums a
   // group at a time
-  auto groups = [&](int words, int n, auto size) {
-    constexpr int G = decltype(size)::value;
-    for (int g0 = wave * G; g0 < n; g0 += kWaves * G) {
-      int of[G];
-      double z[G];
+  auto fine = [&](int words, int n) {
+    for (int g0 = wave * kGroup; g0 < n; g0 += kWaves * kGroup) {
+      int of[kGroup];
+      double z[kGroup];
 #pragma unroll
-      for (int g = 0; g < G; ++g) of[g] = __builtin_amdgcn_readlane(words, min(g0 + g, n - 1));
-      fine_logits<G>(h, w, ld, a.d, of, lane, z);
+      for (int g = 0; g < kGroup; ++g) of[g] = __builtin_amdgcn_readlane(words, min(g0 + g, n - 1));
+      fine_logits(h, w, ld, a.d, of, lane, z);
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int g = 0; g < kGroup; ++g)
         if (lane == g && g0 + g < n) sh.z[g0 + g] = z[g];
     }
-  };
-  auto fine = [&](int words, int n) {
-    if (n <= kWaves * 4) groups(words, n, std::integral_constant<int, 4>());
-    else groups(words, n, std::integral_constant<int, 8>());
     __syncthreads();
     return Ranked<double>{lane < n ? sh.z[lane] : -__builtin_inf(), lane < n ? words : kNoToken};
   };
@@ -468,18 +460,6 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(HeadArgs a, int blocks) {
   if (a.top) alternatives<T, SETS>(a, token, best, e, stat, wave, lane, sh);
 }
 
-__global__ __launch_bounds__(256) void k_logprob_factors(HeadArgs a) {
-  const int r = blockIdx.x * 256 + threadIdx.x;
-  if (r >= piece_rows(a)) return;
-  const int i = a.idx[a.row0 + r], tg = a.tgt[a.row0 + r];
-  const float4 s = a.stats_in[i];
-  const float gp = tg >= 0 && a.grad_logprobs ? a.grad_logprobs[i] : 0.f, ge = a.grad_entropy ? a.grad_entropy[i] : 0.f;
-  a.ts[r] = float4{s.x, -s.y * kLog2e, -fmaf(ge, s.z, gp), -ge * kLn2};
-  // (1 - p from log p, which keeps what a token that is nearly sure still has to learn)
-  const float lp = __builtin_elementwise_maximum(s.w, -126.f / kLog2e);   // (as the other words': no infinity times 0)
-  a.rs[r] = float4{0.f, 0.f, tg >= 0 ? -gp * expm1f(lp) - ge * expf(lp) * (lp + s.z) : 0.f, 0.f};
-}
-
 // Statistics alone: tokens of which a block each goes faster than a wave each.
 constexpr int kFewTokens = 512;
 inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
@@ -499,12 +479,6 @@ hipError_t launch_logprobs(const HeadArgs& a, int dt, hipStream_t s) {
   if (dt != MUON_BF16) hipLaunchKernelGGL((k_logprobs<float, 4>), g, b, 0, s, a, blocks);
   else if (a.sets == 4) hipLaunchKernelGGL((k_logprobs<u16, 4>), g, b, 0, s, a, blocks);
   else hipLaunchKernelGGL((k_logprobs<u16, 2>), g, b, 0, s, a, blocks);
-  return hipGetLastError();
-}
-
-hipError_t launch_logprob_factors(const HeadArgs& a, hipStream_t s) {
-  if (a.rows_max == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_logprob_factors, dim3(cdiv(a.rows_max, 256)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

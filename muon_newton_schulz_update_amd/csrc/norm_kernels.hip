@@ -40,9 +40,12 @@ __device__ __forceinline__ void load_raw(const T* row, int c, int d, Raw<T, CH>&
   } else if (!TAIL) {
     v = {};
   } else {
+    // (loads without a branch each, the row's last element past its end)
     T x[CH];
 #pragma unroll
-    for (int e = 0; e < CH; ++e) x[e] = c + e < d ? row[c + e] : T(0);
+    for (int e = 0; e < CH; ++e) x[e] = row[min(c + e, d - 1)];
+#pragma unroll
+    for (int e = 0; e < CH; ++e) x[e] = c + e < d ? x[e] : T(0);
     __builtin_memcpy(&v, x, sizeof(v));
   }
 }

@@ -175,7 +175,8 @@ struct HeadArgs {
   const float4* stats_in;             // the gradient's: what the forward call left,
   const float* grad_logprobs;         // and the results' gradients, or null
   const float* grad_entropy;
-  float4* ts;                         // piece: {reference, minus log2 of the sum over it, and dz's b and g (head_logprobs.hip)}
+  float4* ts;                         // piece: {reference, minus log2 of the sum over it, and dz's b and g (head_kernels.hip)},
+                                      // or null: not the gradient of log probabilities
 };
 
 // What the logits' launch leaves: statistics and, where kept, exponentials for
@@ -210,8 +211,7 @@ hipError_t launch_head_merge(const HeadArgs& a, int grad, hipStream_t s);
 hipError_t launch_head_dlogits(const HeadArgs& a, int dt, hipStream_t s);
 hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s);   // dh and dw, each if not null
 hipError_t launch_head_gradients_out(const HeadArgs& a, int dt, hipStream_t s);
-// head_logprobs.hip: after the logits' statistics, and before the logits' gradient
+// head_logprobs.hip: after the logits' statistics
 hipError_t launch_logprobs(const HeadArgs& a, int dt, hipStream_t s);
-hipError_t launch_logprob_factors(const HeadArgs& a, hipStream_t s);
 
 }  // namespace muon

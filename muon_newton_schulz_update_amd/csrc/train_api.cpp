@@ -234,7 +234,7 @@ muon_status head_run(muon_handle* h, const HeadCall& c) {
   a.rs = (float4*)(b + o_rs);
   a.tstat = (float4*)(b + o_tstat);
   a.best = (uint2*)(b + o_best);
-  a.ts = (float4*)(b + o_ts);
+  a.ts = c.mode == LOGITS_GRAD ? (float4*)(b + o_ts) : nullptr;
   if (c.mode == LOGITS_GRAD) a.loss = a.lossc;    // (zeros of the ignored tokens go there)
   a.e = b + o_e;
   a.part = (float*)(b + o_part);
@@ -255,7 +255,6 @@ muon_status head_run(muon_handle* h, const HeadCall& c) {
     a.first = k == 0;
     a.last = k + 1 == pieces;
     HIP_DO(h, launch_head_pack(a, dt, s));
-    if (c.mode == LOGITS_GRAD) HIP_DO(h, launch_logprob_factors(a, s));
     HIP_DO(h, launch_head_logits(a, dt, grad ? 1 : 0, c.mode, s));
     if (c.mode == LOGITS_STATS) {
       HIP_DO(h, launch_logprobs(a, dt, s));
