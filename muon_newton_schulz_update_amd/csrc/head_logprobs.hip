@@ -26,8 +26,6 @@
 namespace muon {
 namespace {
 
-typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
-
 constexpr int kSpare = 8;          // candidates beyond the asked-for alternatives
 constexpr float kNan = __builtin_nanf("");
 
@@ -338,7 +336,8 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
     return;
   }
   int count = candidate_sets<T, SETS>(a, best, e, wave, lane, sh);
-  const float bound = lane < count ? sh.sets[lane].bound : kNone;
+  // (no other of a set passes its second largest, nor its largest)
+  const float bound = lane < count ? fminf(sh.sets[lane].bound, sh.sets[lane].z) : kNone;
   int word = lane < count ? sh.sets[lane].word : kNoToken;
   if (target >= 0 && token.z > kNone) {          // (its set leaves it out)
     if (lane == count) word = target;
@@ -375,10 +374,17 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
   }
   __syncthreads();
   found = {lane < count ? sh.z[lane] : -__builtin_inf(), lane < count ? sh.word[lane] : kNoToken};
-  // sets that may have two of the alternatives: all of them (the last one's logit
-  // less a 32-bit sum's error; of an infinite one that is no number, and none is out)
-  const float last = (float)__shfl(found.z, top - 1), least = last - fabsf(last) * 0x1p-18f;
-  for (uint64_t todo = __ballot(bound > kNone && !(bound < least)); todo; todo &= todo - 1) {
+  // sets that may have two of the alternatives: all of them. Out is what is behind the
+  // last alternative by more than a 32-bit sum's error, or as large (no logit of a
+  // zero row or weight has an error) but of later words; more are out as the
+  // alternatives fill.
+  const double reach = (double)bound + fabs((double)bound) * 0x1p-18;
+  auto whole = [&]() {
+    const double last = __shfl(found.z, top - 1);                       // (every lane takes part)
+    const int last_word = __shfl(found.token, top - 1);
+    return __ballot(bound > kNone && !(reach < last || (reach == last && word > last_word)));
+  };
+  for (uint64_t todo = whole(); todo; todo = (todo & (todo - 1)) & whole()) {
     const int first = __builtin_amdgcn_readlane(word, __builtin_ctzll(todo));
     const int member = first / a.vtile * a.vtile + set_column<T, SETS>(column_set<T, SETS>(first % a.vtile), lane);
     const bool in = lane < kSetRows<T> / 2 && member < a.v && member != first && member != target;
