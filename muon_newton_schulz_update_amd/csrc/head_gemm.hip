@@ -1144,6 +1144,10 @@ int tile_of(int dt, int rows, int64_t tiles256, int64_t tiles128) {
   if (tiles256 >= kFewTiles && rows > kHalfTile) return 256;
   return tiles128 >= kFewSmallTiles ? 128 : 64;
 }
+// Statistics with entropy of one row of tokens: 64-tiles that all run at once, four
+// to a CU (one token x 50304 x 768: 64 / 128 16.6 / 18.1 us; the loss alone keeps
+// the order of its sums).
+constexpr int kAllSmallTiles = 1024;
 // The gradients' tiles also go by their own shape (whole calls):
 //   few tokens: dW's K is short, its tiles all start-up and epilogue, which two
 //   workgroups to a CU overlap (128 / 256: 300 tokens x 50304 x 2048 338 / 384
@@ -1228,9 +1232,10 @@ hipError_t launch_head_gradients(const HeadArgs& a, int dt, hipStream_t s) {
 // within 0.3 % (256), 1.1 % (128), 0.6 % (64) and 1.7 % (fp32) of the best
 // parts). dW's parts measured (1 / chosen): 16384 x 6000 x 256 350 / 324 us,
 // 65536 x 256 x 512 646 / 250, fp32 2000 x 300 x 128 78 / 37.
-void head_plan(HeadArgs& a, int dt) {
+void head_plan(HeadArgs& a, int dt, LogitsMode mode) {
   const int rows = a.n < a.piece ? a.n : a.piece, unit = dt == MUON_BF16 ? 64 : 32;
   a.logit_tile = tile_of(dt, rows, (int64_t)cdiv(a.v, 256) * cdiv(rows, 256), (int64_t)cdiv(a.v, 128) * cdiv(rows, 128));
+  if (mode == LOGITS_STATS && rows <= 64 && cdiv(a.v, 64) <= kAllSmallTiles) a.logit_tile = 64;
   a.vtile = a.logit_tile == 64 ? 64 : 128;
   a.n_vt = cdiv(a.v, a.vtile);
   a.sets = a.vtile / (dt == MUON_BF16 ? kSetRows<u16> : kSetRows<float>) * 2;

@@ -203,7 +203,7 @@ __host__ __device__ inline int column_set(int col) {
 
 // Picks the tile edges, the statistics' columns and the splits, from the sizes
 // and from which gradients are wanted (before the workspace is laid out).
-void head_plan(HeadArgs& a, int dt);
+void head_plan(HeadArgs& a, int dt, LogitsMode mode);
 hipError_t launch_head_compact(const HeadArgs& a, hipStream_t s);
 hipError_t launch_head_pack(const HeadArgs& a, int dt, hipStream_t s);
 hipError_t launch_head_logits(const HeadArgs& a, int dt, int keep, LogitsMode mode, hipStream_t s);

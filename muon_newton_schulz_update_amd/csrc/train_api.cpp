@@ -195,7 +195,7 @@ muon_status head_run(muon_handle* h, const HeadCall& c) {
       std::min(kPieceMost, std::max<int64_t>(kPieceRows, (int64_t)(kHeadBytes / row) / kPieceRows * kPieceRows));
   const int64_t pieces = std::max<int64_t>(1, cdiv(a.n, most));
   a.piece = (int)(std::max<int64_t>(1, cdiv(cdiv(a.n, pieces), kPieceRows)) * kPieceRows);
-  head_plan(a, dt);
+  head_plan(a, dt, c.mode);
   // few tokens without gradients, whose rows the products can load as they are:
   // no panels
   a.gather = !grad && direct && a.n > 0 && a.n <= kGatherTokens && a.logit_tile < 256 && (uintptr_t)hid.ptr % 16 == 0 &&
