@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import load_library
-from .training import _checked, _describe, _handle_for, _scalar
+from .training import _checked, _describe, _handle_for, _one_stream_a_leaf, _scalar
 
 
 class LogProbConfig(ctypes.Structure):
@@ -99,6 +99,7 @@ def linear_logprobs_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: to
 class _LinearLogProbs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, targets, top, softcap, ignore_index, handle):
+        _one_stream_a_leaf(ctx, hidden.get_device())
         out = _call(hidden, weight, targets, top, softcap, ignore_index, handle)
         ctx.options = (softcap, ignore_index, handle)
         ctx.save_for_backward(hidden, weight, targets, out[4])
@@ -133,7 +134,9 @@ def linear_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.T
     hidden: (..., D), targets: (...) int64 or int32, weight: (V, D). Tokens whose
     target is ignore_index have zeros, and -1 for their alternatives. logprobs and
     entropy are differentiable in hidden and weight, in reverse mode: the
-    backward pass takes the logits again (`linear_logprobs_grad`)."""
+    backward pass takes the logits again (`linear_logprobs_grad`). A graph that
+    captures it with its backward pass needs its leaves without eager results on
+    other streams; the gradient's own call has no such condition."""
     if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
         return LogProbs(*_LinearLogProbs.apply(hidden, weight, targets, top, softcap, ignore_index, handle))
     return LogProbs(*_call(hidden, weight, targets, top, softcap, ignore_index, handle))

@@ -16,7 +16,7 @@ from typing import NamedTuple
 import torch
 
 from . import MuonMatrix, load_library
-from .training import _checked, _describe, _handle_for
+from .training import _checked, _describe, _handle_for, _one_stream_a_leaf
 
 _SIZE = ctypes.sizeof(MuonMatrix)
 _NAMES = ("x", "y", "post_gain", "pre_gain", "gate", "scale", "dout", "dhidden")
@@ -54,8 +54,15 @@ def _same_shape(x, **others):
             raise ValueError(f"{name} of shape {tuple(t.shape)} beside x of {tuple(x.shape)}")
 
 
+def _check_shapes(x, y, gate, **others):
+    _same_shape(x, y=y, **others)
+    # (rows alone would take a gate whose leading dimensions are y's in another order)
+    if gate is not None and gate.dim() > 1 and gate.shape[:-1].numel() > 1 and gate.shape != x.shape:
+        raise ValueError(f"gate of shape {tuple(gate.shape)} beside y of {tuple(x.shape)}")
+
+
 def _forward(x, y, post_gain, gate, scale, pre_gain, post_norm, pre_norm, eps, dtype, handle):
-    _same_shape(x, y=y)
+    _check_shapes(x, y, gate)
     h = _handle_for((x,), handle)
     native = _describe()
     out = None if y is None else native.empty(h.device, x, x)
@@ -70,7 +77,7 @@ def _forward(x, y, post_gain, gate, scale, pre_gain, post_norm, pre_norm, eps, d
 
 
 def _backward(x, y, post_gain, gate, scale, pre_gain, post_norm, pre_norm, eps, dout, dhidden, wanted, handle):
-    _same_shape(x, y=y, dout=dout, dhidden=dhidden)
+    _check_shapes(x, y, gate, dout=dout, dhidden=dhidden)
     h = _handle_for((x,), handle)
     native = _describe()
     inputs = (x, y, post_gain, gate, scale, pre_gain)
@@ -87,6 +94,7 @@ class _ResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, post_gain, gate, scale, pre_gain, *options):
         post_norm, pre_norm, eps, dtype, handle = ctx.options = options
+        _one_stream_a_leaf(ctx, x.get_device())
         ctx.save_for_backward(x, y, post_gain, gate, scale, pre_gain)
         ctx.set_materialize_grads(False)
         return _forward(x, y, post_gain, gate, scale, pre_gain, post_norm, pre_norm, eps, dtype, handle)
@@ -137,7 +145,9 @@ def residual_norm(x: torch.Tensor, y: torch.Tensor, *, post_norm: bool = True, p
     or y itself without post_norm; hidden likewise from out with pre_gain, None
     without pre_norm. Gains: (D,). gate: one value, (D,), or y's shape and type.
     scale: one value or (D,). Differentiable in every tensor, in reverse mode; the
-    backward pass makes out again from x and y and keeps nothing else."""
+    backward pass makes out again from x and y and keeps nothing else. A graph that
+    captures it with its backward pass needs its leaves without eager results on
+    other streams; `residual_norm_grad` has no such condition."""
     args = (x, y, post_gain, gate, scale, pre_gain, post_norm, pre_norm, eps, None, handle)
     return (_ResidualNorm.apply if _differentiable(x, y, post_gain, gate, scale, pre_gain) else _forward)(*args)
 
