@@ -1,4 +1,4 @@
-// Matrix-core products of the head's cross entropy.
+// Matrix-core products of the head's cross entropy and log probabilities.
 //
 //   logits    z^T = W H^T       vocabulary x tokens, K = width
 //   dhidden   dH  = dz W        tokens x width,      K = vocabulary (in parts)
@@ -498,6 +498,13 @@ __device__ __forceinline__ void store_logits_grad(const HeadArgs& a, f32x16_t (&
 // (4.7 TB/s); fp32 1987 x 30961 x 704 680 (127).
 // Two workgroups of 256 x 128 to a CU, so that one's epilogue runs beside the
 // other's products, took 13 % longer (more operand traffic from LDS).
+//
+// LOGITS_STATS adds each tile's entropy to the statistics and, where alternatives
+// are asked for, each set's largest logits; LOGITS_GRAD, with a token's statistics
+// from an earlier call, leaves the gradient itself (8192 x 50304 x 768, bf16:
+// statistics 570 us, 1.11 PFLOP/s with the matrix cores half busy; gradient 690,
+// 824 MB written under the products: kept exponentials and their own pass take 672
+// + 300).
 // ---------------------------------------------------------------------------
 template <typename T, int TILE, int S, bool FEW, bool GATHER, LogitsMode MODE = LOGITS_LOSS>
 __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2) void k_logits_mfma(HeadArgs a, int keep, int vt, int tt) {

@@ -12,7 +12,10 @@
 // Everything between the loads and the stores is 32-bit, hidden is taken from
 // out before its rounding, and the backward pass makes out again from x and y,
 // which it reads anyway: it saves nothing, and out's rounding is in no gradient.
-// Bound by HBM: each row is read once and held in registers.
+// Bound by HBM: each row is read once and held in registers, the next one is on
+// its way meanwhile. 8192 rows with all their gradients, forward / backward (and
+// the sums of its partials): 768 channels bf16 10.5 us (4.8 TB/s) / 17 (4.4; 4),
+// 2048 of fp32 beside bf16 37.5 (5.4) / 55 (5.5; 5).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,21 +29,26 @@ namespace {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
-// A thread's chunk of CH (4 or 8) channels from c of a row of d as they are in
-// memory, zero past its end; one or two loads where whole, aligned or not. TAIL:
-// whether a row can end inside a chunk.
+// A thread's chunk of CH (4 or 8) channels from c of a row of d, as in memory: one
+// or two loads where whole, aligned or not. TAIL: whether a row can end inside a
+// chunk. Such a chunk and those past it are the row's last CH channels, until
+// `ended` moves them to their places and zeros behind: no load waits for a branch
+// (8192 x 1023 bf16, channel by channel / so: forward 18.7 / 14.7 us, backward 49 /
+// 29). SHORT rows, which can have fewer channels than a chunk and end in every wave,
+// take theirs channel by channel, the last one past the end (16384 x 100: 7.1, moved 9.3).
 template <typename T, int CH>
 struct Raw {
   uint32_t w[CH * sizeof(T) / 4];
 };
-template <bool TAIL, typename T, int CH>
+template <bool TAIL, bool SHORT, typename T, int CH>
 __device__ __forceinline__ void load_raw(const T* row, int c, int d, Raw<T, CH>& v) {
-  if (c + CH <= d) {
+  if constexpr (TAIL && !SHORT) {
+    __builtin_memcpy(&v, row + min(c, d - CH), sizeof(v));
+  } else if (c + CH <= d) {
     __builtin_memcpy(&v, row + c, sizeof(v));
   } else if (!TAIL) {
     v = {};
   } else {
-    // (loads without a branch each, the row's last element past its end)
     T x[CH];
 #pragma unroll
     for (int e = 0; e < CH; ++e) x[e] = row[min(c + e, d - 1)];
@@ -48,6 +56,25 @@ __device__ __forceinline__ void load_raw(const T* row, int c, int d, Raw<T, CH>&
     for (int e = 0; e < CH; ++e) x[e] = c + e < d ? x[e] : T(0);
     __builtin_memcpy(&v, x, sizeof(v));
   }
+}
+// Channels from k on to the front, zeros behind.
+template <typename T, int CH>
+__device__ __forceinline__ void move_down(Raw<T, CH>& v, int k) {
+  constexpr int N = CH * sizeof(T) / 4;
+  const int words = k * (int)sizeof(T) / 4;
+#pragma unroll
+  for (int step = N / 2; step; step /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.w[i] = words & step ? (i + step < N ? v.w[i + step] : 0u) : v.w[i];
+  if (sizeof(T) == 2 && (k & 1))
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.w[i] = v.w[i] >> 16 | (i + 1 < N ? v.w[i + 1] << 16 : 0u);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v.w[i] = words < N ? v.w[i] : 0u;
+}
+template <bool TAIL, bool SHORT, typename T, int CH>
+__device__ __forceinline__ void ended(Raw<T, CH>& v, int c, int d) {
+  if (TAIL && !SHORT && c + CH > d) move_down(v, c + CH - d);
 }
 template <typename T, int CH>
 __device__ __forceinline__ void unpack(const Raw<T, CH>& r, float (&v)[CH]) {
@@ -57,10 +84,11 @@ __device__ __forceinline__ void unpack(const Raw<T, CH>& r, float (&v)[CH]) {
     else v[e] = __uint_as_float(r.w[e]);
   }
 }
-template <bool TAIL, int CH, typename T>
+template <bool TAIL, bool SHORT, int CH, typename T>
 __device__ __forceinline__ void load_chunk(const T* row, int c, int d, float (&v)[CH]) {
   Raw<T, CH> r;
-  load_raw<TAIL>(row, c, d, r);
+  load_raw<TAIL, SHORT>(row, c, d, r);
+  ended<TAIL, SHORT>(r, c, d);
   unpack(r, v);
 }
 template <bool TAIL, int CH, typename T>
@@ -87,11 +115,11 @@ __device__ __forceinline__ float one_value(const NormParam& p, int64_t i) {
   return p.half ? bf2f(((const u16*)p.ptr)[i]) : ((const float*)p.ptr)[i];
 }
 // A parameter's chunk (1 where it is not there; NORM_FULL is the rows').
-template <bool TAIL, int CH>
+template <bool TAIL, bool SHORT, int CH>
 __device__ __forceinline__ void load_param(const NormParam& p, int c, int d, float (&v)[CH]) {
   if (p.kind == NORM_CHANNELS) {
-    if (p.half) load_chunk<TAIL>((const u16*)p.ptr, c, d, v);
-    else load_chunk<TAIL>((const float*)p.ptr, c, d, v);
+    if (p.half) load_chunk<TAIL, SHORT>((const u16*)p.ptr, c, d, v);
+    else load_chunk<TAIL, SHORT>((const float*)p.ptr, c, d, v);
   } else {
     const float x = p.kind == NORM_ONE ? one_value(p, 0) : 1.f;
 #pragma unroll
@@ -123,35 +151,61 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float* sh) {
 }
 
 // A row's operands, loaded together and, where the registers hold two, one row
-// ahead of their use. GENERAL, here and below: with a gate for each element, a scale
-// for each channel, or a row that ends inside a chunk (kept apart for the
-// registers that these take).
-template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL, bool BACKWARD>
+// ahead of their use. Three forms, kept apart for the registers that they take:
+// rows of whole chunks, rows that can end inside one (TAIL), and with a gate for
+// each element or a scale for each channel (MORE, which has TAIL).
+enum NormForm { FORM_WHOLE, FORM_TAIL, FORM_MORE };
+template <typename TX, typename TY, int TPR, int NC, int CH, int FORM, bool BACKWARD>
 struct Row {
+  static constexpr bool TAIL = FORM != FORM_WHOLE, MORE = FORM == FORM_MORE;
+  static constexpr bool SHORT = TPR == 16, LATER = TPR == 1024;   // (LATER: loaded where needed)
   Raw<TX, CH> x[NC], dout[BACKWARD ? NC : 1];
-  Raw<TY, CH> y[NC], g[GENERAL ? NC : 1], dhidden[BACKWARD ? NC : 1];
+  Raw<TY, CH> y[NC], g[MORE ? NC : 1], dhidden[BACKWARD ? NC : 1];
   __device__ __forceinline__ void load(const NormArgs& a, int64_t r, int t) {
     auto rows = [&](auto& to, const void* p, int64_t ld, auto type) {
       typedef decltype(type) T;
 #pragma unroll
-      for (int k = 0; k < NC; ++k) load_raw<GENERAL>((const T*)p + r * ld, CH * (k * TPR + t), a.d, to[k]);
+      for (int k = 0; k < NC; ++k) load_raw<TAIL, SHORT>((const T*)p + r * ld, CH * (k * TPR + t), a.d, to[k]);
     };
     rows(x, a.x.ptr, a.x.ld, TX());
     if (a.y.ptr) rows(y, a.y.ptr, a.y.ld, TY());
-    if constexpr (BACKWARD && !(TPR == 1024 && (NC > 1 || GENERAL))) {
+    if constexpr (BACKWARD && !LATER) {
       if (a.dhidden.ptr) rows(dhidden, a.dhidden.ptr, a.dhidden.ld, TY());
       if (a.dout.ptr) rows(dout, a.dout.ptr, a.dout.ld, TX());
     }
-    if constexpr (GENERAL)
+    if constexpr (MORE)
       if (a.gate.kind == NORM_FULL) rows(g, a.gate.ptr, a.gate.ld, TY());
+  }
+  // (before the first use)
+  __device__ __forceinline__ void arrived(int d, int t) {
+    if constexpr (TAIL && !SHORT) {
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const int c = CH * (k * TPR + t);
+        if (c + CH <= d) continue;
+        ended<TAIL, SHORT>(x[k], c, d);
+        ended<TAIL, SHORT>(y[k], c, d);
+        ended<TAIL, SHORT>(g[MORE ? k : 0], c, d);
+        if constexpr (BACKWARD && !LATER) {
+          ended<TAIL, SHORT>(dhidden[k], c, d);
+          ended<TAIL, SHORT>(dout[k], c, d);
+        }
+      }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ static void load_late(const NormRows& m, int64_t r, int c, int d, Raw<T, CH>& v) {
+    load_raw<TAIL, SHORT>((const T*)m.ptr + r * m.ld, c, d, v);
+    ended<TAIL, SHORT>(v, c, d);
   }
 };
 
 // TPR threads to a row, NC chunks of CH channels to a thread; the threads past TPR
 // of a block have other rows.
-template <typename TX, typename TY, int TPR, int NC, int CH, int BLOCK, bool GENERAL>
+template <typename TX, typename TY, int TPR, int NC, int CH, int BLOCK, int FORM>
 __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
   constexpr int ROWS = BLOCK / TPR;
+  constexpr bool TAIL = FORM != FORM_WHOLE, MORE = FORM == FORM_MORE;
   constexpr bool AHEAD = NC * CH <= 12 || TPR <= 64;
   __shared__ float sh[2][BLOCK / 64];
   const int t = threadIdx.x % TPR, d = a.d;
@@ -160,19 +214,19 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
   // (every thread of a block goes round as often; rows past the last one are
   // the last one again and are not stored)
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-  Row<TX, TY, TPR, NC, CH, GENERAL, false> now, next;
+  Row<TX, TY, TPR, NC, CH, FORM, false> now, next;
   if (AHEAD) next.load(a, min(row, a.n - 1), t);
   const bool there = a.y.ptr != nullptr;
-  float gate[NC][CH], pre[NC][CH], scale[GENERAL ? NC : 1][CH];
+  float gate[NC][CH], pre[NC][CH], scale[MORE ? NC : 1][CH];
   const float scale1 = a.scale.kind == NORM_ONE ? one_value(a.scale, 0) : 1.f;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     const int c = CH * (k * TPR + t);
     float post[CH];
-    if (GENERAL) load_param<GENERAL>(a.scale, c, d, scale[GENERAL ? k : 0]);
-    load_param<GENERAL>(a.pre_gain, c, d, pre[k]);
-    load_param<GENERAL>(a.post_gain, c, d, post);
-    load_param<GENERAL>(a.gate, c, d, gate[k]);
+    if (MORE) load_param<TAIL, TPR == 16>(a.scale, c, d, scale[MORE ? k : 0]);
+    load_param<TAIL, TPR == 16>(a.pre_gain, c, d, pre[k]);
+    load_param<TAIL, TPR == 16>(a.post_gain, c, d, post);
+    load_param<TAIL, TPR == 16>(a.gate, c, d, gate[k]);
 #pragma unroll
     for (int e = 0; e < CH; ++e) gate[k][e] *= post[e];
   }
@@ -184,13 +238,14 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
     } else {
       now.load(a, min(row, a.n - 1), t);
     }
+    now.arrived(d, t);
     float x[NC][CH], s[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       unpack(now.x[k], x[k]);
       if (a.scale.ptr)
 #pragma unroll
-        for (int e = 0; e < CH; ++e) x[k][e] *= GENERAL ? scale[GENERAL ? k : 0][e] : scale1;
+        for (int e = 0; e < CH; ++e) x[k][e] *= MORE ? scale[MORE ? k : 0][e] : scale1;
     }
     if (there) {
       float y[NC][CH], r1 = 1.f;
@@ -206,9 +261,9 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
-        if (GENERAL && a.gate.kind == NORM_FULL) {
+        if (MORE && a.gate.kind == NORM_FULL) {
           float g[CH];
-          unpack(now.g[GENERAL ? k : 0], g);
+          unpack(now.g[MORE ? k : 0], g);
 #pragma unroll
           for (int e = 0; e < CH; ++e) y[k][e] *= g[e];
         }
@@ -218,7 +273,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
     }
     if (a.out.ptr && real)
 #pragma unroll
-      for (int k = 0; k < NC; ++k) store_chunk<GENERAL>((TX*)a.out.ptr + row * a.out.ld, CH * (k * TPR + t), d, x[k]);
+      for (int k = 0; k < NC; ++k) store_chunk<TAIL>((TX*)a.out.ptr + row * a.out.ld, CH * (k * TPR + t), d, x[k]);
     if (a.pre) {
       s[0] = 0.f;
 #pragma unroll
@@ -232,7 +287,7 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
         for (int k = 0; k < NC; ++k) {
 #pragma unroll
           for (int e = 0; e < CH; ++e) x[k][e] *= r2 * pre[k][e];
-          store_chunk<GENERAL>((TY*)a.hidden.ptr + row * a.hidden.ld, CH * (k * TPR + t), d, x[k]);
+          store_chunk<TAIL>((TY*)a.hidden.ptr + row * a.hidden.ld, CH * (k * TPR + t), d, x[k]);
         }
     }
     if (TPR > 64 && r0 + step < a.n) __syncthreads();   // the sums are read before the next row's are written
@@ -242,41 +297,42 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
 // Waves to a SIMD that the backward pass is compiled for, where rows have several
 // waves: as many as the registers hold (a second raw row of 32-bit operands takes
 // twice as many), and four where a block alone has eight.
-constexpr int waves_wanted(int tpr, int nc, bool general, int bytes) {
-  return tpr <= 64 || nc > 1 || general ? 1 : bytes == 2 || tpr > 256 ? 4 : 3;
+constexpr int waves_wanted(int tpr, int nc, bool more, int bytes) {
+  return tpr <= 64 || nc > 1 || more ? 1 : bytes == 2 || tpr > 256 ? 4 : 3;
 }
-template <typename TX, typename TY, int TPR, int NC, int CH, int BLOCK, bool GENERAL>
-__global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) void k_residual_norm_grad(NormArgs a) {
+template <typename TX, typename TY, int TPR, int NC, int CH, int BLOCK, int FORM>
+__global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, sizeof(TX))) void k_residual_norm_grad(NormArgs a) {
   constexpr int ROWS = BLOCK / TPR;
+  constexpr bool TAIL = FORM != FORM_WHOLE, MORE = FORM == FORM_MORE;
   // what the registers hold: the parameters (wide rows read these and the results'
   // gradients again where they are needed), and a second row (4096 x 4096 of 32
   // bits, with / without 117 / 88 us: it does not fit beside eight waves)
-  constexpr bool WIDE = TPR == 1024 && (NC > 1 || GENERAL), AHEAD = !WIDE && !(TPR >= 512 && sizeof(TX) == 4);
+  constexpr bool WIDE = TPR == 1024, AHEAD = !WIDE && !(TPR >= 512 && sizeof(TX) == 4);
   __shared__ float sh[4][2 * (BLOCK / 64)];
   __shared__ float joined[ROWS > 1 ? BLOCK * CH : 1];
   const int t = threadIdx.x % TPR, d = a.d;
   const float inv_d = 1.f / d;
-  const bool there = a.y.ptr != nullptr, full = GENERAL && a.gate.kind == NORM_FULL, normed = a.dhidden.ptr != nullptr;
+  const bool there = a.y.ptr != nullptr, full = MORE && a.gate.kind == NORM_FULL, normed = a.dhidden.ptr != nullptr;
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-  Row<TX, TY, TPR, NC, CH, GENERAL, true> now, next;
+  Row<TX, TY, TPR, NC, CH, FORM, true> now, next;
   if (AHEAD) next.load(a, min(row, a.n - 1), t);
   // gate and post_gain multiplied (post_gain alone where the gate is full)
   auto load_gated = [&](int k, float (&v)[CH]) {
     const int c = CH * (k * TPR + t);
     float post[CH];
-    load_param<GENERAL>(a.post_gain, c, d, post);
-    load_param<GENERAL>(a.gate, c, d, v);
+    load_param<TAIL, TPR == 16>(a.post_gain, c, d, post);
+    load_param<TAIL, TPR == 16>(a.gate, c, d, v);
 #pragma unroll
     for (int e = 0; e < CH; ++e) v[e] *= post[e];
   };
-  float scale[GENERAL ? NC : 1][CH], gated[WIDE ? 1 : NC][CH], pre[WIDE ? 1 : NC][CH];
+  float scale[MORE ? NC : 1][CH], gated[WIDE ? 1 : NC][CH], pre[WIDE ? 1 : NC][CH];
   const float scale1 = a.scale.kind == NORM_ONE ? one_value(a.scale, 0) : 1.f;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    if (GENERAL) load_param<GENERAL>(a.scale, CH * (k * TPR + t), d, scale[GENERAL ? k : 0]);
+    if (MORE) load_param<TAIL, TPR == 16>(a.scale, CH * (k * TPR + t), d, scale[MORE ? k : 0]);
     if (!WIDE) {
-      load_param<GENERAL>(a.pre_gain, CH * (k * TPR + t), d, pre[WIDE ? 0 : k]);
+      load_param<TAIL, TPR == 16>(a.pre_gain, CH * (k * TPR + t), d, pre[WIDE ? 0 : k]);
       load_gated(k, gated[WIDE ? 0 : k]);
     }
   }
@@ -285,17 +341,17 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
     return gated[WIDE ? 0 : k];
   };
   auto pre_of = [&](int k) -> float (&)[CH] {
-    if (WIDE) load_param<GENERAL>(a.pre_gain, CH * (k * TPR + t), d, pre[0]);
+    if (WIDE) load_param<TAIL, TPR == 16>(a.pre_gain, CH * (k * TPR + t), d, pre[0]);
     return pre[WIDE ? 0 : k];
   };
-  auto scale_of = [&](int k, int e) { return GENERAL ? scale[GENERAL ? k : 0][e] : scale1; };
+  auto scale_of = [&](int k, int e) { return MORE ? scale[MORE ? k : 0][e] : scale1; };
   // a single gate's gradient is that of the channels, weighted by post_gain in the end
   const bool vector = (a.want & kWantBlock) || ((a.want & kWantGateOne) && a.post_gain.ptr);
-  float sum_block[NC][CH], sum_scale[GENERAL ? NC : 1][CH], sum_pre[NC][CH], gate_one = 0.f, scale_one = 0.f;
+  float sum_block[NC][CH], sum_scale[MORE ? NC : 1][CH], sum_pre[NC][CH], gate_one = 0.f, scale_one = 0.f;
 #pragma unroll
   for (int k = 0; k < NC; ++k)
 #pragma unroll
-    for (int e = 0; e < CH; ++e) sum_block[k][e] = sum_scale[GENERAL ? k : 0][e] = sum_pre[k][e] = 0.f;
+    for (int e = 0; e < CH; ++e) sum_block[k][e] = sum_scale[MORE ? k : 0][e] = sum_pre[k][e] = 0.f;
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.n; r0 += step, row += step) {
     const bool real = row < a.n;
     if (AHEAD) {
@@ -304,6 +360,7 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
     } else {
       now.load(a, min(row, a.n - 1), t);
     }
+    now.arrived(d, t);
     const int64_t at = min(row, a.n - 1);
     // y becomes yhat, o the row's out
     float y[NC][CH], o[NC][CH], r1 = 1.f;
@@ -332,7 +389,7 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
         for (int e = 0; e < CH; ++e) o[k][e] *= scale_of(k, e);
       if (there) {
         float g[CH];
-        if (full) unpack(now.g[GENERAL ? k : 0], g);
+        if (full) unpack(now.g[MORE ? k : 0], g);
         const float (&w)[CH] = gated_of(k);
 #pragma unroll
         for (int e = 0; e < CH; ++e) o[k][e] = fmaf(full ? w[e] * g[e] : w[e], y[k][e], o[k][e]);
@@ -344,7 +401,7 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         float u[CH];
-        if (WIDE) load_raw<GENERAL>((const TY*)a.dhidden.ptr + at * a.dhidden.ld, CH * (k * TPR + t), d, now.dhidden[0]);
+        if (WIDE) now.load_late(a.dhidden, at, CH * (k * TPR + t), d, now.dhidden[0]);
         unpack(now.dhidden[WIDE ? 0 : k], u);
         const float (&w)[CH] = pre_of(k);
 #pragma unroll
@@ -364,7 +421,7 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
       const int c = CH * (k * TPR + t);
       float dt[CH], x[CH];
       if (a.dout.ptr) {
-        if (WIDE) load_raw<GENERAL>((const TX*)a.dout.ptr + at * a.dout.ld, c, d, now.dout[0]);
+        if (WIDE) now.load_late(a.dout, at, c, d, now.dout[0]);
         unpack(now.dout[WIDE ? 0 : k], dt);
       } else {
 #pragma unroll
@@ -372,7 +429,7 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
       }
       if (normed) {
         float u[CH];
-        if (WIDE) load_raw<GENERAL>((const TY*)a.dhidden.ptr + at * a.dhidden.ld, CH * (k * TPR + t), d, now.dhidden[0]);
+        if (WIDE) now.load_late(a.dhidden, at, CH * (k * TPR + t), d, now.dhidden[0]);
         unpack(now.dhidden[WIDE ? 0 : k], u);
         const float (&w)[CH] = pre_of(k);
 #pragma unroll
@@ -386,25 +443,25 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
         float q[CH];
 #pragma unroll
         for (int e = 0; e < CH; ++e) q[e] = a.scale.ptr ? dt[e] * scale_of(k, e) : dt[e];
-        store_chunk<GENERAL>((TX*)a.dx.ptr + row * a.dx.ld, c, d, q);
+        store_chunk<TAIL>((TX*)a.dx.ptr + row * a.dx.ld, c, d, q);
       }
       if ((a.want & (kWantScale | kWantScaleOne)) && real) {
         unpack(now.x[k], x);
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
-          if (GENERAL && (a.want & kWantScale)) sum_scale[GENERAL ? k : 0][e] = fmaf(dt[e], x[e], sum_scale[GENERAL ? k : 0][e]);
+          if (MORE && (a.want & kWantScale)) sum_scale[MORE ? k : 0][e] = fmaf(dt[e], x[e], sum_scale[MORE ? k : 0][e]);
           else scale_one = fmaf(dt[e], x[e], scale_one);
         }
       }
       if (there) {
         float g[CH];
-        if (full) unpack(now.g[GENERAL ? k : 0], g);
+        if (full) unpack(now.g[MORE ? k : 0], g);
         const float (&w)[CH] = gated_of(k);
         if (full && a.dfull.ptr && real) {
           float q[CH];
 #pragma unroll
           for (int e = 0; e < CH; ++e) q[e] = dt[e] * w[e] * y[k][e];
-          store_chunk<GENERAL>((TY*)a.dfull.ptr + row * a.dfull.ld, c, d, q);
+          store_chunk<TAIL>((TY*)a.dfull.ptr + row * a.dfull.ld, c, d, q);
         }
         if (vector && real) {
 #pragma unroll
@@ -432,7 +489,7 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
       }
       if (real)
 #pragma unroll
-        for (int k = 0; k < NC; ++k) store_chunk<GENERAL>((TY*)a.dy.ptr + row * a.dy.ld, CH * (k * TPR + t), d, o[k]);
+        for (int k = 0; k < NC; ++k) store_chunk<TAIL>((TY*)a.dy.ptr + row * a.dy.ld, CH * (k * TPR + t), d, o[k]);
     }
     if (TPR > 64) __syncthreads();   // the sums are read before the next row's are written
   }
@@ -465,14 +522,14 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, GENERAL, sizeof(TX))) 
     part += a.dp;
   };
   if (a.want & kWantBlock) leave(sum_block);
-  if (GENERAL && (a.want & kWantScale)) leave(sum_scale);
+  if (MORE && (a.want & kWantScale)) leave(sum_scale);
   if (a.want & kWantPre) leave(sum_pre);
   if (a.want & (kWantGateOne | kWantScaleOne)) {
     if (vector) {
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         float post[CH];
-        load_param<GENERAL>(a.post_gain, CH * (k * TPR + t), d, post);
+        load_param<TAIL, TPR == 16>(a.post_gain, CH * (k * TPR + t), d, post);
 #pragma unroll
         for (int e = 0; e < CH; ++e) gate_one = fmaf(post[e], sum_block[k][e], gate_one);
       }
@@ -598,44 +655,47 @@ int blocks_of(int64_t n, int rows, int resident) {
   const int64_t blocks = (n + rows - 1) / rows, rounds = (blocks + resident - 1) / resident;
   return (int)((blocks + rounds - 1) / rounds);
 }
-bool general(const NormArgs& a, int chunk) {
-  return a.gate.kind == NORM_FULL || a.scale.kind == NORM_CHANNELS || a.d % chunk != 0;
+int form_of(const NormArgs& a, int chunk) {
+  if (a.gate.kind == NORM_FULL || a.scale.kind == NORM_CHANNELS) return FORM_MORE;
+  return a.d % chunk != 0 ? FORM_TAIL : FORM_WHOLE;
 }
 
-template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL>
+template <typename TX, typename TY, int TPR, int NC, int CH, int FORM>
 void forward(const NormArgs& a, hipStream_t s) {
   constexpr int BLOCK = whole_rows(TPR, kForwardBlock);
-  static const int most = resident(k_residual_norm<TX, TY, TPR, NC, CH, BLOCK, GENERAL>, BLOCK);
+  static const int most = resident(k_residual_norm<TX, TY, TPR, NC, CH, BLOCK, FORM>, BLOCK);
   const dim3 g((unsigned)blocks_of(a.n, BLOCK / TPR, most));
-  hipLaunchKernelGGL((k_residual_norm<TX, TY, TPR, NC, CH, BLOCK, GENERAL>), g, dim3(BLOCK), 0, s, a);
+  hipLaunchKernelGGL((k_residual_norm<TX, TY, TPR, NC, CH, BLOCK, FORM>), g, dim3(BLOCK), 0, s, a);
 }
 // blocks alone, or the launch
-template <typename TX, typename TY, int TPR, int NC, int CH, bool GENERAL>
+template <typename TX, typename TY, int TPR, int NC, int CH, int FORM>
 int backward(const NormArgs& a, bool launch, hipStream_t s) {
   constexpr int BLOCK = whole_rows(TPR, kBackwardBlock);
-  static const int most = resident(k_residual_norm_grad<TX, TY, TPR, NC, CH, BLOCK, GENERAL>, BLOCK);
+  static const int most = resident(k_residual_norm_grad<TX, TY, TPR, NC, CH, BLOCK, FORM>, BLOCK);
   const int blocks = blocks_of(a.n, BLOCK / TPR, most < kNormMostBlocks ? most : kNormMostBlocks);
-  if (launch) hipLaunchKernelGGL((k_residual_norm_grad<TX, TY, TPR, NC, CH, BLOCK, GENERAL>), dim3(blocks), dim3(BLOCK), 0, s, a);
+  if (launch) hipLaunchKernelGGL((k_residual_norm_grad<TX, TY, TPR, NC, CH, BLOCK, FORM>), dim3(blocks), dim3(BLOCK), 0, s, a);
   return blocks;
 }
 
 #define BY_TYPES(f, TPR, NC, CH, ...)                                                    \
   do {                                                                                   \
-    const bool g = general(a, CH);                                                          \
-    if (x_half) f##_of<u16, u16, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);                    \
-    else if (y_half) f##_of<float, u16, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);             \
-    else f##_of<float, float, TPR, NC, CH>(g, a, ##__VA_ARGS__, s);                       \
+    const int form = form_of(a, CH);                                                     \
+    if (x_half) f##_of<u16, u16, TPR, NC, CH>(form, a, ##__VA_ARGS__, s);                    \
+    else if (y_half) f##_of<float, u16, TPR, NC, CH>(form, a, ##__VA_ARGS__, s);             \
+    else f##_of<float, float, TPR, NC, CH>(form, a, ##__VA_ARGS__, s);                       \
   } while (0)
 
 template <typename TX, typename TY, int TPR, int NC, int CH>
-void forward_of(bool g, const NormArgs& a, hipStream_t s) {
-  if (g) forward<TX, TY, TPR, NC, CH, true>(a, s);
-  else forward<TX, TY, TPR, NC, CH, false>(a, s);
+void forward_of(int form, const NormArgs& a, hipStream_t s) {
+  if (form == FORM_WHOLE) forward<TX, TY, TPR, NC, CH, FORM_WHOLE>(a, s);
+  else if (form == FORM_TAIL) forward<TX, TY, TPR, NC, CH, FORM_TAIL>(a, s);
+  else forward<TX, TY, TPR, NC, CH, FORM_MORE>(a, s);
 }
 template <typename TX, typename TY, int TPR, int NC, int CH>
-void backward_of(bool g, const NormArgs& a, int* blocks, hipStream_t s) {
-  if (g) *blocks = backward<TX, TY, TPR, NC, CH, true>(a, !blocks[1], s);
-  else *blocks = backward<TX, TY, TPR, NC, CH, false>(a, !blocks[1], s);
+void backward_of(int form, const NormArgs& a, int* blocks, hipStream_t s) {
+  if (form == FORM_WHOLE) *blocks = backward<TX, TY, TPR, NC, CH, FORM_WHOLE>(a, !blocks[1], s);
+  else if (form == FORM_TAIL) *blocks = backward<TX, TY, TPR, NC, CH, FORM_TAIL>(a, !blocks[1], s);
+  else *blocks = backward<TX, TY, TPR, NC, CH, FORM_MORE>(a, !blocks[1], s);
 }
 
 }  // namespace
