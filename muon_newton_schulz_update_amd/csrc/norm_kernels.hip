@@ -345,13 +345,34 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
     return pre[WIDE ? 0 : k];
   };
   auto scale_of = [&](int k, int e) { return MORE ? scale[MORE ? k : 0][e] : scale1; };
+  // the channels' sums over the rows: of wide rows in LDS, a thread's own (1024 x
+  // 16384 bf16, in registers / so: 112 / 76 us)
+  constexpr int KEPT = WIDE ? NC * CH / 4 * BLOCK : 1;
+  __shared__ f32x4_t kept[2][KEPT];
+  auto fetch = [&](float (&sum)[CH], int which, int k) {
+    if (WIDE)
+#pragma unroll
+      for (int e = 0; e < CH; e += 4) {
+        const f32x4_t v = kept[which][(k * (CH / 4) + e / 4) * BLOCK + threadIdx.x];
+        sum[e] = v[0], sum[e + 1] = v[1], sum[e + 2] = v[2], sum[e + 3] = v[3];
+      }
+  };
+  auto keep = [&](const float (&sum)[CH], int which, int k) {
+    if (WIDE)
+#pragma unroll
+      for (int e = 0; e < CH; e += 4)
+        kept[which][(k * (CH / 4) + e / 4) * BLOCK + threadIdx.x] = (f32x4_t){sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
+  };
   // a single gate's gradient is that of the channels, weighted by post_gain in the end
   const bool vector = (a.want & kWantBlock) || ((a.want & kWantGateOne) && a.post_gain.ptr);
-  float sum_block[NC][CH], sum_scale[MORE ? NC : 1][CH], sum_pre[NC][CH], gate_one = 0.f, scale_one = 0.f;
+  float sum_block[WIDE ? 1 : NC][CH], sum_scale[MORE ? NC : 1][CH], sum_pre[WIDE ? 1 : NC][CH], gate_one = 0.f, scale_one = 0.f;
 #pragma unroll
-  for (int k = 0; k < NC; ++k)
+  for (int k = 0; k < NC; ++k) {
 #pragma unroll
-    for (int e = 0; e < CH; ++e) sum_block[k][e] = sum_scale[MORE ? k : 0][e] = sum_pre[k][e] = 0.f;
+    for (int e = 0; e < CH; ++e) sum_block[WIDE ? 0 : k][e] = sum_scale[MORE ? k : 0][e] = sum_pre[WIDE ? 0 : k][e] = 0.f;
+    keep(sum_block[0], 0, k);
+    keep(sum_pre[0], 1, k);
+  }
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.n; r0 += step, row += step) {
     const bool real = row < a.n;
     if (AHEAD) {
@@ -432,12 +453,15 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
         if (WIDE) now.load_late(a.dhidden, at, CH * (k * TPR + t), d, now.dhidden[0]);
         unpack(now.dhidden[WIDE ? 0 : k], u);
         const float (&w)[CH] = pre_of(k);
+        float (&sum)[CH] = sum_pre[WIDE ? 0 : k];
+        fetch(sum, 1, k);
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
           const float xh = o[k][e] * r2;
           dt[e] += r2 * (u[e] * w[e] - xh * m);
-          if (real) sum_pre[k][e] = fmaf(u[e], xh, sum_pre[k][e]);
+          if (real) sum[e] = fmaf(u[e], xh, sum[e]);
         }
+        keep(sum, 1, k);
       }
       if (a.dx.ptr && real) {
         float q[CH];
@@ -464,8 +488,11 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
           store_chunk<TAIL>((TY*)a.dfull.ptr + row * a.dfull.ld, c, d, q);
         }
         if (vector && real) {
+          float (&sum)[CH] = sum_block[WIDE ? 0 : k];
+          fetch(sum, 0, k);
 #pragma unroll
-          for (int e = 0; e < CH; ++e) sum_block[k][e] = fmaf(full ? dt[e] * g[e] : dt[e], y[k][e], sum_block[k][e]);
+          for (int e = 0; e < CH; ++e) sum[e] = fmaf(full ? dt[e] * g[e] : dt[e], y[k][e], sum[e]);
+          keep(sum, 0, k);
         } else if ((a.want & kWantGateOne) && real) {
 #pragma unroll
           for (int e = 0; e < CH; ++e) gate_one = fmaf(dt[e], y[k][e], gate_one);
@@ -495,14 +522,17 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
   }
   // the block's partials: rows' sums joined in order
   float* part = a.part + blockIdx.x * a.part_floats;
-  auto leave = [&](auto& sum) {
+  auto leave = [&](auto& sums, int which) {
 #pragma unroll
-    for (int k = 0; k < (int)(sizeof(sum) / sizeof(sum[0])); ++k) {
+    for (int k = 0; k < NC; ++k) {
+      const bool from_lds = WIDE && which < 2;
+      float (&sum)[CH] = sums[from_lds ? 0 : k];
+      if (from_lds) fetch(sum, which, k);
       if constexpr (ROWS > 1) {
         // (threads of neighbouring chunks next to one another: no bank is asked twice)
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < CH; ++e) joined[e * BLOCK + threadIdx.x] = sum[k][e];
+        for (int e = 0; e < CH; ++e) joined[e * BLOCK + threadIdx.x] = sum[e];
         __syncthreads();
         for (int i = threadIdx.x; i < TPR * CH; i += BLOCK) {
           // (neighbouring threads write neighbouring channels)
@@ -516,22 +546,24 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
         const int c = CH * (k * TPR + t);
 #pragma unroll
         for (int e = 0; e < CH; e += 4)
-          if (c + e < a.dp) *(f32x4_t*)(part + c + e) = (f32x4_t){sum[k][e], sum[k][e + 1], sum[k][e + 2], sum[k][e + 3]};
+          if (c + e < a.dp) *(f32x4_t*)(part + c + e) = (f32x4_t){sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
       }
     }
     part += a.dp;
   };
-  if (a.want & kWantBlock) leave(sum_block);
-  if (MORE && (a.want & kWantScale)) leave(sum_scale);
-  if (a.want & kWantPre) leave(sum_pre);
+  if (a.want & kWantBlock) leave(sum_block, 0);
+  if constexpr (MORE)
+    if (a.want & kWantScale) leave(sum_scale, 2);
+  if (a.want & kWantPre) leave(sum_pre, 1);
   if (a.want & (kWantGateOne | kWantScaleOne)) {
     if (vector) {
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         float post[CH];
         load_param<TAIL, TPR == 16>(a.post_gain, CH * (k * TPR + t), d, post);
+        fetch(sum_block[WIDE ? 0 : k], 0, k);
 #pragma unroll
-        for (int e = 0; e < CH; ++e) gate_one = fmaf(post[e], sum_block[k][e], gate_one);
+        for (int e = 0; e < CH; ++e) gate_one = fmaf(post[e], sum_block[WIDE ? 0 : k][e], gate_one);
       }
     }
     gate_one = lanes_sum<64>(gate_one);
