@@ -2,10 +2,13 @@
 // muon_matrix for the C ABI. Argument marshalling only, the same checks as the
 // binding's Python code, natively: from Python each tensor costs about 0.6 us
 // (shape, stride, type, device and pointer are a call each), which for the few
-// dozen tensors of an optimizer's list is several times the GPU's work.
+// dozen tensors of an optimizer's list is several times the GPU's work. The norms,
+// whose GPU work is a few us, are called from here as a whole, through the address
+// of the C entry point.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <ATen/Functions.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -59,6 +62,16 @@ bool describe(const at::Tensor& t, const char* what, long device, muon_matrix* m
     return false;
   }
   m->ptr = any ? t.data_ptr() : nullptr;
+  return true;
+}
+
+// The same of rows: the last dimension's, all the others together.
+bool describe_rows(const at::Tensor& t, const char* what, long device, muon_matrix* m) {
+  if (!describe(t, what, device, m)) return false;
+  if (t.dim() <= 2) return true;
+  const int64_t cols = t.size(-1);
+  m->rows = cols ? t.numel() / cols : 0;
+  m->cols = m->ld = cols;
   return true;
 }
 
@@ -149,11 +162,7 @@ PyObject* pack_rows(PyObject*, PyObject* args) {
       if (o == Py_None) continue;
       const char* what = PyUnicode_AsUTF8(PyTuple_GET_ITEM(names, i));
       const at::Tensor* t = what ? tensor_of(o, what) : nullptr;
-      ok = t && describe(*t, what, device, m + i);
-      if (!ok || t->dim() <= 2) continue;
-      const int64_t cols = t->size(-1);
-      m[i].rows = cols ? t->numel() / cols : 0;
-      m[i].cols = m[i].ld = cols;
+      ok = t && describe_rows(*t, what, device, m + i);
     }
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -197,10 +206,148 @@ PyObject* empty(PyObject*, PyObject* args) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// The norms around a block (norms.py): shapes, results, descriptors and the call.
+// ---------------------------------------------------------------------------
+constexpr int kNormInputs = 6;
+const char* const kNormNames[kNormInputs] = {"x", "y", "post_gain", "gate", "scale", "pre_gain"};
+const char* const kNormGrads[kNormInputs] = {"dx", "dy", "dpost_gain", "dgate", "dscale", "dpre_gain"};
+
+struct NormCall {
+  const at::Tensor* t[kNormInputs] = {};
+  muon_matrix m[kNormInputs];
+  muon_norm_params params;
+  const muon_matrix* at(int i) const { return t[i] ? m + i : nullptr; }
+};
+
+bool same_shape(const at::Tensor& t, const char* what, const at::Tensor& x) {
+  if (t.sizes() == x.sizes()) return true;
+  PyErr_Format(PyExc_ValueError, "%s of shape %s beside x of %s", what, c10::str(t.sizes()).c_str(), c10::str(x.sizes()).c_str());
+  return false;
+}
+
+bool norm_inputs(PyObject* inputs, long device, int post_norm, int pre_norm, double eps, NormCall& c) {
+  if (PyTuple_GET_SIZE(inputs) != kNormInputs) {
+    PyErr_SetString(PyExc_ValueError, "expected six inputs");
+    return false;
+  }
+  for (int i = 0; i < kNormInputs; ++i) {
+    PyObject* o = PyTuple_GET_ITEM(inputs, i);
+    if (i && o == Py_None) continue;
+    if (!(c.t[i] = tensor_of(o, kNormNames[i]))) return false;
+  }
+  if (c.t[1] && !same_shape(*c.t[1], "y", *c.t[0])) return false;
+  // (rows alone would take a gate whose leading dimensions are y's in another order)
+  const at::Tensor* gate = c.t[3];
+  if (gate && gate->dim() > 1 && gate->numel() != gate->size(-1) && !same_shape(*gate, "gate", *c.t[0])) return false;
+  for (int i = 0; i < kNormInputs; ++i)
+    if (c.t[i] && !describe_rows(*c.t[i], kNormNames[i], device, c.m + i)) return false;
+  c.params = muon_norm_params{c.at(2), c.at(5), c.at(3), c.at(4), post_norm, pre_norm, (float)eps};
+  return true;
+}
+
+at::Tensor like(const at::Tensor& t, at::ScalarType type, long device) {
+  return at::empty(t.sizes(), at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)device));
+}
+
+// residual_norm(entry, handle, device, inputs, post_norm, pre_norm, eps, dtype) -> (status, out or None, hidden or None)
+PyObject* residual_norm_of(PyObject*, PyObject* args) {
+  unsigned long long entry, handle;
+  long device;
+  PyObject *inputs, *dtype;
+  int post_norm, pre_norm;
+  double eps;
+  if (!PyArg_ParseTuple(args, "KKlO!ppdO", &entry, &handle, &device, &PyTuple_Type, &inputs, &post_norm, &pre_norm, &eps, &dtype))
+    return nullptr;
+  try {
+    NormCall c;
+    if (!norm_inputs(inputs, device, post_norm, pre_norm, eps, c)) return nullptr;
+    at::Tensor out, hidden;
+    muon_matrix m[2];
+    if (c.t[1]) out = like(*c.t[0], c.t[0]->scalar_type(), device);
+    if (pre_norm)
+      hidden = like(*c.t[0], THPDtype_Check(dtype) ? ((THPDtype*)dtype)->scalar_type : (c.t[1] ? c.t[1] : c.t[0])->scalar_type(), device);
+    if (out.defined() && !describe_rows(out, "out", device, m)) return nullptr;
+    if (hidden.defined() && !describe_rows(hidden, "hidden", device, m + 1)) return nullptr;
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = ((decltype(&residual_norm))entry)((muon_handle*)handle, c.m, c.at(1), &c.params, out.defined() ? m : nullptr,
+                                                hidden.defined() ? m + 1 : nullptr);
+    Py_END_ALLOW_THREADS
+    return Py_BuildValue("(iNN)", status, THPVariable_Wrap(out), THPVariable_Wrap(hidden));
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+// residual_norm_grad(entry, handle, device, inputs, dout, dhidden, wanted, post_norm, pre_norm, eps) ->
+// (status, the six inputs' gradients or None)
+PyObject* residual_norm_grad_of(PyObject*, PyObject* args) {
+  unsigned long long entry, handle;
+  long device;
+  PyObject *inputs, *into[2], *wanted;
+  int post_norm, pre_norm;
+  double eps;
+  if (!PyArg_ParseTuple(args, "KKlO!OOO!ppd", &entry, &handle, &device, &PyTuple_Type, &inputs, &into[0], &into[1], &PyTuple_Type,
+                        &wanted, &post_norm, &pre_norm, &eps))
+    return nullptr;
+  if (PyTuple_GET_SIZE(wanted) != kNormInputs) {
+    PyErr_SetString(PyExc_ValueError, "expected six answers");
+    return nullptr;
+  }
+  PyObject* grads = nullptr;
+  try {
+    NormCall c;
+    const char* const names[2] = {"dout", "dhidden"};
+    const at::Tensor* in[2] = {};
+    muon_matrix m[2], of[kNormInputs];
+    const muon_matrix* to[kNormInputs] = {};
+    if (!norm_inputs(inputs, device, post_norm, pre_norm, eps, c)) return nullptr;
+    for (int i = 0; i < 2; ++i) {
+      if (into[i] == Py_None) continue;
+      if (!(in[i] = tensor_of(into[i], names[i])) || !same_shape(*in[i], names[i], *c.t[0]) ||
+          !describe_rows(*in[i], names[i], device, m + i))
+        return nullptr;
+    }
+    grads = PyTuple_New(kNormInputs);
+    if (!grads) return nullptr;
+    for (int i = 0; i < kNormInputs; ++i) {
+      at::Tensor g;
+      const int want = c.t[i] ? PyObject_IsTrue(PyTuple_GET_ITEM(wanted, i)) : 0;
+      if (want < 0) goto fail;
+      if (want) {
+        g = like(*c.t[i], c.t[i]->scalar_type(), device);
+        if (!describe_rows(g, kNormGrads[i], device, of + i)) goto fail;
+        to[i] = of + i;
+      }
+      PyObject* wrapped = THPVariable_Wrap(std::move(g));
+      if (!wrapped) goto fail;
+      PyTuple_SET_ITEM(grads, i, wrapped);
+    }
+    {
+      const muon_norm_grads g{to[0], to[1], to[2], to[3], to[4], to[5]};
+      int status;
+      Py_BEGIN_ALLOW_THREADS
+      status = ((decltype(&residual_norm_grad))entry)((muon_handle*)handle, c.m, c.at(1), &c.params, in[0] ? m : nullptr,
+                                                       in[1] ? m + 1 : nullptr, &g);
+      Py_END_ALLOW_THREADS
+      return Py_BuildValue("(iN)", status, grads);
+    }
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+fail:
+  Py_XDECREF(grads);
+  return nullptr;
+}
+
 PyMethodDef methods[] = {
     {"empty", empty, METH_VARARGS, "A tensor on the GPU with the shape and type of others."},
     {"pack", pack, METH_VARARGS, "Descriptors of a list of tensors, as bytes."},
     {"pack_rows", pack_rows, METH_VARARGS, "Descriptors of tensors as rows, as bytes, and their address."},
+    {"residual_norm", residual_norm_of, METH_VARARGS, "Results of residual_norm, after its status."},
+    {"residual_norm_grad", residual_norm_grad_of, METH_VARARGS, "Gradients of residual_norm_grad, after its status."},
     {"device_of", device_of, METH_O, "Index of the first tensor on a GPU, or -1."},
     {nullptr, nullptr, 0, nullptr},
 };

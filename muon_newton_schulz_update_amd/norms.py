@@ -15,11 +15,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import MuonMatrix, load_library
+from . import load_library
 from .training import _checked, _describe, _handle_for, _one_stream_a_leaf
-
-_SIZE = ctypes.sizeof(MuonMatrix)
-_NAMES = ("x", "y", "post_gain", "pre_gain", "gate", "scale", "dout", "dhidden")
 
 
 class NormParams(ctypes.Structure):
@@ -42,51 +39,31 @@ class NormGrads(NamedTuple):
     pre_gain: torch.Tensor | None
 
 
-def _addresses(tensors, names, device):
-    """Descriptors of tensors (None: no address), by their last dimension's rows."""
-    words, at = _describe().pack_rows(tensors, names, device)
-    return words, [None if t is None else at + _SIZE * i for i, t in enumerate(tensors)]
+_entries = None
 
 
-def _same_shape(x, **others):
-    for name, t in others.items():
-        if t is not None and t.shape != x.shape:
-            raise ValueError(f"{name} of shape {tuple(t.shape)} beside x of {tuple(x.shape)}")
-
-
-def _check_shapes(x, y, gate, **others):
-    _same_shape(x, y=y, **others)
-    # (rows alone would take a gate whose leading dimensions are y's in another order)
-    if gate is not None and gate.dim() > 1 and gate.shape[:-1].numel() > 1 and gate.shape != x.shape:
-        raise ValueError(f"gate of shape {tuple(gate.shape)} beside y of {tuple(x.shape)}")
+def _entry(i: int) -> int:
+    """Address of a C entry point, for the native binding."""
+    global _entries
+    if _entries is None:
+        lib = load_library()
+        _entries = [ctypes.cast(f, ctypes.c_void_p).value for f in (lib.residual_norm, lib.residual_norm_grad)]
+    return _entries[i]
 
 
 def _forward(x, y, post_gain, gate, scale, pre_gain, post_norm, pre_norm, eps, dtype, handle):
-    _check_shapes(x, y, gate)
     h = _handle_for((x,), handle)
-    native = _describe()
-    out = None if y is None else native.empty(h.device, x, x)
-    hidden = None
-    if pre_norm:
-        hidden = native.empty(h.device, x, x if y is None else y) if dtype is None else torch.empty(
-            x.shape, device=f"cuda:{h.device}", dtype=dtype)
-    words, at = _addresses((x, y, post_gain, pre_gain, gate, scale, out, hidden), _NAMES[:6] + ("out", "hidden"), h.device)
-    params = NormParams(*at[2:6], bool(post_norm), bool(pre_norm), eps)
-    h._check(h._lib.residual_norm(h.ptr, at[0], at[1], ctypes.byref(params), at[6], at[7]))
+    status, out, hidden = _describe().residual_norm(_entry(0), h.ptr.value or 0, h.device, (x, y, post_gain, gate, scale, pre_gain),
+                                                    post_norm, pre_norm, eps, dtype)
+    h._check(status)
     return out, hidden
 
 
 def _backward(x, y, post_gain, gate, scale, pre_gain, post_norm, pre_norm, eps, dout, dhidden, wanted, handle):
-    _check_shapes(x, y, gate, dout=dout, dhidden=dhidden)
     h = _handle_for((x,), handle)
-    native = _describe()
-    inputs = (x, y, post_gain, gate, scale, pre_gain)
-    grads = [native.empty(h.device, t, t) if want and t is not None else None for t, want in zip(inputs, wanted)]
-    words, at = _addresses((x, y, post_gain, pre_gain, gate, scale, dout, dhidden, *grads),
-                           _NAMES + ("dx", "dy", "dpost_gain", "dgate", "dscale", "dpre_gain"), h.device)
-    params = NormParams(*at[2:6], bool(post_norm), bool(pre_norm), eps)
-    h._check(h._lib.residual_norm_grad(h.ptr, at[0], at[1], ctypes.byref(params), at[6], at[7],
-                                       ctypes.byref(_GradPointers(*at[8:]))))
+    status, grads = _describe().residual_norm_grad(_entry(1), h.ptr.value or 0, h.device, (x, y, post_gain, gate, scale, pre_gain),
+                                                   dout, dhidden, wanted, post_norm, pre_norm, eps)
+    h._check(status)
     return NormGrads(*grads)
 
 
