@@ -552,7 +552,9 @@ muon_status linear_cross_entropy_grad(muon_handle* handle, const muon_matrix* hi
  *   dhidden, dweight  as for linear_cross_entropy_grad
  * The alternatives are ranked by the raw logits (a soft cap keeps their order): the
  * top + 8 largest of the fp32 sums are summed again in 64 bits, so neighbours
- * nearer than an fp32 sum's error are in order too. Where fewer than `top` raw
+ * nearer than an fp32 sum's error are in order too. The target's logit, too, is summed
+ * in 64 bits: where it is the largest by far its error would be all of the log
+ * probability's. Where fewer than `top` raw
  * logits are above minus infinity the rest are token -1 with log probability
  * minus infinity; a NaN logit makes a token's values NaN and its alternatives -1.
  * The gradient takes the logits again, as its own product, and with the same

@@ -614,9 +614,11 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
             z = acc[mi][ni][q];
             acc[mi][ni][q] = none;
           }
-      if (cap) z = cap_any(z, a.softcap, a.cap_inv, slope);
-      if (mine) a.zt[r] = z;
-      if (mine && cap) a.zf[r] = slope;
+      if constexpr (MODE == LOGITS_LOSS) {       // (head_logprobs.hip takes the target's in 64 bits)
+        if (cap) z = cap_any(z, a.softcap, a.cap_inv, slope);
+        if (mine) a.zt[r] = z;
+        if (mine && cap) a.zf[r] = slope;
+      }
     }
     float top = kRefFloor;
     if constexpr (MODE == LOGITS_STATS) {

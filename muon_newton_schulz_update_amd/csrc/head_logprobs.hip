@@ -7,7 +7,8 @@
 //
 //   statistics    over tiles, with t the largest of all: S and E joined by
 //                 exp(m - t), E shifted by (m - t) S, the target's term added;
-//                 log p = -log1p(others / target's), H = log S - E log(2) / S
+//                 log p = -log1p(others / target's), H = log S - E log(2) / S;
+//                 the target's logit is summed again in 64 bits
 //   alternatives  a lane's set of logits is a candidate by its largest. The
 //                 top + kSpare best sets by (logit, lowest token) hold the top
 //                 alternatives, each as its set's largest unless a set has two
@@ -20,10 +21,10 @@
 // A block of four waves takes a token: its first reads (statistics, sets, target)
 // are asked for together, the sets stay in registers, and what bounds it is that
 // chain of dependent steps, most of all the candidates' rows of the weight (from
-// the caches: 3000 tokens x 28 of 4 KB are 344 MB). 50304 words: one token top 8
-// 12 us, 1536 tokens top 5 x 768 35, 3000 top 20 x 2048 111 (a wave a token 16, 42,
+// the caches: 3000 tokens x 29 of 4 KB are 356 MB). 50304 words: one token top 8
+// 13 us, 1536 tokens top 5 x 768 38, 3000 top 20 x 2048 115 (a wave a token 16, 42,
 // 149; sorting every set instead of a threshold 88, 166, 596); statistics alone,
-// 8192 tokens, 13 us, of which 52 MB are a read of 8.
+// 8192 tokens, 18 us, of which 52 MB and the targets' 25 are a read of 12.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -44,9 +45,18 @@ __device__ __forceinline__ float scaled_log2(float x, float y) { return __builti
 struct Stat {
   float top, sum, ent;
 };
-// The same over another, larger or equal, reference.
+// The same over another, larger or equal, reference t. The exponential of a
+// difference of 16 is off by 2^-20 from the rounding of its exponent alone (one word
+// or one tile may be all that others there are): what the difference, the product
+// and log2(e) lose is multiplied to it.
 __device__ __forceinline__ Stat over(const Stat& s, float t) {
-  const float x = scaled_log2(s.top, t), f = __builtin_amdgcn_exp2f(x);
+  const float x = scaled_log2(s.top, t);
+  float f = __builtin_amdgcn_exp2f(x);
+  if (x > -200.f) {
+    const float d = s.top - t, b = d - s.top, rest = (s.top - (d - b)) - (t + b);
+    const float lost = fmaf(d, kLog2e, -x) + fmaf(rest, kLog2e, d * 1.92596299e-8f);
+    f = fmaf(f, lost * kLn2, f);
+  }
   return {t, s.sum * f, f * (s.ent + s.sum * x)};
 }
 __device__ __forceinline__ Stat joined(const Stat& a, const Stat& b) {
@@ -78,26 +88,37 @@ __device__ __forceinline__ Stat tiles_stat(const HeadArgs& a, int r, int part, i
   return s;
 }
 
-// A token's place in the call, its target and the target's logit (nothing that
-// means anything where the target is outside the vocabulary).
+// A token's place in the call and its target (-1 outside the vocabulary).
 struct Token {
   int at, target;
-  float z;
 };
-__device__ __forceinline__ Token token_of(const HeadArgs& a, int r) { return {a.idx[a.row0 + r], a.tgt[a.row0 + r], a.zt[r]}; }
+__device__ __forceinline__ Token token_of(const HeadArgs& a, int r) { return {a.idx[a.row0 + r], a.tgt[a.row0 + r]}; }
+
+// The target's logit, from its raw one in 64 bits: a 32-bit value and what its
+// rounding lost. A word that the model has learnt has the largest logit by far, and a
+// 32-bit sum's error of it (2^-20 and more at 16) would be the log probability's and
+// the entropy's; the other words' average out.
+struct Logit {
+  float z, lost;
+};
+__device__ __forceinline__ Logit target_logit(const HeadArgs& a, double raw) {
+  const double c = a.softcap, y = c > 0 ? tanh(raw / c) * c : raw;
+  const float z = (float)y;
+  return {z, fabsf(z) < __builtin_inff() ? (float)(y - (double)z) : 0.f};
+}
 
 // {reference, log of the sum over it, entropy, log probability}
-__device__ __forceinline__ float4 token_stat(const Token& token, Stat s) {
-  const int tg = token.target;
-  const float z = tg >= 0 ? token.z : kRefFloor;
-  const float t = fmaxf(s.top, z), x = scaled_log2(s.top, t);
-  const float f = exp2f(x), others = s.sum * f;
-  float all = others, ent = f * (s.ent + s.sum * x), log_sum = logf(others), logp = kNan;
+__device__ __forceinline__ float4 token_stat(int tg, const Logit& own, Stat s) {
+  const float z = tg >= 0 ? own.z : kRefFloor;
+  const float t = fmaxf(s.top, z);
+  const Stat rest = over(s, t);
+  const float others = rest.sum;
+  float all = others, ent = rest.ent, log_sum = logf(others), logp = kNan;
   if (tg >= 0) {
-    const float y = scaled_log2(z, t), e = exp2f(y);
+    const float y = fmaf(own.lost, kLog2e, scaled_log2(z, t)), e = exp2f(y);
     all += e;
     ent += e * y;
-    log_sum = z == t ? log1pf(others) : logf(all);
+    log_sum = z == t ? log1pf(others + expm1f(own.lost)) : logf(all);
     logp = z - t > -40.f ? -log1pf(others / e) : (z - t) - logf(all);
   }
   if (!(t > kRefFloor)) log_sum = kNan;        // no logit above minus infinity, or none that is a number
@@ -150,39 +171,58 @@ __device__ __forceinline__ void merge_wave(Ranked<F>& x, const Ranked<F>& sorted
 // (Groups of 8 hold twice as many loads in flight, but fewer tokens fit a CU:
 // 3000 x top 20 x 2048 114 us, with 4 111; 1536 x top 5 38, 35.)
 constexpr int kGroup = 4;
-template <typename T>
-__device__ __forceinline__ void fine_logits(const T* h, const T* w, int64_t ld, int d, const int (&words)[kGroup], int lane,
-                                            double (&z)[kGroup]) {
+template <typename T, int G>
+__device__ __forceinline__ void fine_logits(const T* h, const T* w, int64_t ld, int d, const int (&words)[G], int lane,
+                                            double (&z)[G]) {
   constexpr int CH = 16 / (int)sizeof(T);
   auto value = [](T x) -> double {
     if constexpr (sizeof(T) == 2) return (double)bf2f(x);
     else return (double)x;
   };
 #pragma unroll
-  for (int g = 0; g < kGroup; ++g) z[g] = 0;
+  for (int g = 0; g < G; ++g) z[g] = 0;
   for (int c = lane * CH; c < d; c += 64 * CH) {
-    T x[CH], y[kGroup][CH];
+    T x[CH], y[G][CH];
     if (c + CH <= d) {
       __builtin_memcpy(x, h + c, 16);
 #pragma unroll
-      for (int g = 0; g < kGroup; ++g) __builtin_memcpy(y[g], w + words[g] * ld + c, 16);
+      for (int g = 0; g < G; ++g) __builtin_memcpy(y[g], w + words[g] * ld + c, 16);
     } else {
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         x[e] = c + e < d ? h[c + e] : T(0);
 #pragma unroll
-        for (int g = 0; g < kGroup; ++g) y[g][e] = c + e < d ? w[words[g] * ld + c + e] : T(0);
+        for (int g = 0; g < G; ++g) y[g][e] = c + e < d ? w[words[g] * ld + c + e] : T(0);
       }
     }
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
       const double v = value(x[e]);
 #pragma unroll
-      for (int g = 0; g < kGroup; ++g) z[g] = fma(v, value(y[g][e]), z[g]);
+      for (int g = 0; g < G; ++g) z[g] = fma(v, value(y[g][e]), z[g]);
     }
   }
 #pragma unroll
-  for (int g = 0; g < kGroup; ++g) z[g] = lanes_sum<64>(z[g]);
+  for (int g = 0; g < G; ++g) z[g] = lanes_sum<64>(z[g]);
+}
+
+// The caller's rows, whatever the products read.
+template <typename T>
+struct Operands {
+  const T *h, *w;
+  int64_t ld;
+  __device__ __forceinline__ Operands(const HeadArgs& a, int token)
+      : h((const T*)a.h + (int64_t)token * a.ld_h), w((const T*)(a.w_src ? a.w_src : a.w)), ld(a.w_src ? a.ld_src : a.ld_w) {}
+};
+// A token's raw target logit in 64 bits, by a wave.
+template <typename T>
+__device__ __forceinline__ double fine_target(const HeadArgs& a, const Token& token, int lane) {
+  if (token.target < 0) return 0;
+  const Operands<T> o(a, token.at);
+  const int words[1] = {token.target};
+  double z[1];
+  fine_logits(o.h, o.w, o.ld, a.d, words, lane, z);
+  return z[0];
 }
 
 constexpr int kNoToken = 0x7FFFFFFF;
@@ -224,6 +264,7 @@ struct TokenShare {
   Stat stat[kWaves];
   Found of[kWaves][64];            // each wave's sets
   int count[kWaves], total;
+  double target;                   // the target's raw logit
   Found sets[64];
   double z[64];
   int word[64];
@@ -329,31 +370,22 @@ __device__ __forceinline__ int candidate_sets(const HeadArgs& a, const uint2* be
   return sh.total;
 }
 
-// One token's alternatives.
+// One token's alternatives, and its values: its target's logit is summed beside theirs.
 template <typename T, int SETS>
 __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& token, const uint2* best, Sets<SETS>& e,
-                                             const float4& stat, int wave, int lane, TokenShare& sh) {
+                                             const Stat& others, int wave, int lane, TokenShare& sh) {
   const int i = token.at, target = token.target, top = a.top;
   float* logps = a.top_logprobs + (int64_t)i * top;
   int64_t* tokens = a.top_tokens + (int64_t)i * top;
-  if (stat.y != stat.y) {
-    if (wave == 0 && lane < top) {
-      logps[lane] = kNan;
-      tokens[lane] = -1;
-    }
-    return;
-  }
   int count = candidate_sets<T, SETS>(a, best, e, wave, lane, sh);
   // (no other of a set passes its second largest, nor its largest)
   const float bound = lane < count ? fminf(sh.sets[lane].bound, sh.sets[lane].z) : kNone;
   int word = lane < count ? sh.sets[lane].word : kNoToken;
-  if (target >= 0 && token.z > kNone) {          // (its set leaves it out)
+  if (target >= 0) {          // (its set leaves it out)
     if (lane == count) word = target;
     ++count;
   }
-  const T* h = (const T*)a.h + (int64_t)i * a.ld_h;
-  const T* w = (const T*)(a.w_src ? a.w_src : a.w);
-  const int64_t ld = a.w_src ? a.ld_src : a.ld_w;
+  const Operands<T> o(a, i);
   // the first n lanes' words with their 64-bit logits, to which every wave sums a
   // group at a time
   auto fine = [&](int words, int n) {
@@ -362,7 +394,7 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
       double z[kGroup];
 #pragma unroll
       for (int g = 0; g < kGroup; ++g) of[g] = __builtin_amdgcn_readlane(words, min(g0 + g, n - 1));
-      fine_logits(h, w, ld, a.d, of, lane, z);
+      fine_logits(o.h, o.w, o.ld, a.d, of, lane, z);
 #pragma unroll
       for (int g = 0; g < kGroup; ++g)
         if (lane == g && g0 + g < n) sh.z[g0 + g] = z[g];
@@ -371,6 +403,15 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
     return Ranked<double>{lane < n ? sh.z[lane] : -__builtin_inf(), lane < n ? words : kNoToken};
   };
   Ranked<double> found = fine(word, count);
+  const float4 stat = token_stat(target, target_logit(a, target >= 0 ? sh.z[count - 1] : 0.), others);
+  if (threadIdx.x == 0) put_stat(a, i, stat);
+  if (stat.y != stat.y) {
+    if (wave == 0 && lane < top) {
+      logps[lane] = kNan;
+      tokens[lane] = -1;
+    }
+    return;
+  }
   // ranks by counting who is in front
   int rank = 0;
   for (int k = 0; k < count; ++k)
@@ -435,6 +476,7 @@ __device__ __forceinline__ Stat wave_stat(Stat s) {
 }
 
 // Many tokens without alternatives: a wave a token.
+template <typename T>
 __global__ __launch_bounds__(256) void k_logprob_stats(HeadArgs a, int blocks) {
   if ((int)blockIdx.x >= blocks) {
     clear_ignored(a, ((int64_t)blockIdx.x - blocks) * 1024);
@@ -443,7 +485,8 @@ __global__ __launch_bounds__(256) void k_logprob_stats(HeadArgs a, int blocks) {
   const int lane = threadIdx.x & 63, r = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= piece_rows(a)) return;
   const Token token = token_of(a, r);
-  const float4 stat = token_stat(token, wave_stat(tiles_stat(a, r, lane, 64)));
+  const double target = fine_target<T>(a, token, lane);
+  const float4 stat = token_stat(token.target, target_logit(a, target), wave_stat(tiles_stat(a, r, lane, 64)));
   if (lane == 0) put_stat(a, token.at, stat);
 }
 
@@ -465,13 +508,16 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(HeadArgs a, int blocks) {
   if (a.top) e.load(best, a.n_vt, 0);
   Stat s = wave_stat(tiles_stat(a, r, threadIdx.x, kThreads));
   if (lane == 0) sh.stat[wave] = s;
+  if (a.top == 0 && wave == 0) {
+    const double target = fine_target<T>(a, token, lane);
+    if (lane == 0) sh.target = target;
+  }
   __syncthreads();
   s = sh.stat[0];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) s = joined(s, sh.stat[w]);
-  const float4 stat = token_stat(token, s);
-  if (threadIdx.x == 0) put_stat(a, token.at, stat);
-  if (a.top) alternatives<T, SETS>(a, token, best, e, stat, wave, lane, sh);
+  if (a.top) alternatives<T, SETS>(a, token, best, e, s, wave, lane, sh);
+  else if (threadIdx.x == 0) put_stat(a, token.at, token_stat(token.target, target_logit(a, sh.target), s));
 }
 
 // Statistics alone: tokens of which a block each goes faster than a wave each.
@@ -484,7 +530,8 @@ hipError_t launch_logprobs(const HeadArgs& a, int dt, hipStream_t s) {
   const int clear = a.row0 == 0 ? (int)cdiv(a.n, 1024) : 0;
   if (a.top == 0 && a.rows_max > kFewTokens) {
     const int blocks = (int)cdiv(a.rows_max, 4);
-    hipLaunchKernelGGL(k_logprob_stats, dim3(blocks + clear), dim3(256), 0, s, a, blocks);
+    if (dt != MUON_BF16) hipLaunchKernelGGL(k_logprob_stats<float>, dim3(blocks + clear), dim3(256), 0, s, a, blocks);
+    else hipLaunchKernelGGL(k_logprob_stats<u16>, dim3(blocks + clear), dim3(256), 0, s, a, blocks);
     return hipGetLastError();
   }
   const int blocks = a.rows_max;

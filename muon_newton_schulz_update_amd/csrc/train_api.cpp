@@ -212,7 +212,7 @@ muon_status head_run(muon_handle* h, const HeadCall& c) {
   const size_t o_count = take(16), o_idx = take(n * 4), o_tgt = take(n * 4), o_lossc = take(n * 4);
   const bool stats = c.mode == LOGITS_STATS, loss = c.mode == LOGITS_LOSS;
   const size_t o_hp = take(p * a.dp * e), o_tmax = take(loss ? p * a.n_vt * 4 : 0), o_tsum = take(loss ? p * a.n_vt * 4 : 0);
-  const size_t o_zt = take(p * 4), o_zf = take(c.softcap > 0.f ? p * 4 : 0), o_rs = take(p * 16);
+  const size_t o_zt = take(loss ? p * 4 : 0), o_zf = take(loss && c.softcap > 0.f ? p * 4 : 0), o_rs = take(p * 16);
   const size_t o_tstat = take(stats ? p * a.n_vt * 16 : 0), o_best = take(stats && c.top ? p * a.n_vt * a.sets * 8 : 0);
   const size_t o_ts = take(c.mode == LOGITS_GRAD ? p * 16 : 0);
   const size_t o_w = direct ? 0 : take((size_t)a.v * a.dp * e);
