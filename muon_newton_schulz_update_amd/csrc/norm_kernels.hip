@@ -294,6 +294,13 @@ __global__ __launch_bounds__(BLOCK) void k_residual_norm(NormArgs a) {
   }
 }
 
+template <int CH>
+__device__ __forceinline__ void add_products(const float (&a)[CH], const float (&b)[CH], double& sum) {
+#pragma unroll
+  for (int e = 0; e < CH; e += 4)
+    sum += (double)(fmaf(a[e], b[e], a[e + 1] * b[e + 1]) + fmaf(a[e + 2], b[e + 2], a[e + 3] * b[e + 3]));
+}
+
 // Waves to a SIMD that the backward pass is compiled for, where rows have several
 // waves: as many as the registers hold (a second raw row of 32-bit operands takes
 // twice as many), and four where a block alone has eight.
@@ -308,7 +315,8 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
   // gradients again where they are needed), and a second row (4096 x 4096 of 32
   // bits, with / without 117 / 88 us: it does not fit beside eight waves)
   constexpr bool WIDE = TPR == 1024, AHEAD = !WIDE && !(TPR >= 512 && sizeof(TX) == 4);
-  __shared__ float sh[4][2 * (BLOCK / 64)];
+  __shared__ float sh[3][2 * (BLOCK / 64)];
+  __shared__ double ones[BLOCK / 64][2];
   __shared__ float joined[ROWS > 1 ? BLOCK * CH : 1];
   const int t = threadIdx.x % TPR, d = a.d;
   const float inv_d = 1.f / d;
@@ -365,7 +373,9 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
   };
   // a single gate's gradient is that of the channels, weighted by post_gain in the end
   const bool vector = (a.want & kWantBlock) || ((a.want & kWantGateOne) && a.post_gain.ptr);
-  float sum_block[WIDE ? 1 : NC][CH], sum_scale[MORE ? NC : 1][CH], sum_pre[WIDE ? 1 : NC][CH], gate_one = 0.f, scale_one = 0.f;
+  float sum_block[WIDE ? 1 : NC][CH], sum_scale[MORE ? NC : 1][CH], sum_pre[WIDE ? 1 : NC][CH];
+  // (single values are sums over all elements, which may cancel: 64 bits past four)
+  double gate_one = 0, scale_one = 0;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
 #pragma unroll
@@ -472,10 +482,9 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
       if ((a.want & (kWantScale | kWantScaleOne)) && real) {
         unpack(now.x[k], x);
 #pragma unroll
-        for (int e = 0; e < CH; ++e) {
+        for (int e = 0; e < CH; ++e)
           if (MORE && (a.want & kWantScale)) sum_scale[MORE ? k : 0][e] = fmaf(dt[e], x[e], sum_scale[MORE ? k : 0][e]);
-          else scale_one = fmaf(dt[e], x[e], scale_one);
-        }
+        if (a.want & kWantScaleOne) add_products(dt, x, scale_one);
       }
       if (there) {
         float g[CH];
@@ -494,8 +503,7 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
           for (int e = 0; e < CH; ++e) sum[e] = fmaf(full ? dt[e] * g[e] : dt[e], y[k][e], sum[e]);
           keep(sum, 0, k);
         } else if ((a.want & kWantGateOne) && real) {
-#pragma unroll
-          for (int e = 0; e < CH; ++e) gate_one = fmaf(dt[e], y[k][e], gate_one);
+          add_products(dt, y[k], gate_one);
         }
 #pragma unroll
         for (int e = 0; e < CH; ++e) o[k][e] = dt[e] * (full ? w[e] * g[e] : w[e]);
@@ -563,20 +571,22 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
         load_param<TAIL, TPR == 16>(a.post_gain, CH * (k * TPR + t), d, post);
         fetch(sum_block[WIDE ? 0 : k], 0, k);
 #pragma unroll
-        for (int e = 0; e < CH; ++e) gate_one = fmaf(post[e], sum_block[WIDE ? 0 : k][e], gate_one);
+        for (int e = 0; e < CH; ++e) gate_one = fma((double)post[e], (double)sum_block[WIDE ? 0 : k][e], gate_one);
       }
     }
     gate_one = lanes_sum<64>(gate_one);
     scale_one = lanes_sum<64>(scale_one);
     if ((threadIdx.x & 63) == 0) {
-      sh[3][(threadIdx.x >> 6) * 2] = gate_one;
-      sh[3][(threadIdx.x >> 6) * 2 + 1] = scale_one;
+      ones[threadIdx.x >> 6][0] = gate_one;
+      ones[threadIdx.x >> 6][1] = scale_one;
     }
     __syncthreads();
     if (threadIdx.x < 2) {
-      float x = 0.f;
-      for (int w = 0; w < BLOCK / 64; ++w) x += sh[3][w * 2 + threadIdx.x];
-      part[threadIdx.x] = x;
+      double x = 0;
+      for (int w = 0; w < BLOCK / 64; ++w) x += ones[w][threadIdx.x];
+      const float high = (float)x;
+      part[threadIdx.x] = high;
+      part[2 + threadIdx.x] = fabsf(high) < __builtin_inff() ? (float)(x - (double)high) : 0.f;
     }
   }
 }
@@ -628,8 +638,8 @@ __global__ __launch_bounds__(1024) void k_norm_sums(NormSums a) {
     double x = 0, y = 0;
     for (int b = threadIdx.x; b < a.blocks; b += 64) {
       const float* p = a.part + b * a.part_floats + (int64_t)blockIdx.y * a.dp;
-      x += p[0];
-      y += p[1];
+      x += (double)p[0] + (double)p[2];
+      y += (double)p[1] + (double)p[3];
     }
     x = lanes_sum<64>(x);
     y = lanes_sum<64>(y);
