@@ -552,7 +552,8 @@ muon_status linear_cross_entropy_grad(muon_handle* handle, const muon_matrix* hi
  *   dhidden, dweight  as for linear_cross_entropy_grad
  * The alternatives are ranked by the raw logits (a soft cap keeps their order): the
  * top + 8 largest of the fp32 sums are summed again in 64 bits, so neighbours
- * nearer than an fp32 sum's error are in order too. The target's logit, too, is summed
+ * nearer than an fp32 sum's error are in order too (a word is out only where its
+ * fp32 sum is behind those of top + 8 others, in either precision). The target's logit, too, is summed
  * in 64 bits: where it is the largest by far its error would be all of the log
  * probability's. Where fewer than `top` raw
  * logits are above minus infinity the rest are token -1 with log probability

@@ -12,11 +12,11 @@
 //   alternatives  a lane's set of logits is a candidate by its largest. The
 //                 top + kSpare best sets by (logit, lowest token) hold the top
 //                 alternatives, each as its set's largest unless a set has two
-//                 of them, which its second largest tells: then all of the set
-//                 are candidates. Candidates are summed again in 64 bits (from
-//                 16-bit inputs every product is exact) and sorted. What is
-//                 outside the spare sets could only be in front by an error
-//                 of the 32-bit sums that passes over kSpare others.
+//                 words as large as the (top + kSpare)-th, which its second
+//                 largest tells: then all of the set are candidates. Candidates
+//                 are summed again in 64 bits (from 16-bit inputs every product
+//                 is exact) and sorted. What is outside could only be in front
+//                 by an error of the 32-bit sums that passes over kSpare others.
 //
 // A block of four waves takes a token: its first reads (statistics, sets, target)
 // are asked for together, the sets stay in registers, and what bounds it is that
@@ -423,14 +423,16 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
   }
   __syncthreads();
   found = {lane < count ? sh.z[lane] : -__builtin_inf(), lane < count ? sh.word[lane] : kNoToken};
-  // sets that may have two of the alternatives: all of them. Out is what is behind the
-  // last alternative by more than a 32-bit sum's error, or as large (no logit of a
-  // zero row or weight has an error) but of later words; more are out as the
-  // alternatives fill.
+  // sets that may have two of the alternatives: all of them. A set's other words are
+  // out only behind top + kSpare that are found, as its largest is behind those of as
+  // many sets: by the set's second sum in 32 bits, or as large (no logit of a zero row
+  // or weight has an error) but of later words. Its error goes with its products,
+  // however small the sum, so nothing short of other words' places makes up for it.
+  // More sets are out as the words fill.
   const double reach = (double)bound + fabs((double)bound) * 0x1p-18;
   auto whole = [&]() {
-    const double last = __shfl(found.z, top - 1);                       // (every lane takes part)
-    const int last_word = __shfl(found.token, top - 1);
+    const double last = __shfl(found.z, top + kSpare - 1);              // (every lane takes part)
+    const int last_word = __shfl(found.token, top + kSpare - 1);
     return __ballot(bound > kNone && !(reach < last || (reach == last && word > last_word)));
   };
   for (uint64_t todo = whole(); todo; todo = (todo & (todo - 1)) & whole()) {
