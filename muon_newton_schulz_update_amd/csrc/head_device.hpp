@@ -10,6 +10,7 @@ namespace muon {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+constexpr float kNoExp = -256.f;    // an exponent, base 2, whose power of 2 is 0 in 32 bits
 
 __device__ __forceinline__ float bf2f(u16 h) { return __uint_as_float((unsigned int)h << 16); }
 // Two values rounded to nearest even (the hardware's packed conversion).

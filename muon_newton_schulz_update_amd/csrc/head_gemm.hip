@@ -430,8 +430,9 @@ __device__ __forceinline__ void store_logits_grad(const HeadArgs& a, f32x16_t (&
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
       // log p, base 2, from a difference, which is as good as the logits however large
-      // these are (below 2^-126 p counts as 0: what it is multiplied by is no infinity)
-      const float y = __builtin_elementwise_maximum(fmaf(z[mi][q] - ts.x, kLog2e, ts.y), -126.f);
+      // these are (p is 0 past kNoExp, and what it is multiplied by no infinity: a word
+      // that the head masks may have a row as large as its type goes)
+      const float y = __builtin_elementwise_maximum(fmaf(z[mi][q] - ts.x, kLog2e, ts.y), kNoExp);
       e[q] = __builtin_amdgcn_exp2f(y) * fmaf(ts.w, y, ts.z);
     }
     if (cap) {

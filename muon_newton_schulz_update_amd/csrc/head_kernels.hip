@@ -181,7 +181,7 @@ __device__ __forceinline__ void logprob_factors(const HeadArgs& a, int r, int to
   const int tg = checked_target(a, target_at(a.targets, a.target_bytes, token));
   const float4 s = a.stats_in[token];
   const float gp = tg >= 0 && a.grad_logprobs ? a.grad_logprobs[token] : 0.f, ge = a.grad_entropy ? a.grad_entropy[token] : 0.f;
-  const float lp = __builtin_elementwise_maximum(s.w, -126.f / kLog2e);   // (as the other words': no infinity times 0)
+  const float lp = __builtin_elementwise_maximum(s.w, kNoExp * kLn2);   // (as the other words': no infinity times 0)
   a.ts[r] = float4{s.x, -s.y * kLog2e, -fmaf(ge, s.z, gp), -ge * kLn2};
   a.rs[r] = float4{0.f, 0.f, tg >= 0 ? -gp * expm1f(lp) - ge * expf(lp) * (lp + s.z) : 0.f, 0.f};
 }
