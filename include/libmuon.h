@@ -553,11 +553,13 @@ muon_status linear_cross_entropy_grad(muon_handle* handle, const muon_matrix* hi
  * The alternatives are ranked by the raw logits (a soft cap keeps their order): the
  * top + 8 largest of the fp32 sums are summed again in 64 bits, so neighbours
  * nearer than an fp32 sum's error are in order too (a word is out only where its
- * fp32 sum is behind those of top + 8 others, in either precision). The target's logit, too, is summed
- * in 64 bits: where it is the largest by far its error would be all of the log
- * probability's. Where fewer than `top` raw
- * logits are above minus infinity the rest are token -1 with log probability
- * minus infinity; a NaN logit makes a token's values NaN and its alternatives -1.
+ * fp32 sum is behind those of top + 8 others, in either precision). The target's
+ * logit, too, is summed in 64 bits, and where there are alternatives the largest of
+ * theirs counts so in the sums: where one is the largest by far its error would be all
+ * of its log probability's, and the others' sum is kept apart from it. Where fewer
+ * than `top` raw logits are above minus infinity the rest are token -1 with log
+ * probability minus infinity; a NaN logit, or one of infinity that no cap bounds,
+ * makes a token's values NaN and its alternatives -1.
  * The gradient takes the logits again, as its own product, and with the same
  * workspace as linear_cross_entropy_grad; a logit's gradient is rounded once, as
  * the products' operand, and the target's counts with 16 bits of a BF16's 8.

@@ -500,7 +500,8 @@ __device__ __forceinline__ void store_logits_grad(const HeadArgs& a, f32x16_t (&
 // Two workgroups of 256 x 128 to a CU, so that one's epilogue runs beside the
 // other's products, took 13 % longer (more operand traffic from LDS).
 //
-// LOGITS_STATS adds each tile's entropy to the statistics and, where alternatives
+// LOGITS_STATS adds each tile's entropy to the statistics, leaves one of the largest
+// out of the sum (two operations a logit: 1 % of the launch) and, where alternatives
 // are asked for, each set's largest logits; LOGITS_GRAD, with a token's statistics
 // from an earlier call, leaves the gradient itself (8192 x 50304 x 768, bf16:
 // statistics 570 us, 1.11 PFLOP/s with the matrix cores half busy; gradient 690,
@@ -629,20 +630,31 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
         constexpr int LANE_SETS = MI * 32 / kSetRows<T> > 0 ? MI * 32 / kSetRows<T> : 1;
         uint2* to = a.best + ((int64_t)r * a.n_vt + tile) * a.sets + (PAIR ? 2 * wm + hf : hf * LANE_SETS);
         top = fmaxf(top, store_best<T, MI>(&acc[0][ni], NI, to));
-      } else {
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-          for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
       }
-    } else {
+      if (cap) {
+        // (capped before their largest is taken: it is one of them to the last bit)
+        top = kRefFloor;
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+          float slope[16];
+          cap16(acc[mi][ni], a.softcap, a.cap_inv, slope);
+          if (edge) drop_past(acc[mi][ni], mi);
+          if (any_mine) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              if (mi * 32 + 8 * (q >> 2) + (q & 3) == tg) acc[mi][ni][q] = none;
+          }
+        }
+      }
+    }
+    if (MODE != LOGITS_STATS || cap || !a.top) {
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
         for (int q = 0; q < 16; ++q) top = fmaxf(top, acc[mi][ni][q]);
     }
     top = fmaxf(top, __shfl_xor(top, 32));
-    if (cap) {
+    if (MODE != LOGITS_STATS && cap) {
       float slope;
       top = cap_any(top, a.softcap, a.cap_inv, slope);
     }
@@ -655,12 +667,12 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
       ring_barrier();
       top = fmaxf(stat[0], stat[64]);
     }
-    float sum = 0.f, ent = 0.f;
+    float sum = 0.f, ent = 0.f, rest = 0.f;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       float e[16], slope[16];
       f32x16_t z = acc[mi][ni];
-      if (cap) {
+      if (MODE != LOGITS_STATS && cap) {
         cap16(z, a.softcap, a.cap_inv, slope);
         // (a few roundings can put one above the largest's, which for logits of
         // 10^8 and more is past what an exponential may say)
@@ -680,10 +692,13 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
         // is off by more than 1 past 2^24); no smaller than a kept exponential
         // can say (kCodeBase); a maximum that keeps NaN, so that one bad logit
         // reaches the token's loss
-        const float y = __builtin_elementwise_maximum((z[q] - top) * kLog2e, -63.f);
+        const float y = __builtin_elementwise_maximum((z[q] - top) * kLog2e, MODE == LOGITS_STATS ? kNoExp : -63.f);
         e[q] = __builtin_amdgcn_exp2f(y);
         sum += e[q];
-        if constexpr (MODE == LOGITS_STATS) ent = fmaf(e[q], y, ent);
+        if constexpr (MODE == LOGITS_STATS) {
+          ent = fmaf(e[q], y, ent);
+          rest += __builtin_amdgcn_fractf(e[q]);       // (all below 1)
+        }
       }
       if (MODE == LOGITS_STATS || !keep) continue;
       if (cap) {
@@ -718,21 +733,32 @@ __global__ __launch_bounds__((FEW ? 2 : waves_of<T, TILE>()) * 64, S > 5 ? 1 : 2
       }
     }
     sum += __shfl_xor(sum, 32);
-    if constexpr (MODE == LOGITS_STATS) ent += __shfl_xor(ent, 32);
+    if constexpr (MODE == LOGITS_STATS) {
+      ent += __shfl_xor(ent, 32);
+      rest += __shfl_xor(rest, 32);
+    }
     if constexpr (PAIR) {
       if (wm == 1 && hf == 0) {
         stat[128] = sum;
-        if constexpr (MODE == LOGITS_STATS) stat[192] = ent;
+        if constexpr (MODE == LOGITS_STATS) {
+          stat[192] = ent;
+          stat[256] = rest;
+        }
       }
       wait_lgkm0();
       ring_barrier();
       if (wm == 1) return;
       sum += stat[128];
-      if constexpr (MODE == LOGITS_STATS) ent += stat[192];
+      if constexpr (MODE == LOGITS_STATS) {
+        ent += stat[192];
+        rest += stat[256];
+      }
     }
     if (hf == 0) {
       if constexpr (MODE == LOGITS_STATS) {
-        a.tstat[(int64_t)r * a.n_vt + tile] = float4{top, sum, ent, 0.f};
+        // the sum without one of the largest: how many of these there are is a whole number
+        const float ones = rintf(sum - rest), one = ones > 0.f ? 1.f : 0.f;
+        a.tstat[(int64_t)r * a.n_vt + tile] = float4{top, rest + (ones - one), ent, one};
       } else {
         a.tmax[(int64_t)tile * a.piece + r] = top;
         a.tsum[(int64_t)tile * a.piece + r] = sum;

@@ -1,14 +1,17 @@
 // Log probabilities of given tokens under a language-model head, the
 // distribution's entropy and its likeliest tokens, from the statistics that the
 // logits' launch (head_gemm.hip) leaves of each token and tile: the largest logit
-// m, S = sum exp(z - m) and E = sum exp(z - m) log2 exp(z - m), both without the
-// target's term, and, for the alternatives, each lane's largest raw logit with
-// its place and its second largest.
+// m, S = sum exp(z - m) without one of the largest and E = sum exp(z - m) log2 exp(z -
+// m), both without the target's term, and, for the alternatives, each lane's largest
+// raw logit with its place and its second largest.
 //
 //   statistics    over tiles, with t the largest of all: S and E joined by
-//                 exp(m - t), E shifted by (m - t) S, the target's term added;
-//                 log p = -log1p(others / target's), H = log S - E log(2) / S;
-//                 the target's logit is summed again in 64 bits
+//                 exp(m - t), E shifted by (m - t) S; then over the leading
+//                 word, the target or the largest other one, whose term of 1
+//                 is in no sum: log p of it = -log1p(S), H = log1p(S) - E
+//                 log(2) / (1 + S), so a word that is nearly sure keeps all
+//                 bits of what it is not. Its logit is summed again in 64
+//                 bits, if it is the target or alternatives are asked for
 //   alternatives  a lane's set of logits is a candidate by its largest. The
 //                 top + kSpare best sets by (logit, lowest token) hold the top
 //                 alternatives, each as its set's largest unless a set has two
@@ -42,10 +45,12 @@ constexpr float kNan = __builtin_nanf("");
 // still takes for nothing (an exponent of minus infinity times 0 would be NaN).
 __device__ __forceinline__ float scaled_log2(float x, float y) { return __builtin_elementwise_maximum((x - y) * kLog2e, -1000.f); }
 
+// Sums over a reference, a logit of which one word is left out of `sum` (one: 1; its
+// exponential is 1 and its logarithm 0): beside it nothing of the others is lost.
 struct Stat {
-  float top, sum, ent;
+  float top, sum, ent, one;
 };
-// The same over another, larger or equal, reference t. The exponential of a
+// The same over another reference t, no smaller (or next to it). The exponential of a
 // difference of 16 is off by 2^-20 from the rounding of its exponent alone (one word
 // or one tile may be all that others there are): what the difference, the product
 // and log2(e) lose is multiplied to it.
@@ -57,16 +62,22 @@ __device__ __forceinline__ Stat over(const Stat& s, float t) {
     const float lost = fmaf(d, kLog2e, -x) + fmaf(rest, kLog2e, d * 1.92596299e-8f);
     f = fmaf(f, lost * kLn2, f);
   }
-  return {t, s.sum * f, f * (s.ent + s.sum * x)};
+  const bool same = s.top == t;
+  const float sum = same ? s.sum : s.sum + s.one;
+  return {t, sum * f, f * (s.ent + sum * x), same ? s.one : 0.f};
+}
+// Sums added up over one reference, `ones` of which have a word left out.
+__device__ __forceinline__ Stat settled(float t, float sum, float ent, float ones) {
+  return {t, sum + fmaxf(ones - 1.f, 0.f), ent, fminf(ones, 1.f)};
 }
 __device__ __forceinline__ Stat joined(const Stat& a, const Stat& b) {
   const float t = fmaxf(a.top, b.top);
   const Stat x = over(a, t), y = over(b, t);
-  return {t, x.sum + y.sum, x.ent + y.ent};
+  return settled(t, x.sum + y.sum, x.ent + y.ent, x.one + y.one);
 }
 // Every parts-th tile's, eight at a time over their common reference.
 __device__ __forceinline__ Stat tiles_stat(const HeadArgs& a, int r, int part, int parts) {
-  Stat s = {kRefFloor, 0.f, 0.f};
+  Stat s = {kRefFloor, 0.f, 0.f, 0.f};
   for (int t0 = part; t0 < a.n_vt; t0 += 8 * parts) {
     float4 x[8];
 #pragma unroll
@@ -80,10 +91,12 @@ __device__ __forceinline__ Stat tiles_stat(const HeadArgs& a, int r, int part, i
     s = over(s, top);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const Stat y = over(Stat{x[k].x, x[k].y, x[k].z}, top);
+      const Stat y = over(Stat{x[k].x, x[k].y, x[k].z, x[k].w}, top);
       s.sum += y.sum;
       s.ent += y.ent;
+      s.one += y.one;
     }
+    s = settled(top, s.sum, s.ent, s.one);
   }
   return s;
 }
@@ -94,41 +107,60 @@ struct Token {
 };
 __device__ __forceinline__ Token token_of(const HeadArgs& a, int r) { return {a.idx[a.row0 + r], a.tgt[a.row0 + r]}; }
 
-// The target's logit, from its raw one in 64 bits: a 32-bit value and what its
-// rounding lost. A word that the model has learnt has the largest logit by far, and a
-// 32-bit sum's error of it (2^-20 and more at 16) would be the log probability's and
-// the entropy's; the other words' average out.
+// A word's logit, from its raw one in 64 bits: a 32-bit value and what its rounding
+// lost. A word that the model is sure of has the largest logit by far, and a 32-bit
+// sum's error of it (2^-20 and more at 16) would be all of its log probability and much
+// of the entropy; the other words' average out. So the target's is taken in 64 bits,
+// and the largest of the alternatives', where these are asked for.
 struct Logit {
   float z, lost;
+  double exact;
 };
-__device__ __forceinline__ Logit target_logit(const HeadArgs& a, double raw) {
+__device__ __forceinline__ Logit fine_logit(const HeadArgs& a, double raw) {
   const double c = a.softcap, y = c > 0 ? tanh(raw / c) * c : raw;
   const float z = (float)y;
-  return {z, fabsf(z) < __builtin_inff() ? (float)(y - (double)z) : 0.f};
+  // (past 2^24 it would be more than 1, and 32-bit sums of the others as far off)
+  return {z, fabsf(z) < 0x1p24f ? (float)(y - (double)z) : 0.f, y};
 }
+__device__ __forceinline__ Logit rough_logit(float z) { return {z, 0.f, z}; }
 
-// {reference, log of the sum over it, entropy, log probability}
-__device__ __forceinline__ float4 token_stat(int tg, const Logit& own, Stat s) {
-  const float z = tg >= 0 ? own.z : kRefFloor;
-  const float t = fmaxf(s.top, z);
-  const Stat rest = over(s, t);
-  const float others = rest.sum;
-  float all = others, ent = rest.ent, log_sum = logf(others), logp = kNan;
-  if (tg >= 0) {
-    const float y = fmaf(own.lost, kLog2e, scaled_log2(z, t)), e = exp2f(y);
-    all += e;
-    ent += e * y;
-    log_sum = z == t ? log1pf(others + expm1f(own.lost)) : logf(all);
-    logp = z - t > -40.f ? -log1pf(others / e) : (z - t) - logf(all);
+struct TokenStat {
+  float4 of;        // {reference, log of the sum over it, entropy, log probability}
+  float others;     // all but the leading word's exponentials, over that word's
+  double lead;      // its logit
+  bool given;       // it is the target
+};
+// own: the target's logit; s: the others', of which the largest one has the logit alt.
+__device__ __forceinline__ TokenStat token_stat(int tg, const Logit& own, const Stat& s, const Logit& alt) {
+  const bool given = tg >= 0 && own.z >= alt.z;
+  const Logit& lead = given ? own : alt;
+  Stat rest = over(Stat{s.top, s.sum, s.ent, 0.f}, alt.z);
+  float target = 0.f, y = 0.f;
+  if (given) {
+    const float x = alt.lost * kLog2e, e = s.one * exp2f(x);
+    rest = over(Stat{alt.z, rest.sum + e, fmaf(e, x, rest.ent), 0.f}, own.z);
+  } else if (tg >= 0) {
+    y = fmaf(own.lost, kLog2e, scaled_log2(own.z, alt.z));
+    target = exp2f(y);
   }
-  if (!(t > kRefFloor)) log_sum = kNan;        // no logit above minus infinity, or none that is a number
+  // over the leading word's logit to the last bit
+  const float f = expf(-lead.lost);
+  target *= f;
+  const float words = rest.sum * f, others = words + target;
+  const float ent = f * rest.ent + target * y - others * (lead.lost * kLog2e), sum = log1pf(others);
+  float log_sum = lead.lost + sum, logp = kNan;
+  if (given) logp = -sum;
+  else if (tg >= 0) logp = own.z - alt.z > -40.f ? -log1pf((1.f + words) / target) : (own.z - alt.z) - log_sum;
+  // no logit above minus infinity, an infinite one, or none that is a number
+  if (!(lead.z > kRefFloor && lead.z < __builtin_inff())) log_sum = kNan;
   if (log_sum != log_sum) logp = kNan;
-  return {t, log_sum, log_sum - kLn2 * ent / all, logp};
+  return {{lead.z, log_sum, log_sum != log_sum ? kNan : sum - kLn2 * ent / (1.f + others), logp}, others, lead.exact, given};
 }
-__device__ __forceinline__ void put_stat(const HeadArgs& a, int i, const float4& s) {
+// stats: what the gradient takes, whose logits are 32-bit sums all of them
+__device__ __forceinline__ void put_stat(const HeadArgs& a, int i, const float4& s, const float4& stats) {
   a.loss[i] = s.w;
   if (a.entropy) a.entropy[i] = s.z;
-  if (a.stats) a.stats[i] = s;
+  if (a.stats) a.stats[i] = float4{stats.x, stats.y, stats.z, s.w};
 }
 
 // Sorting over a wave, lane 0 first: larger values, then smaller tokens.
@@ -381,6 +413,12 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
   // (no other of a set passes its second largest, nor its largest)
   const float bound = lane < count ? fminf(sh.sets[lane].bound, sh.sets[lane].z) : kNone;
   int word = lane < count ? sh.sets[lane].word : kNoToken;
+  // the one that the statistics have as their largest
+  const float z32 = lane < count ? sh.sets[lane].z : kNone;
+  const float most = over_lanes<64>(z32, [](float x, float y) { return fmaxf(x, y); });      // (every lane takes part)
+  const uint64_t largest = __ballot(z32 > kNone && z32 == most);
+  const int first_lane = largest ? __builtin_ctzll(largest) : -1;
+  const int first = largest ? __builtin_amdgcn_readlane(word, __builtin_ctzll(largest)) : kNoToken;
   if (target >= 0) {          // (its set leaves it out)
     if (lane == count) word = target;
     ++count;
@@ -403,9 +441,13 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
     return Ranked<double>{lane < n ? sh.z[lane] : -__builtin_inf(), lane < n ? words : kNoToken};
   };
   Ranked<double> found = fine(word, count);
-  const float4 stat = token_stat(target, target_logit(a, target >= 0 ? sh.z[count - 1] : 0.), others);
-  if (threadIdx.x == 0) put_stat(a, i, stat);
-  if (stat.y != stat.y) {
+  const Logit own = fine_logit(a, target >= 0 ? sh.z[count - 1] : 0.);
+  Logit alt = first_lane < 0 ? rough_logit(kRefFloor) : fine_logit(a, sh.z[first_lane]);
+  // (a sum further off than that has lost all that these are for)
+  if (!(fabsf(alt.z - others.top) < 64.f)) alt = rough_logit(others.top);
+  const TokenStat stat = token_stat(target, own, others, alt);
+  if (threadIdx.x == 0) put_stat(a, i, stat.of, token_stat(target, own, others, rough_logit(others.top)).of);
+  if (stat.of.y != stat.of.y) {
     if (wave == 0 && lane < top) {
       logps[lane] = kNan;
       tokens[lane] = -1;
@@ -436,9 +478,9 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
     return __ballot(bound > kNone && !(reach < last || (reach == last && word > last_word)));
   };
   for (uint64_t todo = whole(); todo; todo = (todo & (todo - 1)) & whole()) {
-    const int first = __builtin_amdgcn_readlane(word, __builtin_ctzll(todo));
-    const int member = first / a.vtile * a.vtile + set_column<T, SETS>(column_set<T, SETS>(first % a.vtile), lane);
-    const bool in = lane < kSetRows<T> / 2 && member < a.v && member != first && member != target;
+    const int known = __builtin_amdgcn_readlane(word, __builtin_ctzll(todo));
+    const int member = known / a.vtile * a.vtile + set_column<T, SETS>(column_set<T, SETS>(known % a.vtile), lane);
+    const bool in = lane < kSetRows<T> / 2 && member < a.v && member != known && member != target;
     // the members side by side in the first lanes
     const uint64_t mask = __ballot(in);
     __syncthreads();
@@ -452,7 +494,9 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
   if (wave != 0 || lane >= top) return;
   const bool there = found.token != kNoToken && found.z > -__builtin_inf();
   const double c = a.softcap, z = c > 0 ? tanh(found.z / c) * c : found.z;
-  logps[lane] = !there ? kNone : found.token == target ? stat.w : (float)((z - stat.x) - stat.y);
+  // (the leading word's difference is 0 in every bit)
+  const double less = !stat.given && found.token == first ? 0. : z - stat.lead;
+  logps[lane] = !there ? kNone : found.token == target ? stat.of.w : (float)(less - log1p((double)stat.others));
   tokens[lane] = there ? found.token : -1;
 }
 
@@ -472,9 +516,7 @@ __device__ __forceinline__ void clear_ignored(const HeadArgs& a, int64_t from) {
 // All of a wave's statistics joined, the same in every lane.
 __device__ __forceinline__ Stat wave_stat(Stat s) {
   s = over(s, over_lanes<64>(s.top, [](float x, float y) { return fmaxf(x, y); }));
-  s.sum = lanes_sum<64>(s.sum);
-  s.ent = lanes_sum<64>(s.ent);
-  return s;
+  return settled(s.top, lanes_sum<64>(s.sum), lanes_sum<64>(s.ent), lanes_sum<64>(s.one));
 }
 
 // Many tokens without alternatives: a wave a token.
@@ -488,8 +530,9 @@ __global__ __launch_bounds__(256) void k_logprob_stats(HeadArgs a, int blocks) {
   if (r >= piece_rows(a)) return;
   const Token token = token_of(a, r);
   const double target = fine_target<T>(a, token, lane);
-  const float4 stat = token_stat(token.target, target_logit(a, target), wave_stat(tiles_stat(a, r, lane, 64)));
-  if (lane == 0) put_stat(a, token.at, stat);
+  const Stat s = wave_stat(tiles_stat(a, r, lane, 64));
+  const float4 stat = token_stat(token.target, fine_logit(a, target), s, rough_logit(s.top)).of;
+  if (lane == 0) put_stat(a, token.at, stat, stat);
 }
 
 // A block a token.
@@ -519,7 +562,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(HeadArgs a, int blocks) {
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) s = joined(s, sh.stat[w]);
   if (a.top) alternatives<T, SETS>(a, token, best, e, s, wave, lane, sh);
-  else if (threadIdx.x == 0) put_stat(a, token.at, token_stat(token.target, target_logit(a, sh.target), s));
+  else if (threadIdx.x == 0) {
+    const float4 stat = token_stat(token.target, fine_logit(a, sh.target), s, rough_logit(s.top)).of;
+    put_stat(a, token.at, stat, stat);
+  }
 }
 
 // Statistics alone: tokens of which a block each goes faster than a wave each.

@@ -165,8 +165,9 @@ struct HeadArgs {
   // log probabilities (head_logprobs.hip); loss holds them
   int32_t top;                        // alternatives a token
   int32_t sets;                       // sets of a statistic's vocabulary columns
-  float4* tstat;                      // piece x n_vt: largest logit, sum of exponentials over it, sum of exponential
-                                      // times its logarithm (base 2), all without the target's
+  float4* tstat;                      // piece x n_vt, without the target: largest logit, sum of exponentials over it
+                                      // without one of the largest, sum of exponential times its logarithm (base 2),
+                                      // 1 (0: no logit above minus infinity)
   uint2* best;                        // piece x n_vt x sets: each one's largest logit, its place and the second largest
   float* entropy;                     // caller's, n each, or null
   float4* stats;
