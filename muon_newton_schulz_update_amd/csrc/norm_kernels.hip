@@ -325,14 +325,18 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   Row<TX, TY, TPR, NC, CH, FORM, true> now, next;
   if (AHEAD) next.load(a, min(row, a.n - 1), t);
-  // gate and post_gain multiplied (post_gain alone where the gate is full)
+  // gate and post_gain multiplied (post_gain alone where the gate is full or single:
+  // a single one's gradient takes what comes to yhat without it)
+  const float gate1 = a.gate.kind == NORM_ONE ? one_value(a.gate, 0) : 1.f;
   auto load_gated = [&](int k, float (&v)[CH]) {
     const int c = CH * (k * TPR + t);
-    float post[CH];
-    load_param<TAIL, TPR == 16>(a.post_gain, c, d, post);
-    load_param<TAIL, TPR == 16>(a.gate, c, d, v);
+    load_param<TAIL, TPR == 16>(a.post_gain, c, d, v);
+    if (a.gate.kind == NORM_CHANNELS) {
+      float gate[CH];
+      load_param<TAIL, TPR == 16>(a.gate, c, d, gate);
 #pragma unroll
-    for (int e = 0; e < CH; ++e) v[e] *= post[e];
+      for (int e = 0; e < CH; ++e) v[e] *= gate[e];
+    }
   };
   float scale[MORE ? NC : 1][CH], gated[WIDE ? 1 : NC][CH], pre[WIDE ? 1 : NC][CH];
   const float scale1 = a.scale.kind == NORM_ONE ? one_value(a.scale, 0) : 1.f;
@@ -371,10 +375,10 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
       for (int e = 0; e < CH; e += 4)
         kept[which][(k * (CH / 4) + e / 4) * BLOCK + threadIdx.x] = (f32x4_t){sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
   };
-  // a single gate's gradient is that of the channels, weighted by post_gain in the end
-  const bool vector = (a.want & kWantBlock) || ((a.want & kWantGateOne) && a.post_gain.ptr);
+  const bool vector = a.want & kWantBlock, gate_sum = (a.want & kWantGateOne) && a.post_gain.ptr;
   float sum_block[WIDE ? 1 : NC][CH], sum_scale[MORE ? NC : 1][CH], sum_pre[WIDE ? 1 : NC][CH];
-  // (single values are sums over all elements, which may cancel: 64 bits past four)
+  // (single values are sums over all elements, which may cancel: 64 bits past four, or
+  // beside a post_gain past a thread's part of a row, which the way back has anyway)
   double gate_one = 0, scale_one = 0;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
@@ -423,7 +427,7 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
         if (full) unpack(now.g[MORE ? k : 0], g);
         const float (&w)[CH] = gated_of(k);
 #pragma unroll
-        for (int e = 0; e < CH; ++e) o[k][e] = fmaf(full ? w[e] * g[e] : w[e], y[k][e], o[k][e]);
+        for (int e = 0; e < CH; ++e) o[k][e] = fmaf(full ? w[e] * g[e] : w[e] * gate1, y[k][e], o[k][e]);
       }
     }
     float r2 = 0.f, m = 0.f;
@@ -502,27 +506,32 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
 #pragma unroll
           for (int e = 0; e < CH; ++e) sum[e] = fmaf(full ? dt[e] * g[e] : dt[e], y[k][e], sum[e]);
           keep(sum, 0, k);
-        } else if ((a.want & kWantGateOne) && real) {
-          add_products(dt, y[k], gate_one);
         }
+        if ((a.want & kWantGateOne) && !a.post_gain.ptr && real) add_products(dt, y[k], gate_one);
 #pragma unroll
         for (int e = 0; e < CH; ++e) o[k][e] = dt[e] * (full ? w[e] * g[e] : w[e]);
       }
     }
-    if (there && a.dy.ptr) {
+    if (there && (a.dy.ptr || gate_sum)) {
       if (a.post) {
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
           for (int e = 0; e < CH; ++e) v[0] = fmaf(o[k][e], y[k][e], v[0]);
+        if (gate_sum && real) gate_one += (double)v[0];
         row_sums<TPR>(v, sh[2]);
-        const float back = v[0] * inv_d;
+        const float back = v[0] * inv_d, by = r1 * gate1;
 #pragma unroll
         for (int k = 0; k < NC; ++k)
 #pragma unroll
-          for (int e = 0; e < CH; ++e) o[k][e] = r1 * (o[k][e] - y[k][e] * back);
+          for (int e = 0; e < CH; ++e) o[k][e] = by * (o[k][e] - y[k][e] * back);
+      } else {
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+          for (int e = 0; e < CH; ++e) o[k][e] *= gate1;
       }
-      if (real)
+      if (a.dy.ptr && real)
 #pragma unroll
         for (int k = 0; k < NC; ++k) store_chunk<TAIL>((TY*)a.dy.ptr + row * a.dy.ld, CH * (k * TPR + t), d, o[k]);
     }
@@ -564,16 +573,6 @@ __global__ __launch_bounds__(BLOCK, waves_wanted(TPR, NC, FORM == FORM_MORE, siz
     if (a.want & kWantScale) leave(sum_scale, 2);
   if (a.want & kWantPre) leave(sum_pre, 1);
   if (a.want & (kWantGateOne | kWantScaleOne)) {
-    if (vector) {
-#pragma unroll
-      for (int k = 0; k < NC; ++k) {
-        float post[CH];
-        load_param<TAIL, TPR == 16>(a.post_gain, CH * (k * TPR + t), d, post);
-        fetch(sum_block[WIDE ? 0 : k], 0, k);
-#pragma unroll
-        for (int e = 0; e < CH; ++e) gate_one = fma((double)post[e], (double)sum_block[WIDE ? 0 : k][e], gate_one);
-      }
-    }
     gate_one = lanes_sum<64>(gate_one);
     scale_one = lanes_sum<64>(scale_one);
     if ((threadIdx.x & 63) == 0) {
