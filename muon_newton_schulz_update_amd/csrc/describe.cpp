@@ -259,6 +259,10 @@ PyObject* residual_norm_of(PyObject*, PyObject* args) {
   double eps;
   if (!PyArg_ParseTuple(args, "KKlO!ppdO", &entry, &handle, &device, &PyTuple_Type, &inputs, &post_norm, &pre_norm, &eps, &dtype))
     return nullptr;
+  if (dtype != Py_None && !THPDtype_Check(dtype)) {
+    PyErr_Format(PyExc_TypeError, "dtype: expected a torch.dtype or None, got %s", Py_TYPE(dtype)->tp_name);
+    return nullptr;
+  }
   try {
     NormCall c;
     if (!norm_inputs(inputs, device, post_norm, pre_norm, eps, c)) return nullptr;
