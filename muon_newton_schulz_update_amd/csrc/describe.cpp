@@ -8,7 +8,9 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <ATen/Functions.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -186,6 +188,30 @@ PyObject* device_of(PyObject*, PyObject* arg) {
   return PyLong_FromLong(device);
 }
 
+// leaf_elsewhere(tensors) -> whether what adds to the gradient of one of them, a leaf,
+// is there already and runs on another stream than the current one of its device
+PyObject* leaf_elsewhere(PyObject*, PyObject* arg) {
+  PyObject* list = PySequence_Fast(arg, "expected a sequence of tensors");
+  if (!list) return nullptr;
+  bool found = false, ok = true;
+  try {
+    for (Py_ssize_t i = 0; !found && i < PySequence_Fast_GET_SIZE(list); ++i) {
+      PyObject* o = PySequence_Fast_GET_ITEM(list, i);
+      if (!THPVariable_Check(o)) continue;
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (!t.is_cuda() || !t.requires_grad() || t.grad_fn()) continue;
+      const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+      const auto stream = node ? node->stream() : std::nullopt;
+      found = stream && *stream != c10::impl::VirtualGuardImpl(at::kCUDA).getStream(t.device());
+    }
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    ok = false;
+  }
+  Py_DECREF(list);
+  return ok ? PyBool_FromLong(found) : nullptr;
+}
+
 // empty(device, shape_of=None, type_of=None) -> a contiguous tensor on the GPU:
 // the shape of one tensor (None: a scalar), the type of another (None: float32)
 PyObject* empty(PyObject*, PyObject* args) {
@@ -352,6 +378,7 @@ PyMethodDef methods[] = {
     {"pack_rows", pack_rows, METH_VARARGS, "Descriptors of tensors as rows, as bytes, and their address."},
     {"residual_norm", residual_norm_of, METH_VARARGS, "Results of residual_norm, after its status."},
     {"residual_norm_grad", residual_norm_grad_of, METH_VARARGS, "Gradients of residual_norm_grad, after its status."},
+    {"leaf_elsewhere", leaf_elsewhere, METH_O, "Whether a leaf's gradient is added on another stream than the current one."},
     {"device_of", device_of, METH_O, "Index of the first tensor on a GPU, or -1."},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -99,7 +99,7 @@ def linear_logprobs_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: to
 class _LinearLogProbs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, targets, top, softcap, ignore_index, handle):
-        _one_stream_a_leaf(ctx, hidden.get_device())
+        _one_stream_a_leaf((hidden, weight))
         out = _call(hidden, weight, targets, top, softcap, ignore_index, handle)
         ctx.options = (softcap, ignore_index, handle)
         ctx.save_for_backward(hidden, weight, targets, out[4])

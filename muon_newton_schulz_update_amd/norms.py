@@ -71,7 +71,7 @@ class _ResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, post_gain, gate, scale, pre_gain, *options):
         post_norm, pre_norm, eps, dtype, handle = ctx.options = options
-        _one_stream_a_leaf(ctx, x.get_device())
+        _one_stream_a_leaf((x, y, post_gain, gate, scale, pre_gain))
         ctx.save_for_backward(x, y, post_gain, gate, scale, pre_gain)
         ctx.set_materialize_grads(False)
         return _forward(x, y, post_gain, gate, scale, pre_gain, post_norm, pre_norm, eps, dtype, handle)

@@ -62,19 +62,14 @@ def _handle_for(tensors, handle):
     return handle
 
 
-def _one_stream_a_leaf(ctx, device: int) -> None:
+def _one_stream_a_leaf(tensors):
     """For a Function's forward: what adds to a leaf's gradient runs on the stream
-    where the leaf was first used, and lives as long as a result of it. If that is an
-    eager result of another stream, a backward pass cannot be captured, and torch
-    finds out too late to go on: refused here."""
-    if device < 0:
-        return
-    stream = torch._C._cuda_getCurrentRawStream(device)
-    for node, _ in ctx.next_functions:
-        if type(node).__name__ == "AccumulateGrad" and node.metadata.setdefault("libmuon stream", stream) != stream and \
-                torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("a graph captures a result whose leaf has an eager result on another stream: delete that "
-                               "first (with all that was made from it), or capture the call of the gradient itself")
+    where the leaf was first used, by whatever operator, and lives as long as a result
+    of it. If that is an eager result of another stream, a backward pass cannot be
+    captured, and torch finds out too late to go on: refused here."""
+    if _describe().leaf_elsewhere(tensors) and torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("a graph captures a result whose leaf has an eager result on another stream: delete that "
+                           "first (with all that was made from it), or capture the call of the gradient itself")
 
 
 def _scalar(t: torch.Tensor | None, what: str, device: int, n: int | None = None, dtype=torch.float32):
