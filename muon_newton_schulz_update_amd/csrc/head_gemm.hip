@@ -1181,8 +1181,11 @@ int tile_of(int dt, int rows, int64_t tiles256, int64_t tiles128) {
   return tiles128 >= kFewSmallTiles ? 128 : 64;
 }
 // Statistics with entropy of one row of tokens: 64-tiles that all run at once, four
-// to a CU (one token x 50304 x 768: 64 / 128 16.6 / 18.1 us; the loss alone keeps
-// the order of its sums).
+// to a CU, which is worth a little for the narrower heads (one token x 50304 x 768:
+// 64 / 128 16.6 / 18.1 us; whole calls, weights in turn: one token x 50304 x 768 24.3 /
+// 25.2, x 65536 x 768 28.5 / 29.2, x 65536 x 2048 72.4 / 74.1, x 32000 x 768 to 4096
+// within 2 %, x 50304 x 2048 60.1 / 57.5, 64 tokens there 64.6 / 59.2; more tiles than
+// that: 128000 x 2048 134.7 / 126.0). The loss alone keeps the order of its sums.
 constexpr int kAllSmallTiles = 1024;
 // The gradients' tiles also go by their own shape (whole calls):
 //   few tokens: dW's K is short, its tiles all start-up and epilogue, which two

@@ -568,8 +568,12 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(HeadArgs a, int blocks) {
   }
 }
 
-// Statistics alone: tokens of which a block each goes faster than a wave each.
-constexpr int kFewTokens = 512;
+// Statistics alone: tokens of which a block each goes faster than a wave each, where
+// the vocabulary is large (whole calls, a block / a wave each: 1 and 64 tokens x 50304
+// x 768 21.5 / 21.9 and 22.7 / 23.4 us, x 128000 x 768 40.4 / 41.0 and 41.5 / 42.2, x
+// 8000 x 768 12.2 / 11.6 and 13.2 / 12.7; 256 tokens 38.7 / 38.3, 66.1 / 66.5 and 18.7
+// / 18.2; 2048 x 8000 x 768 49 / 45).
+constexpr int kFewTokens = 64;
 inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
 
 }  // namespace

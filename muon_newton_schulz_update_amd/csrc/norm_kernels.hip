@@ -655,9 +655,12 @@ __global__ __launch_bounds__(1024) void k_norm_sums(NormSums a) {
 // sixteen threads up to 128 channels, a wave up to 512, then as many threads as
 // there are chunks. Up to 768 a wave takes three chunks of 4 (two of 8 would leave
 // a quarter of its lanes nothing), but for the forward pass of 16-bit rows two
-// waves are faster, most for few rows (one row of 768: 3.2 / 4.0 us, 8192: 11.1 /
-// 12.2; of 32 bits 17.2 / 15.7; backward 8192 x 768 the same within 2 %, of 32 bits
-// 42 / 30). Up to 8192 the backward pass has the registers of eight waves for two
+// waves are faster where there are few (two waves / one: one row of 768 3.2 / 4.0 us,
+// 8192 9.9 / 9.9, of 32 bits 16.5 / 15.1). Between the two widths, 8192 rows:
+// forward, 16 bits, 520 8.7 / 8.4, 640 9.2 / 9.0, 700 11.1 / 9.9, 32 bits beside 16
+// 10.1 / 10.3, 11.5 / 11.3, 13.5 / 12.7, 32 bits 13.0 / 11.3, 14.2 / 12.8, 17.1 / 14.5;
+// backward 19.7 / 18.9, 20.5 / 20.1, 24.8 / 20.5 and of 32 bits 25.7 / 24.0, 27.0 / 26.6,
+// 32.5 / 28.3. Up to 8192 the backward pass has the registers of eight waves for two
 // chunks a thread, the forward one of sixteen for one (2048 x 8192: backward 43 / 56
 // us, forward 23.5 / 22.5).
 #define BY_WIDTH(d, RUN, RUN_768, RUN_8192)               \
