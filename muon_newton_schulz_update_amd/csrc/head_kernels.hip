@@ -342,7 +342,9 @@ __global__ __launch_bounds__(1024) void k_merge(HeadArgs a, int grad) {
 // kilobytes. Rows past the valid ones (up to a whole panel, a stage of dW) and
 // columns past the vocabulary (a stage of dH) become zero. Bound by HBM: a
 // read and a write of every exponential (8192 x 50304 in 16 bits 300 us, 5.5
-// TB/s). The vocabulary is taken from its end, which the logits' launch wrote
+// TB/s). The lowest kept exponential, 2^-63 of its tile's largest, stands for all
+// below it and counts as 0 (a word that the head masks may have a row as large as
+// its type goes). The vocabulary is taken from its end, which the logits' launch wrote
 // last and the last-level cache still has, to its start, where the weight's
 // gradient begins (from the start 320 us). With few tiles (merged = 0) every
 // block merges its tokens' statistics itself, which costs less than a kernel.
@@ -393,13 +395,14 @@ __global__ __launch_bounds__(256) void k_dlogits(HeadArgs a, int merged, int blo
         const u32x4_t q = *(const u32x4_t*)p;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[2 * e] = __uint_as_float(((q[e] & 0xFFFFu) + kCodeBase) << 13);
-          x[2 * e + 1] = __uint_as_float(((q[e] >> 16) + kCodeBase) << 13);
+          const uint32_t lo = q[e] & 0xFFFFu, hi = q[e] >> 16;
+          x[2 * e] = lo ? __uint_as_float((lo + kCodeBase) << 13) : 0.f;
+          x[2 * e + 1] = hi ? __uint_as_float((hi + kCodeBase) << 13) : 0.f;
         }
       } else {
         const f32x4_t q = *(const f32x4_t*)p;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = q[e];
+        for (int e = 0; e < 4; ++e) x[e] = q[e] == 0x1p-63f ? 0.f : q[e];
       }
 #pragma unroll
       for (int e = 0; e < CH; ++e) x[e] *= f;
