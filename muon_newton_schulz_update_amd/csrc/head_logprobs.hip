@@ -470,15 +470,21 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
   // many sets: by the set's second sum in 32 bits, or as large (no logit of a zero row
   // or weight has an error) but of later words. Its error goes with its products,
   // however small the sum, so nothing short of other words' places makes up for it.
-  // More sets are out as the words fill.
+  // The largest second goes first: more sets are out as the words fill (3000 tokens x
+  // 1000 words, top 20, in any order / so: 425 / 314 us).
   const double reach = (double)bound + fabs((double)bound) * 0x1p-18;
-  auto whole = [&]() {
+  uint64_t left = ~0ull;
+  auto next_set = [&]() {
     const double last = __shfl(found.z, top + kSpare - 1);              // (every lane takes part)
     const int last_word = __shfl(found.token, top + kSpare - 1);
-    return __ballot(bound > kNone && !(reach < last || (reach == last && word > last_word)));
+    const bool in = bound > kNone && !(reach < last || (reach == last && word > last_word)) && (left >> lane & 1);
+    if (!__any(in)) return -1;
+    const float of = in ? bound : kNone, most = over_lanes<64>(of, [](float x, float y) { return fmaxf(x, y); });
+    return __builtin_ctzll(__ballot(of == most));
   };
-  for (uint64_t todo = whole(); todo; todo = (todo & (todo - 1)) & whole()) {
-    const int known = __builtin_amdgcn_readlane(word, __builtin_ctzll(todo));
+  for (int at = next_set(); at >= 0; at = next_set()) {
+    left &= ~(1ull << at);
+    const int known = __builtin_amdgcn_readlane(word, at);
     const int member = known / a.vtile * a.vtile + set_column<T, SETS>(column_set<T, SETS>(known % a.vtile), lane);
     const bool in = lane < kSetRows<T> / 2 && member < a.v && member != known && member != target;
     // the members side by side in the first lanes
