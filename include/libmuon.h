@@ -558,8 +558,9 @@ muon_status linear_cross_entropy_grad(muon_handle* handle, const muon_matrix* hi
  * theirs counts so in the sums: where one is the largest by far its error would be all
  * of its log probability's, and the others' sum is kept apart from it. Where fewer
  * than `top` raw logits are above minus infinity the rest are token -1 with log
- * probability minus infinity; a NaN logit, or one of infinity that no cap bounds,
- * makes a token's values NaN and its alternatives -1.
+ * probability minus infinity; a NaN logit makes a token's values NaN and its
+ * alternatives -1, and so does one of infinity that no cap bounds (the target's
+ * leaves the alternatives' tokens).
  * The gradient takes the logits again, as its own product, and with the same
  * workspace as linear_cross_entropy_grad; a logit's gradient is rounded once, as
  * the products' operand, and the target's counts with 16 bits of a BF16's 8.

@@ -151,10 +151,11 @@ __device__ __forceinline__ TokenStat token_stat(int tg, const Logit& own, const 
   float log_sum = lead.lost + sum, logp = kNan;
   if (given) logp = -sum;
   else if (tg >= 0) logp = own.z - alt.z > -40.f ? -log1pf((1.f + words) / target) : (own.z - alt.z) - log_sum;
-  // no logit above minus infinity, an infinite one, or none that is a number
-  if (!(lead.z > kRefFloor && lead.z < __builtin_inff())) log_sum = kNan;
-  if (log_sum != log_sum) logp = kNan;
-  return {{lead.z, log_sum, log_sum != log_sum ? kNan : sum - kLn2 * ent / (1.f + others), logp}, others, lead.exact, given};
+  float entropy = sum - kLn2 * ent / (1.f + others);
+  if (!(lead.z > kRefFloor)) log_sum = kNan;   // no logit above minus infinity, or none that is a number
+  // (an infinite target leaves the alternatives their order)
+  if (log_sum != log_sum || lead.z == __builtin_inff()) logp = entropy = kNan;
+  return {{lead.z, log_sum, entropy, logp}, others, lead.exact, given};
 }
 // stats: what the gradient takes, whose logits are 32-bit sums all of them
 __device__ __forceinline__ void put_stat(const HeadArgs& a, int i, const float4& s, const float4& stats) {

@@ -66,3 +66,19 @@ def test_words_that_are_equal_in_32_bits(n, top, where, dtype):
     t = torch.arange(n, device="cuda") % 2000
     t[0] = words[1]
     assert torch.equal(mu.linear_logprobs(h, w, t, top=top).top_tokens, order(h, w, top))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n", [2, 90])
+def test_an_infinite_target_leaves_the_alternatives(n, dtype):
+    """Its values are no numbers, as another word's infinity makes them; the alternatives are in order behind it."""
+    h = torch.randn((n, 32), generator=gen(3), device="cuda").to(dtype)
+    w = torch.randn((700, 32), generator=gen(4), device="cuda").to(dtype)
+    h[:, 0], w[:, 0], w[7, 0] = 1, 0, float("inf")
+    t = torch.full((n,), 7, device="cuda")
+    out = mu.linear_logprobs(h, w, t, top=9)
+    assert bool(out.logprobs.isnan().all()) and bool(out.entropy.isnan().all())
+    assert torch.equal(out.top_tokens, order(h, w, 9)) and bool((out.top_logprobs[:, 1:] == -float("inf")).all())
+    t[0] = 3
+    out = mu.linear_logprobs(h, w, t, top=9)
+    assert bool(out.logprobs.isnan().all()) and bool((out.top_tokens[0] == -1).all()) and torch.equal(out.top_tokens[1:], order(h, w, 9)[1:])
