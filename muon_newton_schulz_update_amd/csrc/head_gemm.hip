@@ -501,10 +501,10 @@ __device__ __forceinline__ void store_logits_grad(const HeadArgs& a, f32x16_t (&
 // other's products, took 13 % longer (more operand traffic from LDS).
 //
 // LOGITS_STATS adds each tile's entropy to the statistics, leaves one of the largest
-// out of the sum (two operations a logit: 1 % of the launch) and, where alternatives
+// out of the sum (two operations a logit: 3 % of the launch) and, where alternatives
 // are asked for, each set's largest logits; LOGITS_GRAD, with a token's statistics
 // from an earlier call, leaves the gradient itself (8192 x 50304 x 768, bf16:
-// statistics 570 us, 1.11 PFLOP/s with the matrix cores half busy; gradient 690,
+// statistics 590 us, 1.07 PFLOP/s with the matrix cores 59 % busy; gradient 690,
 // 824 MB written under the products: kept exponentials and their own pass take 672
 // + 300).
 // ---------------------------------------------------------------------------

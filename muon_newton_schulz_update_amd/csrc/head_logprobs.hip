@@ -25,9 +25,10 @@
 // are asked for together, the sets stay in registers, and what bounds it is that
 // chain of dependent steps, most of all the candidates' rows of the weight (from
 // the caches: 3000 tokens x 29 of 4 KB are 356 MB). 50304 words: one token top 8
-// 13 us, 1536 tokens top 5 x 768 38, 3000 top 20 x 2048 115 (a wave a token 16, 42,
-// 149; sorting every set instead of a threshold 88, 166, 596); statistics alone,
-// 8192 tokens, 18 us, of which 52 MB and the targets' 25 are a read of 12.
+// 14 us, 1536 tokens top 5 x 768 40, 3000 top 20 x 2048 125 (before sets had spare
+// places and the leading word 64 bits 13, 37, 114; then a wave a token 16, 42, 149, and
+// sorting every set instead of a threshold 88, 166, 596); statistics alone, 8192
+// tokens, 17 us, of which 52 MB and the targets' 25 are a read of 12.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
