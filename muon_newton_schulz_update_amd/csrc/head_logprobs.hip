@@ -503,8 +503,9 @@ __device__ __forceinline__ void alternatives(const HeadArgs& a, const Token& tok
   const bool there = found.token != kNoToken && found.z > -__builtin_inf();
   const double c = a.softcap, z = c > 0 ? tanh(found.z / c) * c : found.z;
   // (the leading word's difference is 0 in every bit)
-  const double less = !stat.given && found.token == first ? 0. : z - stat.lead;
-  logps[lane] = !there ? kNone : found.token == target ? stat.of.w : (float)(less - log1p((double)stat.others));
+  const double less = (!stat.given && found.token == first ? 0. : z - stat.lead) - log1p((double)stat.others);
+  // (above 0 where the sums have another word, whose products cancel, for far too little)
+  logps[lane] = !there ? kNone : found.token == target ? stat.of.w : less > 0. ? 0.f : (float)less;
   tokens[lane] = there ? found.token : -1;
 }
 

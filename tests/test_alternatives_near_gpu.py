@@ -82,3 +82,13 @@ def test_an_infinite_target_leaves_the_alternatives(n, dtype):
     t[0] = 3
     out = mu.linear_logprobs(h, w, t, top=9)
     assert bool(out.logprobs.isnan().all()) and bool((out.top_tokens[0] == -1).all()) and torch.equal(out.top_tokens[1:], order(h, w, 9)[1:])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 300])
+def test_no_log_probability_is_above_0(n, dtype):
+    """A word of logit 3.5 that is 0 in 32 bits is found first, and its probability, which the sums do not know, is no
+    more than 1."""
+    h, w = cancelling(n, 2000, [512 + SET[2]], [3.5], {700: 0.125}, 5, dtype)
+    out = mu.linear_logprobs(h, w, torch.full((n,), 7, device="cuda"), top=3)
+    assert torch.equal(out.top_tokens, order(h, w, 3)) and bool((out.top_logprobs <= 0).all())
